@@ -376,6 +376,140 @@ int fsa_attention_fwd_host(const fsa_host_io* host, const fsa_device_io* dev, in
                            int Sk, int D, int causal, float scale, int fmt_qk, int fmt_pv, const fsa_opts* opts,
                            fsa_stats* stats, int n_chunks, void* stream);
 
+/* ---------------------------------------------------------- serving: q and k */
+/* Strides of a bf16 tensor indexed [B][S][heads][D], in elements; D is contiguous.
+ * Those of dimensions longer than 1 are non-negative multiples of 8, and not 0 for an
+ * output.  (Heads before positions, as fsa_mx_quantize takes them, is a choice of
+ * strides.) */
+typedef struct {
+  int64_t b, s, h;
+} fsa_strides;
+
+/* Queries and keys from the projection to the attention, in one pass: RMS norm of each
+ * head, y = x / sqrt(mean(x^2) + eps) * weight, and rotation of pairs of its elements by
+ * the position.  Pair i < rotary/2 is (y[i], y[i + rotary/2]), or (y[2i], y[2i+1]) when
+ * interleaved; it turns by pos[b][s][axis] * inv_freq[i].  sections[a] consecutive pairs
+ * turn by axis a (one axis for text; time, height and width for images and video);
+ * elements from `rotary` on pass unrotated.  fp32 arithmetic, angles good to 2^-24 of a
+ * turn up to position 2^24 (2^-16 at 2^31), one rounding to bf16.
+ *   q [B][S][H][D], k [B][S][Hkv][D]: bf16, device, 16-byte aligned, strided
+ *   q_out, k_out: as q and k, strides of their own; may be q and k themselves (same
+ *     pointer and strides), and must not overlap them or each other otherwise
+ *   q_weight, k_weight: bf16 [D], 16-byte aligned, or NULL for ones (NULL without norm)
+ *   pos: int32 [B][S][n_axes]; inv_freq: double [rotary/2] (radians a position);
+ *     both device, unused when rotary is 0
+ * One launch, nothing allocated: may be captured.  Errors: FSA_ERR_INVALID_ARG (null or
+ * misaligned pointer, bad shape or strides, rotary not a multiple of 8 in 0..D, n_axes
+ * not 1..3, sections that do not sum to rotary/2, eps negative or not finite),
+ * FSA_ERR_LAUNCH. */
+typedef struct {
+  const void*    q;
+  const void*    k;
+  void*          q_out;
+  void*          k_out;
+  fsa_strides    q_strides, k_strides, q_out_strides, k_out_strides;
+  const void*    q_weight;
+  const void*    k_weight;
+  const int32_t* pos;
+  const double*  inv_freq;
+  int32_t        B, S, H, Hkv, D, rotary, n_axes;
+  int32_t        sections[3];
+  int32_t        norm;          /* 1: RMS norm, 0: none */
+  int32_t        interleaved;
+  float          eps;
+} fsa_norm_rope;
+
+int fsa_qk_norm_rope(const fsa_norm_rope* args, void* stream);
+
+/* ------------------------------------------------------- serving: the K/V cache */
+/* A pool of pages that holds keys and values in 4 bits (the MXFP4 and NVFP4 operand
+ * formats above).  Blocks run along D for V as well as for K, so that a token is written
+ * once and never again.  fmt FSA_FMT_E2M1: 32 elements a block, E8M0 scale; FSA_FMT_NVFP4:
+ * 16 elements, E4M3 scale; scale and code rules as for the MX tensors above.
+ * A page is [Hkv][page_size/16] groups of 16 tokens.  A group is
+ *   16 rows of K codes, 16 rows of V codes      D/2 bytes each
+ *   16 rows of K scales, 16 rows of V scales    D/32 (E2M1) or D/16 (NVFP4) bytes each
+ * with the scale of block j in byte j, two codes to a byte (the even element in the low
+ * nibble), and the bytes of a code row in the order of the attention's fragments:
+ *   K: byte t*(D/8) + 2s + h holds elements 16s + 4t + 2h and the next (t < 4, h < 2)
+ *   V: byte g*(D/16) + i holds elements 16i + 2g and the next (g < 8)
+ * Which pages belong to a sequence, in order, is said by a row of a block table
+ * (int32 [B][max_pages]); the caller hands out the pages. */
+typedef struct {
+  void*   pages;       /* device, 16-byte aligned, num_pages * fsa_cache_page_bytes */
+  int64_t num_pages;   /* <= 2^31 - 1 */
+  int32_t page_size;   /* tokens: a power of two, 16..1024 */
+  int32_t Hkv, D;      /* D 64 or 128 */
+  int32_t fmt;         /* FSA_FMT_E2M1 or FSA_FMT_NVFP4 */
+} fsa_cache;
+
+/* Bytes of a page (a multiple of 64). */
+int fsa_cache_page_bytes(int page_size, int Hkv, int D, int fmt, size_t* bytes);
+
+/* Quantise new keys and values into the cache.  k, v: bf16 [B][S][Hkv][D], strided,
+ * 16-byte aligned.  lens[b] (int32, device): tokens of sequence b with the new ones;
+ * new_lens[b]: how many are new, at most S (NULL: S each).  Row i < new_lens[b] becomes
+ * token lens[b] - new_lens[b] + i; rows behind (padding) are not read.  Tokens at negative
+ * positions or past the block table are dropped.  A page number outside 0..num_pages-1 is
+ * not followed: its tokens are dropped, and *status (device int32, optional) becomes
+ * FSA_ERR_INVALID_ARG.  Two tokens of one call must not share a place (two sequences whose
+ * tables name one page for their new tokens); what such a place then holds is unspecified.
+ * max_pages * page_size <= 2^30.  One launch, nothing allocated: may be captured.  Errors:
+ * FSA_ERR_INVALID_ARG, FSA_ERR_UNSUPPORTED_FMT (fmt), FSA_ERR_LAUNCH. */
+int fsa_cache_append(const fsa_cache* cache, const void* k, const void* v, const fsa_strides* k_strides,
+                     const fsa_strides* v_strides, int B, int S, const int32_t* block_table, int max_pages,
+                     const int32_t* lens, const int32_t* new_lens, int32_t* status, void* stream);
+
+/* The values that the cache stands for (exact in bf16): row i of sequence b is token
+ * start[b] + i (start NULL: 0) where that lies in 0..lens[b]-1; other rows of k and v are
+ * left as they were.  k or v may be NULL.  Tokens past the block table, or of a page number
+ * outside the pool, read as zeros (the latter sets *status as above).  Shapes, limits and
+ * errors as fsa_cache_append. */
+int fsa_cache_read(const fsa_cache* cache, void* k, void* v, const fsa_strides* k_strides,
+                   const fsa_strides* v_strides, int B, int S, const int32_t* block_table, int max_pages,
+                   const int32_t* lens, const int32_t* start, int32_t* status, void* stream);
+
+/* Attention of few query rows over the cache (decode steps, guessed tokens, chunks of a
+ * prompt): O = softmax(scale Q K^T) V on the values the cache stands for; q is not
+ * quantised, sums and softmax statistics are fp32, probabilities times V's scales are
+ * rounded to f16 (2^-12) before the product with the codes of V, exact down to 2^-28 of
+ * the largest.  Query head h reads kv head h / (H/Hkv).  Row i < q_lens[b] of sequence b
+ * stands at position lens[b] - q_lens[b] + i and sees the keys up to its own position
+ * (causal) or all lens[b]; lens counts the rows' own tokens, which are in the cache
+ * already.  A row that sees nothing gives zeros (lse -inf).  Rows behind q_lens[b] are not
+ * written.  The lengths are read on the device: a captured call follows them.
+ *   q, out: [B][Sq][H][D] strided, 16-byte aligned; out bf16 or fp32 by out_dtype
+ *   lse: optional fp32 [B][Sq][H], natural log of the sum of exp(scale q k)
+ *   lens: int32 [B], cut to max_pages * page_size; q_lens: int32 [B], cut to 0..Sq, or NULL (Sq)
+ *   workspace: fsa_attention_cache_workspace bytes, 16-byte aligned; needs no initial
+ *     value, and is the call's own while it runs (calls that may run at once, captured ones
+ *     included, need one each)
+ *   status: optional device int32: FSA_ERR_INVALID_ARG where a page number lay outside the
+ *     pool (its keys are not seen), FSA_ERR_TIMEOUT where a wait for a copy ran out
+ *     (timeout_ms; 0: 4000), the output then being undefined
+ * B * Sq * H <= 2^27.  Errors: FSA_ERR_INVALID_ARG, FSA_ERR_UNSUPPORTED_FMT,
+ * FSA_ERR_NO_DEVICE, FSA_ERR_LAUNCH.  The work is laid out for the current device, which
+ * must be the one of the pointers and the stream. */
+typedef struct {
+  const void*      q;
+  void*            out;
+  float*           lse;
+  const fsa_cache* cache;
+  const int32_t*   block_table;
+  const int32_t*   lens;
+  const int32_t*   q_lens;
+  void*            workspace;
+  size_t           workspace_bytes;
+  int32_t*         status;
+  fsa_strides      q_strides, out_strides;
+  int32_t          B, H, Sq, max_pages, causal, out_dtype;
+  float            scale;
+  uint32_t         timeout_ms;
+} fsa_cache_attn;
+
+int fsa_attention_cache_workspace(int B, int H, int Hkv, int Sq, int D, size_t* bytes);
+int fsa_attention_cache(const fsa_cache_attn* args, void* stream);
+
 /* ------------------------------------------------------ tensor-core peak probe */
 /* Measurement instrument (the roofline denominator of the attention kernels; the
  * Fused-Softmax brief, abstract, quotes its kernels' throughput on the block-

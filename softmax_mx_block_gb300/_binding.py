@@ -73,6 +73,35 @@ class fsa_device_io(ctypes.Structure):
                 ("v_mx", ctypes.POINTER(fsa_mx_tensor)), ("out", ctypes.c_void_p)]
 
 
+class fsa_strides(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_int64), ("s", ctypes.c_int64), ("h", ctypes.c_int64)]
+
+
+class fsa_norm_rope(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p),
+                ("q_strides", fsa_strides), ("k_strides", fsa_strides), ("q_out_strides", fsa_strides),
+                ("k_out_strides", fsa_strides), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("pos", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p), ("B", ctypes.c_int32), ("S", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32), ("rotary", ctypes.c_int32),
+                ("n_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 3), ("norm", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class fsa_cache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32), ("fmt", ctypes.c_int32)]
+
+
+class fsa_cache_attn(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("cache", ctypes.POINTER(fsa_cache)), ("block_table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("q_lens", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+                ("status", ctypes.c_void_p), ("q_strides", fsa_strides), ("out_strides", fsa_strides),
+                ("B", ctypes.c_int32), ("H", ctypes.c_int32), ("Sq", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("timeout_ms", ctypes.c_uint32)]
+
+
 FSA_OUT_F32, FSA_OUT_BF16 = 0, 1
 STATS_BYTES = 24      # fsa_stats: u64 fallback_events, u64 row_tiles, i32 status, i32 reserved
 
@@ -107,6 +136,13 @@ def load(build_if_missing: bool = True):
             L.fsa_attention_fwd_host.argtypes = [ctypes.POINTER(fsa_host_io), ctypes.POINTER(fsa_device_io),
                                                  i, i, i, i, i, i, i, f, i, i, ctypes.POINTER(fsa_opts), vp, i, vp]
             L.fsa_tune_delta.argtypes = [ctypes.POINTER(fsa_stats), i, f, f, f, ctypes.POINTER(ctypes.c_float)]
+            L.fsa_qk_norm_rope.argtypes = [ctypes.POINTER(fsa_norm_rope), vp]
+            L.fsa_cache_page_bytes.argtypes = [i, i, i, i, ctypes.POINTER(ctypes.c_size_t)]
+            for n in ("fsa_cache_append", "fsa_cache_read"):
+                getattr(L, n).argtypes = [ctypes.POINTER(fsa_cache), vp, vp, ctypes.POINTER(fsa_strides),
+                                          ctypes.POINTER(fsa_strides), i, i, vp, i, vp, vp, vp, vp]
+            L.fsa_attention_cache_workspace.argtypes = [i, i, i, i, i, ctypes.POINTER(ctypes.c_size_t)]
+            L.fsa_attention_cache.argtypes = [ctypes.POINTER(fsa_cache_attn), vp]
             L.fsa_mma_peak.argtypes = [i, i, i, ctypes.c_longlong, vp, ctypes.POINTER(ctypes.c_double), vp]
             L.fsa_bf16_transpose_v.argtypes = [vp, vp, i, i, i, i, vp]
             L.fsa_attention_fwd_bf16.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, i, f, vp, vp]
@@ -117,7 +153,8 @@ def load(build_if_missing: bool = True):
             for n in ("fsa_mx_sizes", "fsa_mx_quantize", "fsa_mx_quantize_qkv", "fsa_attention_fwd",
                       "fsa_attention_fwd_ex", "fsa_bf16_transpose_v", "fsa_attention_fwd_bf16", "fsa_version",
                       "fsa_attention_fwd_layers", "fsa_tune_delta", "fsa_mma_peak", "fsa_attention_fwd_qbf16",
-                      "fsa_attention_fwd_host"):
+                      "fsa_attention_fwd_host", "fsa_qk_norm_rope", "fsa_cache_page_bytes", "fsa_cache_append",
+                      "fsa_cache_read", "fsa_attention_cache_workspace", "fsa_attention_cache"):
                 getattr(L, n).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -515,6 +552,223 @@ def fsa_tune_delta(stats: list, deltas: list, target_rate=0.01, step=4.0, max_de
     d = (ctypes.c_float * max(n, 1))(*[float(x) for x in deltas])
     _check(load().fsa_tune_delta(sarr, n, float(target_rate), float(step), float(max_delta), d), "fsa_tune_delta")
     return [float(d[i]) for i in range(n)]
+
+
+# ----------------------------------------------------------------------------- serving
+def _strided(t: torch.Tensor, name: str, device, heads=None, output=False, dtype=torch.bfloat16) -> fsa_strides:
+    """Strides of a [B,S,heads,D] tensor of `dtype` on `device`, its rows contiguous, 16-byte
+    aligned and, for an output, apart."""
+    if not t.is_cuda:
+        raise FsaError(FSA_ERR_INVALID_ARG, f"{name} must be a CUDA tensor")
+    if t.dtype != dtype or t.dim() != 4 or t.device != device:
+        raise FsaError(FSA_ERR_INVALID_ARG, f"{name} must be a 4-dimensional {dtype} tensor on {device}")
+    if heads is not None and t.shape[2] != heads:
+        raise FsaError(FSA_ERR_INVALID_ARG, f"{name} must have {heads} heads")
+    b, s, h, d = t.stride()
+    if d != 1:
+        raise FsaError(FSA_ERR_INVALID_ARG, f"{name} must be contiguous in its last dimension")
+    for n, st in zip(t.shape, (b, s, h)):
+        if n > 1 and (st % 8 or (output and st == 0)):
+            raise FsaError(FSA_ERR_INVALID_ARG, f"{name} strides must be multiples of 8"
+                                                + (", and an output's rows apart" if output else ""))
+    return fsa_strides(b, s, h)
+
+
+def _index(t, name: str, shape, device, dtype=torch.int32) -> int:
+    """Pointer of a contiguous integer (or other) tensor of the given shape (None: null)."""
+    if t is None:
+        return 0
+    if not t.is_cuda or t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+        raise FsaError(FSA_ERR_INVALID_ARG, f"{name} must be a contiguous {dtype} CUDA tensor {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _on(device):
+    """The device of a call's tensors as the current one (kernels launch on the current device)."""
+    return torch.cuda.device(device)
+
+
+def fsa_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor | None, inv_freq: torch.Tensor | None, *,
+                     sections=None, q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                     norm=True, eps=1e-6, interleaved=False, q_out: torch.Tensor | None = None,
+                     k_out: torch.Tensor | None = None, stream=None) -> tuple:
+    """RMS norm of each head of q [B,S,H,D] and k [B,S,Hkv,D] (bf16, strided) and rotation by
+    position, in one pass.  pos: int32 [B,S] or [B,S,axes]; inv_freq: float64 [rotary/2];
+    sections: pairs of each axis (default: all of one).  q_out, k_out default to contiguous
+    tensors of q's and k's shapes; q and k themselves rotate in place.  Returns (q_out, k_out)."""
+    dev = q.device
+    qs = _strided(q, "q", dev)
+    ks = _strided(k, "k", dev)
+    B, S, H, D = q.shape
+    if k.shape[0] != B or k.shape[1] != S or k.shape[3] != D:
+        raise FsaError(FSA_ERR_INVALID_ARG, "q, k shapes")
+    half, axes = 0, 1
+    if inv_freq is not None:
+        half = inv_freq.numel()
+        _index(inv_freq, "inv_freq", (half,), dev, torch.float64)
+        if pos is None:
+            raise FsaError(FSA_ERR_INVALID_ARG, "a rotation needs pos")
+        axes = 1 if pos.dim() == 2 else pos.shape[-1]
+        _index(pos, "pos", (B, S) if pos.dim() == 2 else (B, S, axes), dev)
+    sections = (half,) if sections is None else tuple(int(x) for x in sections)
+    if len(sections) != axes or axes > 3:
+        raise FsaError(FSA_ERR_INVALID_ARG, f"{len(sections)} sections for {axes} axes (1 to 3)")
+    if q_out is None:
+        q_out = torch.empty((B, S, H, D), dtype=q.dtype, device=dev)
+    if k_out is None:
+        k_out = torch.empty(tuple(k.shape), dtype=k.dtype, device=dev)
+    qos = _strided(q_out, "q_out", dev, output=True)
+    kos = _strided(k_out, "k_out", dev, output=True)
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        raise FsaError(FSA_ERR_INVALID_ARG, "q_out, k_out shapes")
+    args = fsa_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), qs, ks, qos, kos,
+                         _index(q_weight, "q_weight", (D,), dev, torch.bfloat16),
+                         _index(k_weight, "k_weight", (D,), dev, torch.bfloat16),
+                         pos.data_ptr() if half else 0, inv_freq.data_ptr() if half else 0, B, S, H, k.shape[2], D,
+                         2 * half, axes, (ctypes.c_int32 * 3)(*sections), int(bool(norm)), int(bool(interleaved)),
+                         float(eps))
+    with _on(dev):
+        _check(load().fsa_qk_norm_rope(ctypes.byref(args), _stream(stream)), "fsa_qk_norm_rope")
+    return q_out, k_out
+
+
+def fsa_cache_page_bytes(page_size, Hkv, D, fmt) -> int:
+    n = ctypes.c_size_t()
+    _check(load().fsa_cache_page_bytes(int(page_size), int(Hkv), int(D), _fmt(fmt), ctypes.byref(n)), "fsa_cache_page_bytes")
+    return n.value
+
+
+class MxCache:
+    """A pool of pages of 4-bit keys and values (fsa_cache): `pages` is a contiguous uint8
+    tensor [num_pages, fsa_cache_page_bytes] on the GPU, owned by torch."""
+
+    def __init__(self, pages: torch.Tensor, page_size: int, Hkv: int, D: int, fmt):
+        self.pages, self.page_size, self.Hkv, self.D, self.fmt = pages, int(page_size), int(Hkv), int(D), _fmt(fmt)
+        n = fsa_cache_page_bytes(page_size, Hkv, D, self.fmt)
+        if not isinstance(pages, torch.Tensor) or pages.dtype != torch.uint8 or pages.dim() != 2 or pages.shape[1] != n \
+                or not pages.is_contiguous():
+            raise FsaError(FSA_ERR_INVALID_ARG, f"pages must be a contiguous uint8 tensor [num_pages, {n}]")
+
+    def struct(self) -> fsa_cache:
+        if not self.pages.is_cuda:
+            raise FsaError(FSA_ERR_INVALID_ARG, "pages must be a CUDA tensor")
+        return fsa_cache(self.pages.data_ptr(), self.pages.shape[0], self.page_size, self.Hkv, self.D, self.fmt)
+
+
+def empty_cache(num_pages, page_size, Hkv, D, fmt, device=None) -> MxCache:
+    """A cache with room for num_pages * page_size tokens (its bytes are not initialised)."""
+    n = fsa_cache_page_bytes(page_size, Hkv, D, fmt)
+    return MxCache(torch.empty((num_pages, n), dtype=torch.uint8, device=device or "cuda"), page_size, Hkv, D, fmt)
+
+
+def _table(block_table: torch.Tensor, B, device) -> int:
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise FsaError(FSA_ERR_INVALID_ARG, "block_table must be [B, max_pages]")
+    return _index(block_table, "block_table", block_table.shape, device)
+
+
+def fsa_cache_append(cache: MxCache, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor,
+                     new_lens: torch.Tensor | None = None, *, status: torch.Tensor | None = None, stream=None) -> None:
+    """Quantise k, v (bf16 [B,S,Hkv,D], strided) into the cache: row i < new_lens[b] (default
+    all S) becomes token lens[b] - new_lens[b] + i of the sequence whose pages row b of
+    block_table (int32 [B, max_pages]) names.  lens (int32 [B]) counts the new tokens too."""
+    dev = cache.pages.device
+    c = cache.struct()
+    ks = _strided(k, "k", dev, cache.Hkv)
+    vs = _strided(v, "v", dev, cache.Hkv)
+    B, S, _, D = k.shape
+    if v.shape != k.shape or D != cache.D:
+        raise FsaError(FSA_ERR_INVALID_ARG, "k, v shapes")
+    args = (ctypes.byref(c), k.data_ptr(), v.data_ptr(), ctypes.byref(ks), ctypes.byref(vs), B, S,
+            _table(block_table, B, dev), block_table.shape[1], _index(lens, "lens", (B,), dev),
+            _index(new_lens, "new_lens", (B,), dev), _index(status, "status", (1,), dev))
+    with _on(dev):
+        _check(load().fsa_cache_append(*args, _stream(stream)), "fsa_cache_append")
+
+
+def fsa_cache_read(cache: MxCache, block_table: torch.Tensor, lens: torch.Tensor, S: int | None = None, *,
+                   start: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                   v_out: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> tuple:
+    """The values the cache stands for: row i of sequence b is token start[b] + i (default
+    start 0) where that lies before lens[b]; other rows are left as they were.  k_out, v_out:
+    bf16 [B,S,Hkv,D], strided; without either, both are made (zeros, S rows).  Returns
+    (k_out, v_out)."""
+    dev = cache.pages.device
+    c = cache.struct()
+    B = lens.shape[0]
+    if k_out is None and v_out is None:
+        if S is None:
+            raise FsaError(FSA_ERR_INVALID_ARG, "S, k_out or v_out must be given")
+        k_out = torch.zeros((B, S, cache.Hkv, cache.D), dtype=torch.bfloat16, device=dev)
+        v_out = torch.zeros_like(k_out)
+    some = v_out if k_out is None else k_out
+    S = some.shape[1] if S is None else S
+    ptr, strides = [], []
+    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is None:
+            ptr.append(0)
+            strides.append(fsa_strides())
+            continue
+        strides.append(_strided(t, n, dev, cache.Hkv, output=True))
+        if t.shape[0] != B or t.shape[1] != S or t.shape[3] != cache.D:
+            raise FsaError(FSA_ERR_INVALID_ARG, f"{n} must be [B, S, Hkv, D]")
+        ptr.append(t.data_ptr())
+    args = (ctypes.byref(c), ptr[0], ptr[1], ctypes.byref(strides[0]), ctypes.byref(strides[1]), B, S,
+            _table(block_table, B, dev), block_table.shape[1], _index(lens, "lens", (B,), dev),
+            _index(start, "start", (B,), dev), _index(status, "status", (1,), dev))
+    with _on(dev):
+        _check(load().fsa_cache_read(*args, _stream(stream)), "fsa_cache_read")
+    return k_out, v_out
+
+
+def fsa_attention_cache_workspace(B, H, Hkv, Sq, D) -> int:
+    """Bytes of the workspace of fsa_attention_cache on the current device."""
+    n = ctypes.c_size_t()
+    _check(load().fsa_attention_cache_workspace(B, H, Hkv, Sq, D, ctypes.byref(n)), "fsa_attention_cache_workspace")
+    return n.value
+
+
+def fsa_attention_cache(q: torch.Tensor, cache: MxCache, block_table: torch.Tensor, lens: torch.Tensor, *,
+                        q_lens: torch.Tensor | None = None, causal=True, scale=None, out: torch.Tensor | None = None,
+                        lse: torch.Tensor | None = None, out_dtype=None, workspace: torch.Tensor | None = None,
+                        timeout_ms=0, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """O [B,Sq,H,D] (fp32, or bf16 with out_dtype="bf16" or a bf16 `out`) of q (bf16
+    [B,Sq,H,D], strided) over the cached keys and values of sequences of lens[b] tokens
+    (int32 [B]; the rows' own tokens are in the cache).  Row i < q_lens[b] (default all Sq)
+    stands at lens[b] - q_lens[b] + i and, causal, sees the keys up to there; rows behind
+    q_lens[b] are left as they were.  lse: optional fp32 [B,Sq,H] for the log of the
+    softmax sums.  workspace: uint8, at least fsa_attention_cache_workspace bytes (default:
+    one of the call's own)."""
+    dev = cache.pages.device
+    c = cache.struct()
+    qs = _strided(q, "q", dev)
+    B, Sq, H, D = q.shape
+    if D != cache.D or H % cache.Hkv:
+        raise FsaError(FSA_ERR_INVALID_ARG, "q must have the cache's D and a multiple of its heads")
+    od, tdt = _out_dtype(out_dtype if out is None or out_dtype is not None else out.dtype)
+    if out is None:
+        out = torch.empty((B, Sq, H, D), dtype=tdt, device=dev) if q_lens is None else \
+            torch.zeros((B, Sq, H, D), dtype=tdt, device=dev)
+    os_ = _strided(out, "out", dev, output=True, dtype=tdt)
+    if out.shape != q.shape:
+        raise FsaError(FSA_ERR_INVALID_ARG, "out must have q's shape")
+    tab, ln = _table(block_table, B, dev), _index(lens, "lens", (B,), dev)
+    ql, st = _index(q_lens, "q_lens", (B,), dev), _index(status, "status", (1,), dev)
+    le = _index(lse, "lse", (B, Sq, H), dev, torch.float32)
+    with _on(dev):
+        if workspace is None:
+            workspace = torch.empty(fsa_attention_cache_workspace(B, H, cache.Hkv, Sq, D), dtype=torch.uint8, device=dev)
+            if stream is not None:
+                workspace.record_stream(stream)
+        else:
+            _need_cuda(workspace, "workspace", torch.uint8)
+            if workspace.device != dev:
+                raise FsaError(FSA_ERR_INVALID_ARG, f"workspace is on {workspace.device}, the call on {dev}")
+        args = fsa_cache_attn(q.data_ptr(), out.data_ptr(), le, ctypes.pointer(c), tab, ln, ql, workspace.data_ptr(),
+                              workspace.numel(), st, qs, os_, B, H, Sq, block_table.shape[1], int(bool(causal)), od,
+                              D ** -0.5 if scale is None else float(scale), int(timeout_ms))
+        _check(load().fsa_attention_cache(ctypes.byref(args), _stream(stream)), "fsa_attention_cache")
+    return out
 
 
 def fsa_mma_peak(kind: int, n_ctas: int, iters: int, status: torch.Tensor | None = None, n: int = 128,

@@ -34,6 +34,7 @@ def _units():
     units = [("fsa_api", os.path.join(CSRC, "fsa_api.cu"), []),
              ("fsa_quant", os.path.join(CSRC, "fsa_quant.cu"), []),
              ("fsa_peak", os.path.join(CSRC, "fsa_peak.cu"), [])]
+    units += [(n, os.path.join(CSRC, n + ".cu"), []) for n in ("fsa_cache_api", "fsa_cache_attn", "fsa_cache", "fsa_rope")]
     for qk, pv in ATTN_PAIRS:
         units.append((f"fsa_attn_{qk}{pv}", os.path.join(CSRC, "fsa_attn.cu"),
                       [f"-DFSA_INST_QK={qk}", f"-DFSA_INST_PV={pv}"]))

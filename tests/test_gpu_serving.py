@@ -1,0 +1,502 @@
+"""The serving operators against their 64-bit definitions: q/k norm and rotation, the
+paged 4-bit cache written and read, attention over it.
+
+Tolerances are derived, not fitted.  A rounding to a type is off by at most eps/2 of the
+value: bf16 2^-8, f16 2^-11, fp32 2^-24 (torch.finfo(t).eps / 2).
+  - norm and rotation: the fp32 arithmetic before the one rounding to bf16 is off by a few
+    2^-24 of |a| + |b| of the pair, and the angle by 2^-24 of a turn (2^-21.3 rad), so by
+    2^-20 (|a| + |b|) in all.
+  - attention: each probability times its V scale is rounded to f16, 2^-11 of sum p|v| / sum p;
+    the fp32 scores are off by at most (D + 8) 2^-24 of sum |q||k| scale each way, which moves
+    every weight by as much relatively, numerator and denominator; sums, exp2 and the rest
+    2^-18; a probability below f16's range loses at most 2^-25 of 2^8-scaled ones (6 * 2^-33
+    of the largest V block scale doubled) a key.  bf16 output adds 2^-8 of the value.
+"""
+import math
+
+import pytest
+
+import serving_ref as ref
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+def _fsa():
+    import softmax_mx_block_gb300 as fsa
+    return fsa
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def normal(g, *shape):
+    return torch.randn(*shape, generator=g, device="cuda").to(torch.bfloat16)
+
+
+def edge_values(g, *shape):
+    """bf16 with ties of every block maximum, zeros of both signs, whole zero rows, tiny and
+    huge values and strong channels."""
+    x = torch.randn(*shape, generator=g, device="cuda")
+    pick = torch.rand(*shape, generator=g, device="cuda")
+    x = torch.where(pick < 0.2, torch.randint(-24, 25, shape, generator=g, device="cuda") / 4.0, x)
+    x = torch.where((pick > 0.2) & (pick < 0.25), torch.zeros_like(x), x)
+    x = torch.where((pick > 0.25) & (pick < 0.28), -torch.zeros_like(x), x)
+    row = torch.rand(*shape[:-1], 1, generator=g, device="cuda")
+    x = x * torch.where(row < 0.1, 1e-38, 1.0) * torch.where((row > 0.1) & (row < 0.2), 1e30, 1.0)
+    x = x * torch.where((row > 0.2) & (row < 0.25), 0.0, 1.0) * torch.where((row > 0.25) & (row < 0.35), 1e-3, 1.0)
+    return x.to(torch.bfloat16)
+
+
+def make_table(g, lens, page, spare=2, extra=1):
+    need = [-(-n // page) for n in lens]
+    total = sum(need)
+    order = torch.randperm(total + spare, generator=g, device="cuda")[:total].to(torch.int32).tolist()
+    table = torch.full((len(lens), max(need + [1]) + extra), -1, dtype=torch.int32)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = torch.tensor(order[at:at + n], dtype=torch.int32)
+        at += n
+    return table.cuda(), total + spare
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def filled_cache(fsa, g, lens, page, Hkv, D, fmt, make=normal, junk=0xFF):
+    """A cache written by fsa_cache_append whose unused bytes are all `junk` (0xFF: NaN scales)."""
+    table, pages = make_table(g, lens, page)
+    cache = fsa.empty_cache(pages, page, Hkv, D, fmt)
+    cache.pages.fill_(junk)
+    S = max(lens + [1])
+    k, v = make(g, len(lens), S, Hkv, D), make(g, len(lens), S, Hkv, D)
+    fsa.fsa_cache_append(cache, k, v, table, i32(lens), i32(lens))
+    return cache, table, k, v
+
+
+# ------------------------------------------------------------------------ the cache itself
+@pytest.mark.parametrize("fmt", ["E2M1", "NVFP4"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page,Hkv,lens", [(16, 1, [1]), (16, 3, [17, 0, 40]), (64, 8, [5, 64, 65]), (256, 2, [300, 1])])
+def test_append_writes_the_definition(fmt, D, page, Hkv, lens):
+    """Codes and scales bit for bit, nothing else touched."""
+    fsa = _fsa()
+    g = gen(7)
+    cache, table, k, v = filled_cache(fsa, g, lens, page, Hkv, D, fmt, edge_values, junk=0xA5)
+    got = ref.unpack_pages(cache.pages, page, Hkv, D, fmt)
+    want = [torch.full_like(x, 0x5 if i % 2 == 0 else 0xA5) for i, x in enumerate(got)]
+    d = torch.arange(D, device="cuda")
+    for i in (0, 2):
+        want[i][:] = torch.where(d % 2 == 0, 0x5, 0xA).to(torch.uint8)
+    for b, n in enumerate(lens):
+        for s in range(n):
+            page_id, at = int(table[b, s // page]), s % page
+            for i, x in ((0, k), (2, v)):
+                codes, scales = ref.quantise(x[b, s], fmt)
+                want[i][page_id, at], want[i + 1][page_id, at] = codes, scales
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fmt", ["E2M1", "NVFP4"])
+def test_append_matches_the_row_quantiser(fmt):
+    """The same codes and scales as fsa_mx_quantize gives K rows (E2M1 nibbles, even element low)."""
+    fsa = _fsa()
+    B, S, Hkv, D, page = 1, 128, 2, 128, 64
+    k = edge_values(gen(3), B, S, Hkv, D)
+    cache = fsa.empty_cache(2, page, Hkv, D, fmt)
+    table = i32([[0, 1]])
+    fsa.fsa_cache_append(cache, k, k, table, i32([S]))
+    m = fsa.fsa_mx_quantize(k.transpose(1, 2).contiguous(), fsa.FSA_MX_ROWS, fmt)
+    rows = m.codes.reshape(Hkv, S, D // 2)
+    codes = torch.stack((rows & 15, rows >> 4), dim=-1).flatten(-2).transpose(0, 1)
+    kc, _, vc, _ = ref.unpack_pages(cache.pages, page, Hkv, D, fmt)
+    assert torch.equal(kc.flatten(0, 1), codes) and torch.equal(vc.flatten(0, 1), codes)
+
+
+@pytest.mark.parametrize("fmt", ["E2M1", "NVFP4"])
+def test_nonfinite_blocks(fmt):
+    fsa = _fsa()
+    D = 128
+    k = normal(gen(1), 1, 4, 2, D)
+    k[0, 1, 0, 5], k[0, 2, 1, 77], k[0, 3, 0, 127] = math.nan, math.inf, -math.inf
+    cache = fsa.empty_cache(1, 16, 2, D, fmt)
+    table = i32([[0]])
+    fsa.fsa_cache_append(cache, k, k, table, i32([4]))
+    for x, y in zip(fsa.fsa_cache_read(cache, table, i32([4]), 4), (k, k)):
+        want = ref.rounded(y, fmt)
+        assert torch.equal(torch.isnan(x), torch.isnan(want))
+        assert torch.equal(torch.nan_to_num(x.double()), torch.nan_to_num(want))
+    assert int(torch.isnan(x).sum()) == 3 * ref.BLOCK[fmt]
+
+
+@pytest.mark.parametrize("fmt", ["E2M1", "NVFP4"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_append_in_steps_then_read(fmt, D):
+    """A prompt, then chunks and single tokens, padded batches, strided sources (slices of a
+    projection), destinations with heads first; rows outside stay as they were."""
+    fsa = _fsa()
+    g = gen(11)
+    B, Hkv, page = 3, 2, 32
+    total = [70, 33, 5]
+    table, pages = make_table(g, total, page)
+    cache = fsa.empty_cache(pages, page, Hkv, D, fmt)
+    cache.pages.fill_(0xFF)
+    lens = [0] * B
+    kept = [[torch.zeros(0, Hkv, D, device="cuda")] * 2 for _ in range(B)]
+    for S, new in ((40, [40, 20, 0]), (16, [16, 3, 4]), (1, [1, 1, 1]), (20, [13, 9, 0])):
+        qkv = normal(g, B, S, 3 * Hkv, D)
+        k, v = qkv[:, :, Hkv:2 * Hkv], qkv[:, :, 2 * Hkv:]
+        lens = [a + n for a, n in zip(lens, new)]
+        fsa.fsa_cache_append(cache, k, v, table, i32(lens), i32(new))
+        for b in range(B):
+            kept[b] = [torch.cat((a, x[b, :new[b]].float())) for a, x in zip(kept[b], (k, v))]
+    assert lens == total
+    S, start = 50, [3, -2, 0]
+    base = torch.full((2, B, Hkv, S, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    ko, vo = base[0].transpose(1, 2), base[1].transpose(1, 2)
+    fsa.fsa_cache_read(cache, table, i32(lens), start=i32(start), k_out=ko, v_out=vo)
+    for b in range(B):
+        for x, src in ((ko, kept[b][0]), (vo, kept[b][1])):
+            want = torch.full((S, Hkv, D), 7.0, dtype=torch.float64, device="cuda")
+            q = ref.rounded(src.to(torch.bfloat16), fmt)
+            for i in range(S):
+                if 0 <= start[b] + i < lens[b]:
+                    want[i] = q[start[b] + i]
+            assert torch.equal(x[b].double(), want)
+    only = torch.zeros(B, 4, Hkv, D, dtype=torch.bfloat16, device="cuda")
+    assert fsa.fsa_cache_read(cache, table, i32(lens), v_out=only)[0] is None
+    assert torch.equal(only[0].double(), ref.rounded(kept[0][1][:4].to(torch.bfloat16), fmt))
+
+
+def test_bad_pages_are_not_followed():
+    """Negative and too large page numbers, lengths past the table: dropped or zero, and told."""
+    fsa = _fsa()
+    g = gen(5)
+    Hkv, D, page = 2, 64, 16
+    cache = fsa.empty_cache(3, page, Hkv, D, "E2M1")
+    cache.pages.fill_(0xA5)
+    table = i32([[1, 3], [-5, 0]])
+    k = normal(g, 2, 40, Hkv, D)
+    status = i32([0])
+    fsa.fsa_cache_append(cache, k, k, table, i32([40, 32]), i32([40, 32]), status=status)
+    assert int(status) == fsa.FSA_ERR_INVALID_ARG
+    assert bool((cache.pages[2] == 0xA5).all())
+    status.zero_()
+    kb, vb = fsa.fsa_cache_read(cache, table, i32([40, 32]), 40, status=status)
+    assert int(status) == fsa.FSA_ERR_INVALID_ARG
+    want = torch.zeros(2, 40, Hkv, D, dtype=torch.float64, device="cuda")
+    want[0, :16], want[1, 16:32] = ref.rounded(k[0, :16], "E2M1"), ref.rounded(k[1, 16:32], "E2M1")
+    assert torch.equal(kb.double(), want) and torch.equal(vb.double(), want)
+    # the attention does not see the keys of such pages
+    q = normal(g, 2, 3, 4, D)
+    status.zero_()
+    out, lse = torch.empty(2, 3, 4, D, device="cuda"), torch.empty(2, 3, 4, device="cuda")
+    fsa.fsa_attention_cache(q, cache, table, i32([32, 32]), out=out, lse=lse, status=status)
+    assert int(status) == fsa.FSA_ERR_INVALID_ARG
+    check_attention(q, cache, table, [32, 32], [3, 3], True, D ** -0.5, out, lse, torch.zeros_like(out))
+
+
+# ---------------------------------------------------------------------------- the attention
+def check_attention(q, cache, table, lens, q_lens, causal, scale, out, lse, before):
+    B, Sq, H, D = q.shape
+    fmt = {2: "E2M1", 5: "NVFP4"}[cache.fmt]
+    eps_out = 2.0 ** -8 if out.dtype == torch.bfloat16 else 2.0 ** -23
+    for b in range(B):
+        n = min(lens[b], table.shape[1] * cache.page_size)
+        m = min(q_lens[b], Sq)
+        assert torch.equal(out[b, m:], before[b, m:])
+        if m <= 0:
+            continue
+        k, v, live = ref.sequence(cache.pages, table[b], n, cache.page_size, cache.Hkv, D, fmt)
+        want, want_lse, spread, reach, total = ref.attention(q[b, :m], k, v, live, n, m, causal, scale)
+        vtop = torch.nan_to_num(v[live]).abs().max() if n and bool(live.any()) else torch.zeros(())
+        e_s = (D + 8) * 2.0 ** -24 * reach + 2.0 ** -18
+        tol = (2.0 ** -11 + 2 * e_s)[..., None] * spread * 1.01
+        tol = tol + (n * 12 * 2.0 ** -33 * vtop / total.clamp(min=1.0))[..., None] + eps_out * want.abs() + 1e-36
+        got = out[b, :m].double()
+        assert torch.equal(torch.isnan(got), torch.isnan(want)), b
+        off = torch.nan_to_num((got - want).abs() - tol, nan=-1.0)
+        assert bool((off <= 0).all()), (b, float(off.max()), float(want.abs().max()))
+        if lse is not None:
+            g_lse = lse[b, :m].double()
+            assert torch.equal(torch.isinf(g_lse), torch.isinf(want_lse))
+            fine = torch.isfinite(want_lse)
+            assert bool(((g_lse - want_lse).abs()[fine] <= (e_s + 2.0 ** -22 * (want_lse.abs() + 20))[fine]).all())
+
+
+def run_attention(fsa, q, cache, table, lens, q_lens=None, causal=True, scale=None, dtype="f32", seed=0, **kw):
+    B, Sq, H, D = q.shape
+    scale = D ** -0.5 if scale is None else scale
+    t = torch.float32 if dtype == "f32" else torch.bfloat16
+    before = torch.full((B, Sq, H, D), 3.25, dtype=t, device="cuda")
+    out, lse = before.clone(), torch.full((B, Sq, H), 9.0, device="cuda")
+    fsa.fsa_attention_cache(q, cache, table, i32(lens), q_lens=None if q_lens is None else i32(q_lens), causal=causal,
+                            scale=scale, out=out, lse=lse, **kw)
+    check_attention(q, cache, table, lens, q_lens or [Sq] * B, causal, scale, out, lse, before)
+    return out, lse
+
+
+SHAPES = [
+    # B-lens, Sq, H, Hkv, page
+    ([1], 1, 1, 1, 16),
+    ([0], 1, 8, 1, 16),
+    ([0, 1, 15, 16, 17, 31, 32, 33], 1, 8, 2, 16),
+    ([63, 64, 65, 127, 128, 129], 2, 4, 4, 64),
+    ([1, 2, 3, 300], 5, 14, 2, 32),                 # rows before the first key, odd group
+    ([2000], 1, 32, 8, 128),                        # few segments over many warps
+    ([40000, 7], 1, 8, 1, 64),
+    ([777] * 40, 1, 8, 4, 16),                      # many segments, shares that cross them
+    ([5] * 700, 1, 2, 2, 16),                       # more segments than warps
+    ([333, 90], 33, 6, 2, 1024),                    # several passes of columns
+    ([1500], 70, 5, 5, 32),
+]
+
+
+@pytest.mark.parametrize("fmt", ["E2M1", "NVFP4"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,Sq,H,Hkv,page", SHAPES)
+def test_attention_shapes(fmt, D, lens, Sq, H, Hkv, page):
+    fsa = _fsa()
+    g = gen(len(lens) + Sq)
+    cache, table, _, _ = filled_cache(fsa, g, lens, page, Hkv, D, fmt)
+    q = normal(g, len(lens), Sq, H, D)
+    run_attention(fsa, q, cache, table, lens)
+    run_attention(fsa, q, cache, table, lens, causal=False, dtype="bf16")
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("fmt", ["E2M1", "NVFP4"])
+def test_attention_ragged_rows(fmt, causal):
+    """q_lens from none to more than Sq; rows behind stay; strided q and out; strong scores."""
+    fsa = _fsa()
+    g = gen(21)
+    lens, q_lens, Hkv, D, Sq, H = [100, 64, 3, 0, 2500, 31], [4, 0, 4, 2, 9, 1], 2, 128, 4, 8
+    cache, table, _, _ = filled_cache(fsa, g, lens, 32, Hkv, D, fmt)
+    qkv = normal(g, len(lens), Sq, H + 2 * Hkv, D) * 4
+    out, _ = run_attention(fsa, qkv[:, :, :H], cache, table, lens, [min(x, Sq) for x in q_lens], causal)
+    base = torch.full((len(lens), H, Sq, D), 3.25, device="cuda")
+    strided = base.transpose(1, 2)
+    fsa.fsa_attention_cache(qkv[:, :, :H], cache, table, i32(lens), q_lens=i32(q_lens), causal=causal, out=strided)
+    assert torch.equal(strided, out)
+
+
+def test_attention_values_with_range():
+    """V blocks from 2^-30 to 2^20 times the others, whole zero V, a rising maximum, a sink."""
+    fsa = _fsa()
+    g = gen(31)
+    n, Hkv, D = 3000, 2, 128
+    for kind in range(5):
+        k, v = normal(g, 1, n, Hkv, D), normal(g, 1, n, Hkv, D)
+        if kind == 0:
+            v = v * torch.exp2(torch.randint(-15, 16, (1, n, 1, 1), generator=g, device="cuda").float()).to(v.dtype)
+        elif kind == 1:
+            v[:, 1000:] = v[:, 1000:] * 2.0 ** 20
+        elif kind == 2:
+            v.zero_()
+        elif kind == 3:
+            k = k * torch.linspace(0.1, 8.0, n, device="cuda")[None, :, None, None].to(k.dtype)
+            v[:, 100:200] = v[:, 100:200] * 2.0 ** -30
+        else:
+            k[:, 0] = k[:, 0] * 6
+            v[:, 0] = v[:, 0] * 2.0 ** -12
+        for fmt in ("E2M1", "NVFP4"):
+            table, pages = make_table(g, [n], 64)
+            cache = fsa.empty_cache(pages, 64, Hkv, D, fmt)
+            cache.pages.fill_(0xFF)
+            fsa.fsa_cache_append(cache, k, v, table, i32([n]))
+            q = normal(g, 1, 2, 8, D) * 3
+            run_attention(fsa, q, cache, table, [n])
+            for scale in (-0.05, 0.0, 1.0):
+                run_attention(fsa, q, cache, table, [n], scale=scale)
+
+
+@pytest.mark.parametrize("fmt", ["E2M1", "NVFP4"])
+def test_attention_nan_and_masks(fmt):
+    """NaN keys and values reach the rows that see them and no others; NaN and Inf in q stay
+    in their row."""
+    fsa = _fsa()
+    g = gen(41)
+    n, Hkv, D, Sq = 200, 2, 128, 6
+    k, v = normal(g, 1, n, Hkv, D), normal(g, 1, n, Hkv, D)
+    v[0, n - 3, 0, 40] = math.nan                  # rows 3.. see it, in one block of V's dims
+    v[0, 10, 1, 100] = math.inf                    # every row of head 1 sees it
+    table, pages = make_table(g, [n], 16)
+    cache = fsa.empty_cache(pages, 16, Hkv, D, fmt)
+    cache.pages.fill_(0xFF)
+    fsa.fsa_cache_append(cache, k, v, table, i32([n]))
+    q = normal(g, 1, Sq, 4, D)
+    out, _ = run_attention(fsa, q, cache, table, [n])
+    assert bool(torch.isfinite(out[0, :3, :2]).all()) and bool(torch.isnan(out[0, 3:, :2, 32:48]).all())
+    q[0, 1, 0, 3], q[0, 2, 3, 9] = math.nan, math.inf
+    out = fsa.fsa_attention_cache(q, cache, table, i32([n]))
+    assert bool(torch.isnan(out[0, 1, 0]).all()) and bool(torch.isnan(out[0, 2, 3]).all())
+    assert bool(torch.isfinite(out[0, 1, 1]).all()) and bool(torch.isfinite(out[0, 2, 0]).all())
+    k[0, n - 2, 0, 0] = math.nan                   # a NaN key: rows 4 and 5 of head 0's queries
+    fsa.fsa_cache_append(cache, k, v, table, i32([n]))
+    out = fsa.fsa_attention_cache(normal(g, 1, Sq, 4, D), cache, table, i32([n]))
+    assert bool(torch.isnan(out[0, 4:, :2]).all()) and bool(torch.isfinite(out[0, :3, :2]).all())
+
+
+def test_attention_far_pages():
+    """A pool of over 4 GiB: pages whose byte offsets pass 32 bits."""
+    fsa = _fsa()
+    Hkv, D, page = 8, 128, 64
+    per = fsa.fsa_cache_page_bytes(page, Hkv, D, "NVFP4")
+    pages = (5 << 30) // per
+    cache = fsa.empty_cache(pages, page, Hkv, D, "NVFP4")
+    g = gen(51)
+    lens = [130]
+    table = i32([[pages - 1, 2, pages - 7]])
+    k, v = normal(g, 1, 130, Hkv, D), normal(g, 1, 130, Hkv, D)
+    fsa.fsa_cache_append(cache, k, v, table, i32(lens))
+    kb, _ = fsa.fsa_cache_read(cache, table, i32(lens), 130)
+    assert torch.equal(kb.double(), ref.rounded(k, "NVFP4"))
+    small = fsa.MxCache(cache.pages[[pages - 1, 2, pages - 7]].contiguous(), page, Hkv, D, "NVFP4")
+    q = normal(g, 1, 1, 32, D)
+    out = fsa.fsa_attention_cache(q, cache, table, i32(lens))
+    assert torch.equal(out, fsa.fsa_attention_cache(q, small, i32([[0, 1, 2]]), i32(lens)))
+    run_attention(fsa, q, small, i32([[0, 1, 2]]), lens)
+
+
+def test_attention_workspace_streams_and_graph():
+    """A given workspace with any content, another stream, a captured call that follows the
+    lengths and the cache, and the same bits each time."""
+    fsa = _fsa()
+    g = gen(61)
+    Hkv, D, H = 4, 128, 16
+    cache, table, _, _ = filled_cache(fsa, g, [900, 4000], 64, Hkv, D, "E2M1")
+    q = normal(g, 2, 1, H, D)
+    lens = i32([900, 4000])
+    first = fsa.fsa_attention_cache(q, cache, table, lens)
+    ws = torch.full((fsa.fsa_attention_cache_workspace(2, H, Hkv, 1, D),), 0xFF, dtype=torch.uint8, device="cuda")
+    for _ in range(5):
+        assert torch.equal(first, fsa.fsa_attention_cache(q, cache, table, lens, workspace=ws))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = fsa.fsa_attention_cache(q, cache, table, lens, stream=side)
+    side.synchronize()
+    assert torch.equal(first, other)
+    out = torch.zeros(2, 1, H, D, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fsa.fsa_attention_cache(q, cache, table, lens, out=out, workspace=ws)
+    for n in ([900, 4000], [1, 17], [0, 3999], [640, 64]):
+        lens.copy_(i32(n))
+        graph.replay()
+        torch.cuda.synchronize()
+        check_attention(q, cache, table, n, [1, 1], True, D ** -0.5, out, None, out)
+
+
+def test_two_calls_at_once():
+    """Two captured calls with a workspace each, replayed on two streams together."""
+    fsa = _fsa()
+    g = gen(71)
+    Hkv, D, H = 2, 64, 8
+    made = []
+    for n in ([3000, 5], [1200, 2500]):
+        cache, table, _, _ = filled_cache(fsa, g, n, 16, Hkv, D, "NVFP4")
+        q = normal(g, 2, 2, H, D)
+        want = fsa.fsa_attention_cache(q, cache, table, i32(n))
+        ws = torch.empty(fsa.fsa_attention_cache_workspace(2, H, Hkv, 2, D), dtype=torch.uint8, device="cuda")
+        out, lens = torch.zeros_like(want), i32(n)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            fsa.fsa_attention_cache(q, cache, table, lens, out=out, workspace=ws)
+        made.append((graph, out, want, torch.cuda.Stream(), (cache, table, q, ws, lens)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for graph, _, _, stream, _ in made:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, out, want, _, _ in made:
+        assert torch.equal(out, want)
+
+
+# ------------------------------------------------------------------------ norm and rotation
+ROPE = [
+    # B, S, H, Hkv, D, rotary, sections, interleaved, norm, weights
+    (1, 1, 1, 1, 64, 64, (32,), False, True, True),
+    (2, 33, 5, 1, 128, 128, (64,), False, True, True),
+    (2, 33, 5, 1, 128, 128, (64,), True, True, False),
+    (1, 130, 14, 2, 64, 32, (16,), False, False, False),
+    (3, 7, 4, 2, 128, 40, (9, 0, 11), True, True, True),
+    (1, 2500, 8, 8, 128, 128, (22, 21, 21), True, True, True),
+    (2, 2100, 4, 1, 128, 96, (40, 8), False, True, True),
+    (1, 9, 3, 1, 128, 8, (4,), False, True, True),
+    (2, 5, 2, 1, 64, 0, (0,), False, True, True),
+]
+
+
+@pytest.mark.parametrize("B,S,H,Hkv,D,rotary,sections,interleaved,norm,weights", ROPE)
+def test_norm_rope(B, S, H, Hkv, D, rotary, sections, interleaved, norm, weights):
+    fsa = _fsa()
+    g = gen(S + D)
+    qkv = normal(g, B, S, H + 2 * Hkv, D)
+    q, k = qkv[:, :, :H], qkv[:, :, H:H + Hkv]
+    q[0, 0, 0] = 0.0
+    half, axes = rotary // 2, len(sections)
+    pos = torch.randint(-1000, 1 << 21, (B, S, axes), generator=g, device="cuda").to(torch.int32)
+    inv = 1e5 ** (-torch.arange(half, device="cuda", dtype=torch.float64) / max(1, half)) if half else None
+    wq, wk = (normal(g, D) if weights else None for _ in range(2))
+    ko = torch.empty(B, Hkv, S, D, dtype=torch.bfloat16, device="cuda")
+    qo, got_k = fsa.fsa_qk_norm_rope(q, k, pos if half else None, inv, sections=sections, q_weight=wq, k_weight=wk,
+                                     norm=norm, eps=1e-5, interleaved=interleaved, k_out=ko.transpose(1, 2))
+    for got, x, w in ((qo, q, wq), (got_k, k, wk)):
+        want, size = ref.norm_rope(x, w, pos, inv, sections if half else (), norm, 1e-5, interleaved)
+        assert bool(((got.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -20 * size + 1e-36).all())
+    fsa.fsa_qk_norm_rope(q, k, pos if half else None, inv, sections=sections, q_weight=wq, k_weight=wk, norm=norm,
+                         eps=1e-5, interleaved=interleaved, q_out=q, k_out=k)          # in place
+    assert torch.equal(q, qo) and torch.equal(k, got_k)
+
+
+def test_norm_rope_positions():
+    """The extremes of int32, and that a turn by position differs from its neighbours' as it should."""
+    fsa = _fsa()
+    D = 64
+    q = torch.zeros(1, 6, 1, D, dtype=torch.bfloat16, device="cuda")
+    q[..., : D // 2] = 1.0
+    pos = i32([[0, 1, -1, 2 ** 24 + 1, 2 ** 31 - 1, -2 ** 31]])
+    inv = torch.linspace(1.0, 1e-4, D // 2, device="cuda", dtype=torch.float64)
+    out, _ = fsa.fsa_qk_norm_rope(q, q.clone(), pos, inv, norm=False)
+    t = pos[0].double()[:, None] * inv
+    want = torch.cat((torch.cos(t), torch.sin(t)), dim=-1)
+    # 2^-16 of a turn at the ends of the range, 2^-24 within 2^24
+    tol = torch.tensor([2.0 ** -20] * 4 + [2 * math.pi * 2.0 ** -16] * 2, device="cuda")[:, None]
+    assert bool(((out[0, :, 0].double() - want).abs() <= 2.0 ** -8 * want.abs() + tol).all())
+
+
+# ------------------------------------------------------------------------- a run of them all
+@pytest.mark.parametrize("fmt", ["E2M1", "NVFP4"])
+def test_prompt_then_steps(fmt):
+    """A prompt and then single tokens, as a server runs them: prepare q and k, write k and v,
+    attend.  The prompt's attention over the cache agrees with the prompt's own MX attention
+    (fsa_attention_fwd_bf16) on the values read back, and each step with the definition."""
+    fsa = _fsa()
+    g = gen(81)
+    B, H, Hkv, D, page, S = 2, 8, 2, 128, 64, 150
+    inv = 1e4 ** (-torch.arange(D // 2, device="cuda", dtype=torch.float64) / (D // 2))
+    w = [normal(g, D) * 0.1 + 1 for _ in range(2)]
+    table, pages = make_table(g, [S + 8] * B, page)
+    cache = fsa.empty_cache(pages, page, Hkv, D, fmt)
+    n = 0
+    for new in (S, 1, 1, 3):
+        qkv = normal(g, B, new, H + 2 * Hkv, D)
+        pos = (torch.arange(n, n + new, device="cuda", dtype=torch.int32)[None].expand(B, new)).contiguous()
+        q, k = fsa.fsa_qk_norm_rope(qkv[:, :, :H], qkv[:, :, H:H + Hkv], pos, inv, q_weight=w[0], k_weight=w[1])
+        n += new
+        lens = i32([n] * B)
+        fsa.fsa_cache_append(cache, k, qkv[:, :, H + Hkv:], table, lens)
+        out, _ = run_attention(fsa, q, cache, table, [n] * B)
+        if new == S:
+            kb, vb = fsa.fsa_cache_read(cache, table, lens, n)
+            heads = lambda x: x.transpose(1, 2).contiguous()  # noqa: E731
+            vt = fsa.fsa_bf16_transpose_v(heads(vb))
+            whole = fsa.fsa_attention_fwd_bf16(heads(q), heads(kb), vt, causal=True).transpose(1, 2)
+            # the BF16 kernel rounds its probabilities to bf16: 2^-8 of sum p|v|, at most the largest |v|
+            assert float((whole - out).abs().max()) <= (2.0 ** -8 + 2.0 ** -10) * float(vb.abs().max())
