@@ -5,7 +5,9 @@ compiled library every entry point raises."""
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 import threading
 
 import torch
@@ -136,13 +138,12 @@ def load(build_if_missing: bool = True):
             L.fsa_attention_fwd_host.argtypes = [ctypes.POINTER(fsa_host_io), ctypes.POINTER(fsa_device_io),
                                                  i, i, i, i, i, i, i, f, i, i, ctypes.POINTER(fsa_opts), vp, i, vp]
             L.fsa_tune_delta.argtypes = [ctypes.POINTER(fsa_stats), i, f, f, f, ctypes.POINTER(ctypes.c_float)]
-            L.fsa_qk_norm_rope.argtypes = [ctypes.POINTER(fsa_norm_rope), vp]
+            L.fsa_qk_norm_rope.argtypes = [vp, vp]                  # packed fsa_norm_rope
             L.fsa_cache_page_bytes.argtypes = [i, i, i, i, ctypes.POINTER(ctypes.c_size_t)]
             for n in ("fsa_cache_append", "fsa_cache_read"):
-                getattr(L, n).argtypes = [ctypes.POINTER(fsa_cache), vp, vp, ctypes.POINTER(fsa_strides),
-                                          ctypes.POINTER(fsa_strides), i, i, vp, i, vp, vp, vp, vp]
+                getattr(L, n).argtypes = [ctypes.POINTER(fsa_cache), vp, vp, vp, vp, i, i, vp, i, vp, vp, vp, vp]
             L.fsa_attention_cache_workspace.argtypes = [i, i, i, i, i, ctypes.POINTER(ctypes.c_size_t)]
-            L.fsa_attention_cache.argtypes = [ctypes.POINTER(fsa_cache_attn), vp]
+            L.fsa_attention_cache.argtypes = [vp, vp]               # packed fsa_cache_attn
             L.fsa_mma_peak.argtypes = [i, i, i, ctypes.c_longlong, vp, ctypes.POINTER(ctypes.c_double), vp]
             L.fsa_bf16_transpose_v.argtypes = [vp, vp, i, i, i, i, vp]
             L.fsa_attention_fwd_bf16.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, i, f, vp, vp]
@@ -555,37 +556,55 @@ def fsa_tune_delta(stats: list, deltas: list, target_rate=0.01, step=4.0, max_de
 
 
 # ----------------------------------------------------------------------------- serving
-def _strided(t: torch.Tensor, name: str, device, heads=None, output=False, dtype=torch.bfloat16) -> fsa_strides:
-    """Strides of a [B,S,heads,D] tensor of `dtype` on `device`, its rows contiguous, 16-byte
-    aligned and, for an output, apart."""
-    if not t.is_cuda:
-        raise FsaError(FSA_ERR_INVALID_ARG, f"{name} must be a CUDA tensor")
-    if t.dtype != dtype or t.dim() != 4 or t.device != device:
-        raise FsaError(FSA_ERR_INVALID_ARG, f"{name} must be a 4-dimensional {dtype} tensor on {device}")
-    if heads is not None and t.shape[2] != heads:
-        raise FsaError(FSA_ERR_INVALID_ARG, f"{name} must have {heads} heads")
-    b, s, h, d = t.stride()
+# These calls are short (a decode step's kernels run for a few microseconds), so their
+# marshalling is too: one packed argument block a call, integer device numbers, the raw
+# stream.  The packed layouts are those of the C structures above (checked on import).
+_ROPE_ARGS = struct.Struct("@4P12q4P7i3i2if0P")
+_ATTN_ARGS = struct.Struct("@3PP3PPNP6q6ifI")
+_STRIDES = struct.Struct("@3q")
+assert _ROPE_ARGS.size == ctypes.sizeof(fsa_norm_rope) and _ATTN_ARGS.size == ctypes.sizeof(fsa_cache_attn)
+
+
+def _strided(t: torch.Tensor, name: str, device: int, output=False, dtype=torch.bfloat16) -> tuple:
+    """Strides of a [B,S,heads,D] tensor of `dtype` on CUDA device number `device`, its rows
+    contiguous, 16-byte aligned and, for an output, apart."""
+    if t.get_device() != device or device < 0:
+        raise FsaError(FSA_ERR_INVALID_ARG, f"{name} must be a CUDA tensor on the call's device")
+    st = t.stride()
+    if len(st) != 4 or t.dtype != dtype:
+        raise FsaError(FSA_ERR_INVALID_ARG, f"{name} must be a 4-dimensional {dtype} tensor")
+    b, s, h, d = st
     if d != 1:
         raise FsaError(FSA_ERR_INVALID_ARG, f"{name} must be contiguous in its last dimension")
-    for n, st in zip(t.shape, (b, s, h)):
-        if n > 1 and (st % 8 or (output and st == 0)):
-            raise FsaError(FSA_ERR_INVALID_ARG, f"{name} strides must be multiples of 8"
-                                                + (", and an output's rows apart" if output else ""))
-    return fsa_strides(b, s, h)
+    if (b | s | h) & 7 or (output and not (b and s and h)):
+        for n, x in zip(t.shape, (b, s, h)):
+            if n > 1 and (x & 7 or (output and not x)):
+                raise FsaError(FSA_ERR_INVALID_ARG, f"{name} strides must be multiples of 8"
+                                                    + (", and an output's rows apart" if output else ""))
+    return b, s, h
 
 
-def _index(t, name: str, shape, device, dtype=torch.int32) -> int:
+def _index(t, name: str, shape: tuple, device: int, dtype=torch.int32) -> int:
     """Pointer of a contiguous integer (or other) tensor of the given shape (None: null)."""
     if t is None:
         return 0
-    if not t.is_cuda or t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
-        raise FsaError(FSA_ERR_INVALID_ARG, f"{name} must be a contiguous {dtype} CUDA tensor {tuple(shape)} on {device}")
+    if t.get_device() != device or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise FsaError(FSA_ERR_INVALID_ARG, f"{name} must be a contiguous {dtype} CUDA tensor {shape} on the call's device")
     return t.data_ptr()
 
 
-def _on(device):
-    """The device of a call's tensors as the current one (kernels launch on the current device)."""
-    return torch.cuda.device(device)
+def _launch(name: str, device: int, stream, *args):
+    """Call `name` with the tensors' device as the current one (kernels launch on that), on
+    `stream` or the device's current stream."""
+    fn = getattr(_lib or load(), name)
+    raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == device:
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, raw)
+    if status != FSA_OK:
+        raise FsaError(status, name)
 
 
 def fsa_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor | None, inv_freq: torch.Tensor | None, *,
@@ -596,42 +615,43 @@ def fsa_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor | None,
     position, in one pass.  pos: int32 [B,S] or [B,S,axes]; inv_freq: float64 [rotary/2];
     sections: pairs of each axis (default: all of one).  q_out, k_out default to contiguous
     tensors of q's and k's shapes; q and k themselves rotate in place.  Returns (q_out, k_out)."""
-    dev = q.device
-    qs = _strided(q, "q", dev)
-    ks = _strided(k, "k", dev)
-    B, S, H, D = q.shape
-    if k.shape[0] != B or k.shape[1] != S or k.shape[3] != D:
+    dev = q.get_device()
+    qs, ks = _strided(q, "q", dev), _strided(k, "k", dev)
+    shape, k_shape = q.shape, k.shape
+    B, S, H, D = shape
+    Bk, Sk, Hkv, Dk = k_shape
+    if Bk != B or Sk != S or Dk != D:
         raise FsaError(FSA_ERR_INVALID_ARG, "q, k shapes")
-    half, axes = 0, 1
+    half, axes, at, freq = 0, 1, 0, 0
     if inv_freq is not None:
         half = inv_freq.numel()
-        _index(inv_freq, "inv_freq", (half,), dev, torch.float64)
+        freq = _index(inv_freq, "inv_freq", (half,), dev, torch.float64)
         if pos is None:
             raise FsaError(FSA_ERR_INVALID_ARG, "a rotation needs pos")
-        axes = 1 if pos.dim() == 2 else pos.shape[-1]
-        _index(pos, "pos", (B, S) if pos.dim() == 2 else (B, S, axes), dev)
-    sections = (half,) if sections is None else tuple(int(x) for x in sections)
+        if pos.dim() == 2:
+            at = _index(pos, "pos", (B, S), dev)
+        else:
+            axes = pos.shape[-1]
+            at = _index(pos, "pos", (B, S, axes), dev)
+    sections = (half,) if sections is None else tuple(sections)
     if len(sections) != axes or axes > 3:
         raise FsaError(FSA_ERR_INVALID_ARG, f"{len(sections)} sections for {axes} axes (1 to 3)")
     if q_out is None:
-        q_out = torch.empty((B, S, H, D), dtype=q.dtype, device=dev)
+        q_out = torch.empty(shape, dtype=q.dtype, device=q.device)
     if k_out is None:
-        k_out = torch.empty(tuple(k.shape), dtype=k.dtype, device=dev)
-    qos = _strided(q_out, "q_out", dev, output=True)
-    kos = _strided(k_out, "k_out", dev, output=True)
-    if q_out.shape != q.shape or k_out.shape != k.shape:
+        k_out = torch.empty(k_shape, dtype=k.dtype, device=k.device)
+    if q_out.shape != shape or k_out.shape != k_shape:
         raise FsaError(FSA_ERR_INVALID_ARG, "q_out, k_out shapes")
-    args = fsa_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), qs, ks, qos, kos,
-                         _index(q_weight, "q_weight", (D,), dev, torch.bfloat16),
-                         _index(k_weight, "k_weight", (D,), dev, torch.bfloat16),
-                         pos.data_ptr() if half else 0, inv_freq.data_ptr() if half else 0, B, S, H, k.shape[2], D,
-                         2 * half, axes, (ctypes.c_int32 * 3)(*sections), int(bool(norm)), int(bool(interleaved)),
-                         float(eps))
-    with _on(dev):
-        _check(load().fsa_qk_norm_rope(ctypes.byref(args), _stream(stream)), "fsa_qk_norm_rope")
+    args = _ROPE_ARGS.pack(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), *qs, *ks,
+                           *_strided(q_out, "q_out", dev, True), *_strided(k_out, "k_out", dev, True),
+                           _index(q_weight, "q_weight", (D,), dev, torch.bfloat16),
+                           _index(k_weight, "k_weight", (D,), dev, torch.bfloat16), at, freq, B, S, H, Hkv, D,
+                           2 * half, axes, *sections, *(0,) * (3 - axes), 1 if norm else 0, 1 if interleaved else 0, eps)
+    _launch("fsa_qk_norm_rope", dev, stream, args)
     return q_out, k_out
 
 
+@functools.lru_cache(maxsize=256)
 def fsa_cache_page_bytes(page_size, Hkv, D, fmt) -> int:
     n = ctypes.c_size_t()
     _check(load().fsa_cache_page_bytes(int(page_size), int(Hkv), int(D), _fmt(fmt), ctypes.byref(n)), "fsa_cache_page_bytes")
@@ -643,16 +663,17 @@ class MxCache:
     tensor [num_pages, fsa_cache_page_bytes] on the GPU, owned by torch."""
 
     def __init__(self, pages: torch.Tensor, page_size: int, Hkv: int, D: int, fmt):
-        self.pages, self.page_size, self.Hkv, self.D, self.fmt = pages, int(page_size), int(Hkv), int(D), _fmt(fmt)
+        self.pages, self.page_size, self.Hkv, self.D, self.fmt = pages, page_size, Hkv, D, _fmt(fmt)
         n = fsa_cache_page_bytes(page_size, Hkv, D, self.fmt)
         if not isinstance(pages, torch.Tensor) or pages.dtype != torch.uint8 or pages.dim() != 2 or pages.shape[1] != n \
                 or not pages.is_contiguous():
             raise FsaError(FSA_ERR_INVALID_ARG, f"pages must be a contiguous uint8 tensor [num_pages, {n}]")
 
     def struct(self) -> fsa_cache:
-        if not self.pages.is_cuda:
+        pages = self.pages
+        if pages.get_device() < 0:
             raise FsaError(FSA_ERR_INVALID_ARG, "pages must be a CUDA tensor")
-        return fsa_cache(self.pages.data_ptr(), self.pages.shape[0], self.page_size, self.Hkv, self.D, self.fmt)
+        return fsa_cache(pages.data_ptr(), pages.shape[0], self.page_size, self.Hkv, self.D, self.fmt)
 
 
 def empty_cache(num_pages, page_size, Hkv, D, fmt, device=None) -> MxCache:
@@ -661,10 +682,11 @@ def empty_cache(num_pages, page_size, Hkv, D, fmt, device=None) -> MxCache:
     return MxCache(torch.empty((num_pages, n), dtype=torch.uint8, device=device or "cuda"), page_size, Hkv, D, fmt)
 
 
-def _table(block_table: torch.Tensor, B, device) -> int:
-    if block_table.dim() != 2 or block_table.shape[0] != B:
+def _table(block_table: torch.Tensor, B: int, device: int) -> tuple:
+    shape = block_table.shape
+    if len(shape) != 2 or shape[0] != B:
         raise FsaError(FSA_ERR_INVALID_ARG, "block_table must be [B, max_pages]")
-    return _index(block_table, "block_table", block_table.shape, device)
+    return _index(block_table, "block_table", shape, device), shape[1]
 
 
 def fsa_cache_append(cache: MxCache, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor,
@@ -672,18 +694,16 @@ def fsa_cache_append(cache: MxCache, k: torch.Tensor, v: torch.Tensor, block_tab
     """Quantise k, v (bf16 [B,S,Hkv,D], strided) into the cache: row i < new_lens[b] (default
     all S) becomes token lens[b] - new_lens[b] + i of the sequence whose pages row b of
     block_table (int32 [B, max_pages]) names.  lens (int32 [B]) counts the new tokens too."""
-    dev = cache.pages.device
     c = cache.struct()
-    ks = _strided(k, "k", dev, cache.Hkv)
-    vs = _strided(v, "v", dev, cache.Hkv)
-    B, S, _, D = k.shape
-    if v.shape != k.shape or D != cache.D:
+    dev = cache.pages.get_device()
+    ks, vs = _strided(k, "k", dev), _strided(v, "v", dev)
+    B, S, Hkv, D = shape = k.shape
+    if v.shape != shape or D != cache.D or Hkv != cache.Hkv:
         raise FsaError(FSA_ERR_INVALID_ARG, "k, v shapes")
-    args = (ctypes.byref(c), k.data_ptr(), v.data_ptr(), ctypes.byref(ks), ctypes.byref(vs), B, S,
-            _table(block_table, B, dev), block_table.shape[1], _index(lens, "lens", (B,), dev),
-            _index(new_lens, "new_lens", (B,), dev), _index(status, "status", (1,), dev))
-    with _on(dev):
-        _check(load().fsa_cache_append(*args, _stream(stream)), "fsa_cache_append")
+    table, width = _table(block_table, B, dev)
+    _launch("fsa_cache_append", dev, stream, c, k.data_ptr(), v.data_ptr(), _STRIDES.pack(*ks), _STRIDES.pack(*vs), B, S,
+            table, width, _index(lens, "lens", (B,), dev), _index(new_lens, "new_lens", (B,), dev),
+            _index(status, "status", (1,), dev))
 
 
 def fsa_cache_read(cache: MxCache, block_table: torch.Tensor, lens: torch.Tensor, S: int | None = None, *,
@@ -693,31 +713,26 @@ def fsa_cache_read(cache: MxCache, block_table: torch.Tensor, lens: torch.Tensor
     start 0) where that lies before lens[b]; other rows are left as they were.  k_out, v_out:
     bf16 [B,S,Hkv,D], strided; without either, both are made (zeros, S rows).  Returns
     (k_out, v_out)."""
-    dev = cache.pages.device
     c = cache.struct()
+    dev = cache.pages.get_device()
     B = lens.shape[0]
     if k_out is None and v_out is None:
         if S is None:
             raise FsaError(FSA_ERR_INVALID_ARG, "S, k_out or v_out must be given")
-        k_out = torch.zeros((B, S, cache.Hkv, cache.D), dtype=torch.bfloat16, device=dev)
+        k_out = torch.zeros((B, S, cache.Hkv, cache.D), dtype=torch.bfloat16, device=cache.pages.device)
         v_out = torch.zeros_like(k_out)
-    some = v_out if k_out is None else k_out
-    S = some.shape[1] if S is None else S
-    ptr, strides = [], []
-    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is None:
-            ptr.append(0)
-            strides.append(fsa_strides())
-            continue
-        strides.append(_strided(t, n, dev, cache.Hkv, output=True))
-        if t.shape[0] != B or t.shape[1] != S or t.shape[3] != cache.D:
-            raise FsaError(FSA_ERR_INVALID_ARG, f"{n} must be [B, S, Hkv, D]")
-        ptr.append(t.data_ptr())
-    args = (ctypes.byref(c), ptr[0], ptr[1], ctypes.byref(strides[0]), ctypes.byref(strides[1]), B, S,
-            _table(block_table, B, dev), block_table.shape[1], _index(lens, "lens", (B,), dev),
+    S = (v_out if k_out is None else k_out).shape[1] if S is None else S
+    ptr, strides = [0, 0], [None, None]
+    for i, t in enumerate((k_out, v_out)):
+        if t is not None:
+            n = "v_out" if i else "k_out"
+            strides[i] = _STRIDES.pack(*_strided(t, n, dev, True))
+            if t.shape != (B, S, cache.Hkv, cache.D):
+                raise FsaError(FSA_ERR_INVALID_ARG, f"{n} must be [B, S, Hkv, D]")
+            ptr[i] = t.data_ptr()
+    table, width = _table(block_table, B, dev)
+    _launch("fsa_cache_read", dev, stream, c, *ptr, *strides, B, S, table, width, _index(lens, "lens", (B,), dev),
             _index(start, "start", (B,), dev), _index(status, "status", (1,), dev))
-    with _on(dev):
-        _check(load().fsa_cache_read(*args, _stream(stream)), "fsa_cache_read")
     return k_out, v_out
 
 
@@ -739,35 +754,32 @@ def fsa_attention_cache(q: torch.Tensor, cache: MxCache, block_table: torch.Tens
     q_lens[b] are left as they were.  lse: optional fp32 [B,Sq,H] for the log of the
     softmax sums.  workspace: uint8, at least fsa_attention_cache_workspace bytes (default:
     one of the call's own)."""
-    dev = cache.pages.device
     c = cache.struct()
+    dev = cache.pages.get_device()
     qs = _strided(q, "q", dev)
-    B, Sq, H, D = q.shape
+    B, Sq, H, D = shape = q.shape
     if D != cache.D or H % cache.Hkv:
         raise FsaError(FSA_ERR_INVALID_ARG, "q must have the cache's D and a multiple of its heads")
     od, tdt = _out_dtype(out_dtype if out is None or out_dtype is not None else out.dtype)
     if out is None:
-        out = torch.empty((B, Sq, H, D), dtype=tdt, device=dev) if q_lens is None else \
-            torch.zeros((B, Sq, H, D), dtype=tdt, device=dev)
-    os_ = _strided(out, "out", dev, output=True, dtype=tdt)
-    if out.shape != q.shape:
+        out = (torch.empty if q_lens is None else torch.zeros)(shape, dtype=tdt, device=q.device)
+    os_ = _strided(out, "out", dev, True, tdt)
+    if out.shape != shape:
         raise FsaError(FSA_ERR_INVALID_ARG, "out must have q's shape")
-    tab, ln = _table(block_table, B, dev), _index(lens, "lens", (B,), dev)
-    ql, st = _index(q_lens, "q_lens", (B,), dev), _index(status, "status", (1,), dev)
-    le = _index(lse, "lse", (B, Sq, H), dev, torch.float32)
-    with _on(dev):
-        if workspace is None:
-            workspace = torch.empty(fsa_attention_cache_workspace(B, H, cache.Hkv, Sq, D), dtype=torch.uint8, device=dev)
-            if stream is not None:
-                workspace.record_stream(stream)
-        else:
-            _need_cuda(workspace, "workspace", torch.uint8)
-            if workspace.device != dev:
-                raise FsaError(FSA_ERR_INVALID_ARG, f"workspace is on {workspace.device}, the call on {dev}")
-        args = fsa_cache_attn(q.data_ptr(), out.data_ptr(), le, ctypes.pointer(c), tab, ln, ql, workspace.data_ptr(),
-                              workspace.numel(), st, qs, os_, B, H, Sq, block_table.shape[1], int(bool(causal)), od,
-                              D ** -0.5 if scale is None else float(scale), int(timeout_ms))
-        _check(load().fsa_attention_cache(ctypes.byref(args), _stream(stream)), "fsa_attention_cache")
+    if workspace is None:
+        with torch.cuda.device(dev):
+            need = fsa_attention_cache_workspace(B, H, cache.Hkv, Sq, D)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        if stream is not None:
+            workspace.record_stream(stream)
+    table, width = _table(block_table, B, dev)
+    space = _index(workspace, "workspace", (workspace.numel(),), dev, torch.uint8)
+    args = _ATTN_ARGS.pack(q.data_ptr(), out.data_ptr(), _index(lse, "lse", (B, Sq, H), dev, torch.float32),
+                           ctypes.addressof(c), table, _index(lens, "lens", (B,), dev),
+                           _index(q_lens, "q_lens", (B,), dev), space, workspace.numel(),
+                           _index(status, "status", (1,), dev), *qs, *os_, B, H, Sq, width, 1 if causal else 0, od,
+                           D ** -0.5 if scale is None else scale, timeout_ms)
+    _launch("fsa_attention_cache", dev, stream, args)
     return out
 
 
