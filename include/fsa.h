@@ -472,8 +472,8 @@ int fsa_cache_read(const fsa_cache* cache, void* k, void* v, const fsa_strides* 
 /* Attention of few query rows over the cache (decode steps, guessed tokens, chunks of a
  * prompt): O = softmax(scale Q K^T) V on the values the cache stands for; q is not
  * quantised, sums and softmax statistics are fp32, probabilities times V's scales are
- * rounded to f16 (2^-12) before the product with the codes of V, exact down to 2^-28 of
- * the largest.  Query head h reads kv head h / (H/Hkv).  Row i < q_lens[b] of sequence b
+ * rounded to f16 before the product with the codes of V (2^-11 relative, 2^-10 with
+ * NVFP4; an absolute 2^-33 of the largest for those far below it).  Query head h reads kv head h / (H/Hkv).  Row i < q_lens[b] of sequence b
  * stands at position lens[b] - q_lens[b] + i and sees the keys up to its own position
  * (causal) or all lens[b]; lens counts the rows' own tokens, which are in the cache
  * already.  A row that sees nothing gives zeros (lse -inf).  Rows behind q_lens[b] are not

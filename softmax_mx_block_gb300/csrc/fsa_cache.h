@@ -71,8 +71,8 @@ struct CacheAttnArgs {
   const int32_t* table;
   const int32_t* lens;
   const int32_t* q_lens;  // null: Sq each
-  float* partials;        // workspace
-  int4* starts;           // workspace: per warp, the segment that begins in it and goes on
+  float* partials;        // workspace: two partial results a CTA
+  int4* starts;           // workspace: per CTA, the segment that begins in it and goes on, and the CTA where it ends
   int B, H, Sq, G, CT, max_pages, causal, out_bf16;
   float scale_log2;       // |scale| log2 e, or 1 when the scale is 0
   float q_sign;           // the scale's sign (0 for a zero scale)

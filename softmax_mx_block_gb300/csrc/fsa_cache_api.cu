@@ -173,7 +173,8 @@ int fsa_attention_cache_workspace(int B, int H, int Hkv, int Sq, int D, size_t* 
   if (!bytes || !attn_shape_ok(B, H, Hkv, Sq, D)) return FSA_ERR_INVALID_ARG;
   int sms = 0;
   if (!sm_count(&sms)) return FSA_ERR_NO_DEVICE;
-  *bytes = fsa::cache_attn_workspace(fsa::cache_attn_ntiles(Sq * (H / Hkv)), D, sms, nullptr);
+  size_t starts_at;
+  *bytes = fsa::cache_attn_workspace(fsa::cache_attn_ntiles(Sq * (H / Hkv)), D, sms, &starts_at);
   return FSA_OK;
 }
 
@@ -195,7 +196,7 @@ int fsa_attention_cache(const fsa_cache_attn* c, void* stream) {
   int sms = 0;
   if (!sm_count(&sms)) return FSA_ERR_NO_DEVICE;
   const int G = c->H / Hkv, nt = fsa::cache_attn_ntiles(c->Sq * G);
-  size_t starts_at = 0;
+  size_t starts_at;
   if (c->workspace_bytes < fsa::cache_attn_workspace(nt, D, sms, &starts_at)) return FSA_ERR_INVALID_ARG;
   a.q = static_cast<const uint16_t*>(c->q);
   a.out = c->out;

@@ -33,27 +33,38 @@
 namespace fsa {
 namespace {
 
-constexpr int NWC = 12;             // warps of a CTA
+#ifndef NW1
+#define NW1 12
+#endif
+// warps of a CTA, by the registers that a warp's columns take
+template <int D, int NT>
+__host__ __device__ constexpr int cta_warps() { return NT == 1 ? NW1 : D == 128 ? 8 : 12; }
 constexpr int STG = 3;              // stages of a warp's ring
 constexpr int TILE = 32;            // keys of a tile
+#ifndef EXTRA_TILES
+#define EXTRA_TILES 2
+#endif
+constexpr int EXTRA = EXTRA_TILES;  // what a segment's start costs a warp, in tiles
 constexpr float M_NONE = -1e30f;    // maximum of no keys
 constexpr float LAZY = 4.0f;        // log2 of how far a score may beat M
 
 template <int D, int CF, int NT>
 struct Cfg {
   using Gr = CacheGroup<D, CF>;
+  static constexpr int NWC = cta_warps<D, NT>();
   static constexpr int STAGE = 2 * Gr::BYTES;
   static constexpr int COLS = 8 * NT;
   static constexpr int PART = COLS * (D + 2);        // floats of a partial result: rows, maxima, sums
   static constexpr int RING = NWC * STG * STAGE;
   static constexpr int JOIN = NWC * PART * 4;
-  static constexpr int SMEM = 1024 + NWC * 32 * 8 + (RING > JOIN ? RING : JOIN);
+  static constexpr int SMEM = 1024 + NWC * 32 * 8 + JOIN + (RING > JOIN ? RING : JOIN);
 };
 
 // ---------------------------------------------------------------- the work list
 // "Virtual sequence" vb = b * CT + ct: the ct-th pass of columns of sequence b.
 struct Span {
   int qlen, len, kmax, tiles;   // rows, keys, keys that some column sees, tiles (0: no rows)
+  __device__ __forceinline__ int units() const { return tiles ? tiles + EXTRA : 0; }
 };
 __device__ __forceinline__ Span span_of(const CacheAttnArgs& p, int vb, int cols) {
   Span s;
@@ -68,6 +79,26 @@ __device__ __forceinline__ Span span_of(const CacheAttnArgs& p, int vb, int cols
   return s;
 }
 
+// 64-bit quotient of non-negative numbers, by 32-bit division where they fit
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// `total` tiles over n warps: the first `more` of them take base + 1, the others base.
+struct Shares {
+  int64_t base;
+  int more;
+  __device__ __forceinline__ Shares(int64_t total, int n) {
+    base = n > 0 ? quotient(total, n) : 0;
+    more = (int)(total - base * n);
+  }
+  __device__ __forceinline__ int64_t first(int w) const { return base * w + min(w, more); }
+  __device__ __forceinline__ int of(int64_t tile) const {      // the warp that has it
+    const int64_t cut = (base + 1) * more;
+    return tile < cut ? (int)quotient(tile, base + 1) : more + (int)quotient(tile - cut, base);
+  }
+};
+
 // Keys that column c of virtual sequence (b, ct) sees (0 for none and for padding).
 __device__ __forceinline__ int limit_of(const CacheAttnArgs& p, const Span& s, int col) {
   const int i = col / p.G;
@@ -75,79 +106,115 @@ __device__ __forceinline__ int limit_of(const CacheAttnArgs& p, const Span& s, i
   return p.causal ? max(0, s.len - s.qlen + i + 1) : s.len;
 }
 
-__device__ __forceinline__ float e8m0_shifted(uint32_t w, int j) {     // 2^(byte j - 127); 0xFF: Inf, 0: 0
-  return __uint_as_float(((w >> (8 * j)) << 23) & 0x7F800000u);
-}
-
-// scale factors of one row's blocks (NB = D/32 or D/16 of them)
+// Scale bytes of one row as packed words: SB/4 of them (D = 64 with E8M0: two bytes of one).
 template <int D, int CF>
-__device__ __forceinline__ void load_scales(const uint8_t* at, float* f) {
-  if constexpr (CF == CF_MX) {
-    const uint32_t w = D == 128 ? *reinterpret_cast<const uint32_t*>(at) : *reinterpret_cast<const uint16_t*>(at);
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j) f[j] = e8m0_shifted(w, j);
-  } else {
-    uint32_t w[2];
-    if constexpr (D == 128) {
+struct RowScales {
+  static constexpr int N = CacheGroup<D, CF>::SB > 4 ? 2 : 1;
+  uint32_t w[N];
+  __device__ __forceinline__ void load(const uint8_t* at) {
+    if constexpr (CacheGroup<D, CF>::SB == 8) {
       const uint2 u = *reinterpret_cast<const uint2*>(at);
       w[0] = u.x; w[1] = u.y;
-    } else {
+    } else if constexpr (CacheGroup<D, CF>::SB == 4) {
       w[0] = *reinterpret_cast<const uint32_t*>(at);
-    }
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j) {               // pairs of E4M3
-      uint32_t h2;
-      asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}"
-          : "=r"(h2) : "r"(j & 1 ? w[j / 2] >> 16 : w[j / 2]));
-      asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n cvt.f32.f16 %0, lo;\n cvt.f32.f16 %1, hi;\n}"
-          : "=f"(f[2 * j]), "=f"(f[2 * j + 1]) : "r"(h2));
+    } else {
+      w[0] = *reinterpret_cast<const uint16_t*>(at);
     }
   }
+};
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t low_twice(uint32_t x) { return __byte_perm(x, x, 0x1010); }
+__device__ __forceinline__ uint32_t high_twice(uint32_t x) { return __byte_perm(x, x, 0x3232); }
+__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t two_bytes) {     // the low two bytes, exact
+  uint32_t r;
+  asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}" : "=r"(r) : "r"(two_bytes));
+  return r;
+}
+
+// Two E8M0 bytes (the low ones of w) as fp32: 2^(byte - 127), NaN for 0xFF.
+__device__ __forceinline__ void e8m0x2_f32(uint32_t w, float& a, float& b) {
+  uint32_t r;
+  asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.bf16x2.ue8m0x2 %0, lo;\n}" : "=r"(r) : "r"(w));
+  a = __uint_as_float(r << 16);
+  b = __uint_as_float(r & 0xFFFF0000u);
 }
 
 // One warp's running state for one (sequence, kv head, pass of columns).  A thread holds,
 // of n-tile n, columns 8n + 2t and + 1 and, of m-tile i, dims 16i + 2g and + 1.
-template <int D, int NT>
+template <int D, int CF, int NT>
 struct Acc {
+  // the offset of V's scales: p carries 2^(8 - r), 2^r above the scales seen, so that p times
+  // a scale fits f16 (E4M3's range is narrow: there r starts at 0)
+  static constexpr int R_MIN = CF == CF_MX ? -80 : 0;
   float o[D / 16][NT][4];   // [dim 16i+2g: col 2t, 2t+1; dim 16i+2g+1: col 2t, 2t+1]
   float l[NT][2];           // this thread's part of the row sums
   float m[NT][2];           // running maximum (log2 units), the same in all g
-  float r;                  // exponent offset of V's scales
-  float vtop;               // 2^(r + 3): a larger scale raises r
+  float top[NT][2];         // a raw score above this raises m
+  float off[NT][2];         // p = exp2(s * cq + off)
+  int r;
+  uint32_t vtop;            // highest scale byte that r allows, as the high bytes of two halves
+
+  __device__ __forceinline__ void set_r(int x) {
+    r = x;
+    const int byte = CF == CF_MX ? min(x + 3 + 127, 254) : min((x + 10) * 8 - 1, 0x7E);
+    vtop = (uint32_t)byte * 0x01000100u | 0x00FF00FFu;
+  }
+  __device__ __forceinline__ void set_m(int n, int e, float x, float cq) {
+    m[n][e] = x;
+    top[n][e] = (x + LAZY) / cq;
+    off[n][e] = 8.f - (float)r - x;
+  }
+  __device__ __forceinline__ void reset(const float (&cq)[NT][2]) {
+    set_r(R_MIN);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][n][e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[n][e] = 0.f;
+        set_m(n, e, M_NONE, cq[n][e]);
+      }
+    }
+  }
+  // After the last tile: o and l in units of 2^(m + r - 8), the sums over all lanes.
+  __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int x = 4; x < 32; x *= 2) l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], x);
+        m[n][e] += (float)r - 8.f;
+      }
+  }
 };
 
-template <int D, int NT>
-__device__ __forceinline__ void reset(Acc<D, NT>& a) {
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) a.o[i][n][e] = 0.f;
-    a.l[n][0] = a.l[n][1] = 0.f;
-    a.m[n][0] = a.m[n][1] = M_NONE;
-  }
-  a.r = -80.f;
-  a.vtop = 0.f;
-}
-
-// One tile of 32 keys from shared memory.  first: position of the tile's first key.
+// One tile of 32 keys from shared memory.  first: position of the tile's first key; bad:
+// its groups without a page.  MASK: some column does not see some key of the tile.
 template <int D, int CF, int NT, bool MASK>
 __device__ __forceinline__ void tile_step(const uint8_t* st, const uint2 (&q)[D / 16][NT], const float (&cq)[NT][2],
-                                          const int (&lim)[NT][2], int first, uint32_t bad, Acc<D, NT>& a) {
+                                          const int (&lim)[NT][2], int first, uint32_t bad, Acc<D, CF, NT>& a) {
   using Gr = CacheGroup<D, CF>;
-  constexpr int NB = CF == CF_MX ? D / 32 : D / 16;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int tok = (g >> 1) + 4 * (g & 1);            // the key of S^T row g (and 8 more for row g + 8)
   float s[2][NT][4];
-  float vs[2][2][NB];
-  float vmax = 0.f;
+  RowScales<D, CF> vs[2][2];
 #pragma unroll
   for (int gr = 0; gr < 2; ++gr) {
     const uint8_t* base = st + gr * Gr::BYTES;
-    float f0[NB], f1[NB];
-    load_scales<D, CF>(base + Gr::KS + tok * Gr::SB, f0);
-    load_scales<D, CF>(base + Gr::KS + (tok + 8) * Gr::SB, f1);
+    RowScales<D, CF> ks[2];
+    ks[0].load(base + Gr::KS + tok * Gr::SB);
+    ks[1].load(base + Gr::KS + (tok + 8) * Gr::SB);
+    vs[gr][0].load(base + Gr::VS + tok * Gr::SB);
+    vs[gr][1].load(base + Gr::VS + (tok + 8) * Gr::SB);
     uint32_t w0[D / 32], w1[D / 32];
     const uint8_t* kr = base + Gr::K + tok * (D / 2) + t * (D / 8);
     if constexpr (D == 128) {
@@ -163,114 +230,155 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint2 (&q)[D 
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[gr][n][e] = 0.f;
+    [[maybe_unused]] float kf0[2], kf1[2];
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) {
       uint32_t r0[4], r1[4];
       cvt_e2m1x8_f16(w0[j], r0);
       cvt_e2m1x8_f16(w1[j], r1);
+      if constexpr (CF == CF_NV) {                   // code times E4M3 scale: 6 bits, exact in f16
+        const uint32_t f0 = e4m3x2_f16(ks[0].w[j / 2] >> (16 * (j & 1))), f1 = e4m3x2_f16(ks[1].w[j / 2] >> (16 * (j & 1)));
+        const uint32_t f0l = low_twice(f0), f0h = high_twice(f0), f1l = low_twice(f1), f1h = high_twice(f1);
+        r0[0] = hmul2(r0[0], f0l); r0[1] = hmul2(r0[1], f0l); r0[2] = hmul2(r0[2], f0h); r0[3] = hmul2(r0[3], f0h);
+        r1[0] = hmul2(r1[0], f1l); r1[1] = hmul2(r1[1], f1l); r1[2] = hmul2(r1[2], f1h); r1[3] = hmul2(r1[3], f1h);
+      }
       const uint32_t lo[4] = {r0[0], r1[0], r0[1], r1[1]}, hi[4] = {r0[2], r1[2], r0[3], r1[3]};
+      if constexpr (CF == CF_NV) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_f16_16816(c, lo, q[2 * j][n].x, q[2 * j][n].y);
-        if constexpr (CF == CF_NV) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) { s[gr][n][e] = fmaf(c[e], e < 2 ? f0[2 * j] : f1[2 * j], s[gr][n][e]); c[e] = 0.f; }
+        for (int n = 0; n < NT; ++n) {
+          mma_f16_16816(s[gr][n], lo, q[2 * j][n].x, q[2 * j][n].y);
+          mma_f16_16816(s[gr][n], hi, q[2 * j + 1][n].x, q[2 * j + 1][n].y);
         }
-        mma_f16_16816(c, hi, q[2 * j + 1][n].x, q[2 * j + 1][n].y);
-        constexpr int S = CF == CF_NV ? 2 : 1;
+      } else {                                       // the E8M0 scale has fp32's range: on the block's sum
+        if ((j & 1) == 0) {
+          e8m0x2_f32(ks[0].w[0] >> (8 * j), kf0[0], kf0[1]);
+          e8m0x2_f32(ks[1].w[0] >> (8 * j), kf1[0], kf1[1]);
+        }
+        const float f0 = kf0[j & 1], f1 = kf1[j & 1];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[gr][n][e] = fmaf(c[e], e < 2 ? f0[S * j + S - 1] : f1[S * j + S - 1], s[gr][n][e]);
+        for (int n = 0; n < NT; ++n) {
+          float c[4];
+          mma_f16_16816_zero(c, lo, q[2 * j][n].x, q[2 * j][n].y);
+          mma_f16_16816(c, hi, q[2 * j + 1][n].x, q[2 * j + 1][n].y);
+          s[gr][n][0] = fmaf(c[0], f0, s[gr][n][0]);
+          s[gr][n][1] = fmaf(c[1], f0, s[gr][n][1]);
+          s[gr][n][2] = fmaf(c[2], f1, s[gr][n][2]);
+          s[gr][n][3] = fmaf(c[3], f1, s[gr][n][3]);
+        }
       }
     }
-    load_scales<D, CF>(base + Gr::VS + tok * Gr::SB, vs[gr][0]);
-    load_scales<D, CF>(base + Gr::VS + (tok + 8) * Gr::SB, vs[gr][1]);
-    if (MASK) {
+  }
+
+  uint32_t seen[2][NT][2];                           // MASK: all ones in the halves (columns) that see the row
+  if (MASK) {
+#pragma unroll
+    for (int gr = 0; gr < 2; ++gr) {
       const int k0 = first + 16 * gr + tok, k1 = k0 + 8;
       const bool gone = (bad >> gr) & 1;
-      bool seen0 = false, seen1 = false;
+      uint32_t any0 = 0, any1 = 0;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n) {
+        seen[gr][n][0] = gone ? 0u : (k0 < lim[n][0] ? 0xFFFFu : 0u) | (k0 < lim[n][1] ? 0xFFFF0000u : 0u);
+        seen[gr][n][1] = gone ? 0u : (k1 < lim[n][0] ? 0xFFFFu : 0u) | (k1 < lim[n][1] ? 0xFFFF0000u : 0u);
+        any0 |= seen[gr][n][0];
+        any1 |= seen[gr][n][1];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (gone || k0 >= lim[n][e]) s[gr][n][e] = -INFINITY; else seen0 = true;
-          if (gone || k1 >= lim[n][e]) s[gr][n][2 + e] = -INFINITY; else seen1 = true;
-        }
-      // a key that none of this thread's columns sees has no part in R either
+        for (int e = 0; e < 4; ++e)
+          if (!(seen[gr][n][e >> 1] & (e & 1 ? 0xFFFF0000u : 0xFFFFu))) s[gr][n][e] = -INFINITY;
+      }
+      // a key that none of this thread's columns sees has no part in r either
 #pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        if (!seen0) vs[gr][0][j] = 0.f;
-        if (!seen1) vs[gr][1][j] = 0.f;
+      for (int x = 0; x < RowScales<D, CF>::N; ++x) {
+        if (!any0) vs[gr][0].w[x] = 0;
+        if (!any1) vs[gr][1].w[x] = 0;
       }
     }
-#pragma unroll
-    for (int j = 0; j < NB; ++j) vmax = fmaxf(vmax, fmaxf(vs[gr][0][j], vs[gr][1][j]));
   }
 
   // raise the running maxima where a score or a scale asks for it
-  bool raise = vmax > a.vtop;
+  uint32_t vm = 0;                                   // largest scale bytes, in the high bytes of the halves
+#pragma unroll
+  for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int x = 0; x < RowScales<D, CF>::N; ++x) vm = __vimax3_u16x2(vm, vs[gr][h].w[x], vs[gr][h].w[x] << 8);
+  bool raise = __vmaxu2(vm, a.vtop) != a.vtop;
   float top[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      top[n][e] = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e])) * cq[n][e];
-      raise |= top[n][e] > a.m[n][e] + LAZY;
+      top[n][e] = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e]));
+      raise |= top[n][e] > a.top[n][e];
     }
   if (__any_sync(0xFFFFFFFFu, raise)) {
-    float v = 0.f;                                     // the largest finite scale (Inf stands for NaN blocks)
+    constexpr uint32_t NAN_BYTE = CF == CF_MX ? 0xFF : 0x7F;
+    uint32_t v = 0;
 #pragma unroll
     for (int gr = 0; gr < 2; ++gr)
 #pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        if (vs[gr][0][j] <= 3.4e38f) v = fmaxf(v, vs[gr][0][j]);
-        if (vs[gr][1][j] <= 3.4e38f) v = fmaxf(v, vs[gr][1][j]);
-      }
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int x = 1; x < 32; x *= 2) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, x));
-    float r = a.r;
-    if (v > a.vtop) {
-      r = fmaxf((float)((int)(__float_as_uint(v) >> 23) - 126), -80.f);     // 2^r > v
-      a.vtop = r > 123.f ? 3.4e38f : exp2f(r + 3.f);
-    }
+        for (int x = 0; x < Gr::SB; ++x) {
+          const uint32_t byte = (vs[gr][h].w[x / 4] >> (8 * (x % 4))) & 0xFF;
+          if (byte != NAN_BYTE) v = max(v, byte);
+        }
+    v = __reduce_max_sync(0xFFFFFFFFu, v);
+    const int r_old = a.r;
+    if (v > (a.vtop >> 24)) a.set_r(max(Acc<D, CF, NT>::R_MIN, CF == CF_MX ? (int)v - 126 : (int)(v >> 3) - 6));   // 2^r > scale
+    const float fr = (float)(r_old - a.r);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float m = top[n][e];
+        float m = top[n][e] * cq[n][e];
 #pragma unroll
         for (int x = 4; x < 32; x *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
         m = fmaxf(a.m[n][e], m);
-        const float f = exp2f((a.m[n][e] + a.r) - (m + r));
-        a.m[n][e] = m;
+        const float f = exp2f(a.m[n][e] - m + fr);
         a.l[n][e] *= f;
+        a.set_m(n, e, m, cq[n][e]);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) { a.o[i][n][e] *= f; a.o[i][n][2 + e] *= f; }
       }
-    a.r = r;
   }
 
   // probabilities, and the products with V
-  float off[NT][2];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) off[n][e] = 8.f - a.r - a.m[n][e];
 #pragma unroll
   for (int gr = 0; gr < 2; ++gr) {
     const uint8_t* base = st + gr * Gr::BYTES;
+    float x4[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float x = ex2_approx(fmaf(s[gr][n][e], cq[n][e & 1], off[n][e & 1]));
-        s[gr][n][e] = x;
-        a.l[n][e & 1] += x;
+        x4[n][e] = ex2_approx(fmaf(s[gr][n][e], cq[n][e & 1], a.off[n][e & 1]));
+        a.l[n][e & 1] += x4[n][e];
       }
+    // E8M0 scales multiply in fp32 and the product is rounded; E4M3 ones multiply p as f16
+    uint32_t p[NT][2], f[2][Gr::SB / 2];
+    float vf[2][Gr::SB];
+    if constexpr (CF == CF_NV) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        p[n][0] = cvt_f16x2(x4[n][0], x4[n][1]);     // row g: columns 2t, 2t + 1
+        p[n][1] = cvt_f16x2(x4[n][2], x4[n][3]);     // row g + 8
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int x = 0; x < Gr::SB / 2; ++x) f[h][x] = e4m3x2_f16(vs[gr][h].w[x / 2] >> (16 * (x & 1)));
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int x = 0; x < Gr::SB; x += 2) e8m0x2_f32(vs[gr][h].w[0] >> (8 * x), vf[h][x], vf[h][x + 1]);
+    }
     // V rows of the keys t, 4 + t, 8 + t, 12 + t, interleaved so that a pair of f16 is one
     // dim of two keys
     const uint8_t* vr = base + Gr::V + t * (D / 2) + g * (D / 16);
-    uint32_t x[2][2][D / 64], y[2][2][D / 64];     // [][half][word]: x low nibbles (dim 2g), y high (2g + 1)
+    uint32_t x[2][D / 64], y[2][D / 64];             // [half][word]: x low nibbles (dim 2g), y high (2g + 1)
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       uint32_t wa[D / 64], wb[D / 64];
@@ -284,40 +392,89 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint2 (&q)[D 
       }
 #pragma unroll
       for (int k = 0; k < D / 64; ++k) {
-        x[0][hf][k] = (wa[k] & 0x0F0F0F0Fu) | ((wb[k] << 4) & 0xF0F0F0F0u);
-        y[0][hf][k] = ((wa[k] >> 4) & 0x0F0F0F0Fu) | (wb[k] & 0xF0F0F0F0u);
+        x[hf][k] = (wa[k] & 0x0F0F0F0Fu) | ((wb[k] << 4) & 0xF0F0F0F0u);
+        y[hf][k] = ((wa[k] >> 4) & 0x0F0F0F0Fu) | (wb[k] & 0xF0F0F0F0u);
       }
     }
 #pragma unroll
     for (int k = 0; k < D / 64; ++k) {
       uint32_t xa[4], xb[4], ya[4], yb[4];
-      cvt_e2m1x8_f16(x[0][0][k], xa);
-      cvt_e2m1x8_f16(x[0][1][k], xb);
-      cvt_e2m1x8_f16(y[0][0][k], ya);
-      cvt_e2m1x8_f16(y[0][1][k], yb);
+      cvt_e2m1x8_f16(x[0][k], xa);
+      cvt_e2m1x8_f16(x[1][k], xb);
+      cvt_e2m1x8_f16(y[0][k], ya);
+      cvt_e2m1x8_f16(y[1][k], yb);
+      uint32_t b0[NT], b1[NT];
 #pragma unroll
       for (int ii = 0; ii < 4; ++ii) {
         const int i = 4 * k + ii;
-        constexpr int PER = CF == CF_MX ? 2 : 1;      // m-tiles of a scale block
-        const int blk = i / PER;
         const uint32_t va[4] = {xa[ii], ya[ii], xb[ii], yb[ii]};
+        if (CF == CF_NV || (ii & 1) == 0) {           // a new block: 16 or 32 dims
+          const int blk = CF == CF_MX ? i / 2 : i;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float p0 = s[gr][n][0] * vs[gr][0][blk], p1 = s[gr][n][1] * vs[gr][0][blk];
-          float p2 = s[gr][n][2] * vs[gr][1][blk], p3 = s[gr][n][3] * vs[gr][1][blk];
-          if (MASK) {                                  // 0 times a masked key's NaN scale
-            const int k0 = first + 16 * gr + tok, k1 = k0 + 8;
-            if (k0 >= lim[n][0]) p0 = 0.f;
-            if (k0 >= lim[n][1]) p1 = 0.f;
-            if (k1 >= lim[n][0]) p2 = 0.f;
-            if (k1 >= lim[n][1]) p3 = 0.f;
+          for (int n = 0; n < NT; ++n) {
+            uint32_t p0, p1;
+            if constexpr (CF == CF_NV) {
+              p0 = hmul2(p[n][0], blk & 1 ? high_twice(f[0][blk / 2]) : low_twice(f[0][blk / 2]));
+              p1 = hmul2(p[n][1], blk & 1 ? high_twice(f[1][blk / 2]) : low_twice(f[1][blk / 2]));
+            } else {
+              p0 = cvt_f16x2(x4[n][0] * vf[0][blk], x4[n][1] * vf[0][blk]);
+              p1 = cvt_f16x2(x4[n][2] * vf[1][blk], x4[n][3] * vf[1][blk]);
+            }
+            if (MASK) { p0 &= seen[gr][n][0]; p1 &= seen[gr][n][1]; }   // 0 times a masked key's NaN scale
+            b0[n] = transpose_8x8(p0);
+            b1[n] = transpose_8x8(p1);
           }
-          const uint32_t b0 = transpose_8x8(cvt_f16x2(p0, p1)), b1 = transpose_8x8(cvt_f16x2(p2, p3));
-          mma_f16_16816(a.o[i][n], va, b0, b1);
         }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma_f16_16816(a.o[i][n], va, b0[n], b1[n]);
       }
     }
   }
+}
+
+// ------------------------------------------------------------------------ results
+// One finished row: where it goes, and what its sums say.
+struct Row {
+  int64_t at, lse_at;
+  float inv, lse;
+  bool none;               // no key: zeros
+  __device__ __forceinline__ Row(const CacheAttnArgs& p, int b, int hkv, int col, const Span& s, float m, float l) {
+    const int i = col / p.G, h = hkv * p.G + col - i * p.G;
+    at = b * p.os.b + i * p.os.s + h * p.os.h;
+    lse_at = ((int64_t)b * p.Sq + i) * p.H + h;
+    none = limit_of(p, s, col) == 0;
+    inv = 1.0f / l;
+    lse = none ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+  }
+  __device__ __forceinline__ void put(const CacheAttnArgs& p, int d, float2 o) const {
+    o.x = none ? 0.f : o.x * inv;
+    o.y = none ? 0.f : o.y * inv;
+    if (p.out_bf16) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at + d) = cvt_bf16x2(o.x, o.y);
+    else *reinterpret_cast<float2*>(static_cast<float*>(p.out) + at + d) = o;
+  }
+  __device__ __forceinline__ void put_lse(const CacheAttnArgs& p) const {
+    if (p.lse) p.lse[lse_at] = lse;
+  }
+};
+
+// A partial result: the unnormalised rows [COLS][D], their maxima, their sums.
+template <int D, int CF, int NT>
+__device__ __forceinline__ void put_part(float* part, const Acc<D, CF, NT>& a) {
+  constexpr int COLS = 8 * NT;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int col = 8 * n + 2 * t + e;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        *reinterpret_cast<float2*>(part + col * D + 16 * k + 2 * g) = make_float2(a.o[k][n][e], a.o[k][n][2 + e]);
+      if (g == 0) {
+        part[COLS * D + col] = a.m[n][e];
+        part[COLS * (D + 1) + col] = a.l[n][e];
+      }
+    }
 }
 
 // ------------------------------------------------------------------- a warp's ring
@@ -337,87 +494,138 @@ __device__ __forceinline__ int page_of(Pages& pg, int i) {
 }
 
 template <int D, int CF, int NT>
-__global__ void __launch_bounds__(NWC * 32, 1) cache_attn_kernel(const CacheAttnArgs p) {
+__global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(const CacheAttnArgs p) {
   using C = Cfg<D, CF, NT>;
   using Gr = CacheGroup<D, CF>;
+  constexpr int NWC = C::NWC;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem);                  // [NWC][STG]
   int* flag = reinterpret_cast<int*>(smem + 512);                      // abort
-  int* final_seg = reinterpret_cast<int*>(smem + 576);                 // [NWC]
-  int64_t* wsum = reinterpret_cast<int64_t*>(smem + 640);              // [NWC + 1]
+  int64_t* wsum = reinterpret_cast<int64_t*>(smem + 576);              // [NWC]
+  int2* ends = reinterpret_cast<int2*>(smem + 520);                    // x: the first open piece begins, y: tiles behind the last
+  int2* pieces = reinterpret_cast<int2*>(smem + 704);                  // [NWC] segments of the leading and the open piece
   int64_t* pre = reinterpret_cast<int64_t*>(smem + 1024);              // [NWC * 32]
-  uint8_t* ring = smem + 1024 + NWC * 32 * 8;
+  float* leads = reinterpret_cast<float*>(smem + 1024 + NWC * 32 * 8);  // [NWC] parts
+  uint8_t* ring = smem + 1024 + NWC * 32 * 8 + C::JOIN;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const AbortCtl ac{flag, p.status, p.timeout_ns};
 
+  griddep_launch();
   if (threadIdx.x == 0) *flag = 0;
   if (threadIdx.x < NWC * STG) mbar_init(&bars[threadIdx.x], 1);
   fence_mbar_init();
 
-  // the list's length and its prefix sums: a chunk of virtual sequences per thread
+  // the list's length and its prefix sums.  Up to 4 virtual sequences a lane, every warp does
+  // it by itself (no barrier, and the loads of a lane go out together); beyond, the CTA
+  // shares the work, a chunk a thread.
   const int VB = p.B * p.CT;
-  const int chunk = (VB + NWC * 32 - 1) / (NWC * 32);
-  int64_t mine = 0;
-  for (int vb = threadIdx.x * chunk; vb < min(VB, (int)(threadIdx.x + 1) * chunk); ++vb)
-    mine += (int64_t)span_of(p, vb, C::COLS).tiles * p.c.Hkv;
+  const bool small = VB <= 128;
+  const int chunk = small ? (VB + 31) / 32 : (VB + NWC * 32 - 1) / (NWC * 32);
+  const int who = small ? lane : threadIdx.x;
+  int64_t mine = 0, before = 0, total = 0;
+  if (small) {
+    int n[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) n[x] = x < chunk && who * chunk + x < VB ? span_of(p, who * chunk + x, C::COLS).units() : 0;
+    mine = ((int64_t)n[0] + n[1] + n[2] + n[3]) * p.c.Hkv;
+  } else {
+    for (int vb = who * chunk; vb < min(VB, (who + 1) * chunk); ++vb)
+      mine += (int64_t)span_of(p, vb, C::COLS).units() * p.c.Hkv;
+  }
   int64_t inc = mine;
 #pragma unroll
   for (int x = 1; x < 32; x *= 2) {
     const int64_t up = __shfl_up_sync(0xFFFFFFFFu, inc, x);
     if (lane >= x) inc += up;
   }
-  if (lane == 31) wsum[warp] = inc;
-  __syncthreads();
-  int64_t before = 0, total = 0;
+  if (small) {
+    total = __shfl_sync(0xFFFFFFFFu, inc, 31);
+  } else {
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
 #pragma unroll
-  for (int w = 0; w < NWC; ++w) {
-    if (w < warp) before += wsum[w];
-    total += wsum[w];
+    for (int w = 0; w < NWC; ++w) {
+      if (w < warp) before += wsum[w];
+      total += wsum[w];
+    }
+    pre[threadIdx.x] = before + inc - mine;
   }
-  pre[threadIdx.x] = before + inc - mine;
   __syncthreads();
 
   // shares: as few warps of each CTA as give every one of them a tile, so small calls
   // spread over the SMs and no share between two others is empty
-  const int wpc = (int)max((int64_t)1, min((int64_t)NWC, (total + gridDim.x - 1) / gridDim.x));
+  const int wpc = total >= (int64_t)gridDim.x * NWC ? NWC : max(1, ((int)total + (int)gridDim.x - 1) / (int)gridDim.x);
   const int NW = (int)min(total, (int64_t)gridDim.x * wpc);
-  const int W = blockIdx.x * wpc + warp, slot = blockIdx.x * NWC + warp;
+  const Shares sh(total, NW);
+  const int W = blockIdx.x * wpc + warp;
   const bool works = warp < wpc && W < NW;
-  int64_t lo = works ? total * W / NW : 0;
-  const int64_t hi = works ? total * (W + 1) / NW : 0;
-  int4 start = make_int4(-1, 0, 0, 0);
-  int seg_open = -1;                                   // the piece that the loop leaves in `a`
-  Acc<D, NT> a;
+  float* const entering = p.partials + (int64_t)(2 * blockIdx.x) * C::PART;   // the CTA's part of a segment begun before it
+  int64_t lo = works ? sh.first(W) : 0;
+  const int64_t hi = works ? sh.first(W + 1) : 0;
+  // A warp's leading piece is the end of a segment that began before it, its open piece
+  // the one that the loop leaves in `a`, of a segment that others share; -1: none.
+  int seg_lead = -1, seg_open = -1;
+  bool open_begins = false;                            // the open piece is its segment's first
+  int open_rest = 0;                                   // tiles of its segment behind it
+  Acc<D, CF, NT> a;
   float cq[NT][2];
   int lim[NT][2];
   Span sp;
-  int vb = 0, hkv = 0, tile = 0;
+  int vb = 0, hkv = 0, unit = 0;
   uint64_t* bar = bars + warp * STG;
   uint8_t* mem = ring + warp * STG * C::STAGE;
   uint32_t phase = 0;                                  // bit s: the phase to wait for next on stage s
   int stage_in = 0, stage_out = 0;
 
   if (lo < hi) {
-    int j = 0;                                         // the last thread whose chunk begins at or before lo
-    for (int x = 256; x; x >>= 1)
-      if (j + x < NWC * 32 && pre[j + x] <= lo) j += x;
-    int64_t acc = pre[j];
+    int j = 0;                                         // the last chunk that begins at or before lo
+    int64_t acc;
+    if (small) {
+      j = 31 - __clz(__ballot_sync(0xFFFFFFFFu, inc - mine <= lo));
+      acc = __shfl_sync(0xFFFFFFFFu, inc - mine, j);
+    } else {
+      for (int x = 256; x; x >>= 1)
+        if (j + x < NWC * 32 && pre[j + x] <= lo) j += x;
+      acc = pre[j];
+    }
     for (vb = j * chunk;; ++vb) {
       sp = span_of(p, vb, C::COLS);
-      const int64_t n = (int64_t)sp.tiles * p.c.Hkv;
+      const int64_t n = (int64_t)sp.units() * p.c.Hkv;
       if (lo < acc + n) break;
       acc += n;
     }
-    hkv = (int)((lo - acc) / sp.tiles);
-    tile = (int)((lo - acc) % sp.tiles);
+    hkv = (int)quotient(lo - acc, sp.units());
+    unit = (int)(lo - acc - (int64_t)hkv * sp.units());
   }
 
   bool ok = true;
   while (lo < hi && ok) {
     const int b = p.CT == 1 ? vb : vb / p.CT, c0 = (vb - b * p.CT) * C::COLS;
-    const int t0 = tile, t1 = (int)min((int64_t)sp.tiles, t0 + (hi - lo));
+    const int unit1 = (int)min((int64_t)sp.units(), unit + (hi - lo));
+    const int t0 = max(0, unit - EXTRA), t1 = max(0, unit1 - EXTRA);
     const int seg = vb * p.c.Hkv + hkv;
     const int tend = min(t1, (sp.kmax + TILE - 1) / TILE);
+    lo += unit1 - unit;
+    unit = 0;
+    auto next = [&] {                                   // the segment after this one
+      if (lo < hi && ++hkv == p.c.Hkv) {
+        hkv = 0;
+        do { sp = span_of(p, ++vb, C::COLS); } while (sp.tiles == 0);
+      }
+    };
+    if (t0 == t1) { next(); continue; }                 // none of its tiles
+
+    // q's rows, on their way while the pages are looked up
+    uint2 u[NT][D / 16];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int col = c0 + 8 * n + g;                   // fragment columns: g
+      const int i = col / p.G;
+      const uint16_t* src = p.q + b * p.qs.b + i * p.qs.s + (int64_t)(hkv * p.G + col - i * p.G) * p.qs.h + 4 * t;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        u[n][k] = i < sp.qlen ? *reinterpret_cast<const uint2*>(src + 16 * k) : make_uint2(0u, 0u);
+    }
 
     // pages and first copies
     Pages pg{p.table + (int64_t)b * p.max_pages, 0, 0, p.max_pages};
@@ -459,23 +667,14 @@ __global__ void __launch_bounds__(NWC * 32, 1) cache_attn_kernel(const CacheAttn
     for (; issued < min(tend, t0 + STG); ++issued) issue(issued);
 
     // this piece's columns: q as f16 fragments, its factor, its last key
-    reset(a);
     uint2 q[D / 16][NT];
-    int min_lim = 0x7FFFFFFF;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int col = c0 + 8 * n + g;                  // fragment columns: g
-      const int i = col / p.G;
-      const bool live = i < sp.qlen;
-      const uint16_t* src = p.q + b * p.qs.b + i * p.qs.s + (int64_t)(hkv * p.G + col - i * p.G) * p.qs.h + 4 * t;
-      uint2 u[D / 16];
       float top = 0.f;
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        u[k] = live ? *reinterpret_cast<const uint2*>(src + 16 * k) : make_uint2(0u, 0u);
-        top = fmaxf(top, fmaxf(fmaxf(fabsf(__uint_as_float(u[k].x << 16)), fabsf(__uint_as_float(u[k].x & 0xFFFF0000u))),
-                               fmaxf(fabsf(__uint_as_float(u[k].y << 16)), fabsf(__uint_as_float(u[k].y & 0xFFFF0000u)))));
-      }
+      for (int k = 0; k < D / 16; ++k)
+        top = fmaxf(top, fmaxf(fmaxf(fabsf(__uint_as_float(u[n][k].x << 16)), fabsf(__uint_as_float(u[n][k].x & 0xFFFF0000u))),
+                               fmaxf(fabsf(__uint_as_float(u[n][k].y << 16)), fabsf(__uint_as_float(u[n][k].y & 0xFFFF0000u)))));
       top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
       const int e = (int)(__float_as_uint(top) >> 23) - 127;                 // floor(log2 top)
@@ -484,8 +683,8 @@ __global__ void __launch_bounds__(NWC * 32, 1) cache_attn_kernel(const CacheAttn
       const float back = __uint_as_float((uint32_t)(127 - up) << 23);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        q[k][n].x = cvt_f16x2(__uint_as_float(u[k].x << 16) * f, __uint_as_float(u[k].x & 0xFFFF0000u) * f);
-        q[k][n].y = cvt_f16x2(__uint_as_float(u[k].y << 16) * f, __uint_as_float(u[k].y & 0xFFFF0000u) * f);
+        q[k][n].x = cvt_f16x2(__uint_as_float(u[n][k].x << 16) * f, __uint_as_float(u[n][k].x & 0xFFFF0000u) * f);
+        q[k][n].y = cvt_f16x2(__uint_as_float(u[n][k].y << 16) * f, __uint_as_float(u[n][k].y & 0xFFFF0000u) * f);
       }
       // accumulator columns: 2t, 2t + 1
 #pragma unroll
@@ -494,7 +693,8 @@ __global__ void __launch_bounds__(NWC * 32, 1) cache_attn_kernel(const CacheAttn
         lim[n][c] = limit_of(p, sp, c0 + 8 * n + 2 * t + c);
       }
     }
-    min_lim = limit_of(p, sp, c0);                      // the first column sees the fewest keys
+    a.reset(cq);
+    const int min_lim = limit_of(p, sp, c0);            // the first column sees the fewest keys
 
     for (int tl = t0; tl < tend; ++tl) {
       const int s = stage_out;
@@ -517,169 +717,149 @@ __global__ void __launch_bounds__(NWC * 32, 1) cache_attn_kernel(const CacheAttn
       break;
     }
 
-    // row sums over the lanes that share a column
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int x = 4; x < 32; x *= 2) a.l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, a.l[n][e], x);
-
-    lo += t1 - t0;
+    a.finish();
     if (t0 == 0 && t1 == sp.tiles) {                    // all of it: write the rows
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int col = c0 + 8 * n + 2 * t + e, i = col / p.G;
-          if (i >= sp.qlen) continue;
-          const int h = hkv * p.G + col - i * p.G;
-          const bool none = lim[n][e] == 0;
-          const float inv = none ? 0.f : 1.0f / a.l[n][e];
-          const int64_t at = b * p.os.b + i * p.os.s + h * p.os.h + 2 * g;
+          const int col = c0 + 8 * n + 2 * t + e;
+          if (col >= sp.qlen * p.G) continue;
+          const Row row(p, b, hkv, col, sp, a.m[n][e], a.l[n][e]);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const float x = none ? 0.f : a.o[k][n][e] * inv, y = none ? 0.f : a.o[k][n][2 + e] * inv;
-            if (p.out_bf16) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at + 16 * k) = cvt_bf16x2(x, y);
-            else *reinterpret_cast<float2*>(static_cast<float*>(p.out) + at + 16 * k) = make_float2(x, y);
-          }
-          if (p.lse && g == 0)
-            p.lse[((int64_t)b * p.Sq + i) * p.H + h] =
-                none ? -INFINITY : (a.m[n][e] + a.r - 8.f + log2f(a.l[n][e])) * 0.69314718055994530942f;
+          for (int k = 0; k < D / 16; ++k) row.put(p, 16 * k + 2 * g, make_float2(a.o[k][n][e], a.o[k][n][2 + e]));
+          if (g == 0) row.put_lse(p);
         }
     } else if (lo < hi) {                               // the end of a segment that began before this warp
-      float* part = p.partials + (int64_t)(2 * slot) * C::PART;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int col = 8 * n + 2 * t + e;
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            *reinterpret_cast<float2*>(part + col * D + 16 * k + 2 * g) = make_float2(a.o[k][n][e], a.o[k][n][2 + e]);
-          if (g == 0) {
-            part[C::COLS * D + col] = a.m[n][e] + a.r - 8.f;
-            part[C::COLS * (D + 1) + col] = a.l[n][e];
-          }
-        }
+      seg_lead = seg;
+      put_part<D, CF, NT>(warp == 0 ? entering : leads + warp * C::PART, a);
     } else {
       seg_open = seg;
+      open_begins = t0 == 0;
+      open_rest = sp.tiles - t1;
     }
-    if (t0 == 0 && t1 < sp.tiles) {                     // it goes on: where it ends
-      const int64_t end = lo + (sp.tiles - t1) - 1;     // its last tile in the list
-      int64_t w = (end * NW + NW - 1) / total;          // near it: the warp with first <= end < first of the next
-      if (w >= NW) w = NW - 1;
-      while (w > 0 && total * w / NW > end) --w;
-      while (w + 1 < NW && total * (w + 1) / NW <= end) ++w;
-      start = make_int4(seg, (int)w, total * (w + 1) / NW > end + 1, wpc);   // .z: that warp goes on to others
-    }
-    tile = 0;
-    if (lo < hi && t1 == sp.tiles && ++hkv == p.c.Hkv) {
-      hkv = 0;
-      do { sp = span_of(p, ++vb, C::COLS); } while (sp.tiles == 0);
-    }
+    next();
   }
-  if (lane == 0) p.starts[slot] = start;
 
-  // join the CTA's open pieces
-  __syncthreads();
+  // Join the pieces of each segment that the CTA's warps share: the warps whose open pieces
+  // belong to it do it, an even share of the elements each.  A segment that began and ends
+  // in this CTA is written; one that came from the CTA before, or goes on to the next, is
+  // a part for the second kernel.
+  __syncthreads();                                      // every ring is done with
   float* parts = reinterpret_cast<float*>(ring);
-  if (lane == 0) final_seg[warp] = ok ? seg_open : -1;
-  if (ok && seg_open >= 0) {
-    float* part = parts + warp * C::PART;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int col = 8 * n + 2 * t + e;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          *reinterpret_cast<float2*>(part + col * D + 16 * k + 2 * g) = make_float2(a.o[k][n][e], a.o[k][n][2 + e]);
-        if (g == 0) {
-          part[C::COLS * D + col] = a.m[n][e] + a.r - 8.f;
-          part[C::COLS * (D + 1) + col] = a.l[n][e];
-        }
-      }
-  }
+  const int active = max(1, min(wpc, NW - (int)blockIdx.x * wpc));     // warps of this CTA that have a share
+  if (!ok) seg_lead = seg_open = -1;
+  if (lane == 0 && warp == 0) ends->x = open_begins;
+  if (lane == 0 && warp == active - 1) ends->y = open_rest;
+  if (lane == 0) pieces[warp] = make_int2(seg_lead, seg_open);
   __syncthreads();
-  for (int w = 0; w < NWC;) {
-    const int seg = final_seg[w];
-    int end = w + 1;
-    while (end < NWC && final_seg[end] == seg) ++end;
-    if (seg >= 0) {
-      float* dst = p.partials + (int64_t)(2 * (blockIdx.x * NWC + w) + 1) * C::PART;
-      for (int x = threadIdx.x; x < C::COLS * D; x += NWC * 32) {
-        const int col = x / D;
-        float m = M_NONE * 2.f;
-        for (int k = w; k < end; ++k) m = fmaxf(m, parts[k * C::PART + C::COLS * D + col]);
-        float o = 0.f, l = 0.f;
-        for (int k = w; k < end; ++k) {
-          const float* pk = parts + k * C::PART;
-          const float f = exp2f(pk[C::COLS * D + col] - m);
-          o = fmaf(f, pk[x], o);
-          l = fmaf(f, pk[C::COLS * (D + 1) + col], l);
-        }
-        dst[x] = o;
-        if (x % D == 0) {
+  int4 start = make_int4(-1, 0, 0, 0);
+  int w0 = warp, w1 = warp;
+  bool lead = false;
+  if (seg_open >= 0) {
+    while (w0 > 0 && pieces[w0 - 1].y == seg_open) --w0;
+    while (w1 + 1 < active && pieces[w1 + 1].y == seg_open) ++w1;
+    lead = w1 + 1 < active && pieces[w1 + 1].x == seg_open;
+  }
+  const int n = w1 - w0 + 1 + (lead ? 1 : 0);
+  // whether it began in this CTA is known to its first warp, where it ends to its last
+  const bool begins = w0 > 0 || ends->x != 0;
+  const int rest = lead || w1 + 1 < active ? 0 : ends->y;
+  float* dst = !begins ? entering : p.partials + (int64_t)(2 * blockIdx.x + 1) * C::PART;
+  if (seg_open >= 0) {
+    if (begins && rest > 0) start = make_int4(seg_open, sh.of(hi + rest - 1) / wpc, 0, 0);
+    put_part<D, CF, NT>(n == 1 ? dst : parts + warp * C::PART, a);     // (n = 1: it goes on, or came)
+  }
+  if (warp == active - 1 && lane == 0) p.starts[blockIdx.x] = start;
+  __syncthreads();
+  if (seg_open >= 0 && n > 1) {
+    auto part = [&](int k) { return w0 + k <= w1 ? parts + (w0 + k) * C::PART : leads + (w1 + 1) * C::PART; };
+    const bool whole = begins && rest == 0;
+    const int vs = seg_open / p.c.Hkv, hs = seg_open - vs * p.c.Hkv;
+    const int b = p.CT == 1 ? vs : vs / p.CT, c0 = (vs - b * p.CT) * C::COLS;
+    for (int x = (warp - w0) * 32 + lane; x < C::COLS * D / 2; x += (w1 - w0 + 1) * 32) {
+      const int col = x / (D / 2), d = 2 * (x % (D / 2));
+      if (whole && c0 + col >= sp.qlen * p.G) continue;
+      float m = M_NONE * 2.f;
+#pragma unroll 4
+      for (int k = 0; k < n; ++k) m = fmaxf(m, part(k)[C::COLS * D + col]);
+      float2 o = make_float2(0.f, 0.f);
+      float l = 0.f;
+#pragma unroll 4
+      for (int k = 0; k < n; ++k) {
+        const float* pk = part(k);
+        const float f = exp2f(pk[C::COLS * D + col] - m);
+        const float2 v = reinterpret_cast<const float2*>(pk)[x];
+        o.x = fmaf(f, v.x, o.x);
+        o.y = fmaf(f, v.y, o.y);
+        l = fmaf(f, pk[C::COLS * (D + 1) + col], l);
+      }
+      if (whole) {
+        const Row row(p, b, hs, c0 + col, sp, m, l);
+        row.put(p, d, o);
+        if (d == 0) row.put_lse(p);
+      } else {
+        reinterpret_cast<float2*>(dst)[x] = o;
+        if (d == 0) {
           dst[C::COLS * D + col] = m;
           dst[C::COLS * (D + 1) + col] = l;
         }
       }
     }
-    w = end;
   }
 }
 
-// Joins the partial results of the segments that several warps share: a block takes the
-// one that begins in its warp, if it goes on.  Its parts: that warp's own (joined over its
-// CTA), one for each later CTA, and the last warp's, which has one of its own when it
-// goes on to another segment.
+// Joins the parts of the segments that several CTAs share.  Block (c, y) takes the one that
+// begins in CTA c and goes on, columns of the y-th quarter: CTA c's second part and the
+// first part of each later CTA up to the last.
+constexpr int JOIN_THREADS = 128, JOIN_Y = 4;
 template <int D, int NT>
-__global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnArgs p) {
-  constexpr int COLS = 8 * NT, PART = COLS * (D + 2);
+__global__ void __launch_bounds__(JOIN_THREADS) cache_join_kernel(const CacheAttnArgs p) {
+  constexpr int COLS = 8 * NT, PART = COLS * (D + 2), CY = COLS / JOIN_Y;
+  extern __shared__ float weights[];                     // [parts][CY]: M, then the weight of a part
+  __shared__ float sums[CY][2];                          // M and the sum of a column
+  griddep_wait();                                        // the first kernel's results are complete
   const int4 st = p.starts[blockIdx.x];
   if (st.x < 0) return;
+  const int lane = threadIdx.x & 31;
   const int vb = st.x / p.c.Hkv, hkv = st.x - vb * p.c.Hkv;
-  const int b = p.CT == 1 ? vb : vb / p.CT, c0 = (vb - b * p.CT) * COLS;
+  const int b = p.CT == 1 ? vb : vb / p.CT, first = blockIdx.y * CY, c0 = (vb - b * p.CT) * COLS + first;
+  const int n = st.y - (int)blockIdx.x + 1;
+  const float* const parts = p.partials + (int64_t)2 * blockIdx.x * PART;
+  auto part = [&](int k) { return parts + (k == 0 ? (int64_t)PART : (int64_t)2 * k * PART); };
+  for (int x = threadIdx.x; x < n * CY; x += JOIN_THREADS) weights[x] = part(x / CY)[COLS * D + first + x % CY];
   const Span sp = span_of(p, vb, COLS);
-  const int last = st.y, wpc = st.w, first_cta = blockIdx.x / NWC, last_cta = last / wpc;
-  // parts k = 0 .. n-1
-  const bool tail_own = st.z != 0;                       // the last warp's part is its leading one
-  const int ctas = last_cta - first_cta;                 // CTAs after the first
-  const bool last_joined = ctas > 0 && (last_cta * wpc < last || !tail_own);
-  const int n = 1 + max(0, ctas - 1) + (last_joined ? 1 : 0) + (tail_own ? 1 : 0);
-  auto slot = [&](int k) -> const float* {
-    int64_t s;
-    if (k == 0) s = 2 * (int64_t)blockIdx.x + 1;
-    else if (tail_own && k == n - 1) s = 2 * ((int64_t)last_cta * NWC + last % wpc);
-    else s = 2 * (int64_t)(first_cta + k) * NWC + 1;
-    return p.partials + s * PART;
-  };
-  for (int x = threadIdx.x; x < COLS * D / 2; x += 256) {
-    const int c = x / (D / 2), d = 2 * (x % (D / 2));
-    const int col = c0 + c, i = col / p.G;
-    if (i >= sp.qlen) continue;
-    float m = M_NONE * 2.f;
-    for (int k = 0; k < n; ++k) m = fmaxf(m, slot(k)[COLS * D + c]);
-    float o0 = 0.f, o1 = 0.f, l = 0.f;
-    for (int k = 0; k < n; ++k) {
-      const float* pk = slot(k);
-      const float f = exp2f(pk[COLS * D + c] - m);
-      const float2 o = *reinterpret_cast<const float2*>(pk + c * D + d);
-      o0 = fmaf(f, o.x, o0);
-      o1 = fmaf(f, o.y, o1);
-      l = fmaf(f, pk[COLS * (D + 1) + c], l);
+  __syncthreads();
+  if (threadIdx.x < CY * 32) {                           // a warp a column
+    const int c = threadIdx.x / 32;
+    float m = M_NONE * 2.f, l = 0.f;
+    for (int k = lane; k < n; k += 32) m = fmaxf(m, weights[k * CY + c]);
+#pragma unroll
+    for (int x = 1; x < 32; x *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+    for (int k = lane; k < n; k += 32) {
+      const float f = exp2f(weights[k * CY + c] - m);
+      weights[k * CY + c] = f;
+      l = fmaf(f, part(k)[COLS * (D + 1) + first + c], l);
     }
-    const int h = hkv * p.G + col - i * p.G;
-    const bool none = limit_of(p, sp, col) == 0;
-    const float inv = none ? 0.f : 1.0f / l;
-    o0 = none ? 0.f : o0 * inv;
-    o1 = none ? 0.f : o1 * inv;
-    const int64_t at = b * p.os.b + i * p.os.s + h * p.os.h + d;
-    if (p.out_bf16) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at) = cvt_bf16x2(o0, o1);
-    else *reinterpret_cast<float2*>(static_cast<float*>(p.out) + at) = make_float2(o0, o1);
-    if (p.lse && d == 0)
-      p.lse[((int64_t)b * p.Sq + i) * p.H + h] = none ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+#pragma unroll
+    for (int x = 1; x < 32; x *= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
+    if (lane == 0) { sums[c][0] = m; sums[c][1] = l; }
+  }
+  __syncthreads();
+  for (int x = threadIdx.x; x < CY * D / 2; x += JOIN_THREADS) {
+    const int c = x / (D / 2), d = 2 * (x % (D / 2));
+    if (c0 + c >= sp.qlen * p.G) continue;
+    float2 o = make_float2(0.f, 0.f);
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+      const float f = weights[k * CY + c];
+      const float2 v = *reinterpret_cast<const float2*>(part(k) + (first + c) * D + d);
+      o.x = fmaf(f, v.x, o.x);
+      o.y = fmaf(f, v.y, o.y);
+    }
+    const Row row(p, b, hkv, c0 + c, sp, sums[c][0], sums[c][1]);
+    row.put(p, d, o);
+    if (d == 0) row.put_lse(p);
   }
 }
 
@@ -688,20 +868,30 @@ cudaError_t launch(const CacheAttnArgs& a, int sms, cudaStream_t st) {
   using C = Cfg<D, CF, NT>;
   cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, CF, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  cache_attn_kernel<D, CF, NT><<<sms, NWC * 32, C::SMEM, st>>>(a);
+  cache_attn_kernel<D, CF, NT><<<sms, C::NWC * 32, C::SMEM, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cache_join_kernel<D, NT><<<sms * NWC, 256, 0, st>>>(a);
-  return cudaGetLastError();
+  // the second kernel's launch overlaps the first one's run; it waits for its results itself
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(sms, JOIN_Y);
+  cfg.blockDim = dim3(JOIN_THREADS);
+  cfg.dynamicSmemBytes = (size_t)(sms + 2) * (C::COLS / JOIN_Y) * sizeof(float);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_join_kernel<D, NT>, a);
 }
 
 }  // namespace
 
 int cache_attn_ntiles(int cols) { return cols <= 8 ? 1 : 2; }
 
+// parts of the CTAs, two each; where segments begin that go on
 size_t cache_attn_workspace(int nt, int D, int sms, size_t* starts_at) {
-  const size_t parts = (size_t)2 * sms * NWC * 8 * nt * (D + 2) * sizeof(float);
-  if (starts_at) *starts_at = parts;
-  return parts + (size_t)sms * NWC * sizeof(int4);
+  *starts_at = (size_t)2 * sms * 8 * nt * (D + 2) * sizeof(float);
+  return *starts_at + (size_t)sms * sizeof(int4);
 }
 
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, int nt, int sms, cudaStream_t st) {

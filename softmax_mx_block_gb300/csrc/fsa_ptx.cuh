@@ -122,6 +122,11 @@ __device__ __forceinline__ bool mbar_drain(uint64_t* bar, uint32_t parity, const
   return false;
 }
 
+// Programmatic dependent launch: let the next kernel of the stream start (its blocks wait in
+// griddep_wait until this grid has ended and its writes are visible).
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // One lane of a converged warp (the lowest active one) gets true.  The tcgen05
 // issuing warp runs converged and elects its issuing lane per instruction.
 __device__ __forceinline__ bool elect_one() {
@@ -184,6 +189,11 @@ __device__ __forceinline__ void mma_f16_16816(float* d, const uint32_t* a, uint3
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_16816_zero(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {   // D = A * B
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 // Transpose of an 8x8 matrix of 16-bit values held by a warp, row lane/4, columns 2(lane%4), + 1.
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {

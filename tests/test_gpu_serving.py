@@ -6,7 +6,10 @@ value: bf16 2^-8, f16 2^-11, fp32 2^-24 (torch.finfo(t).eps / 2).
   - norm and rotation: the fp32 arithmetic before the one rounding to bf16 is off by a few
     2^-24 of |a| + |b| of the pair, and the angle by 2^-24 of a turn (2^-21.3 rad), so by
     2^-20 (|a| + |b|) in all.
-  - attention: each probability times its V scale is rounded to f16, 2^-11 of sum p|v| / sum p;
+  - attention: each probability times its V scale is rounded to f16, 2^-11 of sum p|v| / sum p.
+    E8M0 scales are powers of two, so that one rounding is all; an E4M3 scale has 4 significant
+    bits, so its product with the rounded probability is rounded again:
+    |f(f(p) s) - p s| <= ((1 + 2^-11)^2 - 1) p s = (2^-10 + 2^-22) p s;
     the fp32 scores are off by at most (D + 8) 2^-24 of sum |q||k| scale each way, which moves
     every weight by as much relatively, numerator and denominator; sums, exp2 and the rest
     2^-18; a probability below f16's range loses at most 2^-25 of 2^8-scaled ones (6 * 2^-33
@@ -216,7 +219,8 @@ def check_attention(q, cache, table, lens, q_lens, causal, scale, out, lse, befo
         want, want_lse, spread, reach, total = ref.attention(q[b, :m], k, v, live, n, m, causal, scale)
         vtop = torch.nan_to_num(v[live]).abs().max() if n and bool(live.any()) else torch.zeros(())
         e_s = (D + 8) * 2.0 ** -24 * reach + 2.0 ** -18
-        tol = (2.0 ** -11 + 2 * e_s)[..., None] * spread * 1.01
+        round_p = 2.0 ** -11 if fmt == "E2M1" else 2.0 ** -10 + 2.0 ** -22
+        tol = (round_p + 2 * e_s)[..., None] * spread * 1.01
         tol = tol + (n * 12 * 2.0 ** -33 * vtop / total.clamp(min=1.0))[..., None] + eps_out * want.abs() + 1e-36
         got = out[b, :m].double()
         assert torch.equal(torch.isnan(got), torch.isnan(want)), b
