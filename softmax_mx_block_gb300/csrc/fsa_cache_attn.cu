@@ -33,13 +33,19 @@
 namespace fsa {
 namespace {
 
+#ifndef NGS
+#define NGS 2
+#endif
 #ifndef NW1
 #define NW1 12
 #endif
 // warps of a CTA, by the registers that a warp's columns take
 template <int D, int NT>
 __host__ __device__ constexpr int cta_warps() { return NT == 1 ? NW1 : D == 128 ? 8 : 12; }
-constexpr int STG = 3;              // stages of a warp's ring
+#ifndef STGS
+#define STGS 3
+#endif
+constexpr int STG = STGS;           // stages of a warp's ring
 constexpr int TILE = 32;            // keys of a tile
 #ifndef EXTRA_TILES
 #define EXTRA_TILES 2
@@ -197,18 +203,18 @@ struct Acc {
   }
 };
 
-// One tile of 32 keys from shared memory.  first: position of the tile's first key; bad:
-// its groups without a page.  MASK: some column does not see some key of the tile.
-template <int D, int CF, int NT, bool MASK>
+// NG groups of 16 keys from shared memory.  first: position of the first key; bad: groups
+// without a page.  MASK: some column does not see some key.
+template <int D, int CF, int NT, int NG, bool MASK>
 __device__ __forceinline__ void tile_step(const uint8_t* st, const uint2 (&q)[D / 16][NT], const float (&cq)[NT][2],
                                           const int (&lim)[NT][2], int first, uint32_t bad, Acc<D, CF, NT>& a) {
   using Gr = CacheGroup<D, CF>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int tok = (g >> 1) + 4 * (g & 1);            // the key of S^T row g (and 8 more for row g + 8)
-  float s[2][NT][4];
-  RowScales<D, CF> vs[2][2];
+  float s[NG][NT][4];
+  RowScales<D, CF> vs[NG][2];
 #pragma unroll
-  for (int gr = 0; gr < 2; ++gr) {
+  for (int gr = 0; gr < NG; ++gr) {
     const uint8_t* base = st + gr * Gr::BYTES;
     RowScales<D, CF> ks[2];
     ks[0].load(base + Gr::KS + tok * Gr::SB);
@@ -269,10 +275,10 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint2 (&q)[D 
     }
   }
 
-  uint32_t seen[2][NT][2];                           // MASK: all ones in the halves (columns) that see the row
+  uint32_t seen[NG][NT][2];                           // MASK: all ones in the halves (columns) that see the row
   if (MASK) {
 #pragma unroll
-    for (int gr = 0; gr < 2; ++gr) {
+    for (int gr = 0; gr < NG; ++gr) {
       const int k0 = first + 16 * gr + tok, k1 = k0 + 8;
       const bool gone = (bad >> gr) & 1;
       uint32_t any0 = 0, any1 = 0;
@@ -298,7 +304,7 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint2 (&q)[D 
   // raise the running maxima where a score or a scale asks for it
   uint32_t vm = 0;                                   // largest scale bytes, in the high bytes of the halves
 #pragma unroll
-  for (int gr = 0; gr < 2; ++gr)
+  for (int gr = 0; gr < NG; ++gr)
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -309,14 +315,15 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint2 (&q)[D 
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      top[n][e] = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e]));
+      top[n][e] = fmaxf(s[0][n][e], s[0][n][2 + e]);
+      if (NG == 2) top[n][e] = fmaxf(top[n][e], fmaxf(s[NG - 1][n][e], s[NG - 1][n][2 + e]));
       raise |= top[n][e] > a.top[n][e];
     }
   if (__any_sync(0xFFFFFFFFu, raise)) {
     constexpr uint32_t NAN_BYTE = CF == CF_MX ? 0xFF : 0x7F;
     uint32_t v = 0;
 #pragma unroll
-    for (int gr = 0; gr < 2; ++gr)
+    for (int gr = 0; gr < NG; ++gr)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -346,7 +353,7 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint2 (&q)[D 
 
   // probabilities, and the products with V
 #pragma unroll
-  for (int gr = 0; gr < 2; ++gr) {
+  for (int gr = 0; gr < NG; ++gr) {
     const uint8_t* base = st + gr * Gr::BYTES;
     float x4[NT][4];
 #pragma unroll
@@ -475,22 +482,6 @@ __device__ __forceinline__ void put_part(float* part, const Acc<D, CF, NT>& a) {
         part[COLS * (D + 1) + col] = a.l[n][e];
       }
     }
-}
-
-// ------------------------------------------------------------------- a warp's ring
-// Page numbers of a piece, 32 at a time in the lanes' registers.
-struct Pages {
-  const int32_t* row;
-  int base, mine, n;
-};
-__device__ __forceinline__ void pages_at(Pages& pg, int i) {
-  pg.base = i;
-  const int at = i + (threadIdx.x & 31);
-  pg.mine = at < pg.n ? pg.row[at] : -1;
-}
-__device__ __forceinline__ int page_of(Pages& pg, int i) {
-  if (i >= pg.base + 32) pages_at(pg, i);
-  return __shfl_sync(0xFFFFFFFFu, pg.mine, i - pg.base);
 }
 
 template <int D, int CF, int NT>
@@ -627,42 +618,42 @@ __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(
         u[n][k] = i < sp.qlen ? *reinterpret_cast<const uint2*>(src + 16 * k) : make_uint2(0u, 0u);
     }
 
-    // pages and first copies
-    Pages pg{p.table + (int64_t)b * p.max_pages, 0, 0, p.max_pages};
-    pages_at(pg, (t0 * TILE) >> p.c.page_shift);
-    uint32_t bads = 0;                                  // 2 bits a stage: groups without a page
+    // Pages of 32 tiles at a time, a tile a lane; the lane that has a tile copies it.
+    const uint8_t* const head = p.c.pages + ((int64_t)hkv << (p.c.page_shift - 4)) * Gr::BYTES;
+    const int32_t* const row = p.table + (int64_t)b * p.max_pages;
+    int batch = 0, page0 = 0, page1 = 0;
+    uint32_t bad0 = 0, bad1 = 0, bads = 0;              // tiles of the batch, and (2 bits each) stages, with groups without a page
+    auto look_up = [&](int first) {
+      batch = first;
+      const int pos = (first + lane) * TILE;
+      const bool in0 = first + lane < tend, in1 = in0 && pos + 16 < sp.kmax;
+      const int i0 = pos >> p.c.page_shift, i1 = (pos + 16) >> p.c.page_shift;
+      page0 = in0 ? row[i0] : -1;
+      page1 = !in1 ? -1 : i1 == i0 ? page0 : row[i1];
+      if ((uint32_t)page0 >= (uint32_t)p.c.num_pages) page0 = -1;
+      if ((uint32_t)page1 >= (uint32_t)p.c.num_pages) page1 = -1;
+      bad0 = __ballot_sync(0xFFFFFFFFu, in0 && page0 < 0);
+      bad1 = __ballot_sync(0xFFFFFFFFu, in1 && page1 < 0);
+      if ((bad0 | bad1) && lane == 0 && p.status) atomicExch(p.status, -1);    // FSA_ERR_INVALID_ARG
+    };
     auto issue = [&](int tl) {
-      const int s = stage_in;
-      stage_in = stage_in + 1 == STG ? 0 : stage_in + 1;
-      const int pos = tl * TILE;
-      const int groups = min(2, (sp.kmax - pos + 15) / 16);
-      uint32_t bad = 0, bytes = 0;
-      const uint8_t* src[2] = {nullptr, nullptr};
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if (k >= groups) continue;
-        const int at = pos + 16 * k;
-        const int page = page_of(pg, at >> p.c.page_shift);
-        if (page < 0 || page >= p.c.num_pages) {
-          bad |= 1u << k;
-        } else {
-          const int inside = at & ((1 << p.c.page_shift) - 1);
-          src[k] = p.c.pages + page * p.c.page_bytes + ((int64_t)(hkv << (p.c.page_shift - 4)) + inside / 16) * Gr::BYTES;
-          bytes += Gr::BYTES;
-        }
-      }
-      bads = (bads & ~(3u << (2 * s))) | bad << (2 * s);
-      if (lane == 0) {
-        if (bad && p.status) atomicExch(p.status, -1);  // FSA_ERR_INVALID_ARG
-        mbar_expect_tx(&bar[s], bytes);
-        if (src[0] && src[1] == src[0] + Gr::BYTES) {
-          bulk_load(mem + s * C::STAGE, src[0], 2 * Gr::BYTES, &bar[s]);
-        } else {
-          if (src[0]) bulk_load(mem + s * C::STAGE, src[0], Gr::BYTES, &bar[s]);
-          if (src[1]) bulk_load(mem + s * C::STAGE + Gr::BYTES, src[1], Gr::BYTES, &bar[s]);
+      const int s = stage_in, at = tl - batch;
+      stage_in = s + 1 == STG ? 0 : s + 1;
+      if (bad0 | bad1 | bads) bads = (bads & ~(3u << (2 * s))) | ((bad0 >> at & 1) | (bad1 >> at & 1) << 1) << (2 * s);
+      if (lane == at) {
+        const int inside = ((tl * TILE) & ((1 << p.c.page_shift) - 1)) / 16;
+        const uint8_t* const src = head + page0 * p.c.page_bytes + inside * Gr::BYTES;
+        uint8_t* const dst = mem + s * C::STAGE;
+        mbar_expect_tx(&bar[s], (page0 >= 0 ? Gr::BYTES : 0) + (page1 >= 0 ? Gr::BYTES : 0));
+        if (p.c.page_shift > 4 && page0 >= 0 && page1 == page0) {
+          bulk_load(dst, src, 2 * Gr::BYTES, &bar[s]);
+        } else {                                        // 16 tokens a page, or a single group left
+          if (page0 >= 0) bulk_load(dst, src, Gr::BYTES, &bar[s]);
+          if (page1 >= 0) bulk_load(dst + Gr::BYTES, head + page1 * p.c.page_bytes + (p.c.page_shift > 4 ? (inside + 1) * Gr::BYTES : 0), Gr::BYTES, &bar[s]);
         }
       }
     };
+    if (t0 < tend) look_up(t0);
     int issued = t0;
     for (; issued < min(tend, t0 + STG); ++issued) issue(issued);
 
@@ -702,10 +693,20 @@ __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(
       phase ^= 1u << s;
       stage_out = stage_out + 1 == STG ? 0 : stage_out + 1;
       const uint32_t bad = (bads >> (2 * s)) & 3;
-      if (bad == 0 && (tl + 1) * TILE <= min_lim) tile_step<D, CF, NT, false>(mem + s * C::STAGE, q, cq, lim, tl * TILE, 0, a);
-      else tile_step<D, CF, NT, true>(mem + s * C::STAGE, q, cq, lim, tl * TILE, bad, a);
+      const uint8_t* at = mem + s * C::STAGE;
+      if (bad == 0 && (tl + 1) * TILE <= min_lim) {
+#pragma unroll 1
+        for (int gr = 0; gr < 2; gr += NGS) tile_step<D, CF, NT, NGS, false>(at + gr * Gr::BYTES, q, cq, lim, tl * TILE + 16 * gr, 0, a);
+      } else {
+#pragma unroll 1
+        for (int gr = 0; gr < 2 && tl * TILE + 16 * gr < sp.kmax; ++gr)
+          tile_step<D, CF, NT, 1, true>(at + gr * Gr::BYTES, q, cq, lim, tl * TILE + 16 * gr, bad >> gr & 1, a);
+      }
       __syncwarp();
-      if (issued < tend) { issue(issued); ++issued; }
+      if (issued < tend) {
+        if (issued - batch == 32) look_up(issued);
+        issue(issued++);
+      }
     }
     if (!ok) {                                          // give up: the copies in flight end first
       for (int k = 0; k < STG; ++k) {
@@ -777,30 +778,35 @@ __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(
     const bool whole = begins && rest == 0;
     const int vs = seg_open / p.c.Hkv, hs = seg_open - vs * p.c.Hkv;
     const int b = p.CT == 1 ? vs : vs / p.CT, c0 = (vs - b * p.CT) * C::COLS;
-    for (int x = (warp - w0) * 32 + lane; x < C::COLS * D / 2; x += (w1 - w0 + 1) * 32) {
-      const int col = x / (D / 2), d = 2 * (x % (D / 2));
-      if (whole && c0 + col >= sp.qlen * p.G) continue;
-      float m = M_NONE * 2.f;
+    for (int col = warp - w0; col < C::COLS; col += w1 - w0 + 1) {     // a warp a column
+      if (c0 + col >= sp.qlen * p.G) break;
+      float m = M_NONE * 2.f, l = 0.f;
+      float2 o[D / 64];
+#pragma unroll
+      for (int x = 0; x < D / 64; ++x) o[x] = make_float2(0.f, 0.f);
 #pragma unroll 4
       for (int k = 0; k < n; ++k) m = fmaxf(m, part(k)[C::COLS * D + col]);
-      float2 o = make_float2(0.f, 0.f);
-      float l = 0.f;
 #pragma unroll 4
       for (int k = 0; k < n; ++k) {
         const float* pk = part(k);
         const float f = exp2f(pk[C::COLS * D + col] - m);
-        const float2 v = reinterpret_cast<const float2*>(pk)[x];
-        o.x = fmaf(f, v.x, o.x);
-        o.y = fmaf(f, v.y, o.y);
         l = fmaf(f, pk[C::COLS * (D + 1) + col], l);
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) {
+          const float2 v = *reinterpret_cast<const float2*>(pk + col * D + 64 * x + 2 * lane);
+          o[x].x = fmaf(f, v.x, o[x].x);
+          o[x].y = fmaf(f, v.y, o[x].y);
+        }
       }
       if (whole) {
         const Row row(p, b, hs, c0 + col, sp, m, l);
-        row.put(p, d, o);
-        if (d == 0) row.put_lse(p);
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) row.put(p, 64 * x + 2 * lane, o[x]);
+        if (lane == 0) row.put_lse(p);
       } else {
-        reinterpret_cast<float2*>(dst)[x] = o;
-        if (d == 0) {
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) *reinterpret_cast<float2*>(dst + col * D + 64 * x + 2 * lane) = o[x];
+        if (lane == 0) {
           dst[C::COLS * D + col] = m;
           dst[C::COLS * (D + 1) + col] = l;
         }
@@ -827,8 +833,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_join_kernel(const CacheAtt
   const int n = st.y - (int)blockIdx.x + 1;
   const float* const parts = p.partials + (int64_t)2 * blockIdx.x * PART;
   auto part = [&](int k) { return parts + (k == 0 ? (int64_t)PART : (int64_t)2 * k * PART); };
-  for (int x = threadIdx.x; x < n * CY; x += JOIN_THREADS) weights[x] = part(x / CY)[COLS * D + first + x % CY];
   const Span sp = span_of(p, vb, COLS);
+  if (c0 >= sp.qlen * p.G) return;
+  for (int x = threadIdx.x; x < n * CY; x += JOIN_THREADS) weights[x] = part(x / CY)[COLS * D + first + x % CY];
   __syncthreads();
   if (threadIdx.x < CY * 32) {                           // a warp a column
     const int c = threadIdx.x / 32;
