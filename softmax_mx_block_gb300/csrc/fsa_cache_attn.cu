@@ -36,6 +36,12 @@ namespace {
 #ifndef NGS
 #define NGS 2
 #endif
+#ifndef WHOLE_T1
+#define WHOLE_T1 24
+#endif
+#ifndef WHOLE_T2
+#define WHOLE_T2 64
+#endif
 #ifndef NW1
 #define NW1 12
 #endif
@@ -484,21 +490,265 @@ __device__ __forceinline__ void put_part(float* part, const Acc<D, CF, NT>& a) {
     }
 }
 
+// ---------------------------------------------------------------------- a warp's work
+// A warp's ring of stages, and where it stands in it.
+struct Ring {
+  uint64_t* bar;
+  uint8_t* mem;
+  uint32_t phase;          // bit s: the phase to wait for next on stage s
+  int in, out;
+};
+
+// The tiles [t0, t1) of one segment: (sequence b, kv head, columns c0 ..).  Leaves the
+// running state in `a`; false if a wait ran out.
+template <int D, int CF, int NT>
+__device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const Span& sp, int b, int hkv, int c0, int t0, int t1,
+                                          Ring& r, const AbortCtl& ac, Acc<D, CF, NT>& a) {
+  using C = Cfg<D, CF, NT>;
+  using Gr = CacheGroup<D, CF>;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  bool ok = true;
+  float cq[NT][2];                                      // what a raw score of a column is multiplied by (log2 units)
+  int lim[NT][2];                                       // how many keys it sees
+  const int tend = min(t1, (sp.kmax + TILE - 1) / TILE);
+  // q's rows, on their way while the pages are looked up
+  uint2 u[NT][D / 16];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int col = c0 + 8 * n + g;                   // fragment columns: g
+    const int i = col / p.G;
+    const uint16_t* src = p.q + b * p.qs.b + i * p.qs.s + (int64_t)(hkv * p.G + col - i * p.G) * p.qs.h + 4 * t;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+      u[n][k] = i < sp.qlen ? *reinterpret_cast<const uint2*>(src + 16 * k) : make_uint2(0u, 0u);
+  }
+
+  // Pages of 32 tiles at a time, a tile a lane; the lane that has a tile copies it.
+  const uint8_t* const head = p.c.pages + ((int64_t)hkv << (p.c.page_shift - 4)) * Gr::BYTES;
+  const int32_t* const row = p.table + (int64_t)b * p.max_pages;
+  int batch = 0, page0 = 0, page1 = 0;
+  uint32_t bad0 = 0, bad1 = 0, bads = 0;              // tiles of the batch, and (2 bits each) stages, with groups without a page
+  auto look_up = [&](int first) {
+    batch = first;
+    const int pos = (first + lane) * TILE;
+    const bool in0 = first + lane < tend, in1 = in0 && pos + 16 < sp.kmax;
+    const int i0 = pos >> p.c.page_shift, i1 = (pos + 16) >> p.c.page_shift;
+    page0 = in0 ? row[i0] : -1;
+    page1 = !in1 ? -1 : i1 == i0 ? page0 : row[i1];
+    if ((uint32_t)page0 >= (uint32_t)p.c.num_pages) page0 = -1;
+    if ((uint32_t)page1 >= (uint32_t)p.c.num_pages) page1 = -1;
+    bad0 = __ballot_sync(0xFFFFFFFFu, in0 && page0 < 0);
+    bad1 = __ballot_sync(0xFFFFFFFFu, in1 && page1 < 0);
+    if ((bad0 | bad1) && lane == 0 && p.status) atomicExch(p.status, -1);    // FSA_ERR_INVALID_ARG
+  };
+  auto issue = [&](int tl) {
+    const int s = r.in, at = tl - batch;
+    r.in = s + 1 == STG ? 0 : s + 1;
+    if (bad0 | bad1 | bads) bads = (bads & ~(3u << (2 * s))) | ((bad0 >> at & 1) | (bad1 >> at & 1) << 1) << (2 * s);
+    if (lane == at) {
+      const int inside = ((tl * TILE) & ((1 << p.c.page_shift) - 1)) / 16;
+      const uint8_t* const src = head + page0 * p.c.page_bytes + inside * Gr::BYTES;
+      uint8_t* const dst = r.mem + s * C::STAGE;
+      mbar_expect_tx(&r.bar[s], (page0 >= 0 ? Gr::BYTES : 0) + (page1 >= 0 ? Gr::BYTES : 0));
+      if (p.c.page_shift > 4 && page0 >= 0 && page1 == page0) {
+        bulk_load(dst, src, 2 * Gr::BYTES, &r.bar[s]);
+      } else {                                        // 16 tokens a page, or a single group left
+        if (page0 >= 0) bulk_load(dst, src, Gr::BYTES, &r.bar[s]);
+        if (page1 >= 0) bulk_load(dst + Gr::BYTES, head + page1 * p.c.page_bytes + (p.c.page_shift > 4 ? (inside + 1) * Gr::BYTES : 0), Gr::BYTES, &r.bar[s]);
+      }
+    }
+  };
+  if (t0 < tend) look_up(t0);
+  int issued = t0;
+  for (; issued < min(tend, t0 + STG); ++issued) issue(issued);
+
+  // this piece's columns: q as f16 fragments, its factor, its last key
+  uint2 q[D / 16][NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+      top = fmaxf(top, fmaxf(fmaxf(fabsf(__uint_as_float(u[n][k].x << 16)), fabsf(__uint_as_float(u[n][k].x & 0xFFFF0000u))),
+                             fmaxf(fabsf(__uint_as_float(u[n][k].y << 16)), fabsf(__uint_as_float(u[n][k].y & 0xFFFF0000u)))));
+    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    const int e = (int)(__float_as_uint(top) >> 23) - 127;                 // floor(log2 top)
+    const int up = e == 128 || top == 0.f ? 0 : min(max(4 - e, -126), 126);
+    const float f = __uint_as_float((uint32_t)(up + 127) << 23) * p.q_sign;
+    const float back = __uint_as_float((uint32_t)(127 - up) << 23);
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      q[k][n].x = cvt_f16x2(__uint_as_float(u[n][k].x << 16) * f, __uint_as_float(u[n][k].x & 0xFFFF0000u) * f);
+      q[k][n].y = cvt_f16x2(__uint_as_float(u[n][k].y << 16) * f, __uint_as_float(u[n][k].y & 0xFFFF0000u) * f);
+    }
+    // accumulator columns: 2t, 2t + 1
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      cq[n][c] = p.scale_log2 * __shfl_sync(0xFFFFFFFFu, back, 4 * (2 * t + c));
+      lim[n][c] = limit_of(p, sp, c0 + 8 * n + 2 * t + c);
+    }
+  }
+  a.reset(cq);
+  const int min_lim = limit_of(p, sp, c0);            // the first column sees the fewest keys
+
+  for (int tl = t0; tl < tend; ++tl) {
+    const int s = r.out;
+    if (!mbar_wait(&r.bar[s], (r.phase >> s) & 1, ac)) { ok = false; break; }
+    r.phase ^= 1u << s;
+    r.out = r.out + 1 == STG ? 0 : r.out + 1;
+    const uint32_t bad = (bads >> (2 * s)) & 3;
+    const uint8_t* at = r.mem + s * C::STAGE;
+    if (bad == 0 && (tl + 1) * TILE <= min_lim) {
+#pragma unroll 1
+      for (int gr = 0; gr < 2; gr += NGS) tile_step<D, CF, NT, NGS, false>(at + gr * Gr::BYTES, q, cq, lim, tl * TILE + 16 * gr, 0, a);
+    } else {
+#pragma unroll 1
+      for (int gr = 0; gr < 2 && tl * TILE + 16 * gr < sp.kmax; ++gr)
+        tile_step<D, CF, NT, 1, true>(at + gr * Gr::BYTES, q, cq, lim, tl * TILE + 16 * gr, bad >> gr & 1, a);
+    }
+    __syncwarp();
+    if (issued < tend) {
+      if (issued - batch == 32) look_up(issued);
+      issue(issued++);
+    }
+  }
+  if (!ok) {                                            // give up: the copies in flight end first
+    for (int k = 0; k < STG; ++k) {
+      const int s = r.out;
+      if (r.out == r.in && k) break;
+      mbar_drain(&r.bar[s], (r.phase >> s) & 1, ac);
+      r.out = s + 1 == STG ? 0 : s + 1;
+    }
+    return false;
+  }
+  a.finish();
+  return true;
+}
+
+// The rows of a segment from one warp's state.
+template <int D, int CF, int NT>
+__device__ __forceinline__ void put_rows(const CacheAttnArgs& p, const Span& sp, int b, int hkv, int c0, const Acc<D, CF, NT>& a) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int col = c0 + 8 * n + 2 * t + e;
+      if (col >= sp.qlen * p.G) continue;
+      const Row row(p, b, hkv, col, sp, a.m[n][e], a.l[n][e]);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) row.put(p, 16 * k + 2 * g, make_float2(a.o[k][n][e], a.o[k][n][2 + e]));
+      if (g == 0) row.put_lse(p);
+    }
+}
+
+// One column of n parts joined by a warp: a lane has dims 64x + 2 lane and the next.
+template <int D, int COLS>
+struct Column {
+  float m, l;
+  float2 o[D / 64];
+  template <class Part>
+  __device__ __forceinline__ Column(Part part, int n, int col) {
+    const int lane = threadIdx.x & 31;
+    m = M_NONE * 2.f;
+    l = 0.f;
+#pragma unroll
+    for (int x = 0; x < D / 64; ++x) o[x] = make_float2(0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) m = fmaxf(m, part(k)[COLS * D + col]);
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const float* const pk = part(k);
+      const float f = exp2f(pk[COLS * D + col] - m);
+      l = fmaf(f, pk[COLS * (D + 1) + col], l);
+#pragma unroll
+      for (int x = 0; x < D / 64; ++x) {
+        const float2 v = *reinterpret_cast<const float2*>(pk + col * D + 64 * x + 2 * lane);
+        o[x].x = fmaf(f, v.x, o[x].x);
+        o[x].y = fmaf(f, v.y, o[x].y);
+      }
+    }
+  }
+  __device__ __forceinline__ void put_row(const CacheAttnArgs& p, const Span& sp, int b, int hkv, int col) const {
+    const int lane = threadIdx.x & 31;
+    const Row row(p, b, hkv, col, sp, m, l);
+#pragma unroll
+    for (int x = 0; x < D / 64; ++x) row.put(p, 64 * x + 2 * lane, o[x]);
+    if (lane == 0) row.put_lse(p);
+  }
+  __device__ __forceinline__ void put_part(float* part, int col) const {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int x = 0; x < D / 64; ++x) *reinterpret_cast<float2*>(part + col * D + 64 * x + 2 * lane) = o[x];
+    if (lane == 0) {
+      part[COLS * D + col] = m;
+      part[COLS * (D + 1) + col] = l;
+    }
+  }
+};
+
+// Few short segments, or many: a CTA of 4 warps each, three CTAs an SM; no list, no second
+// kernel.  Block x is segment x.
+constexpr int WHOLE_WARPS = 4;
+template <int D, int CF, int NT>
+struct WholeCfg {
+  using C = Cfg<D, CF, NT>;
+  static constexpr int RING = WHOLE_WARPS * STG * C::STAGE, JOIN = WHOLE_WARPS * C::PART * 4;
+  static constexpr int SMEM = 1024 + (RING > JOIN ? RING : JOIN);
+  static constexpr int CTAS = NT == 2 && D == 128 ? 2 : 3;
+};
+template <int D, int CF, int NT>
+__global__ void __launch_bounds__(WHOLE_WARPS * 32, WholeCfg<D, CF, NT>::CTAS) cache_attn_whole_kernel(const CacheAttnArgs p) {
+  using C = Cfg<D, CF, NT>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(smem);
+  int* const flag = reinterpret_cast<int*>(smem + 512);
+  uint8_t* const ring = smem + 1024;
+  const int warp = threadIdx.x >> 5;
+  const AbortCtl ac{flag, p.status, p.timeout_ns};
+  const int vb = blockIdx.x / p.c.Hkv, hkv = blockIdx.x - vb * p.c.Hkv;
+  const int b = p.CT == 1 ? vb : vb / p.CT, c0 = (vb - b * p.CT) * C::COLS;
+  const Span sp = span_of(p, vb, C::COLS);
+  if (sp.tiles == 0) return;
+  if (threadIdx.x == 0) *flag = 0;
+  if (threadIdx.x < WHOLE_WARPS * STG) mbar_init(&bars[threadIdx.x], 1);
+  fence_mbar_init();
+  __syncthreads();
+  Ring r{bars + warp * STG, ring + warp * STG * C::STAGE, 0, 0, 0};
+  Acc<D, CF, NT> a;
+  const int n = min(WHOLE_WARPS, sp.tiles), t0 = sp.tiles * warp / n, t1 = sp.tiles * (warp + 1) / n;
+  bool ok = true;
+  if (warp < n) ok = run_piece<D, CF, NT>(p, sp, b, hkv, c0, t0, t1, r, ac, a);
+  if (n == 1) {
+    if (warp == 0 && ok) put_rows<D, CF, NT>(p, sp, b, hkv, c0, a);
+    return;
+  }
+  __syncthreads();                                      // every ring is done with
+  float* const parts = reinterpret_cast<float*>(ring);
+  if (warp < n && ok) put_part<D, CF, NT>(parts + warp * C::PART, a);
+  __syncthreads();
+  if (lds_vol(flag)) return;                            // a wait ran out: the status word says so
+  for (int col = warp; col < C::COLS && c0 + col < sp.qlen * p.G; col += WHOLE_WARPS) {
+    const Column<D, C::COLS> col_sum([&](int k) { return parts + k * C::PART; }, n, col);
+    col_sum.put_row(p, sp, b, hkv, c0 + col);
+  }
+}
+
 template <int D, int CF, int NT>
 __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(const CacheAttnArgs p) {
   using C = Cfg<D, CF, NT>;
-  using Gr = CacheGroup<D, CF>;
   constexpr int NWC = C::NWC;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem);                  // [NWC][STG]
   int* flag = reinterpret_cast<int*>(smem + 512);                      // abort
   int64_t* wsum = reinterpret_cast<int64_t*>(smem + 576);              // [NWC]
   int2* ends = reinterpret_cast<int2*>(smem + 520);                    // x: the first open piece begins, y: tiles behind the last
-  int2* pieces = reinterpret_cast<int2*>(smem + 704);                  // [NWC] segments of the leading and the open piece
+  int4* pieces = reinterpret_cast<int4*>(smem + 704);                  // [NWC] segments of the leading and the open piece; its qlen, len
   int64_t* pre = reinterpret_cast<int64_t*>(smem + 1024);              // [NWC * 32]
   float* leads = reinterpret_cast<float*>(smem + 1024 + NWC * 32 * 8);  // [NWC] parts
   uint8_t* ring = smem + 1024 + NWC * 32 * 8 + C::JOIN;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const AbortCtl ac{flag, p.status, p.timeout_ns};
 
   griddep_launch();
@@ -559,14 +809,9 @@ __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(
   bool open_begins = false;                            // the open piece is its segment's first
   int open_rest = 0;                                   // tiles of its segment behind it
   Acc<D, CF, NT> a;
-  float cq[NT][2];
-  int lim[NT][2];
   Span sp;
   int vb = 0, hkv = 0, unit = 0;
-  uint64_t* bar = bars + warp * STG;
-  uint8_t* mem = ring + warp * STG * C::STAGE;
-  uint32_t phase = 0;                                  // bit s: the phase to wait for next on stage s
-  int stage_in = 0, stage_out = 0;
+  Ring r{bars + warp * STG, ring + warp * STG * C::STAGE, 0, 0, 0};
 
   if (lo < hi) {
     int j = 0;                                         // the last chunk that begins at or before lo
@@ -595,7 +840,6 @@ __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(
     const int unit1 = (int)min((int64_t)sp.units(), unit + (hi - lo));
     const int t0 = max(0, unit - EXTRA), t1 = max(0, unit1 - EXTRA);
     const int seg = vb * p.c.Hkv + hkv;
-    const int tend = min(t1, (sp.kmax + TILE - 1) / TILE);
     lo += unit1 - unit;
     unit = 0;
     auto next = [&] {                                   // the segment after this one
@@ -606,131 +850,10 @@ __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(
     };
     if (t0 == t1) { next(); continue; }                 // none of its tiles
 
-    // q's rows, on their way while the pages are looked up
-    uint2 u[NT][D / 16];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int col = c0 + 8 * n + g;                   // fragment columns: g
-      const int i = col / p.G;
-      const uint16_t* src = p.q + b * p.qs.b + i * p.qs.s + (int64_t)(hkv * p.G + col - i * p.G) * p.qs.h + 4 * t;
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        u[n][k] = i < sp.qlen ? *reinterpret_cast<const uint2*>(src + 16 * k) : make_uint2(0u, 0u);
-    }
-
-    // Pages of 32 tiles at a time, a tile a lane; the lane that has a tile copies it.
-    const uint8_t* const head = p.c.pages + ((int64_t)hkv << (p.c.page_shift - 4)) * Gr::BYTES;
-    const int32_t* const row = p.table + (int64_t)b * p.max_pages;
-    int batch = 0, page0 = 0, page1 = 0;
-    uint32_t bad0 = 0, bad1 = 0, bads = 0;              // tiles of the batch, and (2 bits each) stages, with groups without a page
-    auto look_up = [&](int first) {
-      batch = first;
-      const int pos = (first + lane) * TILE;
-      const bool in0 = first + lane < tend, in1 = in0 && pos + 16 < sp.kmax;
-      const int i0 = pos >> p.c.page_shift, i1 = (pos + 16) >> p.c.page_shift;
-      page0 = in0 ? row[i0] : -1;
-      page1 = !in1 ? -1 : i1 == i0 ? page0 : row[i1];
-      if ((uint32_t)page0 >= (uint32_t)p.c.num_pages) page0 = -1;
-      if ((uint32_t)page1 >= (uint32_t)p.c.num_pages) page1 = -1;
-      bad0 = __ballot_sync(0xFFFFFFFFu, in0 && page0 < 0);
-      bad1 = __ballot_sync(0xFFFFFFFFu, in1 && page1 < 0);
-      if ((bad0 | bad1) && lane == 0 && p.status) atomicExch(p.status, -1);    // FSA_ERR_INVALID_ARG
-    };
-    auto issue = [&](int tl) {
-      const int s = stage_in, at = tl - batch;
-      stage_in = s + 1 == STG ? 0 : s + 1;
-      if (bad0 | bad1 | bads) bads = (bads & ~(3u << (2 * s))) | ((bad0 >> at & 1) | (bad1 >> at & 1) << 1) << (2 * s);
-      if (lane == at) {
-        const int inside = ((tl * TILE) & ((1 << p.c.page_shift) - 1)) / 16;
-        const uint8_t* const src = head + page0 * p.c.page_bytes + inside * Gr::BYTES;
-        uint8_t* const dst = mem + s * C::STAGE;
-        mbar_expect_tx(&bar[s], (page0 >= 0 ? Gr::BYTES : 0) + (page1 >= 0 ? Gr::BYTES : 0));
-        if (p.c.page_shift > 4 && page0 >= 0 && page1 == page0) {
-          bulk_load(dst, src, 2 * Gr::BYTES, &bar[s]);
-        } else {                                        // 16 tokens a page, or a single group left
-          if (page0 >= 0) bulk_load(dst, src, Gr::BYTES, &bar[s]);
-          if (page1 >= 0) bulk_load(dst + Gr::BYTES, head + page1 * p.c.page_bytes + (p.c.page_shift > 4 ? (inside + 1) * Gr::BYTES : 0), Gr::BYTES, &bar[s]);
-        }
-      }
-    };
-    if (t0 < tend) look_up(t0);
-    int issued = t0;
-    for (; issued < min(tend, t0 + STG); ++issued) issue(issued);
-
-    // this piece's columns: q as f16 fragments, its factor, its last key
-    uint2 q[D / 16][NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float top = 0.f;
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        top = fmaxf(top, fmaxf(fmaxf(fabsf(__uint_as_float(u[n][k].x << 16)), fabsf(__uint_as_float(u[n][k].x & 0xFFFF0000u))),
-                               fmaxf(fabsf(__uint_as_float(u[n][k].y << 16)), fabsf(__uint_as_float(u[n][k].y & 0xFFFF0000u)))));
-      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-      const int e = (int)(__float_as_uint(top) >> 23) - 127;                 // floor(log2 top)
-      const int up = e == 128 || top == 0.f ? 0 : min(max(4 - e, -126), 126);
-      const float f = __uint_as_float((uint32_t)(up + 127) << 23) * p.q_sign;
-      const float back = __uint_as_float((uint32_t)(127 - up) << 23);
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        q[k][n].x = cvt_f16x2(__uint_as_float(u[n][k].x << 16) * f, __uint_as_float(u[n][k].x & 0xFFFF0000u) * f);
-        q[k][n].y = cvt_f16x2(__uint_as_float(u[n][k].y << 16) * f, __uint_as_float(u[n][k].y & 0xFFFF0000u) * f);
-      }
-      // accumulator columns: 2t, 2t + 1
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        cq[n][c] = p.scale_log2 * __shfl_sync(0xFFFFFFFFu, back, 4 * (2 * t + c));
-        lim[n][c] = limit_of(p, sp, c0 + 8 * n + 2 * t + c);
-      }
-    }
-    a.reset(cq);
-    const int min_lim = limit_of(p, sp, c0);            // the first column sees the fewest keys
-
-    for (int tl = t0; tl < tend; ++tl) {
-      const int s = stage_out;
-      if (!mbar_wait(&bar[s], (phase >> s) & 1, ac)) { ok = false; break; }
-      phase ^= 1u << s;
-      stage_out = stage_out + 1 == STG ? 0 : stage_out + 1;
-      const uint32_t bad = (bads >> (2 * s)) & 3;
-      const uint8_t* at = mem + s * C::STAGE;
-      if (bad == 0 && (tl + 1) * TILE <= min_lim) {
-#pragma unroll 1
-        for (int gr = 0; gr < 2; gr += NGS) tile_step<D, CF, NT, NGS, false>(at + gr * Gr::BYTES, q, cq, lim, tl * TILE + 16 * gr, 0, a);
-      } else {
-#pragma unroll 1
-        for (int gr = 0; gr < 2 && tl * TILE + 16 * gr < sp.kmax; ++gr)
-          tile_step<D, CF, NT, 1, true>(at + gr * Gr::BYTES, q, cq, lim, tl * TILE + 16 * gr, bad >> gr & 1, a);
-      }
-      __syncwarp();
-      if (issued < tend) {
-        if (issued - batch == 32) look_up(issued);
-        issue(issued++);
-      }
-    }
-    if (!ok) {                                          // give up: the copies in flight end first
-      for (int k = 0; k < STG; ++k) {
-        const int s = stage_out;
-        if (stage_out == stage_in && k) break;
-        mbar_drain(&bar[s], (phase >> s) & 1, ac);
-        stage_out = stage_out + 1 == STG ? 0 : stage_out + 1;
-      }
-      break;
-    }
-
-    a.finish();
+    ok = run_piece<D, CF, NT>(p, sp, b, hkv, c0, t0, t1, r, ac, a);
+    if (!ok) break;
     if (t0 == 0 && t1 == sp.tiles) {                    // all of it: write the rows
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int col = c0 + 8 * n + 2 * t + e;
-          if (col >= sp.qlen * p.G) continue;
-          const Row row(p, b, hkv, col, sp, a.m[n][e], a.l[n][e]);
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) row.put(p, 16 * k + 2 * g, make_float2(a.o[k][n][e], a.o[k][n][2 + e]));
-          if (g == 0) row.put_lse(p);
-        }
+      put_rows<D, CF, NT>(p, sp, b, hkv, c0, a);
     } else if (lo < hi) {                               // the end of a segment that began before this warp
       seg_lead = seg;
       put_part<D, CF, NT>(warp == 0 ? entering : leads + warp * C::PART, a);
@@ -742,77 +865,46 @@ __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(
     next();
   }
 
-  // Join the pieces of each segment that the CTA's warps share: the warps whose open pieces
-  // belong to it do it, an even share of the elements each.  A segment that began and ends
-  // in this CTA is written; one that came from the CTA before, or goes on to the next, is
-  // a part for the second kernel.
+  // Join the pieces of each segment that the CTA's warps share, a column a warp.  A segment
+  // that began and ends in this CTA is written; one that came from the CTA before, or goes
+  // on to the next, is a part for the second kernel.
   __syncthreads();                                      // every ring is done with
   float* parts = reinterpret_cast<float*>(ring);
   const int active = max(1, min(wpc, NW - (int)blockIdx.x * wpc));     // warps of this CTA that have a share
   if (!ok) seg_lead = seg_open = -1;
-  if (lane == 0 && warp == 0) ends->x = open_begins;
-  if (lane == 0 && warp == active - 1) ends->y = open_rest;
-  if (lane == 0) pieces[warp] = make_int2(seg_lead, seg_open);
+  if (lane == 0) {
+    pieces[warp] = make_int4(seg_lead, seg_open, sp.qlen, sp.len);
+    if (warp == 0) ends->x = open_begins;
+    if (warp == active - 1) ends->y = open_rest;
+  }
+  if (seg_open >= 0) put_part<D, CF, NT>(parts + warp * C::PART, a);
   __syncthreads();
   int4 start = make_int4(-1, 0, 0, 0);
-  int w0 = warp, w1 = warp;
-  bool lead = false;
-  if (seg_open >= 0) {
-    while (w0 > 0 && pieces[w0 - 1].y == seg_open) --w0;
-    while (w1 + 1 < active && pieces[w1 + 1].y == seg_open) ++w1;
-    lead = w1 + 1 < active && pieces[w1 + 1].x == seg_open;
-  }
-  const int n = w1 - w0 + 1 + (lead ? 1 : 0);
-  // whether it began in this CTA is known to its first warp, where it ends to its last
-  const bool begins = w0 > 0 || ends->x != 0;
-  const int rest = lead || w1 + 1 < active ? 0 : ends->y;
-  float* dst = !begins ? entering : p.partials + (int64_t)(2 * blockIdx.x + 1) * C::PART;
-  if (seg_open >= 0) {
-    if (begins && rest > 0) start = make_int4(seg_open, sh.of(hi + rest - 1) / wpc, 0, 0);
-    put_part<D, CF, NT>(n == 1 ? dst : parts + warp * C::PART, a);     // (n = 1: it goes on, or came)
-  }
-  if (warp == active - 1 && lane == 0) p.starts[blockIdx.x] = start;
-  __syncthreads();
-  if (seg_open >= 0 && n > 1) {
-    auto part = [&](int k) { return w0 + k <= w1 ? parts + (w0 + k) * C::PART : leads + (w1 + 1) * C::PART; };
-    const bool whole = begins && rest == 0;
-    const int vs = seg_open / p.c.Hkv, hs = seg_open - vs * p.c.Hkv;
+  for (int w0 = 0, w1, turn = 0; w0 < active; w0 = w1) {
+    const int4 pc = pieces[w0];
+    w1 = w0 + 1;
+    if (pc.y < 0) continue;
+    while (w1 < active && pieces[w1].y == pc.y) ++w1;
+    const bool lead = w1 < active && pieces[w1].x == pc.y;
+    const int n = w1 - w0 + (lead ? 1 : 0);
+    // whether it began in this CTA is known to its first warp, where it ends to its last
+    const bool begins = w0 > 0 || ends->x != 0;
+    const int rest = lead || w1 < active ? 0 : ends->y;
+    if (begins && rest > 0) start = make_int4(pc.y, sh.of(sh.first(blockIdx.x * wpc + w1) + rest - 1) / wpc, 0, 0);
+    const int vs = pc.y / p.c.Hkv, hs = pc.y - vs * p.c.Hkv;
     const int b = p.CT == 1 ? vs : vs / p.CT, c0 = (vs - b * p.CT) * C::COLS;
-    for (int col = warp - w0; col < C::COLS; col += w1 - w0 + 1) {     // a warp a column
-      if (c0 + col >= sp.qlen * p.G) break;
-      float m = M_NONE * 2.f, l = 0.f;
-      float2 o[D / 64];
-#pragma unroll
-      for (int x = 0; x < D / 64; ++x) o[x] = make_float2(0.f, 0.f);
-#pragma unroll 4
-      for (int k = 0; k < n; ++k) m = fmaxf(m, part(k)[C::COLS * D + col]);
-#pragma unroll 4
-      for (int k = 0; k < n; ++k) {
-        const float* pk = part(k);
-        const float f = exp2f(pk[C::COLS * D + col] - m);
-        l = fmaf(f, pk[C::COLS * (D + 1) + col], l);
-#pragma unroll
-        for (int x = 0; x < D / 64; ++x) {
-          const float2 v = *reinterpret_cast<const float2*>(pk + col * D + 64 * x + 2 * lane);
-          o[x].x = fmaf(f, v.x, o[x].x);
-          o[x].y = fmaf(f, v.y, o[x].y);
-        }
-      }
-      if (whole) {
-        const Row row(p, b, hs, c0 + col, sp, m, l);
-#pragma unroll
-        for (int x = 0; x < D / 64; ++x) row.put(p, 64 * x + 2 * lane, o[x]);
-        if (lane == 0) row.put_lse(p);
-      } else {
-#pragma unroll
-        for (int x = 0; x < D / 64; ++x) *reinterpret_cast<float2*>(dst + col * D + 64 * x + 2 * lane) = o[x];
-        if (lane == 0) {
-          dst[C::COLS * D + col] = m;
-          dst[C::COLS * (D + 1) + col] = l;
-        }
-      }
+    const Span sg{pc.z, pc.w, 0, 0};
+    const int cols = min(C::COLS, sg.qlen * p.G - c0);
+    int col = warp - turn;                              // the columns of all segments in turn
+    if (col < 0) col += NWC;
+    turn = (turn + cols) % NWC;
+    for (; col < cols; col += NWC) {
+      const Column<D, C::COLS> sum([&](int k) { return w0 + k < w1 ? parts + (w0 + k) * C::PART : leads + w1 * C::PART; }, n, col);
+      if (begins && rest == 0) sum.put_row(p, sg, b, hs, c0 + col);
+      else sum.put_part(begins ? p.partials + (int64_t)(2 * blockIdx.x + 1) * C::PART : entering, col);
     }
   }
+  if (threadIdx.x == 0) p.starts[blockIdx.x] = start;
 }
 
 // Joins the parts of the segments that several CTAs share.  Block (c, y) takes the one that
@@ -870,10 +962,27 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_join_kernel(const CacheAtt
   }
 }
 
+// Which kernel: segments of at most 24 tiles, or of at most 64 when there are two or more
+// for each SM, go to a CTA each; else the list is split evenly.  (The table's width bounds
+// a segment's tiles; the lengths are on the device.)
+bool whole_segments(const CacheAttnArgs& a, int sms) {
+  const int64_t tiles = (((int64_t)a.max_pages << a.c.page_shift) + TILE - 1) / TILE;
+  const int64_t segments = (int64_t)a.B * a.CT * a.c.Hkv;
+  return segments <= INT32_MAX && (tiles <= WHOLE_T1 || (tiles <= WHOLE_T2 && segments >= 2 * sms));
+}
+
 template <int D, int CF, int NT>
 cudaError_t launch(const CacheAttnArgs& a, int sms, cudaStream_t st) {
   using C = Cfg<D, CF, NT>;
-  cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, CF, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  cudaError_t e;
+  if (whole_segments(a, sms)) {
+    constexpr int smem = WholeCfg<D, CF, NT>::SMEM;
+    e = cudaFuncSetAttribute(cache_attn_whole_kernel<D, CF, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cache_attn_whole_kernel<D, CF, NT><<<a.B * a.CT * a.c.Hkv, WHOLE_WARPS * 32, smem, st>>>(a);
+    return cudaGetLastError();
+  }
+  e = cudaFuncSetAttribute(cache_attn_kernel<D, CF, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   cache_attn_kernel<D, CF, NT><<<sms, C::NWC * 32, C::SMEM, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
