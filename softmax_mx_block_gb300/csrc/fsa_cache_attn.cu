@@ -33,9 +33,6 @@
 namespace fsa {
 namespace {
 
-#ifndef NGS
-#define NGS 2
-#endif
 #ifndef WHOLE_T1
 #define WHOLE_T1 24
 #endif
@@ -48,10 +45,6 @@ namespace {
 // warps of a CTA, by the registers that a warp's columns take
 template <int D, int NT>
 __host__ __device__ constexpr int cta_warps() { return NT == 1 ? NW1 : D == 128 ? 8 : 12; }
-#ifndef STGS
-#define STGS 3
-#endif
-constexpr int STG = STGS;           // stages of a warp's ring
 constexpr int TILE = 32;            // keys of a tile
 #ifndef EXTRA_TILES
 #define EXTRA_TILES 2
@@ -67,9 +60,11 @@ struct Cfg {
   static constexpr int STAGE = 2 * Gr::BYTES;
   static constexpr int COLS = 8 * NT;
   static constexpr int PART = COLS * (D + 2);        // floats of a partial result: rows, maxima, sums
+  static constexpr int STG = CF == CF_MX ? 3 : 2;   // stages of a warp's ring
   static constexpr int RING = NWC * STG * STAGE;
   static constexpr int JOIN = NWC * PART * 4;
-  static constexpr int SMEM = 1024 + NWC * 32 * 8 + JOIN + (RING > JOIN ? RING : JOIN);
+  static constexpr int SCALES = TILE * Gr::SB * 8;   // unpacked scales of a tile: a word each for K and for V
+  static constexpr int SMEM = 1024 + NWC * 32 * 8 + NWC * SCALES + JOIN + (RING > JOIN ? RING : JOIN);
 };
 
 // ---------------------------------------------------------------- the work list
@@ -117,23 +112,6 @@ __device__ __forceinline__ int limit_of(const CacheAttnArgs& p, const Span& s, i
   if (i >= s.qlen) return 0;
   return p.causal ? max(0, s.len - s.qlen + i + 1) : s.len;
 }
-
-// Scale bytes of one row as packed words: SB/4 of them (D = 64 with E8M0: two bytes of one).
-template <int D, int CF>
-struct RowScales {
-  static constexpr int N = CacheGroup<D, CF>::SB > 4 ? 2 : 1;
-  uint32_t w[N];
-  __device__ __forceinline__ void load(const uint8_t* at) {
-    if constexpr (CacheGroup<D, CF>::SB == 8) {
-      const uint2 u = *reinterpret_cast<const uint2*>(at);
-      w[0] = u.x; w[1] = u.y;
-    } else if constexpr (CacheGroup<D, CF>::SB == 4) {
-      w[0] = *reinterpret_cast<const uint32_t*>(at);
-    } else {
-      w[0] = *reinterpret_cast<const uint16_t*>(at);
-    }
-  }
-};
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -209,24 +187,94 @@ struct Acc {
   }
 };
 
-// NG groups of 16 keys from shared memory.  first: position of the first key; bad: groups
-// without a page.  MASK: some column does not see some key.
+// The scales of a tile as the products take them, a token a lane: E8M0 as fp32, E4M3 as f16
+// twice in a word.  Every lane of a quad needs the same ones, so they are unpacked once.
+// Layout: 16-byte (or SB-word) pieces [K pieces][32 tokens], then V's.  Returns V's scale
+// bytes.
+template <int D, int CF>
+struct TileScales {
+  static constexpr int SB = CacheGroup<D, CF>::SB;
+  static constexpr int PW = SB < 4 ? SB : 4, PIECES = SB / PW;         // words of a piece, pieces of a row
+  static constexpr int BYTE_WORDS = SB == 8 ? 2 : 1;
+  uint32_t v[BYTE_WORDS];                                              // V's bytes of this lane's token
+
+  static __device__ __forceinline__ void unpack(const uint32_t* w, uint32_t* dst) {
+    uint32_t f[SB];
+#pragma unroll
+    for (int x = 0; x < SB; x += 2) {
+      const uint32_t two = w[x / 4] >> (8 * (x % 4));
+      if constexpr (CF == CF_MX) {
+        float a, b;
+        e8m0x2_f32(two, a, b);
+        f[x] = __float_as_uint(a);
+        f[x + 1] = __float_as_uint(b);
+      } else {
+        const uint32_t h = e4m3x2_f16(two);
+        f[x] = low_twice(h);
+        f[x + 1] = high_twice(h);
+      }
+    }
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int q = 0; q < PIECES; ++q) {
+      if constexpr (PW == 4) *reinterpret_cast<uint4*>(dst + (q * TILE + lane) * 4) = make_uint4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+      else *reinterpret_cast<uint2*>(dst + lane * 2) = make_uint2(f[0], f[1]);
+    }
+  }
+  static __device__ __forceinline__ void bytes(const uint8_t* at, uint32_t* w) {
+    if constexpr (SB == 8) {
+      const uint2 u = *reinterpret_cast<const uint2*>(at);
+      w[0] = u.x; w[1] = u.y;
+    } else if constexpr (SB == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(at);
+    } else {
+      w[0] = *reinterpret_cast<const uint16_t*>(at);
+    }
+  }
+  __device__ __forceinline__ TileScales(const uint8_t* st, uint32_t* dst) {
+    using Gr = CacheGroup<D, CF>;
+    const int lane = threadIdx.x & 31;
+    const uint8_t* const grp = st + (lane >> 4) * Gr::BYTES + (lane & 15) * SB;
+    uint32_t k[BYTE_WORDS];
+    bytes(grp + Gr::KS, k);
+    bytes(grp + Gr::VS, v);
+    unpack(k, dst);
+    unpack(v, dst + TILE * SB);
+  }
+  // a row's scales: word x of token tok, of K (from = sc) or V (from = sc + TILE * SB)
+  static __device__ __forceinline__ void row(const uint32_t* from, int tok, uint32_t* f) {
+#pragma unroll
+    for (int q = 0; q < PIECES; ++q) {
+      if constexpr (PW == 4) {
+        const uint4 u = *reinterpret_cast<const uint4*>(from + (q * TILE + tok) * 4);
+        f[4 * q] = u.x; f[4 * q + 1] = u.y; f[4 * q + 2] = u.z; f[4 * q + 3] = u.w;
+      } else {
+        const uint2 u = *reinterpret_cast<const uint2*>(from + tok * 2);
+        f[0] = u.x; f[1] = u.y;
+      }
+    }
+  }
+};
+
+// NG groups of 16 keys of a tile, from group g0 on, in shared memory.  sc: the tile's unpacked
+// scales; vs: V's scale bytes of this lane's token (0 for a token that no column sees);
+// first: position of the tile's first key; bad: groups without a page.  MASK: some column
+// does not see some key.
 template <int D, int CF, int NT, int NG, bool MASK>
-__device__ __forceinline__ void tile_step(const uint8_t* st, const uint2 (&q)[D / 16][NT], const float (&cq)[NT][2],
+__device__ __forceinline__ void tile_step(const uint8_t* st, const uint32_t* sc, const uint32_t (&vs)[TileScales<D, CF>::BYTE_WORDS], int g0,
+                                          const uint2 (&q)[D / 16][NT], const float (&cq)[NT][2],
                                           const int (&lim)[NT][2], int first, uint32_t bad, Acc<D, CF, NT>& a) {
   using Gr = CacheGroup<D, CF>;
+  using Ts = TileScales<D, CF>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int tok = (g >> 1) + 4 * (g & 1);            // the key of S^T row g (and 8 more for row g + 8)
   float s[NG][NT][4];
-  RowScales<D, CF> vs[NG][2];
 #pragma unroll
   for (int gr = 0; gr < NG; ++gr) {
-    const uint8_t* base = st + gr * Gr::BYTES;
-    RowScales<D, CF> ks[2];
-    ks[0].load(base + Gr::KS + tok * Gr::SB);
-    ks[1].load(base + Gr::KS + (tok + 8) * Gr::SB);
-    vs[gr][0].load(base + Gr::VS + tok * Gr::SB);
-    vs[gr][1].load(base + Gr::VS + (tok + 8) * Gr::SB);
+    const uint8_t* base = st + (g0 + gr) * Gr::BYTES;
+    uint32_t ks[2][Gr::SB];
+    Ts::row(sc, 16 * (g0 + gr) + tok, ks[0]);
+    Ts::row(sc, 16 * (g0 + gr) + tok + 8, ks[1]);
     uint32_t w0[D / 32], w1[D / 32];
     const uint8_t* kr = base + Gr::K + tok * (D / 2) + t * (D / 8);
     if constexpr (D == 128) {
@@ -242,15 +290,13 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint2 (&q)[D 
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[gr][n][e] = 0.f;
-    [[maybe_unused]] float kf0[2], kf1[2];
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) {
       uint32_t r0[4], r1[4];
       cvt_e2m1x8_f16(w0[j], r0);
       cvt_e2m1x8_f16(w1[j], r1);
       if constexpr (CF == CF_NV) {                   // code times E4M3 scale: 6 bits, exact in f16
-        const uint32_t f0 = e4m3x2_f16(ks[0].w[j / 2] >> (16 * (j & 1))), f1 = e4m3x2_f16(ks[1].w[j / 2] >> (16 * (j & 1)));
-        const uint32_t f0l = low_twice(f0), f0h = high_twice(f0), f1l = low_twice(f1), f1h = high_twice(f1);
+        const uint32_t f0l = ks[0][2 * j], f0h = ks[0][2 * j + 1], f1l = ks[1][2 * j], f1h = ks[1][2 * j + 1];
         r0[0] = hmul2(r0[0], f0l); r0[1] = hmul2(r0[1], f0l); r0[2] = hmul2(r0[2], f0h); r0[3] = hmul2(r0[3], f0h);
         r1[0] = hmul2(r1[0], f1l); r1[1] = hmul2(r1[1], f1l); r1[2] = hmul2(r1[2], f1h); r1[3] = hmul2(r1[3], f1h);
       }
@@ -262,11 +308,7 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint2 (&q)[D 
           mma_f16_16816(s[gr][n], hi, q[2 * j + 1][n].x, q[2 * j + 1][n].y);
         }
       } else {                                       // the E8M0 scale has fp32's range: on the block's sum
-        if ((j & 1) == 0) {
-          e8m0x2_f32(ks[0].w[0] >> (8 * j), kf0[0], kf0[1]);
-          e8m0x2_f32(ks[1].w[0] >> (8 * j), kf1[0], kf1[1]);
-        }
-        const float f0 = kf0[j & 1], f1 = kf1[j & 1];
+        const float f0 = __uint_as_float(ks[0][j]), f1 = __uint_as_float(ks[1][j]);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float c[4];
@@ -285,37 +327,24 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint2 (&q)[D 
   if (MASK) {
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr) {
-      const int k0 = first + 16 * gr + tok, k1 = k0 + 8;
-      const bool gone = (bad >> gr) & 1;
-      uint32_t any0 = 0, any1 = 0;
+      const int k0 = first + 16 * (g0 + gr) + tok, k1 = k0 + 8;
+      const bool gone = (bad >> (g0 + gr)) & 1;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         seen[gr][n][0] = gone ? 0u : (k0 < lim[n][0] ? 0xFFFFu : 0u) | (k0 < lim[n][1] ? 0xFFFF0000u : 0u);
         seen[gr][n][1] = gone ? 0u : (k1 < lim[n][0] ? 0xFFFFu : 0u) | (k1 < lim[n][1] ? 0xFFFF0000u : 0u);
-        any0 |= seen[gr][n][0];
-        any1 |= seen[gr][n][1];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (!(seen[gr][n][e >> 1] & (e & 1 ? 0xFFFF0000u : 0xFFFFu))) s[gr][n][e] = -INFINITY;
-      }
-      // a key that none of this thread's columns sees has no part in r either
-#pragma unroll
-      for (int x = 0; x < RowScales<D, CF>::N; ++x) {
-        if (!any0) vs[gr][0].w[x] = 0;
-        if (!any1) vs[gr][1].w[x] = 0;
       }
     }
   }
 
   // raise the running maxima where a score or a scale asks for it
-  uint32_t vm = 0;                                   // largest scale bytes, in the high bytes of the halves
+  uint32_t vm = a.vtop;                              // with this token's scale bytes in the high bytes of the halves
 #pragma unroll
-  for (int gr = 0; gr < NG; ++gr)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int x = 0; x < RowScales<D, CF>::N; ++x) vm = __vimax3_u16x2(vm, vs[gr][h].w[x], vs[gr][h].w[x] << 8);
-  bool raise = __vmaxu2(vm, a.vtop) != a.vtop;
+  for (int x = 0; x < Ts::BYTE_WORDS; ++x) vm = __vimax3_u16x2(vm, vs[x], vs[x] << 8);
+  bool raise = vm != a.vtop;
   float top[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -329,14 +358,10 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint2 (&q)[D 
     constexpr uint32_t NAN_BYTE = CF == CF_MX ? 0xFF : 0x7F;
     uint32_t v = 0;
 #pragma unroll
-    for (int gr = 0; gr < NG; ++gr)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int x = 0; x < Gr::SB; ++x) {
-          const uint32_t byte = (vs[gr][h].w[x / 4] >> (8 * (x % 4))) & 0xFF;
-          if (byte != NAN_BYTE) v = max(v, byte);
-        }
+    for (int x = 0; x < Gr::SB; ++x) {
+      const uint32_t byte = (vs[x / 4] >> (8 * (x % 4))) & 0xFF;
+      if (byte != NAN_BYTE) v = max(v, byte);
+    }
     v = __reduce_max_sync(0xFFFFFFFFu, v);
     const int r_old = a.r;
     if (v > (a.vtop >> 24)) a.set_r(max(Acc<D, CF, NT>::R_MIN, CF == CF_MX ? (int)v - 126 : (int)(v >> 3) - 6));   // 2^r > scale
@@ -360,7 +385,7 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint2 (&q)[D 
   // probabilities, and the products with V
 #pragma unroll
   for (int gr = 0; gr < NG; ++gr) {
-    const uint8_t* base = st + gr * Gr::BYTES;
+    const uint8_t* base = st + (g0 + gr) * Gr::BYTES;
     float x4[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -370,23 +395,15 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint2 (&q)[D 
         a.l[n][e & 1] += x4[n][e];
       }
     // E8M0 scales multiply in fp32 and the product is rounded; E4M3 ones multiply p as f16
-    uint32_t p[NT][2], f[2][Gr::SB / 2];
-    float vf[2][Gr::SB];
+    uint32_t p[NT][2], vf[2][Gr::SB];
+    Ts::row(sc + TILE * Gr::SB, 16 * (g0 + gr) + tok, vf[0]);
+    Ts::row(sc + TILE * Gr::SB, 16 * (g0 + gr) + tok + 8, vf[1]);
     if constexpr (CF == CF_NV) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         p[n][0] = cvt_f16x2(x4[n][0], x4[n][1]);     // row g: columns 2t, 2t + 1
         p[n][1] = cvt_f16x2(x4[n][2], x4[n][3]);     // row g + 8
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int x = 0; x < Gr::SB / 2; ++x) f[h][x] = e4m3x2_f16(vs[gr][h].w[x / 2] >> (16 * (x & 1)));
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int x = 0; x < Gr::SB; x += 2) e8m0x2_f32(vs[gr][h].w[0] >> (8 * x), vf[h][x], vf[h][x + 1]);
     }
     // V rows of the keys t, 4 + t, 8 + t, 12 + t, interleaved so that a pair of f16 is one
     // dim of two keys
@@ -427,11 +444,12 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint2 (&q)[D 
           for (int n = 0; n < NT; ++n) {
             uint32_t p0, p1;
             if constexpr (CF == CF_NV) {
-              p0 = hmul2(p[n][0], blk & 1 ? high_twice(f[0][blk / 2]) : low_twice(f[0][blk / 2]));
-              p1 = hmul2(p[n][1], blk & 1 ? high_twice(f[1][blk / 2]) : low_twice(f[1][blk / 2]));
+              p0 = hmul2(p[n][0], vf[0][blk]);
+              p1 = hmul2(p[n][1], vf[1][blk]);
             } else {
-              p0 = cvt_f16x2(x4[n][0] * vf[0][blk], x4[n][1] * vf[0][blk]);
-              p1 = cvt_f16x2(x4[n][2] * vf[1][blk], x4[n][3] * vf[1][blk]);
+              const float v0 = __uint_as_float(vf[0][blk]), v1 = __uint_as_float(vf[1][blk]);
+              p0 = cvt_f16x2(x4[n][0] * v0, x4[n][1] * v0);
+              p1 = cvt_f16x2(x4[n][2] * v1, x4[n][3] * v1);
             }
             if (MASK) { p0 &= seen[gr][n][0]; p1 &= seen[gr][n][1]; }   // 0 times a masked key's NaN scale
             b0[n] = transpose_8x8(p0);
@@ -495,6 +513,7 @@ __device__ __forceinline__ void put_part(float* part, const Acc<D, CF, NT>& a) {
 struct Ring {
   uint64_t* bar;
   uint8_t* mem;
+  uint32_t* scales;        // of the tile at work
   uint32_t phase;          // bit s: the phase to wait for next on stage s
   int in, out;
 };
@@ -506,6 +525,7 @@ __device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const Span& sp
                                           Ring& r, const AbortCtl& ac, Acc<D, CF, NT>& a) {
   using C = Cfg<D, CF, NT>;
   using Gr = CacheGroup<D, CF>;
+  constexpr int STG = C::STG;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   bool ok = true;
   float cq[NT][2];                                      // what a raw score of a column is multiplied by (log2 units)
@@ -599,13 +619,18 @@ __device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const Span& sp
     r.out = r.out + 1 == STG ? 0 : r.out + 1;
     const uint32_t bad = (bads >> (2 * s)) & 3;
     const uint8_t* at = r.mem + s * C::STAGE;
+    TileScales<D, CF> ts(at, r.scales);
+    __syncwarp();
     if (bad == 0 && (tl + 1) * TILE <= min_lim) {
-#pragma unroll 1
-      for (int gr = 0; gr < 2; gr += NGS) tile_step<D, CF, NT, NGS, false>(at + gr * Gr::BYTES, q, cq, lim, tl * TILE + 16 * gr, 0, a);
+      tile_step<D, CF, NT, 2, false>(at, r.scales, ts.v, 0, q, cq, lim, tl * TILE, 0, a);
     } else {
+      if (tl * TILE + lane >= sp.kmax || (bad >> (lane >> 4) & 1)) {     // no part in the offset of V's scales
+#pragma unroll
+        for (int x = 0; x < TileScales<D, CF>::BYTE_WORDS; ++x) ts.v[x] = 0;
+      }
 #pragma unroll 1
       for (int gr = 0; gr < 2 && tl * TILE + 16 * gr < sp.kmax; ++gr)
-        tile_step<D, CF, NT, 1, true>(at + gr * Gr::BYTES, q, cq, lim, tl * TILE + 16 * gr, bad >> gr & 1, a);
+        tile_step<D, CF, NT, 1, true>(at, r.scales, ts.v, gr, q, cq, lim, tl * TILE, bad, a);
     }
     __syncwarp();
     if (issued < tend) {
@@ -694,17 +719,19 @@ constexpr int WHOLE_WARPS = 4;
 template <int D, int CF, int NT>
 struct WholeCfg {
   using C = Cfg<D, CF, NT>;
-  static constexpr int RING = WHOLE_WARPS * STG * C::STAGE, JOIN = WHOLE_WARPS * C::PART * 4;
-  static constexpr int SMEM = 1024 + (RING > JOIN ? RING : JOIN);
+  static constexpr int RING = WHOLE_WARPS * C::STG * C::STAGE, JOIN = WHOLE_WARPS * C::PART * 4;
+  static constexpr int SMEM = 1024 + WHOLE_WARPS * C::SCALES + (RING > JOIN ? RING : JOIN);
   static constexpr int CTAS = NT == 2 && D == 128 ? 2 : 3;
 };
 template <int D, int CF, int NT>
 __global__ void __launch_bounds__(WHOLE_WARPS * 32, WholeCfg<D, CF, NT>::CTAS) cache_attn_whole_kernel(const CacheAttnArgs p) {
   using C = Cfg<D, CF, NT>;
   extern __shared__ __align__(1024) uint8_t smem[];
+  constexpr int STG = C::STG;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(smem);
   int* const flag = reinterpret_cast<int*>(smem + 512);
-  uint8_t* const ring = smem + 1024;
+  uint32_t* const scales = reinterpret_cast<uint32_t*>(smem + 1024);
+  uint8_t* const ring = smem + 1024 + WHOLE_WARPS * C::SCALES;
   const int warp = threadIdx.x >> 5;
   const AbortCtl ac{flag, p.status, p.timeout_ns};
   const int vb = blockIdx.x / p.c.Hkv, hkv = blockIdx.x - vb * p.c.Hkv;
@@ -715,7 +742,7 @@ __global__ void __launch_bounds__(WHOLE_WARPS * 32, WholeCfg<D, CF, NT>::CTAS) c
   if (threadIdx.x < WHOLE_WARPS * STG) mbar_init(&bars[threadIdx.x], 1);
   fence_mbar_init();
   __syncthreads();
-  Ring r{bars + warp * STG, ring + warp * STG * C::STAGE, 0, 0, 0};
+  Ring r{bars + warp * STG, ring + warp * STG * C::STAGE, scales + warp * C::SCALES / 4, 0, 0, 0};
   Acc<D, CF, NT> a;
   const int n = min(WHOLE_WARPS, sp.tiles), t0 = sp.tiles * warp / n, t1 = sp.tiles * (warp + 1) / n;
   bool ok = true;
@@ -738,7 +765,7 @@ __global__ void __launch_bounds__(WHOLE_WARPS * 32, WholeCfg<D, CF, NT>::CTAS) c
 template <int D, int CF, int NT>
 __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(const CacheAttnArgs p) {
   using C = Cfg<D, CF, NT>;
-  constexpr int NWC = C::NWC;
+  constexpr int NWC = C::NWC, STG = C::STG;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem);                  // [NWC][STG]
   int* flag = reinterpret_cast<int*>(smem + 512);                      // abort
@@ -746,8 +773,9 @@ __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(
   int2* ends = reinterpret_cast<int2*>(smem + 520);                    // x: the first open piece begins, y: tiles behind the last
   int4* pieces = reinterpret_cast<int4*>(smem + 704);                  // [NWC] segments of the leading and the open piece; its qlen, len
   int64_t* pre = reinterpret_cast<int64_t*>(smem + 1024);              // [NWC * 32]
-  float* leads = reinterpret_cast<float*>(smem + 1024 + NWC * 32 * 8);  // [NWC] parts
-  uint8_t* ring = smem + 1024 + NWC * 32 * 8 + C::JOIN;
+  uint32_t* scales = reinterpret_cast<uint32_t*>(smem + 1024 + NWC * 32 * 8);
+  float* leads = reinterpret_cast<float*>(smem + 1024 + NWC * 32 * 8 + NWC * C::SCALES);  // [NWC] parts
+  uint8_t* ring = smem + 1024 + NWC * 32 * 8 + NWC * C::SCALES + C::JOIN;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const AbortCtl ac{flag, p.status, p.timeout_ns};
 
@@ -811,7 +839,7 @@ __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(
   Acc<D, CF, NT> a;
   Span sp;
   int vb = 0, hkv = 0, unit = 0;
-  Ring r{bars + warp * STG, ring + warp * STG * C::STAGE, 0, 0, 0};
+  Ring r{bars + warp * STG, ring + warp * STG * C::STAGE, scales + warp * C::SCALES / 4, 0, 0, 0};
 
   if (lo < hi) {
     int j = 0;                                         // the last chunk that begins at or before lo
