@@ -507,7 +507,9 @@ typedef struct {
   uint32_t         timeout_ms;
 } fsa_cache_attn;
 
-int fsa_attention_cache_workspace(int B, int H, int Hkv, int Sq, int D, size_t* bytes);
+/* Bytes of the workspace of such a call on the current device: 0 where it needs none (short
+ * block tables), and its workspace may then be NULL. */
+int fsa_attention_cache_workspace(const fsa_cache* cache, int B, int H, int Sq, int max_pages, size_t* bytes);
 int fsa_attention_cache(const fsa_cache_attn* args, void* stream);
 
 /* ------------------------------------------------------ tensor-core peak probe */

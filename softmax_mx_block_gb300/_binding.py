@@ -5,9 +5,9 @@ compiled library every entry point raises."""
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.machinery
+import importlib.util
 import os
-import struct
 import threading
 
 import torch
@@ -108,6 +108,7 @@ FSA_OUT_F32, FSA_OUT_BF16 = 0, 1
 STATS_BYTES = 24      # fsa_stats: u64 fallback_events, u64 row_tiles, i32 status, i32 reserved
 
 _lib = None
+_torch_module = None
 _lock = threading.Lock()
 
 
@@ -138,12 +139,13 @@ def load(build_if_missing: bool = True):
             L.fsa_attention_fwd_host.argtypes = [ctypes.POINTER(fsa_host_io), ctypes.POINTER(fsa_device_io),
                                                  i, i, i, i, i, i, i, f, i, i, ctypes.POINTER(fsa_opts), vp, i, vp]
             L.fsa_tune_delta.argtypes = [ctypes.POINTER(fsa_stats), i, f, f, f, ctypes.POINTER(ctypes.c_float)]
-            L.fsa_qk_norm_rope.argtypes = [vp, vp]                  # packed fsa_norm_rope
+            L.fsa_qk_norm_rope.argtypes = [ctypes.POINTER(fsa_norm_rope), vp]
             L.fsa_cache_page_bytes.argtypes = [i, i, i, i, ctypes.POINTER(ctypes.c_size_t)]
             for n in ("fsa_cache_append", "fsa_cache_read"):
-                getattr(L, n).argtypes = [ctypes.POINTER(fsa_cache), vp, vp, vp, vp, i, i, vp, i, vp, vp, vp, vp]
-            L.fsa_attention_cache_workspace.argtypes = [i, i, i, i, i, ctypes.POINTER(ctypes.c_size_t)]
-            L.fsa_attention_cache.argtypes = [vp, vp]               # packed fsa_cache_attn
+                getattr(L, n).argtypes = [ctypes.POINTER(fsa_cache), vp, vp, ctypes.POINTER(fsa_strides),
+                                          ctypes.POINTER(fsa_strides), i, i, vp, i, vp, vp, vp, vp]
+            L.fsa_attention_cache_workspace.argtypes = [ctypes.POINTER(fsa_cache), i, i, i, i, ctypes.POINTER(ctypes.c_size_t)]
+            L.fsa_attention_cache.argtypes = [ctypes.POINTER(fsa_cache_attn), vp]
             L.fsa_mma_peak.argtypes = [i, i, i, ctypes.c_longlong, vp, ctypes.POINTER(ctypes.c_double), vp]
             L.fsa_bf16_transpose_v.argtypes = [vp, vp, i, i, i, i, vp]
             L.fsa_attention_fwd_bf16.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, i, f, vp, vp]
@@ -557,54 +559,23 @@ def fsa_tune_delta(stats: list, deltas: list, target_rate=0.01, step=4.0, max_de
 
 # ----------------------------------------------------------------------------- serving
 # These calls are short (a decode step's kernels run for a few microseconds), so their
-# marshalling is too: one packed argument block a call, integer device numbers, the raw
-# stream.  The packed layouts are those of the C structures above (checked on import).
-_ROPE_ARGS = struct.Struct("@4P12q4P7i3i2if0P")
-_ATTN_ARGS = struct.Struct("@3PP3PPNP6q6ifI")
-_STRIDES = struct.Struct("@3q")
-assert _ROPE_ARGS.size == ctypes.sizeof(fsa_norm_rope) and _ATTN_ARGS.size == ctypes.sizeof(fsa_cache_attn)
+# checks and marshalling are compiled (csrc/fsa_torch.cpp).
+def _serving():
+    """The extension module _fsa_torch (built with the library)."""
+    global _torch_module
+    if _torch_module is None:
+        load()
+        loader = importlib.machinery.ExtensionFileLoader("_fsa_torch", _build.TORCH_MODULE)
+        spec = importlib.util.spec_from_file_location("_fsa_torch", _build.TORCH_MODULE, loader=loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        module.set_error(FsaError)
+        _torch_module = module
+    return _torch_module
 
 
-def _strided(t: torch.Tensor, name: str, device: int, output=False, dtype=torch.bfloat16) -> tuple:
-    """Strides of a [B,S,heads,D] tensor of `dtype` on CUDA device number `device`, its rows
-    contiguous, 16-byte aligned and, for an output, apart."""
-    if t.get_device() != device or device < 0:
-        raise FsaError(FSA_ERR_INVALID_ARG, f"{name} must be a CUDA tensor on the call's device")
-    st = t.stride()
-    if len(st) != 4 or t.dtype != dtype:
-        raise FsaError(FSA_ERR_INVALID_ARG, f"{name} must be a 4-dimensional {dtype} tensor")
-    b, s, h, d = st
-    if d != 1:
-        raise FsaError(FSA_ERR_INVALID_ARG, f"{name} must be contiguous in its last dimension")
-    if (b | s | h) & 7 or (output and not (b and s and h)):
-        for n, x in zip(t.shape, (b, s, h)):
-            if n > 1 and (x & 7 or (output and not x)):
-                raise FsaError(FSA_ERR_INVALID_ARG, f"{name} strides must be multiples of 8"
-                                                    + (", and an output's rows apart" if output else ""))
-    return b, s, h
-
-
-def _index(t, name: str, shape: tuple, device: int, dtype=torch.int32) -> int:
-    """Pointer of a contiguous integer (or other) tensor of the given shape (None: null)."""
-    if t is None:
-        return 0
-    if t.get_device() != device or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        raise FsaError(FSA_ERR_INVALID_ARG, f"{name} must be a contiguous {dtype} CUDA tensor {shape} on the call's device")
-    return t.data_ptr()
-
-
-def _launch(name: str, device: int, stream, *args):
-    """Call `name` with the tensors' device as the current one (kernels launch on that), on
-    `stream` or the device's current stream."""
-    fn = getattr(_lib or load(), name)
-    raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
-    if torch._C._cuda_getDevice() == device:
-        status = fn(*args, raw)
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args, raw)
-    if status != FSA_OK:
-        raise FsaError(status, name)
+def _raw(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def fsa_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor | None, inv_freq: torch.Tensor | None, *,
@@ -615,43 +586,15 @@ def fsa_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor | None,
     position, in one pass.  pos: int32 [B,S] or [B,S,axes]; inv_freq: float64 [rotary/2];
     sections: pairs of each axis (default: all of one).  q_out, k_out default to contiguous
     tensors of q's and k's shapes; q and k themselves rotate in place.  Returns (q_out, k_out)."""
-    dev = q.get_device()
-    qs, ks = _strided(q, "q", dev), _strided(k, "k", dev)
-    shape, k_shape = q.shape, k.shape
-    B, S, H, D = shape
-    Bk, Sk, Hkv, Dk = k_shape
-    if Bk != B or Sk != S or Dk != D:
-        raise FsaError(FSA_ERR_INVALID_ARG, "q, k shapes")
-    half, axes, at, freq = 0, 1, 0, 0
-    if inv_freq is not None:
-        half = inv_freq.numel()
-        freq = _index(inv_freq, "inv_freq", (half,), dev, torch.float64)
-        if pos is None:
-            raise FsaError(FSA_ERR_INVALID_ARG, "a rotation needs pos")
-        if pos.dim() == 2:
-            at = _index(pos, "pos", (B, S), dev)
-        else:
-            axes = pos.shape[-1]
-            at = _index(pos, "pos", (B, S, axes), dev)
-    sections = (half,) if sections is None else tuple(sections)
-    if len(sections) != axes or axes > 3:
-        raise FsaError(FSA_ERR_INVALID_ARG, f"{len(sections)} sections for {axes} axes (1 to 3)")
     if q_out is None:
-        q_out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     if k_out is None:
-        k_out = torch.empty(k_shape, dtype=k.dtype, device=k.device)
-    if q_out.shape != shape or k_out.shape != k_shape:
-        raise FsaError(FSA_ERR_INVALID_ARG, "q_out, k_out shapes")
-    args = _ROPE_ARGS.pack(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), *qs, *ks,
-                           *_strided(q_out, "q_out", dev, True), *_strided(k_out, "k_out", dev, True),
-                           _index(q_weight, "q_weight", (D,), dev, torch.bfloat16),
-                           _index(k_weight, "k_weight", (D,), dev, torch.bfloat16), at, freq, B, S, H, Hkv, D,
-                           2 * half, axes, *sections, *(0,) * (3 - axes), 1 if norm else 0, 1 if interleaved else 0, eps)
-    _launch("fsa_qk_norm_rope", dev, stream, args)
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    (_torch_module or _serving()).norm_rope(q, k, pos, inv_freq, None if sections is None else tuple(sections), q_weight,
+                                            k_weight, norm, eps, interleaved, q_out, k_out, _raw(stream))
     return q_out, k_out
 
 
-@functools.lru_cache(maxsize=256)
 def fsa_cache_page_bytes(page_size, Hkv, D, fmt) -> int:
     n = ctypes.c_size_t()
     _check(load().fsa_cache_page_bytes(int(page_size), int(Hkv), int(D), _fmt(fmt), ctypes.byref(n)), "fsa_cache_page_bytes")
@@ -660,20 +603,15 @@ def fsa_cache_page_bytes(page_size, Hkv, D, fmt) -> int:
 
 class MxCache:
     """A pool of pages of 4-bit keys and values (fsa_cache): `pages` is a contiguous uint8
-    tensor [num_pages, fsa_cache_page_bytes] on the GPU, owned by torch."""
+    tensor [num_pages, fsa_cache_page_bytes] on the GPU, owned by torch; the calls check it."""
+
+    __slots__ = ("pages", "page_size", "Hkv", "D", "fmt")
 
     def __init__(self, pages: torch.Tensor, page_size: int, Hkv: int, D: int, fmt):
         self.pages, self.page_size, self.Hkv, self.D, self.fmt = pages, page_size, Hkv, D, _fmt(fmt)
-        n = fsa_cache_page_bytes(page_size, Hkv, D, self.fmt)
-        if not isinstance(pages, torch.Tensor) or pages.dtype != torch.uint8 or pages.dim() != 2 or pages.shape[1] != n \
-                or not pages.is_contiguous():
-            raise FsaError(FSA_ERR_INVALID_ARG, f"pages must be a contiguous uint8 tensor [num_pages, {n}]")
 
     def struct(self) -> fsa_cache:
-        pages = self.pages
-        if pages.get_device() < 0:
-            raise FsaError(FSA_ERR_INVALID_ARG, "pages must be a CUDA tensor")
-        return fsa_cache(pages.data_ptr(), pages.shape[0], self.page_size, self.Hkv, self.D, self.fmt)
+        return fsa_cache(self.pages.data_ptr(), self.pages.shape[0], self.page_size, self.Hkv, self.D, self.fmt)
 
 
 def empty_cache(num_pages, page_size, Hkv, D, fmt, device=None) -> MxCache:
@@ -682,28 +620,14 @@ def empty_cache(num_pages, page_size, Hkv, D, fmt, device=None) -> MxCache:
     return MxCache(torch.empty((num_pages, n), dtype=torch.uint8, device=device or "cuda"), page_size, Hkv, D, fmt)
 
 
-def _table(block_table: torch.Tensor, B: int, device: int) -> tuple:
-    shape = block_table.shape
-    if len(shape) != 2 or shape[0] != B:
-        raise FsaError(FSA_ERR_INVALID_ARG, "block_table must be [B, max_pages]")
-    return _index(block_table, "block_table", shape, device), shape[1]
-
-
 def fsa_cache_append(cache: MxCache, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor,
                      new_lens: torch.Tensor | None = None, *, status: torch.Tensor | None = None, stream=None) -> None:
     """Quantise k, v (bf16 [B,S,Hkv,D], strided) into the cache: row i < new_lens[b] (default
     all S) becomes token lens[b] - new_lens[b] + i of the sequence whose pages row b of
     block_table (int32 [B, max_pages]) names.  lens (int32 [B]) counts the new tokens too."""
-    c = cache.struct()
-    dev = cache.pages.get_device()
-    ks, vs = _strided(k, "k", dev), _strided(v, "v", dev)
-    B, S, Hkv, D = shape = k.shape
-    if v.shape != shape or D != cache.D or Hkv != cache.Hkv:
-        raise FsaError(FSA_ERR_INVALID_ARG, "k, v shapes")
-    table, width = _table(block_table, B, dev)
-    _launch("fsa_cache_append", dev, stream, c, k.data_ptr(), v.data_ptr(), _STRIDES.pack(*ks), _STRIDES.pack(*vs), B, S,
-            table, width, _index(lens, "lens", (B,), dev), _index(new_lens, "new_lens", (B,), dev),
-            _index(status, "status", (1,), dev))
+    c = cache
+    (_torch_module or _serving()).cache_append(c.pages, c.page_size, c.Hkv, c.D, c.fmt, k, v, block_table, lens, new_lens,
+                                               status, _raw(stream))
 
 
 def fsa_cache_read(cache: MxCache, block_table: torch.Tensor, lens: torch.Tensor, S: int | None = None, *,
@@ -713,33 +637,22 @@ def fsa_cache_read(cache: MxCache, block_table: torch.Tensor, lens: torch.Tensor
     start 0) where that lies before lens[b]; other rows are left as they were.  k_out, v_out:
     bf16 [B,S,Hkv,D], strided; without either, both are made (zeros, S rows).  Returns
     (k_out, v_out)."""
-    c = cache.struct()
-    dev = cache.pages.get_device()
-    B = lens.shape[0]
+    c = cache
     if k_out is None and v_out is None:
         if S is None:
             raise FsaError(FSA_ERR_INVALID_ARG, "S, k_out or v_out must be given")
-        k_out = torch.zeros((B, S, cache.Hkv, cache.D), dtype=torch.bfloat16, device=cache.pages.device)
+        k_out = torch.zeros((lens.shape[0], S, c.Hkv, c.D), dtype=torch.bfloat16, device=c.pages.device)
         v_out = torch.zeros_like(k_out)
-    S = (v_out if k_out is None else k_out).shape[1] if S is None else S
-    ptr, strides = [0, 0], [None, None]
-    for i, t in enumerate((k_out, v_out)):
-        if t is not None:
-            n = "v_out" if i else "k_out"
-            strides[i] = _STRIDES.pack(*_strided(t, n, dev, True))
-            if t.shape != (B, S, cache.Hkv, cache.D):
-                raise FsaError(FSA_ERR_INVALID_ARG, f"{n} must be [B, S, Hkv, D]")
-            ptr[i] = t.data_ptr()
-    table, width = _table(block_table, B, dev)
-    _launch("fsa_cache_read", dev, stream, c, *ptr, *strides, B, S, table, width, _index(lens, "lens", (B,), dev),
-            _index(start, "start", (B,), dev), _index(status, "status", (1,), dev))
+    (_torch_module or _serving()).cache_read(c.pages, c.page_size, c.Hkv, c.D, c.fmt, k_out, v_out, block_table, lens, start,
+                                             status, _raw(stream))
     return k_out, v_out
 
 
-def fsa_attention_cache_workspace(B, H, Hkv, Sq, D) -> int:
-    """Bytes of the workspace of fsa_attention_cache on the current device."""
-    n = ctypes.c_size_t()
-    _check(load().fsa_attention_cache_workspace(B, H, Hkv, Sq, D, ctypes.byref(n)), "fsa_attention_cache_workspace")
+def fsa_attention_cache_workspace(cache: MxCache, B, H, Sq, max_pages) -> int:
+    """Bytes of the workspace of fsa_attention_cache on the current device (0: it needs none)."""
+    n, c = ctypes.c_size_t(), cache.struct()
+    _check(load().fsa_attention_cache_workspace(ctypes.byref(c), B, H, Sq, max_pages, ctypes.byref(n)),
+           "fsa_attention_cache_workspace")
     return n.value
 
 
@@ -754,32 +667,14 @@ def fsa_attention_cache(q: torch.Tensor, cache: MxCache, block_table: torch.Tens
     q_lens[b] are left as they were.  lse: optional fp32 [B,Sq,H] for the log of the
     softmax sums.  workspace: uint8, at least fsa_attention_cache_workspace bytes (default:
     one of the call's own)."""
-    c = cache.struct()
-    dev = cache.pages.get_device()
-    qs = _strided(q, "q", dev)
-    B, Sq, H, D = shape = q.shape
-    if D != cache.D or H % cache.Hkv:
-        raise FsaError(FSA_ERR_INVALID_ARG, "q must have the cache's D and a multiple of its heads")
-    od, tdt = _out_dtype(out_dtype if out is None or out_dtype is not None else out.dtype)
+    c = cache
     if out is None:
-        out = (torch.empty if q_lens is None else torch.zeros)(shape, dtype=tdt, device=q.device)
-    os_ = _strided(out, "out", dev, True, tdt)
-    if out.shape != shape:
-        raise FsaError(FSA_ERR_INVALID_ARG, "out must have q's shape")
-    if workspace is None:
-        with torch.cuda.device(dev):
-            need = fsa_attention_cache_workspace(B, H, cache.Hkv, Sq, D)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        if stream is not None:
-            workspace.record_stream(stream)
-    table, width = _table(block_table, B, dev)
-    space = _index(workspace, "workspace", (workspace.numel(),), dev, torch.uint8)
-    args = _ATTN_ARGS.pack(q.data_ptr(), out.data_ptr(), _index(lse, "lse", (B, Sq, H), dev, torch.float32),
-                           ctypes.addressof(c), table, _index(lens, "lens", (B,), dev),
-                           _index(q_lens, "q_lens", (B,), dev), space, workspace.numel(),
-                           _index(status, "status", (1,), dev), *qs, *os_, B, H, Sq, width, 1 if causal else 0, od,
-                           D ** -0.5 if scale is None else scale, timeout_ms)
-    _launch("fsa_attention_cache", dev, stream, args)
+        _, dtype = _out_dtype(out_dtype)
+        out = (torch.empty if q_lens is None else torch.zeros)(q.shape, dtype=dtype, device=q.device)
+    elif out_dtype is not None and _out_dtype(out_dtype)[1] != out.dtype:
+        raise FsaError(FSA_ERR_INVALID_ARG, f"out is {out.dtype}, not {out_dtype}")
+    (_torch_module or _serving()).attention_cache(c.pages, c.page_size, c.Hkv, c.D, c.fmt, q, out, lse, block_table, lens,
+                                                  q_lens, causal, scale, workspace, timeout_ms, status, _raw(stream))
     return out
 
 

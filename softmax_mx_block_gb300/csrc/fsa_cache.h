@@ -84,9 +84,9 @@ cudaError_t launch_cache_append(const CacheIo& a, cudaStream_t st);
 cudaError_t launch_cache_read(const CacheIo& a, cudaStream_t st);
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t st);
 
-// columns (query rows of one kv head) of a pass, and the workspace of a call
+// columns (query rows of one kv head) of a pass, by eights, and the workspace of a call
 int cache_attn_ntiles(int cols);
-size_t cache_attn_workspace(int nt, int D, int sms, size_t* starts_at);
+size_t cache_attn_workspace(const Cache& c, int B, int H, int Sq, int max_pages, int sms, size_t* starts_at);
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, int nt, int sms, cudaStream_t st);
 
 }  // namespace fsa

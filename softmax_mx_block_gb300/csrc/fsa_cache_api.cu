@@ -53,8 +53,10 @@ bool take_strides(const fsa_strides* st, int B, int S, int H, bool output, fsa::
   return true;
 }
 
+bool pages_ok(int max_pages, int page_size) { return max_pages > 0 && (int64_t)max_pages * page_size <= (1 << 30); }
+
 bool table_ok(const int32_t* table, int max_pages, int page_size) {
-  return table && aligned(table, 4) && max_pages > 0 && (int64_t)max_pages * page_size <= (1 << 30);
+  return table && aligned(table, 4) && pages_ok(max_pages, page_size);
 }
 
 int cache_io(const fsa_cache* cache, const void* k, const void* v, const fsa_strides* ks, const fsa_strides* vs, int B,
@@ -169,12 +171,16 @@ int fsa_qk_norm_rope(const fsa_norm_rope* r, void* stream) {
   return launch_status(fsa::launch_qk_norm_rope(a, static_cast<cudaStream_t>(stream)));
 }
 
-int fsa_attention_cache_workspace(int B, int H, int Hkv, int Sq, int D, size_t* bytes) {
-  if (!bytes || !attn_shape_ok(B, H, Hkv, Sq, D)) return FSA_ERR_INVALID_ARG;
+int fsa_attention_cache_workspace(const fsa_cache* cache, int B, int H, int Sq, int max_pages, size_t* bytes) {
+  fsa::Cache c;
+  if (!bytes) return FSA_ERR_INVALID_ARG;
+  const int st = take_cache(cache, &c);
+  if (st != FSA_OK) return st;
+  if (!attn_shape_ok(B, H, c.Hkv, Sq, c.D) || !pages_ok(max_pages, cache->page_size)) return FSA_ERR_INVALID_ARG;
   int sms = 0;
   if (!sm_count(&sms)) return FSA_ERR_NO_DEVICE;
   size_t starts_at;
-  *bytes = fsa::cache_attn_workspace(fsa::cache_attn_ntiles(Sq * (H / Hkv)), D, sms, &starts_at);
+  *bytes = fsa::cache_attn_workspace(c, B, H, Sq, max_pages, sms, &starts_at);
   return FSA_OK;
 }
 
@@ -184,7 +190,7 @@ int fsa_attention_cache(const fsa_cache_attn* c, void* stream) {
   const int st = take_cache(c->cache, &a.c);
   if (st != FSA_OK) return st;
   const int Hkv = a.c.Hkv, D = a.c.D;
-  if (!c->q || !c->out || !c->lens || !c->workspace || !attn_shape_ok(c->B, c->H, Hkv, c->Sq, D) ||
+  if (!c->q || !c->out || !c->lens || !attn_shape_ok(c->B, c->H, Hkv, c->Sq, D) ||
       !table_ok(c->block_table, c->max_pages, c->cache->page_size) || !std::isfinite(c->scale) ||
       (c->causal != 0 && c->causal != 1) || (c->out_dtype != FSA_OUT_F32 && c->out_dtype != FSA_OUT_BF16) ||
       !aligned(c->q, 16) || !aligned(c->out, 16) || !aligned(c->workspace, 16) || !aligned(c->lens, 4) ||
@@ -197,7 +203,8 @@ int fsa_attention_cache(const fsa_cache_attn* c, void* stream) {
   if (!sm_count(&sms)) return FSA_ERR_NO_DEVICE;
   const int G = c->H / Hkv, nt = fsa::cache_attn_ntiles(c->Sq * G);
   size_t starts_at;
-  if (c->workspace_bytes < fsa::cache_attn_workspace(nt, D, sms, &starts_at)) return FSA_ERR_INVALID_ARG;
+  const size_t need = fsa::cache_attn_workspace(a.c, c->B, c->H, c->Sq, c->max_pages, sms, &starts_at);
+  if (need > 0 && (!c->workspace || c->workspace_bytes < need)) return FSA_ERR_INVALID_ARG;
   a.q = static_cast<const uint16_t*>(c->q);
   a.out = c->out;
   a.lse = c->lse;

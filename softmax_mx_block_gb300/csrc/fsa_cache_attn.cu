@@ -27,6 +27,7 @@
 //     The lengths are read on the device, so a captured call follows them.
 //   - Each warp has a ring of its own: one bulk copy per page part and tile, an mbarrier a
 //     stage.  No warp waits for another before the end.
+#include <atomic>
 #include "fsa_cache.h"
 #include "fsa_ptx.cuh"
 
@@ -267,7 +268,10 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint32_t* sc,
   using Gr = CacheGroup<D, CF>;
   using Ts = TileScales<D, CF>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int tok = (g >> 1) + 4 * (g & 1);            // the key of S^T row g (and 8 more for row g + 8)
+  // the key of S^T row g (and 8 more for row g + 8): 0 5 1 6 2 7 3 4.  Rows 2t and 2t + 1 are
+  // keys of different parity, so the two rows that a quarter of the warp loads lie in
+  // different banks; and the four even rows, which V's loads take together, are keys 0 to 3.
+  const int tok = g & 1 ? 4 + (((g >> 1) + 1) & 3) : g >> 1;
   float s[NG][NT][4];
 #pragma unroll
   for (int gr = 0; gr < NG; ++gr) {
@@ -405,20 +409,21 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint32_t* sc,
         p[n][1] = cvt_f16x2(x4[n][2], x4[n][3]);     // row g + 8
       }
     }
-    // V rows of the keys t, 4 + t, 8 + t, 12 + t, interleaved so that a pair of f16 is one
-    // dim of two keys
+    // V rows of the keys of S^T rows 2t, 2t + 1 and 8 more, interleaved so that a pair of f16
+    // is one dim of two keys
     const uint8_t* vr = base + Gr::V + t * (D / 2) + g * (D / 16);
+    const uint8_t* vr1 = base + Gr::V + (4 + ((t + 1) & 3)) * (D / 2) + g * (D / 16);
     uint32_t x[2][D / 64], y[2][D / 64];             // [half][word]: x low nibbles (dim 2g), y high (2g + 1)
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       uint32_t wa[D / 64], wb[D / 64];
-      const uint8_t* ra = vr + hf * 4 * D;
+      const uint8_t *ra = vr + hf * 4 * D, *rb = vr1 + hf * 4 * D;
       if constexpr (D == 128) {
-        const uint2 ua = *reinterpret_cast<const uint2*>(ra), ub = *reinterpret_cast<const uint2*>(ra + 2 * D);
+        const uint2 ua = *reinterpret_cast<const uint2*>(ra), ub = *reinterpret_cast<const uint2*>(rb);
         wa[0] = ua.x; wa[1] = ua.y; wb[0] = ub.x; wb[1] = ub.y;
       } else {
         wa[0] = *reinterpret_cast<const uint32_t*>(ra);
-        wb[0] = *reinterpret_cast<const uint32_t*>(ra + 2 * D);
+        wb[0] = *reinterpret_cast<const uint32_t*>(rb);
       }
 #pragma unroll
       for (int k = 0; k < D / 64; ++k) {
@@ -993,24 +998,38 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_join_kernel(const CacheAtt
 // Which kernel: segments of at most 24 tiles, or of at most 64 when there are two or more
 // for each SM, go to a CTA each; else the list is split evenly.  (The table's width bounds
 // a segment's tiles; the lengths are on the device.)
-bool whole_segments(const CacheAttnArgs& a, int sms) {
-  const int64_t tiles = (((int64_t)a.max_pages << a.c.page_shift) + TILE - 1) / TILE;
-  const int64_t segments = (int64_t)a.B * a.CT * a.c.Hkv;
+bool whole_segments(const Cache& c, int B, int CT, int max_pages, int sms) {
+  const int64_t tiles = (((int64_t)max_pages << c.page_shift) + TILE - 1) / TILE;
+  const int64_t segments = (int64_t)B * CT * c.Hkv;
   return segments <= INT32_MAX && (tiles <= WHOLE_T1 || (tiles <= WHOLE_T2 && segments >= 2 * sms));
+}
+
+// Opt in to the kernel's shared memory, once a device.
+template <class K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t>& devices) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (devices.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) devices.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 template <int D, int CF, int NT>
 cudaError_t launch(const CacheAttnArgs& a, int sms, cudaStream_t st) {
   using C = Cfg<D, CF, NT>;
   cudaError_t e;
-  if (whole_segments(a, sms)) {
+  static std::atomic<uint64_t> whole_ready{0}, list_ready{0};
+  if (whole_segments(a.c, a.B, a.CT, a.max_pages, sms)) {
     constexpr int smem = WholeCfg<D, CF, NT>::SMEM;
-    e = cudaFuncSetAttribute(cache_attn_whole_kernel<D, CF, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = allow_smem(cache_attn_whole_kernel<D, CF, NT>, smem, whole_ready);
     if (e != cudaSuccess) return e;
     cache_attn_whole_kernel<D, CF, NT><<<a.B * a.CT * a.c.Hkv, WHOLE_WARPS * 32, smem, st>>>(a);
     return cudaGetLastError();
   }
-  e = cudaFuncSetAttribute(cache_attn_kernel<D, CF, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  e = allow_smem(cache_attn_kernel<D, CF, NT>, C::SMEM, list_ready);
   if (e != cudaSuccess) return e;
   cache_attn_kernel<D, CF, NT><<<sms, C::NWC * 32, C::SMEM, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -1033,8 +1052,10 @@ cudaError_t launch(const CacheAttnArgs& a, int sms, cudaStream_t st) {
 int cache_attn_ntiles(int cols) { return cols <= 8 ? 1 : 2; }
 
 // parts of the CTAs, two each; where segments begin that go on
-size_t cache_attn_workspace(int nt, int D, int sms, size_t* starts_at) {
-  *starts_at = (size_t)2 * sms * 8 * nt * (D + 2) * sizeof(float);
+size_t cache_attn_workspace(const Cache& c, int B, int H, int Sq, int max_pages, int sms, size_t* starts_at) {
+  const int cols = Sq * (H / c.Hkv), nt = cache_attn_ntiles(cols);
+  *starts_at = (size_t)2 * sms * 8 * nt * (c.D + 2) * sizeof(float);
+  if (whole_segments(c, B, (cols + 8 * nt - 1) / (8 * nt), max_pages, sms)) return 0;
   return *starts_at + (size_t)sms * sizeof(int4);
 }
 

@@ -377,7 +377,7 @@ def test_attention_workspace_streams_and_graph():
     q = normal(g, 2, 1, H, D)
     lens = i32([900, 4000])
     first = fsa.fsa_attention_cache(q, cache, table, lens)
-    ws = torch.full((fsa.fsa_attention_cache_workspace(2, H, Hkv, 1, D),), 0xFF, dtype=torch.uint8, device="cuda")
+    ws = torch.full((fsa.fsa_attention_cache_workspace(cache, 2, H, 1, table.shape[1]),), 0xFF, dtype=torch.uint8, device="cuda")
     for _ in range(5):
         assert torch.equal(first, fsa.fsa_attention_cache(q, cache, table, lens, workspace=ws))
     side = torch.cuda.Stream()
@@ -406,7 +406,7 @@ def test_two_calls_at_once():
         cache, table, _, _ = filled_cache(fsa, g, n, 16, Hkv, D, "NVFP4")
         q = normal(g, 2, 2, H, D)
         want = fsa.fsa_attention_cache(q, cache, table, i32(n))
-        ws = torch.empty(fsa.fsa_attention_cache_workspace(2, H, Hkv, 2, D), dtype=torch.uint8, device="cuda")
+        ws = torch.empty(fsa.fsa_attention_cache_workspace(cache, 2, H, 2, table.shape[1]), dtype=torch.uint8, device="cuda")
         out, lens = torch.zeros_like(want), i32(n)
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
@@ -420,6 +420,57 @@ def test_two_calls_at_once():
     torch.cuda.synchronize()
     for _, out, want, _, _ in made:
         assert torch.equal(out, want)
+
+
+def test_calls_refuse():
+    """The binding's checks: devices, types, shapes, strides, buffers."""
+    fsa = _fsa()
+    g = gen(5)
+    lens, Hkv, D, page = [40, 2500], 2, 64, 16
+    cache, table, k, v = filled_cache(fsa, g, lens, page, Hkv, D, "E2M1")
+    n, q = i32(lens), normal(g, 2, 3, 4, D)
+    wide, host = torch.zeros(2, 3, 4, 2 * D, dtype=torch.bfloat16, device="cuda"), torch.zeros(2, dtype=torch.int32)
+    need = fsa.fsa_attention_cache_workspace(cache, 2, 4, 3, table.shape[1])
+    assert need > 0
+    pages = cache.pages
+
+    def attn(q=q, c=cache, t=table, l=n, **kw):
+        return lambda: fsa.fsa_attention_cache(q, c, t, l, **kw)
+
+    bad = [attn(q=q.float()), attn(q=q[0]), attn(q=q.transpose(2, 3)), attn(q=q.cpu()), attn(q=normal(g, 2, 3, 3, D)),
+           attn(q=normal(g, 2, 3, 4, 128)), attn(q=wide[..., 1:D + 1]), attn(q=torch.zeros(2, 3, 4, D + 4, device="cuda").bfloat16()[..., :D]),
+           attn(t=table[:1]), attn(t=table.long()), attn(t=table.t()), attn(l=n[:1]), attn(l=n.long()), attn(l=host), attn(q_lens=host),
+           attn(out=torch.zeros(2, 3, 4, D, device="cuda").half()), attn(out=torch.zeros(2, 3, 4, D)), attn(out=q[:, :2]),
+           attn(out=torch.zeros(2, 3, 1, D, device="cuda").expand(2, 3, 4, D)), attn(out=q.float(), out_dtype="bf16"),
+           attn(lse=torch.zeros(2, 4, 3, device="cuda")), attn(lse=torch.zeros(2, 3, 4, device="cuda").double()),
+           attn(workspace=torch.zeros(need - 1, dtype=torch.uint8, device="cuda")), attn(workspace=torch.zeros(need, dtype=torch.uint8)),
+           attn(status=n), attn(timeout_ms=-1), attn(scale=float("nan")),
+           attn(c=fsa.MxCache(pages[:, :-16], page, Hkv, D, "E2M1")), attn(c=fsa.MxCache(pages[::2], page, Hkv, D, "E2M1")),
+           attn(c=fsa.MxCache(pages.view(torch.int8), page, Hkv, D, "E2M1")), attn(c=fsa.MxCache(pages, page, Hkv, D, "NVFP4")),
+           attn(c=fsa.MxCache(pages, 24, Hkv, D, "E2M1")), attn(c=fsa.MxCache(pages.cpu(), page, Hkv, D, "E2M1")),
+           lambda: fsa.fsa_cache_append(cache, k, v[:, :1], table, n), lambda: fsa.fsa_cache_append(cache, q, q, table, n),
+           lambda: fsa.fsa_cache_append(cache, k.float(), v.float(), table, n), lambda: fsa.fsa_cache_append(cache, k, v, table, n, host),
+           lambda: fsa.fsa_cache_read(cache, table, n), lambda: fsa.fsa_cache_read(cache, table, n, k_out=q),
+           lambda: fsa.fsa_cache_read(cache, table, n, k_out=torch.empty_like(k), v_out=torch.empty_like(v[:, :1])),
+           lambda: fsa.fsa_cache_read(cache, table, n, k_out=k[:, :1].expand_as(k)),
+           lambda: fsa.fsa_qk_norm_rope(q, q[:1], None, None), lambda: fsa.fsa_qk_norm_rope(q, q, None, torch.ones(8, device="cuda").double()),
+           lambda: fsa.fsa_qk_norm_rope(q, q, i32([[0] * 3] * 2), torch.ones(8, device="cuda")),
+           lambda: fsa.fsa_qk_norm_rope(q, q, i32([[0] * 3] * 2), torch.ones(40, device="cuda").double()),
+           lambda: fsa.fsa_qk_norm_rope(q, q, i32([[0] * 3] * 2), torch.ones(6, device="cuda").double()),
+           lambda: fsa.fsa_qk_norm_rope(q, q, i32([[0] * 3] * 2), torch.ones(8, device="cuda").double(), sections=(4, 4)),
+           lambda: fsa.fsa_qk_norm_rope(q, q, i32([[[0] * 2] * 3] * 2), torch.ones(8, device="cuda").double(), sections=(4, 5)),
+           lambda: fsa.fsa_qk_norm_rope(q, q, i32([[[0] * 2] * 3] * 2), torch.ones(8, device="cuda").double()),
+           lambda: fsa.fsa_qk_norm_rope(q, q, None, None, norm=False, q_weight=q[0, 0, 0]),
+           lambda: fsa.fsa_qk_norm_rope(q, q, None, None, q_weight=q[0, 0, 0, :8]),
+           lambda: fsa.fsa_qk_norm_rope(q, q, None, None, q_out=q[:, :1].expand_as(q))]
+    for i, call in enumerate(bad):
+        with pytest.raises(fsa.FsaError):
+            call()
+            pytest.fail(f"call {i} was not refused")
+    for call in (lambda: fsa.fsa_attention_cache(q, cache, None, n), lambda: fsa.fsa_cache_append(cache, k, None, table, n)):
+        with pytest.raises(fsa.FsaError, match="tensor"):
+            call()
+    torch.cuda.synchronize()
 
 
 # ------------------------------------------------------------------------ norm and rotation

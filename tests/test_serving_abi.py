@@ -96,15 +96,17 @@ def test_attention_cache_refuses(lib):
     for kw in CACHE_BAD:
         assert call(cache(**kw)) == (fsa.FSA_ERR_UNSUPPORTED_FMT if "fmt" in kw else fsa.FSA_ERR_INVALID_ARG), kw
     for kw in (dict(q=0), dict(q=72), dict(out=0), dict(out=8), dict(lse=2), dict(block_table=0), dict(lens=0), dict(q_lens=2),
-               dict(workspace=0), dict(workspace=8), dict(status=1), dict(B=0), dict(H=3), dict(H=0), dict(Sq=0),
+               dict(workspace=8), dict(status=1), dict(B=0), dict(H=3), dict(H=0), dict(Sq=0),
                dict(max_pages=0), dict(max_pages=(1 << 26) + 1), dict(causal=2), dict(out_dtype=2),
                dict(scale=float("inf")), dict(scale=float("nan")), dict(q_strides=strides(1024, 512, 4)),
                dict(out_strides=strides(1024, 512, 0)), dict(B=1 << 20, Sq=1 << 10)):
         assert call(**kw) == fsa.FSA_ERR_INVALID_ARG, kw
     assert lib.fsa_attention_cache(None, None) == fsa.FSA_ERR_INVALID_ARG
     n = ctypes.c_size_t()
-    for v in ((0, 4, 2, 1, 128), (1, 3, 2, 1, 128), (1, 4, 2, 0, 128), (1, 4, 2, 1, 32)):
-        assert lib.fsa_attention_cache_workspace(*v, ctypes.byref(n)) == fsa.FSA_ERR_INVALID_ARG
+    for v in ((0, 4, 1, 5), (1, 3, 1, 5), (1, 4, 0, 5), (1, 4, 1, 0), (1, 4, 1, 1 << 30)):
+        assert lib.fsa_attention_cache_workspace(ctypes.byref(cache()), *v, ctypes.byref(n)) == fsa.FSA_ERR_INVALID_ARG
+    assert lib.fsa_attention_cache_workspace(ctypes.byref(cache(fmt=4)), 1, 4, 1, 5, ctypes.byref(n)) == fsa.FSA_ERR_UNSUPPORTED_FMT
+    assert lib.fsa_attention_cache_workspace(ctypes.byref(cache()), 1, 4, 1, 5, None) == fsa.FSA_ERR_INVALID_ARG
 
 
 def test_binding_refuses_host_tensors(lib):
@@ -116,11 +118,3 @@ def test_binding_refuses_host_tensors(lib):
                  lambda: fsa.fsa_cache_read(c, i[None], i, 2), lambda: fsa.fsa_attention_cache(x, c, i[None], i)):
         with pytest.raises(fsa.FsaError, match="CUDA tensor"):
             call()
-
-
-def test_cache_refuses_wrong_pages(lib):
-    n = fsa.fsa_cache_page_bytes(16, 4, 128, "E2M1")
-    for pages in (torch.zeros(3, n + 16, dtype=torch.uint8), torch.zeros(3, n, dtype=torch.int8),
-                  torch.zeros(3 * n, dtype=torch.uint8), torch.zeros(6, n, dtype=torch.uint8)[::2]):
-        with pytest.raises(fsa.FsaError, match="pages"):
-            fsa.MxCache(pages, 16, 4, 128, "E2M1")
