@@ -1,40 +1,60 @@
 // fsa_cache.cu -- writing the paged 4-bit K/V cache and reading it back.
 //
-// Both kernels are bound by memory: append reads 2 bytes and writes 0.53 (E2M1) or
-// 0.56 (NVFP4) bytes an element, read the other way round.  D/8 lanes take one token
-// of one kv head, its K row and its V row; a thread's 8 elements of a row are the ones
-// whose codes are 4 consecutive bytes of the cache's row order (fsa_cache.h), so the
-// codes move as whole words and the bf16 pieces of a warp fill whole 32-byte sectors.
-// The rounding is that of fsa_mx_quantize, bit for bit.
+// Both kernels are bound by memory: append reads 2 bytes and writes 0.53 (E2M1) or 0.56
+// (NVFP4) bytes an element, read the other way round.  A warp takes one group (16 tokens of
+// a kv head: a contiguous piece of a page), so that page and addresses are worked out once
+// for 2 * 16 * D elements.  On the bf16 side a lane holds 8 consecutive elements (16 bytes),
+// D/8 lanes a row; on the cache's side one word of a row.  The two orders (fsa_cache.h)
+// differ, so the code words cross the lanes in between: a K word is two halves of two
+// lanes' words, a V word four bytes of four.  The rounding is that of fsa_mx_quantize.
 #include "fsa_cache.h"
 #include "fsa_mx.cuh"
 
 namespace fsa {
 namespace {
 
-constexpr int CIO_THREADS = 256;
+constexpr int CIO_WARPS = 8;
 
-// The place of a sequence's token in the pool (its group's first byte), or null.  A page
-// number outside the pool sets the status word.
-__device__ __forceinline__ uint8_t* group_of(const CacheIo& a, int b, int64_t at, int h, int group_bytes) {
-  const int64_t pi = at >> a.c.page_shift;
-  if (at < 0 || pi >= a.max_pages) return nullptr;
+// A warp's group: rows r0 <= r < r1 of it are rows r - shift of sequence b's tensor.
+struct Group {
+  uint8_t* at;             // null: no page
+  int b, h, r0, r1;
+  int64_t shift;
+};
+
+// Group gi of the warp's sequence, counted from the one that holds its first position;
+// false if none of its rows is asked for.  `first`, `count`: the positions asked for.
+__device__ __forceinline__ bool find_group(const CacheIo& a, int64_t first, int64_t count, int b, int gi, int h, int group_bytes,
+                                           Group& g) {
+  const int64_t g0 = (first > 0 ? first : 0) / 16 + gi, pos = g0 * 16;
+  const int64_t lo = first - pos, hi = first + count - pos;
+  g.r0 = (int)max((int64_t)0, lo);
+  g.r1 = (int)min((int64_t)16, hi);
+  if (g.r0 >= g.r1) return false;
+  g.b = b;
+  g.h = h;
+  g.shift = lo;
+  g.at = nullptr;
+  const int64_t pi = pos >> a.c.page_shift;
+  if (pi >= a.max_pages) return true;
   const int page = a.table[(int64_t)b * a.max_pages + pi];
   if (page < 0 || page >= a.c.num_pages) {
-    if (a.status) atomicExch(a.status, -1);       // FSA_ERR_INVALID_ARG
-    return nullptr;
+    if (a.status && (threadIdx.x & 31) == 0) atomicExch(a.status, -1);       // FSA_ERR_INVALID_ARG
+    return true;
   }
-  const int inside = (int)(at & ((1 << a.c.page_shift) - 1));
-  const int64_t groups = 1 << (a.c.page_shift - 4);
-  return a.c.pages + page * a.c.page_bytes + (h * groups + inside / 16) * group_bytes;
+  const int inside = (int)(pos & ((1 << a.c.page_shift) - 1)) / 16;
+  g.at = a.c.pages + page * a.c.page_bytes + (((int64_t)h << (a.c.page_shift - 4)) + inside) * group_bytes;
+  return true;
 }
 
-// max over the lanes that differ in the given lane bits
-template <int FROM, int TO>
-__device__ __forceinline__ float lanes_max(float x, uint32_t mask) {
-#pragma unroll
-  for (int m = FROM; m < TO; m *= 2) x = fmaxf(x, __shfl_xor_sync(mask, x, m));
-  return x;
+// Which of the launch's groups this warp has: groups of a sequence, then heads, fastest last.
+__device__ __forceinline__ bool my_item(const CacheIo& a, int groups, int& b, int& gi, int& h) {
+  const uint32_t item = blockIdx.x * CIO_WARPS + threadIdx.x / 32;
+  const uint32_t rest = item / (uint32_t)a.c.Hkv;
+  h = (int)(item - rest * a.c.Hkv);
+  b = (int)(rest / (uint32_t)groups);
+  gi = (int)(rest - (uint32_t)b * groups);
+  return b < a.B;
 }
 
 // NaN-keeping magnitude: NaN and Inf become Inf, so that fmaxf passes them on
@@ -43,106 +63,141 @@ __device__ __forceinline__ float magnitude(float x) {
   return a <= 3.4e38f ? a : __uint_as_float(0x7F800000u);
 }
 
-// The scale byte of a block and the code byte of a pair of its elements.
+// 8 consecutive elements of a row, D/8 lanes a row: their codes, element 0 in the lowest
+// nibble, and their block's scale byte.
 template <int CF>
-__device__ __forceinline__ uint32_t scale_byte(float amax) {
-  if constexpr (CF == CF_MX) return block_scale_byte(amax, 2);
-  else return nvfp4_scale_byte(amax, amax > 3.4e38f);
-}
-template <int CF>
-__device__ __forceinline__ uint32_t code_byte(float lo, float hi, uint32_t sb) {
-  if constexpr (CF == CF_MX) {
-    const float mul = pow2_neg((int)sb - 127);
-    return sb == 0xFFu ? 0u : cvt_e2m1x2(__fmul_rn(lo, mul), __fmul_rn(hi, mul));
-  } else {
-    const float s = e4m3_to_f32(sb);
-    return s > 0.0f ? cvt_e2m1x2(__fdiv_rn(lo, s), __fdiv_rn(hi, s)) : 0u;
+__device__ __forceinline__ uint32_t quantise8(uint4 u, uint32_t& sb) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  float x[8], m = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    x[2 * e] = __uint_as_float(w[e] << 16);
+    x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+    m = fmaxf(m, fmaxf(magnitude(x[2 * e]), magnitude(x[2 * e + 1])));
   }
+  m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));              // 16 elements
+  float mul;
+  if constexpr (CF == CF_MX) {
+    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));            // 32
+    sb = block_scale_byte(m, 2);
+    mul = pow2_neg((int)sb - 127);
+    if (sb == 0xFFu) return 0u;
+  } else {
+    sb = nvfp4_scale_byte(m, m > 3.4e38f);
+    const float s = e4m3_to_f32(sb);
+    if (!(s > 0.0f)) return 0u;                                  // zero or NaN
+    // The code nearest x / s, ties to even.  x has 8 significant bits and s has 4, so x / s
+    // either is a tie (0.25, 0.75, .. 5) or is at least 2^-10 of it away from it.  The
+    // product with a reciprocal raised by 2^-20 lies above x / s by 2^-21 to 2^-19 of it;
+    // cut to 12 fraction bits, a tie is that tie and the others stay on their side.
+    mul = __frcp_rn(s) * (1.0f + 0x1p-20f);
+  }
+  uint32_t codes = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float lo = __fmul_rn(x[2 * e], mul), hi = __fmul_rn(x[2 * e + 1], mul);
+    if constexpr (CF == CF_NV) {
+      lo = __uint_as_float(__float_as_uint(lo) & 0xFFFFF800u);
+      hi = __uint_as_float(__float_as_uint(hi) & 0xFFFFF800u);
+    }
+    codes |= cvt_e2m1x2(lo, hi) << (8 * e);
+  }
+  return codes;
+}
+
+// The exchanges between the two orders of a row's codes.  lane = l of a row of L = D/8 lanes
+// (`row`: its first lane); plain word l: elements 8l .. 8l + 7; cache word l: bytes 4l .. 4l + 3.
+// K cache word l = t*(L/4) + w has elements 16s + 4t .. + 3 of s = 2w, 2w + 1: half t%2 of plain
+// words 2s + t/2.  V cache word l = g*(L/8) + i has elements 16s + 2g, + 1 of s = 4i .. 4i + 3: byte
+// g%4 of plain words 2s + g/4.
+template <int L>
+__device__ __forceinline__ uint32_t k_to_cache(uint32_t plain, int row, int l) {
+  const int t = l / (L / 4), w = l % (L / 4);
+  const uint32_t a = __shfl_sync(0xFFFFFFFFu, plain, row + 4 * w + t / 2);
+  const uint32_t b = __shfl_sync(0xFFFFFFFFu, plain, row + 4 * w + 2 + t / 2);
+  return __byte_perm(a, b, t & 1 ? 0x7632 : 0x5410);
+}
+template <int L>
+__device__ __forceinline__ uint32_t k_from_cache(uint32_t cache, int row, int l) {
+  const int s = l / 2, t = 2 * (l & 1);
+  const uint32_t a = __shfl_sync(0xFFFFFFFFu, cache, row + t * (L / 4) + s / 2);
+  const uint32_t b = __shfl_sync(0xFFFFFFFFu, cache, row + (t + 1) * (L / 4) + s / 2);
+  return __byte_perm(a, b, s & 1 ? 0x7632 : 0x5410);
+}
+template <int L>
+__device__ __forceinline__ uint32_t v_to_cache(uint32_t plain, int row, int l) {
+  const int g = l / (L / 8), i = l % (L / 8);
+  uint32_t w[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x) w[x] = __shfl_sync(0xFFFFFFFFu, plain, row + 8 * i + 2 * x + g / 4);
+  const uint32_t pick = (g & 3) * 0x11 + 0x40;                   // byte g%4 of the first, then of the second
+  return __byte_perm(__byte_perm(w[0], w[1], pick), __byte_perm(w[2], w[3], pick), 0x5410);
+}
+template <int L>
+__device__ __forceinline__ uint32_t v_from_cache(uint32_t cache, int row, int l) {
+  const int s = l / 2, g = 4 * (l & 1);
+  uint32_t w[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x) w[x] = __shfl_sync(0xFFFFFFFFu, cache, row + (g + x) * (L / 8) + s / 4);
+  const uint32_t pick = (s & 3) * 0x11 + 0x40;
+  return __byte_perm(__byte_perm(w[0], w[1], pick), __byte_perm(w[2], w[3], pick), 0x5410);
 }
 
 template <int D, int CF>
-__global__ void __launch_bounds__(CIO_THREADS) cache_append_kernel(const CacheIo a) {
+__global__ void __launch_bounds__(CIO_WARPS * 32) cache_append_kernel(const CacheIo a, int groups) {
   using Gr = CacheGroup<D, CF>;
-  constexpr int L = D / 8, C = D / 32;            // lanes of a row; 4-byte words of a K chunk (of a t)
-  const int lane = threadIdx.x % L;
-  const uint32_t mask = (uint32_t)((1ull << L) - 1) << (threadIdx.x % 32 / L * L);
-  const int64_t row = ((int64_t)blockIdx.x * CIO_THREADS + threadIdx.x) / L;
-  const int64_t rows = (int64_t)a.B * a.S * a.c.Hkv;
-  if (row >= rows) return;
-  const int h = (int)(row % a.c.Hkv);
-  const int64_t tokn = row / a.c.Hkv;
-  const int b = (int)(tokn / a.S), s = (int)(tokn % a.S);
+  constexpr int L = D / 8, ROWS = 32 / L, BATCH = 16 / ROWS < 4 ? 16 / ROWS : 4;   // rows at a time, times in a batch
+  constexpr int PER = CF == CF_MX ? 4 : 2;                       // lanes of a block
+  int b, gi, h;
+  if (!my_item(a, groups, b, gi, h)) return;
   const int fresh = a.which ? min(max(a.which[b], 0), a.S) : a.S;
-  if (s >= fresh) return;
-  const int64_t at = (int64_t)a.lens[b] - fresh + s;
-  uint8_t* const grp = group_of(a, b, at, h, Gr::BYTES);
-  if (!grp) return;
-  const int r = (int)(at & 15);
-  const uint16_t* ksrc = a.k + b * a.ks.b + s * a.ks.s + h * a.ks.h;
-  const uint16_t* vsrc = a.v + b * a.vs.b + s * a.vs.s + h * a.vs.h;
-
-  // K: lane = t*C + sp holds elements 16s' + 4t .. + 3 of the steps s' = 2sp, 2sp + 1
-  const int t = lane / C, sp = lane % C;
-  uint2 ku[2];
+  // positions below 0 are dropped: the first of them is 0 then, and row 0 is `skip`
+  const int64_t first = (int64_t)a.lens[b] - fresh, skip = first < 0 ? -first : 0;
+  Group g;
+  if (!find_group(a, first + skip, fresh - skip, b, gi, h, Gr::BYTES, g) || !g.at) return;
+  const int lane = threadIdx.x & 31, l = lane % L, row = lane - l;
+  const uint16_t* const ksrc = a.k + b * a.ks.b + h * a.ks.h + (skip - g.shift) * a.ks.s + 8 * l;
+  const uint16_t* const vsrc = a.v + b * a.vs.b + h * a.vs.h + (skip - g.shift) * a.vs.s + 8 * l;
+#pragma unroll 1
+  for (int base = 0; base < 16; base += ROWS * BATCH) {
+    if (base >= g.r1 || base + ROWS * BATCH <= g.r0) continue;
+    uint4 ku[BATCH], vu[BATCH];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) ku[i] = *reinterpret_cast<const uint2*>(ksrc + 16 * (2 * sp + i) + 4 * t);
-  // V: lane = g*(L/8) + ih holds elements 16i + 2g, + 1 of i = 4ih .. 4ih + 3
-  constexpr int IH = L / 8;
-  const int g = lane / IH, ih = lane % IH;
-  uint32_t vu[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) vu[i] = *reinterpret_cast<const uint32_t*>(vsrc + 16 * (4 * ih + i) + 2 * g);
-
-  {
-    float x[8], m[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      x[4 * i] = bf16_to_f32(ku[i].x & 0xFFFF); x[4 * i + 1] = bf16_to_f32(ku[i].x >> 16);
-      x[4 * i + 2] = bf16_to_f32(ku[i].y & 0xFFFF); x[4 * i + 3] = bf16_to_f32(ku[i].y >> 16);
-      m[i] = fmaxf(fmaxf(magnitude(x[4 * i]), magnitude(x[4 * i + 1])), fmaxf(magnitude(x[4 * i + 2]), magnitude(x[4 * i + 3])));
+    for (int x = 0; x < BATCH; ++x) {
+      const int r = base + x * ROWS + lane / L;
+      const bool in = r >= g.r0 && r < g.r1;
+      ku[x] = in ? *reinterpret_cast<const uint4*>(ksrc + r * a.ks.s) : make_uint4(0u, 0u, 0u, 0u);
+      vu[x] = in ? *reinterpret_cast<const uint4*>(vsrc + r * a.vs.s) : make_uint4(0u, 0u, 0u, 0u);
     }
-    if (CF == CF_MX) m[0] = m[1] = fmaxf(m[0], m[1]);           // both steps lie in one block of 32
-    uint32_t sb[2], w = 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      m[i] = (CF == CF_MX && i == 1) ? m[0] : lanes_max<C, L>(m[i], mask);   // over the t
-      sb[i] = scale_byte<CF>(m[i]);
-      w |= (code_byte<CF>(x[4 * i], x[4 * i + 1], sb[i]) | code_byte<CF>(x[4 * i + 2], x[4 * i + 3], sb[i]) << 8) << (16 * i);
-    }
-    *reinterpret_cast<uint32_t*>(grp + Gr::K + r * (D / 2) + 4 * lane) = w;
-    if (t == 0) {
-      if (CF == CF_MX) grp[Gr::KS + r * Gr::SB + sp] = (uint8_t)sb[0];
-      else *reinterpret_cast<uint16_t*>(grp + Gr::KS + r * Gr::SB + 2 * sp) = (uint16_t)(sb[0] | sb[1] << 8);
-    }
-  }
-  {
-    float x[8], m[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = bf16_to_f32(vu[i] & 0xFFFF); x[2 * i + 1] = bf16_to_f32(vu[i] >> 16);
-      m[i] = fmaxf(magnitude(x[2 * i]), magnitude(x[2 * i + 1]));
-    }
-    if (CF == CF_MX) { m[0] = m[1] = fmaxf(m[0], m[1]); m[2] = m[3] = fmaxf(m[2], m[3]); }
-    uint32_t sb[4], w = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      m[i] = (CF == CF_MX && (i & 1)) ? m[i - 1] : lanes_max<IH, L>(m[i], mask);   // over the g
-      sb[i] = scale_byte<CF>(m[i]);
-      w |= code_byte<CF>(x[2 * i], x[2 * i + 1], sb[i]) << (8 * i);
-    }
-    *reinterpret_cast<uint32_t*>(grp + Gr::V + r * (D / 2) + 4 * lane) = w;
-    if (g == 0) {
-      if (CF == CF_MX) *reinterpret_cast<uint16_t*>(grp + Gr::VS + r * Gr::SB + 2 * ih) = (uint16_t)(sb[0] | sb[2] << 8);
-      else *reinterpret_cast<uint32_t*>(grp + Gr::VS + r * Gr::SB + 4 * ih) = sb[0] | sb[1] << 8 | sb[2] << 16 | sb[3] << 24;
+    for (int x = 0; x < BATCH; ++x) {
+      const int r = base + x * ROWS + lane / L;
+      uint32_t ksb, vsb;
+      const uint32_t kw = k_to_cache<L>(quantise8<CF>(ku[x], ksb), row, l);
+      const uint32_t vw = v_to_cache<L>(quantise8<CF>(vu[x], vsb), row, l);
+      if (r >= g.r0 && r < g.r1) {
+        *reinterpret_cast<uint32_t*>(g.at + Gr::K + r * (D / 2) + 4 * l) = kw;
+        *reinterpret_cast<uint32_t*>(g.at + Gr::V + r * (D / 2) + 4 * l) = vw;
+        if (l % PER == 0) {
+          g.at[Gr::KS + r * Gr::SB + l / PER] = (uint8_t)ksb;
+          g.at[Gr::VS + r * Gr::SB + l / PER] = (uint8_t)vsb;
+        }
+      }
     }
   }
 }
 
-// value pair (bf16x2) of a code byte under a scale: exact, at most 6 significant bits
-__device__ __forceinline__ uint32_t value_pair(uint32_t h2, float s) {
-  float lo, hi;
-  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}" : "=f"(lo), "=f"(hi) : "r"(h2));
-  return cvt_bf16x2(__fmul_rn(lo, s), __fmul_rn(hi, s));
+// The 8 values of a plain word under a scale, as bf16: exact, at most 6 significant bits
+__device__ __forceinline__ uint4 values8(uint32_t codes, float s) {
+  uint32_t h[4], v[4];
+  cvt_e2m1x8_f16(codes, h);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float lo, hi;
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}" : "=f"(lo), "=f"(hi) : "r"(h[e]));
+    v[e] = cvt_bf16x2(__fmul_rn(lo, s), __fmul_rn(hi, s));
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
 }
 template <int CF>
 __device__ __forceinline__ float scale_value(uint32_t sb) {
@@ -151,86 +206,74 @@ __device__ __forceinline__ float scale_value(uint32_t sb) {
 }
 
 template <int D, int CF>
-__global__ void __launch_bounds__(CIO_THREADS) cache_read_kernel(const CacheIo a) {
+__global__ void __launch_bounds__(CIO_WARPS * 32) cache_read_kernel(const CacheIo a, int groups) {
   using Gr = CacheGroup<D, CF>;
-  constexpr int L = D / 8, C = D / 32, IH = L / 8;
-  const int lane = threadIdx.x % L;
-  const int64_t row = ((int64_t)blockIdx.x * CIO_THREADS + threadIdx.x) / L;
-  const int64_t rows = (int64_t)a.B * a.S * a.c.Hkv;
-  if (row >= rows) return;
-  const int h = (int)(row % a.c.Hkv);
-  const int64_t tokn = row / a.c.Hkv;
-  const int b = (int)(tokn / a.S), s = (int)(tokn % a.S);
-  const int64_t at = (int64_t)(a.which ? a.which[b] : 0) + s;
-  if (at < 0 || at >= a.lens[b]) return;
-  const uint8_t* const grp = group_of(a, b, at, h, Gr::BYTES);
-  const int r = (int)(at & 15);
-  if (a.k) {
-    const int t = lane / C, sp = lane % C;
-    uint32_t w = 0, h2[4];
-    float sc[2] = {0.f, 0.f};
-    if (grp) {
-      w = *reinterpret_cast<const uint32_t*>(grp + Gr::K + r * (D / 2) + 4 * lane);
-      if (CF == CF_MX) sc[0] = sc[1] = scale_value<CF>(grp[Gr::KS + r * Gr::SB + sp]);
-      else {
-        const uint32_t u = *reinterpret_cast<const uint16_t*>(grp + Gr::KS + r * Gr::SB + 2 * sp);
-        sc[0] = scale_value<CF>(u & 0xFF); sc[1] = scale_value<CF>(u >> 8);
+  constexpr int L = D / 8, ROWS = 32 / L, BATCH = 16 / ROWS < 4 ? 16 / ROWS : 4;
+  constexpr int PER = CF == CF_MX ? 4 : 2;
+  int b, gi, h;
+  if (!my_item(a, groups, b, gi, h)) return;
+  const int64_t start = a.which ? a.which[b] : 0, skip = start < 0 ? -start : 0;
+  Group g;
+  if (!find_group(a, start + skip, min((int64_t)a.S, (int64_t)a.lens[b] - start) - skip, b, gi, h, Gr::BYTES, g)) return;
+  const int lane = threadIdx.x & 31, l = lane % L, row = lane - l;
+#pragma unroll 1
+  for (int base = 0; base < 16; base += ROWS * BATCH) {
+    if (base >= g.r1 || base + ROWS * BATCH <= g.r0) continue;
+    uint32_t kw[BATCH], vw[BATCH], ks[BATCH], vs[BATCH];
+#pragma unroll
+    for (int x = 0; x < BATCH; ++x) {
+      const int r = base + x * ROWS + lane / L;
+      kw[x] = vw[x] = ks[x] = vs[x] = 0;
+      if (g.at) {
+        kw[x] = *reinterpret_cast<const uint32_t*>(g.at + Gr::K + r * (D / 2) + 4 * l);
+        vw[x] = *reinterpret_cast<const uint32_t*>(g.at + Gr::V + r * (D / 2) + 4 * l);
+        ks[x] = g.at[Gr::KS + r * Gr::SB + l / PER];
+        vs[x] = g.at[Gr::VS + r * Gr::SB + l / PER];
       }
     }
-    cvt_e2m1x8_f16(w, h2);
-    uint16_t* dst = a.k + b * a.ks.b + s * a.ks.s + h * a.ks.h;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      *reinterpret_cast<uint2*>(dst + 16 * (2 * sp + i) + 4 * t) = make_uint2(value_pair(h2[2 * i], sc[i]), value_pair(h2[2 * i + 1], sc[i]));
-  }
-  if (a.v) {
-    const int g = lane / IH, ih = lane % IH;
-    uint32_t w = 0, h2[4];
-    float sc[4] = {0.f, 0.f, 0.f, 0.f};
-    if (grp) {
-      w = *reinterpret_cast<const uint32_t*>(grp + Gr::V + r * (D / 2) + 4 * lane);
-      if (CF == CF_MX) {
-        const uint32_t u = *reinterpret_cast<const uint16_t*>(grp + Gr::VS + r * Gr::SB + 2 * ih);
-        sc[0] = sc[1] = scale_value<CF>(u & 0xFF); sc[2] = sc[3] = scale_value<CF>(u >> 8);
-      } else {
-        const uint32_t u = *reinterpret_cast<const uint32_t*>(grp + Gr::VS + r * Gr::SB + 4 * ih);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sc[i] = scale_value<CF>((u >> (8 * i)) & 0xFF);
-      }
+    for (int x = 0; x < BATCH; ++x) {
+      const int r = base + x * ROWS + lane / L;
+      const int64_t s = skip + r - g.shift;
+      const bool in = r >= g.r0 && r < g.r1;
+      const uint4 k = values8(k_from_cache<L>(kw[x], row, l), scale_value<CF>(ks[x]));
+      const uint4 v = values8(v_from_cache<L>(vw[x], row, l), scale_value<CF>(vs[x]));
+      if (in && a.k) *reinterpret_cast<uint4*>(a.k + b * a.ks.b + s * a.ks.s + h * a.ks.h + 8 * l) = k;
+      if (in && a.v) *reinterpret_cast<uint4*>(a.v + b * a.vs.b + s * a.vs.s + h * a.vs.h + 8 * l) = v;
     }
-    cvt_e2m1x8_f16(w, h2);
-    uint16_t* dst = a.v + b * a.vs.b + s * a.vs.s + h * a.vs.h;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t*>(dst + 16 * (4 * ih + i) + 2 * g) = value_pair(h2[i], sc[i]);
   }
 }
 
-int64_t blocks_of(const CacheIo& a) {
-  return ((int64_t)a.B * a.S * a.c.Hkv * (a.c.D / 8) + CIO_THREADS - 1) / CIO_THREADS;
+// groups that S consecutive tokens can touch
+int groups_of(const CacheIo& a) { return (a.S + 14) / 16 + 1; }
+unsigned blocks_of(const CacheIo& a) {
+  return (unsigned)(((int64_t)a.B * groups_of(a) * a.c.Hkv + CIO_WARPS - 1) / CIO_WARPS);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_append(const CacheIo& a, cudaStream_t st) {
-  const unsigned grid = (unsigned)blocks_of(a);
+  const unsigned grid = blocks_of(a);
+  const int groups = groups_of(a);
   if (a.c.D == 128) {
-    if (a.c.cf == CF_MX) cache_append_kernel<128, CF_MX><<<grid, CIO_THREADS, 0, st>>>(a);
-    else cache_append_kernel<128, CF_NV><<<grid, CIO_THREADS, 0, st>>>(a);
+    if (a.c.cf == CF_MX) cache_append_kernel<128, CF_MX><<<grid, CIO_WARPS * 32, 0, st>>>(a, groups);
+    else cache_append_kernel<128, CF_NV><<<grid, CIO_WARPS * 32, 0, st>>>(a, groups);
   } else {
-    if (a.c.cf == CF_MX) cache_append_kernel<64, CF_MX><<<grid, CIO_THREADS, 0, st>>>(a);
-    else cache_append_kernel<64, CF_NV><<<grid, CIO_THREADS, 0, st>>>(a);
+    if (a.c.cf == CF_MX) cache_append_kernel<64, CF_MX><<<grid, CIO_WARPS * 32, 0, st>>>(a, groups);
+    else cache_append_kernel<64, CF_NV><<<grid, CIO_WARPS * 32, 0, st>>>(a, groups);
   }
   return cudaGetLastError();
 }
 
 cudaError_t launch_cache_read(const CacheIo& a, cudaStream_t st) {
-  const unsigned grid = (unsigned)blocks_of(a);
+  const unsigned grid = blocks_of(a);
+  const int groups = groups_of(a);
   if (a.c.D == 128) {
-    if (a.c.cf == CF_MX) cache_read_kernel<128, CF_MX><<<grid, CIO_THREADS, 0, st>>>(a);
-    else cache_read_kernel<128, CF_NV><<<grid, CIO_THREADS, 0, st>>>(a);
+    if (a.c.cf == CF_MX) cache_read_kernel<128, CF_MX><<<grid, CIO_WARPS * 32, 0, st>>>(a, groups);
+    else cache_read_kernel<128, CF_NV><<<grid, CIO_WARPS * 32, 0, st>>>(a, groups);
   } else {
-    if (a.c.cf == CF_MX) cache_read_kernel<64, CF_MX><<<grid, CIO_THREADS, 0, st>>>(a);
-    else cache_read_kernel<64, CF_NV><<<grid, CIO_THREADS, 0, st>>>(a);
+    if (a.c.cf == CF_MX) cache_read_kernel<64, CF_MX><<<grid, CIO_WARPS * 32, 0, st>>>(a, groups);
+    else cache_read_kernel<64, CF_NV><<<grid, CIO_WARPS * 32, 0, st>>>(a, groups);
   }
   return cudaGetLastError();
 }
