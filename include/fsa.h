@@ -454,7 +454,7 @@ int fsa_cache_page_bytes(int page_size, int Hkv, int D, int fmt, size_t* bytes);
  * not followed: its tokens are dropped, and *status (device int32, optional) becomes
  * FSA_ERR_INVALID_ARG.  Two tokens of one call must not share a place (two sequences whose
  * tables name one page for their new tokens); what such a place then holds is unspecified.
- * max_pages * page_size <= 2^30, B * (S/16 + 2) * Hkv < 2^31.  One launch, nothing allocated: may be captured.  Errors:
+ * max_pages * page_size <= 2^30, B * (S/8 + 2) * Hkv < 2^31.  One launch, nothing allocated: may be captured.  Errors:
  * FSA_ERR_INVALID_ARG, FSA_ERR_UNSUPPORTED_FMT (fmt), FSA_ERR_LAUNCH. */
 int fsa_cache_append(const fsa_cache* cache, const void* k, const void* v, const fsa_strides* k_strides,
                      const fsa_strides* v_strides, int B, int S, const int32_t* block_table, int max_pages,

@@ -1,9 +1,9 @@
 // fsa_cache.cu -- writing the paged 4-bit K/V cache and reading it back.
 //
 // Both kernels are bound by memory: append reads 2 bytes and writes 0.53 (E2M1) or 0.56
-// (NVFP4) bytes an element, read the other way round.  A warp takes one group (16 tokens of
-// a kv head: a contiguous piece of a page), so that page and addresses are worked out once
-// for 2 * 16 * D elements.  On the bf16 side a lane holds 8 consecutive elements (16 bytes),
+// (NVFP4) bytes an element, read the other way round.  A warp takes a run of UNIT tokens of
+// a kv head within a group (a contiguous piece of a page), so that page and addresses are
+// worked out once for 2 * 1024 elements, all of whose loads go out together.  On the bf16 side a lane holds 8 consecutive elements (16 bytes),
 // D/8 lanes a row; on the cache's side one word of a row.  The two orders (fsa_cache.h)
 // differ, so the code words cross the lanes in between: a K word is two halves of two
 // lanes' words, a V word four bytes of four.  The rounding is that of fsa_mx_quantize.
@@ -14,22 +14,26 @@ namespace fsa {
 namespace {
 
 constexpr int CIO_WARPS = 8;
+template <int D>
+constexpr int UNIT = 1024 / D;     // tokens of a warp: 8 or 16
 
-// A warp's group: rows r0 <= r < r1 of it are rows r - shift of sequence b's tensor.
+// A warp's rows r0 <= r < r1 of a group: rows r - shift of sequence b's tensor.
 struct Group {
   uint8_t* at;             // null: no page
   int b, h, r0, r1;
   int64_t shift;
 };
 
-// Group gi of the warp's sequence, counted from the one that holds its first position;
-// false if none of its rows is asked for.  `first`, `count`: the positions asked for.
-__device__ __forceinline__ bool find_group(const CacheIo& a, int64_t first, int64_t count, int b, int gi, int h, int group_bytes,
+// Unit ui of the sequence, counted from the one that holds its first position; false if none
+// of its rows is asked for.  `first`, `count`: the positions asked for.
+template <int U>
+__device__ __forceinline__ bool find_group(const CacheIo& a, int64_t first, int64_t count, int b, int ui, int h, int group_bytes,
                                            Group& g) {
-  const int64_t g0 = (first > 0 ? first : 0) / 16 + gi, pos = g0 * 16;
+  const int64_t at = ((first > 0 ? first : 0) / U + ui) * U, pos = at & ~15ll;      // the unit's first position, its group's
+  const int u0 = (int)(at - pos);
   const int64_t lo = first - pos, hi = first + count - pos;
-  g.r0 = (int)max((int64_t)0, lo);
-  g.r1 = (int)min((int64_t)16, hi);
+  g.r0 = (int)max((int64_t)u0, lo);
+  g.r1 = (int)min((int64_t)(u0 + U), hi);
   if (g.r0 >= g.r1) return false;
   g.b = b;
   g.h = h;
@@ -47,13 +51,13 @@ __device__ __forceinline__ bool find_group(const CacheIo& a, int64_t first, int6
   return true;
 }
 
-// Which of the launch's groups this warp has: groups of a sequence, then heads, fastest last.
-__device__ __forceinline__ bool my_item(const CacheIo& a, int groups, int& b, int& gi, int& h) {
+// Which of the launch's units this warp has: units of a sequence, then heads, fastest last.
+__device__ __forceinline__ bool my_item(const CacheIo& a, int units, int& b, int& ui, int& h) {
   const uint32_t item = blockIdx.x * CIO_WARPS + threadIdx.x / 32;
   const uint32_t rest = item / (uint32_t)a.c.Hkv;
   h = (int)(item - rest * a.c.Hkv);
-  b = (int)(rest / (uint32_t)groups);
-  gi = (int)(rest - (uint32_t)b * groups);
+  b = (int)(rest / (uint32_t)units);
+  ui = (int)(rest - (uint32_t)b * units);
   return b < a.B;
 }
 
@@ -144,44 +148,41 @@ __device__ __forceinline__ uint32_t v_from_cache(uint32_t cache, int row, int l)
 }
 
 template <int D, int CF>
-__global__ void __launch_bounds__(CIO_WARPS * 32) cache_append_kernel(const CacheIo a, int groups) {
+__global__ void __launch_bounds__(CIO_WARPS * 32) cache_append_kernel(const CacheIo a, int units) {
   using Gr = CacheGroup<D, CF>;
-  constexpr int L = D / 8, ROWS = 32 / L, BATCH = 16 / ROWS < 4 ? 16 / ROWS : 4;   // rows at a time, times in a batch
+  constexpr int L = D / 8, ROWS = 32 / L, BATCH = UNIT<D> / ROWS;      // rows at a time, times
   constexpr int PER = CF == CF_MX ? 4 : 2;                       // lanes of a block
-  int b, gi, h;
-  if (!my_item(a, groups, b, gi, h)) return;
+  int b, ui, h;
+  if (!my_item(a, units, b, ui, h)) return;
   const int fresh = a.which ? min(max(a.which[b], 0), a.S) : a.S;
   // positions below 0 are dropped: the first of them is 0 then, and row 0 is `skip`
   const int64_t first = (int64_t)a.lens[b] - fresh, skip = first < 0 ? -first : 0;
   Group g;
-  if (!find_group(a, first + skip, fresh - skip, b, gi, h, Gr::BYTES, g) || !g.at) return;
+  if (!find_group<UNIT<D>>(a, first + skip, fresh - skip, b, ui, h, Gr::BYTES, g) || !g.at) return;
   const int lane = threadIdx.x & 31, l = lane % L, row = lane - l;
   const uint16_t* const ksrc = a.k + b * a.ks.b + h * a.ks.h + (skip - g.shift) * a.ks.s + 8 * l;
   const uint16_t* const vsrc = a.v + b * a.vs.b + h * a.vs.h + (skip - g.shift) * a.vs.s + 8 * l;
-#pragma unroll 1
-  for (int base = 0; base < 16; base += ROWS * BATCH) {
-    if (base >= g.r1 || base + ROWS * BATCH <= g.r0) continue;
-    uint4 ku[BATCH], vu[BATCH];
+  const int base = g.r0 / UNIT<D> * UNIT<D>;
+  uint4 ku[BATCH], vu[BATCH];
 #pragma unroll
-    for (int x = 0; x < BATCH; ++x) {
-      const int r = base + x * ROWS + lane / L;
-      const bool in = r >= g.r0 && r < g.r1;
-      ku[x] = in ? *reinterpret_cast<const uint4*>(ksrc + r * a.ks.s) : make_uint4(0u, 0u, 0u, 0u);
-      vu[x] = in ? *reinterpret_cast<const uint4*>(vsrc + r * a.vs.s) : make_uint4(0u, 0u, 0u, 0u);
-    }
+  for (int x = 0; x < BATCH; ++x) {
+    const int r = base + x * ROWS + lane / L;
+    const bool in = r >= g.r0 && r < g.r1;
+    ku[x] = in ? *reinterpret_cast<const uint4*>(ksrc + r * a.ks.s) : make_uint4(0u, 0u, 0u, 0u);
+    vu[x] = in ? *reinterpret_cast<const uint4*>(vsrc + r * a.vs.s) : make_uint4(0u, 0u, 0u, 0u);
+  }
 #pragma unroll
-    for (int x = 0; x < BATCH; ++x) {
-      const int r = base + x * ROWS + lane / L;
-      uint32_t ksb, vsb;
-      const uint32_t kw = k_to_cache<L>(quantise8<CF>(ku[x], ksb), row, l);
-      const uint32_t vw = v_to_cache<L>(quantise8<CF>(vu[x], vsb), row, l);
-      if (r >= g.r0 && r < g.r1) {
-        *reinterpret_cast<uint32_t*>(g.at + Gr::K + r * (D / 2) + 4 * l) = kw;
-        *reinterpret_cast<uint32_t*>(g.at + Gr::V + r * (D / 2) + 4 * l) = vw;
-        if (l % PER == 0) {
-          g.at[Gr::KS + r * Gr::SB + l / PER] = (uint8_t)ksb;
-          g.at[Gr::VS + r * Gr::SB + l / PER] = (uint8_t)vsb;
-        }
+  for (int x = 0; x < BATCH; ++x) {
+    const int r = base + x * ROWS + lane / L;
+    uint32_t ksb, vsb;
+    const uint32_t kw = k_to_cache<L>(quantise8<CF>(ku[x], ksb), row, l);
+    const uint32_t vw = v_to_cache<L>(quantise8<CF>(vu[x], vsb), row, l);
+    if (r >= g.r0 && r < g.r1) {
+      *reinterpret_cast<uint32_t*>(g.at + Gr::K + r * (D / 2) + 4 * l) = kw;
+      *reinterpret_cast<uint32_t*>(g.at + Gr::V + r * (D / 2) + 4 * l) = vw;
+      if (l % PER == 0) {
+        g.at[Gr::KS + r * Gr::SB + l / PER] = (uint8_t)ksb;
+        g.at[Gr::VS + r * Gr::SB + l / PER] = (uint8_t)vsb;
       }
     }
   }
@@ -206,74 +207,74 @@ __device__ __forceinline__ float scale_value(uint32_t sb) {
 }
 
 template <int D, int CF>
-__global__ void __launch_bounds__(CIO_WARPS * 32) cache_read_kernel(const CacheIo a, int groups) {
+__global__ void __launch_bounds__(CIO_WARPS * 32) cache_read_kernel(const CacheIo a, int units) {
   using Gr = CacheGroup<D, CF>;
-  constexpr int L = D / 8, ROWS = 32 / L, BATCH = 16 / ROWS < 4 ? 16 / ROWS : 4;
+  constexpr int L = D / 8, ROWS = 32 / L, BATCH = UNIT<D> / ROWS;
   constexpr int PER = CF == CF_MX ? 4 : 2;
-  int b, gi, h;
-  if (!my_item(a, groups, b, gi, h)) return;
+  int b, ui, h;
+  if (!my_item(a, units, b, ui, h)) return;
   const int64_t start = a.which ? a.which[b] : 0, skip = start < 0 ? -start : 0;
   Group g;
-  if (!find_group(a, start + skip, min((int64_t)a.S, (int64_t)a.lens[b] - start) - skip, b, gi, h, Gr::BYTES, g)) return;
+  if (!find_group<UNIT<D>>(a, start + skip, min((int64_t)a.S, (int64_t)a.lens[b] - start) - skip, b, ui, h, Gr::BYTES, g)) return;
   const int lane = threadIdx.x & 31, l = lane % L, row = lane - l;
-#pragma unroll 1
-  for (int base = 0; base < 16; base += ROWS * BATCH) {
-    if (base >= g.r1 || base + ROWS * BATCH <= g.r0) continue;
-    uint32_t kw[BATCH], vw[BATCH], ks[BATCH], vs[BATCH];
+  const int base = g.r0 / UNIT<D> * UNIT<D>;
+  uint32_t kw[BATCH], vw[BATCH], ks[BATCH], vs[BATCH];
 #pragma unroll
-    for (int x = 0; x < BATCH; ++x) {
-      const int r = base + x * ROWS + lane / L;
-      kw[x] = vw[x] = ks[x] = vs[x] = 0;
-      if (g.at) {
-        kw[x] = *reinterpret_cast<const uint32_t*>(g.at + Gr::K + r * (D / 2) + 4 * l);
-        vw[x] = *reinterpret_cast<const uint32_t*>(g.at + Gr::V + r * (D / 2) + 4 * l);
-        ks[x] = g.at[Gr::KS + r * Gr::SB + l / PER];
-        vs[x] = g.at[Gr::VS + r * Gr::SB + l / PER];
-      }
+  for (int x = 0; x < BATCH; ++x) {
+    const int r = base + x * ROWS + lane / L;
+    kw[x] = vw[x] = ks[x] = vs[x] = 0;
+    if (g.at) {
+      kw[x] = *reinterpret_cast<const uint32_t*>(g.at + Gr::K + r * (D / 2) + 4 * l);
+      vw[x] = *reinterpret_cast<const uint32_t*>(g.at + Gr::V + r * (D / 2) + 4 * l);
+      ks[x] = g.at[Gr::KS + r * Gr::SB + l / PER];
+      vs[x] = g.at[Gr::VS + r * Gr::SB + l / PER];
     }
+  }
 #pragma unroll
-    for (int x = 0; x < BATCH; ++x) {
-      const int r = base + x * ROWS + lane / L;
-      const int64_t s = skip + r - g.shift;
-      const bool in = r >= g.r0 && r < g.r1;
-      const uint4 k = values8(k_from_cache<L>(kw[x], row, l), scale_value<CF>(ks[x]));
-      const uint4 v = values8(v_from_cache<L>(vw[x], row, l), scale_value<CF>(vs[x]));
-      if (in && a.k) *reinterpret_cast<uint4*>(a.k + b * a.ks.b + s * a.ks.s + h * a.ks.h + 8 * l) = k;
-      if (in && a.v) *reinterpret_cast<uint4*>(a.v + b * a.vs.b + s * a.vs.s + h * a.vs.h + 8 * l) = v;
-    }
+  for (int x = 0; x < BATCH; ++x) {
+    const int r = base + x * ROWS + lane / L;
+    const int64_t s = skip + r - g.shift;
+    const bool in = r >= g.r0 && r < g.r1;
+    const uint4 k = values8(k_from_cache<L>(kw[x], row, l), scale_value<CF>(ks[x]));
+    const uint4 v = values8(v_from_cache<L>(vw[x], row, l), scale_value<CF>(vs[x]));
+    if (in && a.k) *reinterpret_cast<uint4*>(a.k + b * a.ks.b + s * a.ks.s + h * a.ks.h + 8 * l) = k;
+    if (in && a.v) *reinterpret_cast<uint4*>(a.v + b * a.vs.b + s * a.vs.s + h * a.vs.h + 8 * l) = v;
   }
 }
 
-// groups that S consecutive tokens can touch
-int groups_of(const CacheIo& a) { return (a.S + 14) / 16 + 1; }
+// units that S consecutive tokens can touch
+int units_of(const CacheIo& a) {
+  const int u = 1024 / a.c.D;
+  return (a.S + u - 2) / u + 1;
+}
 unsigned blocks_of(const CacheIo& a) {
-  return (unsigned)(((int64_t)a.B * groups_of(a) * a.c.Hkv + CIO_WARPS - 1) / CIO_WARPS);
+  return (unsigned)(((int64_t)a.B * units_of(a) * a.c.Hkv + CIO_WARPS - 1) / CIO_WARPS);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_append(const CacheIo& a, cudaStream_t st) {
   const unsigned grid = blocks_of(a);
-  const int groups = groups_of(a);
+  const int units = units_of(a);
   if (a.c.D == 128) {
-    if (a.c.cf == CF_MX) cache_append_kernel<128, CF_MX><<<grid, CIO_WARPS * 32, 0, st>>>(a, groups);
-    else cache_append_kernel<128, CF_NV><<<grid, CIO_WARPS * 32, 0, st>>>(a, groups);
+    if (a.c.cf == CF_MX) cache_append_kernel<128, CF_MX><<<grid, CIO_WARPS * 32, 0, st>>>(a, units);
+    else cache_append_kernel<128, CF_NV><<<grid, CIO_WARPS * 32, 0, st>>>(a, units);
   } else {
-    if (a.c.cf == CF_MX) cache_append_kernel<64, CF_MX><<<grid, CIO_WARPS * 32, 0, st>>>(a, groups);
-    else cache_append_kernel<64, CF_NV><<<grid, CIO_WARPS * 32, 0, st>>>(a, groups);
+    if (a.c.cf == CF_MX) cache_append_kernel<64, CF_MX><<<grid, CIO_WARPS * 32, 0, st>>>(a, units);
+    else cache_append_kernel<64, CF_NV><<<grid, CIO_WARPS * 32, 0, st>>>(a, units);
   }
   return cudaGetLastError();
 }
 
 cudaError_t launch_cache_read(const CacheIo& a, cudaStream_t st) {
   const unsigned grid = blocks_of(a);
-  const int groups = groups_of(a);
+  const int units = units_of(a);
   if (a.c.D == 128) {
-    if (a.c.cf == CF_MX) cache_read_kernel<128, CF_MX><<<grid, CIO_WARPS * 32, 0, st>>>(a, groups);
-    else cache_read_kernel<128, CF_NV><<<grid, CIO_WARPS * 32, 0, st>>>(a, groups);
+    if (a.c.cf == CF_MX) cache_read_kernel<128, CF_MX><<<grid, CIO_WARPS * 32, 0, st>>>(a, units);
+    else cache_read_kernel<128, CF_NV><<<grid, CIO_WARPS * 32, 0, st>>>(a, units);
   } else {
-    if (a.c.cf == CF_MX) cache_read_kernel<64, CF_MX><<<grid, CIO_WARPS * 32, 0, st>>>(a, groups);
-    else cache_read_kernel<64, CF_NV><<<grid, CIO_WARPS * 32, 0, st>>>(a, groups);
+    if (a.c.cf == CF_MX) cache_read_kernel<64, CF_MX><<<grid, CIO_WARPS * 32, 0, st>>>(a, units);
+    else cache_read_kernel<64, CF_NV><<<grid, CIO_WARPS * 32, 0, st>>>(a, units);
   }
   return cudaGetLastError();
 }

@@ -67,7 +67,7 @@ int cache_io(const fsa_cache* cache, const void* k, const void* v, const fsa_str
   if (B <= 0 || S <= 0 || !lens || !aligned(lens, 4) || !aligned(which, 4) || !aligned(status, 4) ||
       !table_ok(table, max_pages, cache->page_size) || !aligned(k, 16) || !aligned(v, 16))
     return FSA_ERR_INVALID_ARG;
-  if ((int64_t)B * (S / 16 + 2) > INT_MAX / cache->Hkv) return FSA_ERR_INVALID_ARG;       // groups of 16 tokens, counted in 32 bits
+  if ((int64_t)B * (S / 8 + 2) > INT_MAX / cache->Hkv) return FSA_ERR_INVALID_ARG;        // the kernels' units, counted in 32 bits
   if (k && !take_strides(ks, B, S, cache->Hkv, output, &a->ks)) return FSA_ERR_INVALID_ARG;
   if (v && !take_strides(vs, B, S, cache->Hkv, output, &a->vs)) return FSA_ERR_INVALID_ARG;
   a->k = static_cast<uint16_t*>(const_cast<void*>(k));

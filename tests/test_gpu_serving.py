@@ -510,6 +510,26 @@ def test_norm_rope(B, S, H, Hkv, D, rotary, sections, interleaved, norm, weights
     assert torch.equal(q, qo) and torch.equal(k, got_k)
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_norm_rope_infinities(interleaved):
+    """Without the norm, Inf and NaN reach their own pair and nothing else; elements past the
+    rotated ones are copied, the sign of zero with them."""
+    fsa = _fsa()
+    D, rotary = 128, 64
+    q = normal(gen(9), 1, 3, 2, D)
+    q[0, 0, 0, 5], q[0, 1, 1, 100], q[0, 2, 0, 70], q[0, 2, 1, 127] = math.inf, math.nan, -0.0, -math.inf
+    inv = torch.linspace(1.0, 0.1, rotary // 2, device="cuda", dtype=torch.float64)
+    out, _ = fsa.fsa_qk_norm_rope(q, q.clone(), i32([[3, 4, 5]]), inv, norm=False, interleaved=interleaved)
+    got, was = out[..., rotary:].contiguous(), q[..., rotary:].contiguous()
+    nan = torch.isnan(was)                          # a NaN stays one, its bits are not said
+    assert torch.equal(torch.isnan(got), nan)
+    assert torch.equal(got.view(torch.int16)[~nan], was.view(torch.int16)[~nan])
+    odd = ~torch.isfinite(out[..., :rotary])
+    want = torch.zeros_like(odd)
+    want[0, 0, 0, [4, 5] if interleaved else [5, 5 + rotary // 2]] = True
+    assert torch.equal(odd, want)
+
+
 def test_norm_rope_positions():
     """The extremes of int32, and that a turn by position differs from its neighbours' as it should."""
     fsa = _fsa()
