@@ -401,7 +401,7 @@ typedef struct {
  * One launch, nothing allocated: may be captured.  Errors: FSA_ERR_INVALID_ARG (null or
  * misaligned pointer, bad shape or strides, rotary not a multiple of 8 in 0..D, n_axes
  * not 1..3, sections that do not sum to rotary/2, eps negative or not finite),
- * FSA_ERR_LAUNCH. */
+ * FSA_ERR_NO_DEVICE, FSA_ERR_LAUNCH. */
 typedef struct {
   const void*    q;
   const void*    k;

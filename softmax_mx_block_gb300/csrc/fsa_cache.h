@@ -82,7 +82,7 @@ struct CacheAttnArgs {
 
 cudaError_t launch_cache_append(const CacheIo& a, cudaStream_t st);
 cudaError_t launch_cache_read(const CacheIo& a, cudaStream_t st);
-cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t st);
+cudaError_t launch_qk_norm_rope(const RopeArgs& a, int sms, cudaStream_t st);
 
 // columns (query rows of one kv head) of a pass, by eights, and the workspace of a call
 int cache_attn_ntiles(int cols);

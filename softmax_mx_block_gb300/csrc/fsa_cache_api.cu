@@ -168,7 +168,9 @@ int fsa_qk_norm_rope(const fsa_norm_rope* r, void* stream) {
   a.norm = r->norm;
   a.interleaved = r->interleaved;
   a.eps = r->eps;
-  return launch_status(fsa::launch_qk_norm_rope(a, static_cast<cudaStream_t>(stream)));
+  int sms = 0;
+  if (!sm_count(&sms)) return FSA_ERR_NO_DEVICE;
+  return launch_status(fsa::launch_qk_norm_rope(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int fsa_attention_cache_workspace(const fsa_cache* cache, int B, int H, int Sq, int max_pages, size_t* bytes) {

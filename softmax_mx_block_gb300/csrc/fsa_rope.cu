@@ -12,7 +12,7 @@
 // The work is bound by memory (4 bytes an element).  A block takes a few tokens with
 // all their heads: the sines of a token are computed once, by all threads, through shared
 // memory, and then stay in the registers of the threads that have that token, multiplied
-// by the norm's weights.  D/8 lanes hold a row, 8 elements each, chosen so that both
+// by the norm's weights.  D/16 lanes hold a row, 16 elements each, chosen so that both
 // elements of a pair are in one thread, and the arithmetic goes two floats at a time.
 #include "fsa_cache.h"
 #include "fsa_ptx.cuh"
@@ -21,8 +21,9 @@ namespace fsa {
 namespace {
 
 constexpr int ROPE_THREADS = 256;
-constexpr int ROPE_TOKENS = 4;
-constexpr int ROPE_ROWS = 4;       // rows of a thread in flight
+constexpr int ROPE_TOKENS = 16;    // of a block, at most
+constexpr int ROPE_ROWS = 2;       // rows of a thread in flight
+constexpr int ROPE_BLOCKS = 3;     // blocks of an SM
 
 // two floats in one register pair
 struct f2 {
@@ -52,195 +53,237 @@ __device__ __forceinline__ uint32_t pack(f2 a) {
 }
 __device__ __forceinline__ float weight_at(const uint16_t* w, int d) { return w ? __uint_as_float((uint32_t)w[d] << 16) : 1.0f; }
 
-// A thread's share of one tensor (q or k) for its token: rows h = first, first + step, ..
-template <int D>
-struct Rows {
-  const uint16_t* src;     // this lane's elements of the first row
-  uint16_t* dst;
-  int64_t sstep, dstep;    // to the next row
-  int n;                   // rows left
-  uint2 u0[ROPE_ROWS], u1[ROPE_ROWS];
-  __device__ __forceinline__ Rows(const uint16_t* x, const Strides& xs, uint16_t* o, const Strides& os, int heads, int b, int s,
-                                  int first, int step) {
-    src = x + b * xs.b + s * xs.s + first * xs.h;
-    dst = o + b * os.b + s * os.s + first * os.h;
-    sstep = step * xs.h;
-    dstep = step * os.h;
-    n = heads > first ? (heads - first + step - 1) / step : 0;
+// P pairs of elements in the order that the arithmetic takes them: a firsts, b seconds.
+// A lane of a row holds 2P elements: `a` at at0 .. and `b` at at1 .., P consecutive each, or,
+// interleaved, 2P consecutive ones from at0 on (at1 = at0 + P).
+template <int P>
+struct Raw {
+  uint32_t w[P];           // P/2 words from at0, P/2 from at1
+  __device__ __forceinline__ void load(const uint16_t* x, int at0, int at1) {
+    if constexpr (P == 8) {
+      const uint4 u = *reinterpret_cast<const uint4*>(x + at0), v = *reinterpret_cast<const uint4*>(x + at1);
+      w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+      w[4] = v.x; w[5] = v.y; w[6] = v.z; w[7] = v.w;
+    } else {
+      const uint2 u = *reinterpret_cast<const uint2*>(x + at0), v = *reinterpret_cast<const uint2*>(x + at1);
+      w[0] = u.x; w[1] = u.y; w[2] = v.x; w[3] = v.y;
+    }
   }
-  __device__ __forceinline__ void load(int at0, int at1) {
-#pragma unroll
-    for (int r = 0; r < ROPE_ROWS; ++r)
-      if (r < n) {
-        u0[r] = *reinterpret_cast<const uint2*>(src + r * sstep + at0);
-        u1[r] = *reinterpret_cast<const uint2*>(src + r * sstep + at1);
-      }
+  __device__ __forceinline__ void store(uint16_t* x, int at0, int at1) const {
+    if constexpr (P == 8) {
+      *reinterpret_cast<uint4*>(x + at0) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(x + at1) = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
+      *reinterpret_cast<uint2*>(x + at0) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2*>(x + at1) = make_uint2(w[2], w[3]);
+    }
   }
 };
 
-// The loaded rows, normalised, turned and stored.  c0..c3: what the first and the second
-// element of each pair are multiplied by, for the first and the second result.  turns: this
-// thread's elements do (all: every thread's).
-template <int D, bool INTER>
-__device__ __forceinline__ void finish_rows(Rows<D>& x, int at0, int at1, const f2 (&c)[4][2], uint32_t lanes, bool turns, bool all,
-                                            bool norm, float eps) {
-  constexpr int L = D / 8;
+// What the first and the second element of each of the thread's pairs are multiplied by,
+// two pairs a register: first result a * c[0] + b * c[1], second a * c[2] + b * c[3].
+template <int P, bool INTER>
+struct Factors {
+  f2 c[4][P / 2];
+  __device__ __forceinline__ void set(const float2* t, bool turns, const uint16_t* w, int at0, int at1) {
 #pragma unroll
-  for (int r = 0; r < ROPE_ROWS; ++r) {
-    if (r >= x.n) break;
-    // elements in the order that pairs take them: a = firsts, b = seconds of the 4 pairs
-    f2 a[2], b[2];
-    if (INTER) {
-      float v[8];
-      split(unpack(x.u0[r].x), v[0], v[1]);
-      split(unpack(x.u0[r].y), v[2], v[3]);
-      split(unpack(x.u1[r].x), v[4], v[5]);
-      split(unpack(x.u1[r].y), v[6], v[7]);
-      a[0] = make(v[0], v[2]); a[1] = make(v[4], v[6]);
-      b[0] = make(v[1], v[3]); b[1] = make(v[5], v[7]);
-    } else {
-      a[0] = unpack(x.u0[r].x); a[1] = unpack(x.u0[r].y);
-      b[0] = unpack(x.u1[r].x); b[1] = unpack(x.u1[r].y);
-    }
-    float rs = 1.0f;
-    if (norm) {
-      float lo, hi;
-      split(fma(a[0], a[0], fma(a[1], a[1], fma(b[0], b[0], mul(b[1], b[1])))), lo, hi);
-      float ss = lo + hi;
+    for (int e = 0; e < P / 2; ++e) {
+      float f[4][2];
+      const float4 cs = turns ? reinterpret_cast<const float4*>(t)[e] : make_float4(1.f, 0.f, 1.f, 0.f);   // cos, sin of two
 #pragma unroll
-      for (int m = L / 2; m; m >>= 1) ss += __shfl_xor_sync(lanes, ss, m, L);
-      rs = rsqrtf(ss * (1.0f / D) + eps);
-    }
-    const f2 rr = make(rs, rs);
-    f2 p[2], q[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      f2 ap = mul(b[e], c[1][e]), aq = mul(a[e], c[2][e]);
-      p[e] = fma(a[e], c[0][e], ap);
-      q[e] = fma(b[e], c[3][e], aq);
-      if (!all) {                                   // an element that does not turn takes nothing of another
-        p[e].v = turns ? p[e].v : mul(a[e], c[0][e]).v;
-        q[e].v = turns ? q[e].v : mul(b[e], c[3][e]).v;
+      for (int x = 0; x < 2; ++x) {
+        const int i = 2 * e + x;
+        const float wa = weight_at(w, INTER ? at0 + 2 * i : at0 + i), wb = weight_at(w, INTER ? at0 + 2 * i + 1 : at1 + i);
+        const float co = x ? cs.z : cs.x, si = x ? cs.w : cs.y;
+        f[0][x] = wa * co;
+        f[1][x] = -wb * si;
+        f[2][x] = wa * si;
+        f[3][x] = wb * co;
       }
-      p[e] = mul(rr, p[e]);
-      q[e] = mul(rr, q[e]);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) c[x][e] = make(f[x][0], f[x][1]);
     }
-    uint2 o0, o1;
-    if (INTER) {
-      float pv[4], qv[4];
-      split(p[0], pv[0], pv[1]); split(p[1], pv[2], pv[3]);
-      split(q[0], qv[0], qv[1]); split(q[1], qv[2], qv[3]);
-      o0 = make_uint2(cvt_bf16x2(pv[0], qv[0]), cvt_bf16x2(pv[1], qv[1]));
-      o1 = make_uint2(cvt_bf16x2(pv[2], qv[2]), cvt_bf16x2(pv[3], qv[3]));
+  }
+};
+
+// One row, normalised and turned.  lanes: those of the row; turns: this thread's elements do
+// (all: every thread's).
+template <int D, int P, bool INTER>
+__device__ __forceinline__ void turn_row(Raw<P>& x, const Factors<P, INTER>& f, uint32_t lanes, bool turns, bool all, bool norm,
+                                         float eps) {
+  constexpr int L = D / (2 * P);
+  f2 a[P / 2], b[P / 2];
+#pragma unroll
+  for (int e = 0; e < P / 2; ++e) {
+    if (INTER) {           // words 2e and 2e + 1: pairs 2e, 2e + 1
+      const uint32_t u = x.w[2 * e], v = x.w[2 * e + 1];
+      a[e] = make(__uint_as_float(u << 16), __uint_as_float(v << 16));
+      b[e] = make(__uint_as_float(u & 0xFFFF0000u), __uint_as_float(v & 0xFFFF0000u));
     } else {
-      o0 = make_uint2(pack(p[0]), pack(p[1]));
-      o1 = make_uint2(pack(q[0]), pack(q[1]));
+      a[e] = unpack(x.w[e]);
+      b[e] = unpack(x.w[P / 2 + e]);
     }
-    *reinterpret_cast<uint2*>(x.dst + r * x.dstep + at0) = o0;
-    *reinterpret_cast<uint2*>(x.dst + r * x.dstep + at1) = o1;
   }
-  x.src += ROPE_ROWS * x.sstep;
-  x.dst += ROPE_ROWS * x.dstep;
-  x.n -= ROPE_ROWS;
+  float rs = 1.0f;
+  if (norm) {
+    f2 sa = mul(a[0], a[0]), sb = mul(b[0], b[0]);
+#pragma unroll
+    for (int e = 1; e < P / 2; ++e) {
+      sa = fma(a[e], a[e], sa);
+      sb = fma(b[e], b[e], sb);
+    }
+    float s0, s1, s2, s3;
+    split(sa, s0, s1);
+    split(sb, s2, s3);
+    float ss = (s0 + s1) + (s2 + s3);
+#pragma unroll
+    for (int m = L / 2; m; m >>= 1) ss += __shfl_xor_sync(lanes, ss, m, L);
+    rs = rsqrtf(ss * (1.0f / D) + eps);
+  }
+  const f2 rr = make(rs, rs);
+#pragma unroll
+  for (int e = 0; e < P / 2; ++e) {
+    f2 p = fma(a[e], f.c[0][e], mul(b[e], f.c[1][e]));
+    f2 q = fma(b[e], f.c[3][e], mul(a[e], f.c[2][e]));
+    if (!all) {            // an element that does not turn takes nothing of another
+      p.v = turns ? p.v : mul(a[e], f.c[0][e]).v;
+      q.v = turns ? q.v : mul(b[e], f.c[3][e]).v;
+    }
+    p = mul(rr, p);
+    q = mul(rr, q);
+    if (INTER) {
+      float p0, p1, q0, q1;
+      split(p, p0, p1);
+      split(q, q0, q1);
+      x.w[2 * e] = cvt_bf16x2(p0, q0);
+      x.w[2 * e + 1] = cvt_bf16x2(p1, q1);
+    } else {
+      x.w[e] = pack(p);
+      x.w[P / 2 + e] = pack(q);
+    }
+  }
 }
 
-// The factors of the thread's 4 pairs: first result a * c0 + b * c1, second a * c2 + b * c3.
-template <bool INTER>
-__device__ __forceinline__ void factors(const float4& t0, const float4& t1, const uint16_t* w, int at0, int at1, f2 (&c)[4][2]) {
-  const float cs[4] = {t0.x, t0.z, t1.x, t1.z}, sn[4] = {t0.y, t0.w, t1.y, t1.w};
-  float f[4][4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float wa = weight_at(w, INTER ? at0 + 2 * e : at0 + e), wb = weight_at(w, INTER ? at0 + 2 * e + 1 : at1 + e);
-    f[0][e] = wa * cs[e];
-    f[1][e] = -wb * sn[e];
-    f[2][e] = wa * sn[e];
-    f[3][e] = wb * cs[e];
-  }
-#pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    c[x][0] = make(f[x][0], f[x][1]);
-    c[x][1] = make(f[x][2], f[x][3]);
-  }
+// inv_freq / 2 pi as a sum of two floats, without fp64 arithmetic (few lanes have it): the
+// double's leading 24 and following 29 bits, times 1 / 2 pi as two floats.
+__device__ __forceinline__ void turns_of(double freq, float& fh, float& fl) {
+  const uint32_t hi = (uint32_t)__double2hiint(freq), lo = (uint32_t)__double2loint(freq);
+  const int e = (int)(hi >> 20 & 0x7FF) - 1023;
+  fh = fl = 0.f;
+  if (e < -100) return;                             // no angle at any position
+  const float lead = __uint_as_float((hi & 0x80000000u) | (uint32_t)(min(e, 128) + 127) << 23 | (hi & 0xFFFFFu) << 3 | lo >> 29);
+  const float rest = copysignf((float)(lo & 0x1FFFFFFFu) * __uint_as_float((uint32_t)max(e + 127 - 52, 0) << 23), lead);
+  constexpr float ch = 0.15915494309189535f, cl = (float)(0.15915494309189533576888376337251436 - (double)ch);
+  fh = __fmul_rn(lead, ch);
+  fl = fmaf(lead, ch, -fh) + fmaf(lead, cl, rest * ch);
 }
 
-template <int D, bool INTER>
-__global__ void __launch_bounds__(ROPE_THREADS) qk_norm_rope_kernel(const RopeArgs a, int tokens) {
-  constexpr int L = D / 8, GROUPS = ROPE_THREADS / L;
-  __shared__ __align__(16) float2 cs[ROPE_TOKENS * D / 2];        // cos, sin of [token][pair]
+template <int D, int P, bool INTER>
+__global__ void __launch_bounds__(ROPE_THREADS, ROPE_BLOCKS) qk_norm_rope_kernel(const RopeArgs a, int tokens) {
+  constexpr int L = D / (2 * P), GROUPS = ROPE_THREADS / L;
+  __shared__ __align__(16) float2 sines[ROPE_TOKENS * D / 2];     // cos, sin of [token][pair]
   const uint32_t total = (uint32_t)a.B * (uint32_t)a.S;
   const uint32_t first = blockIdx.x * (uint32_t)tokens;
   const int ntok = (int)min((uint32_t)tokens, total - first);
-  // this thread: lane of a row of token j, heads h0, h0 + step, ..
+  // this thread: lane of a row of token j, rows h0, h0 + step, .. of q's heads and then k's
   const int lane = threadIdx.x % L, group = threadIdx.x / L;
   const int step = GROUPS / tokens, j = group / step, h0 = group - j * step;
   const uint32_t lanes = (uint32_t)((1ull << L) - 1) << (threadIdx.x % 32 / L * L);
-  const int at0 = INTER || 4 * lane >= a.half ? 8 * lane : 4 * lane;
-  const int at1 = INTER || 4 * lane >= a.half ? 8 * lane + 4 : a.half + 4 * lane;
+  const bool turns = P * lane < a.half, all = a.half == D / 2;
+  const int at0 = INTER || !turns ? 2 * P * lane : P * lane;
+  const int at1 = INTER || !turns ? 2 * P * lane + P : a.half + P * lane;
   const uint32_t tok = first + min(j, ntok - 1);
   const int b = (int)(tok / (uint32_t)a.S), s = (int)(tok - (uint32_t)b * (uint32_t)a.S);
-  Rows<D> q(a.q, a.qs, a.qo, a.qos, j < ntok ? a.H : 0, b, s, h0, step);
-  q.load(at0, at1);                                               // on their way while the sines are computed
+  const int nq = j < ntok ? a.H : 0, nk = j < ntok ? a.Hkv : 0;
+
+  const uint16_t* src = a.q + b * a.qs.b + s * a.qs.s + h0 * a.qs.h;
+  uint16_t* dst = a.qo + b * a.qos.b + s * a.qos.s + h0 * a.qos.h;
+  int64_t sstep = step * a.qs.h, dstep = step * a.qos.h;
+  Raw<P> x[ROPE_ROWS];
+  int h = h0, n = nq;
+  auto load = [&] {
+#pragma unroll
+    for (int r = 0; r < ROPE_ROWS; ++r)
+      if (h + r * step < n) x[r].load(src + r * sstep, at0, at1);
+  };
+  load();                                                         // on their way while the sines are computed
   if (a.half > 0) {
     const int per = ROPE_THREADS / a.half;        // tokens at a time
     const int i = threadIdx.x % a.half;
     if ((int)threadIdx.x < per * a.half) {
-      const double f = a.inv_freq[i] * 0.15915494309189533576888376337251436;   // 1 / (2 pi)
-      const float fh = (float)f, fl = (float)(f - (double)fh);
+      float fh, fl;
+      turns_of(a.inv_freq[i], fh, fl);
       const int axis = i >= a.first2 ? 2 : i >= a.first1 ? 1 : 0;
-      for (int x = threadIdx.x / a.half; x < ntok; x += per) {
-        const int p = a.pos[((int64_t)first + x) * a.axes + axis];
+      for (int t = threadIdx.x / a.half; t < ntok; t += per) {
+        const int p = a.pos[((int64_t)first + t) * a.axes + axis];
         const float ph = (float)p, pl = (float)((int64_t)p - (int64_t)ph);       // p = ph + pl exactly
-        const float h = __fmul_rn(ph, fh);          // rounded: l below holds what this drops
-        const float l = fmaf(ph, fh, -h) + fmaf(ph, fl, pl * fh);
-        const float turns = (h - rintf(h)) + l;
+        const float g = __fmul_rn(ph, fh);          // rounded: l below holds what this drops
+        const float l = fmaf(ph, fh, -g) + fmaf(ph, fl, pl * fh);
+        const float part = (g - rintf(g)) + l;      // of a turn
         float sn, c;
-        sincospif(2.0f * turns, &sn, &c);
-        cs[x * a.half + i] = make_float2(c, sn);
+        sincospif(2.0f * part, &sn, &c);
+        sines[t * a.half + i] = make_float2(c, sn);
       }
     }
   }
   __syncthreads();
-  if (j >= ntok) return;
-  float4 t0 = make_float4(1.f, 0.f, 1.f, 0.f), t1 = t0;           // past the pairs: no turn
-  if (4 * lane < a.half) {
-    const float4* t = reinterpret_cast<const float4*>(cs + j * a.half + 4 * lane);
-    t0 = t[0];
-    t1 = t[1];
+  Factors<P, INTER> f;
+  const float2* const t = sines + j * a.half + P * lane;
+  // (threads past the pairs hold 2P consecutive elements, unturned)
+  f.set(t, turns, a.wq, at0, at1);
+#pragma unroll 1
+  for (bool keys = false;; keys = true) {
+#pragma unroll 1
+    while (h < n) {
+#pragma unroll
+      for (int r = 0; r < ROPE_ROWS; ++r)
+        if (h + r * step < n) {
+          turn_row<D, P, INTER>(x[r], f, lanes, turns, all, a.norm, a.eps);
+          x[r].store(dst + r * dstep, at0, at1);
+        }
+      h += ROPE_ROWS * step;
+      src += ROPE_ROWS * sstep;
+      dst += ROPE_ROWS * dstep;
+      load();
+    }
+    if (keys) return;
+    src = a.k + b * a.ks.b + s * a.ks.s + h0 * a.ks.h;
+    dst = a.ko + b * a.kos.b + s * a.kos.s + h0 * a.kos.h;
+    sstep = step * a.ks.h;
+    dstep = step * a.kos.h;
+    h = h0;
+    n = nk;
+    load();
+    f.set(t, turns, a.wk, at0, at1);
   }
-  // (threads past the pairs hold 8 consecutive elements: as pairs (x, x + 4) of them, or as
-  // neighbours when interleaved, unturned)
-  const bool turns = 4 * lane < a.half, all = a.half == D / 2;
-  f2 c[4][2];
-  factors<INTER>(t0, t1, a.wq, at0, at1, c);
-  while (true) {
-    finish_rows<D, INTER>(q, at0, at1, c, lanes, turns, all, a.norm, a.eps);
-    if (q.n <= 0) break;
-    q.load(at0, at1);
-  }
-  Rows<D> k(a.k, a.ks, a.ko, a.kos, a.Hkv, b, s, h0, step);
-  if (k.n <= 0) return;
-  k.load(at0, at1);
-  factors<INTER>(t0, t1, a.wk, at0, at1, c);
-  while (true) {
-    finish_rows<D, INTER>(k, at0, at1, c, lanes, turns, all, a.norm, a.eps);
-    if (k.n <= 0) break;
-    k.load(at0, at1);
-  }
+}
+
+template <int D, int P>
+void launch_rows(const RopeArgs& a, unsigned grid, int tokens, cudaStream_t st) {
+  if (a.interleaved) qk_norm_rope_kernel<D, P, true><<<grid, ROPE_THREADS, 0, st>>>(a, tokens);
+  else qk_norm_rope_kernel<D, P, false><<<grid, ROPE_THREADS, 0, st>>>(a, tokens);
 }
 
 }  // namespace
 
-cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t st) {
+cudaError_t launch_qk_norm_rope(const RopeArgs& a, int sms, cudaStream_t st) {
   const int64_t total = (int64_t)a.B * a.S;
-  const int tokens = total >= 4096 ? ROPE_TOKENS : 1;
+  // 16 elements a lane halve the shuffles and the addresses of a row; 8 where the rotated
+  // part is an odd multiple of 8
+  const bool wide = a.half % 8 == 0;
+  // Tokens of a block: four of its groups of lanes each (two heads' rows in flight a group,
+  // and what a block starts with, its pairs' frequencies and weights, spread over 8 tokens of
+  // 128 or 16 of 64 dims: video 496 us, with half as many 546, with a quarter 648), fewer
+  // where that would not leave three blocks for two SMs.
+  int tokens = ROPE_THREADS / (a.D / (wide ? 16 : 8)) / 4;
+  while (tokens > 1 && 2 * total < 3 * (int64_t)tokens * sms) tokens /= 2;
   const unsigned grid = (unsigned)((total + tokens - 1) / tokens);
   if (a.D == 128) {
-    if (a.interleaved) qk_norm_rope_kernel<128, true><<<grid, ROPE_THREADS, 0, st>>>(a, tokens);
-    else qk_norm_rope_kernel<128, false><<<grid, ROPE_THREADS, 0, st>>>(a, tokens);
+    if (wide) launch_rows<128, 8>(a, grid, tokens, st);
+    else launch_rows<128, 4>(a, grid, tokens, st);
   } else {
-    if (a.interleaved) qk_norm_rope_kernel<64, true><<<grid, ROPE_THREADS, 0, st>>>(a, tokens);
-    else qk_norm_rope_kernel<64, false><<<grid, ROPE_THREADS, 0, st>>>(a, tokens);
+    if (wide) launch_rows<64, 8>(a, grid, tokens, st);
+    else launch_rows<64, 4>(a, grid, tokens, st);
   }
   return cudaGetLastError();
 }
