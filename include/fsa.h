@@ -487,7 +487,8 @@ int fsa_cache_read(const fsa_cache* cache, void* k, void* v, const fsa_strides* 
  *   status: optional device int32: FSA_ERR_INVALID_ARG where a page number lay outside the
  *     pool (its keys are not seen), FSA_ERR_TIMEOUT where a wait for a copy ran out
  *     (timeout_ms; 0: 4000), the output then being undefined
- * B * Sq * H <= 2^27.  Errors: FSA_ERR_INVALID_ARG, FSA_ERR_UNSUPPORTED_FMT,
+ * B * Sq * H <= 2^27; B * Hkv * (Sq * H/Hkv / 8 + 1) * (max_pages * page_size / 32 + 9) <= 2^31
+ * (the kernels count tiles over all sequences in 32 bits).  Errors: FSA_ERR_INVALID_ARG, FSA_ERR_UNSUPPORTED_FMT,
  * FSA_ERR_NO_DEVICE, FSA_ERR_LAUNCH.  The work is laid out for the current device, which
  * must be the one of the pointers and the stream. */
 typedef struct {

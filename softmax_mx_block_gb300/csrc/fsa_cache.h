@@ -74,6 +74,7 @@ struct CacheAttnArgs {
   float* partials;        // workspace: two partial results a CTA
   int4* starts;           // workspace: per CTA, the segment that begins in it and goes on, and the CTA where it ends
   int B, H, Sq, G, CT, max_pages, causal, out_bf16;
+  uint32_t g_mul;         // col / G is the high word of col * g_mul (0: it is not)
   float scale_log2;       // |scale| log2 e, or 1 when the scale is 0
   float q_sign;           // the scale's sign (0 for a zero scale)
   int32_t* status;

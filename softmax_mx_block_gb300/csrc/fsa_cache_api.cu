@@ -90,9 +90,14 @@ bool sm_count(int* sms) {
          cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && *sms > 0;
 }
 
-bool attn_shape_ok(int B, int H, int Hkv, int Sq, int D) {
-  return B > 0 && H > 0 && Hkv > 0 && H % Hkv == 0 && Sq > 0 && (D == 64 || D == 128) &&
-         (int64_t)B * Sq * H <= INT_MAX / 16;
+// The kernels count rows and, over all sequences, heads and passes of columns, tiles of 32
+// keys (and what a segment's start weighs, at most 8) in 32 bits.
+bool attn_shape_ok(int B, int H, int Hkv, int Sq, int D, int max_pages, int page_size) {
+  if (!(B > 0 && H > 0 && Hkv > 0 && H % Hkv == 0 && Sq > 0 && (D == 64 || D == 128) && pages_ok(max_pages, page_size) &&
+        (int64_t)B * H <= INT_MAX / 16 / Sq))
+    return false;
+  const int64_t passes = ((int64_t)Sq * (H / Hkv) + 7) / 8, tiles = ((int64_t)max_pages * page_size + 31) / 32 + 8;
+  return (int64_t)B * Hkv <= INT_MAX / passes / tiles;
 }
 
 }  // namespace
@@ -178,7 +183,7 @@ int fsa_attention_cache_workspace(const fsa_cache* cache, int B, int H, int Sq, 
   if (!bytes) return FSA_ERR_INVALID_ARG;
   const int st = take_cache(cache, &c);
   if (st != FSA_OK) return st;
-  if (!attn_shape_ok(B, H, c.Hkv, Sq, c.D) || !pages_ok(max_pages, cache->page_size)) return FSA_ERR_INVALID_ARG;
+  if (!attn_shape_ok(B, H, c.Hkv, Sq, c.D, max_pages, cache->page_size)) return FSA_ERR_INVALID_ARG;
   int sms = 0;
   if (!sm_count(&sms)) return FSA_ERR_NO_DEVICE;
   size_t starts_at;
@@ -192,7 +197,7 @@ int fsa_attention_cache(const fsa_cache_attn* c, void* stream) {
   const int st = take_cache(c->cache, &a.c);
   if (st != FSA_OK) return st;
   const int Hkv = a.c.Hkv, D = a.c.D;
-  if (!c->q || !c->out || !c->lens || !attn_shape_ok(c->B, c->H, Hkv, c->Sq, D) ||
+  if (!c->q || !c->out || !c->lens || !attn_shape_ok(c->B, c->H, Hkv, c->Sq, D, c->max_pages, c->cache->page_size) ||
       !table_ok(c->block_table, c->max_pages, c->cache->page_size) || !std::isfinite(c->scale) ||
       (c->causal != 0 && c->causal != 1) || (c->out_dtype != FSA_OUT_F32 && c->out_dtype != FSA_OUT_BF16) ||
       !aligned(c->q, 16) || !aligned(c->out, 16) || !aligned(c->workspace, 16) || !aligned(c->lens, 4) ||
@@ -217,6 +222,9 @@ int fsa_attention_cache(const fsa_cache_attn* c, void* stream) {
   a.starts = reinterpret_cast<int4*>(static_cast<char*>(c->workspace) + starts_at);
   a.B = c->B; a.H = c->H; a.Sq = c->Sq; a.G = G;
   a.CT = (c->Sq * G + 8 * nt - 1) / (8 * nt);
+  // floor(2^32 / G) + 1 exceeds 2^32 / G by at most 1, so the product is exact for columns
+  // below 2^32 / G
+  a.g_mul = G > 1 && (uint64_t)c->Sq * G * G < (1ull << 32) ? (uint32_t)((1ull << 32) / G + 1) : 0;
   a.max_pages = c->max_pages;
   a.causal = c->causal;
   a.out_bf16 = c->out_dtype == FSA_OUT_BF16;

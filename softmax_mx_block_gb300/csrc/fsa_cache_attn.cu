@@ -60,7 +60,7 @@ struct Cfg {
   static constexpr int NWC = cta_warps<D, NT>();
   static constexpr int STAGE = 2 * Gr::BYTES;
   static constexpr int COLS = 8 * NT;
-  static constexpr int PART = COLS * (D + 2);        // floats of a partial result: rows, maxima, sums
+  static constexpr int PART = COLS * (D + 6);        // floats of a partial result: rows D + 4 apart, maxima, sums
   static constexpr int STG = CF == CF_MX ? 3 : 2;   // stages of a warp's ring
   static constexpr int RING = NWC * STG * STAGE;
   static constexpr int JOIN = NWC * PART * 4;
@@ -70,10 +70,15 @@ struct Cfg {
 
 // ---------------------------------------------------------------- the work list
 // "Virtual sequence" vb = b * CT + ct: the ct-th pass of columns of sequence b.
+// The units of all virtual sequences together fit an int (the host sees to it).
 struct Span {
   int qlen, len, kmax, tiles;   // rows, keys, keys that some column sees, tiles (0: no rows)
   __device__ __forceinline__ int units() const { return tiles ? tiles + EXTRA : 0; }
 };
+// row i of a column i * G + its head: col / G
+__device__ __forceinline__ int row_of(const CacheAttnArgs& p, int col) {
+  return p.g_mul ? (int)__umulhi((uint32_t)col, p.g_mul) : p.G == 1 ? col : col / p.G;
+}
 __device__ __forceinline__ Span span_of(const CacheAttnArgs& p, int vb, int cols) {
   Span s;
   const int b = p.CT == 1 ? vb : vb / p.CT, ct = vb - b * p.CT;
@@ -81,35 +86,29 @@ __device__ __forceinline__ Span span_of(const CacheAttnArgs& p, int vb, int cols
   s.len = (int)min((int64_t)max(p.lens[b], 0), (int64_t)p.max_pages << p.c.page_shift);
   const int c0 = ct * cols;
   if (c0 >= s.qlen * p.G) { s.kmax = s.tiles = 0; return s; }
-  const int last = min(s.qlen - 1, (c0 + cols - 1) / p.G);
+  const int last = min(s.qlen - 1, row_of(p, c0 + cols - 1));
   s.kmax = p.causal ? max(0, s.len - s.qlen + last + 1) : s.len;
   s.tiles = max(1, (s.kmax + TILE - 1) / TILE);      // a tile for rows that see nothing: they are written
   return s;
 }
 
-// 64-bit quotient of non-negative numbers, by 32-bit division where they fit
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
-}
-
-// `total` tiles over n warps: the first `more` of them take base + 1, the others base.
+// `total` units over n warps: the first `more` of them take base + 1, the others base.
 struct Shares {
-  int64_t base;
-  int more;
-  __device__ __forceinline__ Shares(int64_t total, int n) {
-    base = n > 0 ? quotient(total, n) : 0;
-    more = (int)(total - base * n);
+  int base, more;
+  __device__ __forceinline__ Shares(int total, int n) {
+    base = n > 0 ? (int)((uint32_t)total / (uint32_t)n) : 0;
+    more = total - base * n;
   }
-  __device__ __forceinline__ int64_t first(int w) const { return base * w + min(w, more); }
-  __device__ __forceinline__ int of(int64_t tile) const {      // the warp that has it
-    const int64_t cut = (base + 1) * more;
-    return tile < cut ? (int)quotient(tile, base + 1) : more + (int)quotient(tile - cut, base);
+  __device__ __forceinline__ int first(int w) const { return base * w + min(w, more); }
+  __device__ __forceinline__ int of(int unit) const {          // the warp that has it
+    const int cut = (base + 1) * more;
+    return unit < cut ? (int)((uint32_t)unit / (uint32_t)(base + 1)) : more + (int)((uint32_t)(unit - cut) / (uint32_t)base);
   }
 };
 
 // Keys that column c of virtual sequence (b, ct) sees (0 for none and for padding).
 __device__ __forceinline__ int limit_of(const CacheAttnArgs& p, const Span& s, int col) {
-  const int i = col / p.G;
+  const int i = row_of(p, col);
   if (i >= s.qlen) return 0;
   return p.causal ? max(0, s.len - s.qlen + i + 1) : s.len;
 }
@@ -475,7 +474,7 @@ struct Row {
   float inv, lse;
   bool none;               // no key: zeros
   __device__ __forceinline__ Row(const CacheAttnArgs& p, int b, int hkv, int col, const Span& s, float m, float l) {
-    const int i = col / p.G, h = hkv * p.G + col - i * p.G;
+    const int i = row_of(p, col), h = hkv * p.G + col - i * p.G;
     at = b * p.os.b + i * p.os.s + h * p.os.h;
     lse_at = ((int64_t)b * p.Sq + i) * p.H + h;
     none = limit_of(p, s, col) == 0;
@@ -493,10 +492,11 @@ struct Row {
   }
 };
 
-// A partial result: the unnormalised rows [COLS][D], their maxima, their sums.
+// A partial result: the unnormalised rows [COLS][D + 4] (4 more, so that the lanes of a quad,
+// two columns apart, store to different banks), their maxima, their sums.
 template <int D, int CF, int NT>
 __device__ __forceinline__ void put_part(float* part, const Acc<D, CF, NT>& a) {
-  constexpr int COLS = 8 * NT;
+  constexpr int COLS = 8 * NT, DP = D + 4;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -505,10 +505,10 @@ __device__ __forceinline__ void put_part(float* part, const Acc<D, CF, NT>& a) {
       const int col = 8 * n + 2 * t + e;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
-        *reinterpret_cast<float2*>(part + col * D + 16 * k + 2 * g) = make_float2(a.o[k][n][e], a.o[k][n][2 + e]);
+        *reinterpret_cast<float2*>(part + col * DP + 16 * k + 2 * g) = make_float2(a.o[k][n][e], a.o[k][n][2 + e]);
       if (g == 0) {
-        part[COLS * D + col] = a.m[n][e];
-        part[COLS * (D + 1) + col] = a.l[n][e];
+        part[COLS * DP + col] = a.m[n][e];
+        part[COLS * (DP + 1) + col] = a.l[n][e];
       }
     }
 }
@@ -541,7 +541,7 @@ __device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const Span& sp
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int col = c0 + 8 * n + g;                   // fragment columns: g
-    const int i = col / p.G;
+    const int i = row_of(p, col);
     const uint16_t* src = p.q + b * p.qs.b + i * p.qs.s + (int64_t)(hkv * p.G + col - i * p.G) * p.qs.h + 4 * t;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k)
@@ -673,28 +673,35 @@ __device__ __forceinline__ void put_rows(const CacheAttnArgs& p, const Span& sp,
     }
 }
 
-// One column of n parts joined by a warp: a lane has dims 64x + 2 lane and the next.
+// One column of n <= 32 parts joined by a warp: a lane weighs part `lane`, and has dims
+// 64x + 2 lane and the next of the sum.
 template <int D, int COLS>
 struct Column {
+  static constexpr int DP = D + 4;
   float m, l;
   float2 o[D / 64];
   template <class Part>
   __device__ __forceinline__ Column(Part part, int n, int col) {
     const int lane = threadIdx.x & 31;
-    m = M_NONE * 2.f;
-    l = 0.f;
+    const float* const mine = part(min(lane, n - 1));
+    const float mk = lane < n ? mine[COLS * DP + col] : M_NONE * 4.f;
+    l = lane < n ? mine[COLS * (DP + 1) + col] : 0.f;
+    m = mk;
+#pragma unroll
+    for (int x = 1; x < 32; x *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+    const float w = lane < n ? exp2f(mk - m) : 0.f;
+    l = lane < n ? l * w : 0.f;
+#pragma unroll
+    for (int x = 1; x < 32; x *= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
 #pragma unroll
     for (int x = 0; x < D / 64; ++x) o[x] = make_float2(0.f, 0.f);
 #pragma unroll 4
-    for (int k = 0; k < n; ++k) m = fmaxf(m, part(k)[COLS * D + col]);
-#pragma unroll 4
     for (int k = 0; k < n; ++k) {
-      const float* const pk = part(k);
-      const float f = exp2f(pk[COLS * D + col] - m);
-      l = fmaf(f, pk[COLS * (D + 1) + col], l);
+      const float* const pk = part(k) + col * DP + 2 * lane;
+      const float f = __shfl_sync(0xFFFFFFFFu, w, k);
 #pragma unroll
       for (int x = 0; x < D / 64; ++x) {
-        const float2 v = *reinterpret_cast<const float2*>(pk + col * D + 64 * x + 2 * lane);
+        const float2 v = *reinterpret_cast<const float2*>(pk + 64 * x);
         o[x].x = fmaf(f, v.x, o[x].x);
         o[x].y = fmaf(f, v.y, o[x].y);
       }
@@ -710,23 +717,29 @@ struct Column {
   __device__ __forceinline__ void put_part(float* part, int col) const {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int x = 0; x < D / 64; ++x) *reinterpret_cast<float2*>(part + col * D + 64 * x + 2 * lane) = o[x];
+    for (int x = 0; x < D / 64; ++x) *reinterpret_cast<float2*>(part + col * DP + 64 * x + 2 * lane) = o[x];
     if (lane == 0) {
-      part[COLS * D + col] = m;
-      part[COLS * (D + 1) + col] = l;
+      part[COLS * DP + col] = m;
+      part[COLS * (DP + 1) + col] = l;
     }
   }
 };
 
 // Few short segments, or many: a CTA of 4 warps each, three CTAs an SM; no list, no second
 // kernel.  Block x is segment x.
-constexpr int WHOLE_WARPS = 4;
+#ifndef WW
+#define WW 4
+#endif
+#ifndef WC
+#define WC 3
+#endif
+constexpr int WHOLE_WARPS = WW;
 template <int D, int CF, int NT>
 struct WholeCfg {
   using C = Cfg<D, CF, NT>;
   static constexpr int RING = WHOLE_WARPS * C::STG * C::STAGE, JOIN = WHOLE_WARPS * C::PART * 4;
   static constexpr int SMEM = 1024 + WHOLE_WARPS * C::SCALES + (RING > JOIN ? RING : JOIN);
-  static constexpr int CTAS = NT == 2 && D == 128 ? 2 : 3;
+  static constexpr int CTAS = NT == 2 && D == 128 ? (WC + 1) / 2 : WC;
 };
 template <int D, int CF, int NT>
 __global__ void __launch_bounds__(WHOLE_WARPS * 32, WholeCfg<D, CF, NT>::CTAS) cache_attn_whole_kernel(const CacheAttnArgs p) {
@@ -774,10 +787,10 @@ __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem);                  // [NWC][STG]
   int* flag = reinterpret_cast<int*>(smem + 512);                      // abort
-  int64_t* wsum = reinterpret_cast<int64_t*>(smem + 576);              // [NWC]
+  int* wsum = reinterpret_cast<int*>(smem + 576);              // [NWC]
   int2* ends = reinterpret_cast<int2*>(smem + 520);                    // x: the first open piece begins, y: tiles behind the last
   int4* pieces = reinterpret_cast<int4*>(smem + 704);                  // [NWC] segments of the leading and the open piece; its qlen, len
-  int64_t* pre = reinterpret_cast<int64_t*>(smem + 1024);              // [NWC * 32]
+  int* pre = reinterpret_cast<int*>(smem + 1024);              // [NWC * 32]
   uint32_t* scales = reinterpret_cast<uint32_t*>(smem + 1024 + NWC * 32 * 8);
   float* leads = reinterpret_cast<float*>(smem + 1024 + NWC * 32 * 8 + NWC * C::SCALES);  // [NWC] parts
   uint8_t* ring = smem + 1024 + NWC * 32 * 8 + NWC * C::SCALES + C::JOIN;
@@ -796,20 +809,20 @@ __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(
   const bool small = VB <= 128;
   const int chunk = small ? (VB + 31) / 32 : (VB + NWC * 32 - 1) / (NWC * 32);
   const int who = small ? lane : threadIdx.x;
-  int64_t mine = 0, before = 0, total = 0;
+  int mine = 0, before = 0, total = 0;
   if (small) {
     int n[4];
 #pragma unroll
     for (int x = 0; x < 4; ++x) n[x] = x < chunk && who * chunk + x < VB ? span_of(p, who * chunk + x, C::COLS).units() : 0;
-    mine = ((int64_t)n[0] + n[1] + n[2] + n[3]) * p.c.Hkv;
+    mine = (n[0] + n[1] + n[2] + n[3]) * p.c.Hkv;
   } else {
     for (int vb = who * chunk; vb < min(VB, (who + 1) * chunk); ++vb)
-      mine += (int64_t)span_of(p, vb, C::COLS).units() * p.c.Hkv;
+      mine += span_of(p, vb, C::COLS).units() * p.c.Hkv;
   }
-  int64_t inc = mine;
+  int inc = mine;
 #pragma unroll
   for (int x = 1; x < 32; x *= 2) {
-    const int64_t up = __shfl_up_sync(0xFFFFFFFFu, inc, x);
+    const int up = __shfl_up_sync(0xFFFFFFFFu, inc, x);
     if (lane >= x) inc += up;
   }
   if (small) {
@@ -828,14 +841,14 @@ __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(
 
   // shares: as few warps of each CTA as give every one of them a tile, so small calls
   // spread over the SMs and no share between two others is empty
-  const int wpc = total >= (int64_t)gridDim.x * NWC ? NWC : max(1, ((int)total + (int)gridDim.x - 1) / (int)gridDim.x);
-  const int NW = (int)min(total, (int64_t)gridDim.x * wpc);
+  const int wpc = total >= (int)gridDim.x * NWC ? NWC : max(1, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+  const int NW = min(total, (int)gridDim.x * wpc);
   const Shares sh(total, NW);
   const int W = blockIdx.x * wpc + warp;
   const bool works = warp < wpc && W < NW;
   float* const entering = p.partials + (int64_t)(2 * blockIdx.x) * C::PART;   // the CTA's part of a segment begun before it
-  int64_t lo = works ? sh.first(W) : 0;
-  const int64_t hi = works ? sh.first(W + 1) : 0;
+  int lo = works ? sh.first(W) : 0;
+  const int hi = works ? sh.first(W + 1) : 0;
   // A warp's leading piece is the end of a segment that began before it, its open piece
   // the one that the loop leaves in `a`, of a segment that others share; -1: none.
   int seg_lead = -1, seg_open = -1;
@@ -848,7 +861,7 @@ __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(
 
   if (lo < hi) {
     int j = 0;                                         // the last chunk that begins at or before lo
-    int64_t acc;
+    int acc;
     if (small) {
       j = 31 - __clz(__ballot_sync(0xFFFFFFFFu, inc - mine <= lo));
       acc = __shfl_sync(0xFFFFFFFFu, inc - mine, j);
@@ -859,18 +872,18 @@ __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(
     }
     for (vb = j * chunk;; ++vb) {
       sp = span_of(p, vb, C::COLS);
-      const int64_t n = (int64_t)sp.units() * p.c.Hkv;
+      const int n = sp.units() * p.c.Hkv;
       if (lo < acc + n) break;
       acc += n;
     }
-    hkv = (int)quotient(lo - acc, sp.units());
-    unit = (int)(lo - acc - (int64_t)hkv * sp.units());
+    hkv = (int)((uint32_t)(lo - acc) / (uint32_t)sp.units());
+    unit = lo - acc - hkv * sp.units();
   }
 
   bool ok = true;
   while (lo < hi && ok) {
     const int b = p.CT == 1 ? vb : vb / p.CT, c0 = (vb - b * p.CT) * C::COLS;
-    const int unit1 = (int)min((int64_t)sp.units(), unit + (hi - lo));
+    const int unit1 = min(sp.units(), unit + (hi - lo));
     const int t0 = max(0, unit - EXTRA), t1 = max(0, unit1 - EXTRA);
     const int seg = vb * p.c.Hkv + hkv;
     lo += unit1 - unit;
@@ -946,7 +959,7 @@ __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(
 constexpr int JOIN_THREADS = 128, JOIN_Y = 4;
 template <int D, int NT>
 __global__ void __launch_bounds__(JOIN_THREADS) cache_join_kernel(const CacheAttnArgs p) {
-  constexpr int COLS = 8 * NT, PART = COLS * (D + 2), CY = COLS / JOIN_Y;
+  constexpr int COLS = 8 * NT, DP = D + 4, PART = COLS * (D + 6), CY = COLS / JOIN_Y;
   extern __shared__ float weights[];                     // [parts][CY]: M, then the weight of a part
   __shared__ float sums[CY][2];                          // M and the sum of a column
   griddep_wait();                                        // the first kernel's results are complete
@@ -960,7 +973,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_join_kernel(const CacheAtt
   auto part = [&](int k) { return parts + (k == 0 ? (int64_t)PART : (int64_t)2 * k * PART); };
   const Span sp = span_of(p, vb, COLS);
   if (c0 >= sp.qlen * p.G) return;
-  for (int x = threadIdx.x; x < n * CY; x += JOIN_THREADS) weights[x] = part(x / CY)[COLS * D + first + x % CY];
+  for (int x = threadIdx.x; x < n * CY; x += JOIN_THREADS) weights[x] = part(x / CY)[COLS * DP + first + x % CY];
   __syncthreads();
   if (threadIdx.x < CY * 32) {                           // a warp a column
     const int c = threadIdx.x / 32;
@@ -971,7 +984,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_join_kernel(const CacheAtt
     for (int k = lane; k < n; k += 32) {
       const float f = exp2f(weights[k * CY + c] - m);
       weights[k * CY + c] = f;
-      l = fmaf(f, part(k)[COLS * (D + 1) + first + c], l);
+      l = fmaf(f, part(k)[COLS * (DP + 1) + first + c], l);
     }
 #pragma unroll
     for (int x = 1; x < 32; x *= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
@@ -985,7 +998,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_join_kernel(const CacheAtt
 #pragma unroll 8
     for (int k = 0; k < n; ++k) {
       const float f = weights[k * CY + c];
-      const float2 v = *reinterpret_cast<const float2*>(part(k) + (first + c) * D + d);
+      const float2 v = *reinterpret_cast<const float2*>(part(k) + (first + c) * DP + d);
       o.x = fmaf(f, v.x, o.x);
       o.y = fmaf(f, v.y, o.y);
     }
@@ -1054,7 +1067,7 @@ int cache_attn_ntiles(int cols) { return cols <= 8 ? 1 : 2; }
 // parts of the CTAs, two each; where segments begin that go on
 size_t cache_attn_workspace(const Cache& c, int B, int H, int Sq, int max_pages, int sms, size_t* starts_at) {
   const int cols = Sq * (H / c.Hkv), nt = cache_attn_ntiles(cols);
-  *starts_at = (size_t)2 * sms * 8 * nt * (c.D + 2) * sizeof(float);
+  *starts_at = (size_t)2 * sms * 8 * nt * (c.D + 6) * sizeof(float);
   if (whole_segments(c, B, (cols + 8 * nt - 1) / (8 * nt), max_pages, sms)) return 0;
   return *starts_at + (size_t)sms * sizeof(int4);
 }
