@@ -152,6 +152,8 @@ __global__ void __launch_bounds__(CIO_WARPS * 32) cache_append_kernel(const Cach
   using Gr = CacheGroup<D, CF>;
   constexpr int L = D / 8, ROWS = 32 / L, BATCH = UNIT<D> / ROWS;      // rows at a time, times
   constexpr int PER = CF == CF_MX ? 4 : 2;                       // lanes of a block
+  griddep_launch();
+  griddep_wait();
   int b, ui, h;
   if (!my_item(a, units, b, ui, h)) return;
   const int fresh = a.which ? min(max(a.which[b], 0), a.S) : a.S;
@@ -211,6 +213,8 @@ __global__ void __launch_bounds__(CIO_WARPS * 32) cache_read_kernel(const CacheI
   using Gr = CacheGroup<D, CF>;
   constexpr int L = D / 8, ROWS = 32 / L, BATCH = UNIT<D> / ROWS;
   constexpr int PER = CF == CF_MX ? 4 : 2;
+  griddep_launch();
+  griddep_wait();
   int b, ui, h;
   if (!my_item(a, units, b, ui, h)) return;
   const int64_t start = a.which ? a.which[b] : 0, skip = start < 0 ? -start : 0;
@@ -257,26 +261,24 @@ cudaError_t launch_cache_append(const CacheIo& a, cudaStream_t st) {
   const unsigned grid = blocks_of(a);
   const int units = units_of(a);
   if (a.c.D == 128) {
-    if (a.c.cf == CF_MX) cache_append_kernel<128, CF_MX><<<grid, CIO_WARPS * 32, 0, st>>>(a, units);
-    else cache_append_kernel<128, CF_NV><<<grid, CIO_WARPS * 32, 0, st>>>(a, units);
+    if (a.c.cf == CF_MX) return launch_early(cache_append_kernel<128, CF_MX>, dim3(grid), CIO_WARPS * 32, 0, st, a, units);
+    else return launch_early(cache_append_kernel<128, CF_NV>, dim3(grid), CIO_WARPS * 32, 0, st, a, units);
   } else {
-    if (a.c.cf == CF_MX) cache_append_kernel<64, CF_MX><<<grid, CIO_WARPS * 32, 0, st>>>(a, units);
-    else cache_append_kernel<64, CF_NV><<<grid, CIO_WARPS * 32, 0, st>>>(a, units);
+    if (a.c.cf == CF_MX) return launch_early(cache_append_kernel<64, CF_MX>, dim3(grid), CIO_WARPS * 32, 0, st, a, units);
+    else return launch_early(cache_append_kernel<64, CF_NV>, dim3(grid), CIO_WARPS * 32, 0, st, a, units);
   }
-  return cudaGetLastError();
 }
 
 cudaError_t launch_cache_read(const CacheIo& a, cudaStream_t st) {
   const unsigned grid = blocks_of(a);
   const int units = units_of(a);
   if (a.c.D == 128) {
-    if (a.c.cf == CF_MX) cache_read_kernel<128, CF_MX><<<grid, CIO_WARPS * 32, 0, st>>>(a, units);
-    else cache_read_kernel<128, CF_NV><<<grid, CIO_WARPS * 32, 0, st>>>(a, units);
+    if (a.c.cf == CF_MX) return launch_early(cache_read_kernel<128, CF_MX>, dim3(grid), CIO_WARPS * 32, 0, st, a, units);
+    else return launch_early(cache_read_kernel<128, CF_NV>, dim3(grid), CIO_WARPS * 32, 0, st, a, units);
   } else {
-    if (a.c.cf == CF_MX) cache_read_kernel<64, CF_MX><<<grid, CIO_WARPS * 32, 0, st>>>(a, units);
-    else cache_read_kernel<64, CF_NV><<<grid, CIO_WARPS * 32, 0, st>>>(a, units);
+    if (a.c.cf == CF_MX) return launch_early(cache_read_kernel<64, CF_MX>, dim3(grid), CIO_WARPS * 32, 0, st, a, units);
+    else return launch_early(cache_read_kernel<64, CF_NV>, dim3(grid), CIO_WARPS * 32, 0, st, a, units);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace fsa

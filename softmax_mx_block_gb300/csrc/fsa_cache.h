@@ -81,6 +81,24 @@ struct CacheAttnArgs {
   uint64_t timeout_ns;
 };
 
+// Launch a kernel that begins with griddep_launch and griddep_wait (fsa_ptx.cuh): its blocks
+// may be set up while the stream's previous kernel still runs, and wait for its end
+// themselves.  Where the previous kernel is one of these too, that hides about 1 us.
+template <class... Params, class... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 cudaError_t launch_cache_append(const CacheIo& a, cudaStream_t st);
 cudaError_t launch_cache_read(const CacheIo& a, cudaStream_t st);
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, int sms, cudaStream_t st);

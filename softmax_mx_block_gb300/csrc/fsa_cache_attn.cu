@@ -34,23 +34,11 @@
 namespace fsa {
 namespace {
 
-#ifndef WHOLE_T1
-#define WHOLE_T1 24
-#endif
-#ifndef WHOLE_T2
-#define WHOLE_T2 64
-#endif
-#ifndef NW1
-#define NW1 12
-#endif
 // warps of a CTA, by the registers that a warp's columns take
 template <int D, int NT>
-__host__ __device__ constexpr int cta_warps() { return NT == 1 ? NW1 : D == 128 ? 8 : 12; }
+__host__ __device__ constexpr int cta_warps() { return NT == 1 || D == 64 ? 12 : 8; }
 constexpr int TILE = 32;            // keys of a tile
-#ifndef EXTRA_TILES
-#define EXTRA_TILES 2
-#endif
-constexpr int EXTRA = EXTRA_TILES;  // what a segment's start costs a warp, in tiles
+constexpr int EXTRA = 3;            // what a segment's start costs a warp, in tiles
 constexpr float M_NONE = -1e30f;    // maximum of no keys
 constexpr float LAZY = 4.0f;        // log2 of how far a score may beat M
 
@@ -727,19 +715,13 @@ struct Column {
 
 // Few short segments, or many: a CTA of 4 warps each, three CTAs an SM; no list, no second
 // kernel.  Block x is segment x.
-#ifndef WW
-#define WW 4
-#endif
-#ifndef WC
-#define WC 3
-#endif
-constexpr int WHOLE_WARPS = WW;
+constexpr int WHOLE_WARPS = 4;
 template <int D, int CF, int NT>
 struct WholeCfg {
   using C = Cfg<D, CF, NT>;
   static constexpr int RING = WHOLE_WARPS * C::STG * C::STAGE, JOIN = WHOLE_WARPS * C::PART * 4;
   static constexpr int SMEM = 1024 + WHOLE_WARPS * C::SCALES + (RING > JOIN ? RING : JOIN);
-  static constexpr int CTAS = NT == 2 && D == 128 ? (WC + 1) / 2 : WC;
+  static constexpr int CTAS = NT == 2 && D == 128 ? 2 : 3;
 };
 template <int D, int CF, int NT>
 __global__ void __launch_bounds__(WHOLE_WARPS * 32, WholeCfg<D, CF, NT>::CTAS) cache_attn_whole_kernel(const CacheAttnArgs p) {
@@ -752,13 +734,15 @@ __global__ void __launch_bounds__(WHOLE_WARPS * 32, WholeCfg<D, CF, NT>::CTAS) c
   uint8_t* const ring = smem + 1024 + WHOLE_WARPS * C::SCALES;
   const int warp = threadIdx.x >> 5;
   const AbortCtl ac{flag, p.status, p.timeout_ns};
+  griddep_launch();
+  if (threadIdx.x == 0) *flag = 0;
+  if (threadIdx.x < WHOLE_WARPS * STG) mbar_init(&bars[threadIdx.x], 1);
+  fence_mbar_init();
+  griddep_wait();                                       // before any tensor is read
   const int vb = blockIdx.x / p.c.Hkv, hkv = blockIdx.x - vb * p.c.Hkv;
   const int b = p.CT == 1 ? vb : vb / p.CT, c0 = (vb - b * p.CT) * C::COLS;
   const Span sp = span_of(p, vb, C::COLS);
   if (sp.tiles == 0) return;
-  if (threadIdx.x == 0) *flag = 0;
-  if (threadIdx.x < WHOLE_WARPS * STG) mbar_init(&bars[threadIdx.x], 1);
-  fence_mbar_init();
   __syncthreads();
   Ring r{bars + warp * STG, ring + warp * STG * C::STAGE, scales + warp * C::SCALES / 4, 0, 0, 0};
   Acc<D, CF, NT> a;
@@ -801,6 +785,7 @@ __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(
   if (threadIdx.x == 0) *flag = 0;
   if (threadIdx.x < NWC * STG) mbar_init(&bars[threadIdx.x], 1);
   fence_mbar_init();
+  griddep_wait();                                       // before any tensor is read
 
   // the list's length and its prefix sums.  Up to 4 virtual sequences a lane, every warp does
   // it by itself (no barrier, and the loads of a lane go out together); beyond, the CTA
@@ -936,7 +921,7 @@ __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(
     // whether it began in this CTA is known to its first warp, where it ends to its last
     const bool begins = w0 > 0 || ends->x != 0;
     const int rest = lead || w1 < active ? 0 : ends->y;
-    if (begins && rest > 0) start = make_int4(pc.y, sh.of(sh.first(blockIdx.x * wpc + w1) + rest - 1) / wpc, 0, 0);
+    if (begins && rest > 0) start = make_int4(pc.y, sh.of(sh.first(blockIdx.x * wpc + w1) + rest - 1) / wpc, pc.z, pc.w);
     const int vs = pc.y / p.c.Hkv, hs = pc.y - vs * p.c.Hkv;
     const int b = p.CT == 1 ? vs : vs / p.CT, c0 = (vs - b * p.CT) * C::COLS;
     const Span sg{pc.z, pc.w, 0, 0};
@@ -956,24 +941,39 @@ __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(
 // Joins the parts of the segments that several CTAs share.  Block (c, y) takes the one that
 // begins in CTA c and goes on, columns of the y-th quarter: CTA c's second part and the
 // first part of each later CTA up to the last.
-constexpr int JOIN_THREADS = 128, JOIN_Y = 4;
+constexpr int JOIN_THREADS = 128, JOIN_Y = 4, JOIN_AHEAD = 16;
 template <int D, int NT>
 __global__ void __launch_bounds__(JOIN_THREADS) cache_join_kernel(const CacheAttnArgs p) {
-  constexpr int COLS = 8 * NT, DP = D + 4, PART = COLS * (D + 6), CY = COLS / JOIN_Y;
-  extern __shared__ float weights[];                     // [parts][CY]: M, then the weight of a part
+  constexpr int COLS = 8 * NT, DP = D + 4, PART = COLS * (D + 6), CY = COLS / JOIN_Y, PER = CY * D / 2 / JOIN_THREADS + (CY * D / 2 < JOIN_THREADS);
+  extern __shared__ float weights[];                     // [parts][CY]: a part's maximum, then its weight; then its sums
   __shared__ float sums[CY][2];                          // M and the sum of a column
+  griddep_launch();
   griddep_wait();                                        // the first kernel's results are complete
-  const int4 st = p.starts[blockIdx.x];
+  const int4 st = p.starts[blockIdx.x];                  // segment, last CTA, its rows, its keys
   if (st.x < 0) return;
   const int lane = threadIdx.x & 31;
   const int vb = st.x / p.c.Hkv, hkv = st.x - vb * p.c.Hkv;
   const int b = p.CT == 1 ? vb : vb / p.CT, first = blockIdx.y * CY, c0 = (vb - b * p.CT) * COLS + first;
   const int n = st.y - (int)blockIdx.x + 1;
+  const Span sp{st.z, st.w, 0, 0};
+  if (c0 >= sp.qlen * p.G) return;
   const float* const parts = p.partials + (int64_t)2 * blockIdx.x * PART;
   auto part = [&](int k) { return parts + (k == 0 ? (int64_t)PART : (int64_t)2 * k * PART); };
-  const Span sp = span_of(p, vb, COLS);
-  if (c0 >= sp.qlen * p.G) return;
-  for (int x = threadIdx.x; x < n * CY; x += JOIN_THREADS) weights[x] = part(x / CY)[COLS * DP + first + x % CY];
+  // the first parts' rows set out together with all maxima and sums
+  float2 v[PER][JOIN_AHEAD];
+#pragma unroll
+  for (int y = 0; y < PER; ++y) {
+    const int x = threadIdx.x + y * JOIN_THREADS, c = x / (D / 2), d = 2 * (x % (D / 2));
+#pragma unroll
+    for (int k = 0; k < JOIN_AHEAD; ++k)
+      if (k < n && c < CY) v[y][k] = *reinterpret_cast<const float2*>(part(k) + (first + c) * DP + d);
+  }
+  float* const part_sums = weights + n * CY;
+  for (int x = threadIdx.x; x < n * CY; x += JOIN_THREADS) {
+    const float* const pk = part(x / CY) + first + x % CY;
+    weights[x] = pk[COLS * DP];
+    part_sums[x] = pk[COLS * (DP + 1)];
+  }
   __syncthreads();
   if (threadIdx.x < CY * 32) {                           // a warp a column
     const int c = threadIdx.x / 32;
@@ -984,23 +984,31 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_join_kernel(const CacheAtt
     for (int k = lane; k < n; k += 32) {
       const float f = exp2f(weights[k * CY + c] - m);
       weights[k * CY + c] = f;
-      l = fmaf(f, part(k)[COLS * (DP + 1) + first + c], l);
+      l = fmaf(f, part_sums[k * CY + c], l);
     }
 #pragma unroll
     for (int x = 1; x < 32; x *= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
     if (lane == 0) { sums[c][0] = m; sums[c][1] = l; }
   }
   __syncthreads();
-  for (int x = threadIdx.x; x < CY * D / 2; x += JOIN_THREADS) {
-    const int c = x / (D / 2), d = 2 * (x % (D / 2));
-    if (c0 + c >= sp.qlen * p.G) continue;
+#pragma unroll
+  for (int y = 0; y < PER; ++y) {
+    const int x = threadIdx.x + y * JOIN_THREADS, c = x / (D / 2), d = 2 * (x % (D / 2));
+    if (c >= CY || c0 + c >= sp.qlen * p.G) continue;
     float2 o = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < JOIN_AHEAD; ++k)
+      if (k < n) {
+        const float f = weights[k * CY + c];
+        o.x = fmaf(f, v[y][k].x, o.x);
+        o.y = fmaf(f, v[y][k].y, o.y);
+      }
 #pragma unroll 8
-    for (int k = 0; k < n; ++k) {
+    for (int k = JOIN_AHEAD; k < n; ++k) {
       const float f = weights[k * CY + c];
-      const float2 v = *reinterpret_cast<const float2*>(part(k) + (first + c) * DP + d);
-      o.x = fmaf(f, v.x, o.x);
-      o.y = fmaf(f, v.y, o.y);
+      const float2 u = *reinterpret_cast<const float2*>(part(k) + (first + c) * DP + d);
+      o.x = fmaf(f, u.x, o.x);
+      o.y = fmaf(f, u.y, o.y);
     }
     const Row row(p, b, hkv, c0 + c, sp, sums[c][0], sums[c][1]);
     row.put(p, d, o);
@@ -1014,7 +1022,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_join_kernel(const CacheAtt
 bool whole_segments(const Cache& c, int B, int CT, int max_pages, int sms) {
   const int64_t tiles = (((int64_t)max_pages << c.page_shift) + TILE - 1) / TILE;
   const int64_t segments = (int64_t)B * CT * c.Hkv;
-  return segments <= INT32_MAX && (tiles <= WHOLE_T1 || (tiles <= WHOLE_T2 && segments >= 2 * sms));
+  return segments <= INT32_MAX && (tiles <= 24 || (tiles <= 64 && segments >= 2 * sms));
 }
 
 // Opt in to the kernel's shared memory, once a device.
@@ -1039,25 +1047,14 @@ cudaError_t launch(const CacheAttnArgs& a, int sms, cudaStream_t st) {
     constexpr int smem = WholeCfg<D, CF, NT>::SMEM;
     e = allow_smem(cache_attn_whole_kernel<D, CF, NT>, smem, whole_ready);
     if (e != cudaSuccess) return e;
-    cache_attn_whole_kernel<D, CF, NT><<<a.B * a.CT * a.c.Hkv, WHOLE_WARPS * 32, smem, st>>>(a);
-    return cudaGetLastError();
+    return launch_early(cache_attn_whole_kernel<D, CF, NT>, dim3(a.B * a.CT * a.c.Hkv), WHOLE_WARPS * 32, smem, st, a);
   }
   e = allow_smem(cache_attn_kernel<D, CF, NT>, C::SMEM, list_ready);
   if (e != cudaSuccess) return e;
-  cache_attn_kernel<D, CF, NT><<<sms, C::NWC * 32, C::SMEM, st>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  // the second kernel's launch overlaps the first one's run; it waits for its results itself
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sms, JOIN_Y);
-  cfg.blockDim = dim3(JOIN_THREADS);
-  cfg.dynamicSmemBytes = (size_t)(sms + 2) * (C::COLS / JOIN_Y) * sizeof(float);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_join_kernel<D, NT>, a);
+  e = launch_early(cache_attn_kernel<D, CF, NT>, dim3(sms), C::NWC * 32, C::SMEM, st, a);
+  if (e != cudaSuccess) return e;
+  return launch_early(cache_join_kernel<D, NT>, dim3(sms, JOIN_Y), JOIN_THREADS,
+                      (size_t)2 * (sms + 2) * (C::COLS / JOIN_Y) * sizeof(float), st, a);
 }
 
 }  // namespace

@@ -182,6 +182,8 @@ template <int D, int P, bool INTER>
 __global__ void __launch_bounds__(ROPE_THREADS, ROPE_BLOCKS) qk_norm_rope_kernel(const RopeArgs a, int tokens) {
   constexpr int L = D / (2 * P), GROUPS = ROPE_THREADS / L;
   __shared__ __align__(16) float2 sines[ROPE_TOKENS * D / 2];     // cos, sin of [token][pair]
+  griddep_launch();
+  griddep_wait();
   const uint32_t total = (uint32_t)a.B * (uint32_t)a.S;
   const uint32_t first = blockIdx.x * (uint32_t)tokens;
   const int ntok = (int)min((uint32_t)tokens, total - first);
@@ -259,9 +261,9 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_BLOCKS) qk_norm_rope_kernel
 }
 
 template <int D, int P>
-void launch_rows(const RopeArgs& a, unsigned grid, int tokens, cudaStream_t st) {
-  if (a.interleaved) qk_norm_rope_kernel<D, P, true><<<grid, ROPE_THREADS, 0, st>>>(a, tokens);
-  else qk_norm_rope_kernel<D, P, false><<<grid, ROPE_THREADS, 0, st>>>(a, tokens);
+cudaError_t launch_rows(const RopeArgs& a, unsigned grid, int tokens, cudaStream_t st) {
+  return launch_early(a.interleaved ? qk_norm_rope_kernel<D, P, true> : qk_norm_rope_kernel<D, P, false>, dim3(grid),
+                      ROPE_THREADS, 0, st, a, tokens);
 }
 
 }  // namespace
@@ -278,14 +280,8 @@ cudaError_t launch_qk_norm_rope(const RopeArgs& a, int sms, cudaStream_t st) {
   int tokens = ROPE_THREADS / (a.D / (wide ? 16 : 8)) / 4;
   while (tokens > 1 && 2 * total < 3 * (int64_t)tokens * sms) tokens /= 2;
   const unsigned grid = (unsigned)((total + tokens - 1) / tokens);
-  if (a.D == 128) {
-    if (wide) launch_rows<128, 8>(a, grid, tokens, st);
-    else launch_rows<128, 4>(a, grid, tokens, st);
-  } else {
-    if (wide) launch_rows<64, 8>(a, grid, tokens, st);
-    else launch_rows<64, 4>(a, grid, tokens, st);
-  }
-  return cudaGetLastError();
+  if (a.D == 128) return wide ? launch_rows<128, 8>(a, grid, tokens, st) : launch_rows<128, 4>(a, grid, tokens, st);
+  return wide ? launch_rows<64, 8>(a, grid, tokens, st) : launch_rows<64, 4>(a, grid, tokens, st);
 }
 
 }  // namespace fsa
