@@ -17,38 +17,36 @@ constexpr int CIO_WARPS = 8;
 template <int D>
 constexpr int UNIT = 1024 / D;     // tokens of a warp: 8 or 16
 
-// A warp's rows r0 <= r < r1 of a group: rows r - shift of sequence b's tensor.
+// A warp's rows r0 <= r < r1 of the group that begins at pos: rows r - shift of its tensor,
+// counted from the first position asked for.
 struct Group {
-  uint8_t* at;             // null: no page
-  int b, h, r0, r1;
-  int64_t shift;
+  int64_t pos, shift;
+  int r0, r1;
 };
 
 // Unit ui of the sequence, counted from the one that holds its first position; false if none
 // of its rows is asked for.  `first`, `count`: the positions asked for.
 template <int U>
-__device__ __forceinline__ bool find_group(const CacheIo& a, int64_t first, int64_t count, int b, int ui, int h, int group_bytes,
-                                           Group& g) {
-  const int64_t at = ((first > 0 ? first : 0) / U + ui) * U, pos = at & ~15ll;      // the unit's first position, its group's
-  const int u0 = (int)(at - pos);
-  const int64_t lo = first - pos, hi = first + count - pos;
-  g.r0 = (int)max((int64_t)u0, lo);
-  g.r1 = (int)min((int64_t)(u0 + U), hi);
-  if (g.r0 >= g.r1) return false;
-  g.b = b;
-  g.h = h;
-  g.shift = lo;
-  g.at = nullptr;
+__device__ __forceinline__ bool find_rows(int64_t first, int64_t count, int ui, Group& g) {
+  const int64_t at = ((first > 0 ? first : 0) / U + ui) * U;      // the unit's first position
+  g.pos = at & ~15ll;
+  const int u0 = (int)(at - g.pos);
+  g.shift = first - g.pos;
+  g.r0 = (int)max((int64_t)u0, g.shift);
+  g.r1 = (int)max((int64_t)0, min((int64_t)(u0 + U), g.shift + count));
+  return g.r0 < g.r1;
+}
+// Its group in the pool, or null.
+__device__ __forceinline__ uint8_t* find_page(const CacheIo& a, int b, int h, int64_t pos, int group_bytes) {
   const int64_t pi = pos >> a.c.page_shift;
-  if (pi >= a.max_pages) return true;
+  if (pi >= a.max_pages) return nullptr;
   const int page = a.table[(int64_t)b * a.max_pages + pi];
   if (page < 0 || page >= a.c.num_pages) {
     if (a.status && (threadIdx.x & 31) == 0) atomicExch(a.status, -1);       // FSA_ERR_INVALID_ARG
-    return true;
+    return nullptr;
   }
   const int inside = (int)(pos & ((1 << a.c.page_shift) - 1)) / 16;
-  g.at = a.c.pages + page * a.c.page_bytes + (((int64_t)h << (a.c.page_shift - 4)) + inside) * group_bytes;
-  return true;
+  return a.c.pages + page * a.c.page_bytes + (((int64_t)h << (a.c.page_shift - 4)) + inside) * group_bytes;
 }
 
 // Which of the launch's units this warp has: units of a sequence, then heads, fastest last.
@@ -160,7 +158,7 @@ __global__ void __launch_bounds__(CIO_WARPS * 32) cache_append_kernel(const Cach
   // positions below 0 are dropped: the first of them is 0 then, and row 0 is `skip`
   const int64_t first = (int64_t)a.lens[b] - fresh, skip = first < 0 ? -first : 0;
   Group g;
-  if (!find_group<UNIT<D>>(a, first + skip, fresh - skip, b, ui, h, Gr::BYTES, g) || !g.at) return;
+  if (!find_rows<UNIT<D>>(first + skip, fresh - skip, ui, g)) return;
   const int lane = threadIdx.x & 31, l = lane % L, row = lane - l;
   const uint16_t* const ksrc = a.k + b * a.ks.b + h * a.ks.h + (skip - g.shift) * a.ks.s + 8 * l;
   const uint16_t* const vsrc = a.v + b * a.vs.b + h * a.vs.h + (skip - g.shift) * a.vs.s + 8 * l;
@@ -173,18 +171,21 @@ __global__ void __launch_bounds__(CIO_WARPS * 32) cache_append_kernel(const Cach
     ku[x] = in ? *reinterpret_cast<const uint4*>(ksrc + r * a.ks.s) : make_uint4(0u, 0u, 0u, 0u);
     vu[x] = in ? *reinterpret_cast<const uint4*>(vsrc + r * a.vs.s) : make_uint4(0u, 0u, 0u, 0u);
   }
+  uint8_t* const at = find_page(a, b, h, g.pos, Gr::BYTES);      // while they are on their way
+  if (!at) return;
 #pragma unroll
   for (int x = 0; x < BATCH; ++x) {
+    if (base + x * ROWS >= g.r1 || base + (x + 1) * ROWS <= g.r0) continue;      // a single token: one of these has it
     const int r = base + x * ROWS + lane / L;
     uint32_t ksb, vsb;
     const uint32_t kw = k_to_cache<L>(quantise8<CF>(ku[x], ksb), row, l);
     const uint32_t vw = v_to_cache<L>(quantise8<CF>(vu[x], vsb), row, l);
     if (r >= g.r0 && r < g.r1) {
-      *reinterpret_cast<uint32_t*>(g.at + Gr::K + r * (D / 2) + 4 * l) = kw;
-      *reinterpret_cast<uint32_t*>(g.at + Gr::V + r * (D / 2) + 4 * l) = vw;
+      *reinterpret_cast<uint32_t*>(at + Gr::K + r * (D / 2) + 4 * l) = kw;
+      *reinterpret_cast<uint32_t*>(at + Gr::V + r * (D / 2) + 4 * l) = vw;
       if (l % PER == 0) {
-        g.at[Gr::KS + r * Gr::SB + l / PER] = (uint8_t)ksb;
-        g.at[Gr::VS + r * Gr::SB + l / PER] = (uint8_t)vsb;
+        at[Gr::KS + r * Gr::SB + l / PER] = (uint8_t)ksb;
+        at[Gr::VS + r * Gr::SB + l / PER] = (uint8_t)vsb;
       }
     }
   }
@@ -219,7 +220,8 @@ __global__ void __launch_bounds__(CIO_WARPS * 32) cache_read_kernel(const CacheI
   if (!my_item(a, units, b, ui, h)) return;
   const int64_t start = a.which ? a.which[b] : 0, skip = start < 0 ? -start : 0;
   Group g;
-  if (!find_group<UNIT<D>>(a, start + skip, min((int64_t)a.S, (int64_t)a.lens[b] - start) - skip, b, ui, h, Gr::BYTES, g)) return;
+  if (!find_rows<UNIT<D>>(start + skip, min((int64_t)a.S, (int64_t)a.lens[b] - start) - skip, ui, g)) return;
+  const uint8_t* const at = find_page(a, b, h, g.pos, Gr::BYTES);
   const int lane = threadIdx.x & 31, l = lane % L, row = lane - l;
   const int base = g.r0 / UNIT<D> * UNIT<D>;
   uint32_t kw[BATCH], vw[BATCH], ks[BATCH], vs[BATCH];
@@ -227,15 +229,16 @@ __global__ void __launch_bounds__(CIO_WARPS * 32) cache_read_kernel(const CacheI
   for (int x = 0; x < BATCH; ++x) {
     const int r = base + x * ROWS + lane / L;
     kw[x] = vw[x] = ks[x] = vs[x] = 0;
-    if (g.at) {
-      kw[x] = *reinterpret_cast<const uint32_t*>(g.at + Gr::K + r * (D / 2) + 4 * l);
-      vw[x] = *reinterpret_cast<const uint32_t*>(g.at + Gr::V + r * (D / 2) + 4 * l);
-      ks[x] = g.at[Gr::KS + r * Gr::SB + l / PER];
-      vs[x] = g.at[Gr::VS + r * Gr::SB + l / PER];
+    if (at) {
+      kw[x] = *reinterpret_cast<const uint32_t*>(at + Gr::K + r * (D / 2) + 4 * l);
+      vw[x] = *reinterpret_cast<const uint32_t*>(at + Gr::V + r * (D / 2) + 4 * l);
+      ks[x] = at[Gr::KS + r * Gr::SB + l / PER];
+      vs[x] = at[Gr::VS + r * Gr::SB + l / PER];
     }
   }
 #pragma unroll
   for (int x = 0; x < BATCH; ++x) {
+    if (base + x * ROWS >= g.r1 || base + (x + 1) * ROWS <= g.r0) continue;
     const int r = base + x * ROWS + lane / L;
     const int64_t s = skip + r - g.shift;
     const bool in = r >= g.r0 && r < g.r1;

@@ -204,6 +204,31 @@ def test_bad_pages_are_not_followed():
     check_attention(q, cache, table, [32, 32], [3, 3], True, D ** -0.5, out, lse, torch.zeros_like(out))
 
 
+def test_lengths_out_of_range():
+    """Lengths and starts at the ends of int32 ask for nothing: nothing is read, written or
+    attended (a row that sees nothing is zero), whatever the sum of the two would wrap to."""
+    fsa = _fsa()
+    g = gen(15)
+    Hkv, D, page, S, top = 2, 128, 16, 5, 2 ** 31
+    cache, table, k, v = filled_cache(fsa, g, [40], page, Hkv, D, "NVFP4", junk=0x11)
+    before = cache.pages.clone()
+    x = normal(g, 1, S, Hkv, D)
+    for n, m in ((-top, S), (-1, S), (0, 0), (40, -top), (40, -1), (top - 1, S), (-top, top - 1)):
+        fsa.fsa_cache_append(cache, x, x, table, i32([n]), i32([m]))
+        if not (n == top - 1 or (n == 40 and m > 0)):
+            assert torch.equal(cache.pages, before), (n, m)
+    assert torch.equal(cache.pages, before)          # positions behind the table are dropped
+    for n, start in ((-top, top - 1), (-top, 0), (0, -top), (40, top - 1), (-top + 3, top - 1), (-top + 9, top - 8), (40, -top)):
+        base = torch.full((1, S, Hkv, D), 5.0, dtype=torch.bfloat16, device="cuda")
+        fsa.fsa_cache_read(cache, table, i32([n]), start=i32([start]), k_out=base)
+        assert bool((base == 5.0).all()), (n, start)
+    q = normal(g, 1, 3, 4, D)
+    for n, m in ((-top, 3), (-5, top - 1), (-top, -top), (top - 1, -1)):
+        out = torch.full((1, 3, 4, D), 2.0, device="cuda")
+        fsa.fsa_attention_cache(q, cache, table, i32([n]), q_lens=i32([m]), out=out)
+        assert bool((out == (0.0 if m > 0 else 2.0)).all()), (n, m)
+
+
 # ---------------------------------------------------------------------------- the attention
 def check_attention(q, cache, table, lens, q_lens, causal, scale, out, lse, before):
     B, Sq, H, D = q.shape
