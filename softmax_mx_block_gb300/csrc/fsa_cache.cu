@@ -59,52 +59,52 @@ __device__ __forceinline__ bool my_item(const CacheIo& a, int units, int& b, int
   return b < a.B;
 }
 
-// NaN-keeping magnitude: NaN and Inf become Inf, so that fmaxf passes them on
-__device__ __forceinline__ float magnitude(float x) {
-  const float a = fabsf(x);
-  return a <= 3.4e38f ? a : __uint_as_float(0x7F800000u);
-}
+// Cut to 12 fraction bits: a quotient that was raised by 2^-21 to 2^-19 of it becomes a tie
+// again where it was one (see below).
+__device__ __forceinline__ float cut12(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFFF800u); }
 
 // 8 consecutive elements of a row, D/8 lanes a row: their codes, element 0 in the lowest
-// nibble, and their block's scale byte.
+// nibble, and their block's scale byte.  The block's maximum is taken on the bf16 patterns
+// (as integers they are ordered as their magnitudes, Inf and NaN above all).
+//
+// Quotients without a division: amax / 6 and x / s are rounded to a few bits next, to the
+// nearest with ties to even.  bf16 has 8 significant bits, E4M3 4 and 6 is 3 * 2, so a
+// quotient is a tie or at least 2^-10 of it away from one.  The product with a reciprocal
+// raised by 2^-20 lies above the quotient by 2^-21 to 2^-19 of it; cut to 12 fraction bits, a
+// tie is that tie and the others stay on their side.  (The same bytes as the divisions of
+// fsa_mx_quantize for every pair of a bf16 value and a scale.)
 template <int CF>
 __device__ __forceinline__ uint32_t quantise8(uint4 u, uint32_t& sb) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  float x[8], m = 0.f;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    x[2 * e] = __uint_as_float(w[e] << 16);
-    x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-    m = fmaxf(m, fmaxf(magnitude(x[2 * e]), magnitude(x[2 * e + 1])));
-  }
-  m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));              // 16 elements
+  constexpr uint32_t MAG = 0x7FFF7FFFu;
+  uint32_t m = __vmaxu2(__vimax3_u16x2(u.x & MAG, u.y & MAG, u.z & MAG), u.w & MAG);
+  m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));           // 16 elements
+  if constexpr (CF == CF_MX) m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));    // 32
+  m = max(m & 0xFFFFu, m >> 16);
+  const bool finite = m < 0x7F80u;
   float mul;
   if constexpr (CF == CF_MX) {
-    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));            // 32
-    sb = block_scale_byte(m, 2);
-    mul = pow2_neg((int)sb - 127);
-    if (sb == 0xFFu) return 0u;
+    sb = finite ? (uint32_t)max((int)(m >> 7) - 2, 0) : 0xFFu;   // exponent of amax, less 2 (zero and subnormal: 0)
+    mul = __uint_as_float((254u - min(sb, 254u)) << 23);
+    if (!finite) return 0u;
   } else {
-    sb = nvfp4_scale_byte(m, m > 3.4e38f);
+    sb = finite ? cvt_e4m3x2(cut12(__uint_as_float(m << 16) * (0.16666667163372039795f * (1.0f + 0x1p-20f))), 0.f) & 0xFFu : 0x7Fu;
     const float s = e4m3_to_f32(sb);
     if (!(s > 0.0f)) return 0u;                                  // zero or NaN
-    // The code nearest x / s, ties to even.  x has 8 significant bits and s has 4, so x / s
-    // either is a tie (0.25, 0.75, .. 5) or is at least 2^-10 of it away from it.  The
-    // product with a reciprocal raised by 2^-20 lies above x / s by 2^-21 to 2^-19 of it;
-    // cut to 12 fraction bits, a tie is that tie and the others stay on their side.
-    mul = __frcp_rn(s) * (1.0f + 0x1p-20f);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(mul) : "f"(s));
+    mul *= 1.0f + 0x1p-20f;
   }
-  uint32_t codes = 0;
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  float x[8];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    float lo = __fmul_rn(x[2 * e], mul), hi = __fmul_rn(x[2 * e + 1], mul);
+    x[2 * e] = __uint_as_float(w[e] << 16) * mul;
+    x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u) * mul;
     if constexpr (CF == CF_NV) {
-      lo = __uint_as_float(__float_as_uint(lo) & 0xFFFFF800u);
-      hi = __uint_as_float(__float_as_uint(hi) & 0xFFFFF800u);
+      x[2 * e] = cut12(x[2 * e]);
+      x[2 * e + 1] = cut12(x[2 * e + 1]);
     }
-    codes |= cvt_e2m1x2(lo, hi) << (8 * e);
   }
-  return codes;
+  return cvt_e2m1x8(x);
 }
 
 // The exchanges between the two orders of a row's codes.  lane = l of a row of L = D/8 lanes

@@ -121,6 +121,41 @@ def test_append_matches_the_row_quantiser(fmt):
     assert torch.equal(kc.flatten(0, 1), codes) and torch.equal(vc.flatten(0, 1), codes)
 
 
+def test_every_value_under_every_scale():
+    """NVFP4 codes and scales of every finite bf16 value as a block's maximum, and of every
+    significand under every scale (the divisions that the kernel does not do): as
+    fsa_mx_quantize."""
+    fsa = _fsa()
+    bits = torch.arange(0x7F80, dtype=torch.int32, device="cuda")
+    tops = (bits | (bits % 2 << 15)).to(torch.int16).view(torch.bfloat16)        # either sign
+    g = gen(2)
+    blocks = [tops[:, None].expand(-1, 16) * torch.rand(len(tops), 16, generator=g, device="cuda").to(torch.bfloat16)]
+    blocks[0] = blocks[0].clone()
+    blocks[0][:, 3] = tops
+    # maxima 6 s for all scales s, with 15 values of every significand and exponent below it
+    s = torch.tensor([ref.scale_values(torch.tensor([b], dtype=torch.uint8), "NVFP4").item() for b in range(1, 127)], device="cuda")
+    sig = torch.arange(128, 256, device="cuda", dtype=torch.float64) / 128
+    vals = (sig[None, :] * torch.exp2(torch.arange(-5, 3, device="cuda", dtype=torch.float64))[:, None]).flatten()   # x / s near 0.06 .. 8
+    x = (s[:, None].double() * 1.0).log2().floor().exp2() * vals[None, :]
+    x = torch.minimum(x, 6 * s[:, None].double()).reshape(len(s), -1)
+    x = torch.nn.functional.pad(x, (0, -x.shape[1] % 15)).reshape(len(s), -1, 15)
+    blocks.append(torch.cat(((6 * s)[:, None, None].expand(-1, x.shape[1], 1), x), dim=2).reshape(-1, 16).to(torch.bfloat16))
+    flat = torch.cat([b.flatten() for b in blocks])
+    n = -(-flat.numel() // (128 * 128)) * 128
+    k = torch.nn.functional.pad(flat, (0, n * 128 - flat.numel())).reshape(1, n, 1, 128)
+    cache = fsa.empty_cache(n // 128, 128, 1, 128, "NVFP4")
+    table = torch.arange(n // 128, device="cuda", dtype=torch.int32)[None]
+    fsa.fsa_cache_append(cache, k, k, table, i32([n]))
+    m = fsa.fsa_mx_quantize(k.transpose(1, 2).contiguous(), fsa.FSA_MX_ROWS, "NVFP4")
+    rows = m.codes.reshape(n, 64)
+    codes = torch.stack((rows & 15, rows >> 4), dim=-1).flatten(-2)
+    r, b = torch.arange(n, device="cuda")[:, None], torch.arange(8, device="cuda")[None]
+    scales = m.scales.reshape(n // 128, 2, 512)[r // 128, b // 4, r % 32 * 16 + r % 128 // 32 * 4 + b % 4]
+    kc, ks, vc, vs = ref.unpack_pages(cache.pages, 128, 1, 128, "NVFP4")
+    for c, sc in ((kc, ks), (vc, vs)):
+        assert torch.equal(sc.reshape(n, 8), scales) and torch.equal(c.reshape(n, 128), codes)
+
+
 @pytest.mark.parametrize("fmt", ["E2M1", "NVFP4"])
 def test_nonfinite_blocks(fmt):
     fsa = _fsa()
