@@ -661,51 +661,56 @@ __device__ __forceinline__ void put_rows(const CacheAttnArgs& p, const Span& sp,
     }
 }
 
-// One column of n <= 32 parts joined by a warp: a lane weighs part `lane`, and has dims
-// 64x + 2 lane and the next of the sum.
+// One column of n <= 16 parts joined by half a warp: a lane weighs part `lane`, and has dims
+// 4 (16x + lane) .. + 3 of the sum.  Both halves run it together, on columns of their own.
 template <int D, int COLS>
 struct Column {
   static constexpr int DP = D + 4;
   float m, l;
-  float2 o[D / 64];
+  float4 o[D / 64];
   template <class Part>
   __device__ __forceinline__ Column(Part part, int n, int col) {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 15;
     const float* const mine = part(min(lane, n - 1));
     const float mk = lane < n ? mine[COLS * DP + col] : M_NONE * 4.f;
     l = lane < n ? mine[COLS * (DP + 1) + col] : 0.f;
     m = mk;
 #pragma unroll
-    for (int x = 1; x < 32; x *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+    for (int x = 1; x < 16; x *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
     const float w = lane < n ? exp2f(mk - m) : 0.f;
     l = lane < n ? l * w : 0.f;
 #pragma unroll
-    for (int x = 1; x < 32; x *= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
+    for (int x = 1; x < 16; x *= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
 #pragma unroll
-    for (int x = 0; x < D / 64; ++x) o[x] = make_float2(0.f, 0.f);
+    for (int x = 0; x < D / 64; ++x) o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int k = 0; k < n; ++k) {
-      const float* const pk = part(k) + col * DP + 2 * lane;
-      const float f = __shfl_sync(0xFFFFFFFFu, w, k);
+      const float* const pk = part(k) + col * DP + 4 * lane;
+      const float f = __shfl_sync(0xFFFFFFFFu, w, k, 16);
 #pragma unroll
       for (int x = 0; x < D / 64; ++x) {
-        const float2 v = *reinterpret_cast<const float2*>(pk + 64 * x);
+        const float4 v = *reinterpret_cast<const float4*>(pk + 64 * x);
         o[x].x = fmaf(f, v.x, o[x].x);
         o[x].y = fmaf(f, v.y, o[x].y);
+        o[x].z = fmaf(f, v.z, o[x].z);
+        o[x].w = fmaf(f, v.w, o[x].w);
       }
     }
   }
   __device__ __forceinline__ void put_row(const CacheAttnArgs& p, const Span& sp, int b, int hkv, int col) const {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 15;
     const Row row(p, b, hkv, col, sp, m, l);
 #pragma unroll
-    for (int x = 0; x < D / 64; ++x) row.put(p, 64 * x + 2 * lane, o[x]);
+    for (int x = 0; x < D / 64; ++x) {
+      row.put(p, 64 * x + 4 * lane, make_float2(o[x].x, o[x].y));
+      row.put(p, 64 * x + 4 * lane + 2, make_float2(o[x].z, o[x].w));
+    }
     if (lane == 0) row.put_lse(p);
   }
   __device__ __forceinline__ void put_part(float* part, int col) const {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 15;
 #pragma unroll
-    for (int x = 0; x < D / 64; ++x) *reinterpret_cast<float2*>(part + col * DP + 64 * x + 2 * lane) = o[x];
+    for (int x = 0; x < D / 64; ++x) *reinterpret_cast<float4*>(part + col * DP + 64 * x + 4 * lane) = o[x];
     if (lane == 0) {
       part[COLS * DP + col] = m;
       part[COLS * (DP + 1) + col] = l;
@@ -713,8 +718,8 @@ struct Column {
   }
 };
 
-// Few short segments, or many: a CTA of 4 warps each, three CTAs an SM; no list, no second
-// kernel.  Block x is segment x.
+// Short segments: a CTA of 4 warps each, three CTAs an SM; no list, no second kernel.  Block x
+// is segment x.
 constexpr int WHOLE_WARPS = 4;
 template <int D, int CF, int NT>
 struct WholeCfg {
@@ -758,9 +763,10 @@ __global__ void __launch_bounds__(WHOLE_WARPS * 32, WholeCfg<D, CF, NT>::CTAS) c
   if (warp < n && ok) put_part<D, CF, NT>(parts + warp * C::PART, a);
   __syncthreads();
   if (lds_vol(flag)) return;                            // a wait ran out: the status word says so
-  for (int col = warp; col < C::COLS && c0 + col < sp.qlen * p.G; col += WHOLE_WARPS) {
-    const Column<D, C::COLS> col_sum([&](int k) { return parts + k * C::PART; }, n, col);
-    col_sum.put_row(p, sp, b, hkv, c0 + col);
+  const int cols = min(C::COLS, sp.qlen * p.G - c0), half = (threadIdx.x >> 4) & 1;
+  for (int first = 2 * warp; first < cols; first += 2 * WHOLE_WARPS) {
+    const Column<D, C::COLS> sum([&](int k) { return parts + k * C::PART; }, n, first + half);
+    if (first + half < cols) sum.put_row(p, sp, b, hkv, c0 + first + half);
   }
 }
 
@@ -896,7 +902,7 @@ __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(
     next();
   }
 
-  // Join the pieces of each segment that the CTA's warps share, a column a warp.  A segment
+  // Join the pieces of each segment that the CTA's warps share, a column half a warp.  A segment
   // that began and ends in this CTA is written; one that came from the CTA before, or goes
   // on to the next, is a part for the second kernel.
   __syncthreads();                                      // every ring is done with
@@ -925,12 +931,14 @@ __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(
     const int vs = pc.y / p.c.Hkv, hs = pc.y - vs * p.c.Hkv;
     const int b = p.CT == 1 ? vs : vs / p.CT, c0 = (vs - b * p.CT) * C::COLS;
     const Span sg{pc.z, pc.w, 0, 0};
-    const int cols = min(C::COLS, sg.qlen * p.G - c0);
-    int col = warp - turn;                              // the columns of all segments in turn
-    if (col < 0) col += NWC;
-    turn = (turn + cols) % NWC;
-    for (; col < cols; col += NWC) {
+    const int cols = min(C::COLS, sg.qlen * p.G - c0), half = lane >> 4;
+    int first = warp - turn;                            // pairs of columns of all segments in turn
+    if (first < 0) first += NWC;
+    turn = (turn + (cols + 1) / 2) % NWC;
+    for (first *= 2; first < cols; first += 2 * NWC) {
+      const int col = first + half;                     // (COLS is even: column `cols` lies in the parts)
       const Column<D, C::COLS> sum([&](int k) { return w0 + k < w1 ? parts + (w0 + k) * C::PART : leads + w1 * C::PART; }, n, col);
+      if (col >= cols) continue;
       if (begins && rest == 0) sum.put_row(p, sg, b, hs, c0 + col);
       else sum.put_part(begins ? p.partials + (int64_t)(2 * blockIdx.x + 1) * C::PART : entering, col);
     }
@@ -1016,13 +1024,15 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_join_kernel(const CacheAtt
   }
 }
 
-// Which kernel: segments of at most 24 tiles, or of at most 64 when there are two or more
-// for each SM, go to a CTA each; else the list is split evenly.  (The table's width bounds
-// a segment's tiles; the lengths are on the device.)
+// Which kernel: a CTA for each segment where none is longer than 24 tiles and there are at most
+// 8 an SM, else the list split evenly.  (The table's width bounds a segment's tiles; the
+// lengths are on the device.)  Measured, list / whole, us, 8 kv heads of 128 dims, E2M1:
+//   1 sequence of 100, 760, 1500 keys: 8.6 / 4.0, 9.0 / 8.4, 9.5 / 13.3
+//   64 sequences of 100, 760, 1500 keys: 13.0 / 8.3, 23.1 / 19.7, 33.1 / 31.7
+//   256 sequences of 1 to 100, 1 to 760: 17.5 / 18.3, 24.0 / 28.1 (2048 segments)
 bool whole_segments(const Cache& c, int B, int CT, int max_pages, int sms) {
   const int64_t tiles = (((int64_t)max_pages << c.page_shift) + TILE - 1) / TILE;
-  const int64_t segments = (int64_t)B * CT * c.Hkv;
-  return segments <= INT32_MAX && (tiles <= 24 || (tiles <= 64 && segments >= 2 * sms));
+  return tiles <= 24 && (int64_t)B * CT * c.Hkv <= 8 * (int64_t)sms;
 }
 
 // Opt in to the kernel's shared memory, once a device.
