@@ -473,12 +473,15 @@ int fsa_cache_read(const fsa_cache* cache, void* k, void* v, const fsa_strides* 
  * prompt): O = softmax(scale Q K^T) V on the values the cache stands for; q is not
  * quantised, sums and softmax statistics are fp32, probabilities times V's scales are
  * rounded to f16 before the product with the codes of V (2^-11 relative, 2^-10 with
- * NVFP4; an absolute 2^-33 of the largest for those far below it).  Query head h reads kv head h / (H/Hkv).  Row i < q_lens[b] of sequence b
+ * NVFP4; an absolute 2^-33 of the largest for those far below it, with NVFP4
+ * block scales over 8 in V times the scale).  Query head h reads kv head h / (H/Hkv).  Row i < q_lens[b] of sequence b
  * stands at position lens[b] - q_lens[b] + i and sees the keys up to its own position
  * (causal) or all lens[b]; lens counts the rows' own tokens, which are in the cache
  * already.  A row that sees nothing gives zeros (lse -inf).  Rows behind q_lens[b] are not
  * written.  The lengths are read on the device: a captured call follows them.
  *   q, out: [B][Sq][H][D] strided, 16-byte aligned; out bf16 or fp32 by out_dtype
+ *   scale: of any sign, |scale| <= 1e30; keys of magnitudes up to 2^115 (beyond, fp32 scores
+ *     may overflow)
  *   lse: optional fp32 [B][Sq][H], natural log of the sum of exp(scale q k)
  *   lens: int32 [B], cut to max_pages * page_size; q_lens: int32 [B], cut to 0..Sq, or NULL (Sq)
  *   workspace: fsa_attention_cache_workspace bytes, 16-byte aligned; needs no initial

@@ -578,6 +578,14 @@ def _raw(stream):
     return None if stream is None else stream.cuda_stream
 
 
+def _new(make, shape, dtype, device, stream):
+    """A tensor that a call on `stream` (None: the current one) writes, made on that stream."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
 def fsa_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor | None, inv_freq: torch.Tensor | None, *,
                      sections=None, q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
                      norm=True, eps=1e-6, interleaved=False, q_out: torch.Tensor | None = None,
@@ -587,9 +595,9 @@ def fsa_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor | None,
     sections: pairs of each axis (default: all of one).  q_out, k_out default to contiguous
     tensors of q's and k's shapes; q and k themselves rotate in place.  Returns (q_out, k_out)."""
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = _new(torch.empty, q.shape, q.dtype, q.device, stream)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        k_out = _new(torch.empty, k.shape, k.dtype, k.device, stream)
     (_torch_module or _serving()).norm_rope(q, k, pos, inv_freq, None if sections is None else tuple(sections), q_weight,
                                             k_weight, norm, eps, interleaved, q_out, k_out, _raw(stream))
     return q_out, k_out
@@ -624,7 +632,8 @@ def fsa_cache_append(cache: MxCache, k: torch.Tensor, v: torch.Tensor, block_tab
                      new_lens: torch.Tensor | None = None, *, status: torch.Tensor | None = None, stream=None) -> None:
     """Quantise k, v (bf16 [B,S,Hkv,D], strided) into the cache: row i < new_lens[b] (default
     all S) becomes token lens[b] - new_lens[b] + i of the sequence whose pages row b of
-    block_table (int32 [B, max_pages]) names.  lens (int32 [B]) counts the new tokens too."""
+    block_table (int32 [B, max_pages]) names.  lens (int32 [B]) counts the new tokens too.
+    status: int32 [1], set where a page number lies outside the pool (the token is dropped)."""
     c = cache
     (_torch_module or _serving()).cache_append(c.pages, c.page_size, c.Hkv, c.D, c.fmt, k, v, block_table, lens, new_lens,
                                                status, _raw(stream))
@@ -635,14 +644,16 @@ def fsa_cache_read(cache: MxCache, block_table: torch.Tensor, lens: torch.Tensor
                    v_out: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> tuple:
     """The values the cache stands for: row i of sequence b is token start[b] + i (default
     start 0) where that lies before lens[b]; other rows are left as they were.  k_out, v_out:
-    bf16 [B,S,Hkv,D], strided; without either, both are made (zeros, S rows).  Returns
+    bf16 [B,S,Hkv,D], strided; without either, both are made (zeros, S rows).  status: int32
+    [1], set where a page number lies outside the pool (the token reads as zeros).  Returns
     (k_out, v_out)."""
     c = cache
     if k_out is None and v_out is None:
         if S is None:
             raise FsaError(FSA_ERR_INVALID_ARG, "S, k_out or v_out must be given")
-        k_out = torch.zeros((lens.shape[0], S, c.Hkv, c.D), dtype=torch.bfloat16, device=c.pages.device)
-        v_out = torch.zeros_like(k_out)
+        shape = (lens.shape[0], S, c.Hkv, c.D)
+        k_out = _new(torch.zeros, shape, torch.bfloat16, c.pages.device, stream)
+        v_out = _new(torch.zeros, shape, torch.bfloat16, c.pages.device, stream)
     (_torch_module or _serving()).cache_read(c.pages, c.page_size, c.Hkv, c.D, c.fmt, k_out, v_out, block_table, lens, start,
                                              status, _raw(stream))
     return k_out, v_out
@@ -666,11 +677,12 @@ def fsa_attention_cache(q: torch.Tensor, cache: MxCache, block_table: torch.Tens
     stands at lens[b] - q_lens[b] + i and, causal, sees the keys up to there; rows behind
     q_lens[b] are left as they were.  lse: optional fp32 [B,Sq,H] for the log of the
     softmax sums.  workspace: uint8, at least fsa_attention_cache_workspace bytes (default:
-    one of the call's own)."""
+    one of the call's own).  status: int32 [1], set where a page number lies outside the pool
+    or a wait runs out."""
     c = cache
     if out is None:
         _, dtype = _out_dtype(out_dtype)
-        out = (torch.empty if q_lens is None else torch.zeros)(q.shape, dtype=dtype, device=q.device)
+        out = _new(torch.empty if q_lens is None else torch.zeros, q.shape, dtype, q.device, stream)
     elif out_dtype is not None and _out_dtype(out_dtype)[1] != out.dtype:
         raise FsaError(FSA_ERR_INVALID_ARG, f"out is {out.dtype}, not {out_dtype}")
     (_torch_module or _serving()).attention_cache(c.pages, c.page_size, c.Hkv, c.D, c.fmt, q, out, lse, block_table, lens,

@@ -13,7 +13,7 @@
 namespace fsa {
 namespace {
 
-constexpr int CIO_WARPS = 8;
+constexpr int CIO_WARPS = 4;
 template <int D>
 constexpr int UNIT = 1024 / D;     // tokens of a warp: 8 or 16
 

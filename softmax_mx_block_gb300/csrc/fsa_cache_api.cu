@@ -198,7 +198,7 @@ int fsa_attention_cache(const fsa_cache_attn* c, void* stream) {
   if (st != FSA_OK) return st;
   const int Hkv = a.c.Hkv, D = a.c.D;
   if (!c->q || !c->out || !c->lens || !attn_shape_ok(c->B, c->H, Hkv, c->Sq, D, c->max_pages, c->cache->page_size) ||
-      !table_ok(c->block_table, c->max_pages, c->cache->page_size) || !std::isfinite(c->scale) ||
+      !table_ok(c->block_table, c->max_pages, c->cache->page_size) || !(std::fabs(c->scale) <= 1e30f) ||
       (c->causal != 0 && c->causal != 1) || (c->out_dtype != FSA_OUT_F32 && c->out_dtype != FSA_OUT_BF16) ||
       !aligned(c->q, 16) || !aligned(c->out, 16) || !aligned(c->workspace, 16) || !aligned(c->lens, 4) ||
       !aligned(c->q_lens, 4) || !aligned(c->lse, 4) || !aligned(c->status, 4))

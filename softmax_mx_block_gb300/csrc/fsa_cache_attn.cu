@@ -39,7 +39,8 @@ template <int D, int NT>
 __host__ __device__ constexpr int cta_warps() { return NT == 1 || D == 64 ? 12 : 8; }
 constexpr int TILE = 32;            // keys of a tile
 constexpr int EXTRA = 3;            // what a segment's start costs a warp, in tiles
-constexpr float M_NONE = -1e30f;    // maximum of no keys
+constexpr float M_NONE = -1e30f;    // maximum of no parts (log2 units)
+constexpr float S_NONE = -3e38f;    // maximum of no keys (raw scores)
 constexpr float LAZY = 4.0f;        // log2 of how far a score may beat M
 
 template <int D, int CF, int NT>
@@ -131,9 +132,8 @@ struct Acc {
   static constexpr int R_MIN = CF == CF_MX ? -80 : 0;
   float o[D / 16][NT][4];   // [dim 16i+2g: col 2t, 2t+1; dim 16i+2g+1: col 2t, 2t+1]
   float l[NT][2];           // this thread's part of the row sums
-  float m[NT][2];           // running maximum (log2 units), the same in all g
+  float m[NT][2];           // running maximum of the raw scores, the same in all g
   float top[NT][2];         // a raw score above this raises m
-  float off[NT][2];         // p = exp2(s * cq + off)
   int r;
   uint32_t vtop;            // highest scale byte that r allows, as the high bytes of two halves
 
@@ -144,8 +144,7 @@ struct Acc {
   }
   __device__ __forceinline__ void set_m(int n, int e, float x, float cq) {
     m[n][e] = x;
-    top[n][e] = (x + LAZY) / cq;
-    off[n][e] = 8.f - (float)r - x;
+    top[n][e] = x + LAZY / cq;
   }
   __device__ __forceinline__ void reset(const float (&cq)[NT][2]) {
     set_r(R_MIN);
@@ -158,19 +157,19 @@ struct Acc {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         l[n][e] = 0.f;
-        set_m(n, e, M_NONE, cq[n][e]);
+        set_m(n, e, S_NONE, cq[n][e]);
       }
     }
   }
-  // After the last tile: o and l in units of 2^(m + r - 8), the sums over all lanes.
-  __device__ __forceinline__ void finish() {
+  // After the last tile: m in log2 units, o and l in units of 2^m, the sums over all lanes.
+  __device__ __forceinline__ void finish(const float (&cq)[NT][2]) {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int x = 4; x < 32; x *= 2) l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], x);
-        m[n][e] += (float)r - 8.f;
+        m[n][e] = fmaf(m[n][e], cq[n][e], (float)r - 8.f);
       }
   }
 };
@@ -361,11 +360,11 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint32_t* sc,
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float m = top[n][e] * cq[n][e];
+        float m = top[n][e];
 #pragma unroll
         for (int x = 4; x < 32; x *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
         m = fmaxf(a.m[n][e], m);
-        const float f = exp2f(a.m[n][e] - m + fr);
+        const float f = exp2f(fmaf(a.m[n][e] - m, cq[n][e], fr));
         a.l[n][e] *= f;
         a.set_m(n, e, m, cq[n][e]);
 #pragma unroll
@@ -373,7 +372,9 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint32_t* sc,
       }
   }
 
-  // probabilities, and the products with V
+  // probabilities (the difference first: its error is relative to it, however large the scores),
+  // and the products with V
+  const float shift = 8.f - (float)a.r;
 #pragma unroll
   for (int gr = 0; gr < NG; ++gr) {
     const uint8_t* base = st + (g0 + gr) * Gr::BYTES;
@@ -382,7 +383,7 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint32_t* sc,
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        x4[n][e] = ex2_approx(fmaf(s[gr][n][e], cq[n][e & 1], a.off[n][e & 1]));
+        x4[n][e] = ex2_approx(fmaf(s[gr][n][e] - a.m[n][e & 1], cq[n][e & 1], shift));
         a.l[n][e & 1] += x4[n][e];
       }
     // E8M0 scales multiply in fp32 and the product is rounded; E4M3 ones multiply p as f16
@@ -598,7 +599,7 @@ __device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const Span& sp
     // accumulator columns: 2t, 2t + 1
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      cq[n][c] = p.scale_log2 * __shfl_sync(0xFFFFFFFFu, back, 4 * (2 * t + c));
+      cq[n][c] = fmaxf(p.scale_log2 * __shfl_sync(0xFFFFFFFFu, back, 4 * (2 * t + c)), 1.2e-38f);   // (0 times -inf is NaN)
       lim[n][c] = limit_of(p, sp, c0 + 8 * n + 2 * t + c);
     }
   }
@@ -640,7 +641,7 @@ __device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const Span& sp
     }
     return false;
   }
-  a.finish();
+  a.finish(cq);
   return true;
 }
 

@@ -256,9 +256,10 @@ PyObject* attention_cache(PyObject* const* a) {
     size_t need = 0;
     done(fsa_attention_cache_workspace(&c.c, r.B, r.H, r.Sq, r.max_pages, &need), "fsa_attention_cache_workspace");
     if (need > 0) {
+      // made on the call's stream, so that what is freed there is used again only behind it
+      c10::cuda::OptionalCUDAStreamGuard guard;
+      if (a[16] != Py_None) guard.reset_stream(c10::cuda::getStreamFromExternal((cudaStream_t)on.stream, (c10::DeviceIndex)c.device));
       own = at::empty({(int64_t)need}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, (c10::DeviceIndex)c.device));
-      if (a[16] != Py_None)
-        own.record_stream(c10::cuda::getStreamFromExternal((cudaStream_t)on.stream, (c10::DeviceIndex)c.device));
       r.workspace = own.data_ptr();
       r.workspace_bytes = need;
     }

@@ -13,7 +13,11 @@ value: bf16 2^-8, f16 2^-11, fp32 2^-24 (torch.finfo(t).eps / 2).
     the fp32 scores are off by at most (D + 8) 2^-24 of sum |q||k| scale each way, which moves
     every weight by as much relatively, numerator and denominator; sums, exp2 and the rest
     2^-18; a probability below f16's range loses at most 2^-25 of 2^8-scaled ones (6 * 2^-33
-    of the largest V block scale doubled) a key.  bf16 output adds 2^-8 of the value.
+    of the largest V block scale doubled) a key.  With E4M3 scales p itself is rounded as
+    p 2^(8 - r), where r = 0 unless a scale is 8 or more, and 2^r is at most twice the largest
+    scale s (s <= vtop / 5.5, as amax / 6 rounds to it): the loss of p is 2^-25 / 2^(8 - r), of
+    the product 2^(r - 33) |v|, so the bound carries max(1, 2 vtop / 5.5).  bf16 output adds
+    2^-8 of the value.
 """
 import math
 
@@ -281,7 +285,8 @@ def check_attention(q, cache, table, lens, q_lens, causal, scale, out, lse, befo
         e_s = (D + 8) * 2.0 ** -24 * reach + 2.0 ** -18
         round_p = 2.0 ** -11 if fmt == "E2M1" else 2.0 ** -10 + 2.0 ** -22
         tol = (round_p + 2 * e_s)[..., None] * spread * 1.01
-        tol = tol + (n * 12 * 2.0 ** -33 * vtop / total.clamp(min=1.0))[..., None] + eps_out * want.abs() + 1e-36
+        far = n * 12 * 2.0 ** -33 * vtop * ((vtop / 2.75).clamp(min=1.0) if fmt == "NVFP4" else 1.0)
+        tol = tol + (far / total.clamp(min=1.0))[..., None] + eps_out * want.abs() + 1e-36
         got = out[b, :m].double()
         assert torch.equal(torch.isnan(got), torch.isnan(want)), b
         off = torch.nan_to_num((got - want).abs() - tol, nan=-1.0)
@@ -454,6 +459,69 @@ def test_attention_workspace_streams_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         check_attention(q, cache, table, n, [1, 1], True, D ** -0.5, out, None, out)
+
+
+def test_calls_on_a_stream_of_their_own():
+    """Outputs and workspace that a call makes for itself are made on its stream: a busy current
+    stream does not write over them, nor they over its tensors."""
+    fsa = _fsa()
+    g = gen(65)
+    Hkv, D, H = 4, 128, 16
+    lens = [3000, 1999]
+    cache, table, _, _ = filled_cache(fsa, g, lens, 64, Hkv, D, "E2M1")
+    q, n, m = normal(g, 2, 3, H, D), i32(lens), i32([3, 1])
+    want = fsa.fsa_attention_cache(q, cache, table, n, q_lens=m)
+    back = fsa.fsa_cache_read(cache, table, n, 3000)
+    turned = fsa.fsa_qk_norm_rope(q, q[:, :, :Hkv], None, None)
+    side = torch.cuda.Stream()
+    big = torch.ones(1 << 28, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for _ in range(10):
+            big.mul_(1.0)                          # about 3 ms of work
+            torch.full((2, 3, H, D), 7.0, device="cuda")
+            torch.full((2, 3000, Hkv, D), 7.0, device="cuda", dtype=torch.bfloat16)
+            torch.full((1 << 23,), 7, device="cuda", dtype=torch.uint8)
+        a = fsa.fsa_attention_cache(q, cache, table, n, q_lens=m, stream=side)
+        b = fsa.fsa_cache_read(cache, table, n, 3000, stream=side)
+        c = fsa.fsa_qk_norm_rope(q, q[:, :, :Hkv], None, None, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(a, want) and all(torch.equal(x, y) for x, y in zip(b + c, back + turned))
+
+
+def test_tiny_and_large_scores():
+    """q of every size that bf16 has, scales of many: the scores' factor neither vanishes nor
+    overflows."""
+    fsa = _fsa()
+    g = gen(67)
+    n, Hkv, D = 300, 1, 64
+    for kexp in (-60, 0, 60):
+        table, pages = make_table(g, [n], 16)
+        cache = fsa.empty_cache(pages, 16, Hkv, D, "E2M1")
+        cache.pages.fill_(0xFF)
+        k = (torch.randn(1, n, Hkv, D, generator=g, device="cuda") * 2.0 ** kexp).to(torch.bfloat16)
+        fsa.fsa_cache_append(cache, k, normal(g, 1, n, Hkv, D), table, i32([n]))
+        for qexp in (-126, -60, 0, 60):
+            q = (torch.randn(1, 2, 8, D, generator=g, device="cuda") * 2.0 ** qexp).to(torch.bfloat16)
+            for scale in (2.0 ** -(kexp + qexp) if abs(kexp + qexp) < 99 else 1e30, 1e-12):
+                if kexp + qexp + math.log2(scale) < 8:      # scores that softmax still tells apart in fp32
+                    run_attention(fsa, q, cache, table, [n], scale=scale)
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_configurations(seed):
+    """Seeded random shapes, lengths, formats, masks, strides and value ranges."""
+    import random
+    fsa = _fsa()
+    r, g = random.Random(1000 + seed), gen(1000 + seed)
+    D, fmt, page = r.choice((64, 128)), r.choice(("E2M1", "NVFP4")), r.choice((16, 32, 64, 128, 512))
+    Hkv, G, Sq = r.choice((1, 2, 3, 8)), r.choice((1, 2, 4, 5, 7, 8, 16)), r.choice((1, 1, 2, 3, 5, 17))
+    B, top = r.choice((1, 2, 5, 33, 150)), r.choice((3, 40, 500, 760, 3000))
+    lens = [r.choice((0, 1, r.randint(0, top), r.randint(0, top), top)) for _ in range(B)]
+    q_lens = [r.randint(0, Sq + 1) for _ in range(B)] if r.random() < 0.5 else None
+    cache, table, _, _ = filled_cache(fsa, g, lens, page, Hkv, D, fmt, r.choice((normal, edge_values if top < 100 else normal)))
+    wide = normal(g, B, Sq, Hkv * G + 2, D) * r.choice((0.1, 1.0, 5.0))
+    run_attention(fsa, wide[:, :, 1:-1], cache, table, lens, q_lens, r.random() < 0.7, dtype=r.choice(("f32", "bf16")))
 
 
 def test_two_calls_at_once():
