@@ -14,16 +14,20 @@
 // memory, and then stay in the registers of the threads that have that token, multiplied
 // by the norm's weights.  D/16 lanes hold a row, 16 elements each, chosen so that both
 // elements of a pair are in one thread, and the arithmetic goes two floats at a time.
+#include <algorithm>
 #include "fsa_cache.h"
 #include "fsa_ptx.cuh"
 
 namespace fsa {
 namespace {
 
-constexpr int ROPE_THREADS = 256;
-constexpr int ROPE_TOKENS = 16;    // of a block, at most
+constexpr int ROPE_THREADS = 64;   // 8 or 16 rows at once; small blocks end one by one (256 threads: video 495 us, 64: 479)
+constexpr int ROPE_TOKENS = 4;     // of a block, at most
 constexpr int ROPE_ROWS = 2;       // rows of a thread in flight
-constexpr int ROPE_BLOCKS = 3;     // blocks of an SM
+// Blocks of an SM: 12 of at most 80 registers where there are more blocks than run at once (8:
+// video 543 us), 8 of 128 registers, without spills, where all do (12: the half-rotated
+// batch of 4593 tokens 7.3 us, 8: 5.5).
+constexpr int ROPE_MANY = 12, ROPE_FEW = 8;
 
 // two floats in one register pair
 struct f2 {
@@ -178,8 +182,8 @@ __device__ __forceinline__ void turns_of(double freq, float& fh, float& fl) {
   fl = fmaf(lead, ch, -fh) + fmaf(lead, cl, rest * ch);
 }
 
-template <int D, int P, bool INTER>
-__global__ void __launch_bounds__(ROPE_THREADS, ROPE_BLOCKS) qk_norm_rope_kernel(const RopeArgs a, int tokens) {
+template <int D, int P, bool INTER, int BLOCKS>
+__global__ void __launch_bounds__(ROPE_THREADS, BLOCKS) qk_norm_rope_kernel(const RopeArgs a, int tokens) {
   constexpr int L = D / (2 * P), GROUPS = ROPE_THREADS / L;
   __shared__ __align__(16) float2 sines[ROPE_TOKENS * D / 2];     // cos, sin of [token][pair]
   griddep_launch();
@@ -260,10 +264,15 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_BLOCKS) qk_norm_rope_kernel
   }
 }
 
+template <int D, int P, bool INTER>
+cudaError_t launch_rows(const RopeArgs& a, unsigned grid, int tokens, int sms, cudaStream_t st) {
+  return launch_early(grid > (unsigned)(ROPE_FEW * sms) ? qk_norm_rope_kernel<D, P, INTER, ROPE_MANY>
+                                                        : qk_norm_rope_kernel<D, P, INTER, ROPE_FEW>,
+                      dim3(grid), ROPE_THREADS, 0, st, a, tokens);
+}
 template <int D, int P>
-cudaError_t launch_rows(const RopeArgs& a, unsigned grid, int tokens, cudaStream_t st) {
-  return launch_early(a.interleaved ? qk_norm_rope_kernel<D, P, true> : qk_norm_rope_kernel<D, P, false>, dim3(grid),
-                      ROPE_THREADS, 0, st, a, tokens);
+cudaError_t launch_rows(const RopeArgs& a, unsigned grid, int tokens, int sms, cudaStream_t st) {
+  return a.interleaved ? launch_rows<D, P, true>(a, grid, tokens, sms, st) : launch_rows<D, P, false>(a, grid, tokens, sms, st);
 }
 
 }  // namespace
@@ -273,15 +282,15 @@ cudaError_t launch_qk_norm_rope(const RopeArgs& a, int sms, cudaStream_t st) {
   // 16 elements a lane halve the shuffles and the addresses of a row; 8 where the rotated
   // part is an odd multiple of 8
   const bool wide = a.half % 8 == 0;
-  // Tokens of a block: four of its groups of lanes each (two heads' rows in flight a group,
-  // and what a block starts with, its pairs' frequencies and weights, spread over 8 tokens of
-  // 128 or 16 of 64 dims: video 496 us, with half as many 546, with a quarter 648), fewer
-  // where that would not leave three blocks for two SMs.
-  int tokens = ROPE_THREADS / (a.D / (wide ? 16 : 8)) / 4;
-  while (tokens > 1 && 2 * total < 3 * (int64_t)tokens * sms) tokens /= 2;
+  // Tokens of a block: four of its groups of lanes each (with the pairs' frequencies and the
+  // weights, which a block starts with, used for a quarter of a token's heads; with half
+  // as many tokens the video took 10% longer), fewer where that would not leave two blocks
+  // for each SM.
+  int tokens = std::max(1, ROPE_THREADS / (a.D / (wide ? 16 : 8)) / 4);
+  while (tokens > 1 && total < 2 * (int64_t)tokens * sms) tokens /= 2;
   const unsigned grid = (unsigned)((total + tokens - 1) / tokens);
-  if (a.D == 128) return wide ? launch_rows<128, 8>(a, grid, tokens, st) : launch_rows<128, 4>(a, grid, tokens, st);
-  return wide ? launch_rows<64, 8>(a, grid, tokens, st) : launch_rows<64, 4>(a, grid, tokens, st);
+  if (a.D == 128) return wide ? launch_rows<128, 8>(a, grid, tokens, sms, st) : launch_rows<128, 4>(a, grid, tokens, sms, st);
+  return wide ? launch_rows<64, 8>(a, grid, tokens, sms, st) : launch_rows<64, 4>(a, grid, tokens, sms, st);
 }
 
 }  // namespace fsa
