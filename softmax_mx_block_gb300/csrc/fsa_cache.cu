@@ -160,32 +160,34 @@ __global__ void __launch_bounds__(CIO_WARPS * 32) cache_append_kernel(const Cach
   Group g;
   if (!find_rows<UNIT<D>>(first + skip, fresh - skip, ui, g)) return;
   const int lane = threadIdx.x & 31, l = lane % L, row = lane - l;
-  const uint16_t* const ksrc = a.k + b * a.ks.b + h * a.ks.h + (skip - g.shift) * a.ks.s + 8 * l;
-  const uint16_t* const vsrc = a.v + b * a.vs.b + h * a.vs.h + (skip - g.shift) * a.vs.s + 8 * l;
-  const int base = g.r0 / UNIT<D> * UNIT<D>;
+  const int r = g.r0 / UNIT<D> * UNIT<D> + lane / L;             // this lane's row the first time, ROWS on each time
+  const uint16_t* ksrc = a.k + b * a.ks.b + h * a.ks.h + (skip - g.shift + r) * a.ks.s + 8 * l;
+  const uint16_t* vsrc = a.v + b * a.vs.b + h * a.vs.h + (skip - g.shift + r) * a.vs.s + 8 * l;
   uint4 ku[BATCH], vu[BATCH];
 #pragma unroll
   for (int x = 0; x < BATCH; ++x) {
-    const int r = base + x * ROWS + lane / L;
-    const bool in = r >= g.r0 && r < g.r1;
-    ku[x] = in ? *reinterpret_cast<const uint4*>(ksrc + r * a.ks.s) : make_uint4(0u, 0u, 0u, 0u);
-    vu[x] = in ? *reinterpret_cast<const uint4*>(vsrc + r * a.vs.s) : make_uint4(0u, 0u, 0u, 0u);
+    const bool in = r + x * ROWS >= g.r0 && r + x * ROWS < g.r1;
+    ku[x] = in ? *reinterpret_cast<const uint4*>(ksrc) : make_uint4(0u, 0u, 0u, 0u);
+    vu[x] = in ? *reinterpret_cast<const uint4*>(vsrc) : make_uint4(0u, 0u, 0u, 0u);
+    ksrc += ROWS * a.ks.s;
+    vsrc += ROWS * a.vs.s;
   }
   uint8_t* const at = find_page(a, b, h, g.pos, Gr::BYTES);      // while they are on their way
   if (!at) return;
+  uint8_t* const codes = at + r * (D / 2) + 4 * l;
+  uint8_t* const scales = at + Gr::KS + r * Gr::SB + l / PER;
 #pragma unroll
   for (int x = 0; x < BATCH; ++x) {
-    if (base + x * ROWS >= g.r1 || base + (x + 1) * ROWS <= g.r0) continue;      // a single token: one of these has it
-    const int r = base + x * ROWS + lane / L;
+    if (r - lane / L + x * ROWS >= g.r1 || r - lane / L + (x + 1) * ROWS <= g.r0) continue;      // a single token: one of these has it
     uint32_t ksb, vsb;
     const uint32_t kw = k_to_cache<L>(quantise8<CF>(ku[x], ksb), row, l);
     const uint32_t vw = v_to_cache<L>(quantise8<CF>(vu[x], vsb), row, l);
-    if (r >= g.r0 && r < g.r1) {
-      *reinterpret_cast<uint32_t*>(at + Gr::K + r * (D / 2) + 4 * l) = kw;
-      *reinterpret_cast<uint32_t*>(at + Gr::V + r * (D / 2) + 4 * l) = vw;
+    if (r + x * ROWS >= g.r0 && r + x * ROWS < g.r1) {
+      *reinterpret_cast<uint32_t*>(codes + x * ROWS * (D / 2) + Gr::K) = kw;
+      *reinterpret_cast<uint32_t*>(codes + x * ROWS * (D / 2) + Gr::V) = vw;
       if (l % PER == 0) {
-        at[Gr::KS + r * Gr::SB + l / PER] = (uint8_t)ksb;
-        at[Gr::VS + r * Gr::SB + l / PER] = (uint8_t)vsb;
+        scales[x * ROWS * Gr::SB] = (uint8_t)ksb;
+        scales[x * ROWS * Gr::SB + Gr::VS - Gr::KS] = (uint8_t)vsb;
       }
     }
   }
@@ -205,8 +207,13 @@ __device__ __forceinline__ uint4 values8(uint32_t codes, float s) {
 }
 template <int CF>
 __device__ __forceinline__ float scale_value(uint32_t sb) {
-  if constexpr (CF == CF_MX) return sb == 0xFFu ? __uint_as_float(0x7FC00000u) : sb ? __uint_as_float(sb << 23) : __uint_as_float(0x00400000u);
-  else return e4m3_to_f32(sb);
+  if constexpr (CF == CF_MX) {
+    float f, unused;
+    e8m0x2_f32(sb, f, unused);
+    return f;
+  } else {
+    return e4m3_to_f32(sb);
+  }
 }
 
 template <int D, int CF>
@@ -223,29 +230,33 @@ __global__ void __launch_bounds__(CIO_WARPS * 32) cache_read_kernel(const CacheI
   if (!find_rows<UNIT<D>>(start + skip, min((int64_t)a.S, (int64_t)a.lens[b] - start) - skip, ui, g)) return;
   const uint8_t* const at = find_page(a, b, h, g.pos, Gr::BYTES);
   const int lane = threadIdx.x & 31, l = lane % L, row = lane - l;
-  const int base = g.r0 / UNIT<D> * UNIT<D>;
+  const int r = g.r0 / UNIT<D> * UNIT<D> + lane / L;             // this lane's row the first time, ROWS on each time
+  const uint8_t* const codes = at + r * (D / 2) + 4 * l;
+  const uint8_t* const scales = at + Gr::KS + r * Gr::SB + l / PER;
   uint32_t kw[BATCH], vw[BATCH], ks[BATCH], vs[BATCH];
 #pragma unroll
   for (int x = 0; x < BATCH; ++x) {
-    const int r = base + x * ROWS + lane / L;
     kw[x] = vw[x] = ks[x] = vs[x] = 0;
     if (at) {
-      kw[x] = *reinterpret_cast<const uint32_t*>(at + Gr::K + r * (D / 2) + 4 * l);
-      vw[x] = *reinterpret_cast<const uint32_t*>(at + Gr::V + r * (D / 2) + 4 * l);
-      ks[x] = at[Gr::KS + r * Gr::SB + l / PER];
-      vs[x] = at[Gr::VS + r * Gr::SB + l / PER];
+      kw[x] = *reinterpret_cast<const uint32_t*>(codes + x * ROWS * (D / 2) + Gr::K);
+      vw[x] = *reinterpret_cast<const uint32_t*>(codes + x * ROWS * (D / 2) + Gr::V);
+      ks[x] = scales[x * ROWS * Gr::SB];
+      vs[x] = scales[x * ROWS * Gr::SB + Gr::VS - Gr::KS];
     }
   }
+  uint16_t* kdst = a.k + b * a.ks.b + h * a.ks.h + (skip - g.shift + r) * a.ks.s + 8 * l;
+  uint16_t* vdst = a.v + b * a.vs.b + h * a.vs.h + (skip - g.shift + r) * a.vs.s + 8 * l;
 #pragma unroll
   for (int x = 0; x < BATCH; ++x) {
-    if (base + x * ROWS >= g.r1 || base + (x + 1) * ROWS <= g.r0) continue;
-    const int r = base + x * ROWS + lane / L;
-    const int64_t s = skip + r - g.shift;
-    const bool in = r >= g.r0 && r < g.r1;
-    const uint4 k = values8(k_from_cache<L>(kw[x], row, l), scale_value<CF>(ks[x]));
-    const uint4 v = values8(v_from_cache<L>(vw[x], row, l), scale_value<CF>(vs[x]));
-    if (in && a.k) *reinterpret_cast<uint4*>(a.k + b * a.ks.b + s * a.ks.s + h * a.ks.h + 8 * l) = k;
-    if (in && a.v) *reinterpret_cast<uint4*>(a.v + b * a.vs.b + s * a.vs.s + h * a.vs.h + 8 * l) = v;
+    if (r - lane / L + x * ROWS < g.r1 && r - lane / L + (x + 1) * ROWS > g.r0) {
+      const bool in = r + x * ROWS >= g.r0 && r + x * ROWS < g.r1;
+      const uint4 k = values8(k_from_cache<L>(kw[x], row, l), scale_value<CF>(ks[x]));
+      const uint4 v = values8(v_from_cache<L>(vw[x], row, l), scale_value<CF>(vs[x]));
+      if (in && a.k) *reinterpret_cast<uint4*>(kdst) = k;
+      if (in && a.v) *reinterpret_cast<uint4*>(vdst) = v;
+    }
+    kdst += ROWS * a.ks.s;
+    vdst += ROWS * a.vs.s;
   }
 }
 

@@ -115,14 +115,6 @@ __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t two_bytes) {     // the 
   return r;
 }
 
-// Two E8M0 bytes (the low ones of w) as fp32: 2^(byte - 127), NaN for 0xFF.
-__device__ __forceinline__ void e8m0x2_f32(uint32_t w, float& a, float& b) {
-  uint32_t r;
-  asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.bf16x2.ue8m0x2 %0, lo;\n}" : "=r"(r) : "r"(w));
-  a = __uint_as_float(r << 16);
-  b = __uint_as_float(r & 0xFFFF0000u);
-}
-
 // One warp's running state for one (sequence, kv head, pass of columns).  A thread holds,
 // of n-tile n, columns 8n + 2t and + 1 and, of m-tile i, dims 16i + 2g and + 1.
 template <int D, int CF, int NT>
