@@ -55,8 +55,6 @@ __device__ __forceinline__ uint32_t pack(f2 a) {
   split(a, lo, hi);
   return cvt_bf16x2(lo, hi);
 }
-__device__ __forceinline__ float weight_at(const uint16_t* w, int d) { return w ? __uint_as_float((uint32_t)w[d] << 16) : 1.0f; }
-
 // P pairs of elements in the order that the arithmetic takes them: a firsts, b seconds.
 // A lane of a row holds 2P elements: `a` at at0 .. and `b` at at1 .., P consecutive each, or,
 // interleaved, 2P consecutive ones from at0 on (at1 = at0 + P).
@@ -84,28 +82,40 @@ struct Raw {
   }
 };
 
+// The first and the second elements of pairs 2e and 2e + 1.
+template <int P, bool INTER>
+__device__ __forceinline__ void firsts_seconds(const Raw<P>& x, int e, f2& a, f2& b) {
+  if (INTER) {             // words 2e and 2e + 1
+    const uint32_t u = x.w[2 * e], v = x.w[2 * e + 1];
+    a = make(__uint_as_float(u << 16), __uint_as_float(v << 16));
+    b = make(__uint_as_float(u & 0xFFFF0000u), __uint_as_float(v & 0xFFFF0000u));
+  } else {
+    a = unpack(x.w[e]);
+    b = unpack(x.w[P / 2 + e]);
+  }
+}
+
 // What the first and the second element of each of the thread's pairs are multiplied by,
 // two pairs a register: first result a * c[0] + b * c[1], second a * c[2] + b * c[3].
 template <int P, bool INTER>
 struct Factors {
   f2 c[4][P / 2];
   __device__ __forceinline__ void set(const float2* t, bool turns, const uint16_t* w, int at0, int at1) {
+    Raw<P> raw;                                     // the weights, as a row
+    if (w) raw.load(w, at0, at1);
+    else
+#pragma unroll
+      for (int e = 0; e < P; ++e) raw.w[e] = 0x3F803F80u;       // ones
 #pragma unroll
     for (int e = 0; e < P / 2; ++e) {
-      float f[4][2];
+      f2 wa, wb;
+      firsts_seconds<P, INTER>(raw, e, wa, wb);
       const float4 cs = turns ? reinterpret_cast<const float4*>(t)[e] : make_float4(1.f, 0.f, 1.f, 0.f);   // cos, sin of two
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int i = 2 * e + x;
-        const float wa = weight_at(w, INTER ? at0 + 2 * i : at0 + i), wb = weight_at(w, INTER ? at0 + 2 * i + 1 : at1 + i);
-        const float co = x ? cs.z : cs.x, si = x ? cs.w : cs.y;
-        f[0][x] = wa * co;
-        f[1][x] = -wb * si;
-        f[2][x] = wa * si;
-        f[3][x] = wb * co;
-      }
-#pragma unroll
-      for (int x = 0; x < 4; ++x) c[x][e] = make(f[x][0], f[x][1]);
+      const f2 co = make(cs.x, cs.z), si = make(cs.y, cs.w);
+      c[0][e] = mul(wa, co);
+      c[1][e] = mul(wb, make(-cs.y, -cs.w));
+      c[2][e] = mul(wa, si);
+      c[3][e] = mul(wb, co);
     }
   }
 };
@@ -118,16 +128,7 @@ __device__ __forceinline__ void turn_row(Raw<P>& x, const Factors<P, INTER>& f, 
   constexpr int L = D / (2 * P);
   f2 a[P / 2], b[P / 2];
 #pragma unroll
-  for (int e = 0; e < P / 2; ++e) {
-    if (INTER) {           // words 2e and 2e + 1: pairs 2e, 2e + 1
-      const uint32_t u = x.w[2 * e], v = x.w[2 * e + 1];
-      a[e] = make(__uint_as_float(u << 16), __uint_as_float(v << 16));
-      b[e] = make(__uint_as_float(u & 0xFFFF0000u), __uint_as_float(v & 0xFFFF0000u));
-    } else {
-      a[e] = unpack(x.w[e]);
-      b[e] = unpack(x.w[P / 2 + e]);
-    }
-  }
+  for (int e = 0; e < P / 2; ++e) firsts_seconds<P, INTER>(x, e, a[e], b[e]);
   float rs = 1.0f;
   if (norm) {
     f2 sa = mul(a[0], a[0]), sb = mul(b[0], b[0]);
