@@ -7,6 +7,12 @@
 // D/8 lanes a row; on the cache's side one word of a row.  The two orders (fsa_cache.h)
 // differ, so the code words cross the lanes in between: a K word is two halves of two
 // lanes' words, a V word four bytes of four.  The rounding is that of fsa_mx_quantize.
+//
+// Measured (one GB300): reading 128K tokens of 8 kv heads back 104 us for 688 MB (6.6 TB/s,
+// 0.97 of the copy bandwidth); four prompts of up to 4096 tokens written and read back 25.7 us
+// for 118 MB of unavoidable bytes, two kernels that at this size are bound by their
+// instructions (2.7 and 3.0 a cycle) as much as by memory; a step of 128 single tokens written
+// and read back 4.1 us, two launches.
 #include "fsa_cache.h"
 #include "fsa_mx.cuh"
 

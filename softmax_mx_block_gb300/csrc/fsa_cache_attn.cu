@@ -11,22 +11,35 @@
 // on its own keys with m16n8k16 products whose m is the keys (S^T = K Q^T) and then
 // D (O^T = V^T P^T), n the query rows ("columns" here: 8 or 16 a pass).
 //
-//   - The codes go to the products unscaled: E2M1 to f16 is exact in one instruction a
-//     pair.  K's scales multiply the fp32 sums of each block; V's scales multiply the
-//     probabilities before they are rounded to f16 (11 bits).  Q as f16 with a power of
-//     two per row is exact down to 2^-28 of the row's maximum.
-//   - The f16 probabilities get a shift R, the running maximum exponent of V's scales, so
-//     that p * scale stays below 2^15; 2^28 below that they are still exact to 11 bits.
-//     The running maximum M of the scores is raised only when a score beats it by more
-//     than 2^4 (then the sums are rescaled), so most tiles need no reduction over lanes.
-//     Both offsets multiply numerator and denominator alike and cancel.
+//   - E2M1 to f16 is exact in one instruction a pair.  An E8M0 scale of K multiplies the fp32
+//     sum of its block; an E4M3 one multiplies the codes (6 bits: exact in f16).  V's scales
+//     multiply the probabilities: E8M0 in fp32 before they are rounded to f16, E4M3 as f16
+//     after (a second rounding).  Q as f16 with a power of two per row is exact down to 2^-18
+//     of the row's maximum and off by at most 2^-29 of it below.
+//   - A tile's scales are unpacked once, a token a lane, through shared memory: every lane of
+//     a quad needs the same ones (13% of the arithmetic pipe with E8M0, 22% with E4M3).
+//   - The f16 probabilities carry 2^(8 - r), r the running maximum exponent of V's scales,
+//     so that p * scale stays below 2^15.  The running maximum m of the raw scores is raised
+//     only when a score beats it by more than 2^4 in the softmax (then the sums are
+//     rescaled), so most tiles need one vote and no reduction over lanes.  Both offsets
+//     multiply numerator and denominator alike and cancel.
 //   - Work is split evenly over the warps of one CTA per SM: all (sequence, kv head, 32-key
-//     tile) triples in one list, a contiguous share each.  A warp's share of a sequence
-//     that others share too is a partial result (maximum, sum, unnormalised rows); the
-//     warps of a CTA join theirs in shared memory, and a second kernel joins the CTAs'.
-//     The lengths are read on the device, so a captured call follows them.
+//     tile) triples in one list, a contiguous share each, a segment's start weighing as
+//     three tiles (measured: 64 ragged sequences 53 us without, 44 with two, 43 with three).
+//     A warp's share of a segment that others share too is a partial result (maximum, sum,
+//     unnormalised rows); the warps of a CTA join theirs in shared memory, and a second
+//     kernel, launched early, joins the CTAs'.  The lengths are read on the device, so a
+//     captured call follows them.  Short tables take a kernel of a CTA a segment instead.
 //   - Each warp has a ring of its own: one bulk copy per page part and tile, an mbarrier a
-//     stage.  No warp waits for another before the end.
+//     stage, the lane that looked the page up copies it.  No warp waits for another before
+//     the end.  12 warps of 168 registers: 16 of 128 spilled and were no faster, 8 were 5%
+//     slower.
+//
+// Measured (one GB300, copies at 6.79 TB/s): 8 sequences of 128K tokens, 8 kv heads, 4 query
+// heads each: E2M1 5.62 TB/s, NVFP4 5.41 TB/s of cache; one sequence 36.4 us for 143 MB, of
+// which 22 us stream at 6.4 TB/s and the rest is the list, the first copies, the joins.
+// Counters at that size: 257 (E2M1) and 293 (NVFP4) warp instructions for 16 keys of a kv
+// head, 2.3 a cycle, the arithmetic pipe 58%, tensor 29%, shared memory 49 to 60%.
 #include <atomic>
 #include "fsa_cache.h"
 #include "fsa_ptx.cuh"
@@ -1017,7 +1030,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_join_kernel(const CacheAtt
   }
 }
 
-// Which kernel: a CTA for each segment where none is longer than 24 tiles and there are at most
+// Which kernel: a CTA for each segment where none is longer than 28 tiles and there are at most
 // 8 an SM, else the list split evenly.  (The table's width bounds a segment's tiles; the
 // lengths are on the device.)  Measured, list / whole, us, 8 kv heads of 128 dims, E2M1:
 //   1 sequence of 100, 760, 1500 keys: 8.6 / 4.0, 9.0 / 8.4, 9.5 / 13.3
@@ -1025,7 +1038,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_join_kernel(const CacheAtt
 //   256 sequences of 1 to 100, 1 to 760: 17.5 / 18.3, 24.0 / 28.1 (2048 segments)
 bool whole_segments(const Cache& c, int B, int CT, int max_pages, int sms) {
   const int64_t tiles = (((int64_t)max_pages << c.page_shift) + TILE - 1) / TILE;
-  return tiles <= 24 && (int64_t)B * CT * c.Hkv <= 8 * (int64_t)sms;
+  return tiles <= 28 && (int64_t)B * CT * c.Hkv <= 8 * (int64_t)sms;
 }
 
 // Opt in to the kernel's shared memory, once a device.

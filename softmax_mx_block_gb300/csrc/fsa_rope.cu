@@ -14,6 +14,9 @@
 // memory, and then stay in the registers of the threads that have that token, multiplied
 // by the norm's weights.  D/16 lanes hold a row, 16 elements each, chosen so that both
 // elements of a pair are in one thread, and the arithmetic goes two floats at a time.
+//
+// Measured (one GB300): 75600 patches of 40 + 40 heads of 128 474 us (6.5 TB/s, 0.96 of the copy
+// bandwidth), 16K tokens of 32 + 8 heads 60 us (0.82), 64 tokens of a decode step 3.6 us.
 #include <algorithm>
 #include "fsa_cache.h"
 #include "fsa_ptx.cuh"
