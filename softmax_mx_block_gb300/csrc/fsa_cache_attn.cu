@@ -25,21 +25,23 @@
 //     multiply numerator and denominator alike and cancel.
 //   - Work is split evenly over the warps of one CTA per SM: all (sequence, kv head, 32-key
 //     tile) triples in one list, a contiguous share each, a segment's start weighing as
-//     three tiles (measured: 64 ragged sequences 53 us without, 44 with two, 43 with three).
+//     three tiles (64 ragged sequences: 59 us at none, 36.2 at two, 35.6 at three, 36.5 at four).
 //     A warp's share of a segment that others share too is a partial result (maximum, sum,
 //     unnormalised rows); the warps of a CTA join theirs in shared memory, and a second
 //     kernel, launched early, joins the CTAs'.  The lengths are read on the device, so a
 //     captured call follows them.  Short tables take a kernel of a CTA a segment instead.
 //   - Each warp has a ring of its own: one bulk copy per page part and tile, an mbarrier a
 //     stage, the lane that looked the page up copies it.  No warp waits for another before
-//     the end.  12 warps of 168 registers: 16 of 128 spilled and were no faster, 8 were 5%
-//     slower.
+//     the end.  Two stages: 24 tiles in flight an SM cover the latency, and a third cost 3%.
+//     12 warps of 168 registers: 8 were 5 to 7% slower, 10 (uneven over the four schedulers)
+//     10%, 14 and 16 (spills) 12%.
 //
 // Measured (one GB300, copies at 6.79 TB/s): 8 sequences of 128K tokens, 8 kv heads, 4 query
-// heads each: E2M1 5.62 TB/s, NVFP4 5.41 TB/s of cache; one sequence 36.4 us for 143 MB, of
-// which 22 us stream at 6.4 TB/s and the rest is the list, the first copies, the joins.
-// Counters at that size: 257 (E2M1) and 293 (NVFP4) warp instructions for 16 keys of a kv
-// head, 2.3 a cycle, the arithmetic pipe 58%, tensor 29%, shared memory 49 to 60%.
+// heads each: E2M1 198 us, 5.77 TB/s of cache, NVFP4 223 us, 5.41 TB/s; one sequence 35.5 us
+// for 143 MB.  Of that 1.4 us go until the list is summed, 0.6 until a warp has its place in it,
+// 1.7 until its first copies are on their way; the warps of a CTA end 2.8 us before its slowest
+// on average, its join takes 1.3, the second kernel 3.  Counters at the large sizes: 257 (E2M1) and
+// 293 (NVFP4) warp instructions for 16 keys of a kv head, 2.3 a cycle.
 #include <atomic>
 #include "fsa_cache.h"
 #include "fsa_ptx.cuh"
@@ -63,7 +65,7 @@ struct Cfg {
   static constexpr int STAGE = 2 * Gr::BYTES;
   static constexpr int COLS = 8 * NT;
   static constexpr int PART = COLS * (D + 6);        // floats of a partial result: rows D + 4 apart, maxima, sums
-  static constexpr int STG = CF == CF_MX ? 3 : 2;   // stages of a warp's ring
+  static constexpr int STG = 2;                      // stages of a warp's ring
   static constexpr int RING = NWC * STG * STAGE;
   static constexpr int JOIN = NWC * PART * 4;
   static constexpr int SCALES = TILE * Gr::SB * 8;   // unpacked scales of a tile: a word each for K and for V
@@ -1033,9 +1035,10 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_join_kernel(const CacheAtt
 // Which kernel: a CTA for each segment where none is longer than 28 tiles and there are at most
 // 8 an SM, else the list split evenly.  (The table's width bounds a segment's tiles; the
 // lengths are on the device.)  Measured, list / whole, us, 8 kv heads of 128 dims, E2M1:
-//   1 sequence of 100, 760, 1500 keys: 8.6 / 4.0, 9.0 / 8.4, 9.5 / 13.3
-//   64 sequences of 100, 760, 1500 keys: 13.0 / 8.3, 23.1 / 19.7, 33.1 / 31.7
-//   256 sequences of 1 to 100, 1 to 760: 17.5 / 18.3, 24.0 / 28.1 (2048 segments)
+//   1 sequence of 100, 760, 890, 1020, 1500 keys: 8.5 / 3.9, 9.0 / 8.4, 9.1 / 9.2, 9.3 / 10.0, 9.5 / 13.3
+//   64 sequences of 100, 890, 1500 keys: 13.1 / 8.0, 25.2 / 22.0, 33.4 / 31.8
+//   152 sequences (8 segments an SM) of 100, 890, 1 to 890: 17.0 / 13.1, 43.7 / 39.8, 19.4 / 19.4
+//   256 sequences of 100, 1 to 100, 1 to 890: 19.7 / 20.5, 17.4 / 17.9, 24.7 / 29.5
 bool whole_segments(const Cache& c, int B, int CT, int max_pages, int sms) {
   const int64_t tiles = (((int64_t)max_pages << c.page_shift) + TILE - 1) / TILE;
   return tiles <= 28 && (int64_t)B * CT * c.Hkv <= 8 * (int64_t)sms;
