@@ -82,12 +82,20 @@ int cache_io(const fsa_cache* cache, const void* k, const void* v, const fsa_str
   return FSA_OK;
 }
 
-int launch_status(cudaError_t e) { return e == cudaSuccess ? FSA_OK : FSA_ERR_LAUNCH; }
+// (a failed call's error is reported here, and not to whoever asks the runtime next)
+int launch_status(cudaError_t e) {
+  if (e == cudaSuccess) return FSA_OK;
+  cudaGetLastError();
+  return FSA_ERR_LAUNCH;
+}
 
 bool sm_count(int* sms) {
   int dev = 0;
-  return cudaGetDevice(&dev) == cudaSuccess &&
-         cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && *sms > 0;
+  if (cudaGetDevice(&dev) == cudaSuccess &&
+      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && *sms > 0)
+    return true;
+  cudaGetLastError();
+  return false;
 }
 
 // The kernels count rows and, over all sequences, heads and passes of columns, tiles of 32

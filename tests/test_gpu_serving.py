@@ -19,6 +19,7 @@ value: bf16 2^-8, f16 2^-11, fp32 2^-24 (torch.finfo(t).eps / 2).
     the product 2^(r - 33) |v|, so the bound carries max(1, 2 vtop / 5.5).  bf16 output adds
     2^-8 of the value.
 """
+import ctypes
 import math
 
 import pytest
@@ -598,6 +599,29 @@ def test_calls_refuse():
     for call in (lambda: fsa.fsa_attention_cache(q, cache, None, n), lambda: fsa.fsa_cache_append(cache, k, None, table, n)):
         with pytest.raises(fsa.FsaError, match="tensor"):
             call()
+    torch.cuda.synchronize()
+
+
+def test_a_failed_launch_leaves_no_error_behind():
+    """A launch that the runtime refuses (on the default stream, while one that waits for it is
+    captured) is reported by the call, and not again to the runtime's next user."""
+    fsa = _fsa()
+    cache, table, k, v = filled_cache(fsa, gen(3), [20], 16, 1, 64, "E2M1")
+    runtime = ctypes.CDLL("libcudart.so.13")
+    stream, n, graph = ctypes.c_void_p(), i32([20]), ctypes.c_void_p()
+    assert runtime.cudaStreamCreate(ctypes.byref(stream)) == 0
+    torch.cuda.synchronize()
+    assert runtime.cudaStreamBeginCapture(stream, 0) == 0
+    try:
+        with pytest.raises(fsa.FsaError) as e:
+            fsa.fsa_cache_append(cache, k, v, table, n, stream=torch.cuda.default_stream())
+        left = runtime.cudaPeekAtLastError()
+    finally:
+        runtime.cudaStreamEndCapture(stream, ctypes.byref(graph))     # it is void
+        runtime.cudaGetLastError()
+        runtime.cudaStreamDestroy(stream)
+    assert e.value.status == fsa.FSA_ERR_LAUNCH and left == 0
+    fsa.fsa_cache_append(cache, k, v, table, n)
     torch.cuda.synchronize()
 
 
