@@ -3,10 +3,10 @@
 // Both kernels are bound by memory: append reads 2 bytes and writes 0.53 (E2M1) or 0.56
 // (NVFP4) bytes an element, read the other way round.  A warp takes a run of UNIT tokens of
 // a kv head within a group (a contiguous piece of a page), so that page and addresses are
-// worked out once for 2 * 1024 elements, all of whose loads go out together.  On the bf16 side a lane holds 8 consecutive elements (16 bytes),
-// D/8 lanes a row; on the cache's side one word of a row.  The two orders (fsa_cache.h)
-// differ, so the code words cross the lanes in between: a K word is two halves of two
-// lanes' words, a V word four bytes of four.  The rounding is that of fsa_mx_quantize.
+// worked out once for 2 * 1024 elements, all of whose loads go out together.  On the bf16
+// side a lane holds 8 consecutive elements (16 bytes), D/8 lanes a row; on the cache's side
+// one word of a row.  The two orders (fsa_cache.h) differ, so the code words cross the lanes
+// in between: a K word is two halves of two lanes' words, a V word four bytes of four.  The rounding is that of fsa_mx_quantize.
 //
 // Measured (one GB300): reading 128K tokens of 8 kv heads back 104 us for 688 MB (6.6 TB/s,
 // 0.97 of the copy bandwidth); four prompts of up to 4096 tokens written and read back 25.7 us
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(CIO_WARPS * 32) cache_read_kernel(const CacheI
 // units that S consecutive tokens can touch
 int units_of(const CacheIo& a) {
   const int u = 1024 / a.c.D;
-  return (a.S + u - 2) / u + 1;
+  return (int)(((int64_t)a.S + u - 2) / u + 1);
 }
 unsigned blocks_of(const CacheIo& a) {
   return (unsigned)(((int64_t)a.B * units_of(a) * a.c.Hkv + CIO_WARPS - 1) / CIO_WARPS);

@@ -551,6 +551,23 @@ def test_two_calls_at_once():
         assert torch.equal(out, want)
 
 
+def test_append_of_the_longest_padding():
+    """S at the end of its range, all but a few rows of it padding (a broadcast row): the count
+    of the warps' units does not wrap."""
+    fsa = _fsa()
+    g = gen(33)
+    cache, table, _, _ = filled_cache(fsa, g, [20], 16, 1, 64, "NVFP4", junk=0xA5)
+    before = cache.pages.clone()
+    row = normal(g, 1, 1, 1, 64)
+    wide = row.expand(1, 2 ** 31 - 1, 1, 64)
+    fsa.fsa_cache_append(cache, wide, wide, table, i32([12]), i32([0]))
+    assert torch.equal(cache.pages, before)
+    fsa.fsa_cache_append(cache, wide, wide, table, i32([12]), i32([3]))
+    kb, vb = fsa.fsa_cache_read(cache, table, i32([12]), 3, start=i32([9]))
+    want = ref.rounded(row, "NVFP4").expand(1, 3, 1, 64)
+    assert torch.equal(kb.double(), want) and torch.equal(vb.double(), want)
+
+
 def test_calls_refuse():
     """The binding's checks: devices, types, shapes, strides, buffers."""
     fsa = _fsa()
