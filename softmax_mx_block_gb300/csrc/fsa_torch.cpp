@@ -84,6 +84,12 @@ double real(PyObject* o) {
   return v;
 }
 
+int truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw 0;
+  return v;
+}
+
 // The tensors' device as the current one while the call is made, and its stream.
 struct Launch {
   c10::cuda::CUDAGuard guard;
@@ -139,7 +145,7 @@ PyObject* norm_rope(PyObject* const* a) {
   same_shape(ko, k, "k_out, k");
   if (k.size(0) != q.size(0) || k.size(1) != q.size(1) || k.size(3) != q.size(3)) refuse(FSA_ERR_INVALID_ARG, "q, k shapes");
   const int64_t B = q.size(0), S = q.size(1), D = q.size(3);
-  if (B > INT32_MAX || S > INT32_MAX) refuse(FSA_ERR_INVALID_ARG, "q, k shapes");
+  if (B > INT32_MAX || S > INT32_MAX || q.size(2) > INT32_MAX || k.size(2) > INT32_MAX) refuse(FSA_ERR_INVALID_ARG, "q, k shapes");
   int64_t half = 0, axes = 1;
   if (a[3] != Py_None) {
     const at::Tensor& f = tensor(a[3], "inv_freq");
@@ -168,7 +174,7 @@ PyObject* norm_rope(PyObject* const* a) {
   r.k_weight = plain<void>(a[6], "k_weight", dev, at::kBFloat16, {D});
   r.B = (int)B; r.S = (int)S; r.H = (int)q.size(2); r.Hkv = (int)k.size(2); r.D = (int)D;
   r.rotary = (int)(2 * half); r.n_axes = (int)axes;
-  r.norm = PyObject_IsTrue(a[7]); r.eps = (float)real(a[8]); r.interleaved = PyObject_IsTrue(a[9]);
+  r.norm = truth(a[7]); r.eps = (float)real(a[8]); r.interleaved = truth(a[9]);
   const Launch on(dev, a[12]);
   done(fsa_qk_norm_rope(&r, on.stream), "fsa_qk_norm_rope");
   Py_RETURN_NONE;
@@ -244,7 +250,7 @@ PyObject* attention_cache(PyObject* const* a) {
   r.q_lens = plain<int32_t>(a[10], "q_lens", c.device, at::kInt, {B});
   r.status = plain<int32_t>(a[15], "status", c.device, at::kInt, {1});
   r.B = (int)B; r.H = (int)H; r.Sq = (int)Sq; r.max_pages = table.width;
-  r.causal = PyObject_IsTrue(a[11]);
+  r.causal = truth(a[11]);
   r.out_dtype = out.scalar_type() == at::kBFloat16 ? FSA_OUT_BF16 : FSA_OUT_F32;
   r.scale = a[12] == Py_None ? (c.c.D == 64 ? 0.125f : 0.08838834764831845f) : (float)real(a[12]);
   const long long limit = number(a[14]);

@@ -568,6 +568,24 @@ def test_append_of_the_longest_padding():
     assert torch.equal(kb.double(), want) and torch.equal(vb.double(), want)
 
 
+def test_flags_without_a_truth_value():
+    """What bool() raises for a flag is what the call raises."""
+    fsa = _fsa()
+    g = gen(4)
+    cache, table, _, _ = filled_cache(fsa, g, [20], 16, 1, 64, "E2M1")
+    q = normal(g, 1, 1, 1, 64)
+
+    class Neither:
+        def __bool__(self):
+            raise ValueError("neither")
+
+    for call in (lambda f: fsa.fsa_qk_norm_rope(q, q.clone(), None, None, norm=f),
+                 lambda f: fsa.fsa_qk_norm_rope(q, q.clone(), None, None, interleaved=f),
+                 lambda f: fsa.fsa_attention_cache(q, cache, table, i32([20]), causal=f)):
+        with pytest.raises(ValueError, match="neither"):
+            call(Neither())
+
+
 def test_calls_refuse():
     """The binding's checks: devices, types, shapes, strides, buffers."""
     fsa = _fsa()
