@@ -40,8 +40,8 @@
 // heads each: E2M1 198 us, 5.77 TB/s of cache, NVFP4 223 us, 5.41 TB/s; one sequence 35.5 us
 // for 143 MB.  Of that 1.4 us go until the list is summed, 0.6 until a warp has its place in it,
 // 1.7 until its first copies are on their way; the warps of a CTA end 2.8 us before its slowest
-// on average, its join takes 1.3, the second kernel 3.  Counters at the large sizes: 257 (E2M1) and
-// 293 (NVFP4) warp instructions for 16 keys of a kv head, 2.3 a cycle.
+// on average, its join takes 1.3, the second kernel 3.  Counters at the large sizes: 265 (E2M1) and
+// 295 (NVFP4) warp instructions for 16 keys of a kv head, 2.5 and 2.4 a cycle of 4.
 #include <atomic>
 #include "fsa_cache.h"
 #include "fsa_ptx.cuh"

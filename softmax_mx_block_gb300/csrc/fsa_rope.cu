@@ -15,8 +15,10 @@
 // by the norm's weights.  D/16 lanes hold a row, 16 elements each, chosen so that both
 // elements of a pair are in one thread, and the arithmetic goes two floats at a time.
 //
-// Measured (one GB300): 75600 patches of 40 + 40 heads of 128 474 us (6.5 TB/s, 0.96 of the copy
-// bandwidth), 16K tokens of 32 + 8 heads 60 us (0.82), 64 tokens of a decode step 3.6 us.
+// Measured (one GB300): 75600 patches of 40 + 40 heads of 128 471 us (6.6 TB/s, 0.97 of the copy
+// bandwidth), 16K tokens of 32 + 8 heads 59.5 us (0.83: about 7 us to start and to run out, and
+// heads before positions cost 5%, their rows of two tokens being 512 bytes), 64 tokens of a
+// decode step 3.6 us.
 #include <algorithm>
 #include "fsa_cache.h"
 #include "fsa_ptx.cuh"
@@ -288,10 +290,13 @@ cudaError_t launch_qk_norm_rope(const RopeArgs& a, int sms, cudaStream_t st) {
   const bool wide = a.half % 8 == 0;
   // Tokens of a block: four of its groups of lanes each (with the pairs' frequencies and the
   // weights, which a block starts with, used for a quarter of a token's heads; with half
-  // as many tokens the video took 10% longer), fewer where that would not leave two blocks
-  // for each SM.
+  // as many tokens the video took 10% longer); fewer while all blocks still run at once, 8 an
+  // SM (us without / with: 1000 tokens of 32 + 8 heads of 128 7.5 / 5.6, of 8 + 8 5.1 / 4.4; 1800 of
+  // 14 + 2 heads of 64 5.2 / 4.2).  Up to 12 an SM, 1800 tokens of 32 + 8 heads would take 9.3
+  // instead of 10.1, but of 8 + 8 5.8 instead of 5.3; beyond that two waves, 2000 of 8 + 8 7.4
+  // instead of 5.3.
   int tokens = std::max(1, ROPE_THREADS / (a.D / (wide ? 16 : 8)) / 4);
-  while (tokens > 1 && total < 2 * (int64_t)tokens * sms) tokens /= 2;
+  while (tokens > 1 && 2 * total <= ROPE_FEW * (int64_t)tokens * sms) tokens /= 2;
   const unsigned grid = (unsigned)((total + tokens - 1) / tokens);
   if (a.D == 128) return wide ? launch_rows<128, 8>(a, grid, tokens, sms, st) : launch_rows<128, 4>(a, grid, tokens, sms, st);
   return wide ? launch_rows<64, 8>(a, grid, tokens, sms, st) : launch_rows<64, 4>(a, grid, tokens, sms, st);
