@@ -468,12 +468,12 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint32_t* sc,
 struct Row {
   int64_t at, lse_at;
   float inv, lse;
-  bool none;               // no key: zeros
+  bool none;               // no key: zeros (none by the lengths, or none on a page of the pool: nothing was summed)
   __device__ __forceinline__ Row(const CacheAttnArgs& p, int b, int hkv, int col, const Span& s, float m, float l) {
     const int i = row_of(p, col), h = hkv * p.G + col - i * p.G;
     at = b * p.os.b + i * p.os.s + h * p.os.h;
     lse_at = ((int64_t)b * p.Sq + i) * p.H + h;
-    none = limit_of(p, s, col) == 0;
+    none = limit_of(p, s, col) == 0 || l == 0.f;
     inv = 1.0f / l;
     lse = none ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
   }
@@ -596,7 +596,9 @@ __device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const Span& sp
     top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
     const int e = (int)(__float_as_uint(top) >> 23) - 127;                 // floor(log2 top)
     const int up = e == 128 || top == 0.f ? 0 : min(max(4 - e, -126), 126);
-    const float f = __uint_as_float((uint32_t)(up + 127) << 23) * p.q_sign;
+    // (a row with an infinity becomes NaN as a whole, as its softmax is, even if all scores were
+    // -inf: a sum of 0 then says that no key was seen)
+    const float f = e == 128 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(up + 127) << 23) * p.q_sign;
     const float back = __uint_as_float((uint32_t)(127 - up) << 23);
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {

@@ -1,0 +1,74 @@
+"""The serving operators at the ends of what they accept: rows all of whose pages lie outside
+the pool, scores near the ends of fp32 split over warps and CTAs, values near the ends of bf16,
+the quantiser's scales.  Tolerances as derived in test_gpu_serving.py, or exact."""
+import math
+
+import pytest
+
+import serving_ref as ref
+from test_gpu_serving import _fsa, check_attention, edge_values, filled_cache, gen, i32, make_table, normal, run_attention
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+def wide_table(table, width):
+    """The table with -1 columns up to `width`: beyond 896 tokens the attention splits one list
+    of tiles evenly over the CTAs, whatever the lengths."""
+    return torch.nn.functional.pad(table, (0, max(0, width - table.shape[1])), value=-1)
+
+
+# Lengths, kv heads and table widths (pages of 16) that end in each way of writing a row:
+SPLITS = [
+    pytest.param([20], 1, 4, id="one warp"),
+    pytest.param([600], 2, 40, id="warps of a CTA, short table"),
+    pytest.param([20, 9], 1, 100, id="one warp, list"),
+    pytest.param([777] * 40, 8, 100, id="warps of a CTA, list"),
+    pytest.param([5000], 1, 320, id="CTAs"),
+    pytest.param([9000, 31, 4000], 2, 600, id="CTAs and warps"),
+]
+
+
+# ------------------------------------------------------------------- rows that see no key
+@pytest.mark.parametrize("lens,Hkv,width", SPLITS)
+@pytest.mark.parametrize("fmt,D,dtype", [("E2M1", 128, "f32"), ("NVFP4", 128, "bf16"), ("E2M1", 64, "bf16"), ("NVFP4", 64, "f32")])
+def test_rows_all_of_whose_pages_are_outside(fmt, D, dtype, lens, Hkv, width):
+    """Keys on pages outside the pool are not seen; a row that sees nothing else is zero, its
+    lse -inf, however the keys are split.  Each other sequence as without them."""
+    fsa = _fsa()
+    g = gen(91)
+    cache, table, _, _ = filled_cache(fsa, g, lens, 16, Hkv, D, fmt)
+    table = wide_table(table, width)
+    for which in (range(len(lens)), range(0, len(lens), 2)):
+        for bad in (-1, cache.pages.shape[0]):
+            t = table.clone()
+            for b in which:
+                t[b] = bad
+            for Sq in (1, 3):
+                q, status = normal(g, len(lens), Sq, 4 * Hkv, D), i32([0])
+                out, lse = run_attention(fsa, q, cache, t, lens, causal=Sq == 1, dtype=dtype, status=status)
+                assert int(status) == fsa.FSA_ERR_INVALID_ARG
+                for b in which:
+                    assert bool((out[b] == 0).all()) and bool((lse[b] == -math.inf).all())
+
+
+@pytest.mark.parametrize("lens,Hkv,width", SPLITS)
+def test_infinite_queries(lens, Hkv, width):
+    """A row of q with an infinity has infinite scores: NaN, also where all of them are -inf;
+    without a key it is zero all the same."""
+    fsa = _fsa()
+    g = gen(93)
+    B, D, S = len(lens), 128, max(lens)
+    table, pages = make_table(g, lens, 16)
+    table = wide_table(table, width)
+    cache = fsa.empty_cache(pages, 16, Hkv, D, "E2M1")
+    k, v = normal(g, B, S, Hkv, D), normal(g, B, S, Hkv, D)
+    k[..., 5] = 4.0
+    fsa.fsa_cache_append(cache, k, v, table, i32(lens), i32(lens))
+    q = normal(g, B, 2, 4 * Hkv, D)
+    q[:, 0, 1, 5] = -math.inf
+    q[:, 1, 2, 5] = math.inf
+    out, lse = run_attention(fsa, q, cache, table, lens, causal=False)
+    assert bool(torch.isnan(out[:, 0, 1]).all()) and bool(torch.isnan(out[:, 1, 2]).all()) and int(torch.isnan(lse).sum()) == 2 * B
+    out, lse = run_attention(fsa, q, cache, torch.full_like(table, -1), lens, causal=False)
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all())
