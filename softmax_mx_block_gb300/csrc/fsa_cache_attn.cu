@@ -54,7 +54,6 @@ template <int D, int NT>
 __host__ __device__ constexpr int cta_warps() { return NT == 1 || D == 64 ? 12 : 8; }
 constexpr int TILE = 32;            // keys of a tile
 constexpr int EXTRA = 3;            // what a segment's start costs a warp, in tiles
-constexpr float M_NONE = -1e30f;    // maximum of no parts (log2 units)
 constexpr float S_NONE = -3e38f;    // maximum of no keys (raw scores)
 constexpr float LAZY = 4.0f;        // log2 of how far a score may beat M
 
@@ -64,7 +63,7 @@ struct Cfg {
   static constexpr int NWC = cta_warps<D, NT>();
   static constexpr int STAGE = 2 * Gr::BYTES;
   static constexpr int COLS = 8 * NT;
-  static constexpr int PART = COLS * (D + 6);        // floats of a partial result: rows D + 4 apart, maxima, sums
+  static constexpr int PART = COLS * (D + 6);        // floats of a partial result (put_part)
   static constexpr int STG = 2;                      // stages of a warp's ring
   static constexpr int RING = NWC * STG * STAGE;
   static constexpr int JOIN = NWC * PART * 4;
@@ -141,6 +140,7 @@ struct Acc {
   float l[NT][2];           // this thread's part of the row sums
   float m[NT][2];           // running maximum of the raw scores, the same in all g
   float top[NT][2];         // a raw score above this raises m
+  float cq[NT][2];          // what a raw score is multiplied by (log2 units)
   int r;
   uint32_t vtop;            // highest scale byte that r allows, as the high bytes of two halves
 
@@ -149,11 +149,11 @@ struct Acc {
     const int byte = CF == CF_MX ? min(x + 3 + 127, 254) : min((x + 10) * 8 - 1, 0x7E);
     vtop = (uint32_t)byte * 0x01000100u | 0x00FF00FFu;
   }
-  __device__ __forceinline__ void set_m(int n, int e, float x, float cq) {
+  __device__ __forceinline__ void set_m(int n, int e, float x) {
     m[n][e] = x;
-    top[n][e] = x + LAZY / cq;
+    top[n][e] = x + LAZY / cq[n][e];
   }
-  __device__ __forceinline__ void reset(const float (&cq)[NT][2]) {
+  __device__ __forceinline__ void reset() {             // with cq set
     set_r(R_MIN);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -164,20 +164,18 @@ struct Acc {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         l[n][e] = 0.f;
-        set_m(n, e, S_NONE, cq[n][e]);
+        set_m(n, e, S_NONE);
       }
     }
   }
-  // After the last tile: m in log2 units, o and l in units of 2^m, the sums over all lanes.
-  __device__ __forceinline__ void finish(const float (&cq)[NT][2]) {
+  // After the last tile: the sums over all lanes.
+  __device__ __forceinline__ void finish() {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int x = 4; x < 32; x *= 2) l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], x);
-        m[n][e] = fmaf(m[n][e], cq[n][e], (float)r - 8.f);
-      }
   }
 };
 
@@ -256,8 +254,7 @@ struct TileScales {
 // does not see some key.
 template <int D, int CF, int NT, int NG, bool MASK>
 __device__ __forceinline__ void tile_step(const uint8_t* st, const uint32_t* sc, const uint32_t (&vs)[TileScales<D, CF>::BYTE_WORDS], int g0,
-                                          const uint2 (&q)[D / 16][NT], const float (&cq)[NT][2],
-                                          const int (&lim)[NT][2], int first, uint32_t bad, Acc<D, CF, NT>& a) {
+                                          const uint2 (&q)[D / 16][NT], const int (&lim)[NT][2], int first, uint32_t bad, Acc<D, CF, NT>& a) {
   using Gr = CacheGroup<D, CF>;
   using Ts = TileScales<D, CF>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -371,9 +368,9 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint32_t* sc,
 #pragma unroll
         for (int x = 4; x < 32; x *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
         m = fmaxf(a.m[n][e], m);
-        const float f = exp2f(fmaf(a.m[n][e] - m, cq[n][e], fr));
+        const float f = exp2f(fmaf(a.m[n][e] - m, a.cq[n][e], fr));
         a.l[n][e] *= f;
-        a.set_m(n, e, m, cq[n][e]);
+        a.set_m(n, e, m);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) { a.o[i][n][e] *= f; a.o[i][n][2 + e] *= f; }
       }
@@ -390,7 +387,7 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint32_t* sc,
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        x4[n][e] = ex2_approx(fmaf(s[gr][n][e] - a.m[n][e & 1], cq[n][e & 1], shift));
+        x4[n][e] = ex2_approx(fmaf(s[gr][n][e] - a.m[n][e & 1], a.cq[n][e & 1], shift));
         a.l[n][e & 1] += x4[n][e];
       }
     // E8M0 scales multiply in fp32 and the product is rounded; E4M3 ones multiply p as f16
@@ -464,18 +461,23 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint32_t* sc,
 }
 
 // ------------------------------------------------------------------------ results
+// What a row's sums say: its maximum raw score, the sum of exp2((s - m) cq + 8 - r) over its keys, and
+// the two numbers that go with them.
+struct Sum {
+  float m, l, r, cq;
+};
 // One finished row: where it goes, and what its sums say.
 struct Row {
   int64_t at, lse_at;
   float inv, lse;
   bool none;               // no key: zeros (none by the lengths, or none on a page of the pool: nothing was summed)
-  __device__ __forceinline__ Row(const CacheAttnArgs& p, int b, int hkv, int col, const Span& s, float m, float l) {
+  __device__ __forceinline__ Row(const CacheAttnArgs& p, int b, int hkv, int col, const Span& s, const Sum& sum) {
     const int i = row_of(p, col), h = hkv * p.G + col - i * p.G;
     at = b * p.os.b + i * p.os.s + h * p.os.h;
     lse_at = ((int64_t)b * p.Sq + i) * p.H + h;
-    none = limit_of(p, s, col) == 0 || l == 0.f;
-    inv = 1.0f / l;
-    lse = none ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+    none = limit_of(p, s, col) == 0 || sum.l == 0.f;
+    inv = 1.0f / sum.l;
+    lse = none ? -INFINITY : fmaf(sum.m, sum.cq, sum.r - 8.f + log2f(sum.l)) * 0.69314718055994530942f;
   }
   __device__ __forceinline__ void put(const CacheAttnArgs& p, int d, float2 o) const {
     o.x = none ? 0.f : o.x * inv;
@@ -489,7 +491,24 @@ struct Row {
 };
 
 // A partial result: the unnormalised rows [COLS][D + 4] (4 more, so that the lanes of a quad,
-// two columns apart, store to different banks), their maxima, their sums.
+// two columns apart, store to different banks; r and cq are in the first two of them), their
+// maxima, their sums.  The maxima are raw scores: in log2 units and with r in them, scores far
+// from zero would swallow r and the differences between parts.
+template <int D, int COLS>
+__device__ __forceinline__ void put_sum(float* part, int col, const Sum& s) {
+  *reinterpret_cast<float2*>(part + col * (D + 4) + D) = make_float2(s.r, s.cq);
+  part[COLS * (D + 4) + col] = s.m;
+  part[COLS * (D + 5) + col] = s.l;
+}
+template <int D, int COLS>
+__device__ __forceinline__ Sum get_sum(const float* part, int col) {
+  const float2 f = *reinterpret_cast<const float2*>(part + col * (D + 4) + D);
+  return {part[COLS * (D + 4) + col], part[COLS * (D + 5) + col], f.x, f.y};
+}
+// What a part counts in a join to maximum m and offset r: nothing if it saw no key.
+__device__ __forceinline__ float part_weight(const Sum& s, float m, float r) {
+  return s.l == 0.f ? 0.f : exp2f(fmaf(s.m - m, s.cq, s.r - r));
+}
 template <int D, int CF, int NT>
 __device__ __forceinline__ void put_part(float* part, const Acc<D, CF, NT>& a) {
   constexpr int COLS = 8 * NT, DP = D + 4;
@@ -502,10 +521,7 @@ __device__ __forceinline__ void put_part(float* part, const Acc<D, CF, NT>& a) {
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
         *reinterpret_cast<float2*>(part + col * DP + 16 * k + 2 * g) = make_float2(a.o[k][n][e], a.o[k][n][2 + e]);
-      if (g == 0) {
-        part[COLS * DP + col] = a.m[n][e];
-        part[COLS * (DP + 1) + col] = a.l[n][e];
-      }
+      if (g == 0) put_sum<D, COLS>(part, col, Sum{a.m[n][e], a.l[n][e], (float)a.r, a.cq[n][e]});
     }
 }
 
@@ -529,7 +545,6 @@ __device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const Span& sp
   constexpr int STG = C::STG;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   bool ok = true;
-  float cq[NT][2];                                      // what a raw score of a column is multiplied by (log2 units)
   int lim[NT][2];                                       // how many keys it sees
   const int tend = min(t1, (sp.kmax + TILE - 1) / TILE);
   // q's rows, on their way while the pages are looked up
@@ -608,11 +623,11 @@ __device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const Span& sp
     // accumulator columns: 2t, 2t + 1
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      cq[n][c] = fmaxf(p.scale_log2 * __shfl_sync(0xFFFFFFFFu, back, 4 * (2 * t + c)), 1.2e-38f);   // (0 times -inf is NaN)
+      a.cq[n][c] = fmaxf(p.scale_log2 * __shfl_sync(0xFFFFFFFFu, back, 4 * (2 * t + c)), 1.2e-38f);   // (0 times -inf is NaN)
       lim[n][c] = limit_of(p, sp, c0 + 8 * n + 2 * t + c);
     }
   }
-  a.reset(cq);
+  a.reset();
   const int min_lim = limit_of(p, sp, c0);            // the first column sees the fewest keys
 
   for (int tl = t0; tl < tend; ++tl) {
@@ -625,7 +640,7 @@ __device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const Span& sp
     TileScales<D, CF> ts(at, r.scales);
     __syncwarp();
     if (bad == 0 && (tl + 1) * TILE <= min_lim) {
-      tile_step<D, CF, NT, 2, false>(at, r.scales, ts.v, 0, q, cq, lim, tl * TILE, 0, a);
+      tile_step<D, CF, NT, 2, false>(at, r.scales, ts.v, 0, q, lim, tl * TILE, 0, a);
     } else {
       if (tl * TILE + lane >= sp.kmax || (bad >> (lane >> 4) & 1)) {     // no part in the offset of V's scales
 #pragma unroll
@@ -633,7 +648,7 @@ __device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const Span& sp
       }
 #pragma unroll 1
       for (int gr = 0; gr < 2 && tl * TILE + 16 * gr < sp.kmax; ++gr)
-        tile_step<D, CF, NT, 1, true>(at, r.scales, ts.v, gr, q, cq, lim, tl * TILE, bad, a);
+        tile_step<D, CF, NT, 1, true>(at, r.scales, ts.v, gr, q, lim, tl * TILE, bad, a);
     }
     __syncwarp();
     if (issued < tend) {
@@ -650,7 +665,7 @@ __device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const Span& sp
     }
     return false;
   }
-  a.finish(cq);
+  a.finish();
   return true;
 }
 
@@ -664,7 +679,7 @@ __device__ __forceinline__ void put_rows(const CacheAttnArgs& p, const Span& sp,
     for (int e = 0; e < 2; ++e) {
       const int col = c0 + 8 * n + 2 * t + e;
       if (col >= sp.qlen * p.G) continue;
-      const Row row(p, b, hkv, col, sp, a.m[n][e], a.l[n][e]);
+      const Row row(p, b, hkv, col, sp, Sum{a.m[n][e], a.l[n][e], (float)a.r, a.cq[n][e]});
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) row.put(p, 16 * k + 2 * g, make_float2(a.o[k][n][e], a.o[k][n][2 + e]));
       if (g == 0) row.put_lse(p);
@@ -676,21 +691,25 @@ __device__ __forceinline__ void put_rows(const CacheAttnArgs& p, const Span& sp,
 template <int D, int COLS>
 struct Column {
   static constexpr int DP = D + 4;
-  float m, l;
+  Sum s;
   float4 o[D / 64];
   template <class Part>
   __device__ __forceinline__ Column(Part part, int n, int col) {
     const int lane = threadIdx.x & 15;
-    const float* const mine = part(min(lane, n - 1));
-    const float mk = lane < n ? mine[COLS * DP + col] : M_NONE * 4.f;
-    l = lane < n ? mine[COLS * (DP + 1) + col] : 0.f;
-    m = mk;
+    s = get_sum<D, COLS>(part(min(lane, n - 1)), col);
+    if (lane >= n) s.l = 0.f;
+    float m = s.l == 0.f ? -INFINITY : s.m, r = s.l == 0.f ? -INFINITY : s.r;
 #pragma unroll
-    for (int x = 1; x < 16; x *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
-    const float w = lane < n ? exp2f(mk - m) : 0.f;
-    l = lane < n ? l * w : 0.f;
+    for (int x = 1; x < 16; x *= 2) {
+      m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+      r = fmaxf(r, __shfl_xor_sync(0xFFFFFFFFu, r, x));
+    }
+    const float w = part_weight(s, m, r);
+    s.m = m;
+    s.r = r;
+    s.l *= w;
 #pragma unroll
-    for (int x = 1; x < 16; x *= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
+    for (int x = 1; x < 16; x *= 2) s.l += __shfl_xor_sync(0xFFFFFFFFu, s.l, x);
 #pragma unroll
     for (int x = 0; x < D / 64; ++x) o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -709,7 +728,7 @@ struct Column {
   }
   __device__ __forceinline__ void put_row(const CacheAttnArgs& p, const Span& sp, int b, int hkv, int col) const {
     const int lane = threadIdx.x & 15;
-    const Row row(p, b, hkv, col, sp, m, l);
+    const Row row(p, b, hkv, col, sp, s);
 #pragma unroll
     for (int x = 0; x < D / 64; ++x) {
       row.put(p, 64 * x + 4 * lane, make_float2(o[x].x, o[x].y));
@@ -721,10 +740,7 @@ struct Column {
     const int lane = threadIdx.x & 15;
 #pragma unroll
     for (int x = 0; x < D / 64; ++x) *reinterpret_cast<float4*>(part + col * DP + 64 * x + 4 * lane) = o[x];
-    if (lane == 0) {
-      part[COLS * DP + col] = m;
-      part[COLS * (DP + 1) + col] = l;
-    }
+    if (lane == 0) put_sum<D, COLS>(part, col, s);
   }
 };
 
@@ -963,8 +979,8 @@ constexpr int JOIN_THREADS = 128, JOIN_Y = 4, JOIN_AHEAD = 16;
 template <int D, int NT>
 __global__ void __launch_bounds__(JOIN_THREADS) cache_join_kernel(const CacheAttnArgs p) {
   constexpr int COLS = 8 * NT, DP = D + 4, PART = COLS * (D + 6), CY = COLS / JOIN_Y, PER = CY * D / 2 / JOIN_THREADS + (CY * D / 2 < JOIN_THREADS);
-  extern __shared__ float weights[];                     // [parts][CY]: a part's maximum, then its weight; then its sums
-  __shared__ float sums[CY][2];                          // M and the sum of a column
+  extern __shared__ Sum part_sums[];                     // [parts][CY]; l is then a part's weight
+  __shared__ Sum sums[CY];
   griddep_launch();
   griddep_wait();                                        // the first kernel's results are complete
   const int4 st = p.starts[blockIdx.x];                  // segment, last CTA, its rows, its keys
@@ -986,27 +1002,30 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_join_kernel(const CacheAtt
     for (int k = 0; k < JOIN_AHEAD; ++k)
       if (k < n && c < CY) v[y][k] = *reinterpret_cast<const float2*>(part(k) + (first + c) * DP + d);
   }
-  float* const part_sums = weights + n * CY;
-  for (int x = threadIdx.x; x < n * CY; x += JOIN_THREADS) {
-    const float* const pk = part(x / CY) + first + x % CY;
-    weights[x] = pk[COLS * DP];
-    part_sums[x] = pk[COLS * (DP + 1)];
-  }
+  for (int x = threadIdx.x; x < n * CY; x += JOIN_THREADS) part_sums[x] = get_sum<D, COLS>(part(x / CY), first + x % CY);
   __syncthreads();
   if (threadIdx.x < CY * 32) {                           // a warp a column
     const int c = threadIdx.x / 32;
-    float m = M_NONE * 2.f, l = 0.f;
-    for (int k = lane; k < n; k += 32) m = fmaxf(m, weights[k * CY + c]);
-#pragma unroll
-    for (int x = 1; x < 32; x *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+    float m = -INFINITY, r = -INFINITY, l = 0.f;
     for (int k = lane; k < n; k += 32) {
-      const float f = exp2f(weights[k * CY + c] - m);
-      weights[k * CY + c] = f;
-      l = fmaf(f, part_sums[k * CY + c], l);
+      const Sum s = part_sums[k * CY + c];
+      m = fmaxf(m, s.l == 0.f ? -INFINITY : s.m);
+      r = fmaxf(r, s.l == 0.f ? -INFINITY : s.r);
+    }
+#pragma unroll
+    for (int x = 1; x < 32; x *= 2) {
+      m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+      r = fmaxf(r, __shfl_xor_sync(0xFFFFFFFFu, r, x));
+    }
+    for (int k = lane; k < n; k += 32) {
+      const Sum s = part_sums[k * CY + c];
+      const float f = part_weight(s, m, r);
+      part_sums[k * CY + c].l = f;
+      l = fmaf(f, s.l, l);
     }
 #pragma unroll
     for (int x = 1; x < 32; x *= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
-    if (lane == 0) { sums[c][0] = m; sums[c][1] = l; }
+    if (lane == 0) sums[c] = Sum{m, l, r, part_sums[c].cq};
   }
   __syncthreads();
 #pragma unroll
@@ -1017,18 +1036,18 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_join_kernel(const CacheAtt
 #pragma unroll
     for (int k = 0; k < JOIN_AHEAD; ++k)
       if (k < n) {
-        const float f = weights[k * CY + c];
+        const float f = part_sums[k * CY + c].l;
         o.x = fmaf(f, v[y][k].x, o.x);
         o.y = fmaf(f, v[y][k].y, o.y);
       }
 #pragma unroll 8
     for (int k = JOIN_AHEAD; k < n; ++k) {
-      const float f = weights[k * CY + c];
+      const float f = part_sums[k * CY + c].l;
       const float2 u = *reinterpret_cast<const float2*>(part(k) + (first + c) * DP + d);
       o.x = fmaf(f, u.x, o.x);
       o.y = fmaf(f, u.y, o.y);
     }
-    const Row row(p, b, hkv, c0 + c, sp, sums[c][0], sums[c][1]);
+    const Row row(p, b, hkv, c0 + c, sp, sums[c]);
     row.put(p, d, o);
     if (d == 0) row.put_lse(p);
   }
@@ -1075,7 +1094,7 @@ cudaError_t launch(const CacheAttnArgs& a, int sms, cudaStream_t st) {
   e = launch_early(cache_attn_kernel<D, CF, NT>, dim3(sms), C::NWC * 32, C::SMEM, st, a);
   if (e != cudaSuccess) return e;
   return launch_early(cache_join_kernel<D, NT>, dim3(sms, JOIN_Y), JOIN_THREADS,
-                      (size_t)2 * (sms + 2) * (C::COLS / JOIN_Y) * sizeof(float), st, a);
+                      (size_t)(sms + 2) * (C::COLS / JOIN_Y) * sizeof(Sum), st, a);
 }
 
 }  // namespace

@@ -72,3 +72,59 @@ def test_infinite_queries(lens, Hkv, width):
     assert bool(torch.isnan(out[:, 0, 1]).all()) and bool(torch.isnan(out[:, 1, 2]).all()) and int(torch.isnan(lse).sum()) == 2 * B
     out, lse = run_attention(fsa, q, cache, torch.full_like(table, -1), lens, causal=False)
     assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+
+
+# ---------------------------------------------------------------------------- far scores
+@pytest.mark.parametrize("lens,Hkv,width", SPLITS)
+@pytest.mark.parametrize("kind", ["scale", "keys", "high"])
+@pytest.mark.parametrize("fmt", ["E2M1", "NVFP4"])
+def test_far_scores_of_split_rows(fmt, kind, lens, Hkv, width):
+    """All scores of a row equal and far below (or above) zero: the mean of V, however the keys
+    are split.  Every weight is exactly 1, so the rounding of p times V's scale is all there is
+    besides fp32 sums (2^-18)."""
+    fsa = _fsa()
+    if kind == "keys" and fmt == "NVFP4":
+        pytest.skip("keys of 2^113 are beyond NVFP4's scales")
+    g = gen(95)
+    B, D, S, H = len(lens), 64, max(lens), 2 * Hkv
+    table, pages = make_table(g, lens, 16)
+    table = wide_table(table, width)
+    cache = fsa.empty_cache(pages, 16, Hkv, D, fmt)
+    k, v = torch.zeros(B, S, Hkv, D, dtype=torch.bfloat16, device="cuda"), normal(g, B, S, Hkv, D)
+    k[..., 0] = 2.0 ** 113 if kind == "keys" else 4.0
+    fsa.fsa_cache_append(cache, k, v, table, i32(lens), i32(lens))
+    q = torch.zeros(B, 1, H, D, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0 if kind == "high" else -1.0
+    scale = 1.0 if kind == "keys" else 1e30
+    out, lse = torch.empty(B, 1, H, D, device="cuda"), torch.empty(B, 1, H, device="cuda")
+    fsa.fsa_attention_cache(q, cache, table, i32(lens), scale=scale, out=out, lse=lse)
+    score = float(q[0, 0, 0, 0]) * float(ref.rounded(k[0, 0, 0], fmt)[0]) * scale        # (NVFP4 keeps 4 as 4.125)
+    for b, n in enumerate(lens):
+        vq = ref.rounded(v[b, :n], fmt).repeat_interleave(2, dim=1)
+        tol = (2.0 ** -10 + 2.0 ** -18) * vq.abs().mean(0)
+        assert bool(((out[b, 0].double() - vq.mean(0)).abs() <= tol).all()), b
+        assert bool(((lse[b, 0].double() / score - 1).abs() <= 2.0 ** -18).all())
+
+
+def test_far_scores_beside_pages_outside():
+    """Parts of a row without a key do not count in the join, wherever the others' scores lie."""
+    fsa = _fsa()
+    g = gen(97)
+    n, D, page = 6000, 64, 16
+    table, pages = make_table(g, [n], page)
+    cache = fsa.empty_cache(pages, page, 1, D, "E2M1")
+    k, v = torch.zeros(1, n, 1, D, dtype=torch.bfloat16, device="cuda"), normal(g, 1, n, 1, D)
+    k[..., 0] = 4.0
+    fsa.fsa_cache_append(cache, k, v, table, i32([n]))
+    q = torch.zeros(1, 1, 2, D, dtype=torch.bfloat16, device="cuda")
+    for first, last in ((0, 3000), (3000, n), (16, n - 16), (0, n - 16)):
+        t = table.clone()
+        t[0, first // page:last // page] = -1
+        live = torch.ones(n, dtype=torch.bool, device="cuda")
+        live[first // page * page:last // page * page] = False
+        vq = ref.rounded(v[0], "E2M1")[live]
+        for sign, scale in ((-1.0, 1e30), (1.0, 1e30), (-1.0, 1e-30), (-1.0, 0.125)):
+            q[..., 0] = sign
+            out = fsa.fsa_attention_cache(q, cache, t, i32([n]), scale=scale)
+            tol = (2.0 ** -10 + 2.0 ** -18) * vq.abs().mean(0)
+            assert bool(((out[0, 0].double() - vq.mean(0)).abs() <= tol).all()), (first, last, sign, scale)
