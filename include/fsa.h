@@ -480,8 +480,9 @@ int fsa_cache_read(const fsa_cache* cache, void* k, void* v, const fsa_strides* 
  * already.  A row that sees nothing gives zeros (lse -inf).  Rows behind q_lens[b] are not
  * written.  The lengths are read on the device: a captured call follows them.
  *   q, out: [B][Sq][H][D] strided, 16-byte aligned; out bf16 or fp32 by out_dtype
- *   scale: of any sign, |scale| <= 1e30; keys of magnitudes up to 2^115 (beyond, fp32 scores
- *     may overflow)
+ *   scale: of any sign, |scale| <= 1e30.  Keys of magnitudes up to 2^115, scale times q finite
+ *     in fp32, and |scale| times the sum of |q k| below 2^126: a row beyond that may be NaN or
+ *     zeros; the rows beside it are as without it
  *   lse: optional fp32 [B][Sq][H], natural log of the sum of exp(scale q k)
  *   lens: int32 [B], cut to max_pages * page_size; q_lens: int32 [B], cut to 0..Sq, or NULL (Sq)
  *   workspace: fsa_attention_cache_workspace bytes, 16-byte aligned; needs no initial

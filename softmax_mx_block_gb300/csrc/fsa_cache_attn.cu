@@ -151,7 +151,7 @@ struct Acc {
   }
   __device__ __forceinline__ void set_m(int n, int e, float x) {
     m[n][e] = x;
-    top[n][e] = x + LAZY / cq[n][e];
+    top[n][e] = x + fminf(LAZY / cq[n][e], 3.4e38f);   // (finite from no keys on: scores of fp32's top quarter raise m)
   }
   __device__ __forceinline__ void reset() {             // with cq set
     set_r(R_MIN);
@@ -623,7 +623,7 @@ __device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const Span& sp
     // accumulator columns: 2t, 2t + 1
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      a.cq[n][c] = fmaxf(p.scale_log2 * __shfl_sync(0xFFFFFFFFu, back, 4 * (2 * t + c)), 1.2e-38f);   // (0 times -inf is NaN)
+      a.cq[n][c] = fmaxf(p.scale_log2 * __shfl_sync(0xFFFFFFFFu, back, 4 * (2 * t + c)), 1.4e-45f);   // (0 times -inf is NaN)
       lim[n][c] = limit_of(p, sp, c0 + 8 * n + 2 * t + c);
     }
   }

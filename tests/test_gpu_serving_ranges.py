@@ -128,3 +128,38 @@ def test_far_scores_beside_pages_outside():
             out = fsa.fsa_attention_cache(q, cache, t, i32([n]), scale=scale)
             tol = (2.0 ** -10 + 2.0 ** -18) * vq.abs().mean(0)
             assert bool(((out[0, 0].double() - vq.mean(0)).abs() <= tol).all()), (first, last, sign, scale)
+
+
+@pytest.mark.parametrize("lens,Hkv,width", SPLITS)
+@pytest.mark.parametrize("scale", [0.6, 0.125, 1e-3])
+def test_tiny_queries_huge_keys(scale, lens, Hkv, width):
+    """q at the least normal bf16 number, keys at 2^115: the factor of the scores (below fp32's
+    normal range) is the scale's."""
+    fsa = _fsa()
+    g = gen(99)
+    B, D, S = len(lens), 128, max(lens)
+    table, pages = make_table(g, lens, 16)
+    table = wide_table(table, width)
+    cache = fsa.empty_cache(pages, 16, Hkv, D, "E2M1")
+    way = torch.where(torch.rand(B, S, Hkv, 1, generator=g, device="cuda") < 0.5, -1.0, 1.0)
+    k = (way * 2.0 ** 115).expand(B, S, Hkv, D).to(torch.bfloat16)
+    v = (way + 0.25 * torch.randn(B, S, Hkv, D, generator=g, device="cuda")).to(torch.bfloat16)
+    fsa.fsa_cache_append(cache, k, v, table, i32(lens), i32(lens))
+    q = torch.full((B, 2, 4 * Hkv, D), 1.984375 * 2.0 ** -126, device="cuda").to(torch.bfloat16)
+    q[:, 1] *= 2.0 ** -4
+    run_attention(fsa, q, cache, table, lens, causal=False, scale=scale)
+
+
+def test_queries_beyond_the_range_stay_alone():
+    """Where scale times q leaves fp32 a row may be NaN; the rows beside it are not touched."""
+    fsa = _fsa()
+    g = gen(101)
+    for lens, width in (([300], 20), ([5000], 320)):
+        cache, table, _, _ = filled_cache(fsa, g, lens, 16, 1, 64, "E2M1")
+        table = wide_table(table, width)
+        q = normal(g, 1, 1, 8, 64) * 1e-30
+        want = fsa.fsa_attention_cache(q, cache, table, i32(lens), scale=1e30)
+        q[0, 0, 3] = q[0, 0, 3] * 1e30 * 1e30
+        out = fsa.fsa_attention_cache(q, cache, table, i32(lens), scale=1e30)
+        keep = torch.arange(8, device="cuda") != 3
+        assert torch.equal(out[:, :, keep], want[:, :, keep]) and bool(torch.isfinite(want).all())
