@@ -19,7 +19,9 @@
 //   - A tile's scales are unpacked once, a token a lane, through shared memory: every lane of
 //     a quad needs the same ones (13% of the arithmetic pipe with E8M0, 22% with E4M3).
 //   - The f16 probabilities carry 2^(8 - r), r the running maximum exponent of V's scales,
-//     so that p * scale stays below 2^15.  The running maximum m of the raw scores is raised
+//     so that p * scale stays below 2^15.  With E8M0 scales r spans fp32's whole range: what of
+//     it exceeds 2^40 divides the unpacked scales instead, so that no weight down to 2^-94 of the
+//     largest is flushed from the sum.  The running maximum m of the raw scores is raised
 //     only when a score beats it by more than 2^4 in the softmax (then the sums are
 //     rescaled), so most tiles need one vote and no reduction over lanes.  Both offsets
 //     multiply numerator and denominator alike and cancel.
@@ -129,6 +131,13 @@ __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t two_bytes) {     // the 
   return r;
 }
 
+// The part of the offset r that the probabilities and their sum carry, and the part that divides
+// V's scales.  2^40: p goes down to 2^(8 - 40 - 94), fp32's end, and from the least r, -80, a sum is
+// brought to the highest by one factor, 2^-120.
+constexpr int R_CAP = 40;
+template <class R>
+__device__ __forceinline__ R p_offset(R r) { return r < (R)R_CAP ? r : (R)R_CAP; }
+
 // One warp's running state for one (sequence, kv head, pass of columns).  A thread holds,
 // of n-tile n, columns 8n + 2t and + 1 and, of m-tile i, dims 16i + 2g and + 1.
 template <int D, int CF, int NT>
@@ -141,11 +150,14 @@ struct Acc {
   float m[NT][2];           // running maximum of the raw scores, the same in all g
   float top[NT][2];         // a raw score above this raises m
   float cq[NT][2];          // what a raw score is multiplied by (log2 units)
-  int r;
+  int r;                    // o holds exp2((s - m) cq + 8 - r) times values, l the same with p_offset(r)
+  float shift;              // 8 - p_offset(r)
   uint32_t vtop;            // highest scale byte that r allows, as the high bytes of two halves
 
+  static __device__ __forceinline__ int offset(int x) { return CF == CF_MX ? p_offset(x) : x; }     // (E4M3's r: 0 to 9)
   __device__ __forceinline__ void set_r(int x) {
     r = x;
+    shift = 8.f - (float)offset(x);
     const int byte = CF == CF_MX ? min(x + 3 + 127, 254) : min((x + 10) * 8 - 1, 0x7E);
     vtop = (uint32_t)byte * 0x01000100u | 0x00FF00FFu;
   }
@@ -233,6 +245,19 @@ struct TileScales {
     unpack(k, dst);
     unpack(v, dst + TILE * SB);
   }
+  // V's scales of this lane's token times 2^e, -88 <= e <= 88 (all lanes together)
+  static __device__ __forceinline__ void shift_v(uint32_t* dst, int e) {
+    const float f = __uint_as_float((uint32_t)(127 + e) << 23);
+    uint32_t w[SB];
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+    row(dst, lane, w);
+#pragma unroll
+    for (int q = 0; q < PIECES; ++q)
+#pragma unroll
+      for (int x = 0; x < PW; ++x) dst[(q * TILE + lane) * PW + x] = __float_as_uint(__uint_as_float(w[q * PW + x]) * f);
+    __syncwarp();
+  }
   // a row's scales: word x of token tok, of K (from = sc) or V (from = sc + TILE * SB)
   static __device__ __forceinline__ void row(const uint32_t* from, int tok, uint32_t* f) {
 #pragma unroll
@@ -253,7 +278,7 @@ struct TileScales {
 // first: position of the tile's first key; bad: groups without a page.  MASK: some column
 // does not see some key.
 template <int D, int CF, int NT, int NG, bool MASK>
-__device__ __forceinline__ void tile_step(const uint8_t* st, const uint32_t* sc, const uint32_t (&vs)[TileScales<D, CF>::BYTE_WORDS], int g0,
+__device__ __forceinline__ void tile_step(const uint8_t* st, uint32_t* sc, const uint32_t (&vs)[TileScales<D, CF>::BYTE_WORDS], int g0,
                                           const uint2 (&q)[D / 16][NT], const int (&lim)[NT][2], int first, uint32_t bad, Acc<D, CF, NT>& a) {
   using Gr = CacheGroup<D, CF>;
   using Ts = TileScales<D, CF>;
@@ -359,7 +384,11 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint32_t* sc,
     v = __reduce_max_sync(0xFFFFFFFFu, v);
     const int r_old = a.r;
     if (v > (a.vtop >> 24)) a.set_r(max(Acc<D, CF, NT>::R_MIN, CF == CF_MX ? (int)v - 126 : (int)(v >> 3) - 6));   // 2^r > scale
-    const float fr = (float)(r_old - a.r);
+    const int dr = r_old - a.r, dl = a.offset(r_old) - a.offset(a.r);
+    const float fr = (float)dr, fl = (float)dl;
+    if constexpr (CF == CF_MX) {                     // this tile's scales are divided by what r_old had over the cap
+      if (dr != dl) Ts::shift_v(sc + TILE * Gr::SB, dr - dl);
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -369,7 +398,7 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint32_t* sc,
         for (int x = 4; x < 32; x *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
         m = fmaxf(a.m[n][e], m);
         const float f = exp2f(fmaf(a.m[n][e] - m, a.cq[n][e], fr));
-        a.l[n][e] *= f;
+        a.l[n][e] *= CF == CF_MX ? exp2f(fmaf(a.m[n][e] - m, a.cq[n][e], fl)) : f;
         a.set_m(n, e, m);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) { a.o[i][n][e] *= f; a.o[i][n][2 + e] *= f; }
@@ -378,7 +407,6 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint32_t* sc,
 
   // probabilities (the difference first: its error is relative to it, however large the scores),
   // and the products with V
-  const float shift = 8.f - (float)a.r;
 #pragma unroll
   for (int gr = 0; gr < NG; ++gr) {
     const uint8_t* base = st + (g0 + gr) * Gr::BYTES;
@@ -387,7 +415,7 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint32_t* sc,
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        x4[n][e] = ex2_approx(fmaf(s[gr][n][e] - a.m[n][e & 1], a.cq[n][e & 1], shift));
+        x4[n][e] = ex2_approx(fmaf(s[gr][n][e] - a.m[n][e & 1], a.cq[n][e & 1], a.shift));
         a.l[n][e & 1] += x4[n][e];
       }
     // E8M0 scales multiply in fp32 and the product is rounded; E4M3 ones multiply p as f16
@@ -461,8 +489,8 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, const uint32_t* sc,
 }
 
 // ------------------------------------------------------------------------ results
-// What a row's sums say: its maximum raw score, the sum of exp2((s - m) cq + 8 - r) over its keys, and
-// the two numbers that go with them.
+// What a row's sums say: its maximum raw score, the sum of exp2((s - m) cq + 8 - p_offset(r)) over its
+// keys, and the two numbers that go with them.
 struct Sum {
   float m, l, r, cq;
 };
@@ -476,8 +504,8 @@ struct Row {
     at = b * p.os.b + i * p.os.s + h * p.os.h;
     lse_at = ((int64_t)b * p.Sq + i) * p.H + h;
     none = limit_of(p, s, col) == 0 || sum.l == 0.f;
-    inv = 1.0f / sum.l;
-    lse = none ? -INFINITY : fmaf(sum.m, sum.cq, sum.r - 8.f + log2f(sum.l)) * 0.69314718055994530942f;
+    inv = exp2f(sum.r - p_offset(sum.r)) / sum.l;
+    lse = none ? -INFINITY : fmaf(sum.m, sum.cq, p_offset(sum.r) - 8.f + log2f(sum.l)) * 0.69314718055994530942f;
   }
   __device__ __forceinline__ void put(const CacheAttnArgs& p, int d, float2 o) const {
     o.x = none ? 0.f : o.x * inv;
@@ -505,10 +533,14 @@ __device__ __forceinline__ Sum get_sum(const float* part, int col) {
   const float2 f = *reinterpret_cast<const float2*>(part + col * (D + 4) + D);
   return {part[COLS * (D + 4) + col], part[COLS * (D + 5) + col], f.x, f.y};
 }
-// What a part counts in a join to maximum m and offset r: nothing if it saw no key.
-__device__ __forceinline__ float part_weight(const Sum& s, float m, float r) {
-  return s.l == 0.f ? 0.f : exp2f(fmaf(s.m - m, s.cq, s.r - r));
-}
+// What a part's rows and its sum count in a join to maximum m and offset r: nothing if it saw no key.
+struct PartWeight {
+  float o, l;
+  __device__ __forceinline__ PartWeight(const Sum& s, float m, float r) {
+    o = s.l == 0.f ? 0.f : exp2f(fmaf(s.m - m, s.cq, s.r - r));
+    l = s.l == 0.f ? 0.f : exp2f(fmaf(s.m - m, s.cq, p_offset(s.r) - p_offset(r)));
+  }
+};
 template <int D, int CF, int NT>
 __device__ __forceinline__ void put_part(float* part, const Acc<D, CF, NT>& a) {
   constexpr int COLS = 8 * NT, DP = D + 4;
@@ -638,6 +670,7 @@ __device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const Span& sp
     const uint32_t bad = (bads >> (2 * s)) & 3;
     const uint8_t* at = r.mem + s * C::STAGE;
     TileScales<D, CF> ts(at, r.scales);
+    if (CF == CF_MX && a.shift == 8.f - R_CAP) ts.shift_v(r.scales + TILE * Gr::SB, R_CAP - a.r);
     __syncwarp();
     if (bad == 0 && (tl + 1) * TILE <= min_lim) {
       tile_step<D, CF, NT, 2, false>(at, r.scales, ts.v, 0, q, lim, tl * TILE, 0, a);
@@ -704,10 +737,10 @@ struct Column {
       m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
       r = fmaxf(r, __shfl_xor_sync(0xFFFFFFFFu, r, x));
     }
-    const float w = part_weight(s, m, r);
+    const PartWeight w(s, m, r);
     s.m = m;
     s.r = r;
-    s.l *= w;
+    s.l *= w.l;
 #pragma unroll
     for (int x = 1; x < 16; x *= 2) s.l += __shfl_xor_sync(0xFFFFFFFFu, s.l, x);
 #pragma unroll
@@ -715,7 +748,7 @@ struct Column {
 #pragma unroll 4
     for (int k = 0; k < n; ++k) {
       const float* const pk = part(k) + col * DP + 4 * lane;
-      const float f = __shfl_sync(0xFFFFFFFFu, w, k, 16);
+      const float f = __shfl_sync(0xFFFFFFFFu, w.o, k, 16);
 #pragma unroll
       for (int x = 0; x < D / 64; ++x) {
         const float4 v = *reinterpret_cast<const float4*>(pk + 64 * x);
@@ -979,7 +1012,7 @@ constexpr int JOIN_THREADS = 128, JOIN_Y = 4, JOIN_AHEAD = 16;
 template <int D, int NT>
 __global__ void __launch_bounds__(JOIN_THREADS) cache_join_kernel(const CacheAttnArgs p) {
   constexpr int COLS = 8 * NT, DP = D + 4, PART = COLS * (D + 6), CY = COLS / JOIN_Y, PER = CY * D / 2 / JOIN_THREADS + (CY * D / 2 < JOIN_THREADS);
-  extern __shared__ Sum part_sums[];                     // [parts][CY]; l is then a part's weight
+  extern __shared__ Sum part_sums[];                     // [parts][CY]; l is then the weight of a part's rows
   __shared__ Sum sums[CY];
   griddep_launch();
   griddep_wait();                                        // the first kernel's results are complete
@@ -1019,9 +1052,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_join_kernel(const CacheAtt
     }
     for (int k = lane; k < n; k += 32) {
       const Sum s = part_sums[k * CY + c];
-      const float f = part_weight(s, m, r);
-      part_sums[k * CY + c].l = f;
-      l = fmaf(f, s.l, l);
+      const PartWeight f(s, m, r);
+      part_sums[k * CY + c].l = f.o;
+      l = fmaf(f.l, s.l, l);
     }
 #pragma unroll
     for (int x = 1; x < 32; x *= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);

@@ -163,3 +163,54 @@ def test_queries_beyond_the_range_stay_alone():
         out = fsa.fsa_attention_cache(q, cache, table, i32(lens), scale=1e30)
         keep = torch.arange(8, device="cuda") != 3
         assert torch.equal(out[:, :, keep], want[:, :, keep]) and bool(torch.isfinite(want).all())
+
+
+# ---------------------------------------------------------------------------- far values
+@pytest.mark.parametrize("top", [90, 100, 120, 127])
+@pytest.mark.parametrize("lens,width", [([600], 40), ([20000], 1300)])
+def test_huge_values_beside_small_weights(lens, width, top):
+    """One key of weight 1, all others of 2^-15 or so, V at 2^top: the small weights count in the
+    sum and in the product."""
+    fsa = _fsa()
+    g = gen(103)
+    n, D, Hkv = lens[0], 128, 2
+    table, pages = make_table(g, lens, 16)
+    table = wide_table(table, width)
+    cache = fsa.empty_cache(pages, 16, Hkv, D, "E2M1")
+    k = torch.zeros(1, n, Hkv, D, dtype=torch.bfloat16, device="cuda")
+    v = (-torch.rand(1, n, Hkv, D, generator=g, device="cuda") * 2.0 ** top).to(torch.bfloat16)
+    q = torch.zeros(1, 1, 8, D, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    for sink in (0, n // 2, n - 1):
+        k.zero_()
+        k[0, sink, :, 0] = 1.0
+        vs = v.clone()
+        vs[0, sink] = 1.5 * 2.0 ** top
+        fsa.fsa_cache_append(cache, k, vs, table, i32(lens))
+        run_attention(fsa, q, cache, table, lens, scale=math.log(min(n, 16384)))
+        run_attention(fsa, q, cache, table, lens, scale=16.0, dtype="bf16")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,Hkv,width", SPLITS)
+@pytest.mark.parametrize("kind", ["rising", "falling", "any", "after zeros"])
+def test_values_of_every_size(kind, lens, Hkv, width, D):
+    """V from 2^-80 to 2^127, a size a token, in every order: the running offset of V's scales
+    moves over its whole range without losing the sum of the weights."""
+    fsa = _fsa()
+    g = gen(105)
+    B, S = len(lens), max(lens)
+    table, pages = make_table(g, lens, 16)
+    table = wide_table(table, width)
+    cache = fsa.empty_cache(pages, 16, Hkv, D, "E2M1")
+    at = torch.linspace(-80, 126.9, S, device="cuda")
+    at = {"rising": at, "falling": at.flip(0), "any": at[torch.randperm(S, generator=g, device="cuda")],
+          "after zeros": torch.where(torch.arange(S, device="cuda") < S // 2, -200.0, 126.0)}[kind]
+    size = torch.exp2(at.double())[None, :, None, None]
+    v = (size * (1 + torch.rand(B, S, Hkv, D, generator=g, device="cuda"))).clamp(max=3.3e38)
+    v = v * torch.where(torch.rand(B, S, Hkv, D, generator=g, device="cuda") < 0.5, -1, 1)
+    k = normal(g, B, S, Hkv, D)
+    fsa.fsa_cache_append(cache, k, v.to(torch.bfloat16), table, i32(lens), i32(lens))
+    for Sq in (1, 4):
+        run_attention(fsa, normal(g, B, Sq, 4 * Hkv, D), cache, table, lens)
+    run_attention(fsa, normal(g, B, 1, 4 * Hkv, D) * 4, cache, table, lens, dtype="bf16")
