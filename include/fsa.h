@@ -439,7 +439,7 @@ typedef struct {
   void*   pages;       /* device, 16-byte aligned, num_pages * fsa_cache_page_bytes */
   int64_t num_pages;   /* <= 2^31 - 1 */
   int32_t page_size;   /* tokens: a power of two, 16..1024 */
-  int32_t Hkv, D;      /* D 64 or 128 */
+  int32_t Hkv, D;      /* Hkv 1..65535, D 64 or 128 */
   int32_t fmt;         /* FSA_FMT_E2M1 or FSA_FMT_NVFP4 */
 } fsa_cache;
 
@@ -492,7 +492,7 @@ int fsa_cache_read(const fsa_cache* cache, void* k, void* v, const fsa_strides* 
  *   status: optional device int32: FSA_ERR_INVALID_ARG where a page number lay outside the
  *     pool (its keys are not seen), FSA_ERR_TIMEOUT where a wait for a copy ran out
  *     (timeout_ms; 0: 4000), the output then being undefined
- * B * Sq * H <= 2^27; B * Hkv * (Sq * H/Hkv / 8 + 1) * (max_pages * page_size / 32 + 9) <= 2^31
+ * B * Sq * H <= 2^27; B * Hkv * (Sq * H/Hkv / 8 + 1) * (max_pages * page_size / 32 + 9) < 2^31
  * (the kernels count tiles over all sequences in 32 bits).  Errors: FSA_ERR_INVALID_ARG, FSA_ERR_UNSUPPORTED_FMT,
  * FSA_ERR_NO_DEVICE, FSA_ERR_LAUNCH.  The work is laid out for the current device, which
  * must be the one of the pointers and the stream. */

@@ -102,7 +102,7 @@ bool sm_count(int* sms) {
 // keys (and what a segment's start weighs, at most 8) in 32 bits.
 bool attn_shape_ok(int B, int H, int Hkv, int Sq, int D, int max_pages, int page_size) {
   if (!(B > 0 && H > 0 && Hkv > 0 && H % Hkv == 0 && Sq > 0 && (D == 64 || D == 128) && pages_ok(max_pages, page_size) &&
-        (int64_t)B * H <= INT_MAX / 16 / Sq))
+        (int64_t)B * H <= (1 << 27) / Sq))
     return false;
   const int64_t passes = ((int64_t)Sq * (H / Hkv) + 7) / 8, tiles = ((int64_t)max_pages * page_size + 31) / 32 + 8;
   return (int64_t)B * Hkv <= INT_MAX / passes / tiles;
