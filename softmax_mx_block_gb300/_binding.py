@@ -121,7 +121,7 @@ def load(build_if_missing: bool = True):
     global _lib
     with _lock:
         if _lib is None:
-            path = _build.build() if build_if_missing else _build.LIB
+            path = _build.build_library() if build_if_missing else _build.LIB
             if not os.path.exists(path):
                 raise RuntimeError(f"libfsa.so not found at {path}")
             L = ctypes.CDLL(path)
@@ -561,12 +561,13 @@ def fsa_tune_delta(stats: list, deltas: list, target_rate=0.01, step=4.0, max_de
 # These calls are short (a decode step's kernels run for a few microseconds), so their
 # checks and marshalling are compiled (csrc/fsa_torch.cpp).
 def _serving():
-    """The extension module _fsa_torch (built with the library)."""
+    """The extension module _fsa_torch (built first if it is missing, stale or of another torch)."""
     global _torch_module
     if _torch_module is None:
         load()
-        loader = importlib.machinery.ExtensionFileLoader("_fsa_torch", _build.TORCH_MODULE)
-        spec = importlib.util.spec_from_file_location("_fsa_torch", _build.TORCH_MODULE, loader=loader)
+        path = _build.build_torch_module()
+        loader = importlib.machinery.ExtensionFileLoader("_fsa_torch", path)
+        spec = importlib.util.spec_from_file_location("_fsa_torch", path, loader=loader)
         module = importlib.util.module_from_spec(spec)
         loader.exec_module(module)
         module.set_error(FsaError)
