@@ -473,8 +473,8 @@ int fsa_cache_read(const fsa_cache* cache, void* k, void* v, const fsa_strides* 
  * prompt): O = softmax(scale Q K^T) V on the values the cache stands for; q is not
  * quantised, sums and softmax statistics are fp32, probabilities times V's scales are
  * rounded to f16 before the product with the codes of V (2^-11 relative, 2^-10 with
- * NVFP4; for products far below the largest block scale in V, an absolute 2^-33 of it, or of
- * 2^-80 where all E8M0 scales are smaller; with NVFP4 block scales over 8 in V times the
+ * NVFP4; for products far below the largest block scale in V that the row sees, an absolute
+ * 2^-33 of it, or of 2^-80 where all E8M0 scales are smaller; with NVFP4 block scales over 8 in V times the
  * scale).  V may have any magnitude that bf16 has.  Query head h reads kv head h / (H/Hkv).  Row i < q_lens[b] of sequence b
  * stands at position lens[b] - q_lens[b] + i and sees the keys up to its own position
  * (causal) or all lens[b]; lens counts the rows' own tokens, which are in the cache

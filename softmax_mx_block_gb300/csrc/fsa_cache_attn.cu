@@ -137,6 +137,8 @@ __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t two_bytes) {     // the 
 constexpr int R_CAP = 40;
 template <class R>
 __device__ __forceinline__ R p_offset(R r) { return r < (R)R_CAP ? r : (R)R_CAP; }
+// 1 over the part that divides V's scales
+__device__ __forceinline__ float excess(int r) { return __uint_as_float((uint32_t)(127 + p_offset(r) - r) << 23); }
 
 // One warp's running state for one (sequence, kv head, pass of columns).  A thread holds,
 // of n-tile n, columns 8n + 2t and + 1 and, of m-tile i, dims 16i + 2g and + 1.
@@ -153,13 +155,21 @@ struct Acc {
   int r;                    // o holds exp2((s - m) cq + 8 - r) times values, l the same with p_offset(r)
   float shift;              // 8 - p_offset(r)
   uint32_t vtop;            // highest scale byte that r allows, as the high bytes of two halves
+  // The columns' offsets: r, but for rows of which some do not see some keys of the last tiles.
+  // There each column goes by the keys it sees, so that a value behind a row does not take
+  // bits from it.
+  int rc[NT][2];
 
   static __device__ __forceinline__ int offset(int x) { return CF == CF_MX ? p_offset(x) : x; }     // (E4M3's r: 0 to 9)
   __device__ __forceinline__ void set_r(int x) {
     r = x;
     shift = 8.f - (float)offset(x);
-    const int byte = CF == CF_MX ? min(x + 3 + 127, 254) : min((x + 10) * 8 - 1, 0x7E);
-    vtop = (uint32_t)byte * 0x01000100u | 0x00FF00FFu;
+    vtop = (uint32_t)allowed(x) * 0x01000100u | 0x00FF00FFu;
+  }
+  static __device__ __forceinline__ int allowed(int x) { return CF == CF_MX ? min(x + 3 + 127, 254) : min((x + 10) * 8 - 1, 0x7E); }
+  // the offset to go on with from x when a scale byte v comes: 2^r > scale
+  static __device__ __forceinline__ int raised(int x, int v) {
+    return v > allowed(x) ? max(R_MIN, CF == CF_MX ? v - 126 : (v >> 3) - 6) : x;
   }
   __device__ __forceinline__ void set_m(int n, int e, float x) {
     m[n][e] = x;
@@ -275,9 +285,10 @@ struct TileScales {
 
 // NG groups of 16 keys of a tile, from group g0 on, in shared memory.  sc: the tile's unpacked
 // scales; vs: V's scale bytes of this lane's token (0 for a token that no column sees);
-// first: position of the tile's first key; bad: groups without a page.  MASK: some column
-// does not see some key.
-template <int D, int CF, int NT, int NG, bool MASK>
+// first: position of the tile's first key; bad: groups without a page.  MASK 1: some column
+// does not see some key, but those with rows see the same ones; 2: they do not, and each has an
+// offset of its own.
+template <int D, int CF, int NT, int NG, int MASK>
 __device__ __forceinline__ void tile_step(const uint8_t* st, uint32_t* sc, const uint32_t (&vs)[TileScales<D, CF>::BYTE_WORDS], int g0,
                                           const uint2 (&q)[D / 16][NT], const int (&lim)[NT][2], int first, uint32_t bad, Acc<D, CF, NT>& a) {
   using Gr = CacheGroup<D, CF>;
@@ -381,18 +392,34 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, uint32_t* sc, const
       const uint32_t byte = (vs[x / 4] >> (8 * (x % 4))) & 0xFF;
       if (byte != NAN_BYTE) v = max(v, byte);
     }
-    v = __reduce_max_sync(0xFFFFFFFFu, v);
-    const int r_old = a.r;
-    if (v > (a.vtop >> 24)) a.set_r(max(Acc<D, CF, NT>::R_MIN, CF == CF_MX ? (int)v - 126 : (int)(v >> 3) - 6));   // 2^r > scale
-    const int dr = r_old - a.r, dl = a.offset(r_old) - a.offset(a.r);
-    const float fr = (float)dr, fl = (float)dl;
-    if constexpr (CF == CF_MX) {                     // this tile's scales are divided by what r_old had over the cap
-      if (dr != dl) Ts::shift_v(sc + TILE * Gr::SB, dr - dl);
+    int dr, dl;                                      // the offset's change, for the rows and for the sums
+    if constexpr (MASK < 2) {
+      const int r_old = a.r;
+      a.set_r(a.raised(r_old, (int)__reduce_max_sync(0xFFFFFFFFu, v)));
+      dr = r_old - a.r;
+      dl = a.offset(r_old) - a.offset(a.r);
+      if constexpr (CF == CF_MX) {                   // this tile's scales are divided by what r_old had over the cap
+        if (dr != dl) Ts::shift_v(sc + TILE * Gr::SB, dr - dl);
+      }
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
+        if constexpr (MASK == 2) {
+          int mine = 0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {              // the columns of the lanes t = c
+            const int last = __shfl_sync(0xFFFFFFFFu, lim[n][e], c);
+            const int most = (int)__reduce_max_sync(0xFFFFFFFFu, first + lane < last ? v : 0u);
+            if (t == c) mine = most;
+          }
+          const int r_old = a.rc[n][e];
+          a.rc[n][e] = a.raised(r_old, mine);
+          dr = r_old - a.rc[n][e];
+          dl = a.offset(r_old) - a.offset(a.rc[n][e]);
+        }
+        const float fr = (float)dr, fl = (float)dl;
         float m = top[n][e];
 #pragma unroll
         for (int x = 4; x < 32; x *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
@@ -415,7 +442,7 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, uint32_t* sc, const
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        x4[n][e] = ex2_approx(fmaf(s[gr][n][e] - a.m[n][e & 1], a.cq[n][e & 1], a.shift));
+        x4[n][e] = ex2_approx(fmaf(s[gr][n][e] - a.m[n][e & 1], a.cq[n][e & 1], MASK == 2 ? 8.f - (float)a.offset(a.rc[n][e & 1]) : a.shift));
         a.l[n][e & 1] += x4[n][e];
       }
     // E8M0 scales multiply in fp32 and the product is rounded; E4M3 ones multiply p as f16
@@ -472,9 +499,14 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, uint32_t* sc, const
               p0 = hmul2(p[n][0], vf[0][blk]);
               p1 = hmul2(p[n][1], vf[1][blk]);
             } else {
-              const float v0 = __uint_as_float(vf[0][blk]), v1 = __uint_as_float(vf[1][blk]);
-              p0 = cvt_f16x2(x4[n][0] * v0, x4[n][1] * v0);
-              p1 = cvt_f16x2(x4[n][2] * v1, x4[n][3] * v1);
+              float va0 = __uint_as_float(vf[0][blk]), vb0 = va0, va1 = __uint_as_float(vf[1][blk]), vb1 = va1;
+              if constexpr (MASK == 2) {              // divided by what the columns' offsets have over the cap
+                const float fa = excess(a.rc[n][0]), fb = excess(a.rc[n][1]);
+                va0 *= fa; va1 *= fa;
+                vb0 *= fb; vb1 *= fb;
+              }
+              p0 = cvt_f16x2(x4[n][0] * va0, x4[n][1] * vb0);
+              p1 = cvt_f16x2(x4[n][2] * va1, x4[n][3] * vb1);
             }
             if (MASK) { p0 &= seen[gr][n][0]; p1 &= seen[gr][n][1]; }   // 0 times a masked key's NaN scale
             b0[n] = transpose_8x8(p0);
@@ -553,7 +585,7 @@ __device__ __forceinline__ void put_part(float* part, const Acc<D, CF, NT>& a) {
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
         *reinterpret_cast<float2*>(part + col * DP + 16 * k + 2 * g) = make_float2(a.o[k][n][e], a.o[k][n][2 + e]);
-      if (g == 0) put_sum<D, COLS>(part, col, Sum{a.m[n][e], a.l[n][e], (float)a.r, a.cq[n][e]});
+      if (g == 0) put_sum<D, COLS>(part, col, Sum{a.m[n][e], a.l[n][e], (float)a.rc[n][e], a.cq[n][e]});
     }
 }
 
@@ -662,32 +694,61 @@ __device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const Span& sp
   a.reset();
   const int min_lim = limit_of(p, sp, c0);            // the first column sees the fewest keys
 
-  for (int tl = t0; tl < tend; ++tl) {
+  // the tiles that all columns see alike, and those behind some row (their rows' own tokens)
+  const int alike = min_lim == sp.kmax ? tend : min(tend, min_lim / TILE);
+  uint32_t bad = 0;
+  const uint8_t* at = nullptr;
+  auto arrived = [&] {
     const int s = r.out;
-    if (!mbar_wait(&r.bar[s], (r.phase >> s) & 1, ac)) { ok = false; break; }
+    if (!mbar_wait(&r.bar[s], (r.phase >> s) & 1, ac)) return false;
     r.phase ^= 1u << s;
     r.out = r.out + 1 == STG ? 0 : r.out + 1;
-    const uint32_t bad = (bads >> (2 * s)) & 3;
-    const uint8_t* at = r.mem + s * C::STAGE;
-    TileScales<D, CF> ts(at, r.scales);
-    if (CF == CF_MX && a.shift == 8.f - R_CAP) ts.shift_v(r.scales + TILE * Gr::SB, R_CAP - a.r);
-    __syncwarp();
-    if (bad == 0 && (tl + 1) * TILE <= min_lim) {
-      tile_step<D, CF, NT, 2, false>(at, r.scales, ts.v, 0, q, lim, tl * TILE, 0, a);
-    } else {
-      if (tl * TILE + lane >= sp.kmax || (bad >> (lane >> 4) & 1)) {     // no part in the offset of V's scales
+    bad = (bads >> (2 * s)) & 3;
+    at = r.mem + s * C::STAGE;
+    return true;
+  };
+  auto unseen = [&](int tl, TileScales<D, CF>& ts) {      // no part in the offset of V's scales
+    if (tl * TILE + lane >= sp.kmax || (bad >> (lane >> 4) & 1)) {
 #pragma unroll
-        for (int x = 0; x < TileScales<D, CF>::BYTE_WORDS; ++x) ts.v[x] = 0;
-      }
-#pragma unroll 1
-      for (int gr = 0; gr < 2 && tl * TILE + 16 * gr < sp.kmax; ++gr)
-        tile_step<D, CF, NT, 1, true>(at, r.scales, ts.v, gr, q, lim, tl * TILE, bad, a);
+      for (int x = 0; x < TileScales<D, CF>::BYTE_WORDS; ++x) ts.v[x] = 0;
     }
+  };
+  auto go_on = [&] {
     __syncwarp();
     if (issued < tend) {
       if (issued - batch == 32) look_up(issued);
       issue(issued++);
     }
+  };
+  int tl = t0;
+  for (; tl < alike; ++tl) {
+    ok = arrived();
+    if (!ok) break;
+    TileScales<D, CF> ts(at, r.scales);
+    if (CF == CF_MX && a.shift == 8.f - R_CAP) ts.shift_v(r.scales + TILE * Gr::SB, R_CAP - a.r);
+    __syncwarp();
+    if (bad == 0 && (tl + 1) * TILE <= min_lim) {
+      tile_step<D, CF, NT, 2, 0>(at, r.scales, ts.v, 0, q, lim, tl * TILE, 0, a);
+    } else {
+      unseen(tl, ts);
+#pragma unroll 1
+      for (int gr = 0; gr < 2 && tl * TILE + 16 * gr < sp.kmax; ++gr)
+        tile_step<D, CF, NT, 1, 1>(at, r.scales, ts.v, gr, q, lim, tl * TILE, bad, a);
+    }
+    go_on();
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) a.rc[n][0] = a.rc[n][1] = a.r;
+  for (; ok && tl < tend; ++tl) {
+    ok = arrived();
+    if (!ok) break;
+    TileScales<D, CF> ts(at, r.scales);
+    __syncwarp();
+    unseen(tl, ts);
+#pragma unroll 1
+    for (int gr = 0; gr < 2 && tl * TILE + 16 * gr < sp.kmax; ++gr)
+      tile_step<D, CF, NT, 1, 2>(at, r.scales, ts.v, gr, q, lim, tl * TILE, bad, a);
+    go_on();
   }
   if (!ok) {                                            // give up: the copies in flight end first
     for (int k = 0; k < STG; ++k) {
@@ -712,7 +773,7 @@ __device__ __forceinline__ void put_rows(const CacheAttnArgs& p, const Span& sp,
     for (int e = 0; e < 2; ++e) {
       const int col = c0 + 8 * n + 2 * t + e;
       if (col >= sp.qlen * p.G) continue;
-      const Row row(p, b, hkv, col, sp, Sum{a.m[n][e], a.l[n][e], (float)a.r, a.cq[n][e]});
+      const Row row(p, b, hkv, col, sp, Sum{a.m[n][e], a.l[n][e], (float)a.rc[n][e], a.cq[n][e]});
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) row.put(p, 16 * k + 2 * g, make_float2(a.o[k][n][e], a.o[k][n][2 + e]));
       if (g == 0) row.put_lse(p);

@@ -214,3 +214,29 @@ def test_values_of_every_size(kind, lens, Hkv, width, D):
     for Sq in (1, 4):
         run_attention(fsa, normal(g, B, Sq, 4 * Hkv, D), cache, table, lens)
     run_attention(fsa, normal(g, B, 1, 4 * Hkv, D) * 4, cache, table, lens, dtype="bf16")
+
+
+@pytest.mark.parametrize("fmt,D,top", [("E2M1", 128, 30), ("E2M1", 128, 127), ("E2M1", 64, 80), ("NVFP4", 128, 11), ("NVFP4", 64, 11)])
+@pytest.mark.parametrize("lens,Hkv,width", SPLITS + [pytest.param([33, 5], 1, 4, id="two tiles"), pytest.param([96], 2, 100, id="a tile a CTA")])
+def test_values_behind_a_row(lens, Hkv, width, fmt, D, top):
+    """Values at positions behind a row, however large, do not change the row: it is held to
+    the bounds of the keys that it sees."""
+    fsa = _fsa()
+    g = gen(107)
+    B, S = len(lens), max(lens)
+    table, pages = make_table(g, lens, 16)
+    table = wide_table(table, width)
+    cache = fsa.empty_cache(pages, 16, Hkv, D, fmt)
+    for G, Sq in ((4, 2), (4, 5), (1, 17)):
+        k, v = normal(g, B, S, Hkv, D), normal(g, B, S, Hkv, D) * 2.0 ** -6
+        for b, n in enumerate(lens):
+            for i in range(1, min(n, Sq)):             # each new position larger than the one before
+                v[b, n - Sq + i if n >= Sq else i] *= 2.0 ** (6 + top * i / Sq)
+        fsa.fsa_cache_append(cache, k, v, table, i32(lens), i32(lens))
+        q, scale = normal(g, B, Sq, G * Hkv, D), D ** -0.5
+        out, lse = torch.empty(B, Sq, G * Hkv, D, device="cuda"), torch.empty(B, Sq, G * Hkv, device="cuda")
+        fsa.fsa_attention_cache(q, cache, table, i32(lens), out=out, lse=lse)
+        for i in range(Sq):
+            rows = slice(i, i + 1)
+            check_attention(q[:, rows], cache, table, [max(0, n - Sq + 1 + i) for n in lens], [1] * B, True, scale, out[:, rows],
+                            lse[:, rows], out[:, rows])
