@@ -240,3 +240,30 @@ def test_values_behind_a_row(lens, Hkv, width, fmt, D, top):
             rows = slice(i, i + 1)
             check_attention(q[:, rows], cache, table, [max(0, n - Sq + 1 + i) for n in lens], [1] * B, True, scale, out[:, rows],
                             lse[:, rows], out[:, rows])
+
+
+@pytest.mark.parametrize("seed", range(30))
+def test_random_ranges(seed):
+    """Seeded random shapes with pages outside the pool here and there, values of random sizes,
+    rows that see different keys."""
+    import random
+    fsa = _fsa()
+    r, g = random.Random(500 + seed), gen(500 + seed)
+    D, fmt, page = r.choice((64, 128)), r.choice(("E2M1", "NVFP4")), r.choice((16, 32, 128))
+    Hkv, G, Sq = r.choice((1, 2, 5)), r.choice((1, 3, 8)), r.choice((1, 2, 5, 17))
+    B, top = r.choice((1, 4, 40)), r.choice((40, 500, 3000))
+    lens = [r.choice((0, 1, r.randint(0, top), top)) for _ in range(B)]
+    q_lens = [r.randint(0, Sq) for _ in range(B)] if r.random() < 0.5 else None
+    table, pages = make_table(g, lens, page)
+    table = wide_table(table, r.choice((0, 1000 // page + 1)))
+    cache = fsa.empty_cache(pages, page, Hkv, D, fmt)
+    cache.pages.fill_(0xFF)
+    S = max(lens + [1])
+    low, high = (-60, 126) if fmt == "E2M1" else (-6, 10)
+    size = torch.exp2(torch.randint(low, high, (B, S, 1, 1), generator=g, device="cuda").double())
+    v = (normal(g, B, S, Hkv, D).double() * (size if r.random() < 0.7 else 1.0)).clamp(-3.3e38, 3.3e38).to(torch.bfloat16)
+    fsa.fsa_cache_append(cache, normal(g, B, S, Hkv, D), v, table, i32(lens), i32(lens))
+    gone = torch.rand(table.shape, generator=g, device="cuda") < r.choice((0.0, 0.1, 0.6))
+    table = torch.where(gone, torch.where(torch.rand(table.shape, generator=g, device="cuda") < 0.5, -1, pages).int(), table)
+    q = normal(g, B, Sq, Hkv * G, D) * r.choice((1.0, 4.0))
+    run_attention(fsa, q, cache, table, lens, q_lens, r.random() < 0.8, scale=r.choice((None, -0.1, 0.3)), dtype=r.choice(("f32", "bf16")))
