@@ -267,3 +267,50 @@ def test_random_ranges(seed):
     table = torch.where(gone, torch.where(torch.rand(table.shape, generator=g, device="cuda") < 0.5, -1, pages).int(), table)
     q = normal(g, B, Sq, Hkv * G, D) * r.choice((1.0, 4.0))
     run_attention(fsa, q, cache, table, lens, q_lens, r.random() < 0.8, scale=r.choice((None, -0.1, 0.3)), dtype=r.choice(("f32", "bf16")))
+
+
+@pytest.mark.parametrize("width", [512, 2048])
+@pytest.mark.parametrize("fmt", ["E2M1", "NVFP4"])
+def test_a_captured_step_goes_on(fmt, width):
+    """A decode step (prepare, write, attend) captured once and replayed: it follows positions,
+    lengths and contents on the device, with the bits of the same calls made one by one."""
+    fsa = _fsa()
+    g = gen(109)
+    B, H, Hkv, D, page = 3, 8, 2, 128, 16
+    lens = [300, 17, 1]
+    table, pages = make_table(g, [n + 8 for n in lens], page)
+    table = wide_table(table, width // page)
+    inv = 1e4 ** (-torch.arange(D // 2, device="cuda", dtype=torch.float64) / (D // 2))
+    w = normal(g, D)
+    caches = [fsa.empty_cache(pages, page, Hkv, D, fmt) for _ in range(2)]
+    k, v = normal(g, B, 300, Hkv, D), normal(g, B, 300, Hkv, D)
+    for cache in caches:
+        cache.pages.fill_(0xFF)
+        fsa.fsa_cache_append(cache, k, v, table, i32(lens), i32(lens))
+    qkv, pos, n = normal(g, B, 1, H + 2 * Hkv, D), i32([[x] for x in lens]), i32(lens)
+
+    def step(cache, qkv, pos, n):
+        q, k = fsa.fsa_qk_norm_rope(qkv[:, :, :H], qkv[:, :, H:H + Hkv], pos, inv, q_weight=w, k_weight=w)
+        n = n + 1
+        fsa.fsa_cache_append(cache, k, qkv[:, :, H + Hkv:], table, n)
+        return fsa.fsa_attention_cache(q, cache, table, n, out_dtype="bf16")
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    kept = caches[0].pages.clone()
+    with torch.cuda.stream(side):
+        step(caches[0], qkv, pos, n)                   # warm
+    torch.cuda.current_stream().wait_stream(side)
+    caches[0].pages.copy_(kept)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(caches[0], qkv, pos, n)
+    for _ in range(6):
+        fresh = normal(g, *qkv.shape)
+        want = step(caches[1], fresh, pos.clone(), n.clone())
+        qkv.copy_(fresh)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(caches[0].pages, caches[1].pages)
+        pos += 1
+        n += 1
