@@ -1,15 +1,17 @@
 // fsa_cache_attn.cu -- attention of few query rows over the paged 4-bit cache
-// (decode steps, guessed tokens, prompt chunks).
+// (decode steps, guessed tokens, short prompt chunks).
 //
 //   o = softmax(scale q K^T) V  over the keys a row sees, K and V the values the cache
 //   stands for (codes times block scales), q as given, sums in fp32.
 //
 // What bounds it: the cache is read once, 1.06 (E2M1) or 1.125 (NVFP4) bytes per pair of
-// K and V elements.  A kv head has only G x Sq query rows (often 8 or fewer), so a 128-row
-// tcgen05 tile would be nearly all padding, and V's scales run along D while its product
-// runs along the keys, which the block-scaled instructions cannot take.  So each warp works
-// on its own keys with m16n8k16 products whose m is the keys (S^T = K Q^T) and then
-// D (O^T = V^T P^T), n the query rows ("columns" here: 8 or 16 a pass).
+// K and V elements, as long as a kv head has no more than 16 query rows (G x Sq); it is read and
+// converted again for each 16 more.  V's scales run along D while its product runs along the
+// keys, which the block-scaled tcgen05 instructions cannot take, and q would have to be split
+// or quantised for them; the f16 ones would need the codes converted into shared memory.  So
+// each warp works on its own keys with m16n8k16 products whose m is the keys (S^T = K Q^T) and
+// then D (O^T = V^T P^T), n the query rows ("columns" here: 8 or 16 a pass), the codes converted
+// in registers.
 //
 //   - E2M1 to f16 is exact in one instruction a pair.  An E8M0 scale of K multiplies the fp32
 //     sum of its block; an E4M3 one multiplies the codes (6 bits: exact in f16).  V's scales
@@ -21,10 +23,10 @@
 //   - The f16 probabilities carry 2^(8 - r), r the running maximum exponent of V's scales,
 //     so that p * scale stays below 2^15.  With E8M0 scales r spans fp32's whole range: what of
 //     it exceeds 2^40 divides the unpacked scales instead, so that no weight down to 2^-94 of the
-//     largest is flushed from the sum.  The running maximum m of the raw scores is raised
-//     only when a score beats it by more than 2^4 in the softmax (then the sums are
-//     rescaled), so most tiles need one vote and no reduction over lanes.  Both offsets
-//     multiply numerator and denominator alike and cancel.
+//     largest is flushed from the sum.  The rows of a pass share r while they see the same keys;
+//     in the last tiles, where they do not, each has its own.  The running maximum m of the raw
+//     scores is raised only when a score beats it by more than 2^4 in the softmax (then the
+//     sums are rescaled), so most tiles need one vote and no reduction over lanes.
 //   - Work is split evenly over the warps of one CTA per SM: all (sequence, kv head, 32-key
 //     tile) triples in one list, a contiguous share each, a segment's start weighing as
 //     three tiles (64 ragged sequences: 59 us at none, 36.2 at two, 35.6 at three, 36.5 at four).
@@ -36,10 +38,12 @@
 //     stage, the lane that looked the page up copies it.  No warp waits for another before
 //     the end.  Two stages: 24 tiles in flight an SM cover the latency, and a third cost 3%.
 //     12 warps of 168 registers: 8 were 5 to 7% slower, 10 (uneven over the four schedulers)
-//     10%, 14 and 16 (spills) 12%.
+//     10%, 14 and 16 12% (more spills: with 12 the E2M1 instance of 128 dims and 8 columns spills 76
+//     bytes, the NVFP4 one 24; those of 64 dims and 16 columns 48 and 44; of 128 dims and 16 columns,
+//     8 warps of 255, the E2M1 one 116; the others none).
 //
 // Measured (one GB300, copies at 6.79 TB/s): 8 sequences of 128K tokens, 8 kv heads, 4 query
-// heads each: E2M1 198 us, 5.77 TB/s of cache, NVFP4 223 us, 5.41 TB/s; one sequence 35.5 us
+// heads each: E2M1 199 us, 5.74 TB/s of cache, NVFP4 221 us, 5.47 TB/s; one sequence 35.7 us
 // for 143 MB.  Of that 1.4 us go until the list is summed, 0.6 until a warp has its place in it,
 // 1.7 until its first copies are on their way; the warps of a CTA end 2.8 us before its slowest
 // on average, its join takes 1.3, the second kernel 3.  Counters at the large sizes: 265 (E2M1) and
@@ -151,7 +155,7 @@ struct Acc {
   float l[NT][2];           // this thread's part of the row sums
   float m[NT][2];           // running maximum of the raw scores, the same in all g
   float top[NT][2];         // a raw score above this raises m
-  float cq[NT][2];          // what a raw score was multiplied by (log2 units); set by finish
+  float cq[NT][2];          // what a raw score was multiplied by (log2 units); last set by finish
   int r;                    // o holds exp2((s - m) cq + 8 - r) times values, l the same with p_offset(r)
   float shift;              // 8 - p_offset(r)
   uint32_t vtop;            // highest scale byte that r allows, as the high bytes of two halves
@@ -613,8 +617,11 @@ __device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const Span& sp
   constexpr int STG = C::STG;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   bool ok = true;
-  // (cq beside `a`, not in it, until the end: 8 sequences of 128K E2M1 keys 199 us, in it 204)
-  float cq[NT][2];                                      // what a raw score of a column is multiplied by (log2 units)
+  // What a raw score of a column is multiplied by (log2 units): beside `a` until the end for 8
+  // columns, in it for 16 (us beside / in it: 8 sequences of 128K E2M1 keys 199 / 204, 8 of 32K NVFP4 keys
+  // with 16 columns 94 / 89; the others within 1%).
+  float own[NT][2];
+  float (&cq)[NT][2] = NT == 1 ? own : a.cq;
   int lim[NT][2];                                       // how many keys it sees
   const int tend = min(t1, (sp.kmax + TILE - 1) / TILE);
   // q's rows, on their way while the pages are looked up
@@ -1156,10 +1163,15 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_join_kernel(const CacheAtt
 // Which kernel: a CTA for each segment where none is longer than 28 tiles and there are at most
 // 8 an SM, else the list split evenly.  (The table's width bounds a segment's tiles; the
 // lengths are on the device.)  Measured, list / whole, us, 8 kv heads of 128 dims, E2M1:
-//   1 sequence of 100, 760, 890, 1020, 1500 keys: 8.5 / 3.9, 9.0 / 8.4, 9.1 / 9.2, 9.3 / 10.0, 9.5 / 13.3
-//   64 sequences of 100, 890, 1500 keys: 13.1 / 8.0, 25.2 / 22.0, 33.4 / 31.8
-//   152 sequences (8 segments an SM) of 100, 890, 1 to 890: 17.0 / 13.1, 43.7 / 39.8, 19.4 / 19.4
-//   256 sequences of 100, 1 to 100, 1 to 890: 19.7 / 20.5, 17.4 / 17.9, 24.7 / 29.5
+//   1 sequence of 100, 760, 890, 1020, 1500 keys: 8.9 / 4.2, 9.3 / 8.7, 9.5 / 9.5, 9.7 / 10.3, 9.9 / 13.5
+//   64 sequences of 100, 890, 1500 keys: 13.2 / 8.8, 25.0 / 23.0, 32.9 / 32.4
+//   152 sequences (8 segments an SM) of 100, 890, 1 to 890: 17.6 / 14.1, 43.7 / 40.3, 20.0 / 20.5
+//   256 sequences of 100, 1 to 100, 1 to 890: 21.0 / 21.8, 18.1 / 19.2, 27.1 / 32.1
+// and 2 kv heads of 64 dims, 7 query heads each, 2 rows, NVFP4:
+//   1 sequence of 100, 760, 890, 1020, 1500 keys: 8.6 / 4.9, 9.3 / 9.2, 10.6 / 10.0, 10.0 / 10.8, 12.8 / 14.0
+//   64 sequences of 100, 890, 1500 keys: 11.4 / 6.3, 15.0 / 13.0, 16.4 / 18.4
+//   152 sequences of 100, 890, 1 to 890: 14.5 / 6.9, 20.2 / 14.6, 14.1 / 12.0
+// The rule goes by what the host knows: one short sequence in a wide table takes the list.
 bool whole_segments(const Cache& c, int B, int CT, int max_pages, int sms) {
   const int64_t tiles = (((int64_t)max_pages << c.page_shift) + TILE - 1) / TILE;
   return tiles <= 28 && (int64_t)B * CT * c.Hkv <= 8 * (int64_t)sms;
