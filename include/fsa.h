@@ -391,7 +391,10 @@ typedef struct {
  * interleaved; it turns by pos[b][s][axis] * inv_freq[i].  sections[a] consecutive pairs
  * turn by axis a (one axis for text; time, height and width for images and video);
  * elements from `rotary` on pass unrotated.  fp32 arithmetic, angles good to 2^-24 of a
- * turn up to position 2^24 (2^-16 at 2^31), one rounding to bf16.
+ * turn up to position 2^24 (2^-16 at 2^31) for |inv_freq| up to 1 and in proportion beyond,
+ * one rounding to bf16.  The norm is of each head by itself, with one weight of D for all of
+ * them; a model that normalises all heads of its projection together has this call without
+ * norm for the rotation.
  *   q [B][S][H][D], k [B][S][Hkv][D]: bf16, device, 16-byte aligned, strided
  *   q_out, k_out: as q and k, strides of their own; may be q and k themselves (same
  *     pointer and strides), and must not overlap them or each other otherwise
@@ -469,8 +472,9 @@ int fsa_cache_read(const fsa_cache* cache, void* k, void* v, const fsa_strides* 
                    const fsa_strides* v_strides, int B, int S, const int32_t* block_table, int max_pages,
                    const int32_t* lens, const int32_t* start, int32_t* status, void* stream);
 
-/* Attention of few query rows over the cache (decode steps, guessed tokens, chunks of a
- * prompt): O = softmax(scale Q K^T) V on the values the cache stands for; q is not
+/* Attention of few query rows over the cache (decode steps, guessed tokens, short chunks of a
+ * prompt; the cache is read again for each 16 rows a kv head, so from about 400 on
+ * fsa_cache_read and fsa_attention_fwd_bf16 on what it gives are faster): O = softmax(scale Q K^T) V on the values the cache stands for; q is not
  * quantised, sums and softmax statistics are fp32, probabilities times V's scales are
  * rounded to f16 before the product with the codes of V (2^-11 relative, 2^-10 with
  * NVFP4; for products far below the largest block scale in V that the row sees, an absolute

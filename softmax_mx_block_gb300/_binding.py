@@ -676,7 +676,9 @@ def fsa_attention_cache(q: torch.Tensor, cache: MxCache, block_table: torch.Tens
     [B,Sq,H,D], strided) over the cached keys and values of sequences of lens[b] tokens
     (int32 [B]; the rows' own tokens are in the cache).  Row i < q_lens[b] (default all Sq)
     stands at lens[b] - q_lens[b] + i and, causal, sees the keys up to there; rows behind
-    q_lens[b] are left as they were.  lse: optional fp32 [B,Sq,H] for the log of the
+    q_lens[b] are left as they were.  The cache is read again for each 16 rows a kv head: for
+    chunks of more than about 400 of them fsa_cache_read and fsa_attention_fwd_bf16 are faster.
+    lse: optional fp32 [B,Sq,H] for the log of the
     softmax sums.  workspace: uint8, at least fsa_attention_cache_workspace bytes (default:
     one of the call's own).  status: int32 [1], set where a page number lies outside the pool
     or a wait runs out."""
