@@ -619,7 +619,7 @@ __device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const Span& sp
   bool ok = true;
   // What a raw score of a column is multiplied by (log2 units): beside `a` until the end for 8
   // columns, in it for 16 (us beside / in it: 8 sequences of 128K E2M1 keys 199 / 204, 8 of 32K NVFP4 keys
-  // with 16 columns 94 / 89; the others within 1%).
+  // with 16 columns 94 / 89; the others within 3%).
   float own[NT][2];
   float (&cq)[NT][2] = NT == 1 ? own : a.cq;
   int lim[NT][2];                                       // how many keys it sees
