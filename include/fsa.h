@@ -463,6 +463,24 @@ int fsa_cache_append(const fsa_cache* cache, const void* k, const void* v, const
                      const fsa_strides* v_strides, int B, int S, const int32_t* block_table, int max_pages,
                      const int32_t* lens, const int32_t* new_lens, int32_t* status, void* stream);
 
+/* The projection's q, k and v of new tokens in one pass: q normalised and rotated into q_out
+ * as fsa_qk_norm_rope does (the same bits), k normalised and rotated and v as they are into
+ * the cache as fsa_cache_append puts them.  k is rounded once, to 4 bits: its codes and scales
+ * are those of the exact values, for positions up to 2^24 (angles pos * inv_freq rounded to
+ * 64 bits); beyond, of values within the error of fsa_qk_norm_rope.
+ *   args: as fsa_qk_norm_rope, without k_out (NULL).  pos may be NULL with one axis: a token
+ *     then turns by its place in its sequence, lens[b] - new_lens[b] + i.  q_out may be q, and
+ *     must not overlap k or v.
+ *   v: bf16 [B][S][Hkv][D] and its strides, block_table, lens, new_lens, status, dropped
+ *     tokens and bad pages: as fsa_cache_append.  Row i < new_lens[b] of q is written whether
+ *     its token is dropped or not; rows behind are neither read nor written.
+ * One launch, nothing allocated: may be captured.  Errors: FSA_ERR_INVALID_ARG (as the two
+ * calls; Hkv or D other than the cache's), FSA_ERR_UNSUPPORTED_FMT, FSA_ERR_NO_DEVICE,
+ * FSA_ERR_LAUNCH. */
+int fsa_cache_append_rope(const fsa_norm_rope* args, const fsa_cache* cache, const void* v, const fsa_strides* v_strides,
+                          const int32_t* block_table, int max_pages, const int32_t* lens, const int32_t* new_lens,
+                          int32_t* status, void* stream);
+
 /* The values that the cache stands for (exact in bf16): row i of sequence b is token
  * start[b] + i (start NULL: 0) where that lies in 0..lens[b]-1; other rows of k and v are
  * left as they were.  k or v may be NULL.  Tokens past the block table, or of a page number
@@ -521,6 +539,27 @@ typedef struct {
  * block tables), and its workspace may then be NULL. */
 int fsa_attention_cache_workspace(const fsa_cache* cache, int B, int H, int Sq, int max_pages, size_t* bytes);
 int fsa_attention_cache(const fsa_cache_attn* args, void* stream);
+
+/* As fsa_attention_cache, causal, with a window: of the keys up to its own position a row at
+ * position p sees the last `window` (j > p - window; its own token is one) and the first
+ * `sinks` of the sequence (j < sinks).  Only the pages of keys that some row sees are read.
+ * window >= 1, sinks >= 0, args->causal 1, else FSA_ERR_INVALID_ARG.  The workspace is
+ * fsa_attention_cache_window_workspace bytes. */
+int fsa_attention_cache_window_workspace(const fsa_cache* cache, int B, int H, int Sq, int max_pages, int window, int sinks,
+                                         size_t* bytes);
+int fsa_attention_cache_window(const fsa_cache_attn* args, int window, int sinks, void* stream);
+
+/* What fsa_attention_cache computes, for chunks of new tokens (a prompt's, or the next turn's
+ * of a conversation): rows go 256 a kv head at a time over the cache, which is turned into bf16
+ * operands once for each 256 (those values are exact).  Scores are sums of bf16 products in
+ * fp32, sums and maxima fp32; probabilities are rounded to bf16 for the product with V (2^-8
+ * of each); keys below 2^-100 and values below 2^-100 lose bits (an absolute 2^-117).
+ * A row that sees a token with a non-finite key or value is NaN as a whole.
+ * window and sinks as above; window 0: none (sinks 0 too), causal or not.
+ * args as there, with a workspace of fsa_attention_chunk_workspace bytes.
+ * B * Sq * H <= 2^27; B * Hkv * ceil(Sq * H/Hkv / 256) * (ceil(max_pages * page_size / 128) + 4) < 2^31. */
+int fsa_attention_chunk_workspace(const fsa_cache* cache, int B, int H, int Sq, int max_pages, size_t* bytes);
+int fsa_attention_chunk(const fsa_cache_attn* args, int window, int sinks, void* stream);
 
 /* ------------------------------------------------------ tensor-core peak probe */
 /* Measurement instrument (the roofline denominator of the attention kernels; the

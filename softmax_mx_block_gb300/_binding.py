@@ -146,6 +146,12 @@ def load(build_if_missing: bool = True):
                                           ctypes.POINTER(fsa_strides), i, i, vp, i, vp, vp, vp, vp]
             L.fsa_attention_cache_workspace.argtypes = [ctypes.POINTER(fsa_cache), i, i, i, i, ctypes.POINTER(ctypes.c_size_t)]
             L.fsa_attention_cache.argtypes = [ctypes.POINTER(fsa_cache_attn), vp]
+            L.fsa_attention_cache_window_workspace.argtypes = [ctypes.POINTER(fsa_cache)] + [i] * 6 + [ctypes.POINTER(ctypes.c_size_t)]
+            L.fsa_attention_chunk_workspace.argtypes = [ctypes.POINTER(fsa_cache), i, i, i, i, ctypes.POINTER(ctypes.c_size_t)]
+            for n in ("fsa_attention_cache_window", "fsa_attention_chunk"):
+                getattr(L, n).argtypes = [ctypes.POINTER(fsa_cache_attn), i, i, vp]
+            L.fsa_cache_append_rope.argtypes = [ctypes.POINTER(fsa_norm_rope), ctypes.POINTER(fsa_cache), vp,
+                                                ctypes.POINTER(fsa_strides), vp, i, vp, vp, vp, vp]
             L.fsa_mma_peak.argtypes = [i, i, i, ctypes.c_longlong, vp, ctypes.POINTER(ctypes.c_double), vp]
             L.fsa_bf16_transpose_v.argtypes = [vp, vp, i, i, i, i, vp]
             L.fsa_attention_fwd_bf16.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, i, f, vp, vp]
@@ -157,7 +163,9 @@ def load(build_if_missing: bool = True):
                       "fsa_attention_fwd_ex", "fsa_bf16_transpose_v", "fsa_attention_fwd_bf16", "fsa_version",
                       "fsa_attention_fwd_layers", "fsa_tune_delta", "fsa_mma_peak", "fsa_attention_fwd_qbf16",
                       "fsa_attention_fwd_host", "fsa_qk_norm_rope", "fsa_cache_page_bytes", "fsa_cache_append",
-                      "fsa_cache_read", "fsa_attention_cache_workspace", "fsa_attention_cache"):
+                      "fsa_cache_read", "fsa_attention_cache_workspace", "fsa_attention_cache", "fsa_cache_append_rope",
+                      "fsa_attention_cache_window_workspace", "fsa_attention_cache_window",
+                      "fsa_attention_chunk_workspace", "fsa_attention_chunk"):
                 getattr(L, n).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -640,6 +648,24 @@ def fsa_cache_append(cache: MxCache, k: torch.Tensor, v: torch.Tensor, block_tab
                                                status, _raw(stream))
 
 
+def fsa_cache_append_rope(cache: MxCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor,
+                          lens: torch.Tensor, new_lens: torch.Tensor | None = None, *, pos: torch.Tensor | None = None,
+                          inv_freq: torch.Tensor | None = None, sections=None, q_weight: torch.Tensor | None = None,
+                          k_weight: torch.Tensor | None = None, norm=True, eps=1e-6, interleaved=False,
+                          q_out: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """What fsa_qk_norm_rope makes of q [B,S,H,D] (returned: q_out, by default a contiguous tensor of
+    q's shape), and k [B,S,Hkv,D], normalised and rotated too, and v quantised into the cache as
+    by fsa_cache_append, in one pass; k is rounded once.  pos as there; without it a token turns
+    by its place in its sequence, lens[b] - new_lens[b] + i.  Rows behind new_lens[b] are neither read nor written."""
+    if q_out is None:
+        q_out = _new(torch.empty if new_lens is None else torch.zeros, q.shape, q.dtype, q.device, stream)
+    c = cache
+    (_torch_module or _serving()).cache_append_rope(c.pages, c.page_size, c.Hkv, c.D, c.fmt, q, k, pos, inv_freq,
+                                                    None if sections is None else tuple(sections), q_weight, k_weight, norm,
+                                                    eps, interleaved, q_out, v, block_table, lens, new_lens, status, _raw(stream))
+    return q_out
+
+
 def fsa_cache_read(cache: MxCache, block_table: torch.Tensor, lens: torch.Tensor, S: int | None = None, *,
                    start: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
                    v_out: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> tuple:
@@ -660,37 +686,67 @@ def fsa_cache_read(cache: MxCache, block_table: torch.Tensor, lens: torch.Tensor
     return k_out, v_out
 
 
-def fsa_attention_cache_workspace(cache: MxCache, B, H, Sq, max_pages) -> int:
+def fsa_attention_cache_workspace(cache: MxCache, B, H, Sq, max_pages, window=None, sinks=0) -> int:
     """Bytes of the workspace of fsa_attention_cache on the current device (0: it needs none)."""
     n, c = ctypes.c_size_t(), cache.struct()
-    _check(load().fsa_attention_cache_workspace(ctypes.byref(c), B, H, Sq, max_pages, ctypes.byref(n)),
-           "fsa_attention_cache_workspace")
+    if window is None and sinks == 0:
+        _check(load().fsa_attention_cache_workspace(ctypes.byref(c), B, H, Sq, max_pages, ctypes.byref(n)),
+               "fsa_attention_cache_workspace")
+    else:
+        _check(load().fsa_attention_cache_window_workspace(ctypes.byref(c), B, H, Sq, max_pages, 0 if window is None else window,
+                                                           sinks, ctypes.byref(n)), "fsa_attention_cache_window_workspace")
     return n.value
 
 
-def fsa_attention_cache(q: torch.Tensor, cache: MxCache, block_table: torch.Tensor, lens: torch.Tensor, *,
-                        q_lens: torch.Tensor | None = None, causal=True, scale=None, out: torch.Tensor | None = None,
-                        lse: torch.Tensor | None = None, out_dtype=None, workspace: torch.Tensor | None = None,
-                        timeout_ms=0, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """O [B,Sq,H,D] (fp32, or bf16 with out_dtype="bf16" or a bf16 `out`) of q (bf16
-    [B,Sq,H,D], strided) over the cached keys and values of sequences of lens[b] tokens
-    (int32 [B]; the rows' own tokens are in the cache).  Row i < q_lens[b] (default all Sq)
-    stands at lens[b] - q_lens[b] + i and, causal, sees the keys up to there; rows behind
-    q_lens[b] are left as they were.  The cache is read again for each 16 rows a kv head: for
-    chunks of more than about 400 of them fsa_cache_read and fsa_attention_fwd_bf16 are faster.
-    lse: optional fp32 [B,Sq,H] for the log of the
-    softmax sums.  workspace: uint8, at least fsa_attention_cache_workspace bytes (default:
-    one of the call's own).  status: int32 [1], set where a page number lies outside the pool
-    or a wait runs out."""
+def fsa_attention_chunk_workspace(cache: MxCache, B, H, Sq, max_pages) -> int:
+    """Bytes of the workspace of fsa_attention_chunk on the current device (0: it needs none)."""
+    n, c = ctypes.c_size_t(), cache.struct()
+    _check(load().fsa_attention_chunk_workspace(ctypes.byref(c), B, H, Sq, max_pages, ctypes.byref(n)),
+           "fsa_attention_chunk_workspace")
+    return n.value
+
+
+def _attend(name, q, cache, block_table, lens, q_lens, causal, scale, window, sinks, out, lse, out_dtype, workspace, timeout_ms,
+            status, stream):
     c = cache
     if out is None:
         _, dtype = _out_dtype(out_dtype)
         out = _new(torch.empty if q_lens is None else torch.zeros, q.shape, dtype, q.device, stream)
     elif out_dtype is not None and _out_dtype(out_dtype)[1] != out.dtype:
         raise FsaError(FSA_ERR_INVALID_ARG, f"out is {out.dtype}, not {out_dtype}")
-    (_torch_module or _serving()).attention_cache(c.pages, c.page_size, c.Hkv, c.D, c.fmt, q, out, lse, block_table, lens,
-                                                  q_lens, causal, scale, workspace, timeout_ms, status, _raw(stream))
+    getattr(_torch_module or _serving(), name)(c.pages, c.page_size, c.Hkv, c.D, c.fmt, q, out, lse, block_table, lens, q_lens,
+                                               causal, scale, workspace, timeout_ms, status, _raw(stream), window, sinks)
     return out
+
+
+def fsa_attention_cache(q: torch.Tensor, cache: MxCache, block_table: torch.Tensor, lens: torch.Tensor, *,
+                        q_lens: torch.Tensor | None = None, causal=True, scale=None, window: int | None = None, sinks=0,
+                        out: torch.Tensor | None = None, lse: torch.Tensor | None = None, out_dtype=None,
+                        workspace: torch.Tensor | None = None, timeout_ms=0, status: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor:
+    """O [B,Sq,H,D] (fp32, or bf16 with out_dtype="bf16" or a bf16 `out`) of q (bf16
+    [B,Sq,H,D], strided) over the cached keys and values of sequences of lens[b] tokens
+    (int32 [B]; the rows' own tokens are in the cache).  Row i < q_lens[b] (default all Sq)
+    stands at lens[b] - q_lens[b] + i and, causal, sees the keys up to there; rows behind
+    q_lens[b] are left as they were.  window (with causal only): of these keys it sees the last
+    `window`, its own among them, and the first `sinks` of the sequence.  The cache is read again
+    for each 16 rows a kv head: fsa_attention_chunk is for more.  lse: optional fp32 [B,Sq,H] for
+    the log of the softmax sums.  workspace: uint8, at least fsa_attention_cache_workspace bytes
+    (default: one of the call's own).  status: int32 [1], set where a page number lies outside
+    the pool or a wait runs out."""
+    return _attend("attention_cache", q, cache, block_table, lens, q_lens, causal, scale, window, sinks, out, lse, out_dtype,
+                   workspace, timeout_ms, status, stream)
+
+
+def fsa_attention_chunk(q: torch.Tensor, cache: MxCache, block_table: torch.Tensor, lens: torch.Tensor, *,
+                        q_lens: torch.Tensor | None = None, causal=True, scale=None, window: int | None = None, sinks=0,
+                        out: torch.Tensor | None = None, lse: torch.Tensor | None = None, out_dtype=None,
+                        workspace: torch.Tensor | None = None, timeout_ms=0, status: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor:
+    """What fsa_attention_cache computes, for chunks of a prompt: 256 rows a kv head at a time, on
+    the tensor cores in bf16.  Arguments as there (workspace: fsa_attention_chunk_workspace bytes)."""
+    return _attend("attention_chunk", q, cache, block_table, lens, q_lens, causal, scale, window, sinks, out, lse, out_dtype,
+                   workspace, timeout_ms, status, stream)
 
 
 def fsa_mma_peak(kind: int, n_ctas: int, iters: int, status: torch.Tensor | None = None, n: int = 128,

@@ -62,6 +62,18 @@ struct RopeArgs {
   float eps;
 };
 
+struct AppendRopeArgs {   // r.k is read only (r.ko is null); r.pos null: by their places in the sequences
+  RopeArgs r;
+  Cache c;
+  const uint16_t* v;
+  Strides vs;
+  const int32_t* table;   // [B][max_pages]
+  const int32_t* lens;    // [B]
+  const int32_t* which;   // new tokens of each sequence (null: S)
+  int max_pages;
+  int32_t* status;
+};
+
 struct CacheAttnArgs {
   Cache c;
   const uint16_t* q;
@@ -74,6 +86,8 @@ struct CacheAttnArgs {
   float* partials;        // workspace: two partial results a CTA
   int4* starts;           // workspace: per CTA, the segment that begins in it and goes on, and the CTA where it ends
   int B, H, Sq, G, CT, max_pages, causal, out_bf16;
+  int window, sinks;      // of the keys before a row the last `window` and the first `sinks` (window 0: all)
+  int whole;              // chunks: a segment is one CTA's (CT: blocks of 256 rows)
   uint32_t g_mul;         // col / G is the high word of col * g_mul (0: it is not)
   float scale_log2;       // |scale| log2 e, or 1 when the scale is 0
   float q_sign;           // the scale's sign (0 for a zero scale)
@@ -102,10 +116,18 @@ cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, unsigned threads,
 cudaError_t launch_cache_append(const CacheIo& a, cudaStream_t st);
 cudaError_t launch_cache_read(const CacheIo& a, cudaStream_t st);
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, int sms, cudaStream_t st);
+cudaError_t launch_append_rope(const AppendRopeArgs& a, int sms, cudaStream_t st);
 
 // columns (query rows of one kv head) of a pass, by eights, and the workspace of a call
 int cache_attn_ntiles(int cols);
-size_t cache_attn_workspace(const Cache& c, int B, int H, int Sq, int max_pages, int sms, size_t* starts_at);
+size_t cache_attn_workspace(const Cache& c, int B, int H, int Sq, int max_pages, int window, int sinks, int sms, size_t* starts_at);
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, int nt, int sms, cudaStream_t st);
+cudaError_t launch_cache_attn_window(const CacheAttnArgs& a, int nt, int sms, cudaStream_t st);      // a.window > 0
+
+// chunks: blocks of a sequence's rows (of a kv head), whether its segments are one CTA's each
+int cache_chunk_blocks(int rows);
+bool cache_chunk_whole(const Cache& c, int max_pages);
+size_t cache_chunk_workspace(const Cache& c, int max_pages, int sms, size_t* starts_at);
+cudaError_t launch_cache_chunk(const CacheAttnArgs& a, int sms, cudaStream_t st);
 
 }  // namespace fsa

@@ -48,9 +48,15 @@
 // 1.7 until its first copies are on their way; the warps of a CTA end 2.8 us before its slowest
 // on average, its join takes 1.3, the second kernel 3.  Counters at the large sizes: 265 (E2M1) and
 // 295 (NVFP4) warp instructions for 16 keys of a kv head, 2.5 and 2.4 a cycle of 4.
+#include <algorithm>
 #include <atomic>
 #include "fsa_cache.h"
 #include "fsa_ptx.cuh"
+
+// 1: the calls with a window (a translation unit of their own)
+#ifndef FSA_CACHE_WINDOW
+#define FSA_CACHE_WINDOW 0
+#endif
 
 namespace fsa {
 namespace {
@@ -83,21 +89,51 @@ struct Cfg {
 struct Span {
   int qlen, len, kmax, tiles;   // rows, keys, keys that some column sees, tiles (0: no rows)
   __device__ __forceinline__ int units() const { return tiles ? tiles + EXTRA : 0; }
+  __device__ __forceinline__ int key_tiles() const { return (kmax + TILE - 1) / TILE; }
+  __device__ __forceinline__ int at(int t) const { return t; }
 };
+// With a window: a segment's tiles are those of the first keys (`sinks` of them), then those that
+// some column's window reaches, beginning with the ones that lie in all windows: all tiles that
+// the columns see alike come first, then the ends of their rows, then the windows' beginnings.
+struct SpanWindow : Span {
+  int low, high;                // the first keys of the first and of the last column's window
+  int lead, w0, u0, end;        // tiles of the first keys; first tile of some window, of all windows; last and 1
+  __device__ __forceinline__ int key_tiles() const { return lead + end - w0; }
+  __device__ __forceinline__ int at(int t) const {              // the t-th tile's place among the keys
+    const int x = t - lead + u0;
+    return t < lead ? t : x < end ? x : x - end + w0;
+  }
+};
+template <bool WIN> struct SpanOf { using type = Span; };
+template <> struct SpanOf<true> { using type = SpanWindow; };
 // row i of a column i * G + its head: col / G
 __device__ __forceinline__ int row_of(const CacheAttnArgs& p, int col) {
   return p.g_mul ? (int)__umulhi((uint32_t)col, p.g_mul) : p.G == 1 ? col : col / p.G;
 }
-__device__ __forceinline__ Span span_of(const CacheAttnArgs& p, int vb, int cols) {
-  Span s;
+template <bool WIN>
+__device__ __forceinline__ typename SpanOf<WIN>::type span_of(const CacheAttnArgs& p, int vb, int cols) {
+  typename SpanOf<WIN>::type s;
   const int b = p.CT == 1 ? vb : vb / p.CT, ct = vb - b * p.CT;
   s.qlen = p.q_lens ? min(max(p.q_lens[b], 0), p.Sq) : p.Sq;
   s.len = (int)min((int64_t)max(p.lens[b], 0), (int64_t)p.max_pages << p.c.page_shift);
   const int c0 = ct * cols;
-  if (c0 >= s.qlen * p.G) { s.kmax = s.tiles = 0; return s; }
+  if (c0 >= s.qlen * p.G) {
+    s.kmax = s.tiles = 0;
+    if constexpr (WIN) s.low = s.high = s.lead = s.w0 = s.u0 = s.end = 0;
+    return s;
+  }
   const int last = min(s.qlen - 1, row_of(p, c0 + cols - 1));
   s.kmax = p.causal ? max(0, s.len - s.qlen + last + 1) : s.len;
-  s.tiles = max(1, (s.kmax + TILE - 1) / TILE);      // a tile for rows that see nothing: they are written
+  if constexpr (WIN) {
+    s.low = max(0, s.len - s.qlen + row_of(p, c0) + 1 - p.window);
+    s.high = max(0, s.kmax - p.window);
+    s.end = (s.kmax + TILE - 1) / TILE;
+    s.w0 = min(s.low / TILE, s.end);
+    s.lead = min((p.sinks + TILE - 1) / TILE, s.w0);
+    // (where the columns are one row's their windows begin alike, inside a tile or not)
+    s.u0 = s.low == s.high ? s.w0 : min((s.high + TILE - 1) / TILE, s.end);
+  }
+  s.tiles = max(1, s.key_tiles());                   // a tile for rows that see nothing: they are written
   return s;
 }
 
@@ -120,6 +156,12 @@ __device__ __forceinline__ int limit_of(const CacheAttnArgs& p, const Span& s, i
   const int i = row_of(p, col);
   if (i >= s.qlen) return 0;
   return p.causal ? max(0, s.len - s.qlen + i + 1) : s.len;
+}
+
+// Whether key k is one of the first that a column sees of its `lim`, or in its window.
+template <bool WIN>
+__device__ __forceinline__ bool sees(const CacheAttnArgs& p, int k, int lim) {
+  return k < lim && (!WIN || k >= lim - p.window || k < p.sinks);
 }
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -294,8 +336,8 @@ struct TileScales {
 // first: position of the tile's first key; bad: groups without a page.  MASK 1: some column
 // does not see some key, but those with rows see the same ones; 2: they do not, and each has an
 // offset of its own.
-template <int D, int CF, int NT, int NG, int MASK>
-__device__ __forceinline__ void tile_step(const uint8_t* st, uint32_t* sc, const uint32_t (&vs)[TileScales<D, CF>::BYTE_WORDS], int g0,
+template <int D, int CF, int NT, int NG, int MASK, bool WIN>
+__device__ __forceinline__ void tile_step(const CacheAttnArgs& p, const uint8_t* st, uint32_t* sc, const uint32_t (&vs)[TileScales<D, CF>::BYTE_WORDS], int g0,
                                           const uint2 (&q)[D / 16][NT], const float (&cq)[NT][2],
                                           const int (&lim)[NT][2], int first, uint32_t bad, Acc<D, CF, NT>& a) {
   using Gr = CacheGroup<D, CF>;
@@ -368,8 +410,8 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, uint32_t* sc, const
       const bool gone = (bad >> (g0 + gr)) & 1;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        seen[gr][n][0] = gone ? 0u : (k0 < lim[n][0] ? 0xFFFFu : 0u) | (k0 < lim[n][1] ? 0xFFFF0000u : 0u);
-        seen[gr][n][1] = gone ? 0u : (k1 < lim[n][0] ? 0xFFFFu : 0u) | (k1 < lim[n][1] ? 0xFFFF0000u : 0u);
+        seen[gr][n][0] = gone ? 0u : (sees<WIN>(p, k0, lim[n][0]) ? 0xFFFFu : 0u) | (sees<WIN>(p, k0, lim[n][1]) ? 0xFFFF0000u : 0u);
+        seen[gr][n][1] = gone ? 0u : (sees<WIN>(p, k1, lim[n][0]) ? 0xFFFFu : 0u) | (sees<WIN>(p, k1, lim[n][1]) ? 0xFFFF0000u : 0u);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (!(seen[gr][n][e >> 1] & (e & 1 ? 0xFFFF0000u : 0xFFFFu))) s[gr][n][e] = -INFINITY;
@@ -418,7 +460,7 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, uint32_t* sc, const
 #pragma unroll
           for (int c = 0; c < 4; ++c) {              // the columns of the lanes t = c
             const int last = __shfl_sync(0xFFFFFFFFu, lim[n][e], c);
-            const int most = (int)__reduce_max_sync(0xFFFFFFFFu, first + lane < last ? v : 0u);
+            const int most = (int)__reduce_max_sync(0xFFFFFFFFu, sees<WIN>(p, first + lane, last) ? v : 0u);
             if (t == c) mine = most;
           }
           const int r_old = a.rc[n][e];
@@ -454,14 +496,14 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, uint32_t* sc, const
         a.l[n][e & 1] += x4[n][e];
       }
     // E8M0 scales multiply in fp32 and the product is rounded; E4M3 ones multiply p as f16
-    uint32_t p[NT][2], vf[2][Gr::SB];
+    uint32_t pr[NT][2], vf[2][Gr::SB];
     Ts::row(sc + TILE * Gr::SB, 16 * (g0 + gr) + tok, vf[0]);
     Ts::row(sc + TILE * Gr::SB, 16 * (g0 + gr) + tok + 8, vf[1]);
     if constexpr (CF == CF_NV) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        p[n][0] = cvt_f16x2(x4[n][0], x4[n][1]);     // row g: columns 2t, 2t + 1
-        p[n][1] = cvt_f16x2(x4[n][2], x4[n][3]);     // row g + 8
+        pr[n][0] = cvt_f16x2(x4[n][0], x4[n][1]);    // row g: columns 2t, 2t + 1
+        pr[n][1] = cvt_f16x2(x4[n][2], x4[n][3]);    // row g + 8
       }
     }
     // V rows of the keys of S^T rows 2t, 2t + 1 and 8 more, interleaved so that a pair of f16
@@ -504,8 +546,8 @@ __device__ __forceinline__ void tile_step(const uint8_t* st, uint32_t* sc, const
           for (int n = 0; n < NT; ++n) {
             uint32_t p0, p1;
             if constexpr (CF == CF_NV) {
-              p0 = hmul2(p[n][0], vf[0][blk]);
-              p1 = hmul2(p[n][1], vf[1][blk]);
+              p0 = hmul2(pr[n][0], vf[0][blk]);
+              p1 = hmul2(pr[n][1], vf[1][blk]);
             } else {
               float va0 = __uint_as_float(vf[0][blk]), vb0 = va0, va1 = __uint_as_float(vf[1][blk]), vb1 = va1;
               if constexpr (MASK == 2) {              // divided by what the columns' offsets have over the cap
@@ -609,8 +651,8 @@ struct Ring {
 
 // The tiles [t0, t1) of one segment: (sequence b, kv head, columns c0 ..).  Leaves the
 // running state in `a`; false if a wait ran out.
-template <int D, int CF, int NT>
-__device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const Span& sp, int b, int hkv, int c0, int t0, int t1,
+template <int D, int CF, int NT, bool WIN>
+__device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const typename SpanOf<WIN>::type& sp, int b, int hkv, int c0, int t0, int t1,
                                           Ring& r, const AbortCtl& ac, Acc<D, CF, NT>& a) {
   using C = Cfg<D, CF, NT>;
   using Gr = CacheGroup<D, CF>;
@@ -623,7 +665,7 @@ __device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const Span& sp
   float own[NT][2];
   float (&cq)[NT][2] = NT == 1 ? own : a.cq;
   int lim[NT][2];                                       // how many keys it sees
-  const int tend = min(t1, (sp.kmax + TILE - 1) / TILE);
+  const int tend = min(t1, sp.key_tiles());
   // q's rows, on their way while the pages are looked up
   uint2 u[NT][D / 16];
 #pragma unroll
@@ -643,7 +685,7 @@ __device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const Span& sp
   uint32_t bad0 = 0, bad1 = 0, bads = 0;              // tiles of the batch, and (2 bits each) stages, with groups without a page
   auto look_up = [&](int first) {
     batch = first;
-    const int pos = (first + lane) * TILE;
+    const int pos = sp.at(first + lane) * TILE;
     const bool in0 = first + lane < tend, in1 = in0 && pos + 16 < sp.kmax;
     const int i0 = pos >> p.c.page_shift, i1 = (pos + 16) >> p.c.page_shift;
     page0 = in0 ? row[i0] : -1;
@@ -655,11 +697,11 @@ __device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const Span& sp
     if ((bad0 | bad1) && lane == 0 && p.status) atomicExch(p.status, -1);    // FSA_ERR_INVALID_ARG
   };
   auto issue = [&](int tl) {
-    const int s = r.in, at = tl - batch;
+    const int s = r.in, at = tl - batch, k0 = sp.at(tl) * TILE;
     r.in = s + 1 == STG ? 0 : s + 1;
     if (bad0 | bad1 | bads) bads = (bads & ~(3u << (2 * s))) | ((bad0 >> at & 1) | (bad1 >> at & 1) << 1) << (2 * s);
     if (lane == at) {
-      const int inside = ((tl * TILE) & ((1 << p.c.page_shift) - 1)) / 16;
+      const int inside = (k0 & ((1 << p.c.page_shift) - 1)) / 16;
       const uint8_t* const src = head + page0 * p.c.page_bytes + inside * Gr::BYTES;
       uint8_t* const dst = r.mem + s * C::STAGE;
       mbar_expect_tx(&r.bar[s], (page0 >= 0 ? Gr::BYTES : 0) + (page1 >= 0 ? Gr::BYTES : 0));
@@ -708,7 +750,8 @@ __device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const Span& sp
   const int min_lim = limit_of(p, sp, c0);            // the first column sees the fewest keys
 
   // the tiles that all columns see alike, and those behind some row (their rows' own tokens)
-  const int alike = min_lim == sp.kmax ? tend : min(tend, min_lim / TILE);
+  int alike = min_lim == sp.kmax ? tend : min(tend, min_lim / TILE);
+  if constexpr (WIN) alike = min_lim == sp.kmax ? tend : min(tend, sp.lead + max(0, min_lim / TILE - sp.u0));
   uint32_t bad = 0;
   const uint8_t* at = nullptr;
   auto arrived = [&] {
@@ -720,8 +763,10 @@ __device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const Span& sp
     at = r.mem + s * C::STAGE;
     return true;
   };
-  auto unseen = [&](int tl, TileScales<D, CF>& ts) {      // no part in the offset of V's scales
-    if (tl * TILE + lane >= sp.kmax || (bad >> (lane >> 4) & 1)) {
+  auto unseen = [&](int k0, TileScales<D, CF>& ts) {      // no part in the offset of V's scales
+    bool none = k0 + lane >= sp.kmax || (bad >> (lane >> 4) & 1);
+    if constexpr (WIN) none = none || (k0 + lane < sp.low && k0 + lane >= p.sinks);
+    if (none) {
 #pragma unroll
       for (int x = 0; x < TileScales<D, CF>::BYTE_WORDS; ++x) ts.v[x] = 0;
     }
@@ -740,13 +785,16 @@ __device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const Span& sp
     TileScales<D, CF> ts(at, r.scales);
     if (CF == CF_MX && a.shift == 8.f - R_CAP) ts.shift_v(r.scales + TILE * Gr::SB, R_CAP - a.r);
     __syncwarp();
-    if (bad == 0 && (tl + 1) * TILE <= min_lim) {
-      tile_step<D, CF, NT, 2, 0>(at, r.scales, ts.v, 0, q, cq, lim, tl * TILE, 0, a);
+    const int k0 = sp.at(tl) * TILE;
+    bool whole = bad == 0 && k0 + TILE <= min_lim;
+    if constexpr (WIN) whole = whole && (k0 >= sp.high || k0 + TILE <= p.sinks);
+    if (whole) {
+      tile_step<D, CF, NT, 2, 0, WIN>(p, at, r.scales, ts.v, 0, q, cq, lim, k0, 0, a);
     } else {
-      unseen(tl, ts);
+      unseen(k0, ts);
 #pragma unroll 1
-      for (int gr = 0; gr < 2 && tl * TILE + 16 * gr < sp.kmax; ++gr)
-        tile_step<D, CF, NT, 1, 1>(at, r.scales, ts.v, gr, q, cq, lim, tl * TILE, bad, a);
+      for (int gr = 0; gr < 2 && k0 + 16 * gr < sp.kmax; ++gr)
+        tile_step<D, CF, NT, 1, 1, WIN>(p, at, r.scales, ts.v, gr, q, cq, lim, k0, bad, a);
     }
     go_on();
   }
@@ -757,10 +805,11 @@ __device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const Span& sp
     if (!ok) break;
     TileScales<D, CF> ts(at, r.scales);
     __syncwarp();
-    unseen(tl, ts);
+    const int k0 = sp.at(tl) * TILE;
+    unseen(k0, ts);
 #pragma unroll 1
-    for (int gr = 0; gr < 2 && tl * TILE + 16 * gr < sp.kmax; ++gr)
-      tile_step<D, CF, NT, 1, 2>(at, r.scales, ts.v, gr, q, cq, lim, tl * TILE, bad, a);
+    for (int gr = 0; gr < 2 && k0 + 16 * gr < sp.kmax; ++gr)
+      tile_step<D, CF, NT, 1, 2, WIN>(p, at, r.scales, ts.v, gr, q, cq, lim, k0, bad, a);
     go_on();
   }
   if (!ok) {                                            // give up: the copies in flight end first
@@ -861,7 +910,7 @@ struct WholeCfg {
   static constexpr int SMEM = 1024 + WHOLE_WARPS * C::SCALES + (RING > JOIN ? RING : JOIN);
   static constexpr int CTAS = NT == 2 && D == 128 ? 2 : 3;
 };
-template <int D, int CF, int NT>
+template <int D, int CF, int NT, bool WIN>
 __global__ void __launch_bounds__(WHOLE_WARPS * 32, WholeCfg<D, CF, NT>::CTAS) cache_attn_whole_kernel(const CacheAttnArgs p) {
   using C = Cfg<D, CF, NT>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -879,14 +928,14 @@ __global__ void __launch_bounds__(WHOLE_WARPS * 32, WholeCfg<D, CF, NT>::CTAS) c
   griddep_wait();                                       // before any tensor is read
   const int vb = blockIdx.x / p.c.Hkv, hkv = blockIdx.x - vb * p.c.Hkv;
   const int b = p.CT == 1 ? vb : vb / p.CT, c0 = (vb - b * p.CT) * C::COLS;
-  const Span sp = span_of(p, vb, C::COLS);
+  const auto sp = span_of<WIN>(p, vb, C::COLS);
   if (sp.tiles == 0) return;
   __syncthreads();
   Ring r{bars + warp * STG, ring + warp * STG * C::STAGE, scales + warp * C::SCALES / 4, 0, 0, 0};
   Acc<D, CF, NT> a;
   const int n = min(WHOLE_WARPS, sp.tiles), t0 = sp.tiles * warp / n, t1 = sp.tiles * (warp + 1) / n;
   bool ok = true;
-  if (warp < n) ok = run_piece<D, CF, NT>(p, sp, b, hkv, c0, t0, t1, r, ac, a);
+  if (warp < n) ok = run_piece<D, CF, NT, WIN>(p, sp, b, hkv, c0, t0, t1, r, ac, a);
   if (n == 1) {
     if (warp == 0 && ok) put_rows<D, CF, NT>(p, sp, b, hkv, c0, a);
     return;
@@ -903,7 +952,7 @@ __global__ void __launch_bounds__(WHOLE_WARPS * 32, WholeCfg<D, CF, NT>::CTAS) c
   }
 }
 
-template <int D, int CF, int NT>
+template <int D, int CF, int NT, bool WIN>
 __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(const CacheAttnArgs p) {
   using C = Cfg<D, CF, NT>;
   constexpr int NWC = C::NWC, STG = C::STG;
@@ -937,11 +986,11 @@ __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(
   if (small) {
     int n[4];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) n[x] = x < chunk && who * chunk + x < VB ? span_of(p, who * chunk + x, C::COLS).units() : 0;
+    for (int x = 0; x < 4; ++x) n[x] = x < chunk && who * chunk + x < VB ? span_of<WIN>(p, who * chunk + x, C::COLS).units() : 0;
     mine = (n[0] + n[1] + n[2] + n[3]) * p.c.Hkv;
   } else {
     for (int vb = who * chunk; vb < min(VB, (who + 1) * chunk); ++vb)
-      mine += span_of(p, vb, C::COLS).units() * p.c.Hkv;
+      mine += span_of<WIN>(p, vb, C::COLS).units() * p.c.Hkv;
   }
   int inc = mine;
 #pragma unroll
@@ -979,7 +1028,7 @@ __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(
   bool open_begins = false;                            // the open piece is its segment's first
   int open_rest = 0;                                   // tiles of its segment behind it
   Acc<D, CF, NT> a;
-  Span sp;
+  typename SpanOf<WIN>::type sp;
   int vb = 0, hkv = 0, unit = 0;
   Ring r{bars + warp * STG, ring + warp * STG * C::STAGE, scales + warp * C::SCALES / 4, 0, 0, 0};
 
@@ -995,7 +1044,7 @@ __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(
       acc = pre[j];
     }
     for (vb = j * chunk;; ++vb) {
-      sp = span_of(p, vb, C::COLS);
+      sp = span_of<WIN>(p, vb, C::COLS);
       const int n = sp.units() * p.c.Hkv;
       if (lo < acc + n) break;
       acc += n;
@@ -1015,12 +1064,12 @@ __global__ void __launch_bounds__(cta_warps<D, NT>() * 32, 1) cache_attn_kernel(
     auto next = [&] {                                   // the segment after this one
       if (lo < hi && ++hkv == p.c.Hkv) {
         hkv = 0;
-        do { sp = span_of(p, ++vb, C::COLS); } while (sp.tiles == 0);
+        do { sp = span_of<WIN>(p, ++vb, C::COLS); } while (sp.tiles == 0);
       }
     };
     if (t0 == t1) { next(); continue; }                 // none of its tiles
 
-    ok = run_piece<D, CF, NT>(p, sp, b, hkv, c0, t0, t1, r, ac, a);
+    ok = run_piece<D, CF, NT, WIN>(p, sp, b, hkv, c0, t0, t1, r, ac, a);
     if (!ok) break;
     if (t0 == 0 && t1 == sp.tiles) {                    // all of it: write the rows
       put_rows<D, CF, NT>(p, sp, b, hkv, c0, a);
@@ -1172,8 +1221,10 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_join_kernel(const CacheAtt
 //   64 sequences of 100, 890, 1500 keys: 11.4 / 6.3, 15.0 / 13.0, 16.4 / 18.4
 //   152 sequences of 100, 890, 1 to 890: 14.5 / 6.9, 20.2 / 14.6, 14.1 / 12.0
 // The rule goes by what the host knows: one short sequence in a wide table takes the list.
-bool whole_segments(const Cache& c, int B, int CT, int max_pages, int sms) {
-  const int64_t tiles = (((int64_t)max_pages << c.page_shift) + TILE - 1) / TILE;
+// A window bounds the tiles too: those of its keys and of the rows' own at any offset, and the first keys'.
+bool whole_segments(const Cache& c, int B, int CT, int Sq, int max_pages, int window, int sinks, int sms) {
+  int64_t tiles = (((int64_t)max_pages << c.page_shift) + TILE - 1) / TILE;
+  if (window) tiles = std::min(tiles, ((int64_t)window + Sq + 2 * TILE - 3) / TILE + ((int64_t)sinks + TILE - 1) / TILE);
   return tiles <= 28 && (int64_t)B * CT * c.Hkv <= 8 * (int64_t)sms;
 }
 
@@ -1194,16 +1245,17 @@ template <int D, int CF, int NT>
 cudaError_t launch(const CacheAttnArgs& a, int sms, cudaStream_t st) {
   using C = Cfg<D, CF, NT>;
   cudaError_t e;
+  constexpr bool WIN = FSA_CACHE_WINDOW;
   static std::atomic<uint64_t> whole_ready{0}, list_ready{0};
-  if (whole_segments(a.c, a.B, a.CT, a.max_pages, sms)) {
+  if (whole_segments(a.c, a.B, a.CT, a.Sq, a.max_pages, a.window, a.sinks, sms)) {
     constexpr int smem = WholeCfg<D, CF, NT>::SMEM;
-    e = allow_smem(cache_attn_whole_kernel<D, CF, NT>, smem, whole_ready);
+    e = allow_smem(cache_attn_whole_kernel<D, CF, NT, WIN>, smem, whole_ready);
     if (e != cudaSuccess) return e;
-    return launch_early(cache_attn_whole_kernel<D, CF, NT>, dim3(a.B * a.CT * a.c.Hkv), WHOLE_WARPS * 32, smem, st, a);
+    return launch_early(cache_attn_whole_kernel<D, CF, NT, WIN>, dim3(a.B * a.CT * a.c.Hkv), WHOLE_WARPS * 32, smem, st, a);
   }
-  e = allow_smem(cache_attn_kernel<D, CF, NT>, C::SMEM, list_ready);
+  e = allow_smem(cache_attn_kernel<D, CF, NT, WIN>, C::SMEM, list_ready);
   if (e != cudaSuccess) return e;
-  e = launch_early(cache_attn_kernel<D, CF, NT>, dim3(sms), C::NWC * 32, C::SMEM, st, a);
+  e = launch_early(cache_attn_kernel<D, CF, NT, WIN>, dim3(sms), C::NWC * 32, C::SMEM, st, a);
   if (e != cudaSuccess) return e;
   return launch_early(cache_join_kernel<D, NT>, dim3(sms, JOIN_Y), JOIN_THREADS,
                       (size_t)(sms + 2) * (C::COLS / JOIN_Y) * sizeof(Sum), st, a);
@@ -1211,17 +1263,23 @@ cudaError_t launch(const CacheAttnArgs& a, int sms, cudaStream_t st) {
 
 }  // namespace
 
+#if !FSA_CACHE_WINDOW
 int cache_attn_ntiles(int cols) { return cols <= 8 ? 1 : 2; }
 
 // parts of the CTAs, two each; where segments begin that go on
-size_t cache_attn_workspace(const Cache& c, int B, int H, int Sq, int max_pages, int sms, size_t* starts_at) {
+size_t cache_attn_workspace(const Cache& c, int B, int H, int Sq, int max_pages, int window, int sinks, int sms, size_t* starts_at) {
   const int cols = Sq * (H / c.Hkv), nt = cache_attn_ntiles(cols);
   *starts_at = (size_t)2 * sms * 8 * nt * (c.D + 6) * sizeof(float);
-  if (whole_segments(c, B, (cols + 8 * nt - 1) / (8 * nt), max_pages, sms)) return 0;
+  if (whole_segments(c, B, (cols + 8 * nt - 1) / (8 * nt), Sq, max_pages, window, sinks, sms)) return 0;
   return *starts_at + (size_t)sms * sizeof(int4);
 }
+#endif
 
+#if FSA_CACHE_WINDOW
+cudaError_t launch_cache_attn_window(const CacheAttnArgs& a, int nt, int sms, cudaStream_t st) {
+#else
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, int nt, int sms, cudaStream_t st) {
+#endif
   if (a.c.D == 128) {
     if (a.c.cf == CF_MX) return nt == 1 ? launch<128, CF_MX, 1>(a, sms, st) : launch<128, CF_MX, 2>(a, sms, st);
     return nt == 1 ? launch<128, CF_NV, 1>(a, sms, st) : launch<128, CF_NV, 2>(a, sms, st);

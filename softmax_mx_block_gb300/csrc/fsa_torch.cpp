@@ -4,6 +4,7 @@
 // the Python side of a call has to cost no more; the same checks in Python took 10 to 20 us.
 // Nothing is computed or kept here.
 #include <Python.h>
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <cuda_runtime.h>
@@ -132,17 +133,20 @@ struct Table {
   }
 };
 
-// norm_rope(q, k, pos, inv_freq, sections, q_weight, k_weight, norm, eps, interleaved, q_out, k_out, stream)
-PyObject* norm_rope(PyObject* const* a) {
-  const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &qo = tensor(a[10], "q_out"), &ko = tensor(a[11], "k_out");
-  const int dev = device_of(q, "q");
+// q, k, pos, inv_freq, sections, q_weight, k_weight, norm, eps, interleaved, q_out at a[0..10]; ko: k_out, or null for
+// keys that go into the cache, which turn by their places where pos is None
+fsa_norm_rope rope_args(PyObject* const* a, int dev, const at::Tensor* ko) {
+  const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &qo = tensor(a[10], "q_out");
   fsa_norm_rope r{};
   r.q_strides = strided(q, "q", dev, false);
   r.k_strides = strided(k, "k", dev, false);
   r.q_out_strides = strided(qo, "q_out", dev, true);
-  r.k_out_strides = strided(ko, "k_out", dev, true);
   same_shape(qo, q, "q_out, q");
-  same_shape(ko, k, "k_out, k");
+  if (ko) {
+    r.k_out_strides = strided(*ko, "k_out", dev, true);
+    same_shape(*ko, k, "k_out, k");
+    r.k_out = ko->data_ptr();
+  }
   if (k.size(0) != q.size(0) || k.size(1) != q.size(1) || k.size(3) != q.size(3)) refuse(FSA_ERR_INVALID_ARG, "q, k shapes");
   const int64_t B = q.size(0), S = q.size(1), D = q.size(3);
   if (B > INT32_MAX || S > INT32_MAX || q.size(2) > INT32_MAX || k.size(2) > INT32_MAX) refuse(FSA_ERR_INVALID_ARG, "q, k shapes");
@@ -151,13 +155,15 @@ PyObject* norm_rope(PyObject* const* a) {
     const at::Tensor& f = tensor(a[3], "inv_freq");
     half = f.numel();
     r.inv_freq = plain<double>(a[3], "inv_freq", dev, at::kDouble, {half});
-    if (a[2] == Py_None) refuse(FSA_ERR_INVALID_ARG, "a rotation needs pos");
-    const at::Tensor& p = tensor(a[2], "pos");
-    if (p.dim() == 3) {
-      axes = p.size(2);
-      r.pos = plain<int32_t>(a[2], "pos", dev, at::kInt, {B, S, axes});
-    } else {
-      r.pos = plain<int32_t>(a[2], "pos", dev, at::kInt, {B, S});
+    if (a[2] == Py_None && ko) refuse(FSA_ERR_INVALID_ARG, "a rotation needs pos");
+    if (a[2] != Py_None) {
+      const at::Tensor& p = tensor(a[2], "pos");
+      if (p.dim() == 3) {
+        axes = p.size(2);
+        r.pos = plain<int32_t>(a[2], "pos", dev, at::kInt, {B, S, axes});
+      } else {
+        r.pos = plain<int32_t>(a[2], "pos", dev, at::kInt, {B, S});
+      }
     }
   }
   if (half > D / 2) refuse(FSA_ERR_INVALID_ARG, "inv_freq has more than D/2 pairs");
@@ -169,14 +175,41 @@ PyObject* norm_rope(PyObject* const* a) {
       refuse(FSA_ERR_INVALID_ARG, "sections must be a tuple of one number for each of %lld axes (1 to 3)", (long long)axes);
     for (int i = 0; i < axes; ++i) r.sections[i] = small_number(PyTuple_GET_ITEM(a[4], i));
   }
-  r.q = q.data_ptr(); r.k = k.data_ptr(); r.q_out = qo.data_ptr(); r.k_out = ko.data_ptr();
+  r.q = q.data_ptr(); r.k = k.data_ptr(); r.q_out = qo.data_ptr();
   r.q_weight = plain<void>(a[5], "q_weight", dev, at::kBFloat16, {D});
   r.k_weight = plain<void>(a[6], "k_weight", dev, at::kBFloat16, {D});
   r.B = (int)B; r.S = (int)S; r.H = (int)q.size(2); r.Hkv = (int)k.size(2); r.D = (int)D;
   r.rotary = (int)(2 * half); r.n_axes = (int)axes;
   r.norm = truth(a[7]); r.eps = (float)real(a[8]); r.interleaved = truth(a[9]);
+  return r;
+}
+
+// norm_rope(q, k, pos, inv_freq, sections, q_weight, k_weight, norm, eps, interleaved, q_out, k_out, stream)
+PyObject* norm_rope(PyObject* const* a) {
+  const int dev = device_of(tensor(a[0], "q"), "q");
+  const fsa_norm_rope r = rope_args(a, dev, &tensor(a[11], "k_out"));
   const Launch on(dev, a[12]);
   done(fsa_qk_norm_rope(&r, on.stream), "fsa_qk_norm_rope");
+  Py_RETURN_NONE;
+}
+
+// cache_append_rope(pages, page_size, Hkv, D, fmt, q, k, pos, inv_freq, sections, q_weight, k_weight, norm, eps, interleaved,
+//                   q_out, v, block_table, lens, new_lens, status, stream)
+PyObject* cache_append_rope(PyObject* const* a) {
+  const CacheArg c(a);
+  const fsa_norm_rope r = rope_args(a + 5, c.device, nullptr);
+  const at::Tensor &k = tensor(a[6], "k"), &v = tensor(a[16], "v");
+  const fsa_strides vs = strided(v, "v", c.device, false);
+  same_shape(v, k, "k, v");
+  if (k.size(2) != c.c.Hkv || k.size(3) != c.c.D) refuse(FSA_ERR_INVALID_ARG, "k, v shapes");
+  const Table table(a[17], r.B, c.device);
+  if (a[18] == Py_None) invalid("lens", "must be given");
+  const int32_t* lens = plain<int32_t>(a[18], "lens", c.device, at::kInt, {r.B});
+  const int32_t* fresh = plain<int32_t>(a[19], "new_lens", c.device, at::kInt, {r.B});
+  int32_t* status = plain<int32_t>(a[20], "status", c.device, at::kInt, {1});
+  const Launch on(c.device, a[21]);
+  done(fsa_cache_append_rope(&r, &c.c, v.data_ptr(), &vs, table.at, table.width, lens, fresh, status, on.stream),
+       "fsa_cache_append_rope");
   Py_RETURN_NONE;
 }
 
@@ -226,9 +259,9 @@ PyObject* cache_read(PyObject* const* a) {
   Py_RETURN_NONE;
 }
 
-// attention_cache(pages, page_size, Hkv, D, fmt, q, out, lse, block_table, lens, q_lens, causal, scale, workspace,
-//                 timeout_ms, status, stream); scale None: D^-1/2; workspace None: one of the call's own
-PyObject* attention_cache(PyObject* const* a) {
+// pages, page_size, Hkv, D, fmt, q, out, lse, block_table, lens, q_lens, causal, scale, workspace, timeout_ms, status,
+// stream, window, sinks; scale None: D^-1/2; workspace None: one of the call's own; window None: no window
+PyObject* attend(PyObject* const* a, bool chunk) {
   const CacheArg c(a);
   const at::Tensor &q = tensor(a[5], "q"), &out = tensor(a[6], "out");
   fsa_cache_attn r{};
@@ -256,11 +289,24 @@ PyObject* attention_cache(PyObject* const* a) {
   const long long limit = number(a[14]);
   if (limit < 0 || limit > UINT32_MAX) invalid("timeout_ms", "is out of range");
   r.timeout_ms = (uint32_t)limit;
+  int window = 0;
+  if (a[17] != Py_None) {
+    const long long w = number(a[17]);
+    if (w < 1) invalid("window", "must be at least 1 (the row's own token)");
+    if (!r.causal) invalid("window", "goes with causal attention");
+    window = (int)std::min<long long>(w, INT32_MAX);
+  }
+  const long long first = number(a[18]);
+  if (first < 0) invalid("sinks", "must not be negative");
+  if (first > 0 && !window) invalid("sinks", "go with a window");
+  const int sinks = (int)std::min<long long>(first, INT32_MAX);
   const Launch on(c.device, a[16]);
   at::Tensor own;
   if (a[13] == Py_None) {
     size_t need = 0;
-    done(fsa_attention_cache_workspace(&c.c, r.B, r.H, r.Sq, r.max_pages, &need), "fsa_attention_cache_workspace");
+    if (chunk) done(fsa_attention_chunk_workspace(&c.c, r.B, r.H, r.Sq, r.max_pages, &need), "fsa_attention_chunk_workspace");
+    else if (window) done(fsa_attention_cache_window_workspace(&c.c, r.B, r.H, r.Sq, r.max_pages, window, sinks, &need), "fsa_attention_cache_window_workspace");
+    else done(fsa_attention_cache_workspace(&c.c, r.B, r.H, r.Sq, r.max_pages, &need), "fsa_attention_cache_workspace");
     if (need > 0) {
       // made on the call's stream, so that what is freed there is used again only behind it
       c10::cuda::OptionalCUDAStreamGuard guard;
@@ -274,9 +320,13 @@ PyObject* attention_cache(PyObject* const* a) {
     r.workspace = plain<void>(a[13], "workspace", c.device, at::kByte, {ws.numel()});
     r.workspace_bytes = (size_t)ws.numel();
   }
-  done(fsa_attention_cache(&r, on.stream), "fsa_attention_cache");
+  if (chunk) done(fsa_attention_chunk(&r, window, sinks, on.stream), "fsa_attention_chunk");
+  else if (window) done(fsa_attention_cache_window(&r, window, sinks, on.stream), "fsa_attention_cache_window");
+  else done(fsa_attention_cache(&r, on.stream), "fsa_attention_cache");
   Py_RETURN_NONE;
 }
+PyObject* attention_cache(PyObject* const* a) { return attend(a, false); }
+PyObject* attention_chunk(PyObject* const* a) { return attend(a, true); }
 
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -310,7 +360,7 @@ PyObject* set_error(PyObject*, PyObject* cls) {
 
 #define FSA_ENTRY(name, n) {#name, (PyCFunction)(void (*)(void))entry<name, n>, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FSA_ENTRY(norm_rope, 13), FSA_ENTRY(cache_append, 12), FSA_ENTRY(cache_read, 12),
-                         FSA_ENTRY(attention_cache, 17), {"set_error", set_error, METH_O, nullptr},
+                         FSA_ENTRY(attention_cache, 19), FSA_ENTRY(attention_chunk, 19), FSA_ENTRY(cache_append_rope, 22), {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fsa_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

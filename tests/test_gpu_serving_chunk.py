@@ -1,0 +1,255 @@
+"""Attention of chunks over the paged 4-bit cache (fsa_attention_chunk) against its 64-bit definition.
+
+The tolerance, with eps/2 of a type as a rounding's largest relative error:
+  - a score is a sum of D exact products in fp32, each addition off by at most 2^-23 (it may cut), so by
+    (D + 8) 2^-23 of scale * sum |q||k|, and moves a weight by as much relatively, in the numerator
+    and in the denominator: twice that of sum p|v| / sum p;
+  - a probability is rounded to bf16, 2^-8 of it: 2^-8 of sum p|v| / sum p;
+  - its exponential and the sums, 16 keys an addition, a rescaling a tile: (n / 16 + n / 128) 2^-23 + 2^-18 of the same;
+  - a weight below fp32's normal range is flushed: 2^-126 against a running maximum that the largest score beats by at most 2^8, so
+    where the sum is at least 2^-8 .. 2^8 of the largest weight, n 2^-118 of the largest |v|; operands below 2^-110 lose 2^-118;
+  - an output in bf16 is rounded by 2^-8 of it.
+The log of the sums: the scores' error, and 2^-18."""
+import math
+
+import pytest
+
+import serving_window_ref as win
+from test_gpu_serving import _fsa, filled_cache, gen, i32, make_table, normal
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+def check(out, lse, q, seqs, q_lens, causal, scale, window, sinks, dtype):
+    for b, (k, v, live) in enumerate(seqs):
+        m, n, D = q_lens[b], k.shape[0], q.shape[-1]
+        want, want_lse, spread, reach = win.attention(q[b, :m], k, v, live, causal, scale, window, sinks)
+        score = (D + 8) * 2.0 ** -23 * reach
+        tol = spread * (2 * score + 2.0 ** -8 + (n / 16 + n / 128) * 2.0 ** -23 + 2.0 ** -18)[..., None]
+        tol = tol + n * 2.0 ** -118 * (1 + (float(v.abs().max()) if n else 0))
+        if dtype == "bf16":
+            tol = tol + 2.0 ** -8 * (want.abs() + tol)
+        got = out[b, :m].double()
+        bad = ~((got - want).abs() <= tol)
+        assert not bool(bad.any()), (b, int(bad.sum()), float(((got - want).abs() / tol.clamp(min=1e-30)).max()))
+        if lse is not None:
+            none = torch.isinf(want_lse)
+            assert torch.equal(none, torch.isinf(lse[b, :m]))
+            off = (lse[b, :m].double() - want_lse).abs()
+            assert bool((off[~none] <= (score + 2.0 ** -18 * (1 + want_lse.abs()))[~none]).all())
+
+
+def run(fsa, q, cache, table, lens, q_lens=None, causal=True, scale=None, window=None, sinks=0, dtype="f32", fmt=None, **kw):
+    """One call, its rows checked, the others left as they were."""
+    B, Sq, H, D = q.shape
+    real = [Sq] * B if q_lens is None else q_lens
+    out = torch.full((B, Sq, H, D), 7.0, dtype=torch.float32 if dtype == "f32" else torch.bfloat16, device="cuda")
+    lse = torch.full((B, Sq, H), 7.0, device="cuda")
+    got = fsa.fsa_attention_chunk(q, cache, table, i32(lens), q_lens=None if q_lens is None else i32(q_lens), causal=causal,
+                                  scale=scale, window=window, sinks=sinks, out=out, lse=lse, **kw)
+    assert got is out
+    for b, m in enumerate(real):
+        assert bool((out[b, m:] == 7.0).all()) and bool((lse[b, m:] == 7.0).all())
+    seqs = win.sequences(cache, table, lens, cache.Hkv, D, {v: k for k, v in fsa.FMT_BY_NAME.items()}[cache.fmt])
+    check(out, lse, q, seqs, real, causal, D ** -0.5 if scale is None else scale, window or 0, sinks, dtype)
+    return out, lse
+
+
+# lengths, rows, heads, kv heads, page: one tile and block, their edges, several of each
+SHAPES = [([1], 1, 1, 1, 16), ([77], 77, 4, 1, 16), ([128], 128, 1, 1, 64), ([129], 129, 1, 1, 64), ([127, 256], 64, 4, 2, 32),
+          ([700], 65, 4, 1, 128), ([300, 5, 1000], 5, 7, 1, 16), ([513, 640], 300, 2, 2, 256), ([2000], 33, 8, 8, 64),
+          ([4000, 17], 17, 24, 24, 32), ([1, 1024, 90], 90, 8, 2, 1024)]
+
+
+@pytest.mark.parametrize("fmt", ["E2M1", "NVFP4"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,Sq,H,Hkv,page", SHAPES)
+def test_shapes(fmt, D, lens, Sq, H, Hkv, page):
+    fsa = _fsa()
+    g = gen(len(lens) + Sq)
+    cache, table, _, _ = filled_cache(fsa, g, lens, page, Hkv, D, fmt)
+    q = normal(g, len(lens), Sq, H, D)
+    run(fsa, q, cache, table, lens)
+    run(fsa, q, cache, table, lens, causal=False, dtype="bf16")
+    run(fsa, q, cache, table, lens, window=50, sinks=3, dtype="bf16")
+
+
+@pytest.mark.parametrize("fmt,D", [("E2M1", 128), ("NVFP4", 64)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (2, 130), (127, 0), (128, 1), (129, 4), (500, 16), (900, 700), (2 ** 31 - 1, 0), (5, 2 ** 31 - 1)])
+def test_windows(fmt, D, window, sinks):
+    fsa = _fsa()
+    g = gen(window % 1000 + sinks % 1000)
+    lens, q_lens = [1500, 40, 0, 700, 2100], [90, 40, 0, 300, 1]
+    cache, table, _, _ = filled_cache(fsa, g, lens, 32, 2, D, fmt)
+    q = normal(g, len(lens), 300, 6, D) * 3
+    run(fsa, q, cache, table, lens, q_lens, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("fmt", ["E2M1", "NVFP4"])
+def test_ragged_rows(fmt, causal):
+    """q_lens from none to more than there are tokens (rows before the first see nothing); strided q and out; a table far wider than
+    the sequences; strong scores."""
+    fsa = _fsa()
+    g = gen(21)
+    lens, q_lens, Hkv, D, Sq, H = [100, 640, 3, 0, 2500, 31], [40, 0, 4, 2, 200, 100], 2, 128, 200, 8
+    cache, table, _, _ = filled_cache(fsa, g, lens, 32, Hkv, D, fmt)
+    table = torch.nn.functional.pad(table, (0, 300), value=-1)
+    qkv = normal(g, len(lens), Sq, H + 2 * Hkv, D) * 4
+    out, _ = run(fsa, qkv[:, :, :H], cache, table, lens, q_lens, causal)
+    strided = torch.full((len(lens), H, Sq, D), 7.0, device="cuda").transpose(1, 2)
+    fsa.fsa_attention_chunk(qkv[:, :, :H], cache, table, i32(lens), q_lens=i32(q_lens), causal=causal, out=strided)
+    assert torch.equal(strided, out)
+
+
+def test_blocks_with_and_without_a_second_tile():
+    """Many short segments a CTA, some of more than 128 rows and some of fewer, none among them."""
+    fsa = _fsa()
+    g = gen(29)
+    lens = [300, 40, 700, 260, 33, 500, 129, 9] * 5
+    q_lens = [130, 3, 65, 64, 0, 128, 60, 9] * 5
+    for fmt, Hkv, causal in (("E2M1", 24, True), ("NVFP4", 8, False)):
+        cache, table, _, _ = filled_cache(fsa, g, lens, 16, Hkv, 64, fmt)
+        table = torch.nn.functional.pad(table, (0, 3), value=-1)
+        run(fsa, normal(g, len(lens), 130, 2 * Hkv, 64), cache, table, lens, q_lens, causal)
+        run(fsa, normal(g, len(lens), 130, 2 * Hkv, 64), cache, table[:, :32].contiguous(), [min(n, 512) for n in lens], q_lens, causal, dtype="bf16")
+
+
+def test_long_keys_over_many_ctas():
+    """Few rows over many keys: parts of a segment from all CTAs, joined; rows that see none of a part."""
+    fsa = _fsa()
+    g = gen(5)
+    for fmt, D, Hkv in (("E2M1", 128, 1), ("NVFP4", 64, 2)):
+        lens = [40000, 300]
+        cache, table, _, _ = filled_cache(fsa, g, lens, 64, Hkv, D, fmt)
+        q = normal(g, 2, 60, 4 * Hkv, D)
+        run(fsa, q, cache, table, lens)
+        run(fsa, q, cache, table, lens, window=20000, sinks=200, dtype="bf16")
+        run(fsa, q * 30, cache, table, lens, [7, 60], dtype="bf16")
+
+
+@pytest.mark.parametrize("fmt", ["E2M1", "NVFP4"])
+def test_scales_and_ranges(fmt):
+    """Scales of every sign; values and keys far from one, a rising maximum, strong first tokens."""
+    fsa = _fsa()
+    g = gen(31)
+    n, Hkv, D = 1300, 2, 128
+    for kind in range(5):
+        k, v = normal(g, 1, n, Hkv, D), normal(g, 1, n, Hkv, D)
+        if kind == 0:
+            v = v * torch.exp2(torch.randint(-15, 16, (1, n, 1, 1), generator=g, device="cuda").float()).to(v.dtype)
+        elif kind == 1:
+            v[:, 500:], k = v[:, 500:] * 2.0 ** 24, k * 2.0 ** -20
+        elif kind == 2:
+            v.zero_()
+        elif kind == 3:
+            k = k * torch.linspace(0.1, 8.0, n, device="cuda")[None, :, None, None].to(k.dtype)
+            v[:, 100:200] = v[:, 100:200] * 2.0 ** -30
+        else:
+            k[:, 0] = k[:, 0] * 2.0 ** 30
+            k[:, 1:] = k[:, 1:] * 2.0 ** 20
+            v[:, 0] = v[:, 0] * 2.0 ** -12
+        table, pages = make_table(g, [n], 64)
+        cache = fsa.empty_cache(pages, 64, Hkv, D, fmt)
+        cache.pages.fill_(0xFF)
+        fsa.fsa_cache_append(cache, k, v, table, i32([n]))
+        q = normal(g, 1, 70, 8, D) * (3 if kind != 4 else 2.0 ** -22)
+        for scale in (None, -0.05, 0.0, 1.0):
+            run(fsa, q, cache, table, [n], scale=scale)
+
+
+@pytest.mark.parametrize("fmt", ["E2M1", "NVFP4"])
+def test_nan_stays_with_its_rows(fmt):
+    """A token with a non-finite key or value makes the rows NaN that see it, and no others; so does a
+    row of q; bytes of unused places (here NaN scales) count nothing."""
+    fsa = _fsa()
+    g = gen(41)
+    n, Hkv, D, Sq = 400, 2, 128, 150
+    k, v = normal(g, 1, n, Hkv, D), normal(g, 1, n, Hkv, D)
+    table, pages = make_table(g, [n], 16)
+    cache = fsa.empty_cache(pages, 16, Hkv, D, fmt)
+    cache.pages.fill_(0xFF)
+    q = normal(g, 1, Sq, 8, D)
+    fsa.fsa_cache_append(cache, k, v, table, i32([n]))
+    clean = fsa.fsa_attention_chunk(q, cache, table, i32([n]))
+    assert bool(torch.isfinite(clean).all())
+    v[0, n - 30, 0, 40] = math.nan                 # rows Sq - 30 .. of head 0's queries
+    k[0, n - 100, 1, 7] = math.inf                 # rows Sq - 100 .. of head 1's
+    fsa.fsa_cache_append(cache, k, v, table, i32([n]))
+    out = fsa.fsa_attention_chunk(q, cache, table, i32([n]))
+    for h, first in ((0, Sq - 30), (1, Sq - 100)):
+        part = slice(4 * h, 4 * h + 4)
+        assert torch.equal(out[0, :first, part], clean[0, :first, part]) and bool(torch.isnan(out[0, first:, part]).all())
+    out = fsa.fsa_attention_chunk(q, cache, table, i32([n]), window=20, sinks=0)
+    nan = torch.isnan(out[0]).all(-1)
+    assert torch.equal(nan, torch.isnan(out[0]).any(-1))
+    row = torch.arange(Sq, device="cuda")
+    assert torch.equal(nan[:, 0], (row >= Sq - 30) & (row < Sq - 10)) and torch.equal(nan[:, 4], (row >= Sq - 100) & (row < Sq - 80))
+    q[0, 60, 3, 5], q[0, 61, 2, 9] = math.nan, -math.inf
+    out = fsa.fsa_attention_chunk(q, cache, table, i32([n]))
+    assert bool(torch.isnan(out[0, 60, 3]).all()) and bool(torch.isnan(out[0, 61, 2]).all()) and bool(torch.isfinite(out[0, 60, 2]).all())
+
+
+def test_bad_pages_and_lengths():
+    """Pages outside the pool are not seen and set the status; lengths are cut to the table and at 0."""
+    fsa = _fsa()
+    g = gen(43)
+    lens, Hkv, D, fmt = [700, 300, 90], 2, 128, "NVFP4"
+    cache, table, _, _ = filled_cache(fsa, g, lens, 16, Hkv, D, fmt)
+    q, status = normal(g, 3, 80, 4, D), i32([0])
+    run(fsa, q, cache, table, lens, status=status)
+    assert int(status) == 0
+    bad = table.clone()
+    bad[0, 3], bad[0, 20], bad[1, :], bad[2, 5] = cache.pages.shape[0], -5, 1 << 30, -1
+    run(fsa, q, cache, bad, lens, status=status)
+    assert int(status) == fsa.FSA_ERR_INVALID_ARG
+    wide = fsa.fsa_attention_chunk(q, cache, table[:, :10].contiguous(), i32([1 << 30, 300, 90]))
+    assert torch.equal(wide, fsa.fsa_attention_chunk(q, cache, table[:, :10].contiguous(), i32([160, 160, 90])))
+    none, lse = torch.full((3, 80, 4, D), 7.0, device="cuda"), torch.zeros(3, 80, 4, device="cuda")
+    fsa.fsa_attention_chunk(q, cache, table, i32([-5, -(1 << 31), 0]), out=none, lse=lse)
+    assert bool((none == 0).all()) and bool((lse == -math.inf).all())
+
+
+def test_workspace_streams_and_graph():
+    """A given workspace with any content, another stream, a captured call that follows the lengths, the same bits
+    each time."""
+    fsa = _fsa()
+    g = gen(61)
+    Hkv, D, H, Sq = 4, 128, 16, 70
+    cache, table, _, _ = filled_cache(fsa, g, [900, 4000], 64, Hkv, D, "E2M1")
+    q = normal(g, 2, Sq, H, D)
+    lens, q_lens = i32([900, 4000]), i32([70, 33])
+    first = fsa.fsa_attention_chunk(q, cache, table, lens, q_lens=q_lens)
+    ws = torch.full((fsa.fsa_attention_chunk_workspace(cache, 2, H, Sq, table.shape[1]),), 0xFF, dtype=torch.uint8, device="cuda")
+    for _ in range(5):
+        assert torch.equal(first, fsa.fsa_attention_chunk(q, cache, table, lens, q_lens=q_lens, workspace=ws))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = fsa.fsa_attention_chunk(q, cache, table, lens, q_lens=q_lens, stream=side)
+    side.synchronize()
+    assert torch.equal(first, other)
+    out = torch.zeros(2, Sq, H, D, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fsa.fsa_attention_chunk(q, cache, table, lens, q_lens=q_lens, out=out, workspace=ws)
+    for n, m in (([900, 4000], [70, 33]), ([1, 17], [1, 17]), ([0, 3999], [5, 70]), ([640, 64], [0, 64])):
+        lens.copy_(i32(n))
+        q_lens.copy_(i32(m))
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, fsa.fsa_attention_chunk(q, cache, table, lens, q_lens=q_lens))
+
+
+def test_as_the_decode_call():
+    """The same attention as fsa_attention_cache, to both calls' rounding (bf16 2^-8, f16 2^-10 of each weight)."""
+    fsa = _fsa()
+    g = gen(71)
+    for fmt in ("E2M1", "NVFP4"):
+        lens = [1200, 77]
+        cache, table, _, v = filled_cache(fsa, g, lens, 16, 2, 64, fmt)
+        q = normal(g, 2, 40, 8, 64)
+        for kw in ({}, dict(causal=False), dict(window=100, sinks=2)):
+            a = fsa.fsa_attention_chunk(q, cache, table, i32(lens), **kw)
+            b = fsa.fsa_attention_cache(q, cache, table, i32(lens), **kw)
+            assert float((a - b).abs().max()) <= 2 * (2.0 ** -8 + 2.0 ** -10 + 2.0 ** -12) * float(v.abs().max())
