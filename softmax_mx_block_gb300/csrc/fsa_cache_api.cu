@@ -141,14 +141,25 @@ bool sm_count(int* sms) {
   return false;
 }
 
+bool rows_ok(int B, int H, int Hkv, int Sq, int D, int max_pages, int page_size) {
+  return B > 0 && H > 0 && Hkv > 0 && H % Hkv == 0 && Sq > 0 && (D == 64 || D == 128) && pages_ok(max_pages, page_size) &&
+         (int64_t)B * H <= (1 << 27) / Sq;
+}
+
 // The kernels count rows and, over all sequences, heads and passes of columns, tiles of 32
 // keys (and what a segment's start weighs, at most 8) in 32 bits.
 bool attn_shape_ok(int B, int H, int Hkv, int Sq, int D, int max_pages, int page_size) {
-  if (!(B > 0 && H > 0 && Hkv > 0 && H % Hkv == 0 && Sq > 0 && (D == 64 || D == 128) && pages_ok(max_pages, page_size) &&
-        (int64_t)B * H <= (1 << 27) / Sq))
-    return false;
+  if (!rows_ok(B, H, Hkv, Sq, D, max_pages, page_size)) return false;
   const int64_t passes = ((int64_t)Sq * (H / Hkv) + 7) / 8, tiles = ((int64_t)max_pages * page_size + 31) / 32 + 8;
   return (int64_t)B * Hkv <= INT_MAX / passes / tiles;
+}
+
+// The kernel counts key tiles of 128 over all blocks of 256 rows (and what a block weighs beside
+// them, at most 4 more) in 32 bits.
+bool chunk_shape_ok(int B, int H, int Hkv, int Sq, int D, int max_pages, int page_size) {
+  if (!rows_ok(B, H, Hkv, Sq, D, max_pages, page_size)) return false;
+  const int64_t blocks = fsa::cache_chunk_blocks(Sq * (H / Hkv)), tiles = ((int64_t)max_pages * page_size + 127) / 128 + 4;
+  return (int64_t)B * Hkv <= INT_MAX / blocks / tiles;
 }
 
 // A window of at least the row itself, and the first keys beside it.
@@ -176,12 +187,12 @@ int attn_workspace(const fsa_cache* cache, int B, int H, int Sq, int max_pages, 
 }
 
 // What the calls that attend over the cache have in common: their checks, and what the kernels take.
-int take_attn(const fsa_cache_attn* c, int window, int sinks, fsa::CacheAttnArgs* a) {
+int take_attn(const fsa_cache_attn* c, int window, int sinks, bool (*shape_ok)(int, int, int, int, int, int, int), fsa::CacheAttnArgs* a) {
   if (!c) return FSA_ERR_INVALID_ARG;
   const int st = take_cache(c->cache, &a->c);
   if (st != FSA_OK) return st;
   const int Hkv = a->c.Hkv, D = a->c.D;
-  if (!c->q || !c->out || !c->lens || !attn_shape_ok(c->B, c->H, Hkv, c->Sq, D, c->max_pages, c->cache->page_size) ||
+  if (!c->q || !c->out || !c->lens || !shape_ok(c->B, c->H, Hkv, c->Sq, D, c->max_pages, c->cache->page_size) ||
       !table_ok(c->block_table, c->max_pages, c->cache->page_size) || !(std::fabs(c->scale) <= 1e30f) ||
       (c->causal != 0 && c->causal != 1) || (c->out_dtype != FSA_OUT_F32 && c->out_dtype != FSA_OUT_BF16) ||
       !aligned(c->q, 16) || !aligned(c->out, 16) || !aligned(c->workspace, 16) || !aligned(c->lens, 4) ||
@@ -220,7 +231,7 @@ bool take_workspace(const fsa_cache_attn* c, size_t need, size_t starts_at, fsa:
 
 int attention_cache(const fsa_cache_attn* c, int window, int sinks, void* stream) {
   fsa::CacheAttnArgs a{};
-  const int st = take_attn(c, window, sinks, &a);
+  const int st = take_attn(c, window, sinks, attn_shape_ok, &a);
   if (st != FSA_OK) return st;
   int sms = 0;
   if (!sm_count(&sms)) return FSA_ERR_NO_DEVICE;
@@ -234,14 +245,6 @@ int attention_cache(const fsa_cache_attn* c, int window, int sinks, void* stream
   a.g_mul = G > 1 && (uint64_t)c->Sq * G * G < (1ull << 32) ? (uint32_t)((1ull << 32) / G + 1) : 0;
   const cudaStream_t on = static_cast<cudaStream_t>(stream);
   return launch_status(a.window ? fsa::launch_cache_attn_window(a, nt, sms, on) : fsa::launch_cache_attn(a, nt, sms, on));
-}
-
-// The kernel counts key tiles of 128 over all blocks of 256 rows (and what a block weighs beside
-// them, at most 4 more) in 32 bits.
-bool chunk_shape_ok(int B, int H, int Hkv, int Sq, int D, int max_pages, int page_size) {
-  if (!attn_shape_ok(B, H, Hkv, Sq, D, max_pages, page_size)) return false;
-  const int64_t blocks = fsa::cache_chunk_blocks(Sq * (H / Hkv)), tiles = ((int64_t)max_pages * page_size + 127) / 128 + 4;
-  return (int64_t)B * Hkv <= INT_MAX / blocks / tiles;
 }
 
 }  // namespace
@@ -341,9 +344,8 @@ int fsa_attention_chunk_workspace(const fsa_cache* cache, int B, int H, int Sq, 
 int fsa_attention_chunk(const fsa_cache_attn* c, int window, int sinks, void* stream) {
   if (!c || window < 0 || sinks < 0 || (window > 0 && c->causal != 1) || (window == 0 && sinks > 0)) return FSA_ERR_INVALID_ARG;
   fsa::CacheAttnArgs a{};
-  const int st = take_attn(c, window, sinks, &a);
+  const int st = take_attn(c, window, sinks, chunk_shape_ok, &a);
   if (st != FSA_OK) return st;
-  if (!chunk_shape_ok(c->B, c->H, a.c.Hkv, c->Sq, a.c.D, c->max_pages, c->cache->page_size)) return FSA_ERR_INVALID_ARG;
   int sms = 0;
   if (!sm_count(&sms)) return FSA_ERR_NO_DEVICE;
   size_t starts_at;
