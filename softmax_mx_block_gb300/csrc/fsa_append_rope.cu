@@ -7,12 +7,12 @@
 //   y = x / sqrt(mean(x^2) + eps) * w,  (a, b) -> (a cos t - b sin t, a sin t + b cos t),  t = pos * inv_freq
 // (through bf16 they would be rounded twice).  They are computed in fp32, whose error is
 // known: with Y the row's largest |y|, |a| + |b| <= 2 Y for every pair, the angle is off by at most
-// 2^-22.3 (half an ulp of a part of a turn, for positions up to 2^24), cos and sin by 2^-23 of 1, the factor
-// of the norm by 2^-21.4 of itself and each operation by 2^-24, together below 2^-19 Y.  So each
-// block is rounded twice, from y - 2^-18 Y and from y + 2^-18 Y (the quotient by an E4M3 scale is off by
-// at most 2^-19 too); where scale and codes agree, as in all but about one warp in 100, they are
-// the exact ones, and where they do not the warp's rows are computed in fp64.  Elements that neither
-// a norm nor an angle touches are exact as they are, and rounded as fsa_cache_append does.
+// 2^-22.3 (an ulp of a part of a turn, for positions up to 2^24), cos and sin by 2^-23 and the two products by
+// 2^-24 each, together 2^-20.2 Y; the norm's factor by 2^-21.4 of y, a quotient by an E4M3 scale by 2^-22.4: in
+// all 2^-19.4 Y.  So each block is rounded twice, from y - 2^-19 Y and from y + 2^-19 Y; where scale and
+// codes agree, as in all but about one warp in 100, they are the exact ones, and what is left open is
+// computed in fp64.  Elements that neither a norm nor an angle touches are exact as they are, and
+// rounded as fsa_cache_append does.
 //
 // Bound by memory: 4 H + 4 Hkv + 2 Hkv (0.53 or 0.56) bytes a token and dim.  A block takes a
 // few tokens with all their heads, as fsa_qk_norm_rope does: the sines of a token are computed
@@ -26,7 +26,7 @@
 namespace fsa {
 namespace {
 
-constexpr float SURE = 0x1p-18f;      // of a row's largest |y|: more than the fp32 arithmetic is off by
+constexpr float SURE = 0x1p-19f;      // of a row's largest |y|: more than the fp32 arithmetic is off by
 constexpr int KV_ROWS = 2;            // rows of a thread in flight, of k and of v each
 
 struct Place {
@@ -123,31 +123,116 @@ __device__ __forceinline__ uint4 others_of(uint4 x, int half, int row, int l) {
 __device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// The codes and the scale byte of a lane's eight, in fp64 from the definition (all lanes of a
-// warp, D/8 a row).
+// What the fp32 values of a lane's eight say of their codes.
+struct Codes {
+  uint32_t codes, sb;
+  uint32_t open;       // nibbles that the values' error leaves open
+  bool scale_open;     // whether it leaves the block's scale open
+};
+
+// 8 values y +- d of a lane (d >= 0; 0: exactly y) as codes and scale byte.
+template <int CF>
+__device__ __forceinline__ Codes codes_of(const float (&y)[8], float d) {
+  Codes r;
+  float top = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(y[e]));
+  float tlo = fmaxf(top - d, 0.f), thi = top + d;
+#pragma unroll
+  for (int m = 1; m < (CF == CF_MX ? 4 : 2); m *= 2) {
+    tlo = fmaxf(tlo, __shfl_xor_sync(0xFFFFFFFFu, tlo, m));
+    thi = fmaxf(thi, __shfl_xor_sync(0xFFFFFFFFu, thi, m));
+  }
+  const bool exact = d == 0.f;
+  float mul;
+  if constexpr (CF == CF_MX) {
+    const uint32_t m = __float_as_uint(thi) >> 23;               // exponent, less 2 (zero and subnormal: 0)
+    r.sb = (uint32_t)max((int)m - 2, 0);
+    r.scale_open = m >= 0xFF || r.sb != (uint32_t)max((int)(__float_as_uint(tlo) >> 23) - 2, 0);
+    mul = __uint_as_float((254u - r.sb) << 23);
+  } else {
+    // (1/6 as a float is half an ulp above it; raised by 2^-20 and cut, ties stay ties: fsa_cache_codes.cuh)
+    constexpr float SIXTH = 0.16666667163372039795f, RAISE = 1.0f + 0x1p-20f, LESS = 1.0f - 0x1p-20f;
+    const bool known = thi == tlo;
+    r.sb = cvt_e4m3x2(known ? cut12(thi * (SIXTH * RAISE)) : thi * (SIXTH * RAISE), 0.f) & 0xFFu;
+    r.scale_open = !(thi < 3e38f) || (!known && r.sb != (cvt_e4m3x2(tlo * (SIXTH * LESS), 0.f) & 0xFFu));
+    const float s = e4m3_to_f32(r.sb);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(mul) : "f"(s));
+    mul = s > 0.f ? (exact ? mul * RAISE : mul) : 0.f;           // (codes of a zero scale are zeros, without signs)
+  }
+  float x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    x[e] = (y[e] + d) * mul;
+    if (CF == CF_NV && exact) x[e] = cut12(x[e]);
+  }
+  r.codes = cvt_e2m1x8(x);
+  if (CF == CF_NV && mul == 0.f) r.codes = 0u;
+  r.open = 0u;
+  if (!exact && !(CF == CF_NV && mul == 0.f)) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = (y[e] - d) * mul;
+    r.open = r.codes ^ cvt_e2m1x8(x);
+  }
+  return r;
+}
+
+// The codes that are open (and all of a block whose scale is) in fp64 from the definition; all
+// lanes of a warp, D/8 a row.  One GB300's fp64 pipe takes 16 cycles a warp instruction and a sine with its
+// cosine about 50, so what is not needed is left out, and the sum of squares is kept as two floats.
 template <int D, bool INTER, int CF>
-__device__ __noinline__ uint2 exact_codes(const RopeArgs& a, uint4 own, uint4 others, const int32_t* pos, int place, int l) {
+__device__ __noinline__ void close_codes(const RopeArgs& a, uint4 own, uint4 others, const int32_t* pos, int place, int l, Codes& r) {
   constexpr int L = D / 8, PER = CF == CF_MX ? 4 : 2;
   const uint32_t w[4] = {own.x, own.y, own.z, own.w}, v[4] = {others.x, others.y, others.z, others.w};
-  double rr = 1.0, top = 0.0, y[8];
+  double rr = 1.0;
   if (a.norm) {
-    double ss = 0.0;
+    float hi = 0.f, lo = 0.f;                        // squares of bf16 are exact in fp32; a sum and what it drops
+    auto add = [&](float x) {
+      const float s = hi + x, t = s - hi;
+      lo += (hi - (s - t)) + (x - t);
+      hi = s;
+    };
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const double p = lo_bf16(w[i]), q = hi_bf16(w[i]);
-      ss += p * p + q * q;
+      add(__fmul_rn(lo_bf16(w[i]), lo_bf16(w[i])));
+      add(__fmul_rn(hi_bf16(w[i]), hi_bf16(w[i])));
     }
 #pragma unroll
-    for (int m = 1; m < L; m *= 2) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, m);
-    rr = 1.0 / sqrt(ss / D + (double)a.eps);
+    for (int m = 1; m < L; m *= 2) {
+      const float h = __shfl_xor_sync(0xFFFFFFFFu, hi, m), k = __shfl_xor_sync(0xFFFFFFFFu, lo, m);
+      add(h);
+      lo += k;
+    }
+    double mean = ((double)hi + (double)lo) * (1.0 / D) + (double)a.eps;
+    const bool within = hi < 0x1p100f && mean > 0x1p-90;
+    if (within) {
+      const double y = (double)rsqrtf((float)mean), e = ::fma(-mean * y, y, 1.0);      // |e| < 2^-20: the next term is e^3
+      rr = ::fma(y * e, ::fma(0.375, e, 0.5), y);
+    }
+    if (!__all_sync(0xFFFFFFFFu, within)) {          // beyond fp32's range (the warp's rows go along: they shuffle)
+      double ss = 0.0;
+#pragma unroll 1
+      for (int e = 0; e < 8; ++e) {
+        const double x = e & 1 ? hi_bf16(w[e >> 1]) : lo_bf16(w[e >> 1]);
+        ss += x * x;
+      }
+#pragma unroll
+      for (int m = 1; m < L; m *= 2) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, m);
+      if (!within) rr = 1.0 / sqrt(ss / D + (double)a.eps);
+    }
   }
+  if (r.scale_open) r.open = 0xFFFFFFFFu;
   bool finite = true;
+  double top = 0.0, y[8];
 #pragma unroll 1
   for (int e = 0; e < 8; ++e) {
+    const bool mine = r.open >> (4 * e) & 15u;
+    y[e] = 0.0;
+    if (!__any_sync(0xFFFFFFFFu, mine)) continue;
     const int at = 8 * l + e;
     double x = e & 1 ? hi_bf16(w[e >> 1]) : lo_bf16(w[e >> 1]);
     if (a.norm) x *= rr * (a.wk ? (double)bf16_to_f32(a.wk[at]) : 1.0);
-    if (at < 2 * a.half) {
+    if (mine && at < 2 * a.half) {
       int pair, other;
       bool second;
       pair_of<INTER>(at, a.half, pair, other, second);
@@ -168,78 +253,34 @@ __device__ __noinline__ uint2 exact_codes(const RopeArgs& a, uint4 own, uint4 ot
     top = fmax(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
     finite &= (bool)__shfl_xor_sync(0xFFFFFFFFu, (int)finite, m);
   }
-  uint32_t byte;
-  double inv = 0.0;                       // 1 over the scale, for E8M0
-  double scale = 0.0;
+  double scale;
   if constexpr (CF == CF_MX) {
-    const int e = max((int)((uint32_t)__double2hiint(top) >> 20 & 0x7FF) - 1023 - 2, -127);
-    byte = finite ? (uint32_t)(min(e, 127) + 127) : 0xFFu;
-    inv = __hiloint2double((1023 - min(e, 127)) << 20, 0);
+    if (r.scale_open) {
+      const int e = min(max((int)((uint32_t)__double2hiint(top) >> 20 & 0x7FF) - 1023 - 2, -127), 127);
+      r.sb = finite ? (uint32_t)(e + 127) : 0xFFu;
+    }
+    scale = __hiloint2double((int)(1023 - 127 + min(r.sb, 254u)) << 20, 0);
   } else {
-    const double t = fmin(top / 6.0, 448.0);
-    const int ex = max((int)((uint32_t)__double2hiint(t) >> 20 & 0x7FF) - 1023, -6);
-    const double n = rint(t * __hiloint2double((1023 + 3 - ex) << 20, 0));            // 8..16 steps, or fewer when subnormal
-    scale = n * __hiloint2double((1023 + ex - 3) << 20, 0);
-    byte = !finite ? 0x7Fu : (uint32_t)(n < 8.0 ? n : (ex + 7) * 8 + n - 8.0);
+    if (r.scale_open) {
+      const double t = fmin(top / 6.0, 448.0);
+      const int ex = max((int)((uint32_t)__double2hiint(t) >> 20 & 0x7FF) - 1023, -6);
+      const double n = rint(t * __hiloint2double((1023 + 3 - ex) << 20, 0));          // 8..16 steps, or fewer when subnormal
+      r.sb = !finite ? 0x7Fu : (uint32_t)(n < 8.0 ? n : (ex + 7) * 8 + n - 8.0);
+    }
+    scale = (double)e4m3_to_f32(r.sb);
   }
-  uint32_t codes = 0;
+  // the borders times the scale are exact
 #pragma unroll 1
   for (int e = 0; e < 8; ++e) {
-    const double q = CF == CF_MX ? y[e] * inv : scale > 0.0 ? y[e] / scale : 0.0, m = fabs(q);
-    const uint32_t code = (m > 0.25) + (m >= 0.75) + (m > 1.25) + (m >= 1.75) + (m > 2.5) + (m >= 3.5) + (m > 5.0);
-    codes |= (code | (signbit(q) ? 8u : 0u)) << (4 * e);
+    const bool mine = r.open >> (4 * e) & 15u;
+    if (!__any_sync(0xFFFFFFFFu, mine)) continue;
+    const double m = fabs(y[e]);
+    uint32_t code = (m > 0.25 * scale) + (m >= 0.75 * scale) + (m > 1.25 * scale) + (m >= 1.75 * scale) + (m > 2.5 * scale) +
+                    (m >= 3.5 * scale) + (m > 5.0 * scale);
+    code |= signbit(y[e]) ? 8u : 0u;
+    if (CF == CF_NV && scale == 0.0) code = 0u;
+    if (mine) r.codes = (r.codes & ~(15u << (4 * e))) | (finite ? code : 0u) << (4 * e);
   }
-  return make_uint2(finite ? codes : 0u, byte);
-}
-
-// 8 values y +- d of a lane (d >= 0) as codes and scale byte; false where some value of the interval
-// would get others.
-template <int CF>
-__device__ __forceinline__ bool sure_codes(const float (&y)[8], float d, uint32_t& codes, uint32_t& sb) {
-  float top = 0.f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(y[e]));
-  float tlo = fmaxf(top - d, 0.f), thi = top + d;
-#pragma unroll
-  for (int m = 1; m < (CF == CF_MX ? 4 : 2); m *= 2) {
-    tlo = fmaxf(tlo, __shfl_xor_sync(0xFFFFFFFFu, tlo, m));
-    thi = fmaxf(thi, __shfl_xor_sync(0xFFFFFFFFu, thi, m));
-  }
-  bool sure;
-  float mul;
-  if constexpr (CF == CF_MX) {
-    const uint32_t m = __float_as_uint(thi) >> 23;               // exponent, less 2 (zero and subnormal: 0)
-    sb = (uint32_t)max((int)m - 2, 0);
-    sure = m < 0xFF && sb == (uint32_t)max((int)(__float_as_uint(tlo) >> 23) - 2, 0);
-    mul = __uint_as_float((254u - sb) << 23);
-  } else {
-    constexpr float SIXTH = 0.16666667163372039795f;             // (half an ulp above 1/6: within the 2^-20)
-    const float c = 1.0f + 0x1p-20f;
-    if (thi == tlo) {
-      sb = cvt_e4m3x2(cut12(thi * (SIXTH * c)), 0.f) & 0xFFu;
-      sure = thi < 3e38f;
-    } else {
-      sb = cvt_e4m3x2(thi * (SIXTH * c), 0.f) & 0xFFu;
-      sure = thi < 3e38f && sb == (cvt_e4m3x2(tlo * (SIXTH * (1.0f - 0x1p-20f)), 0.f) & 0xFFu);
-    }
-    const float s = e4m3_to_f32(sb);
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(mul) : "f"(s));
-    mul = s > 0.f ? mul * c : 0.f;
-    sure = sure && (s > 0.f || thi == 0.f);                        // (codes of a zero scale are zeros without signs)
-  }
-  float x[8];
-  const bool exact = d == 0.f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    x[e] = (y[e] + d) * mul;
-    if (CF == CF_NV && exact) x[e] = cut12(x[e]);
-  }
-  codes = cvt_e2m1x8(x);
-  if (CF == CF_NV && mul == 0.f) codes = 0u;
-  if (exact) return sure;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = (y[e] - d) * mul;
-  return sure && (codes == cvt_e2m1x8(x) || (CF == CF_NV && mul == 0.f));
 }
 
 template <int D, int P, bool INTER, int CF, int BLOCKS>
@@ -286,6 +327,24 @@ __global__ void __launch_bounds__(ROPE_THREADS, BLOCKS) append_rope_kernel(const
   const uint32_t ktok = first + min(kj, ntok - 1);
   Place at = place_of(p, ktok, Gr::BYTES, keys && kj < ntok);
   if (kj >= ntok) at.live = false;
+  const int kb = (int)(ktok / (uint32_t)a.S), ks = (int)(ktok - (uint32_t)kb * (uint32_t)a.S);
+  int kh = kgroup - kj * kstep;
+  const uint16_t* ksrc = a.k + kb * a.ks.b + ks * a.ks.s + kh * a.ks.h + 8 * l;
+  const uint16_t* vsrc = p.v + kb * p.vs.b + ks * p.vs.s + kh * p.vs.h + 8 * l;
+  const int64_t head = ((int64_t)1 << (p.c.page_shift - 4)) * Gr::BYTES;
+  const bool kept = at.group != nullptr;
+  uint8_t* codes = at.group + kh * head + at.row * (D / 2) + 4 * l;
+  uint8_t* scales = at.group + kh * head + Gr::KS + at.row * Gr::SB + l / PER;
+  uint4 ku[KV_ROWS], vu[KV_ROWS];
+  auto load_kv = [&] {
+#pragma unroll
+    for (int r = 0; r < KV_ROWS; ++r) {
+      const bool in = kept && kh + r * kstep < a.Hkv;
+      ku[r] = in ? *reinterpret_cast<const uint4*>(ksrc + r * kstep * a.ks.h) : make_uint4(0u, 0u, 0u, 0u);
+      vu[r] = in ? *reinterpret_cast<const uint4*>(vsrc + r * kstep * p.vs.h) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  if (!queries) load_kv();                                        // (the queries' rows would keep them waiting)
 
   if (a.half > 0) {
     const int per = ROPE_THREADS / a.half;        // tokens at a time
@@ -321,26 +380,12 @@ __global__ void __launch_bounds__(ROPE_THREADS, BLOCKS) append_rope_kernel(const
   }
   if (!keys) return;
 
-  // keys and values: every lane of a warp goes along (their rows end together)
-  const int kb = (int)(ktok / (uint32_t)a.S), ks = (int)(ktok - (uint32_t)kb * (uint32_t)a.S);
-  int kh = kgroup - kj * kstep;
-  const uint16_t* ksrc = a.k + kb * a.ks.b + ks * a.ks.s + kh * a.ks.h + 8 * l;
-  const uint16_t* vsrc = p.v + kb * p.vs.b + ks * p.vs.s + kh * p.vs.h + 8 * l;
-  const int64_t head = ((int64_t)1 << (p.c.page_shift - 4)) * Gr::BYTES;
-  const bool kept = at.group != nullptr;
-  uint8_t* codes = at.group + kh * head + at.row * (D / 2) + 4 * l;
-  uint8_t* scales = at.group + kh * head + Gr::KS + at.row * Gr::SB + l / PER;
+  // every lane of a warp goes along (their rows end together)
   Lane8 f;
   set_lane<D, INTER>(f, a, sines + kj * a.half, l);
 #pragma unroll 1
   for (int n = a.Hkv; n > 0; n -= KV_ROWS * kstep) {
-    uint4 ku[KV_ROWS], vu[KV_ROWS];
-#pragma unroll
-    for (int r = 0; r < KV_ROWS; ++r) {
-      const bool in = kept && kh + r * kstep < a.Hkv;
-      ku[r] = in ? *reinterpret_cast<const uint4*>(ksrc + r * kstep * a.ks.h) : make_uint4(0u, 0u, 0u, 0u);
-      vu[r] = in ? *reinterpret_cast<const uint4*>(vsrc + r * kstep * p.vs.h) : make_uint4(0u, 0u, 0u, 0u);
-    }
+    if (queries || n < a.Hkv) load_kv();
 #pragma unroll
     for (int r = 0; r < KV_ROWS; ++r) {
       if (n <= r * kstep) break;                                  // (the same for all)
@@ -371,21 +416,28 @@ __global__ void __launch_bounds__(ROPE_THREADS, BLOCKS) append_rope_kernel(const
       for (int e = 0; e < 8; ++e) y[e] *= rs;
       top *= rs;
       sure = sure && top < 0x1p120f && (top > 0x1p-90f || top == 0.f);
-      uint32_t kc, ksb, vsb;
+      uint32_t vsb;
       const bool in = kept && kh + r * kstep < a.Hkv;
-      sure = (sure_codes<CF>(y, f.exact ? 0.f : top * SURE, kc, ksb) && sure) || !in;
-      if (!__all_sync(0xFFFFFFFFu, sure)) {
-        const uint2 e = exact_codes<D, INTER, CF>(a, ku[r], others, a.pos ? a.pos + (int64_t)ktok * a.axes : nullptr, at.pos, l);
-        kc = e.x;
-        ksb = e.y;
+      // (maxima drop NaN: an element that is not finite leaves its block open)
+      constexpr uint32_t MAG = 0x7FFF7FFFu;
+      const uint32_t most = __vmaxu2(__vimax3_u16x2(w[0] & MAG, w[1] & MAG, w[2] & MAG),
+                                     __vimax3_u16x2(w[3] & MAG, __vmaxu2(v[0] & MAG, v[1] & MAG), __vmaxu2(v[2] & MAG, v[3] & MAG)));
+      const bool finite = max(most & 0xFFFFu, most >> 16) < 0x7F80u;
+      Codes kc = codes_of<CF>(y, !finite ? INFINITY : f.exact ? 0.f : top * SURE);
+      kc.scale_open = in && (kc.scale_open || !sure);
+      kc.open = in ? kc.open : 0u;
+      if (__any_sync(0xFFFFFFFFu, kc.scale_open || kc.open != 0u)) {
+        Codes c = kc;                                             // (in memory only here)
+        close_codes<D, INTER, CF>(a, ku[r], others, a.pos ? a.pos + (int64_t)ktok * a.axes : nullptr, at.pos, l, c);
+        kc = c;
       }
-      const uint32_t kw = k_to_cache<LK>(kc, row0, l);
+      const uint32_t kw = k_to_cache<LK>(kc.codes, row0, l);
       const uint32_t vw = v_to_cache<LK>(quantise8<CF>(vu[r], vsb), row0, l);
       if (in) {
         *reinterpret_cast<uint32_t*>(codes + r * kstep * head + Gr::K) = kw;
         *reinterpret_cast<uint32_t*>(codes + r * kstep * head + Gr::V) = vw;
         if (l % PER == 0) {
-          scales[r * kstep * head] = (uint8_t)ksb;
+          scales[r * kstep * head] = (uint8_t)kc.sb;
           scales[r * kstep * head + Gr::VS - Gr::KS] = (uint8_t)vsb;
         }
       }
