@@ -5,21 +5,23 @@
 //
 // A kv head's query rows (its G heads' rows of each token, in order) go 256 at a time, two tiles
 // of 128, over the key tiles of 128 that some of them see:
-//   - bound by the products, 4 D flops a seen pair: tcgen05 kind::f16 MMAs on bf16.  The block-scaled
-//     kinds cannot take V's scales, which run across its product's summation, nor q unrounded.  A
-//     code times its scale is exact in bf16, so four warps turn a tile's codes into bf16 operands in
-//     shared memory, once for 256 rows (as long as both products of one tile of 128 rows take).
+//   - bound by the products, 4 D flops a seen pair: tcgen05 kind::f16 MMAs.  The block-scaled
+//     kinds cannot take V's scales, which run across its product's summation, nor q unrounded.  So
+//     four warps turn a tile's codes into 16-bit operands in shared memory, once for 256 rows.
 //   - A cache row's bytes are in the order of other fragments (fsa_cache.h); here a word becomes
-//     a 16-byte piece of its row, nibbles i and i + 4 side by side, so the operands' columns are
-//     permuted: those of K alike in q, which is permuted as it is loaded, those of V in the output's
-//     columns, which are put in order as they are stored.  K is K-major; V needs no transposition, as
-//     the second operand of a product over the keys it is MN-major.
-//   - E2M1's exponent and fraction put into bf16's lowest bits are the value times 2^-126, a zero
-//     or a subnormal included; one product with the scale times 2^(126 - 16) gives the operand, 2^-16
-//     of the value (the largest scales need a second one).  The softmax factor and the end make up for it.
+//     a 16-byte piece of its row, so the operands' columns are permuted: those of K alike in q, which is
+//     permuted as it is loaded, those of V in the output's columns, which are put in order as they are
+//     stored.  K is K-major; V needs no transposition, as the second operand of a product over the keys it
+//     is MN-major.
+//   - NVFP4: a code is one conversion to f16, its E4M3 scale one product, both exact; q goes as f16 too, with a
+//     power of two a row (exact down to 2^-18 of its row's maximum, off by at most 2^-29 of it below).
+//   - E8M0 scales have fp32's range.  K is bf16: E2M1's exponent and fraction put into bf16's lowest bits are the
+//     value times 2^-126, a zero or a subnormal included; one product with the scale times 2^(126 - 16)
+//     gives 2^-16 of the value (the largest scales need a second one), and the softmax factor makes up for it.  V is
+//     f16 too, exactly, where all scales of a tile lie in 2^-23 .. 2^13, and otherwise bf16, and P alike.
 //   - S, then P over it, and O stay in tensor memory: 128 columns each for both row tiles.  While
-//     the softmax of one row tile runs, the other's products do.  P is rounded to bf16 (2^-8 of each
-//     weight; the output's own rounding is as large); sums and maxima are fp32.  The running maximum
+//     the softmax of one row tile runs, the other's products do.  P is rounded to f16 (2^-11 of each
+//     weight, 2^-32 absolute; where V is bf16 to that, 2^-8); sums and maxima are fp32.  The running maximum
 //     is raised only when a score beats it by more than 2^8 in the softmax.
 //   - The work, (sequence, row block, kv head, key tile), is one list split evenly over one CTA per
 //     SM (a segment's start weighing as EXTRA tiles); parts of a segment that several CTAs share are
@@ -40,7 +42,7 @@ constexpr int EXTRA = 3;              // what a segment's start costs a CTA, in 
 constexpr int THREADS = 512;          // warps 0..7 softmax (a row a thread), 8..11 operands, 12 copies, 13 MMA
 constexpr int RAW = 3;                // stages of 64 keys of codes
 constexpr float LAZY = 8.0f;          // log2 of how far a score may beat the running maximum
-constexpr float SHIFT_UP = 65536.0f;  // 2^16, the operands being 2^-16 of K and V
+constexpr float UP = 7.0f;            // weights carry 2^7: at most 2^15, in f16
 constexpr float NONE = -INFINITY;
 
 template <int D, int CF>
@@ -52,9 +54,10 @@ struct Cfg {
   static constexpr int STAGE = 4 * Gr::BYTES;            // 64 keys
   static constexpr int OFF_Q = 0, OFF_K = 2 * TILE, OFF_V = 4 * TILE, OFF_RAW = 6 * TILE;
   static constexpr int OFF_BAR = (OFF_RAW + RAW * STAGE + 63) / 64 * 64;
-  static constexpr int OFF_FLAGS = OFF_BAR + 256;        // [4 tiles][4 warps] of {absent keys, keys with a NaN in V}
-  static constexpr int OFF_MISC = OFF_FLAGS + 128;       // absent groups of the raw stages, tmem base, abort flag, warp sums
-  static constexpr int OFF_PRE = OFF_MISC + 128;         // [THREADS] prefix sums of the list
+  static constexpr int OFF_FLAGS = OFF_BAR + 256;        // [4 tiles] of absent keys, keys with a NaN in V, V as bf16: a word a warp
+  static constexpr int OFF_MISC = OFF_FLAGS + 4 * 48;    // absent groups of the raw stages, tmem base, abort flag, warp sums
+  static constexpr int OFF_WALK = OFF_MISC + 128;        // where each warp is in the list
+  static constexpr int OFF_PRE = OFF_WALK + 16 * 80;     // [THREADS] prefix sums of the list
   static constexpr int SMEM = OFF_PRE + THREADS * 4 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static constexpr uint32_t T_S = 0, T_O = 256;          // tensor memory: + 128 (S), + D (O) for the second row tile
@@ -66,7 +69,6 @@ struct Span {
   int qlen, len, kmax;      // rows' tokens, keys, keys that some row of the block sees
   int rows;                 // of the block
   int lead, w0, tiles;      // tiles of the first keys, first tile of some window, tiles in all
-  __device__ __forceinline__ int at(int t) const { return t < lead ? t : t - lead + w0; }
 };
 // virtual sequence vb = b * p.CT + block of rows
 __device__ __forceinline__ Span span_of(const CacheAttnArgs& p, int vb) {
@@ -108,8 +110,11 @@ struct Walk {
   int lo, hi, vb, hkv, unit;
   Span sp;
   int t0, t1, rest;         // the piece: tiles t0 .. t1 - 1 of its segment, and the units behind it
-  __device__ __forceinline__ Walk(const CacheAttnArgs& p, const int* pre, int chunk, int lo_, int hi_) : lo(lo_), hi(hi_) {
-    vb = hkv = unit = 0;
+  __device__ __forceinline__ void start(const CacheAttnArgs& p, const int* pre, int chunk, int lo_, int hi_) {
+    lo = lo_;
+    hi = hi_;
+    vb = hkv = unit = t0 = t1 = rest = 0;
+    sp = Span{};
     if (lo >= hi) return;
     int j = 0;                                           // the last chunk that begins at or before lo
     for (int x = THREADS / 2; x; x >>= 1)
@@ -147,14 +152,33 @@ struct Walk {
     }
     return false;
   }
-  __device__ __forceinline__ bool begins() const { return t0 == 0; }
-  __device__ __forceinline__ bool ends() const { return t1 == sp.tiles; }
 };
+static_assert(sizeof(Walk) <= 80, "");
+// A warp's next piece.  The walk itself waits in shared memory, out of the registers.
+struct Piece {
+  int vb, hkv, t0, t1, lead, w0, rows, kmax, qlen, len, last;     // last: the CTA that has the segment's end
+  bool begins, ends;
+  __device__ __forceinline__ int at(int t) const { return t < lead ? t : t - lead + w0; }
+};
+__device__ __forceinline__ bool next_piece(const CacheAttnArgs& p, Walk* slot, const Shares& sh, Piece& c) {
+  __syncwarp();
+  Walk w = *slot;
+  if (!w.next(p)) return false;
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) *slot = w;
+  c = {w.vb, w.hkv, w.t0, w.t1, w.sp.lead, w.sp.w0, w.sp.rows, w.sp.kmax, w.sp.qlen, w.sp.len, p.whole ? 0 : sh.of(w.lo + w.rest - 1), w.t0 == 0, w.t1 == w.sp.tiles};
+  return true;
+}
 
 // ---------------------------------------------------------------- operands from codes
 __device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 // The eight codes of a word as bf16 of value * 2^-126: nibbles i and i + 4 in word i.
@@ -165,111 +189,167 @@ __device__ __forceinline__ void spread(uint32_t w, uint32_t (&o)[4]) {
   o[2] = ((w << 4) & SIGN) | ((w >> 2) & MAG);
   o[3] = (w & SIGN) | ((w >> 6) & MAG);
 }
-// A block scale as a bf16 factor 2^(126 - 16) * scale, in both halves of a word, and what is
-// missing from it (more: its factor, 1 but for E8M0 scales over 2^17)
-__device__ __forceinline__ uint32_t e8m0_factor(uint32_t byte) {
-  const uint32_t f = byte == 0xFFu ? 0x7FC0u : min(byte + 110u, 254u) << 7;
-  return f * 0x10001u;
+__device__ __forceinline__ uint32_t byte_of(const uint32_t (&w)[2], int i) { return (w[i / 4] >> (8 * (i % 4))) & 0xFFu; }
+// E8M0 scales as factors, twice in a word: of bf16, 2^(126 - 16) * scale (up to 2^17: MOST16); of f16 (2^-23 to 2^13)
+constexpr uint32_t MOST16 = 127 + 17, LEAST_F16 = 127 - 23, MOST_F16 = 127 + 13;
+__device__ __forceinline__ uint32_t e8m0_bf16(uint32_t byte) { return (byte == 0xFFu ? 0x7FC0u : min(byte + 110u, 254u) << 7) * 0x10001u; }
+__device__ __forceinline__ uint32_t e8m0_f16(uint32_t byte) {
+  return (byte > 112u ? (byte - 112u) << 10 : 1u << (byte - 103u)) * 0x10001u;
 }
-__device__ __forceinline__ uint32_t e8m0_more(uint32_t byte) { return (byte > 144u && byte != 0xFFu ? (byte - 144u + 127u) << 7 : 0x3F80u) * 0x10001u; }
-// (up to 2^118: exact, as the scale's four bits are)
-__device__ __forceinline__ uint32_t e4m3_factor(uint32_t byte) {
-  const float f = e4m3_to_f32(byte) * 0x1p110f;
-  return (__float_as_uint(f) >> 16) * 0x10001u;
+__device__ __forceinline__ uint32_t e4m3_f16(uint32_t byte) {
+  uint32_t r;
+  asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}" : "=r"(r) : "r"(byte * 0x101u));
+  return r;
 }
-__device__ __forceinline__ uint32_t low_high(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7610); }   // a's low half, b's high
 
-// One row (key) of K or of V: its codes at `src`, scale bytes `sb`, into row `row` of the operand.
-template <int D, int CF, bool VALUES>
-__device__ __forceinline__ void put_operand(uint8_t* dst, int row, const uint8_t* src, const uint32_t (&sb)[2], bool gone) {
-  constexpr int PIECES = D / 32;                         // of 16 bytes (four words) of codes
-  constexpr int SB = CacheGroup<D, CF>::SB;
-  uint32_t f[SB], more[SB];
-  bool big = false;
+// 16-byte piece of an operand's row: in atoms of 64 columns, swizzled
+__device__ __forceinline__ void put_piece(uint8_t* row_at, int row, int piece, const uint32_t (&o)[4]) {
+  *reinterpret_cast<uint4*>(row_at + (piece >> 3) * (KEYS * 128) + (((piece & 7) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// How a row's words become a row of an operand: f(word, its place among the four of 16 bytes, o).
+// Neighbouring lanes take the 16-byte pieces in turn, so that neither the loads nor the stores of a
+// quarter of the warp share banks (D 64: the loads do, two and two).
+template <int D, class F>
+__device__ __forceinline__ void put_row(uint8_t* dst, int row, const uint8_t* src, F f) {
+  uint8_t* const at = dst + row * 128;
+  uint4 u[D / 32];
 #pragma unroll
-  for (int i = 0; i < SB; ++i) {
-    const uint32_t byte = (sb[i / 4] >> (8 * (i % 4))) & 0xFFu;
-    if constexpr (CF == CF_MX) {
-      f[i] = e8m0_factor(byte);
-      more[i] = e8m0_more(byte);
-      big |= byte > 144u && byte != 0xFFu;
-      if (VALUES && byte == 0xFFu) f[i] = 0u;
-    } else {
-      f[i] = e4m3_factor(byte);
-      if (VALUES && (byte & 0x7Fu) == 0x7Fu) f[i] = 0u;
-    }
-    if (gone) f[i] = 0u;
-  }
-  // two factors a word (pairs 0, 1 and pairs 2, 3 of its four), by the word's place among the four
-  uint32_t fa[4], fb[4], ma[4];
+  for (int c = 0; c < D / 32; ++c) u[c] = *reinterpret_cast<const uint4*>(src + 16 * (D == 128 ? (c + (row >> 1)) & 3 : c));
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    if constexpr (!VALUES) {                             // word 4t + w (D 64: 2t + w): elements 32w + 4t + 0..3, + 16 .. 19
-      const int w = x % (D / 32);
-      fa[x] = fb[x] = CF == CF_MX ? f[w] : low_high(f[2 * w % SB], f[(2 * w + 1) % SB]);
-      ma[x] = CF == CF_MX ? more[w] : 0u;
-    } else {                                             // word 2g + y (D 64: g): elements 64y + 2g + 0, 1, + 16, 17, + 32, 33, + 48, 49
-      const int y = D == 128 ? x % 2 : 0;
-      if constexpr (CF == CF_MX) {
-        fa[x] = fb[x] = low_high(f[2 * y], f[2 * y + 1]);
-        ma[x] = low_high(more[2 * y], more[2 * y + 1]);
-      } else {
-        fa[x] = low_high(f[(4 * y) % SB], f[(4 * y + 2) % SB]);
-        fb[x] = low_high(f[(4 * y + 1) % SB], f[(4 * y + 3) % SB]);
-        ma[x] = 0u;
-      }
-    }
-  }
-  uint8_t* const out = dst + row * 128;
-#pragma unroll
-  for (int c = 0; c < PIECES; ++c) {
-    // neighbouring lanes take the pieces in turn, so that neither the loads nor the stores of a
-    // quarter of the warp share banks (D 64: the loads do, two and two)
+  for (int c = 0; c < D / 32; ++c) {
     const int cc = D == 128 ? (c + (row >> 1)) & 3 : c;
-    const uint4 u = *reinterpret_cast<const uint4*>(src + 16 * cc);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const uint32_t w[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       uint32_t o[4];
-      spread(w[x], o);
-      o[0] = bmul2(o[0], fa[x]);
-      o[1] = bmul2(o[1], fa[x]);
-      o[2] = bmul2(o[2], fb[x]);
-      o[3] = bmul2(o[3], fb[x]);
-      if (CF == CF_MX && big) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = bmul2(o[e], ma[x]);
-      }
-      const int piece = 4 * cc + x;                      // of the row's D/8
-      *reinterpret_cast<uint4*>(out + (piece >> 3) * (KEYS * 128) + (((piece & 7) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+      f(w[x], x, o);
+      put_piece(at, row, 4 * cc + x, o);
     }
   }
 }
+// A row of K.  Word 4t + w (D 64: 2t + w) holds elements 32w + 4t + 0..3 and 16 on, whose scales are those of
+// block w (E8M0) or 2w and 2w + 1 (E4M3).  gone: its codes are not there.
+template <int D, int CF>
+__device__ __forceinline__ void put_key(uint8_t* dst, int row, const uint8_t* src, const uint32_t (&sb)[2], bool gone) {
+  if constexpr (CF == CF_MX) {
+    uint32_t f[D / 32];
+    bool big = false;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint32_t byte = byte_of(sb, i);
+      f[i] = gone ? 0u : e8m0_bf16(byte);
+      big |= byte > MOST16 && byte != 0xFFu && !gone;
+    }
+    auto word = [&](uint32_t w, int x, uint32_t (&o)[4]) {
+      spread(w, o);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = bmul2(o[e], f[x % (D / 32)]);
+    };
+    put_row<D>(dst, row, src, word);
+    if (__any_sync(0xFFFFFFFFu, big)) {                          // again, by what the factors were cut by too
+      put_row<D>(dst, row, src, [&](uint32_t w, int x, uint32_t (&o)[4]) {
+        const uint32_t byte = byte_of(sb, x % (D / 32)), more = byte > MOST16 && byte != 0xFFu ? (byte - MOST16 + 127u) << 7 : 0x3F80u;
+        word(w, x, o);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = bmul2(o[e], more * 0x10001u);
+      });
+    }
+  } else {
+    uint32_t f[D / 16];
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) f[i] = gone ? 0u : e4m3_f16(byte_of(sb, i));
+    put_row<D>(dst, row, src, [&](uint32_t w, int x, uint32_t (&o)[4]) {
+      cvt_e2m1x8_f16(w, o);
+      const int b = x % (D / 32);
+      o[0] = hmul2(o[0], f[2 * b]);
+      o[1] = hmul2(o[1], f[2 * b]);
+      o[2] = hmul2(o[2], f[2 * b + 1]);
+      o[3] = hmul2(o[3], f[2 * b + 1]);
+    });
+  }
+}
+// A row of V.  Word 2g + y (D 64: g) holds elements 64y + 2g, + 1, and 16, 32 and 48 on.  A scale that is NaN
+// counts as zero.  wide: as bf16.
+template <int D, int CF>
+__device__ __forceinline__ void put_value(uint8_t* dst, int row, const uint8_t* src, const uint32_t (&sb)[2], bool gone, bool wide) {
+  constexpr int SB = CacheGroup<D, CF>::SB;
+  if (CF == CF_MX && wide) {
+    float f[SB];
+#pragma unroll
+    for (int i = 0; i < SB; ++i) {
+      const uint32_t byte = byte_of(sb, i);
+      f[i] = gone || byte == 0xFFu ? 0.f : __uint_as_float(byte ? byte << 23 : 1u << 22);
+    }
+    put_row<D>(dst, row, src, [&](uint32_t w, int x, uint32_t (&o)[4]) {
+      cvt_e2m1x8_f16(w, o);
+      const int y = D == 128 ? x % 2 : 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float lo, hi;
+        asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}" : "=f"(lo), "=f"(hi) : "r"(o[e]));
+        o[e] = cvt_bf16x2(lo * f[2 * y + e / 2], hi * f[2 * y + e / 2]);
+      }
+    });
+    return;
+  }
+  uint32_t f[SB];
+#pragma unroll
+  for (int i = 0; i < SB; ++i) {
+    const uint32_t byte = byte_of(sb, i);
+    const bool none = gone || (CF == CF_MX ? byte == 0xFFu : (byte & 0x7Fu) == 0x7Fu);
+    f[i] = none ? 0u : CF == CF_MX ? e8m0_f16(byte) : e4m3_f16(byte);
+  }
+  put_row<D>(dst, row, src, [&](uint32_t w, int x, uint32_t (&o)[4]) {
+    cvt_e2m1x8_f16(w, o);
+    const int y = D == 128 ? x % 2 : 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = hmul2(o[e], CF == CF_MX ? f[2 * y + e / 2] : f[4 * y + e]);
+  });
+}
 
-// Row `row` of a tile of q, in the order of K's columns.
-template <int D>
-__device__ __forceinline__ void put_query(uint8_t* dst, int row, const uint16_t* src, uint32_t flip, uint32_t keep) {
-  uint8_t* const out = dst + row * 128;
+// Row `row` of a tile of q (zeros without src), in the order of K's columns; returns what its scores are to be multiplied by.
+template <int D, int CF>
+__device__ __forceinline__ float put_query(uint8_t* dst, int row, const uint16_t* src, float sign, float scale_log2) {
+  uint8_t* const at = dst + row * 128;
+  uint4 u[D / 8];
+#pragma unroll
+  for (int k = 0; k < D / 8; ++k) u[k] = src ? *reinterpret_cast<const uint4*>(src + 8 * k) : make_uint4(0u, 0u, 0u, 0u);
+  float f = 1.f, c = scale_log2;
+  if constexpr (CF == CF_NV) {                                   // (as fsa_cache_attn.cu has q)
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < D / 8; ++k)
+      m = __vmaxu2(m, __vmaxu2(__vimax3_u16x2(u[k].x & 0x7FFF7FFFu, u[k].y & 0x7FFF7FFFu, u[k].z & 0x7FFF7FFFu), u[k].w & 0x7FFF7FFFu));
+    m = max(m & 0xFFFFu, m >> 16);
+    const int e = (int)(m >> 7) - 127;                           // floor(log2) of the row's maximum
+    const int up = e == 128 || m == 0 ? 0 : min(max(4 - e, -126), 126);
+    f = e == 128 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(up + 127) << 23) * sign;
+    c = fmaxf(scale_log2 * __uint_as_float((uint32_t)(127 - up) << 23), 1.4e-45f);      // (0 times -inf is NaN)
+  }
+  const uint32_t flip = sign < 0.f ? 0x80008000u : 0u, keep = sign == 0.f ? 0u : 0xFFFFFFFFu;
+  auto turn = [&](uint32_t w) {
+    if constexpr (CF == CF_NV) return cvt_f16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
+    else return (w ^ flip) & keep;
+  };
 #pragma unroll
   for (int w = 0; w < D / 32; ++w)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {                        // elements 32w + 8h + 0..7 and 16 on: words of t = 2h, 2h + 1
-      uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-      if (src) {
-        a = *reinterpret_cast<const uint4*>(src + 32 * w + 8 * h);
-        b = *reinterpret_cast<const uint4*>(src + 32 * w + 8 * h + 16);
-      }
-      const uint32_t ax[4] = {a.x, a.y, a.z, a.w}, bx[4] = {b.x, b.y, b.z, b.w};
+    for (int h = 0; h < 2; ++h) {                                // elements 32w + 8h + 0..7 and 16 on: words of t = 2h, 2h + 1
+      const uint4 a = u[4 * w + h], b = u[4 * w + h + 2];
+      const uint32_t ax[4] = {turn(a.x), turn(a.y), turn(a.z), turn(a.w)}, bx[4] = {turn(b.x), turn(b.y), turn(b.z), turn(b.w)};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         uint32_t o[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          o[e] = (__byte_perm(ax[2 * k + e / 2], bx[2 * k + e / 2], e & 1 ? 0x7632 : 0x5410) ^ flip) & keep;
-        const int piece = (D / 32) * (2 * h + k) + w;
-        *reinterpret_cast<uint4*>(out + (piece >> 3) * (KEYS * 128) + (((piece & 7) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int e = 0; e < 4; ++e) {
+          if (CF == CF_NV) o[e] = e < 2 ? ax[2 * k + e] : bx[2 * k + e - 2];
+          else o[e] = __byte_perm(ax[2 * k + e / 2], bx[2 * k + e / 2], e & 1 ? 0x7632 : 0x5410);
+        }
+        put_piece(at, row, (D / 32) * (2 * h + k) + w, o);
       }
     }
+  return c;
 }
 
 // ------------------------------------------------------------------------ small things
@@ -289,10 +369,24 @@ __device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+// Instruction descriptors of f16 operands, and the bit of a second operand that is MN-major
+__device__ __forceinline__ constexpr uint32_t idesc_f16(int N) { return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24); }
+constexpr uint32_t MN_MAJOR_B = 1u << 16;
 // bits i of a word with base + i < n
 __device__ __forceinline__ uint32_t below(int n, int base) {
   const int k = n - base;
   return k <= 0 ? 0u : k >= 32 ? 0xFFFFFFFFu : (1u << k) - 1u;
+}
+
+// Scores of 32 keys: -inf where the row does not see the key; their maximum.
+__device__ __forceinline__ float mask32(uint32_t (&r)[32], uint32_t seen) {
+  float m = NONE;
+#pragma unroll
+  for (int e = 0; e < 32; ++e) {
+    if (!(seen >> e & 1)) r[e] = 0xFF800000u;
+    m = fmaxf(m, __uint_as_float(r[e]));
+  }
+  return m;
 }
 
 struct Out {                // where a row goes
@@ -328,7 +422,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
   uint64_t* const o_full = k_full + 12;        // [2] and its output
   uint64_t* const q_full = k_full + 14;        // [2] q is there (4 warps; only where the row tile has rows)
   uint64_t* const drain = k_full + 16;
-  uint2* const flags = reinterpret_cast<uint2*>(sm + C::OFF_FLAGS);
+  uint32_t* const flags = reinterpret_cast<uint32_t*>(sm + C::OFF_FLAGS);      // [4 tiles][3][4]
   uint32_t* const absent = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);      // [RAW]
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC + 16);
   int* const abort_flag = reinterpret_cast<int*>(sm + C::OFF_MISC + 20);
@@ -379,11 +473,16 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
   const int NW = min((int)gridDim.x, p.whole ? total : max(1, total / (EXTRA + 1)));
   const Shares sh(total, NW);
   const bool works = (int)blockIdx.x < NW && total > 0;
-  Walk w(p, pre, chunk, works ? sh.first(blockIdx.x) : 0, works ? sh.first(blockIdx.x + 1) : 0);
+  Walk* const walk = reinterpret_cast<Walk*>(sm + C::OFF_WALK) + warp;
+  {
+    Walk w;
+    w.start(p, pre, chunk, works ? sh.first(blockIdx.x) : 0, works ? sh.first(blockIdx.x + 1) : 0);
+    if (lane == 0) *walk = w;
+  }
 
   if (warp < 8) {
     // ============================================================ softmax, a row a thread
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     const int rt = warp >> 2, rl = threadIdx.x & 127;
     const uint32_t tl = tbase + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t tS = tl + C::T_S + 128 * rt, tO = tl + C::T_O + D * rt;
@@ -394,58 +493,69 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
       if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
       return __all_sync(0xFFFFFFFFu, mbar_wait<false>(bar, parity, ac));
     };
-    while (ok && w.next(p)) {
-      const Span& sp = w.sp;
-      const int b = w.vb / p.CT, row = (w.vb - b * p.CT) * ROWS + 128 * rt + rl;
-      const bool active = sp.rows > 128 * rt, valid = 128 * rt + rl < sp.rows;
-      const int i = row / p.G, h = w.hkv * p.G + row - i * p.G;
-      const int T = w.t1 - w.t0;
-      if (active && T > 0) {
-        put_query<D>(sm + C::OFF_Q + rt * C::TILE, rl, valid ? p.q + b * p.qs.b + i * p.qs.s + h * p.qs.h : nullptr,
-                     p.q_sign < 0.f ? 0x80008000u : 0u, p.q_sign == 0.f ? 0u : 0xFFFFFFFFu);
-        fence_proxy_async_smem();
-        __syncwarp();
-        mbar_arrive_elect(q_full + rt);
+    Piece pc;
+    while (ok && next_piece(p, walk, sh, pc)) {
+      const int b = pc.vb / p.CT, row = (pc.vb - b * p.CT) * ROWS + 128 * rt + rl;
+      const bool active = pc.rows > 128 * rt, valid = 128 * rt + rl < pc.rows;
+      const int T = pc.t1 - pc.t0;
+      if (pc.begins && !pc.ends) start = make_int4(pc.vb * p.c.Hkv + pc.hkv, pc.last, pc.qlen, pc.len);
+      if (!active) { slot += T; continue; }
+      float cq = 1.f;
+      int lim = 0;
+      {
+        const int i = row / p.G, h = pc.hkv * p.G + row - i * p.G;
+        if (T > 0) {
+          cq = put_query<D, CF>(sm + C::OFF_Q + rt * C::TILE, rl, valid ? p.q + b * p.qs.b + i * p.qs.s + h * p.qs.h : nullptr, p.q_sign, p.scale_log2);
+          fence_proxy_async_smem();
+          __syncwarp();
+          mbar_arrive_elect(q_full + rt);
+        }
+        if (valid) lim = p.causal ? max(0, pc.len - pc.qlen + i + 1) : pc.len;
       }
-      if (w.begins() && !w.ends()) start = make_int4(w.vb * p.c.Hkv + w.hkv, sh.of(w.lo + w.rest - 1), sp.qlen, sp.len);
-      const int lim = !valid ? 0 : p.causal ? max(0, sp.len - sp.qlen + i + 1) : sp.len;
       const int wlo = p.window ? lim - p.window : 0;
       float M = NONE;
       uint64_t l2 = pk2(0.f, 0.f), l3 = l2;
-      if (!active) { slot += T; continue; }
       for (int j = 0; j < T; ++j, ++n, ++slot) {
-        const int k0 = sp.at(w.t0 + j) * KEYS;
+        const int k0 = pc.at(pc.t0 + j) * KEYS;
         ok = wait(s_full + rt, n & 1);
         if (!ok) break;
         tc_fence_after();
-        uint32_t raw[128];
+        // the maximum of all, then block after block of 32 (64 scores at a time in registers; the last two are read twice)
+        uint32_t ra[32], rb[32];
         float bm[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32_max(tS + 32 * c, raw + 32 * c, bm[c]);
-        const uint4 fl0 = *reinterpret_cast<const uint4*>(flags + 4 * (slot & 3)), fl1 = *reinterpret_cast<const uint4*>(flags + 4 * (slot & 3) + 2);
-        const uint32_t gone[4] = {fl0.x, fl0.z, fl1.x, fl1.z}, nans[4] = {fl0.y, fl0.w, fl1.y, fl1.w};
-        const bool told = (fl0.x | fl0.y | fl0.z | fl0.w | fl1.x | fl1.y | fl1.z | fl1.w) != 0;
-        tc_wait_ld();
+        tmem_ld32_max(tS + 64, ra, bm[2]);
+        tmem_ld32_max(tS + 96, rb, bm[3]);
+        const uint32_t* const fl = flags + 12 * (slot & 3);
+        uint32_t told;
+        bool wide = false;
+        {
+          const uint4 a = reinterpret_cast<const uint4*>(fl)[0], c = reinterpret_cast<const uint4*>(fl)[1];
+          told = a.x | a.y | a.z | a.w | c.x | c.y | c.z | c.w;
+          if constexpr (CF == CF_MX) {
+            const uint4 t = reinterpret_cast<const uint4*>(fl)[2];
+            wide = (t.x | t.y | t.z | t.w) != 0;
+          }
+        }
         // the keys that the row does not see (all rows of a warp go along)
-        if (__any_sync(0xFFFFFFFFu, told || k0 + KEYS > lim || (k0 < wlo && k0 + KEYS > p.sinks))) {
+        const bool masked = __any_sync(0xFFFFFFFFu, told != 0 || k0 + KEYS > lim || (k0 < wlo && k0 + KEYS > p.sinks));
+        uint32_t seen[4] = {};
+        if (masked) {
           uint32_t bad = 0;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const int base = k0 + 32 * c;
-            uint32_t seen = below(lim, base) & ~gone[c];
-            if (p.window) seen &= ~below(wlo, base) | below(p.sinks, base);
-            bad |= seen & nans[c];
-            float m = NONE;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              if (!(seen >> e & 1)) raw[32 * c + e] = 0xFF800000u;
-              m = fmaxf(m, __uint_as_float(raw[32 * c + e]));
-            }
-            bm[c] = m;
+            seen[c] = below(lim, k0 + 32 * c) & ~fl[c];
+            if (p.window) seen[c] &= ~below(wlo, k0 + 32 * c) | below(p.sinks, k0 + 32 * c);
+            bad |= seen[c] & fl[4 + c];
           }
           if (bad) l2 = pk2(__uint_as_float(0x7FC00000u), 0.f);
         }
-        const float x = fmaxf(fmaxf(bm[0], bm[1]), fmaxf(bm[2], bm[3])) * p.scale_log2;
+        tc_wait_ld();
+        if (masked) { bm[2] = mask32(ra, seen[2]); bm[3] = mask32(rb, seen[3]); }
+        tmem_ld32_max(tS, ra, bm[0]);
+        tmem_ld32_max(tS + 32, rb, bm[1]);
+        tc_wait_ld();
+        if (masked) { bm[0] = mask32(ra, seen[0]); bm[1] = mask32(rb, seen[1]); }
+        const float x = fmaxf(fmaxf(bm[0], bm[1]), fmaxf(bm[2], bm[3])) * cq;
         float alpha = 1.f;
         if (M == NONE) {
           M = x;
@@ -458,32 +568,47 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
         // (the scores of this tile are there, so the products of the tile before are done)
         if (j > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
 #pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
-            uint32_t o[16];
-            TmemLd<16>::run(tO + c, o);
+          for (int c = 0; c < D; c += 8) {
+            uint32_t o[8];
+            TmemLd<8>::run(tO + c, o);
             tc_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            TmemSt<16>::run(tO + c, o);
+            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            TmemSt<8>::run(tO + c, o);
           }
         }
-        const float nM = M == NONE ? 0.f : -M;           // no key yet: every score is -inf, every weight 0
-        const uint64_t c2 = pk2(p.scale_log2, p.scale_log2), nM2 = pk2(nM, nM);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pw[16];
+        const float nM = M == NONE ? 0.f : UP - M;       // no key yet: every score is -inf, every weight 0
+        const uint64_t c2 = pk2(cq, cq), nM2 = pk2(nM, nM);
+        auto weigh = [&](uint32_t (&r)[32], int c) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             float a, bb;
-            upk2(ffma2(pk2(__uint_as_float(raw[32 * c + 2 * e]), __uint_as_float(raw[32 * c + 2 * e + 1])), c2, nM2), a, bb);
+            upk2(ffma2(pk2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), c2, nM2), a, bb);
             a = ex2_approx(a);
             bb = ex2_approx(bb);
             if (e & 1) l3 = fadd2(l3, pk2(a, bb));
             else l2 = fadd2(l2, pk2(a, bb));
-            pw[e] = cvt_bf16x2(a, bb);
+            r[2 * e] = __float_as_uint(a);
+            r[2 * e + 1] = __float_as_uint(bb);
           }
-          TmemSt<16>::run(tS + 16 * c, pw);
-        }
+          uint32_t pw[16];
+          if (CF == CF_MX && wide) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pw[e] = cvt_bf16x2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pw[e] = cvt_f16x2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+          }
+          TmemSt<16>::run(tS + 16 * c, pw);              // over scores that have been read
+        };
+        weigh(ra, 0);
+        tmem_ld_cols<32>(tS + 64, ra);
+        weigh(rb, 1);
+        tmem_ld_cols<32>(tS + 96, rb);
+        tc_wait_ld();
+        if (masked) { mask32(ra, seen[2]); mask32(rb, seen[3]); }
+        weigh(ra, 2);
+        weigh(rb, 3);
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -500,11 +625,11 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
       upk2(l2, la, lb);
       upk2(l3, lc, ld);
       const float l = (la + lb) + (lc + ld);
-      const bool whole = w.begins() && w.ends(), none = l == 0.f;
-      const float inv = whole ? (none ? 0.f : SHIFT_UP / l) : SHIFT_UP;
-      const Out out = out_of(p, b, w.hkv, row);
-      float* const part = p.partials + (int64_t)(2 * blockIdx.x + (w.begins() ? 1 : 0)) * C::PART;
-#pragma unroll
+      const bool whole = pc.begins && pc.ends, none = l == 0.f;
+      const float inv = !whole ? 1.f : none ? 0.f : 1.f / l;
+      const Out out = out_of(p, b, pc.hkv, row);
+      float* const part = p.partials + (int64_t)(2 * blockIdx.x + (pc.begins ? 1 : 0)) * C::PART;
+#pragma unroll 1
       for (int y = 0; y < D / 64; ++y) {
         uint32_t o[8][8];
         if (T > 0) {
@@ -513,16 +638,15 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
           tc_wait_ld();
         }
         if (!valid) continue;
-        // dim 64y + 2g + {0, 32, 1, 33, 16, 48, 17, 49} of each eight
-        constexpr int FROM[4][2] = {{0, 2}, {4, 6}, {1, 3}, {5, 7}};
+        // dims 64y + 16s + 2g, + 1 at 2s, 2s + 1 of each eight
 #pragma unroll
         for (int s = 0; s < 4; ++s)
 #pragma unroll
           for (int g = 0; g < 8; g += 2) {
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             if (T > 0 && !(whole && none))
-              v = make_float4(__uint_as_float(o[g][FROM[s][0]]) * inv, __uint_as_float(o[g][FROM[s][1]]) * inv,
-                              __uint_as_float(o[g + 1][FROM[s][0]]) * inv, __uint_as_float(o[g + 1][FROM[s][1]]) * inv);
+              v = make_float4(__uint_as_float(o[g][2 * s]) * inv, __uint_as_float(o[g][2 * s + 1]) * inv,
+                              __uint_as_float(o[g + 1][2 * s]) * inv, __uint_as_float(o[g + 1][2 * s + 1]) * inv);
             const int d = 64 * y + 16 * s + 2 * g;
             if (whole) put4(p, out.at + d, v);
             else *reinterpret_cast<float4*>(part + (128 * rt + rl) * D + d) = v;
@@ -533,7 +657,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
           part[ROWS * D + 128 * rt + rl] = M;
           part[ROWS * (D + 1) + 128 * rt + rl] = l;
         } else if (p.lse) {
-          p.lse[out.lse_at] = none ? NONE : (M + log2f(l)) * 0.69314718055994530942f;
+          p.lse[out.lse_at] = none ? NONE : (M - UP + log2f(l)) * 0.69314718055994530942f;
         }
       }
       tc_fence_before();
@@ -541,19 +665,19 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
     if (threadIdx.x == 0 && !p.whole) p.starts[blockIdx.x] = ok ? start : make_int4(-1, 0, 0, 0);
   } else if (warp < 12) {
     // ============================================================ operands from codes, a key a thread
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     const int dw = warp - 8, row = 32 * dw + lane;
     uint32_t n = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, ac)); };
-    while (ok && w.next(p)) {
-      for (int t = w.t0; t < w.t1; ++t, ++n) {
-        const int k0 = w.sp.at(t) * KEYS;
+    Piece pc;
+    while (ok && next_piece(p, walk, sh, pc)) {
+      for (int t = pc.t0; t < pc.t1; ++t, ++n) {
         const uint32_t half = 2 * n + (dw >> 1), rs = half % RAW, kb = n & 1;
         ok = wait(raw_full + rs, (half / RAW) & 1) && (n < 2 || wait(k_empty + kb, (n / 2 - 1) & 1));
         if (!ok) break;
         const int grp = 2 * (dw & 1) + (lane >> 4);      // of the stage's four
-        const bool gone = (absent[rs] >> grp & 1) || k0 + row >= w.sp.kmax;
+        const bool gone = (absent[rs] >> grp & 1) || pc.at(t) * KEYS + row >= pc.kmax;
         const uint8_t* const base = sm + C::OFF_RAW + rs * C::STAGE + grp * Gr::BYTES;
         uint32_t ks[2] = {0u, 0u}, vs[2] = {0u, 0u};
         const uint8_t *kp = base + Gr::KS + (lane & 15) * Gr::SB, *vp = base + Gr::VS + (lane & 15) * Gr::SB;
@@ -567,21 +691,34 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
           ks[0] = *reinterpret_cast<const uint16_t*>(kp);
           vs[0] = *reinterpret_cast<const uint16_t*>(vp);
         }
-        bool nan = false;
+        bool nan = false, far = false;
 #pragma unroll
         for (int i = 0; i < Gr::SB; ++i) {
-          const uint32_t byte = (vs[i / 4] >> (8 * (i % 4))) & 0xFFu;
+          const uint32_t byte = byte_of(vs, i);
           nan |= CF == CF_MX ? byte == 0xFFu : (byte & 0x7Fu) == 0x7Fu;
+          far |= CF == CF_MX && byte != 0xFFu && (byte < LEAST_F16 || byte > MOST_F16);
         }
         const uint32_t gones = __ballot_sync(0xFFFFFFFFu, gone), nans = __ballot_sync(0xFFFFFFFFu, nan && !gone);
-        if (lane == 0) flags[4 * (n & 3) + dw] = make_uint2(gones, nans);
-        put_operand<D, CF, false>(sm + C::OFF_K + kb * C::TILE, row, base + Gr::K + (lane & 15) * (D / 2), ks, gone);
+        const uint32_t fars = CF == CF_MX ? __ballot_sync(0xFFFFFFFFu, far && !gone) : 0u;
+        uint32_t* const fl = flags + 12 * (n & 3) + dw;
+        if (lane == 0) {
+          fl[0] = gones;
+          fl[4] = nans;
+          if (CF == CF_MX) fl[8] = fars;
+        }
+        put_key<D, CF>(sm + C::OFF_K + kb * C::TILE, row, base + Gr::K + (lane & 15) * (D / 2), ks, gone);
         fence_proxy_async_smem();
         __syncwarp();
         mbar_arrive_elect(k_full + kb);
         ok = n < 2 || wait(v_empty + kb, (n / 2 - 1) & 1);
         if (!ok) break;
-        put_operand<D, CF, true>(sm + C::OFF_V + kb * C::TILE, row, base + Gr::V + (lane & 15) * (D / 2), vs, gone);
+        bool wide = false;
+        if constexpr (CF == CF_MX) {                     // the four warps agree on V's type
+          named_bar_sync(1, 128);
+          const uint4 a = *reinterpret_cast<const uint4*>(flags + 12 * (n & 3) + 8);
+          wide = (a.x | a.y | a.z | a.w) != 0;
+        }
+        put_value<D, CF>(sm + C::OFF_V + kb * C::TILE, row, base + Gr::V + (lane & 15) * (D / 2), vs, gone, wide);
         fence_proxy_async_smem();
         __syncwarp();
         mbar_arrive_elect(v_full + kb);
@@ -589,20 +726,21 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 12) {
       // ========================================================== copies: 16 groups of 16 keys at a time
       uint32_t n = 0;                          // stages
       bool ok = true;
-      while (ok && w.next(p)) {
+      Piece w;
+      while (ok && next_piece(p, walk, sh, w)) {
         const int b = w.vb / p.CT;
         const uint8_t* const head = p.c.pages + ((int64_t)w.hkv << (p.c.page_shift - 4)) * Gr::BYTES;
         const int32_t* const table = p.table + (int64_t)b * p.max_pages;
         // the page of lane's group of tiles t .. t + 3 (-1: none)
         auto look_up = [&](int t) {
-          const int v = t + (lane >> 3), pos = w.sp.at(v) * KEYS + 16 * (lane & 7);
+          const int v = t + (lane >> 3), pos = w.at(v) * KEYS + 16 * (lane & 7);
           int page = -1;
-          if (v < w.t1 && pos < w.sp.kmax) {
+          if (v < w.t1 && pos < w.kmax) {
             page = table[pos >> p.c.page_shift];
             if ((uint32_t)page >= (uint32_t)p.c.num_pages) {
               page = -1;
@@ -627,7 +765,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
             }
             __syncwarp();
             if ((lane >> 2) == x && page >= 0) {
-              const int pos = w.sp.at(t + (lane >> 3)) * KEYS + 16 * (lane & 7);
+              const int pos = w.at(t + (lane >> 3)) * KEYS + 16 * (lane & 7);
               const int inside = (pos & ((1 << p.c.page_shift) - 1)) / 16;
               bulk_load(sm + C::OFF_RAW + rs * C::STAGE + (lane & 3) * Gr::BYTES, head + page * p.c.page_bytes + inside * Gr::BYTES,
                         Gr::BYTES, raw_full + rs);
@@ -649,18 +787,19 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
         for (int i = 0; i < D / 16; ++i) {
           const uint32_t off = (i / 4) * C::ATOM + (i % 4) * 32;
           mma_f16_ss_p(elect_u32(), tbase + C::T_S + 128 * rt, smem_desc(sQ + rt * C::TILE + off, 16, 1024, 2),
-                       smem_desc(sK + kb * C::TILE + off, 16, 1024, 2), idesc_f16_bf16(128), i > 0);
+                       smem_desc(sK + kb * C::TILE + off, 16, 1024, 2), CF == CF_MX ? idesc_f16_bf16(128) : idesc_f16(128), i > 0);
         }
         tc_commit_p(elect_u32(), s_full + rt);
       };
-      auto products = [&](int rt, uint32_t vb, bool more) {
+      auto products = [&](int rt, uint32_t vb, bool more, uint32_t idesc) {
 #pragma unroll
         for (int i = 0; i < KEYS / 16; ++i)              // V is MN-major: 64 dims an atom, 8 keys 1024 bytes
           mma_f16_ts_p(elect_u32(), tbase + C::T_O + D * rt, tbase + C::T_S + 128 * rt + 8 * i,
-                       smem_desc(sV + vb * C::TILE + 2048 * i, C::ATOM, 1024, 2), idesc_f16_bf16(D) | 1u << 16, more || i > 0);
+                       smem_desc(sV + vb * C::TILE + 2048 * i, C::ATOM, 1024, 2), idesc, more || i > 0);
       };
-      while (ok && w.next(p)) {
-        const int T = w.t1 - w.t0, tiles = w.sp.rows > 128 ? 2 : 1;
+      Piece w;
+      while (ok && next_piece(p, walk, sh, w)) {
+        const int T = w.t1 - w.t0, tiles = w.rows > 128 ? 2 : 1;
         if (T == 0) continue;
         ok = wait(k_full + (n & 1), (n / 2) & 1);
         for (int rt = 0; ok && rt < tiles; ++rt) {
@@ -674,12 +813,17 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
         tc_commit_p(elect_u32(), k_empty + (n & 1));
         for (int j = 0; ok && j < T; ++j, ++n) {
           ok = wait(v_full + (n & 1), (n / 2) & 1);
+          uint32_t type = idesc_f16(D) | MN_MAJOR_B;
+          if constexpr (CF == CF_MX) {
+            const uint4 a = *reinterpret_cast<const uint4*>(flags + 12 * (n & 3) + 8);
+            if ((a.x | a.y | a.z | a.w) != 0) type = idesc_f16_bf16(D) | MN_MAJOR_B;
+          }
           for (int rt = 0; ok && rt < tiles; ++rt) {
             ok = wait(p_full + rt, np[rt] & 1);
             if (!ok) break;
             ++np[rt];
             tc_fence_after();
-            products(rt, n & 1, j > 0);
+            products(rt, n & 1, j > 0, type);
             if (j + 1 < T) {
               if (rt == 0) ok = wait(k_full + ((n + 1) & 1), ((n + 1) / 2) & 1);
               if (!ok) break;
@@ -765,7 +909,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_chunk_join_kernel(const Ca
       if (p.out_bf16) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + out.at + 2 * lane) = cvt_bf16x2(x, y);
       else *reinterpret_cast<float2*>(static_cast<float*>(p.out) + out.at + 2 * lane) = make_float2(x, y);
     }
-    if (lane == 0 && p.lse) p.lse[out.lse_at] = none ? NONE : (m + log2f(l)) * 0.69314718055994530942f;
+    if (lane == 0 && p.lse) p.lse[out.lse_at] = none ? NONE : (m - UP + log2f(l)) * 0.69314718055994530942f;
   }
 }
 

@@ -4,10 +4,12 @@ The tolerance, with eps/2 of a type as a rounding's largest relative error:
   - a score is a sum of D exact products in fp32, each addition off by at most 2^-23 (it may cut), so by
     (D + 8) 2^-23 of scale * sum |q||k|, and moves a weight by as much relatively, in the numerator
     and in the denominator: twice that of sum p|v| / sum p;
-  - a probability is rounded to bf16, 2^-8 of it: 2^-8 of sum p|v| / sum p;
+  - a probability is rounded to f16, 2^-11 of it (where V goes as bf16, E8M0 scales outside 2^-23 .. 2^13, to bf16, 2^-8):
+    that of sum p|v| / sum p.  The largest carries at least 2^7, and below 2^-14 a step is 2^-24: half of that over 2^7,
+    2^-32 of the largest |v|, a key; times 2 for sums that are reached by rescaling;
   - its exponential and the sums, 16 keys an addition, a rescaling a tile: (n / 16 + n / 128) 2^-23 + 2^-18 of the same;
-  - a weight below fp32's normal range is flushed: 2^-126 against a running maximum that the largest score beats by at most 2^8, so
-    where the sum is at least 2^-8 .. 2^8 of the largest weight, n 2^-118 of the largest |v|; operands below 2^-110 lose 2^-118;
+  - q goes as f16 beside NVFP4 keys, exact to 2^-18 of its row's maximum and off by at most 2^-29 of that below: 2^-29 max|q| sum|k|
+    in a score, times scale;
   - an output in bf16 is rounded by 2^-8 of it.
 The log of the sums: the scores' error, and 2^-18."""
 import math
@@ -21,13 +23,22 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 
-def check(out, lse, q, seqs, q_lens, causal, scale, window, sinks, dtype):
+def far_scales(v):
+    """Whether a block of 32 may have an E8M0 scale (its maximum's power of two, less two) outside 2^-23 .. 2^13."""
+    top = v.unflatten(-1, (-1, 32)).abs().amax(-1)
+    return bool(((top < 2.0 ** -20) | (top >= 2.0 ** 14)).any())
+
+
+def check(out, lse, q, seqs, q_lens, causal, scale, window, sinks, dtype, fmt):
     for b, (k, v, live) in enumerate(seqs):
         m, n, D = q_lens[b], k.shape[0], q.shape[-1]
         want, want_lse, spread, reach = win.attention(q[b, :m], k, v, live, causal, scale, window, sinks)
         score = (D + 8) * 2.0 ** -23 * reach
-        tol = spread * (2 * score + 2.0 ** -8 + (n / 16 + n / 128) * 2.0 ** -23 + 2.0 ** -18)[..., None]
-        tol = tol + n * 2.0 ** -118 * (1 + (float(v.abs().max()) if n else 0))
+        if fmt == "NVFP4" and n:
+            score = score + 2.0 ** -29 * abs(scale) * q[b, :m].double().abs().amax(-1) * float(k.abs().sum(-1).max())
+        step = 2.0 ** -8 if fmt == "E2M1" and far_scales(v) else 2.0 ** -11
+        tol = spread * (2 * score + step + (n / 16 + n / 128) * 2.0 ** -23 + 2.0 ** -18)[..., None]
+        tol = tol + n * 2.0 ** -31 * (float(v.abs().max()) if n else 0)
         if dtype == "bf16":
             tol = tol + 2.0 ** -8 * (want.abs() + tol)
         got = out[b, :m].double()
@@ -40,7 +51,7 @@ def check(out, lse, q, seqs, q_lens, causal, scale, window, sinks, dtype):
             assert bool((off[~none] <= (score + 2.0 ** -18 * (1 + want_lse.abs()))[~none]).all())
 
 
-def run(fsa, q, cache, table, lens, q_lens=None, causal=True, scale=None, window=None, sinks=0, dtype="f32", fmt=None, **kw):
+def run(fsa, q, cache, table, lens, q_lens=None, causal=True, scale=None, window=None, sinks=0, dtype="f32", **kw):
     """One call, its rows checked, the others left as they were."""
     B, Sq, H, D = q.shape
     real = [Sq] * B if q_lens is None else q_lens
@@ -51,8 +62,9 @@ def run(fsa, q, cache, table, lens, q_lens=None, causal=True, scale=None, window
     assert got is out
     for b, m in enumerate(real):
         assert bool((out[b, m:] == 7.0).all()) and bool((lse[b, m:] == 7.0).all())
-    seqs = win.sequences(cache, table, lens, cache.Hkv, D, {v: k for k, v in fsa.FMT_BY_NAME.items()}[cache.fmt])
-    check(out, lse, q, seqs, real, causal, D ** -0.5 if scale is None else scale, window or 0, sinks, dtype)
+    fmt = {v: k for k, v in fsa.FMT_BY_NAME.items()}[cache.fmt]
+    seqs = win.sequences(cache, table, lens, cache.Hkv, D, fmt)
+    check(out, lse, q, seqs, real, causal, D ** -0.5 if scale is None else scale, window or 0, sinks, dtype, fmt)
     return out, lse
 
 
