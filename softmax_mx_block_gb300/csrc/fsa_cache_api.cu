@@ -353,7 +353,7 @@ int fsa_attention_chunk(const fsa_cache_attn* c, int window, int sinks, void* st
   if (!take_workspace(c, need, starts_at, &a)) return FSA_ERR_INVALID_ARG;
   a.CT = fsa::cache_chunk_blocks(c->Sq * a.G);
   a.whole = fsa::cache_chunk_whole(a.c, c->max_pages);
-  if (a.c.cf == fsa::CF_MX) a.scale_log2 *= 65536.0f;       // there the kernel's K is 2^-16 of what the cache stands for
+  if (a.c.cf == fsa::CF_MX) a.scale_log2 *= 0x1p40f;       // there the kernel's K is 2^-40 of what the cache stands for
   return launch_status(fsa::launch_cache_chunk(a, sms, static_cast<cudaStream_t>(stream)));
 }
 

@@ -16,8 +16,8 @@
 //   - NVFP4: a code is one conversion to f16, its E4M3 scale one product, both exact; q goes as f16 too, with a
 //     power of two a row (exact down to 2^-18 of its row's maximum, off by at most 2^-29 of it below).
 //   - E8M0 scales have fp32's range.  K is bf16: E2M1's exponent and fraction put into bf16's lowest bits are the
-//     value times 2^-126, a zero or a subnormal included; one product with the scale times 2^(126 - 16)
-//     gives 2^-16 of the value (the largest scales need a second one), and the softmax factor makes up for it.  V is
+//     value times 2^-126, a zero or a subnormal included; one product with the scale times 2^(126 - 40)
+//     gives 2^-40 of the value, and the softmax factor makes up for it (keys of 2^44 and more are infinite).  V is
 //     f16 too, exactly, where all scales of a tile lie in 2^-23 .. 2^13, and otherwise bf16, and P alike.
 //   - S, then P over it, and O stay in tensor memory: 128 columns each for both row tiles.  While
 //     the softmax of one row tile runs, the other's products do.  P is rounded to f16 (2^-11 of each
@@ -190,9 +190,10 @@ __device__ __forceinline__ void spread(uint32_t w, uint32_t (&o)[4]) {
   o[3] = (w & SIGN) | ((w >> 6) & MAG);
 }
 __device__ __forceinline__ uint32_t byte_of(const uint32_t (&w)[2], int i) { return (w[i / 4] >> (8 * (i % 4))) & 0xFFu; }
-// E8M0 scales as factors, twice in a word: of bf16, 2^(126 - 16) * scale (up to 2^17: MOST16); of f16 (2^-23 to 2^13)
-constexpr uint32_t MOST16 = 127 + 17, LEAST_F16 = 127 - 23, MOST_F16 = 127 + 13;
-__device__ __forceinline__ uint32_t e8m0_bf16(uint32_t byte) { return (byte == 0xFFu ? 0x7FC0u : min(byte + 110u, 254u) << 7) * 0x10001u; }
+// E8M0 scales as factors, twice in a word: of bf16, 2^(126 - 40) * scale (from 2^42 on infinite: 0 times that is NaN);
+// of f16 (2^-23 to 2^13)
+constexpr uint32_t LEAST_F16 = 127 - 23, MOST_F16 = 127 + 13;
+__device__ __forceinline__ uint32_t e8m0_bf16(uint32_t byte) { return (min(byte + 86u, 255u) << 7) * 0x10001u; }
 __device__ __forceinline__ uint32_t e8m0_f16(uint32_t byte) {
   return (byte > 112u ? (byte - 112u) << 10 : 1u << (byte - 103u)) * 0x10001u;
 }
@@ -234,27 +235,13 @@ template <int D, int CF>
 __device__ __forceinline__ void put_key(uint8_t* dst, int row, const uint8_t* src, const uint32_t (&sb)[2], bool gone) {
   if constexpr (CF == CF_MX) {
     uint32_t f[D / 32];
-    bool big = false;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const uint32_t byte = byte_of(sb, i);
-      f[i] = gone ? 0u : e8m0_bf16(byte);
-      big |= byte > MOST16 && byte != 0xFFu && !gone;
-    }
-    auto word = [&](uint32_t w, int x, uint32_t (&o)[4]) {
+    for (int i = 0; i < D / 32; ++i) f[i] = gone ? 0u : e8m0_bf16(byte_of(sb, i));
+    put_row<D>(dst, row, src, [&](uint32_t w, int x, uint32_t (&o)[4]) {
       spread(w, o);
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[e] = bmul2(o[e], f[x % (D / 32)]);
-    };
-    put_row<D>(dst, row, src, word);
-    if (__any_sync(0xFFFFFFFFu, big)) {                          // again, by what the factors were cut by too
-      put_row<D>(dst, row, src, [&](uint32_t w, int x, uint32_t (&o)[4]) {
-        const uint32_t byte = byte_of(sb, x % (D / 32)), more = byte > MOST16 && byte != 0xFFu ? (byte - MOST16 + 127u) << 7 : 0x3F80u;
-        word(w, x, o);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = bmul2(o[e], more * 0x10001u);
-      });
-    }
+    });
   } else {
     uint32_t f[D / 16];
 #pragma unroll
@@ -269,30 +256,18 @@ __device__ __forceinline__ void put_key(uint8_t* dst, int row, const uint8_t* sr
     });
   }
 }
+// A word times a scale in fp32, as bf16 (the rare ways: small, and out of the way of the others' registers)
+__device__ __forceinline__ uint32_t scaled_bf16(uint32_t f16x2, float f) {
+  float lo, hi;
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}" : "=f"(lo), "=f"(hi) : "r"(f16x2));
+  return cvt_bf16x2(lo * f, hi * f);
+}
+__device__ __forceinline__ float e8m0_f32(uint32_t byte) { return __uint_as_float(byte ? byte << 23 : 1u << 22); }
 // A row of V.  Word 2g + y (D 64: g) holds elements 64y + 2g, + 1, and 16, 32 and 48 on.  A scale that is NaN
-// counts as zero.  wide: as bf16.
+// counts as zero.
 template <int D, int CF>
-__device__ __forceinline__ void put_value(uint8_t* dst, int row, const uint8_t* src, const uint32_t (&sb)[2], bool gone, bool wide) {
+__device__ __forceinline__ void put_value(uint8_t* dst, int row, const uint8_t* src, const uint32_t (&sb)[2], bool gone) {
   constexpr int SB = CacheGroup<D, CF>::SB;
-  if (CF == CF_MX && wide) {
-    float f[SB];
-#pragma unroll
-    for (int i = 0; i < SB; ++i) {
-      const uint32_t byte = byte_of(sb, i);
-      f[i] = gone || byte == 0xFFu ? 0.f : __uint_as_float(byte ? byte << 23 : 1u << 22);
-    }
-    put_row<D>(dst, row, src, [&](uint32_t w, int x, uint32_t (&o)[4]) {
-      cvt_e2m1x8_f16(w, o);
-      const int y = D == 128 ? x % 2 : 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float lo, hi;
-        asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}" : "=f"(lo), "=f"(hi) : "r"(o[e]));
-        o[e] = cvt_bf16x2(lo * f[2 * y + e / 2], hi * f[2 * y + e / 2]);
-      }
-    });
-    return;
-  }
   uint32_t f[SB];
 #pragma unroll
   for (int i = 0; i < SB; ++i) {
@@ -306,6 +281,22 @@ __device__ __forceinline__ void put_value(uint8_t* dst, int row, const uint8_t* 
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] = hmul2(o[e], CF == CF_MX ? f[2 * y + e / 2] : f[4 * y + e]);
   });
+}
+// The same as bf16, with any E8M0 scale.
+template <int D>
+__device__ __forceinline__ void put_value_far(uint8_t* dst, int row, const uint8_t* src, uint32_t sb, bool gone) {
+#pragma unroll 1
+  for (int i = 0; i < D / 8; ++i) {
+    const int y = D == 128 ? i % 2 : 0;
+    uint32_t o[4];
+    cvt_e2m1x8_f16(*reinterpret_cast<const uint32_t*>(src + 4 * i), o);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t byte = sb >> (8 * (2 * y + e / 2)) & 0xFFu;
+      o[e] = scaled_bf16(o[e], gone || byte == 0xFFu ? 0.f : e8m0_f32(byte));
+    }
+    put_piece(dst + row * 128, row, i, o);
+  }
 }
 
 // Row `row` of a tile of q (zeros without src), in the order of K's columns; returns what its scores are to be multiplied by.
@@ -579,7 +570,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
         }
         const float nM = M == NONE ? 0.f : UP - M;       // no key yet: every score is -inf, every weight 0
         const uint64_t c2 = pk2(cq, cq), nM2 = pk2(nM, nM);
-        auto weigh = [&](uint32_t (&r)[32], int c) {
+        auto weigh = [&](uint32_t (&r)[32], int c, auto pack) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             float a, bb;
@@ -592,23 +583,29 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
             r[2 * e + 1] = __float_as_uint(bb);
           }
           uint32_t pw[16];
-          if (CF == CF_MX && wide) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) pw[e] = cvt_bf16x2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) pw[e] = cvt_f16x2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
-          }
+          for (int e = 0; e < 16; ++e) pw[e] = pack(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
           TmemSt<16>::run(tS + 16 * c, pw);              // over scores that have been read
         };
-        weigh(ra, 0);
-        tmem_ld_cols<32>(tS + 64, ra);
-        weigh(rb, 1);
-        tmem_ld_cols<32>(tS + 96, rb);
-        tc_wait_ld();
-        if (masked) { mask32(ra, seen[2]); mask32(rb, seen[3]); }
-        weigh(ra, 2);
-        weigh(rb, 3);
+        auto f16 = [](float a, float bb) { return cvt_f16x2(a, bb); };
+        if (CF == CF_MX && wide) {                       // (rare: block after block, read again)
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld_cols<32>(tS + 32 * c, ra);
+            tc_wait_ld();
+            if (masked) mask32(ra, c == 0 ? seen[0] : c == 1 ? seen[1] : c == 2 ? seen[2] : seen[3]);
+            weigh(ra, c, [](float a, float bb) { return cvt_bf16x2(a, bb); });
+          }
+        } else {
+          weigh(ra, 0, f16);
+          tmem_ld_cols<32>(tS + 64, ra);
+          weigh(rb, 1, f16);
+          tmem_ld_cols<32>(tS + 96, rb);
+          tc_wait_ld();
+          if (masked) { mask32(ra, seen[2]); mask32(rb, seen[3]); }
+          weigh(ra, 2, f16);
+          weigh(rb, 3, f16);
+        }
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -718,7 +715,10 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
           const uint4 a = *reinterpret_cast<const uint4*>(flags + 12 * (n & 3) + 8);
           wide = (a.x | a.y | a.z | a.w) != 0;
         }
-        put_value<D, CF>(sm + C::OFF_V + kb * C::TILE, row, base + Gr::V + (lane & 15) * (D / 2), vs, gone, wide);
+        uint8_t* const dst = sm + C::OFF_V + kb * C::TILE;
+        const uint8_t* const src = base + Gr::V + (lane & 15) * (D / 2);
+        if (CF == CF_MX && wide) put_value_far<D>(dst, row, src, vs[0], gone);
+        else put_value<D, CF>(dst, row, src, vs, gone);
         fence_proxy_async_smem();
         __syncwarp();
         mbar_arrive_elect(v_full + kb);
