@@ -779,23 +779,32 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
     } else if (warp == 13) {
       // ========================================================== products
       auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xFFFFFFFFu, mbar_wait<false>(bar, parity, ac)); };
-      const uint32_t sQ = smem_u32(sm + C::OFF_Q), sK = smem_u32(sm + C::OFF_K), sV = smem_u32(sm + C::OFF_V);
+      // the operands' descriptors; what is added to one is its offset over 16
+      const uint64_t dQ = smem_desc(smem_u32(sm + C::OFF_Q), 16, 1024, 2), dK = smem_desc(smem_u32(sm + C::OFF_K), 16, 1024, 2);
+      const uint64_t dV = smem_desc(smem_u32(sm + C::OFF_V), C::ATOM, 1024, 2);      // MN-major: 64 dims an atom, 8 keys 1024 bytes
       uint32_t n = 0, nq[2] = {0, 0}, np[2] = {0, 0};
       bool ok = true;
+      // (one lane issues them all: with an election for each, and its address worked out there, the issue took longer
+      // than the products)
       auto scores = [&](int rt, uint32_t kb) {
+        if (elect_one()) {
+          const uint64_t q = dQ + rt * (C::TILE / 16), k = dK + kb * (C::TILE / 16);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint32_t off = (i / 4) * C::ATOM + (i % 4) * 32;
-          mma_f16_ss_p(elect_u32(), tbase + C::T_S + 128 * rt, smem_desc(sQ + rt * C::TILE + off, 16, 1024, 2),
-                       smem_desc(sK + kb * C::TILE + off, 16, 1024, 2), CF == CF_MX ? idesc_f16_bf16(128) : idesc_f16(128), i > 0);
+          for (int i = 0; i < D / 16; ++i)
+            mma_f16_ss(tbase + C::T_S + 128 * rt, q + ((i / 4) * C::ATOM + (i % 4) * 32) / 16, k + ((i / 4) * C::ATOM + (i % 4) * 32) / 16,
+                       CF == CF_MX ? idesc_f16_bf16(128) : idesc_f16(128), i > 0);
+          tc_commit(s_full + rt);
         }
-        tc_commit_p(elect_u32(), s_full + rt);
+        __syncwarp();
       };
       auto products = [&](int rt, uint32_t vb, bool more, uint32_t idesc) {
+        if (elect_one()) {
+          const uint64_t v = dV + vb * (C::TILE / 16);
 #pragma unroll
-        for (int i = 0; i < KEYS / 16; ++i)              // V is MN-major: 64 dims an atom, 8 keys 1024 bytes
-          mma_f16_ts_p(elect_u32(), tbase + C::T_O + D * rt, tbase + C::T_S + 128 * rt + 8 * i,
-                       smem_desc(sV + vb * C::TILE + 2048 * i, C::ATOM, 1024, 2), idesc, more || i > 0);
+          for (int i = 0; i < KEYS / 16; ++i)
+            mma_f16_ts(tbase + C::T_O + D * rt, tbase + C::T_S + 128 * rt + 8 * i, v + i * (2048 / 16), idesc, more || i > 0);
+        }
+        __syncwarp();
       };
       Piece w;
       while (ok && next_piece(p, walk, sh, w)) {
