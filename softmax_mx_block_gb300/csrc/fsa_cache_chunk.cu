@@ -60,7 +60,10 @@ struct Cfg {
   static constexpr int OFF_PRE = OFF_WALK + 16 * 80;     // [THREADS] prefix sums of the list
   static constexpr int SMEM = OFF_PRE + THREADS * 4 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
-  static constexpr uint32_t T_S = 0, T_O = 256;          // tensor memory: + 128 (S), + D (O) for the second row tile
+  // tensor memory: + 128 (S), + D (O), + P_STEP (P) for the second row tile.  With D 64 P has columns of its own, and the next
+  // tile's scores are computed while this one's softmax runs; with D 128 it lies over the scores.
+  static constexpr bool APART = D == 64;
+  static constexpr uint32_t T_S = 0, T_O = 256, T_P = APART ? 384 : 0, P_STEP = APART ? 64 : 128;
   static constexpr int PART = ROWS * (D + 2);            // floats of a partial result: rows, maxima, sums
 };
 
@@ -412,7 +415,9 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
   uint64_t* const p_full = k_full + 10;        // [2] and its probabilities (4 warps)
   uint64_t* const o_full = k_full + 12;        // [2] and its output
   uint64_t* const q_full = k_full + 14;        // [2] q is there (4 warps; only where the row tile has rows)
-  uint64_t* const drain = k_full + 16;
+  uint64_t* const s_free = k_full + 16;        // [2] APART: the scores have been read (4 warps)
+  uint64_t* const o_done = k_full + 18;        // [2] APART: a tile's products with V are done
+  uint64_t* const drain = k_full + 20;
   uint32_t* const flags = reinterpret_cast<uint32_t*>(sm + C::OFF_FLAGS);      // [4 tiles][3][4]
   uint32_t* const absent = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);      // [RAW]
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC + 16);
@@ -429,6 +434,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
       mbar_init(v_full + i, 4); mbar_init(v_empty + i, 1);
       mbar_init(s_full + i, 1); mbar_init(p_full + i, 4);
       mbar_init(o_full + i, 1); mbar_init(q_full + i, 4);
+      mbar_init(s_free + i, 4); mbar_init(o_done + i, 1);
     }
     mbar_init(drain, 1);
     sts_vol(abort_flag, 0);
@@ -476,7 +482,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
     asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     const int rt = warp >> 2, rl = threadIdx.x & 127;
     const uint32_t tl = tbase + ((uint32_t)(32 * (warp & 3)) << 16);
-    const uint32_t tS = tl + C::T_S + 128 * rt, tO = tl + C::T_O + D * rt;
+    const uint32_t tS = tl + C::T_S + 128 * rt, tP = tl + C::T_P + C::P_STEP * rt, tO = tl + C::T_O + D * rt;
     uint32_t n = 0, pieces = 0, slot = 0;      // tiles and pieces of this row tile, tiles of the CTA
     int4 start = make_int4(-1, 0, 0, 0);
     bool ok = true;
@@ -556,8 +562,14 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
           l2 = ffma2(l2, pk2(alpha, alpha), pk2(0.f, 0.f));
           l3 = ffma2(l3, pk2(alpha, alpha), pk2(0.f, 0.f));
         }
-        // (the scores of this tile are there, so the products of the tile before are done)
+        // (the scores of this tile are there, so the products of the tile before, or APART of the one before that, are
+        // done; those of this tile wait for this warp, so the barrier's parity tells)
         if (j > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
+          if constexpr (C::APART) {
+            ok = wait(o_done + rt, (n - 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+          }
 #pragma unroll 1
           for (int c = 0; c < D; c += 8) {
             uint32_t o[8];
@@ -585,9 +597,17 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
           uint32_t pw[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) pw[e] = pack(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
-          TmemSt<16>::run(tS + 16 * c, pw);              // over scores that have been read
+          TmemSt<16>::run(tP + 16 * c, pw);              // (over scores that have been read, or apart)
         };
         auto f16 = [](float a, float bb) { return cvt_f16x2(a, bb); };
+        if constexpr (C::APART) {
+          // P of the tile before has been multiplied before its columns are written again
+          if (j > 0) {
+            ok = wait(o_done + rt, (n - 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+          }
+        }
         if (CF == CF_MX && wide) {                       // (rare: block after block, read again)
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
@@ -597,14 +617,27 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
             weigh(ra, c, [](float a, float bb) { return cvt_bf16x2(a, bb); });
           }
         } else {
+          auto f16 = [](float a, float bb) { return cvt_f16x2(a, bb); };
           weigh(ra, 0, f16);
           tmem_ld_cols<32>(tS + 64, ra);
           weigh(rb, 1, f16);
           tmem_ld_cols<32>(tS + 96, rb);
           tc_wait_ld();
+          if constexpr (C::APART) {
+            tc_fence_before();
+            __syncwarp();
+            mbar_arrive_elect(s_free + rt);
+          }
           if (masked) { mask32(ra, seen[2]); mask32(rb, seen[3]); }
           weigh(ra, 2, f16);
           weigh(rb, 3, f16);
+        }
+        if constexpr (C::APART && CF == CF_MX) {
+          if (wide) {
+            tc_fence_before();
+            __syncwarp();
+            mbar_arrive_elect(s_free + rt);
+          }
         }
         tc_wait_st();
         tc_fence_before();
@@ -802,7 +835,8 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
           const uint64_t v = dV + vb * (C::TILE / 16);
 #pragma unroll
           for (int i = 0; i < KEYS / 16; ++i)
-            mma_f16_ts(tbase + C::T_O + D * rt, tbase + C::T_S + 128 * rt + 8 * i, v + i * (2048 / 16), idesc, more || i > 0);
+            mma_f16_ts(tbase + C::T_O + D * rt, tbase + C::T_P + C::P_STEP * rt + 8 * i, v + i * (2048 / 16), idesc, more || i > 0);
+          if (C::APART) tc_commit(o_done + rt);
         }
         __syncwarp();
       };
@@ -827,24 +861,34 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
             const uint4 a = *reinterpret_cast<const uint4*>(flags + 12 * (n & 3) + 8);
             if ((a.x | a.y | a.z | a.w) != 0) type = idesc_f16_bf16(D) | MN_MAJOR_B;
           }
+          if (C::APART && j + 1 < T) {         // the next scores first
+            ok = ok && wait(k_full + ((n + 1) & 1), ((n + 1) / 2) & 1);
+            for (int rt = 0; ok && rt < tiles; ++rt) {
+              ok = wait(s_free + rt, np[rt] & 1);
+              if (!ok) break;
+              tc_fence_after();
+              scores(rt, (n + 1) & 1);
+            }
+            if (ok) tc_commit_p(elect_u32(), k_empty + ((n + 1) & 1));
+          }
           for (int rt = 0; ok && rt < tiles; ++rt) {
             ok = wait(p_full + rt, np[rt] & 1);
             if (!ok) break;
             ++np[rt];
             tc_fence_after();
             products(rt, n & 1, j > 0, type);
-            if (j + 1 < T) {
+            if (j + 1 == T) {
+              tc_commit_p(elect_u32(), o_full + rt);
+            } else if (!C::APART) {
               if (rt == 0) ok = wait(k_full + ((n + 1) & 1), ((n + 1) / 2) & 1);
               if (!ok) break;
               tc_fence_after();
               scores(rt, (n + 1) & 1);
-            } else {
-              tc_commit_p(elect_u32(), o_full + rt);
             }
           }
           if (!ok) break;
           tc_commit_p(elect_u32(), v_empty + (n & 1));
-          if (j + 1 < T) tc_commit_p(elect_u32(), k_empty + ((n + 1) & 1));
+          if (!C::APART && j + 1 < T) tc_commit_p(elect_u32(), k_empty + ((n + 1) & 1));
         }
       }
       tc_commit_p(elect_u32(), drain);         // all products end before tensor memory is freed
