@@ -6,13 +6,14 @@
 // its codes and scales are those of the exact values
 //   y = x / sqrt(mean(x^2) + eps) * w,  (a, b) -> (a cos t - b sin t, a sin t + b cos t),  t = pos * inv_freq
 // (through bf16 they would be rounded twice).  They are computed in fp32, whose error is
-// known: with Y the row's largest |y|, |a| + |b| <= 2 Y for every pair, the angle is off by at most
-// 2^-22.3 (an ulp of a part of a turn, for positions up to 2^24), cos and sin by 2^-23 and the two products by
-// 2^-24 each, together 2^-20.2 Y; the norm's factor by 2^-21.4 of y, a quotient by an E4M3 scale by 2^-22.4: in
-// all 2^-19.4 Y.  So each block is rounded twice, from y - 2^-19 Y and from y + 2^-19 Y; where scale and
-// codes agree, as in all but about one warp in 100, they are the exact ones, and what is left open is
-// computed again to 2^-43.  Elements that neither a norm nor an angle touches are exact as they are, and
-// rounded as fsa_cache_append does.
+// known: with Y the row's largest |y|, |a| + |b| <= 2 Y for every pair; the angle is off by at most 2^-23.3 (a part of
+// a turn by 2^-26, for positions up to 2^24), cos and sin by an ulp, 2^-24, their products with the weights and
+// the two products of a pair by 2^-24 each: 2^-21.1 Y together.  The norm's factor is off by 2^-21.7 of y (seven additions
+// on the way to a sum of exact squares, half of that, and 2^-23.4), a quotient by an E4M3 scale by 2^-22.4, the two
+// below by 2^-24: in all 1.05 2^-20 Y.  So each block is rounded twice, from y - 1.25 2^-20 Y and from y + 1.25 2^-20 Y;
+// where scale and codes agree, as in all but about one warp in 150, they are the exact ones, and what is left open
+// is computed again to 2^-43.  Elements that neither a norm nor an angle touches are
+// exact as they are, and rounded as fsa_cache_append does.
 //
 // Bound by memory: 4 H + 4 Hkv + 2 Hkv (0.53 or 0.56) bytes a token and dim.  A block takes a
 // few tokens with all their heads, as fsa_qk_norm_rope does: the sines of a token are computed
@@ -26,7 +27,7 @@
 namespace fsa {
 namespace {
 
-constexpr float SURE = 0x1p-19f;      // of a row's largest |y|: more than the fp32 arithmetic is off by
+constexpr float SURE = 0x1.4p-20f;      // of a row's largest |y|: more than the fp32 arithmetic is off by
 constexpr int KV_ROWS = 2;            // rows of a thread in flight, of k and of v each
 constexpr int APPEND_MANY = 10, APPEND_FEW = 8;       // blocks of an SM where there are more than run at once, and where all do
 
@@ -478,11 +479,11 @@ __device__ __forceinline__ void put_key(const AppendRopeArgs& p, const Lane8& f,
   const bool all = 2 * a.half == D;
   const uint4 others = a.half > 0 ? others_of<D, INTER>(ku, a.half, row0, l) : ku;
   const uint32_t w[4] = {ku.x, ku.y, ku.z, ku.w}, v[4] = {others.x, others.y, others.z, others.w};
-  f2 y[4], sq;
+  f2 y[4], sq[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const f2 o = unpack(w[i]), z = mul(o, f.own[i]);
-    sq = i ? fma(o, o, sq) : mul(o, o);
+    sq[i] = mul(o, o);                                          // (exact)
     y[i] = fma(unpack(v[i]), f.other[i], z);
     if (!all && !(f.turned >> (i / 2) & 1)) y[i] = z;         // (an element that does not turn takes nothing of another)
   }
@@ -500,12 +501,13 @@ __device__ __forceinline__ void put_key(const AppendRopeArgs& p, const Lane8& f,
   float rs = 1.f;
   bool sure = true;
   if (a.norm) {                                               // (with an element that is not finite: not sure)
-    split(sq, ss, s1);
+    split(add(add(sq[0], sq[1]), add(sq[2], sq[3])), ss, s1);
     ss += s1;
 #pragma unroll
     for (int m = 1; m < LK; m *= 2) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, m);
     const float mean = ss * (1.0f / D) + a.eps;
     rs = rsqrtf(mean);
+    rs = fmaf(rs * 0.5f, fmaf(-mean * rs, rs, 1.f), rs);        // (a step of Newton's: off by 2^-23.4)
     sure = mean > 0x1p-90f && mean < 0x1p120f;                // (squares below fp32's range are nothing beside that)
   }
   sure = sure && most * rs < 0x1p120f && (most * rs > 0x1p-90f || most == 0.f);

@@ -903,9 +903,9 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
 }
 
 // Joins the parts of the segments that several CTAs share.  Block (c, y) takes the one that
-// begins in CTA c and goes on, 32 rows of it: CTA c's second part and the first part of each
-// later CTA up to the last.  A warp a row, a lane D/32 dims.
-constexpr int JOIN_ROWS = 32, JOIN_THREADS = 256;
+// begins in CTA c and goes on, 8 rows of it, a warp a row and a lane D/32 dims: CTA c's second part and the
+// first part of each later CTA up to the last.  The first parts' rows set out together with all maxima and sums.
+constexpr int JOIN_ROWS = 8, JOIN_THREADS = 256, JOIN_AHEAD = 4;
 template <int D>
 __global__ void __launch_bounds__(JOIN_THREADS) cache_chunk_join_kernel(const CacheAttnArgs p) {
   constexpr int PART = ROWS * (D + 2), PER = D / 32;
@@ -914,56 +914,76 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_chunk_join_kernel(const Ca
   const int4 st = p.starts[blockIdx.x];        // segment, last CTA, its rows' tokens, its keys
   if (st.x < 0) return;
   const int lane = threadIdx.x & 31, vb = st.x / p.c.Hkv, hkv = st.x - vb * p.c.Hkv, b = vb / p.CT;
-  const int n = st.y - (int)blockIdx.x + 1;
+  const int n = st.y - (int)blockIdx.x + 1, r = blockIdx.y * JOIN_ROWS + threadIdx.x / 32;
+  if (r >= min(ROWS, st.z * p.G - (vb - b * p.CT) * ROWS)) return;
   const float* const parts = p.partials + (int64_t)2 * blockIdx.x * PART;
   auto part = [&](int k) { return parts + (k == 0 ? (int64_t)PART : (int64_t)2 * k * PART); };
-  const int rows = min(ROWS, st.z * p.G - (vb - b * p.CT) * ROWS);
-  for (int r = blockIdx.y * JOIN_ROWS + threadIdx.x / 32; r < min(rows, ((int)blockIdx.y + 1) * JOIN_ROWS); r += JOIN_THREADS / 32) {
-    float m = NONE;
-    for (int k = lane; k < n; k += 32) m = fmaxf(m, part(k)[ROWS * D + r]);
-#pragma unroll
-    for (int x = 16; x; x /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
-    float l = 0.f, o[PER] = {};
-    for (int k0 = 0; k0 < n; k0 += 32) {
-      float f = 0.f;
-      if (k0 + lane < n) {
-        const float* const pk = part(k0 + lane);
-        const float mk = pk[ROWS * D + r], lk = pk[ROWS * (D + 1) + r];
-        f = lk == 0.f ? 0.f : exp2f(mk - m);
-        l = fmaf(f, lk, l);
-      }
-#pragma unroll 8
-      for (int k = 0; k < min(32, n - k0); ++k) {
-        const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
-        const float* const src = part(k0 + k) + r * D + PER * lane;
-        float v[PER];
-        if constexpr (PER == 4) {
-          const float4 u = *reinterpret_cast<const float4*>(src);
-          v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
-        } else {
-          const float2 u = *reinterpret_cast<const float2*>(src);
-          v[0] = u.x; v[1] = u.y;
-        }
-        if (fk != 0.f) {                       // (a part that saw nothing counts nothing)
-#pragma unroll
-          for (int e = 0; e < PER; ++e) o[e] = fmaf(fk, v[e], o[e]);
-        }
-      }
-    }
-#pragma unroll
-    for (int x = 16; x; x /= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
-    const bool none = l == 0.f;
-    const float inv = none ? 0.f : 1.0f / l;
-    const Out out = out_of(p, b, hkv, (vb - b * p.CT) * ROWS + r);
+  auto row = [&](int k, float (&v)[PER]) {
+    const float* const src = part(k) + r * D + PER * lane;
     if constexpr (PER == 4) {
-      put4(p, out.at + 4 * lane, none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv));
+      const float4 u = *reinterpret_cast<const float4*>(src);
+      v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
     } else {
-      const float x = none ? 0.f : o[0] * inv, y = none ? 0.f : o[1] * inv;
-      if (p.out_bf16) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + out.at + 2 * lane) = cvt_bf16x2(x, y);
-      else *reinterpret_cast<float2*>(static_cast<float*>(p.out) + out.at + 2 * lane) = make_float2(x, y);
+      const float2 u = *reinterpret_cast<const float2*>(src);
+      v[0] = u.x; v[1] = u.y;
     }
-    if (lane == 0 && p.lse) p.lse[out.lse_at] = none ? NONE : (m - UP + log2f(l)) * 0.69314718055994530942f;
+  };
+  float v[JOIN_AHEAD][PER];
+#pragma unroll
+  for (int k = 0; k < JOIN_AHEAD; ++k)
+    if (k < n) row(k, v[k]);
+  float mk = NONE, lk = 0.f, m = NONE;         // of part `lane`
+  if (lane < n) {
+    mk = part(lane)[ROWS * D + r];
+    lk = part(lane)[ROWS * (D + 1) + r];
+    m = mk;
   }
+  for (int k = lane + 32; k < n; k += 32) m = fmaxf(m, part(k)[ROWS * D + r]);
+#pragma unroll
+  for (int x = 16; x; x /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+  float l = 0.f, o[PER] = {};
+  for (int k0 = 0; k0 < n; k0 += 32) {
+    if (k0 > 0) {
+      const bool in = k0 + lane < n;
+      mk = in ? part(k0 + lane)[ROWS * D + r] : NONE;
+      lk = in ? part(k0 + lane)[ROWS * (D + 1) + r] : 0.f;
+    }
+    const float f = lk == 0.f ? 0.f : exp2f(mk - m);     // (a part that saw nothing counts nothing)
+    l = fmaf(f, lk, l);
+    auto add = [&](int k, const float (&u)[PER]) {
+      const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
+      if (fk != 0.f) {
+#pragma unroll
+        for (int e = 0; e < PER; ++e) o[e] = fmaf(fk, u[e], o[e]);
+      }
+    };
+    int k = 0;
+    if (k0 == 0) {
+#pragma unroll
+      for (int x = 0; x < JOIN_AHEAD; ++x)
+        if (x < n) add(x, v[x]);
+      k = JOIN_AHEAD;
+    }
+#pragma unroll 8
+    for (; k < min(32, n - k0); ++k) {
+      float u[PER];
+      row(k0 + k, u);
+      add(k, u);
+    }
+  }
+#pragma unroll
+  for (int x = 16; x; x /= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
+  const bool none = l == 0.f;
+  const float inv = none ? 0.f : 1.0f / l;
+  const Out out = out_of(p, b, hkv, (vb - b * p.CT) * ROWS + r);
+  if constexpr (PER == 4) {
+    put4(p, out.at + 4 * lane, none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv));
+  } else {
+    const float x = none ? 0.f : o[0] * inv, y = none ? 0.f : o[1] * inv;
+    if (p.out_bf16) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + out.at + 2 * lane) = cvt_bf16x2(x, y);
+    else *reinterpret_cast<float2*>(static_cast<float*>(p.out) + out.at + 2 * lane) = make_float2(x, y);
+  }
+  if (lane == 0 && p.lse) p.lse[out.lse_at] = none ? NONE : (m - UP + log2f(l)) * 0.69314718055994530942f;
 }
 
 // Opt in to the kernel's shared memory, once a device.
