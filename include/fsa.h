@@ -466,8 +466,8 @@ int fsa_cache_append(const fsa_cache* cache, const void* k, const void* v, const
 /* The projection's q, k and v of new tokens in one pass: q normalised and rotated into q_out
  * as fsa_qk_norm_rope does (the same bits), k normalised and rotated and v as they are into
  * the cache as fsa_cache_append puts them.  k is rounded once, to 4 bits: its codes and scales
- * are those of the exact values, for positions up to 2^24 (angles pos * inv_freq rounded to
- * 64 bits); beyond, of values within the error of fsa_qk_norm_rope.
+ * are those of the exact values, for positions up to 2^24 and |inv_freq| up to 1 (angles
+ * pos * inv_freq rounded to 64 bits); beyond, of values within the error of fsa_qk_norm_rope.
  *   args: as fsa_qk_norm_rope, without k_out (NULL).  pos may be NULL with one axis: a token
  *     then turns by its place in its sequence, lens[b] - new_lens[b] + i.  q_out may be q, and
  *     must not overlap k or v.
@@ -550,11 +550,16 @@ int fsa_attention_cache_window_workspace(const fsa_cache* cache, int B, int H, i
 int fsa_attention_cache_window(const fsa_cache_attn* args, int window, int sinks, void* stream);
 
 /* What fsa_attention_cache computes, for chunks of new tokens (a prompt's, or the next turn's
- * of a conversation): rows go 256 a kv head at a time over the cache, which is turned into bf16
- * operands once for each 256 (those values are exact).  Scores are sums of bf16 products in
- * fp32, sums and maxima fp32; probabilities are rounded to bf16 for the product with V (2^-8
- * of each); keys below 2^-100 and values below 2^-100 lose bits (an absolute 2^-117).
- * A row that sees a token with a non-finite key or value is NaN as a whole.
+ * of a conversation): rows go 256 a kv head at a time over the cache, whose codes are turned
+ * into 16-bit operands once for each 256.  Scores are sums of exact products in fp32, sums and
+ * maxima fp32; with NVFP4 q goes as f16, exact down to 2^-18 of its row's largest magnitude and
+ * off by at most 2^-29 of that below.  Probabilities are rounded to f16 for the product with V
+ * (2^-11 of each, or an absolute 2^-32 of the largest value for small ones); with E2M1, where V's block scales in a tile of 128 keys
+ * leave 2^-23 .. 2^13, to bf16 (2^-8).
+ * E2M1 keys of 2^44 and more count as not finite, those below 2^-86 lose bits, as do values below
+ * 2^-126; values up to 2^100.  |scale| <= 2^80.
+ * A row that sees a token with a non-finite key or value is NaN as a whole, and so is a row of
+ * q that is not finite; the rows beside it are as without it.
  * window and sinks as above; window 0: none (sinks 0 too), causal or not.
  * args as there, with a workspace of fsa_attention_chunk_workspace bytes.
  * B * Sq * H <= 2^27; B * Hkv * ceil(Sq * H/Hkv / 256) * (ceil(max_pages * page_size / 128) + 4) < 2^31. */

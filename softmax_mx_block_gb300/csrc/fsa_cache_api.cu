@@ -346,6 +346,7 @@ int fsa_attention_chunk(const fsa_cache_attn* c, int window, int sinks, void* st
   fsa::CacheAttnArgs a{};
   const int st = take_attn(c, window, sinks, chunk_shape_ok, &a);
   if (st != FSA_OK) return st;
+  if (!(std::fabs(c->scale) <= 0x1p80f)) return FSA_ERR_INVALID_ARG;   // 2^40 of it below has to stay finite
   int sms = 0;
   if (!sm_count(&sms)) return FSA_ERR_NO_DEVICE;
   size_t starts_at;

@@ -17,7 +17,7 @@
 //     power of two a row (exact down to 2^-18 of its row's maximum, off by at most 2^-29 of it below).
 //   - E8M0 scales have fp32's range.  K is bf16: E2M1's exponent and fraction put into bf16's lowest bits are the
 //     value times 2^-126, a zero or a subnormal included; one product with the scale times 2^(126 - 40)
-//     gives 2^-40 of the value, and the softmax factor makes up for it (keys of 2^44 and more are infinite).  V is
+//     gives 2^-40 of the value, and the softmax factor makes up for it (keys of 2^44 and more count as NaN).  V is
 //     f16 too, exactly, where all scales of a tile lie in 2^-23 .. 2^13, and otherwise bf16, and P alike.
 //   - S, then P over it, and O stay in tensor memory: 128 columns each for both row tiles.  While
 //     the softmax of one row tile runs, the other's products do.  P is rounded to f16 (2^-11 of each
@@ -193,10 +193,10 @@ __device__ __forceinline__ void spread(uint32_t w, uint32_t (&o)[4]) {
   o[3] = (w & SIGN) | ((w >> 6) & MAG);
 }
 __device__ __forceinline__ uint32_t byte_of(const uint32_t (&w)[2], int i) { return (w[i / 4] >> (8 * (i % 4))) & 0xFFu; }
-// E8M0 scales as factors, twice in a word: of bf16, 2^(126 - 40) * scale (from 2^42 on infinite: 0 times that is NaN);
+// E8M0 scales as factors, twice in a word: of bf16, 2^(126 - 40) * scale (NaN from 2^42 on);
 // of f16 (2^-23 to 2^13)
 constexpr uint32_t LEAST_F16 = 127 - 23, MOST_F16 = 127 + 13;
-__device__ __forceinline__ uint32_t e8m0_bf16(uint32_t byte) { return (min(byte + 86u, 255u) << 7) * 0x10001u; }
+__device__ __forceinline__ uint32_t e8m0_bf16(uint32_t byte) { return (byte < 169u ? (byte + 86u) << 7 : 0x7FC0u) * 0x10001u; }
 __device__ __forceinline__ uint32_t e8m0_f16(uint32_t byte) {
   return (byte > 112u ? (byte - 112u) << 10 : 1u << (byte - 103u)) * 0x10001u;
 }
@@ -599,7 +599,6 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
           for (int e = 0; e < 16; ++e) pw[e] = pack(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
           TmemSt<16>::run(tP + 16 * c, pw);              // (over scores that have been read, or apart)
         };
-        auto f16 = [](float a, float bb) { return cvt_f16x2(a, bb); };
         if constexpr (C::APART) {
           // P of the tile before has been multiplied before its columns are written again
           if (j > 0) {

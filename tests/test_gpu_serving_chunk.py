@@ -171,8 +171,34 @@ def test_scales_and_ranges(fmt):
             run(fsa, q, cache, table, [n], scale=scale)
 
 
+def test_ends_of_the_key_and_value_ranges():
+    """E2M1 keys up to the last that is finite (below 2^44), values of 2^100 and of 2^-100 in the same sequence, scales
+    that bring the scores back to one; a key of 2^44 makes the rows NaN that see it."""
+    fsa = _fsa()
+    g = gen(37)
+    n, Hkv, D = 500, 2, 128
+    k, v = normal(g, 1, n, Hkv, D), normal(g, 1, n, Hkv, D)
+    k = torch.sign(k) * torch.linspace(1.0, 6.0, n, device="cuda")[None, :, None, None].to(k.dtype)
+    v[:, 200:300], v[:, 300:] = v[:, 200:300] * 2.0 ** 98, v[:, 300:] * 2.0 ** -100
+    table, pages = make_table(g, [n], 64)
+    cache = fsa.empty_cache(pages, 64, Hkv, D, "E2M1")
+    q = normal(g, 1, 70, 8, D)
+    for power, scale in ((41, 2.0 ** -45), (-60, 2.0 ** 56), (-84, 2.0 ** 80)):
+        fsa.fsa_cache_append(cache, k * 2.0 ** power, v, table, i32([n]))
+        run(fsa, q, cache, table, [n], scale=scale)
+        run(fsa, q, cache, table, [n], scale=-scale, window=100, sinks=3)
+    k = k * 2.0 ** 41
+    k[0, n - 20, 0] = -2.0 ** 45                   # rows 50 .. of head 0's queries
+    fsa.fsa_cache_append(cache, k, v, table, i32([n]))
+    out = fsa.fsa_attention_chunk(q.abs(), cache, table, i32([n]), scale=2.0 ** -45)
+    nan = torch.isnan(out[0]).all(-1)
+    assert torch.equal(nan, torch.isnan(out[0]).any(-1)) and bool(nan[50:, :4].all())
+    assert not bool(nan[:50].any()) and not bool(nan[:, 4:].any())
+
+
 @pytest.mark.parametrize("fmt", ["E2M1", "NVFP4"])
-def test_nan_stays_with_its_rows(fmt):
+@pytest.mark.parametrize("wide", [0, 40])      # columns of the table that no sequence reaches: its segments are shared, and joined
+def test_nan_stays_with_its_rows(fmt, wide):
     """A token with a non-finite key or value makes the rows NaN that see it, and no others; so does a
     row of q; bytes of unused places (here NaN scales) count nothing."""
     fsa = _fsa()
@@ -180,6 +206,7 @@ def test_nan_stays_with_its_rows(fmt):
     n, Hkv, D, Sq = 400, 2, 128, 150
     k, v = normal(g, 1, n, Hkv, D), normal(g, 1, n, Hkv, D)
     table, pages = make_table(g, [n], 16)
+    table = torch.nn.functional.pad(table, (0, wide), value=-1)
     cache = fsa.empty_cache(pages, 16, Hkv, D, fmt)
     cache.pages.fill_(0xFF)
     q = normal(g, 1, Sq, 8, D)
