@@ -302,48 +302,57 @@ __device__ __forceinline__ void put_value_far(uint8_t* dst, int row, const uint8
   }
 }
 
-// Row `row` of a tile of q (zeros without src), in the order of K's columns; returns what its scores are to be multiplied by.
+// A warp's 32 rows of a tile of q, from `row0` on, in the order of K's columns; src: this lane's row (zeros without one).
+// Neighbouring lanes take 16-byte pieces of a row.  Returns what the scores of this lane's row are to be multiplied by.
 template <int D, int CF>
-__device__ __forceinline__ float put_query(uint8_t* dst, int row, const uint16_t* src, float sign, float scale_log2) {
-  uint8_t* const at = dst + row * 128;
-  uint4 u[D / 8];
-#pragma unroll
-  for (int k = 0; k < D / 8; ++k) u[k] = src ? *reinterpret_cast<const uint4*>(src + 8 * k) : make_uint4(0u, 0u, 0u, 0u);
-  float f = 1.f, c = scale_log2;
-  if constexpr (CF == CF_NV) {                                   // (as fsa_cache_attn.cu has q)
-    uint32_t m = 0;
-#pragma unroll
-    for (int k = 0; k < D / 8; ++k)
-      m = __vmaxu2(m, __vmaxu2(__vimax3_u16x2(u[k].x & 0x7FFF7FFFu, u[k].y & 0x7FFF7FFFu, u[k].z & 0x7FFF7FFFu), u[k].w & 0x7FFF7FFFu));
-    m = max(m & 0xFFFFu, m >> 16);
-    const int e = (int)(m >> 7) - 127;                           // floor(log2) of the row's maximum
-    const int up = e == 128 || m == 0 ? 0 : min(max(4 - e, -126), 126);
-    f = e == 128 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(up + 127) << 23) * sign;
-    c = fmaxf(scale_log2 * __uint_as_float((uint32_t)(127 - up) << 23), 1.4e-45f);      // (0 times -inf is NaN)
-  }
+__device__ __forceinline__ float put_queries(uint8_t* dst, int row0, const uint16_t* src, float sign, float scale_log2) {
+  constexpr int L = D / 8, RPI = 32 / L, AHEAD = 8;                // lanes of a row, rows and loads at a time
+  const int lane = threadIdx.x & 31, ch = lane % L, sub = lane / L;
+  const int w = ch / 4, h = ch & 1, side = ch >> 1 & 1;            // elements 32w + 16 side + 8h + 0..7
   const uint32_t flip = sign < 0.f ? 0x80008000u : 0u, keep = sign == 0.f ? 0u : 0xFFFFFFFFu;
-  auto turn = [&](uint32_t w) {
-    if constexpr (CF == CF_NV) return cvt_f16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
-    else return (w ^ flip) & keep;
-  };
+  float cq = scale_log2;
+#pragma unroll 1
+  for (int k0 = 0; k0 < 32 / RPI; k0 += AHEAD) {
+    uint4 u[AHEAD];
 #pragma unroll
-  for (int w = 0; w < D / 32; ++w)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {                                // elements 32w + 8h + 0..7 and 16 on: words of t = 2h, 2h + 1
-      const uint4 a = u[4 * w + h], b = u[4 * w + h + 2];
-      const uint32_t ax[4] = {turn(a.x), turn(a.y), turn(a.z), turn(a.w)}, bx[4] = {turn(b.x), turn(b.y), turn(b.z), turn(b.w)};
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint32_t o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (CF == CF_NV) o[e] = e < 2 ? ax[2 * k + e] : bx[2 * k + e - 2];
-          else o[e] = __byte_perm(ax[2 * k + e / 2], bx[2 * k + e / 2], e & 1 ? 0x7632 : 0x5410);
-        }
-        put_piece(at, row, (D / 32) * (2 * h + k) + w, o);
-      }
+    for (int k = 0; k < AHEAD; ++k) {
+      const uint16_t* const from = reinterpret_cast<const uint16_t*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(src), RPI * (k0 + k) + sub));
+      u[k] = from ? *reinterpret_cast<const uint4*>(from + 8 * ch) : make_uint4(0u, 0u, 0u, 0u);
     }
-  return c;
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      uint32_t t[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+      if constexpr (CF == CF_NV) {                                 // (as fsa_cache_attn.cu has q)
+        uint32_t m = __vmaxu2(__vimax3_u16x2(t[0] & 0x7FFF7FFFu, t[1] & 0x7FFF7FFFu, t[2] & 0x7FFF7FFFu), t[3] & 0x7FFF7FFFu);
+#pragma unroll
+        for (int x = 1; x < L; x *= 2) m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+        m = max(m & 0xFFFFu, m >> 16);
+        const int e = (int)(m >> 7) - 127;                         // floor(log2) of the row's maximum
+        const int up = e == 128 || m == 0 ? 0 : min(max(4 - e, -126), 126);
+        const float f = e == 128 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(up + 127) << 23) * sign;
+        const float c = fmaxf(scale_log2 * __uint_as_float((uint32_t)(127 - up) << 23), 1.4e-45f);      // (0 times -inf is NaN)
+        const float theirs = __shfl_sync(0xFFFFFFFFu, c, lane % RPI * L);
+        if (lane / RPI == k0 + k) cq = theirs;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = cvt_f16x2(__uint_as_float(t[i] << 16) * f, __uint_as_float(t[i] & 0xFFFF0000u) * f);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = (t[i] ^ flip) & keep;
+      }
+      // elements 16 on have the same places: the lane that has them takes the upper halves of both, this one the lower
+      const uint32_t x0 = __shfl_xor_sync(0xFFFFFFFFu, side ? t[0] : t[2], 2), x1 = __shfl_xor_sync(0xFFFFFFFFu, side ? t[1] : t[3], 2);
+      const uint32_t ax[2] = {side ? x0 : t[0], side ? x1 : t[1]}, bx[2] = {side ? t[2] : x0, side ? t[3] : x1};
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (CF == CF_NV) o[i] = i < 2 ? ax[i] : bx[i - 2];
+        else o[i] = __byte_perm(ax[i / 2], bx[i / 2], i & 1 ? 0x7632 : 0x5410);
+      }
+      const int row = row0 + RPI * (k0 + k) + sub;
+      put_piece(dst + row * 128, row, (D / 32) * (2 * h + side) + w, o);
+    }
+  }
+  return cq;
 }
 
 // ------------------------------------------------------------------------ small things
@@ -502,7 +511,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
       {
         const int i = row / p.G, h = pc.hkv * p.G + row - i * p.G;
         if (T > 0) {
-          cq = put_query<D, CF>(sm + C::OFF_Q + rt * C::TILE, rl, valid ? p.q + b * p.qs.b + i * p.qs.s + h * p.qs.h : nullptr, p.q_sign, p.scale_log2);
+          cq = put_queries<D, CF>(sm + C::OFF_Q + rt * C::TILE, 32 * (warp & 3), valid ? p.q + b * p.qs.b + i * p.qs.s + h * p.qs.h : nullptr, p.q_sign, p.scale_log2);
           fence_proxy_async_smem();
           __syncwarp();
           mbar_arrive_elect(q_full + rt);
@@ -658,28 +667,59 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
       const float inv = !whole ? 1.f : none ? 0.f : 1.f / l;
       const Out out = out_of(p, b, pc.hkv, row);
       float* const part = p.partials + (int64_t)(2 * blockIdx.x + (pc.begins ? 1 : 0)) * C::PART;
+      // Rows go out by way of the warp's rows of Q, whose products are done, so that neighbouring lanes store
+      // neighbouring dims.  Loops stay loops: this runs once a piece, and what it costs is the fetching of its instructions.
+      constexpr int AT_ONCE = D / 4;                       // rows of 64 floats that fit there
+      uint8_t* const mine = sm + C::OFF_Q + rt * C::TILE + 32 * (warp & 3) * 128;
+      auto staged = [&](int r, int c) {                  // four floats c of row r
+        const int x = c ^ (r & 7);
+        return reinterpret_cast<float4*>(mine + (x & 7) * 16 + (D == 128 ? (x >> 3) * C::ATOM + r * 128 : (2 * r + (x >> 3)) * 128));
+      };
+      const int rows = min(32, pc.rows - 128 * rt - 32 * (warp & 3));            // of the warp
+      const bool zeros = T == 0 || (whole && none);
 #pragma unroll 1
       for (int y = 0; y < D / 64; ++y) {
-        uint32_t o[8][8];
-        if (T > 0) {
+#pragma unroll 1
+        for (int r0 = 0; r0 < rows; r0 += AT_ONCE) {
+#pragma unroll 1
+          for (int g = 0; g < 8; g += 2) {               // dims 64y + 16s + 2g, + 1 at 2s, 2s + 1 of each eight
+            uint32_t o[2][8];
+            TmemLd<8>::run(tO + 8 * (g * (D / 64) + y), o[0]);
+            TmemLd<8>::run(tO + 8 * ((g + 1) * (D / 64) + y), o[1]);
+            tc_wait_ld();
+            if (D == 128 || (lane & AT_ONCE) == r0) {
 #pragma unroll
-          for (int g = 0; g < 8; ++g) TmemLd<8>::run(tO + 8 * (g * (D / 64) + y), o[g]);
-          tc_wait_ld();
-        }
-        if (!valid) continue;
-        // dims 64y + 16s + 2g, + 1 at 2s, 2s + 1 of each eight
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-#pragma unroll
-          for (int g = 0; g < 8; g += 2) {
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (T > 0 && !(whole && none))
-              v = make_float4(__uint_as_float(o[g][2 * s]) * inv, __uint_as_float(o[g][2 * s + 1]) * inv,
-                              __uint_as_float(o[g + 1][2 * s]) * inv, __uint_as_float(o[g + 1][2 * s + 1]) * inv);
-            const int d = 64 * y + 16 * s + 2 * g;
-            if (whole) put4(p, out.at + d, v);
-            else *reinterpret_cast<float4*>(part + (128 * rt + rl) * D + d) = v;
+              for (int s = 0; s < 4; ++s) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (!zeros)
+                  v = make_float4(__uint_as_float(o[0][2 * s]) * inv, __uint_as_float(o[0][2 * s + 1]) * inv,
+                                  __uint_as_float(o[1][2 * s]) * inv, __uint_as_float(o[1][2 * s + 1]) * inv);
+                *staged(lane % AT_ONCE, 4 * s + g / 2) = v;
+              }
+            }
           }
+          __syncwarp();
+          const int c = lane & 15, d = 64 * y + 4 * c;
+#pragma unroll 1
+          for (int k0 = 0; k0 < AT_ONCE / 2; k0 += 4) {
+            int64_t to[4];
+            float4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int at = 2 * (k0 + k) + (lane >> 4);
+              to[k] = __shfl_sync(0xFFFFFFFFu, out.at, r0 + at);
+              v[k] = *staged(at, c);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int r = r0 + 2 * (k0 + k) + (lane >> 4);
+              if (r >= rows) continue;
+              if (whole) put4(p, to[k] + d, v[k]);
+              else *reinterpret_cast<float4*>(part + (128 * rt + 32 * (warp & 3) + r) * D + d) = v[k];
+            }
+          }
+          __syncwarp();
+        }
       }
       if (valid) {
         if (!whole) {
