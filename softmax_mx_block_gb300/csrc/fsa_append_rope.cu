@@ -15,11 +15,17 @@
 // is computed again to 2^-43.  Elements that neither a norm nor an angle touches are
 // exact as they are, and rounded as fsa_cache_append does.
 //
-// Bound by memory: 4 H + 4 Hkv + 2 Hkv (0.53 or 0.56) bytes a token and dim.  A block takes a
-// few tokens with all their heads, as fsa_qk_norm_rope does: the sines of a token are computed
-// once, for the rows of q (D/16 lanes each, both elements of a pair in a lane) and of k (D/8 lanes,
-// 8 consecutive elements a lane, as the quantisation wants them; a pair's other element comes from
-// another lane).
+// To move: 4 H + 4 Hkv + 2 Hkv (0.53 or 0.56) bytes a token and dim.  A block has the queries of a few
+// tokens or the keys and values of a few: the sines of a token are computed once a block, for the rows of q (D/16
+// lanes each, both elements of a pair in a lane) or of k (D/8 lanes, 8 consecutive elements a lane, as the
+// quantisation wants them; a pair's other element comes from another lane).  (All heads of a token in one
+// block: 120 us instead of 99 for 16384 tokens; the keys' lanes waited for the queries'.)
+//
+// Measured (one GB300, calls in a graph, 32+8 heads of 128, NVFP4, against fsa_qk_norm_rope and fsa_cache_append in
+// turn): 64 tokens 5.7 us (5.8), 512 8.0 (9.4), 2048 17.2 (15.5), 16384 96 (76), where memory takes 52.  From about a
+// thousand tokens on it is bound by instructions, 59 M a warp for 16384 tokens, 2 of 4 a cycle: half of them turn the
+// keys, whose two roundings and whose register need beside the rare ways cost what the saved pass over k gives; the
+// codes are those of the exact keys, which the two calls' are not.
 #include <algorithm>
 #include "fsa_cache_codes.cuh"
 #include "fsa_rope.cuh"
@@ -28,8 +34,9 @@ namespace fsa {
 namespace {
 
 constexpr float SURE = 0x1.4p-20f;      // of a row's largest |y|: more than the fp32 arithmetic is off by
-constexpr int KV_ROWS = 2;            // rows of a thread in flight, of k and of v each
-constexpr int APPEND_MANY = 10, APPEND_FEW = 8;       // blocks of an SM where there are more than run at once, and where all do
+// Blocks of an SM: where there are more than run at once (16384 tokens, 32+8 heads: 12 96.2 us, 11 97.4, 10 99.0; 80
+// registers and some spills), and where all do (no spills: 64 tokens 5.7 us instead of 6.1).
+constexpr int APPEND_MANY = 12, APPEND_FEW = 8;
 
 struct Place {
   int pos;             // what it turns by, if no positions are given
@@ -661,14 +668,14 @@ __global__ void __launch_bounds__(ROPE_THREADS, BLOCKS) append_rope_kernel(const
   const uint16_t* vsrc = p.v + b * p.vs.b + s * p.vs.s + h * p.vs.h + 8 * l;
   const int64_t kstep = step * a.ks.h, vstep = step * p.vs.h;
   const bool live = j < ntok && place_of(p, tok, 0, false).live;
-  uint4 ku[KV_ROWS], vu[KV_ROWS];
-  auto load = [&](int r, int on) {                // row r + on from here
-    const bool in = live && h + (r + on) * step < a.Hkv;
-    ku[r] = in ? *reinterpret_cast<const uint4*>(ksrc + (r + on) * kstep) : make_uint4(0u, 0u, 0u, 0u);
-    vu[r] = in ? *reinterpret_cast<const uint4*>(vsrc + (r + on) * vstep) : make_uint4(0u, 0u, 0u, 0u);
+  uint4 ku, vu, kn, vn;                           // this row's, and the next one's on their way
+  auto load = [&](int on, uint4& k, uint4& v) {   // row `on` from here
+    const bool in = live && h + on * step < a.Hkv;
+    k = in ? *reinterpret_cast<const uint4*>(ksrc + on * kstep) : make_uint4(0u, 0u, 0u, 0u);
+    v = in ? *reinterpret_cast<const uint4*>(vsrc + on * vstep) : make_uint4(0u, 0u, 0u, 0u);
   };
-#pragma unroll
-  for (int r = 0; r < KV_ROWS; ++r) load(r, 0);           // before the place is looked up
+  load(0, ku, vu);                                // before the place is looked up
+  load(1, kn, vn);
   const Place at = place_of(p, tok, Gr::BYTES, live);
   const bool kept = at.group != nullptr;
   const int64_t head = ((int64_t)1 << (p.c.page_shift - 4)) * Gr::BYTES;
@@ -678,21 +685,20 @@ __global__ void __launch_bounds__(ROPE_THREADS, BLOCKS) append_rope_kernel(const
   turn();
   Lane8 f;
   set_lane<D, INTER>(f, a, sines + j * a.half, l);
-  // every lane of a warp goes along (their rows end together)
+  // every lane of a warp goes along (their rows end together); the loop has one row's code, not two: what is to
+  // be fetched counts
 #pragma unroll 1
-  for (int n = a.Hkv; n > 0; n -= KV_ROWS * step) {
-#pragma unroll
-    for (int r = 0; r < KV_ROWS; ++r) {
-      if (n <= r * step) break;                   // (the same for all)
-      const bool in = kept && h + r * step < a.Hkv;
-      const int64_t to = (h + r * step) * head;
-      put_key<D, INTER, CF>(p, f, ku[r], in, pos, at.pos, codes + to, scales + to);
-      put_value<D, CF>(vu[r], in, codes + to, scales + to);
-      load(r, KV_ROWS);
-    }
-    h += KV_ROWS * step;
-    ksrc += KV_ROWS * kstep;
-    vsrc += KV_ROWS * vstep;
+  for (int n = a.Hkv; n > 0; n -= step) {
+    const bool in = kept && h < a.Hkv;
+    const int64_t to = h * head;
+    put_key<D, INTER, CF>(p, f, ku, in, pos, at.pos, codes + to, scales + to);
+    put_value<D, CF>(vu, in, codes + to, scales + to);
+    ku = kn;
+    vu = vn;
+    load(2, kn, vn);
+    h += step;
+    ksrc += kstep;
+    vsrc += vstep;
   }
 }
 

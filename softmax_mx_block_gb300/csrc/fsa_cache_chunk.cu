@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
       if (pc.begins && !pc.ends) start = make_int4(pc.vb * p.c.Hkv + pc.hkv, pc.last, pc.qlen, pc.len);
       if (!active) { slot += T; continue; }
       float cq = 1.f;
-      int lim = 0;
+      int lim = INT32_MAX;                                         // (rows that are none need no masks)
       {
         const int i = row / p.G, h = pc.hkv * p.G + row - i * p.G;
         if (T > 0) {
@@ -518,10 +518,23 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
         }
         if (valid) lim = p.causal ? max(0, pc.len - pc.qlen + i + 1) : pc.len;
       }
-      const int wlo = p.window ? lim - p.window : 0;
+      const int wlo = p.window && valid ? lim - p.window : 0;
       float M = NONE;
       uint64_t l2 = pk2(0.f, 0.f), l3 = l2;
-      for (int j = 0; j < T; ++j, ++n, ++slot) {
+      int j = 0;
+      if (pc.rows <= 128 * rt + 32 * (warp & 3))                 // none of the warp's rows is one: it only goes along
+        for (; ok && j < T; ++j, ++n, ++slot) {
+          ok = wait(s_full + rt, n & 1);
+          tc_fence_before();
+          __syncwarp();
+          if constexpr (C::APART) {
+            mbar_arrive_elect(s_free + rt);
+            if (ok && j > 0) ok = wait(o_done + rt, (n - 1) & 1);        // (so that the last tile's p_full has had all its arrivals)
+          }
+          mbar_arrive_elect(p_full + rt);
+        }
+#pragma unroll 1
+      for (; ok && j < T; ++j, ++n, ++slot) {
         const int k0 = pc.at(pc.t0 + j) * KEYS;
         ok = wait(s_full + rt, n & 1);
         if (!ok) break;
