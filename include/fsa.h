@@ -490,9 +490,9 @@ int fsa_cache_read(const fsa_cache* cache, void* k, void* v, const fsa_strides* 
                    const fsa_strides* v_strides, int B, int S, const int32_t* block_table, int max_pages,
                    const int32_t* lens, const int32_t* start, int32_t* status, void* stream);
 
-/* Attention of few query rows over the cache (decode steps, guessed tokens, short chunks of a
- * prompt; the cache is read again for each 16 rows a kv head, so from about 400 on
- * fsa_cache_read and fsa_attention_fwd_bf16 on what it gives are faster): O = softmax(scale Q K^T) V on the values the cache stands for; q is not
+/* Attention of few query rows over the cache (decode steps, guessed tokens; the cache is read
+ * again for each 16 rows a kv head, so from about 60 on fsa_attention_chunk is faster, with 64
+ * dims from about 80): O = softmax(scale Q K^T) V on the values the cache stands for; q is not
  * quantised, sums and softmax statistics are fp32, probabilities times V's scales are
  * rounded to f16 before the product with the codes of V (2^-11 relative, 2^-10 with
  * NVFP4; for products far below the largest block scale in V that the row sees, an absolute

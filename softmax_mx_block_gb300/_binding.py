@@ -744,7 +744,7 @@ def fsa_attention_chunk(q: torch.Tensor, cache: MxCache, block_table: torch.Tens
                         workspace: torch.Tensor | None = None, timeout_ms=0, status: torch.Tensor | None = None,
                         stream=None) -> torch.Tensor:
     """What fsa_attention_cache computes, for chunks of a prompt: 256 rows a kv head at a time, on
-    the tensor cores in bf16.  Arguments as there (workspace: fsa_attention_chunk_workspace bytes)."""
+    the tensor cores in 16 bits; faster from about 60 rows a kv head on.  Arguments as there (workspace: fsa_attention_chunk_workspace bytes)."""
     return _attend("attention_chunk", q, cache, block_table, lens, q_lens, causal, scale, window, sinks, out, lse, out_dtype,
                    workspace, timeout_ms, status, stream)
 

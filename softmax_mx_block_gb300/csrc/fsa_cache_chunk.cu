@@ -28,6 +28,17 @@
 //     joined by a second kernel.  Lengths are read on the device.
 //   - A row that sees a token whose values are not finite (the scale's NaN) is NaN as a whole; the others
 //     are as without it (its V is zero in the operand, and a bit tells the rows).
+//
+// Measured (one GB300, cuBLAS at 1943 TFLOP/s in bf16): 2048 tokens over 128K keys, 32/8 heads of 128: NVFP4 1590
+// TFLOP/s (2.74 ms), E2M1 1147 (3.80); heads of 64: 902 (2.42) and 757 (2.88).  Eight sequences of 8192 keys,
+// 64 tokens each, NVFP4: 74 us, where fsa_attention_cache takes 321.
+// What bounds it: of the about 3100 cycles of a tile of 128 dims (NVFP4) its products take 2050 at the nominal rate; a row tile's chain, its
+// scores, their maximum (510 cycles), exponentials (1300), products, is as long, and the two row tiles' chains cover each
+// other but for their ends.  The operand warps need 2400 of these cycles; with E2M1, K through bf16, 3100 and more, and
+// they are the bound there.  With 64 dims the products are half as long and the rest is not.  Instructions are fetched
+// too slowly for all of the code to be straight (0.4 to 0.9 of the 7 to 11 cycles between a warp's instructions
+// wait for them): what runs once a piece is in loops.  A piece costs about 12000 cycles beside its tiles: q (2500 to 8000, by
+// where it lies), the first scores, the last products, the rows' way out (4000).
 #include <algorithm>
 #include <atomic>
 #include "fsa_cache.h"
@@ -38,7 +49,7 @@ namespace {
 
 constexpr int ROWS = 256;             // of a block: two tiles of 128
 constexpr int KEYS = 128;             // of a tile
-constexpr int EXTRA = 3;              // what a segment's start costs a CTA, in tiles
+constexpr int EXTRA = 3;              // what a segment's start costs a CTA, in tiles (eight turns: 1 174 us, 2 160, 3 150, 5 148, 8 157)
 constexpr int THREADS = 512;          // warps 0..7 softmax (a row a thread), 8..11 operands, 12 copies, 13 MMA
 constexpr int RAW = 3;                // stages of 64 keys of codes
 constexpr float LAZY = 8.0f;          // log2 of how far a score may beat the running maximum
@@ -61,7 +72,8 @@ struct Cfg {
   static constexpr int SMEM = OFF_PRE + THREADS * 4 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   // tensor memory: + 128 (S), + D (O), + P_STEP (P) for the second row tile.  With D 64 P has columns of its own, and the next
-  // tile's scores are computed while this one's softmax runs; with D 128 it lies over the scores.
+  // tile's scores are computed while this one's softmax runs (NVFP4 882 TFLOP/s instead of 818, E2M1 734 instead of 743);
+  // with D 128 it lies over the scores, for want of columns.
   static constexpr bool APART = D == 64;
   static constexpr uint32_t T_S = 0, T_O = 256, T_P = APART ? 384 : 0, P_STEP = APART ? 64 : 128;
   static constexpr int PART = ROWS * (D + 2);            // floats of a partial result: rows, maxima, sums
@@ -488,6 +500,8 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
 
   if (warp < 8) {
     // ============================================================ softmax, a row a thread
+    // (8 warps of 176, 4 of 96, 4 of 64: the launch's 16 of 128.  184 and 96 and 48: NVFP4 2% more, E2M1 4% less; 168, 104, 72:
+    // NVFP4 4% less)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     const int rt = warp >> 2, rl = threadIdx.x & 127;
     const uint32_t tl = tbase + ((uint32_t)(32 * (warp & 3)) << 16);
@@ -1073,7 +1087,9 @@ cudaError_t launch(const CacheAttnArgs& a, int sms, cudaStream_t st) {
 
 int cache_chunk_blocks(int rows) { return (rows + ROWS - 1) / ROWS; }
 
-// Segments of at most 4 tiles are not shared: a CTA each, no second kernel.
+// Segments of at most 4 tiles are not shared: a CTA each, no second kernel (64 tokens over 512 keys, NVFP4, in tables
+// of 512 and of 576 tokens, which are shared: 4 sequences 18.0 and 25.0 us, 32 34 and 52, 64 67 and 82; 256 of 256 keys
+// 178 and 206).
 bool cache_chunk_whole(const Cache& c, int max_pages) { return ((int64_t)max_pages << c.page_shift) <= 4 * KEYS; }
 
 // parts of the CTAs, two each; where segments begin that go on
