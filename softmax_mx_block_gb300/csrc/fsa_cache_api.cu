@@ -346,7 +346,6 @@ int fsa_attention_chunk(const fsa_cache_attn* c, int window, int sinks, void* st
   fsa::CacheAttnArgs a{};
   const int st = take_attn(c, window, sinks, chunk_shape_ok, &a);
   if (st != FSA_OK) return st;
-  if (!(std::fabs(c->scale) <= 0x1p80f)) return FSA_ERR_INVALID_ARG;   // 2^40 of it below has to stay finite
   int sms = 0;
   if (!sm_count(&sms)) return FSA_ERR_NO_DEVICE;
   size_t starts_at;
@@ -354,7 +353,6 @@ int fsa_attention_chunk(const fsa_cache_attn* c, int window, int sinks, void* st
   if (!take_workspace(c, need, starts_at, &a)) return FSA_ERR_INVALID_ARG;
   a.CT = fsa::cache_chunk_blocks(c->Sq * a.G);
   a.whole = fsa::cache_chunk_whole(a.c, c->max_pages);
-  if (a.c.cf == fsa::CF_MX) a.scale_log2 *= 0x1p40f;       // there the kernel's K is 2^-40 of what the cache stands for
   return launch_status(fsa::launch_cache_chunk(a, sms, static_cast<cudaStream_t>(stream)));
 }
 

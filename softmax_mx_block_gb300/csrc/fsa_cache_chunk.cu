@@ -13,12 +13,11 @@
 //     permuted as it is loaded, those of V in the output's columns, which are put in order as they are
 //     stored.  K is K-major; V needs no transposition, as the second operand of a product over the keys it
 //     is MN-major.
-//   - NVFP4: a code is one conversion to f16, its E4M3 scale one product, both exact; q goes as f16 too, with a
-//     power of two a row (exact down to 2^-18 of its row's maximum, off by at most 2^-29 of it below).
-//   - E8M0 scales have fp32's range.  K is bf16: E2M1's exponent and fraction put into bf16's lowest bits are the
-//     value times 2^-126, a zero or a subnormal included; one product with the scale times 2^(126 - 40)
-//     gives 2^-40 of the value, and the softmax factor makes up for it (keys of 2^44 and more count as NaN).  V is
-//     f16 too, exactly, where all scales of a tile lie in 2^-23 .. 2^13, and otherwise bf16, and P alike.
+//   - All operands are f16.  A code is one conversion, its scale one product: exact for E4M3 scales, and for E8M0
+//     scales of 2^-23 .. 2^13.  Those have fp32's range: a key with others is divided by a power of two that makes its
+//     largest scale 2^13, and its scores are multiplied by that (its blocks below 2^-36 of its largest lose bits); 32 keys
+//     with others in V have V, and P with it, as bf16.  q has a power of two a row (exact down to 2^-18 of its row's
+//     maximum, off by at most 2^-29 of it below).
 //   - S, then P over it, and O stay in tensor memory: 128 columns each for both row tiles.  While
 //     the softmax of one row tile runs, the other's products do.  P is rounded to f16 (2^-11 of each
 //     weight, 2^-32 absolute; where V is bf16 to that, 2^-8); sums and maxima are fp32.  The running maximum
@@ -65,11 +64,12 @@ struct Cfg {
   static constexpr int STAGE = 4 * Gr::BYTES;            // 64 keys
   static constexpr int OFF_Q = 0, OFF_K = 2 * TILE, OFF_V = 4 * TILE, OFF_RAW = 6 * TILE;
   static constexpr int OFF_BAR = (OFF_RAW + RAW * STAGE + 63) / 64 * 64;
-  static constexpr int OFF_FLAGS = OFF_BAR + 256;        // [4 tiles] of absent keys, keys with a NaN in V, V as bf16: a word a warp
-  static constexpr int OFF_MISC = OFF_FLAGS + 4 * 48;    // absent groups of the raw stages, tmem base, abort flag, warp sums
+  static constexpr int OFF_FLAGS = OFF_BAR + 256;        // [4 tiles] of absent keys, keys with a NaN in V, V as bf16, keys with a shift: a word a warp
+  static constexpr int OFF_MISC = OFF_FLAGS + 4 * 64;    // absent groups of the raw stages, tmem base, abort flag, warp sums
   static constexpr int OFF_WALK = OFF_MISC + 128;        // where each warp is in the list
   static constexpr int OFF_PRE = OFF_WALK + 16 * 80;     // [THREADS] prefix sums of the list
-  static constexpr int SMEM = OFF_PRE + THREADS * 4 + 1024;
+  static constexpr int OFF_SHIFT = OFF_PRE + THREADS * 4;                    // E8M0: [4 tiles][KEYS] powers of two out of K
+  static constexpr int SMEM = OFF_SHIFT + (CF == CF_MX ? 4 * KEYS * 2 : 0) + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   // tensor memory: + 128 (S), + D (O), + P_STEP (P) for the second row tile.  With D 64 P has columns of its own, and the next
   // tile's scores are computed while this one's softmax runs (NVFP4 882 TFLOP/s instead of 818, E2M1 734 instead of 743);
@@ -186,31 +186,21 @@ __device__ __forceinline__ bool next_piece(const CacheAttnArgs& p, Walk* slot, c
 }
 
 // ---------------------------------------------------------------- operands from codes
-__device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// The eight codes of a word as bf16 of value * 2^-126: nibbles i and i + 4 in word i.
-__device__ __forceinline__ void spread(uint32_t w, uint32_t (&o)[4]) {
-  constexpr uint32_t SIGN = 0x80008000u, MAG = 0x01C001C0u;
-  o[0] = ((w << 12) & SIGN) | ((w << 6) & MAG);
-  o[1] = ((w << 8) & SIGN) | ((w << 2) & MAG);
-  o[2] = ((w << 4) & SIGN) | ((w >> 2) & MAG);
-  o[3] = (w & SIGN) | ((w >> 6) & MAG);
-}
 __device__ __forceinline__ uint32_t byte_of(const uint32_t (&w)[2], int i) { return (w[i / 4] >> (8 * (i % 4))) & 0xFFu; }
-// E8M0 scales as factors, twice in a word: of bf16, 2^(126 - 40) * scale (NaN from 2^42 on);
-// of f16 (2^-23 to 2^13)
+// E8M0 scales as factors of f16, twice in a word: exact from 2^-23 to 2^13, whose products with a code are too
 constexpr uint32_t LEAST_F16 = 127 - 23, MOST_F16 = 127 + 13;
-__device__ __forceinline__ uint32_t e8m0_bf16(uint32_t byte) { return (byte < 169u ? (byte + 86u) << 7 : 0x7FC0u) * 0x10001u; }
 __device__ __forceinline__ uint32_t e8m0_f16(uint32_t byte) {
   return (byte > 112u ? (byte - 112u) << 10 : 1u << (byte - 103u)) * 0x10001u;
+}
+// K's, `shift` powers of two less; the least are zeros then, and NaN stays
+__device__ __forceinline__ uint32_t e8m0_f16_shifted(uint32_t byte, int shift) {
+  const int b = (int)byte - shift;
+  return byte == 0xFFu ? 0x7E007E00u : b < 103 ? 0u : e8m0_f16((uint32_t)b);
 }
 __device__ __forceinline__ uint32_t e4m3_f16(uint32_t byte) {
   uint32_t r;
@@ -223,39 +213,45 @@ __device__ __forceinline__ void put_piece(uint8_t* row_at, int row, int piece, c
   *reinterpret_cast<uint4*>(row_at + (piece >> 3) * (KEYS * 128) + (((piece & 7) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// How a row's words become a row of an operand: f(word, its place among the four of 16 bytes, o).
-// Neighbouring lanes take the 16-byte pieces in turn, so that neither the loads nor the stores of a
+// A row's 16-byte pieces.  Neighbouring lanes take them in turn, so that neither these loads nor the stores of a
 // quarter of the warp share banks (D 64: the loads do, two and two).
-template <int D, class F>
-__device__ __forceinline__ void put_row(uint8_t* dst, int row, const uint8_t* src, F f) {
-  uint8_t* const at = dst + row * 128;
+template <int D>
+__device__ __forceinline__ int piece_of(int row, int c) { return D == 128 ? (c + (row >> 1)) & 3 : c; }
+template <int D>
+struct Row {
   uint4 u[D / 32];
+  __device__ __forceinline__ void load(int row, const uint8_t* src) {
 #pragma unroll
-  for (int c = 0; c < D / 32; ++c) u[c] = *reinterpret_cast<const uint4*>(src + 16 * (D == 128 ? (c + (row >> 1)) & 3 : c));
+    for (int c = 0; c < D / 32; ++c) u[c] = *reinterpret_cast<const uint4*>(src + 16 * piece_of<D>(row, c));
+  }
+};
+// How a row's words become a row of an operand: f(word, its place among the four of 16 bytes, o).
+template <int D, class F>
+__device__ __forceinline__ void put_row(uint8_t* dst, int row, const Row<D>& r, F f) {
+  uint8_t* const at = dst + row * 128;
 #pragma unroll
   for (int c = 0; c < D / 32; ++c) {
-    const int cc = D == 128 ? (c + (row >> 1)) & 3 : c;
-    const uint32_t w[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
+    const uint32_t w[4] = {r.u[c].x, r.u[c].y, r.u[c].z, r.u[c].w};
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       uint32_t o[4];
       f(w[x], x, o);
-      put_piece(at, row, 4 * cc + x, o);
+      put_piece(at, row, 4 * piece_of<D>(row, c) + x, o);
     }
   }
 }
 // A row of K.  Word 4t + w (D 64: 2t + w) holds elements 32w + 4t + 0..3 and 16 on, whose scales are those of
-// block w (E8M0) or 2w and 2w + 1 (E4M3).  gone: its codes are not there.
+// block w (E8M0) or 2w and 2w + 1 (E4M3).  gone: its codes are not there.  shift: of E8M0 scales, see above.
 template <int D, int CF>
-__device__ __forceinline__ void put_key(uint8_t* dst, int row, const uint8_t* src, const uint32_t (&sb)[2], bool gone) {
+__device__ __forceinline__ void put_key(uint8_t* dst, int row, const Row<D>& src, const uint32_t (&sb)[2], bool gone, int shift) {
   if constexpr (CF == CF_MX) {
     uint32_t f[D / 32];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) f[i] = gone ? 0u : e8m0_bf16(byte_of(sb, i));
+    for (int i = 0; i < D / 32; ++i) f[i] = gone ? 0u : e8m0_f16_shifted(byte_of(sb, i), shift);
     put_row<D>(dst, row, src, [&](uint32_t w, int x, uint32_t (&o)[4]) {
-      spread(w, o);
+      cvt_e2m1x8_f16(w, o);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = bmul2(o[e], f[x % (D / 32)]);
+      for (int e = 0; e < 4; ++e) o[e] = hmul2(o[e], f[x % (D / 32)]);
     });
   } else {
     uint32_t f[D / 16];
@@ -281,7 +277,7 @@ __device__ __forceinline__ float e8m0_f32(uint32_t byte) { return __uint_as_floa
 // A row of V.  Word 2g + y (D 64: g) holds elements 64y + 2g, + 1, and 16, 32 and 48 on.  A scale that is NaN
 // counts as zero.
 template <int D, int CF>
-__device__ __forceinline__ void put_value(uint8_t* dst, int row, const uint8_t* src, const uint32_t (&sb)[2], bool gone) {
+__device__ __forceinline__ void put_value(uint8_t* dst, int row, const Row<D>& src, const uint32_t (&sb)[2], bool gone) {
   constexpr int SB = CacheGroup<D, CF>::SB;
   uint32_t f[SB];
 #pragma unroll
@@ -316,12 +312,11 @@ __device__ __forceinline__ void put_value_far(uint8_t* dst, int row, const uint8
 
 // A warp's 32 rows of a tile of q, from `row0` on, in the order of K's columns; src: this lane's row (zeros without one).
 // Neighbouring lanes take 16-byte pieces of a row.  Returns what the scores of this lane's row are to be multiplied by.
-template <int D, int CF>
+template <int D>
 __device__ __forceinline__ float put_queries(uint8_t* dst, int row0, const uint16_t* src, float sign, float scale_log2) {
   constexpr int L = D / 8, RPI = 32 / L, AHEAD = 8;                // lanes of a row, rows and loads at a time
   const int lane = threadIdx.x & 31, ch = lane % L, sub = lane / L;
   const int w = ch / 4, h = ch & 1, side = ch >> 1 & 1;            // elements 32w + 16 side + 8h + 0..7
-  const uint32_t flip = sign < 0.f ? 0x80008000u : 0u, keep = sign == 0.f ? 0u : 0xFFFFFFFFu;
   float cq = scale_log2;
 #pragma unroll 1
   for (int k0 = 0; k0 < 32 / RPI; k0 += AHEAD) {
@@ -334,32 +329,23 @@ __device__ __forceinline__ float put_queries(uint8_t* dst, int row0, const uint1
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) {
       uint32_t t[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
-      if constexpr (CF == CF_NV) {                                 // (as fsa_cache_attn.cu has q)
-        uint32_t m = __vmaxu2(__vimax3_u16x2(t[0] & 0x7FFF7FFFu, t[1] & 0x7FFF7FFFu, t[2] & 0x7FFF7FFFu), t[3] & 0x7FFF7FFFu);
+      // (as fsa_cache_attn.cu has q)
+      uint32_t m = __vmaxu2(__vimax3_u16x2(t[0] & 0x7FFF7FFFu, t[1] & 0x7FFF7FFFu, t[2] & 0x7FFF7FFFu), t[3] & 0x7FFF7FFFu);
 #pragma unroll
-        for (int x = 1; x < L; x *= 2) m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
-        m = max(m & 0xFFFFu, m >> 16);
-        const int e = (int)(m >> 7) - 127;                         // floor(log2) of the row's maximum
-        const int up = e == 128 || m == 0 ? 0 : min(max(4 - e, -126), 126);
-        const float f = e == 128 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(up + 127) << 23) * sign;
-        const float c = fmaxf(scale_log2 * __uint_as_float((uint32_t)(127 - up) << 23), 1.4e-45f);      // (0 times -inf is NaN)
-        const float theirs = __shfl_sync(0xFFFFFFFFu, c, lane % RPI * L);
-        if (lane / RPI == k0 + k) cq = theirs;
+      for (int x = 1; x < L; x *= 2) m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+      m = max(m & 0xFFFFu, m >> 16);
+      const int e = (int)(m >> 7) - 127;                   // floor(log2) of the row's maximum
+      const int up = e == 128 || m == 0 ? 0 : min(max(4 - e, -126), 126);
+      const float f = e == 128 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(up + 127) << 23) * sign;
+      const float c = fmaxf(scale_log2 * __uint_as_float((uint32_t)(127 - up) << 23), 1.4e-45f);      // (0 times -inf is NaN)
+      const float theirs = __shfl_sync(0xFFFFFFFFu, c, lane % RPI * L);
+      if (lane / RPI == k0 + k) cq = theirs;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) t[i] = cvt_f16x2(__uint_as_float(t[i] << 16) * f, __uint_as_float(t[i] & 0xFFFF0000u) * f);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) t[i] = (t[i] ^ flip) & keep;
-      }
+      for (int i = 0; i < 4; ++i) t[i] = cvt_f16x2(__uint_as_float(t[i] << 16) * f, __uint_as_float(t[i] & 0xFFFF0000u) * f);
       // elements 16 on have the same places: the lane that has them takes the upper halves of both, this one the lower
       const uint32_t x0 = __shfl_xor_sync(0xFFFFFFFFu, side ? t[0] : t[2], 2), x1 = __shfl_xor_sync(0xFFFFFFFFu, side ? t[1] : t[3], 2);
       const uint32_t ax[2] = {side ? x0 : t[0], side ? x1 : t[1]}, bx[2] = {side ? t[2] : x0, side ? t[3] : x1};
-      uint32_t o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (CF == CF_NV) o[i] = i < 2 ? ax[i] : bx[i - 2];
-        else o[i] = __byte_perm(ax[i / 2], bx[i / 2], i & 1 ? 0x7632 : 0x5410);
-      }
+      const uint32_t o[4] = {ax[0], ax[1], bx[0], bx[1]};
       const int row = row0 + RPI * (k0 + k) + sub;
       put_piece(dst + row * 128, row, (D / 32) * (2 * h + side) + w, o);
     }
@@ -439,7 +425,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
   uint64_t* const s_free = k_full + 16;        // [2] APART: the scores have been read (4 warps)
   uint64_t* const o_done = k_full + 18;        // [2] APART: a tile's products with V are done
   uint64_t* const drain = k_full + 20;
-  uint32_t* const flags = reinterpret_cast<uint32_t*>(sm + C::OFF_FLAGS);      // [4 tiles][3][4]
+  uint32_t* const flags = reinterpret_cast<uint32_t*>(sm + C::OFF_FLAGS);      // [4 tiles][4][4]
   uint32_t* const absent = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);      // [RAW]
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC + 16);
   int* const abort_flag = reinterpret_cast<int*>(sm + C::OFF_MISC + 20);
@@ -525,7 +511,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
       {
         const int i = row / p.G, h = pc.hkv * p.G + row - i * p.G;
         if (T > 0) {
-          cq = put_queries<D, CF>(sm + C::OFF_Q + rt * C::TILE, 32 * (warp & 3), valid ? p.q + b * p.qs.b + i * p.qs.s + h * p.qs.h : nullptr, p.q_sign, p.scale_log2);
+          cq = put_queries<D>(sm + C::OFF_Q + rt * C::TILE, 32 * (warp & 3), valid ? p.q + b * p.qs.b + i * p.qs.s + h * p.qs.h : nullptr, p.q_sign, p.scale_log2);
           fence_proxy_async_smem();
           __syncwarp();
           mbar_arrive_elect(q_full + rt);
@@ -556,19 +542,22 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
         // The maximum of all, then block after block of 32 (64 scores at a time in registers; the last two are read twice).
         // Halves as a loop where that is no slower: the fetching of instructions counts here (NVFP4 1564 to 1596 TFLOP/s).
         uint32_t ra[32], rb[32];
-        const uint32_t* const fl = flags + 12 * (slot & 3);
+        const uint32_t* const fl = flags + 16 * (slot & 3);
         uint32_t told;
         bool wide = false;
+        bool far = false;                                // some keys have a shift
         {
           const uint4 a = reinterpret_cast<const uint4*>(fl)[0], c = reinterpret_cast<const uint4*>(fl)[1];
           told = a.x | a.y | a.z | a.w | c.x | c.y | c.z | c.w;
           if constexpr (CF == CF_MX) {
             const uint4 t = reinterpret_cast<const uint4*>(fl)[2];
             wide = (t.x | t.y | t.z | t.w) != 0;
+            const uint4 f = reinterpret_cast<const uint4*>(fl)[3];
+            far = (f.x | f.y | f.z | f.w) != 0;
           }
         }
         // the keys that the row does not see (all rows of a warp go along)
-        const bool masked = __any_sync(0xFFFFFFFFu, told != 0 || k0 + KEYS > lim || (k0 < wlo && k0 + KEYS > p.sinks));
+        const bool masked = __any_sync(0xFFFFFFFFu, wide || far || told != 0 || k0 + KEYS > lim || (k0 < wlo && k0 + KEYS > p.sinks));
         uint32_t seen[4] = {};
         if (masked) {
           uint32_t bad = 0;
@@ -581,6 +570,31 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
           if (bad) l2 = pk2(__uint_as_float(0x7FC00000u), 0.f);
         }
         float top = NONE;
+        // 32 scores of a tile with shifts (rare)
+        auto far32 = [&](int c) {
+          tmem_ld_cols<32>(tS + 32 * c, ra);
+          tc_wait_ld();
+          if (CF == CF_MX && far) {
+            const int4* const at = reinterpret_cast<const int4*>(sm + C::OFF_SHIFT) + (KEYS * (slot & 3) + 32 * c) / 8;
+            const uint32_t these = fl[12 + c];
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              const int4 eight = at[e / 8];
+              const int words[4] = {eight.x, eight.y, eight.z, eight.w};
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {                // (in two steps: it may lie beyond a float's powers of two)
+                const int by = these ? (i & 1 ? words[i / 2] >> 16 : (int)(int16_t)words[i / 2]) : 0, half = by >> 1;
+                ra[e + i] = __float_as_uint(__uint_as_float(ra[e + i]) * __uint_as_float((uint32_t)(127 + half) << 23) *
+                                            __uint_as_float((uint32_t)(127 + by - half) << 23));
+              }
+            }
+          }
+          return mask32(ra, c == 0 ? seen[0] : c == 1 ? seen[1] : c == 2 ? seen[2] : seen[3]);
+        };
+        if (CF == CF_MX && far) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) top = fmaxf(top, far32(c));
+        } else {
 #pragma unroll 1
         for (int c = 2; c >= 0; c -= 2) {
           float ma, mb;
@@ -589,6 +603,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
           tc_wait_ld();
           if (masked) { ma = mask32(ra, c ? seen[2] : seen[0]); mb = mask32(rb, c ? seen[3] : seen[1]); }
           top = fmaxf(top, fmaxf(ma, mb));
+        }
         }
         const float x = top * cq;
         float alpha = 1.f;
@@ -645,13 +660,12 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
             tc_fence_after();
           }
         }
-        if (CF == CF_MX && wide) {                       // (rare: block after block, read again)
+        if (CF == CF_MX && (wide || far)) {              // (rare: block after block, read again)
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            tmem_ld_cols<32>(tS + 32 * c, ra);
-            tc_wait_ld();
-            if (masked) mask32(ra, c == 0 ? seen[0] : c == 1 ? seen[1] : c == 2 ? seen[2] : seen[3]);
-            weigh(ra, c, [](float a, float bb) { return cvt_bf16x2(a, bb); });
+            far32(c);
+            const bool w = fl[8 + c] != 0;
+            weigh(ra, c, [&](float a, float bb) { return w ? cvt_bf16x2(a, bb) : cvt_f16x2(a, bb); });
           }
         } else {
           auto f16 = [](float a, float bb) { return cvt_f16x2(a, bb); };
@@ -673,7 +687,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
           }
         }
         if constexpr (C::APART && CF == CF_MX) {
-          if (wide) {
+          if (wide || far) {
             tc_fence_before();
             __syncwarp();
             mbar_arrive_elect(s_free + rt);
@@ -792,41 +806,61 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
           ks[0] = *reinterpret_cast<const uint16_t*>(kp);
           vs[0] = *reinterpret_cast<const uint16_t*>(vp);
         }
-        bool nan = false, far = false;
+        bool nan = false, far = false, kfar = false;
+        uint32_t kmax = 0;
 #pragma unroll
         for (int i = 0; i < Gr::SB; ++i) {
           const uint32_t byte = byte_of(vs, i);
           nan |= CF == CF_MX ? byte == 0xFFu : (byte & 0x7Fu) == 0x7Fu;
           far |= CF == CF_MX && byte != 0xFFu && (byte < LEAST_F16 || byte > MOST_F16);
+          if constexpr (CF == CF_MX) {
+            const uint32_t k = byte_of(ks, i);
+            if (k != 0xFFu && k != 0u && !gone) {         // (the least scale is that of a block of zeros)
+              kfar |= k < LEAST_F16 || k > MOST_F16;
+              kmax = max(kmax, k);
+            }
+          }
         }
         const uint32_t gones = __ballot_sync(0xFFFFFFFFu, gone), nans = __ballot_sync(0xFFFFFFFFu, nan && !gone);
         const uint32_t fars = CF == CF_MX ? __ballot_sync(0xFFFFFFFFu, far && !gone) : 0u;
-        uint32_t* const fl = flags + 12 * (n & 3) + dw;
+        // (a key with a scale that is not exact in f16: divided by what makes its largest 2^13)
+        const int shift = CF == CF_MX && kfar ? (int)kmax - (int)MOST_F16 : 0;
+        const uint32_t kfars = CF == CF_MX ? __ballot_sync(0xFFFFFFFFu, shift != 0) : 0u;
+        uint32_t* const fl = flags + 16 * (n & 3);
         if (lane == 0) {
-          fl[0] = gones;
-          fl[4] = nans;
-          if (CF == CF_MX) fl[8] = fars;
+          fl[dw] = gones;
+          fl[4 + dw] = nans;
+          if (CF == CF_MX) {
+            fl[8 + dw] = fars;
+            fl[12 + dw] = kfars;
+          }
         }
-        put_key<D, CF>(sm + C::OFF_K + kb * C::TILE, row, base + Gr::K + (lane & 15) * (D / 2), ks, gone);
+        if (CF == CF_MX && kfars) reinterpret_cast<int16_t*>(sm + C::OFF_SHIFT)[KEYS * (n & 3) + row] = (int16_t)shift;
+        Row<D> r;
+        r.load(row, base + Gr::K + (lane & 15) * (D / 2));
+        put_key<D, CF>(sm + C::OFF_K + kb * C::TILE, row, r, ks, gone, shift);
         fence_proxy_async_smem();
         __syncwarp();
         mbar_arrive_elect(k_full + kb);
-        ok = n < 2 || wait(v_empty + kb, (n / 2 - 1) & 1);
-        if (!ok) break;
-        bool wide = false;
-        if constexpr (CF == CF_MX) {                     // the four warps agree on V's type
-          named_bar_sync(1, 128);
-          const uint4 a = *reinterpret_cast<const uint4*>(flags + 12 * (n & 3) + 8);
-          wide = (a.x | a.y | a.z | a.w) != 0;
-        }
-        uint8_t* const dst = sm + C::OFF_V + kb * C::TILE;
         const uint8_t* const src = base + Gr::V + (lane & 15) * (D / 2);
-        if (CF == CF_MX && wide) put_value_far<D>(dst, row, src, vs[0], gone);
-        else put_value<D, CF>(dst, row, src, vs, gone);
+        uint8_t* const dst = sm + C::OFF_V + kb * C::TILE;
+        if (CF == CF_MX && fars) {
+          ok = n < 2 || wait(v_empty + kb, (n / 2 - 1) & 1);
+          if (!ok) break;
+          put_value_far<D>(dst, row, src, vs[0], gone);
+          __syncwarp();
+          mbar_arrive_elect(raw_empty + rs);
+        } else {                                         // (the stage is free before V's place is)
+          r.load(row, src);
+          __syncwarp();
+          mbar_arrive_elect(raw_empty + rs);
+          ok = n < 2 || wait(v_empty + kb, (n / 2 - 1) & 1);
+          if (!ok) break;
+          put_value<D, CF>(dst, row, r, vs, gone);
+        }
         fence_proxy_async_smem();
         __syncwarp();
         mbar_arrive_elect(v_full + kb);
-        mbar_arrive_elect(raw_empty + rs);
       }
     }
   } else {
@@ -896,17 +930,19 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
 #pragma unroll
           for (int i = 0; i < D / 16; ++i)
             mma_f16_ss(tbase + C::T_S + 128 * rt, q + ((i / 4) * C::ATOM + (i % 4) * 32) / 16, k + ((i / 4) * C::ATOM + (i % 4) * 32) / 16,
-                       CF == CF_MX ? idesc_f16_bf16(128) : idesc_f16(128), i > 0);
+                       idesc_f16(128), i > 0);
           tc_commit(s_full + rt);
         }
         __syncwarp();
       };
-      auto products = [&](int rt, uint32_t vb, bool more, uint32_t idesc) {
+      auto products = [&](int rt, uint32_t vb, bool more, uint4 wide) {
         if (elect_one()) {
           const uint64_t v = dV + vb * (C::TILE / 16);
+          const uint32_t of[4] = {wide.x, wide.y, wide.z, wide.w};
 #pragma unroll
           for (int i = 0; i < KEYS / 16; ++i)
-            mma_f16_ts(tbase + C::T_O + D * rt, tbase + C::T_P + C::P_STEP * rt + 8 * i, v + i * (2048 / 16), idesc, more || i > 0);
+            mma_f16_ts(tbase + C::T_O + D * rt, tbase + C::T_P + C::P_STEP * rt + 8 * i, v + i * (2048 / 16),
+                       MN_MAJOR_B | (CF == CF_MX && of[i / 2] ? idesc_f16_bf16(D) : idesc_f16(D)), more || i > 0);
           if (C::APART) tc_commit(o_done + rt);
         }
         __syncwarp();
@@ -927,11 +963,8 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
         tc_commit_p(elect_u32(), k_empty + (n & 1));
         for (int j = 0; ok && j < T; ++j, ++n) {
           ok = wait(v_full + (n & 1), (n / 2) & 1);
-          uint32_t type = idesc_f16(D) | MN_MAJOR_B;
-          if constexpr (CF == CF_MX) {
-            const uint4 a = *reinterpret_cast<const uint4*>(flags + 12 * (n & 3) + 8);
-            if ((a.x | a.y | a.z | a.w) != 0) type = idesc_f16_bf16(D) | MN_MAJOR_B;
-          }
+          uint4 wide = make_uint4(0u, 0u, 0u, 0u);         // of each operand warp's keys: V and P are bf16
+          if constexpr (CF == CF_MX) wide = reinterpret_cast<const uint4*>(flags + 16 * (n & 3))[2];
           if (C::APART && j + 1 < T) {         // the next scores first
             ok = ok && wait(k_full + ((n + 1) & 1), ((n + 1) / 2) & 1);
             for (int rt = 0; ok && rt < tiles; ++rt) {
@@ -947,7 +980,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
             if (!ok) break;
             ++np[rt];
             tc_fence_after();
-            products(rt, n & 1, j > 0, type);
+            products(rt, n & 1, j > 0, wide);
             if (j + 1 == T) {
               tc_commit_p(elect_u32(), o_full + rt);
             } else if (!C::APART) {
