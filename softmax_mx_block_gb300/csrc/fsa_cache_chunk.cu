@@ -28,16 +28,17 @@
 //   - A row that sees a token whose values are not finite (the scale's NaN) is NaN as a whole; the others
 //     are as without it (its V is zero in the operand, and a bit tells the rows).
 //
-// Measured (one GB300, cuBLAS at 1943 TFLOP/s in bf16): 2048 tokens over 128K keys, 32/8 heads of 128: NVFP4 1590
-// TFLOP/s (2.74 ms), E2M1 1147 (3.80); heads of 64: 902 (2.42) and 757 (2.88).  Eight sequences of 8192 keys,
+// Measured (one GB300, cuBLAS at 1943 TFLOP/s in bf16): 2048 tokens over 128K keys, 32/8 heads of 128: NVFP4 1600
+// TFLOP/s (2.73 ms), E2M1 1339 (3.26); heads of 64: 942 (2.32) and 714 (3.05).  Eight sequences of 8192 keys,
 // 64 tokens each, NVFP4: 74 us, where fsa_attention_cache takes 321.
-// What bounds it: of the about 3100 cycles of a tile of 128 dims (NVFP4) its products take 2050 at the nominal rate; a row tile's chain, its
-// scores, their maximum (510 cycles), exponentials (1300), products, is as long, and the two row tiles' chains cover each
-// other but for their ends.  The operand warps need 2400 of these cycles; with E2M1, K through bf16, 3100 and more, and
-// they are the bound there.  With 64 dims the products are half as long and the rest is not.  Instructions are fetched
-// too slowly for all of the code to be straight (0.4 to 0.9 of the 7 to 11 cycles between a warp's instructions
-// wait for them): what runs once a piece is in loops.  A piece costs about 12000 cycles beside its tiles: q (2500 to 8000, by
-// where it lies), the first scores, the last products, the rows' way out (4000).
+// What bounds it: of the about 3100 cycles of a tile of 128 dims (NVFP4) its products take 2050 at the nominal rate; a row
+// tile's chain, its scores, their maximum (800 cycles), exponentials (1050), products, is as long, and the two row tiles'
+// chains cover each other but for their ends.  The operand warps work 2100 of these cycles.  E2M1 is slower by what tells
+// the rare scales and by their ways, which cost the softmax registers and fetches (exponentials 1400, K 1650).  With 64
+// dims the products are half as long and the rest is not.  Instructions are fetched too slowly for all of the code to be
+// straight (0.4 to 0.9 of the 7 to 11 cycles between a warp's instructions wait for them): what runs once a piece is in
+// loops.  A piece costs about 12000 cycles beside its tiles: q (2500 to 8000, by where it lies), the first scores, the last
+// products, the rows' way out (4000).
 #include <algorithm>
 #include <atomic>
 #include "fsa_cache.h"
@@ -544,8 +545,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
         uint32_t ra[32], rb[32];
         const uint32_t* const fl = flags + 16 * (slot & 3);
         uint32_t told;
-        bool wide = false;
-        bool far = false;                                // some keys have a shift
+        bool wide = false, far = false;                  // V, and P with it, is bf16 for some keys; some keys have a shift
         {
           const uint4 a = reinterpret_cast<const uint4*>(fl)[0], c = reinterpret_cast<const uint4*>(fl)[1];
           told = a.x | a.y | a.z | a.w | c.x | c.y | c.z | c.w;
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
           }
         }
         // the keys that the row does not see (all rows of a warp go along)
-        const bool masked = __any_sync(0xFFFFFFFFu, wide || far || told != 0 || k0 + KEYS > lim || (k0 < wlo && k0 + KEYS > p.sinks));
+        const bool masked = __any_sync(0xFFFFFFFFu, told != 0 || k0 + KEYS > lim || (k0 < wlo && k0 + KEYS > p.sinks));
         uint32_t seen[4] = {};
         if (masked) {
           uint32_t bad = 0;
@@ -569,32 +569,25 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
           }
           if (bad) l2 = pk2(__uint_as_float(0x7FC00000u), 0.f);
         }
-        float top = NONE;
-        // 32 scores of a tile with shifts (rare)
-        auto far32 = [&](int c) {
-          tmem_ld_cols<32>(tS + 32 * c, ra);
-          tc_wait_ld();
-          if (CF == CF_MX && far) {
-            const int4* const at = reinterpret_cast<const int4*>(sm + C::OFF_SHIFT) + (KEYS * (slot & 3) + 32 * c) / 8;
-            const uint32_t these = fl[12 + c];
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              const int4 eight = at[e / 8];
-              const int words[4] = {eight.x, eight.y, eight.z, eight.w};
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {                // (in two steps: it may lie beyond a float's powers of two)
-                const int by = these ? (i & 1 ? words[i / 2] >> 16 : (int)(int16_t)words[i / 2]) : 0, half = by >> 1;
-                ra[e + i] = __float_as_uint(__uint_as_float(ra[e + i]) * __uint_as_float((uint32_t)(127 + half) << 23) *
-                                            __uint_as_float((uint32_t)(127 + by - half) << 23));
-              }
-            }
-          }
-          return mask32(ra, c == 0 ? seen[0] : c == 1 ? seen[1] : c == 2 ? seen[2] : seen[3]);
-        };
-        if (CF == CF_MX && far) {
+        if (CF == CF_MX && far) {                        // (rare: eight scores at a time, each times its key's power of two)
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) top = fmaxf(top, far32(c));
-        } else {
+          for (int c = 0; c < KEYS / 8; ++c) {
+            if (fl[12 + c / 4] == 0) continue;           // (the same for all: none of these 32 keys has one)
+            uint32_t o[8];
+            TmemLd<8>::run(tS + 8 * c, o);
+            const int4 by8 = reinterpret_cast<const int4*>(sm + C::OFF_SHIFT)[KEYS / 8 * (slot & 3) + c];
+            const int by2[4] = {by8.x, by8.y, by8.z, by8.w};
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {                // (in two steps: it may lie beyond a float's powers of two)
+              const int by = e & 1 ? by2[e / 2] >> 16 : (int)(int16_t)by2[e / 2], half = by >> 1;
+              o[e] = __float_as_uint(__uint_as_float(o[e]) * __uint_as_float((uint32_t)(127 + half) << 23) * __uint_as_float((uint32_t)(127 + by - half) << 23));
+            }
+            TmemSt<8>::run(tS + 8 * c, o);
+          }
+          tc_wait_st();
+        }
+        float top = NONE;
 #pragma unroll 1
         for (int c = 2; c >= 0; c -= 2) {
           float ma, mb;
@@ -603,7 +596,6 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
           tc_wait_ld();
           if (masked) { ma = mask32(ra, c ? seen[2] : seen[0]); mb = mask32(rb, c ? seen[3] : seen[1]); }
           top = fmaxf(top, fmaxf(ma, mb));
-        }
         }
         const float x = top * cq;
         float alpha = 1.f;
@@ -660,16 +652,19 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
             tc_fence_after();
           }
         }
-        if (CF == CF_MX && (wide || far)) {              // (rare: block after block, read again)
+        if (CF == CF_MX && wide) {                       // (rare: block after block, read again)
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            far32(c);
+            tmem_ld_cols<32>(tS + 32 * c, ra);
+            tc_wait_ld();
+            if (masked) mask32(ra, c == 0 ? seen[0] : c == 1 ? seen[1] : c == 2 ? seen[2] : seen[3]);
             const bool w = fl[8 + c] != 0;
             weigh(ra, c, [&](float a, float bb) { return w ? cvt_bf16x2(a, bb) : cvt_f16x2(a, bb); });
           }
         } else {
           auto f16 = [](float a, float bb) { return cvt_f16x2(a, bb); };
-#pragma unroll (CF == CF_MX ? 1 : 2)      // (as a loop E2M1 1156 TFLOP/s instead of 1136, NVFP4 1402 instead of 1564)
+          // (as a loop NVFP4 1402 TFLOP/s instead of 1564, E2M1 1309 instead of 1354, but with 64 dims 714 instead of 678)
+#pragma unroll (CF == CF_MX && D == 64 ? 1 : 2)
           for (int c = 0; c < 4; c += 2) {
             if (c > 0) {
               tc_wait_ld();
@@ -687,7 +682,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
           }
         }
         if constexpr (C::APART && CF == CF_MX) {
-          if (wide || far) {
+          if (wide) {
             tc_fence_before();
             __syncwarp();
             mbar_arrive_elect(s_free + rt);
