@@ -554,8 +554,8 @@ int fsa_attention_cache_window(const fsa_cache_attn* args, int window, int sinks
  * into 16-bit operands once for each 256.  Scores are sums of exact products in fp32, sums and
  * maxima fp32; q goes as f16, exact down to 2^-18 of its row's largest magnitude and off by at
  * most 2^-29 of that below.  Probabilities are rounded to f16 for the product with V
- * (2^-11 of each, or an absolute 2^-32 of the largest value for small ones); with E2M1, where V's block scales in a tile of
- * 128 keys leave 2^-23 .. 2^13, to bf16 (2^-8).  E2M1 keys up to 2^115, values up to 2^100;
+ * (2^-11 of each, or an absolute 2^-32 of the largest value for small ones); with E2M1, where V's block scales in
+ * a tile's 32 keys (seen by the row or not) leave 2^-23 .. 2^13, to bf16 (2^-8) for these keys.  E2M1 keys up to 2^115, values up to 2^100;
  * blocks of a key below 2^-36 of its largest lose bits, as do keys below 2^-100 and values below 2^-126.
  * |scale| times a row's largest sum of |q k| below 2^26: beyond, where a score's rounding in fp32 is more
  * than the softmax's distances, the row may be NaN or zeros.

@@ -73,7 +73,7 @@ struct Cfg {
   static constexpr int SMEM = OFF_SHIFT + (CF == CF_MX ? 4 * KEYS * 2 : 0) + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   // tensor memory: + 128 (S), + D (O), + P_STEP (P) for the second row tile.  With D 64 P has columns of its own, and the next
-  // tile's scores are computed while this one's softmax runs (NVFP4 882 TFLOP/s instead of 818, E2M1 734 instead of 743);
+  // tile's scores are computed while this one's softmax runs (NVFP4 882 TFLOP/s instead of 818, E2M1 714 instead of 706);
   // with D 128 it lies over the scores, for want of columns.
   static constexpr bool APART = D == 64;
   static constexpr uint32_t T_S = 0, T_O = 256, T_P = APART ? 384 : 0, P_STEP = APART ? 64 : 128;
@@ -413,9 +413,11 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
   uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
-  uint64_t* const raw_full = bars;             // [RAW] codes have landed
-  uint64_t* const raw_empty = bars + RAW;      // [RAW] and been read (2 warps)
-  uint64_t* const k_full = bars + 2 * RAW;     // [2] operand written (4 warps)
+  // A stage takes halves of tiles in turn, read by warps 8, 9 and by 10, 11.  Either pair has barriers of its own for them, and
+  // so sees every phase: by one that both use, a pair ahead of a copy for the other would take that one's phase for its own.
+  uint64_t* const raw_full = bars;             // [2][RAW] codes have landed
+  uint64_t* const raw_empty = bars + 2 * RAW;  // [RAW] and been read (2 warps)
+  uint64_t* const k_full = bars + 3 * RAW;     // [2] operand written (4 warps)
   uint64_t* const k_empty = k_full + 2;        // [2] and multiplied
   uint64_t* const v_full = k_full + 4;
   uint64_t* const v_empty = k_full + 6;
@@ -436,7 +438,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
 
   griddep_launch();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < RAW; ++i) { mbar_init(raw_full + i, 1); mbar_init(raw_empty + i, 2); }
+    for (int i = 0; i < RAW; ++i) { mbar_init(raw_full + i, 1); mbar_init(raw_full + RAW + i, 1); mbar_init(raw_empty + i, 2); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(k_full + i, 4); mbar_init(k_empty + i, 1);
       mbar_init(v_full + i, 4); mbar_init(v_empty + i, 1);
@@ -487,8 +489,8 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
 
   if (warp < 8) {
     // ============================================================ softmax, a row a thread
-    // (8 warps of 176, 4 of 96, 4 of 64: the launch's 16 of 128.  184 and 96 and 48: NVFP4 2% more, E2M1 4% less; 168, 104, 72:
-    // NVFP4 4% less)
+    // (8 warps of 176, 4 of 96, 4 of 64: the launch's 16 of 128.  184, 96, 48: NVFP4 2% more, E2M1 2% less; 168, 104, 72: NVFP4 4%
+    // less, E2M1 2% more)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     const int rt = warp >> 2, rl = threadIdx.x & 127;
     const uint32_t tl = tbase + ((uint32_t)(32 * (warp & 3)) << 16);
@@ -783,8 +785,8 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
     Piece pc;
     while (ok && next_piece(p, walk, sh, pc)) {
       for (int t = pc.t0; t < pc.t1; ++t, ++n) {
-        const uint32_t half = 2 * n + (dw >> 1), rs = half % RAW, kb = n & 1;
-        ok = wait(raw_full + rs, (half / RAW) & 1) && (n < 2 || wait(k_empty + kb, (n / 2 - 1) & 1));
+        const uint32_t pair = dw >> 1, rs = (2 * n + pair) % RAW, kb = n & 1;
+        ok = wait(raw_full + RAW * pair + rs, (n / RAW) & 1) && (n < 2 || wait(k_empty + kb, (n / 2 - 1) & 1));
         if (!ok) break;
         const int grp = 2 * (dw & 1) + (lane >> 4);      // of the stage's four
         const bool gone = (absent[rs] >> grp & 1) || pc.at(t) * KEYS + row >= pc.kmax;
@@ -889,26 +891,27 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
           const uint32_t here = __ballot_sync(0xFFFFFFFFu, page >= 0);
           for (int x = 0; ok && x < 2 * min(4, w.t1 - t); ++x, ++n) {
             const uint32_t rs = n % RAW;
+            uint64_t* const full = raw_full + RAW * (n & 1) + rs;
             ok = n < RAW || __all_sync(0xFFFFFFFFu, mbar_wait(raw_empty + rs, (n / RAW - 1) & 1, ac));
             if (!ok) break;
             const uint32_t four = here >> (4 * x) & 15u;
             if (lane == 0) {
               absent[rs] = four ^ 15u;
-              mbar_expect_tx(raw_full + rs, __popc(four) * Gr::BYTES);
+              mbar_expect_tx(full, __popc(four) * Gr::BYTES);
             }
             __syncwarp();
             if ((lane >> 2) == x && page >= 0) {
               const int pos = w.at(t + (lane >> 3)) * KEYS + 16 * (lane & 7);
               const int inside = (pos & ((1 << p.c.page_shift) - 1)) / 16;
               bulk_load(sm + C::OFF_RAW + rs * C::STAGE + (lane & 3) * Gr::BYTES, head + page * p.c.page_bytes + inside * Gr::BYTES,
-                        Gr::BYTES, raw_full + rs);
+                        Gr::BYTES, full);
             }
             __syncwarp();
           }
         }
       }
       // the copies in flight end before the CTA does
-      for (uint32_t x = n > RAW ? n - RAW : 0; x < n; ++x) mbar_drain(raw_full + x % RAW, (x / RAW) & 1, ac);
+      for (uint32_t x = n > RAW ? n - RAW : 0; x < n; ++x) mbar_drain(raw_full + RAW * (x & 1) + x % RAW, (x / (2 * RAW)) & 1, ac);
     } else if (warp == 13) {
       // ========================================================== products
       auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xFFFFFFFFu, mbar_wait<false>(bar, parity, ac)); };
