@@ -28,9 +28,9 @@
 //   - A row that sees a token whose values are not finite (the scale's NaN) is NaN as a whole; the others
 //     are as without it (its V is zero in the operand, and a bit tells the rows).
 //
-// Measured (one GB300, cuBLAS at 1943 TFLOP/s in bf16): 2048 tokens over 128K keys, 32/8 heads of 128: NVFP4 1600
-// TFLOP/s (2.73 ms), E2M1 1339 (3.26); heads of 64: 942 (2.32) and 714 (3.05).  Eight sequences of 8192 keys,
-// 64 tokens each, NVFP4: 74 us, where fsa_attention_cache takes 321.
+// Measured (one GB300, cuBLAS at 1943 TFLOP/s in bf16): 2048 tokens over 128K keys, 32/8 heads of 128: NVFP4 1590
+// TFLOP/s (2.74 ms), E2M1 1394 (3.13); heads of 64: 942 (2.32) and 701 (3.11).  Eight sequences of 8192 keys,
+// 64 tokens each, NVFP4: 73 us, where fsa_attention_cache takes 321.
 // What bounds it: of the about 3100 cycles of a tile of 128 dims (NVFP4) its products take 2050 at the nominal rate; a row
 // tile's chain, its scores, their maximum (800 cycles), exponentials (1050), products, is as long, and the two row tiles'
 // chains cover each other but for their ends.  The operand warps work 2100 of these cycles.  E2M1 is slower by what tells
@@ -1119,8 +1119,8 @@ cudaError_t launch(const CacheAttnArgs& a, int sms, cudaStream_t st) {
 int cache_chunk_blocks(int rows) { return (rows + ROWS - 1) / ROWS; }
 
 // Segments of at most 4 tiles are not shared: a CTA each, no second kernel (64 tokens over 512 keys, NVFP4, in tables
-// of 512 and of 576 tokens, which are shared: 4 sequences 18.0 and 25.0 us, 32 34 and 52, 64 67 and 82; 256 of 256 keys
-// 178 and 206).
+// of 512 and of 576 tokens, which are shared: 4 sequences 18 and 25 us, 32 34 and 52, 64 67 and 82; 256 of 256 keys
+// 180 and 207).
 bool cache_chunk_whole(const Cache& c, int max_pages) { return ((int64_t)max_pages << c.page_shift) <= 4 * KEYS; }
 
 // parts of the CTAs, two each; where segments begin that go on
