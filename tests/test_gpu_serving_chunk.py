@@ -281,6 +281,28 @@ def test_workspace_streams_and_graph():
         assert torch.equal(out, fsa.fsa_attention_chunk(q, cache, table, lens, q_lens=q_lens))
 
 
+@pytest.mark.parametrize("fmt,D", [("NVFP4", 64), ("E2M1", 128)])
+def test_the_same_bits_beside_other_traffic(fmt, D):
+    """Many runs with cold caches and memory busy beside them, so that copies come late and out of turn."""
+    fsa = _fsa()
+    g = gen(83)
+    lens = [9000, 700]
+    cache, table, _, _ = filled_cache(fsa, g, lens, 64, 4, D, fmt)
+    q, status = normal(g, 2, 150, 16, D), i32([0])
+    first, _ = run(fsa, q, cache, table, lens, status=status)
+    other, side = torch.zeros(32 << 20, device="cuda"), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out, bad = torch.empty_like(first), torch.zeros(1, device="cuda")
+    for i in range(400):
+        if i % 4 == 0:
+            with torch.cuda.stream(side):
+                other.add_(1.0)
+        fsa.fsa_attention_chunk(q, cache, table, i32(lens), out=out, status=status)
+        bad += (out != first).any()
+    torch.cuda.synchronize()
+    assert int(bad) == 0 and int(status) == 0
+
+
 def test_as_the_decode_call():
     """The same attention as fsa_attention_cache, to both calls' rounding (bf16 2^-8, f16 2^-10 of each weight)."""
     fsa = _fsa()
