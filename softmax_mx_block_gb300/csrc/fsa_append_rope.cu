@@ -18,8 +18,7 @@
 // To move: 4 H + 4 Hkv + 2 Hkv (0.53 or 0.56) bytes a token and dim.  A block has the queries of a few
 // tokens or the keys and values of a few: the sines of a token are computed once a block, for the rows of q (D/16
 // lanes each, both elements of a pair in a lane) or of k (D/8 lanes, 8 consecutive elements a lane, as the
-// quantisation wants them; a pair's other element comes from another lane).  (All heads of a token in one
-// block: 120 us instead of 99 for 16384 tokens; the keys' lanes waited for the queries'.)
+// quantisation wants them; a pair's other element comes from another lane).
 //
 // Measured (one GB300, calls in a graph, 32+8 heads of 128, NVFP4, against fsa_qk_norm_rope and fsa_cache_append in
 // turn): 64 tokens 5.7 us (5.8), 512 8.0 (9.4), 2048 17.2 (15.5), 16384 96 (76), where memory takes 52.  From about a
