@@ -96,6 +96,7 @@ struct Span {
   __device__ __forceinline__ int units() const { return tiles ? tiles + EXTRA : 0; }
   __device__ __forceinline__ int key_tiles() const { return (kmax + TILE - 1) / TILE; }
   __device__ __forceinline__ int at(int t) const { return t; }
+  __device__ __forceinline__ bool some_see(const CacheAttnArgs&, int) const { return true; }
 };
 // With a window: a segment's tiles are those of the first keys (`sinks` of them), then those that
 // some column's window reaches, beginning with the ones that lie in all windows: all tiles that
@@ -108,6 +109,8 @@ struct SpanWindow : Span {
     const int x = t - lead + u0;
     return t < lead ? t : x < end ? x : x - end + w0;
   }
+  // whether some column sees a key of pos .. pos + 15, if these are keys: other pages may be anyone's
+  __device__ __forceinline__ bool some_see(const CacheAttnArgs& p, int pos) const { return pos < p.sinks || pos + 16 > low; }
 };
 template <bool WIN> struct SpanOf { using type = Span; };
 template <> struct SpanOf<true> { using type = SpanWindow; };
@@ -338,7 +341,7 @@ struct TileScales {
 
 // NG groups of 16 keys of a tile, from group g0 on, in shared memory.  sc: the tile's unpacked
 // scales; vs: V's scale bytes of this lane's token (0 for a token that no column sees);
-// first: position of the tile's first key; bad: groups without a page.  MASK 1: some column
+// first: position of the tile's first key; bad: groups that are not there (no page, or no column sees them).  MASK 1: some column
 // does not see some key, but those with rows see the same ones; 2: they do not, and each has an
 // offset of its own.
 template <int D, int CF, int NT, int NG, int MASK, bool WIN>
@@ -687,19 +690,22 @@ __device__ __forceinline__ bool run_piece(const CacheAttnArgs& p, const typename
   const uint8_t* const head = p.c.pages + ((int64_t)hkv << (p.c.page_shift - 4)) * Gr::BYTES;
   const int32_t* const row = p.table + (int64_t)b * p.max_pages;
   int batch = 0, page0 = 0, page1 = 0;
-  uint32_t bad0 = 0, bad1 = 0, bads = 0;              // tiles of the batch, and (2 bits each) stages, with groups without a page
+  uint32_t bad0 = 0, bad1 = 0, bads = 0;              // tiles of the batch, and (2 bits each) stages, with groups that are not there
   auto look_up = [&](int first) {
     batch = first;
     const int pos = sp.at(first + lane) * TILE;
     const bool in0 = first + lane < tend, in1 = in0 && pos + 16 < sp.kmax;
     const int i0 = pos >> p.c.page_shift, i1 = (pos + 16) >> p.c.page_shift;
-    page0 = in0 ? row[i0] : -1;
-    page1 = !in1 ? -1 : i1 == i0 ? page0 : row[i1];
+    const bool see0 = in0 && sp.some_see(p, pos), see1 = in1 && sp.some_see(p, pos + 16);
+    page0 = see0 ? row[i0] : -1;
+    page1 = !see1 ? -1 : i1 == i0 && see0 ? page0 : row[i1];
     if ((uint32_t)page0 >= (uint32_t)p.c.num_pages) page0 = -1;
     if ((uint32_t)page1 >= (uint32_t)p.c.num_pages) page1 = -1;
     bad0 = __ballot_sync(0xFFFFFFFFu, in0 && page0 < 0);
     bad1 = __ballot_sync(0xFFFFFFFFu, in1 && page1 < 0);
-    if ((bad0 | bad1) && lane == 0 && p.status) atomicExch(p.status, -1);    // FSA_ERR_INVALID_ARG
+    bool wrong = bad0 | bad1;
+    if constexpr (WIN) wrong = wrong && __any_sync(0xFFFFFFFFu, (see0 && page0 < 0) || (see1 && page1 < 0));
+    if (wrong && lane == 0 && p.status) atomicExch(p.status, -1);    // FSA_ERR_INVALID_ARG
   };
   auto issue = [&](int tl) {
     const int s = r.in, at = tl - batch, k0 = sp.at(tl) * TILE;
