@@ -84,6 +84,7 @@ struct Cfg {
 struct Span {
   int qlen, len, kmax;      // rows' tokens, keys, keys that some row of the block sees
   int rows;                 // of the block
+  int low;                  // the first key of the first row's window
   int lead, w0, tiles;      // tiles of the first keys, first tile of some window, tiles in all
 };
 // virtual sequence vb = b * p.CT + block of rows
@@ -93,12 +94,13 @@ __device__ __forceinline__ Span span_of(const CacheAttnArgs& p, int vb) {
   s.qlen = p.q_lens ? min(max(p.q_lens[b], 0), p.Sq) : p.Sq;
   s.len = (int)min((int64_t)max(p.lens[b], 0), (int64_t)p.max_pages << p.c.page_shift);
   s.rows = min(ROWS, s.qlen * p.G - r0);
-  s.kmax = s.lead = s.w0 = s.tiles = 0;
+  s.kmax = s.low = s.lead = s.w0 = s.tiles = 0;
   if (s.rows <= 0) return s;
   s.kmax = p.causal ? max(0, s.len - s.qlen + (r0 + s.rows - 1) / p.G + 1) : s.len;
   const int end = (s.kmax + KEYS - 1) / KEYS;
   if (p.window) {
-    s.w0 = min(max(0, s.len - s.qlen + r0 / p.G + 1 - p.window) / KEYS, end);
+    s.low = max(0, s.len - s.qlen + r0 / p.G + 1 - p.window);
+    s.w0 = min(s.low / KEYS, end);
     s.lead = min((p.sinks + KEYS - 1) / KEYS, s.w0);
   }
   s.tiles = s.lead + end - s.w0;
@@ -172,7 +174,7 @@ struct Walk {
 static_assert(sizeof(Walk) <= 80, "");
 // A warp's next piece.  The walk itself waits in shared memory, out of the registers.
 struct Piece {
-  int vb, hkv, t0, t1, lead, w0, rows, kmax, qlen, len, last;     // last: the CTA that has the segment's end
+  int vb, hkv, t0, t1, low, lead, w0, rows, kmax, qlen, len, last;     // last: the CTA that has the segment's end
   bool begins, ends;
   __device__ __forceinline__ int at(int t) const { return t < lead ? t : t - lead + w0; }
 };
@@ -182,7 +184,7 @@ __device__ __forceinline__ bool next_piece(const CacheAttnArgs& p, Walk* slot, c
   if (!w.next(p)) return false;
   __syncwarp();
   if ((threadIdx.x & 31) == 0) *slot = w;
-  c = {w.vb, w.hkv, w.t0, w.t1, w.sp.lead, w.sp.w0, w.sp.rows, w.sp.kmax, w.sp.qlen, w.sp.len, p.whole ? 0 : sh.of(w.lo + w.rest - 1), w.t0 == 0, w.t1 == w.sp.tiles};
+  c = {w.vb, w.hkv, w.t0, w.t1, w.sp.low, w.sp.lead, w.sp.w0, w.sp.rows, w.sp.kmax, w.sp.qlen, w.sp.len, p.whole ? 0 : sh.of(w.lo + w.rest - 1), w.t0 == 0, w.t1 == w.sp.tiles};
   return true;
 }
 
@@ -789,7 +791,9 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
         ok = wait(raw_full + RAW * pair + rs, (n / RAW) & 1) && (n < 2 || wait(k_empty + kb, (n / 2 - 1) & 1));
         if (!ok) break;
         const int grp = 2 * (dw & 1) + (lane >> 4);      // of the stage's four
-        const bool gone = (absent[rs] >> grp & 1) || pc.at(t) * KEYS + row >= pc.kmax;
+        const int key = pc.at(t) * KEYS + row;
+        bool gone = (absent[rs] >> grp & 1) || key >= pc.kmax;
+        if (p.window) gone = gone || (key < pc.low && key >= p.sinks);       // (no row of the block sees it)
         const uint8_t* const base = sm + C::OFF_RAW + rs * C::STAGE + grp * Gr::BYTES;
         uint32_t ks[2] = {0u, 0u}, vs[2] = {0u, 0u};
         const uint8_t *kp = base + Gr::KS + (lane & 15) * Gr::SB, *vp = base + Gr::VS + (lane & 15) * Gr::SB;
@@ -871,11 +875,11 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
         const int b = w.vb / p.CT;
         const uint8_t* const head = p.c.pages + ((int64_t)w.hkv << (p.c.page_shift - 4)) * Gr::BYTES;
         const int32_t* const table = p.table + (int64_t)b * p.max_pages;
-        // the page of lane's group of tiles t .. t + 3 (-1: none)
+        // the page of lane's group of tiles t .. t + 3 (-1: none, or no row sees any of its keys)
         auto look_up = [&](int t) {
           const int v = t + (lane >> 3), pos = w.at(v) * KEYS + 16 * (lane & 7);
           int page = -1;
-          if (v < w.t1 && pos < w.kmax) {
+          if (v < w.t1 && pos < w.kmax && (pos < p.sinks || pos + 16 > w.low)) {
             page = table[pos >> p.c.page_shift];
             if ((uint32_t)page >= (uint32_t)p.c.num_pages) {
               page = -1;

@@ -1,4 +1,5 @@
-"""Keys that no row sees, before a window and behind the first tokens: their pages are not looked up and change no bit."""
+"""Keys that no row sees, before a window and behind the first tokens: their pages are not looked up, and neither these
+nor their tokens change a bit."""
 import pytest
 
 from test_gpu_serving import _fsa, filled_cache, gen, i32, normal
@@ -61,3 +62,32 @@ def check_pages(call, shapes, page, fmt, D):
 def test_pages_of_few_rows(fmt, D, page):
     """One row and several, in one block of rows and in three."""
     check_pages(_fsa().fsa_attention_cache, [(1, 4), (5, 1), (9, 4)], page, fmt, D)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64])
+@pytest.mark.parametrize("fmt,D", [("E2M1", 128), ("NVFP4", 64)])
+def test_pages_of_chunks(fmt, D, page):
+    """Rows of one block, of two tiles, and of three blocks."""
+    check_pages(_fsa().fsa_attention_chunk, [(5, 4), (40, 4), (150, 4)], page, fmt, D)
+
+
+@pytest.mark.parametrize("name", ["fsa_attention_cache", "fsa_attention_chunk"])
+@pytest.mark.parametrize("fmt", ["E2M1", "NVFP4"])
+def test_tokens_beside_the_seen_ones(fmt, name):
+    """Tokens that no row sees, on the pages of seen ones: far scales, zeros, NaN."""
+    fsa = _fsa()
+    call, g, page, D = getattr(fsa, name), gen(5), 64, 128
+    cache, table, k, v = filled_cache(fsa, g, LENS, page, 2, D, fmt)
+    for Sq in (1, 6):
+        q = normal(g, len(LENS), Sq, 4, D)
+        for window, sinks in WINDOWS:
+            fsa.fsa_cache_append(cache, k, v, table, i32(LENS), i32(LENS))
+            want = call(q, cache, table, i32(LENS), window=window, sinks=sinks)
+            for what in (2.0 ** 60, 2.0 ** -40, 0.0, float("nan")):
+                k2, v2 = k.clone(), v.clone()
+                for b, n in enumerate(LENS):
+                    part = slice(*unseen(n, Sq, window, sinks))
+                    k2[b, part] *= what
+                    v2[b, part] *= what
+                fsa.fsa_cache_append(cache, k2, v2, table, i32(LENS), i32(LENS))
+                assert torch.equal(want, call(q, cache, table, i32(LENS), window=window, sinks=sinks)), (Sq, window, sinks, what)
