@@ -555,8 +555,9 @@ int fsa_attention_cache_window(const fsa_cache_attn* args, int window, int sinks
  * maxima fp32; q goes as f16, exact down to 2^-18 of its row's largest magnitude and off by at
  * most 2^-29 of that below.  Probabilities are rounded to f16 for the product with V
  * (2^-11 of each, or an absolute 2^-32 of the largest value for small ones); with E2M1, where V's block scales in
- * a tile's 32 keys (seen by the row or not) leave 2^-23 .. 2^13, to bf16 (2^-8) for these keys.  E2M1 keys up to 2^115, values up to 2^100;
- * blocks of a key below 2^-36 of its largest lose bits, as do keys below 2^-100 and values below 2^-126.
+ * a tile's 32 keys (seen by the row or not) leave 2^-23 .. 2^13, to bf16 (2^-8) for these keys (a block of zeros has no such scale).  E2M1 keys up to
+ * 2^115, values up to 2^100; blocks of a key below 2^-36 of its largest lose bits, as do keys below 2^-100 and values below
+ * 2^-126; a block of values that are all below 2^-124 counts as zeros.
  * |scale| times a row's largest sum of |q k| below 2^26: beyond, where a score's rounding in fp32 is more
  * than the softmax's distances, the row may be NaN or zeros.
  * A row that sees a token with a non-finite key or value is NaN as a whole, and so is a row of

@@ -276,9 +276,8 @@ __device__ __forceinline__ uint32_t scaled_bf16(uint32_t f16x2, float f) {
   asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}" : "=f"(lo), "=f"(hi) : "r"(f16x2));
   return cvt_bf16x2(lo * f, hi * f);
 }
-__device__ __forceinline__ float e8m0_f32(uint32_t byte) { return __uint_as_float(byte ? byte << 23 : 1u << 22); }
 // A row of V.  Word 2g + y (D 64: g) holds elements 64y + 2g, + 1, and 16, 32 and 48 on.  A scale that is NaN
-// counts as zero.
+// counts as zero, and so does the least E8M0 one, a block of zeros' (2^-127: of values below 2^-124).
 template <int D, int CF>
 __device__ __forceinline__ void put_value(uint8_t* dst, int row, const Row<D>& src, const uint32_t (&sb)[2], bool gone) {
   constexpr int SB = CacheGroup<D, CF>::SB;
@@ -286,7 +285,7 @@ __device__ __forceinline__ void put_value(uint8_t* dst, int row, const Row<D>& s
 #pragma unroll
   for (int i = 0; i < SB; ++i) {
     const uint32_t byte = byte_of(sb, i);
-    const bool none = gone || (CF == CF_MX ? byte == 0xFFu : (byte & 0x7Fu) == 0x7Fu);
+    const bool none = gone || (CF == CF_MX ? byte == 0xFFu || byte == 0u : (byte & 0x7Fu) == 0x7Fu);
     f[i] = none ? 0u : CF == CF_MX ? e8m0_f16(byte) : e4m3_f16(byte);
   }
   put_row<D>(dst, row, src, [&](uint32_t w, int x, uint32_t (&o)[4]) {
@@ -296,7 +295,7 @@ __device__ __forceinline__ void put_value(uint8_t* dst, int row, const Row<D>& s
     for (int e = 0; e < 4; ++e) o[e] = hmul2(o[e], CF == CF_MX ? f[2 * y + e / 2] : f[4 * y + e]);
   });
 }
-// The same as bf16, with any E8M0 scale.
+// The same as bf16, with any E8M0 scale (byte << 23 is 0 for the least).
 template <int D>
 __device__ __forceinline__ void put_value_far(uint8_t* dst, int row, const uint8_t* src, uint32_t sb, bool gone) {
 #pragma unroll 1
@@ -307,7 +306,7 @@ __device__ __forceinline__ void put_value_far(uint8_t* dst, int row, const uint8
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const uint32_t byte = sb >> (8 * (2 * y + e / 2)) & 0xFFu;
-      o[e] = scaled_bf16(o[e], gone || byte == 0xFFu ? 0.f : e8m0_f32(byte));
+      o[e] = scaled_bf16(o[e], gone || byte == 0xFFu ? 0.f : __uint_as_float(byte << 23));
     }
     put_piece(dst + row * 128, row, i, o);
   }
@@ -807,16 +806,16 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
           ks[0] = *reinterpret_cast<const uint16_t*>(kp);
           vs[0] = *reinterpret_cast<const uint16_t*>(vp);
         }
-        bool nan = false, far = false, kfar = false;
+        bool nan = false, far = false, kfar = false;     // (the least scale is that of a block of zeros, and not far)
         uint32_t kmax = 0;
 #pragma unroll
         for (int i = 0; i < Gr::SB; ++i) {
           const uint32_t byte = byte_of(vs, i);
           nan |= CF == CF_MX ? byte == 0xFFu : (byte & 0x7Fu) == 0x7Fu;
-          far |= CF == CF_MX && byte != 0xFFu && (byte < LEAST_F16 || byte > MOST_F16);
+          far |= CF == CF_MX && byte != 0xFFu && byte != 0u && (byte < LEAST_F16 || byte > MOST_F16);
           if constexpr (CF == CF_MX) {
             const uint32_t k = byte_of(ks, i);
-            if (k != 0xFFu && k != 0u && !gone) {         // (the least scale is that of a block of zeros)
+            if (k != 0xFFu && k != 0u && !gone) {
               kfar |= k < LEAST_F16 || k > MOST_F16;
               kmax = max(kmax, k);
             }
