@@ -693,8 +693,10 @@ def fsa_attention_cache_workspace(cache: MxCache, B, H, Sq, max_pages, window=No
         _check(load().fsa_attention_cache_workspace(ctypes.byref(c), B, H, Sq, max_pages, ctypes.byref(n)),
                "fsa_attention_cache_workspace")
     else:
-        _check(load().fsa_attention_cache_window_workspace(ctypes.byref(c), B, H, Sq, max_pages, 0 if window is None else window,
-                                                           sinks, ctypes.byref(n)), "fsa_attention_cache_window_workspace")
+        # (ctypes would cut them to their low 32 bits; the call itself takes larger ones as the largest)
+        window, sinks = (max(-1, min(x, 2 ** 31 - 1)) for x in (0 if window is None else window, sinks))
+        _check(load().fsa_attention_cache_window_workspace(ctypes.byref(c), B, H, Sq, max_pages, window, sinks, ctypes.byref(n)),
+               "fsa_attention_cache_window_workspace")
     return n.value
 
 
