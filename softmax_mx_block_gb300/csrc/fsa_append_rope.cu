@@ -226,6 +226,53 @@ __device__ __forceinline__ void cos_sin64(double t, double& c, double& s) {
   if (quarter & 2) s = -s;
 }
 
+// A value as the sum of two floats, the second below half an ulp of the first.
+struct Two {
+  float h, l;
+};
+__device__ __forceinline__ Two sum2(float h, float l) {        // |h| >= |l|
+  const float s = h + l;
+  return {s, l - (s - h)};
+}
+__device__ __forceinline__ bool over(Two a, Two b) { return a.h > b.h || (a.h == b.h && a.l > b.l); }
+// n 2^-63
+__device__ __forceinline__ Two fraction63(uint64_t n) {
+  const float h = (float)n;                                      // (2^63 at most)
+  return {h * 0x1p-63f, (float)(int64_t)(n - (uint64_t)h) * 0x1p-63f};
+}
+
+// cos and sin of p * freq to 2^-42, in integers: freq / 2 pi with 96 fraction bits times p leaves the turn's 64;
+// quarter turns taken off, the rest times 2 pi is x <= pi / 4 with 63, and Taylor's series with x^2 as a
+// fraction of 64, term after term from below.
+__device__ __forceinline__ void cos_sin63(int p, double freq, Two& c, Two& s) {
+  const uint64_t bits = (uint64_t)__double_as_longlong(freq);
+  const uint64_t m = (bits & 0xFFFFFFFFFFFFFull) | 0x10000000000000ull;
+  const int down = 1075 - 30 - (int)(bits >> 52 & 0x7FF);        // freq = m 2^(-30 - down)
+  const unsigned __int128 q = (unsigned __int128)m * 0xA2F9836E4E44152Aull;               // 2^66 / 2 pi
+  // (of a frequency of 2^23 and more whole turns are cut off on the left)
+  const unsigned __int128 turn96 = down >= 128 || down <= -128 ? 0 : down >= 0 ? q >> down : q << -down;
+  const uint64_t turn = (uint64_t)((turn96 * (p < 0 ? 0u - (uint32_t)p : (uint32_t)p)) >> 32);
+  const uint32_t quarter = (uint32_t)((turn + (1ull << 61)) >> 62);
+  const int64_t rest = (int64_t)(turn - ((uint64_t)quarter << 62));
+  const uint64_t x = __umul64hi((uint64_t)llabs(rest) * 4, 0xC90FDAA22168C235ull);          // pi / 4
+  const uint64_t z = __umul64hi(x, x) << 2;
+  constexpr uint64_t ONE = 1ull << 63;
+  uint64_t a = ONE / 39916800 - __umul64hi(ONE / 6227020800ull, z), b = ONE / 479001600 - __umul64hi(ONE / 87178291200ull, z);
+  a = ONE / 362880 - __umul64hi(a, z);  b = ONE / 3628800 - __umul64hi(b, z);
+  a = ONE / 5040 - __umul64hi(a, z);    b = ONE / 40320 - __umul64hi(b, z);
+  a = ONE / 120 - __umul64hi(a, z);     b = ONE / 720 - __umul64hi(b, z);
+  a = ONE / 6 - __umul64hi(a, z);       b = ONE / 24 - __umul64hi(b, z);
+  a = ONE - __umul64hi(a, z);           b = ONE / 2 - __umul64hi(b, z);
+  b = ONE - __umul64hi(b, z);
+  a = __umul64hi(a, x) << 1;
+  Two sn = fraction63(a), co = fraction63(b);
+  if (rest < 0) sn = {-sn.h, -sn.l};
+  c = quarter & 1 ? sn : co;
+  s = quarter & 1 ? co : sn;
+  if ((quarter & 3) == 1 || (quarter & 3) == 2) c = {-c.h, -c.l};
+  if (((quarter & 2) != 0) != ((p < 0) != (freq < 0.0))) s = {-s.h, -s.l};
+}
+
 // 1 / sqrt(x), whatever its size
 __device__ __noinline__ double rsqrt64(double x) { return 1.0 / sqrt(x); }
 
@@ -299,7 +346,16 @@ __device__ __noinline__ Codes close_codes64(const RopeArgs& a, uint4 own, uint4 
         if (a.wk) z *= (double)bf16_to_f32(a.wk[other]);
         const int axis = pair >= a.first2 ? 2 : pair >= a.first1 ? 1 : 0;
         double sn, c;
-        cos_sin64((double)(pos ? pos[axis] : place) * a.inv_freq[pair], c, sn);
+        const int p = pos ? pos[axis] : place;
+        const double t = (double)p * a.inv_freq[pair];
+        if (fabs(t) >= 0x1p51 && fabs(t) < INFINITY) {    // (in fp64 its part of a turn would be lost)
+          Two c2, s2;
+          cos_sin63(p, a.inv_freq[pair], c2, s2);
+          c = (double)c2.h + c2.l;
+          sn = (double)s2.h + s2.l;
+        } else {
+          cos_sin64(t, c, sn);
+        }
         y = ::fma(z, second ? sn : -sn, y * c);
       }
       y *= rr;
@@ -328,52 +384,6 @@ __device__ __noinline__ Codes close_codes64(const RopeArgs& a, uint4 own, uint4 
     }
   }
   return r;
-}
-
-// A value as the sum of two floats, the second below half an ulp of the first.
-struct Two {
-  float h, l;
-};
-__device__ __forceinline__ Two sum2(float h, float l) {        // |h| >= |l|
-  const float s = h + l;
-  return {s, l - (s - h)};
-}
-__device__ __forceinline__ bool over(Two a, Two b) { return a.h > b.h || (a.h == b.h && a.l > b.l); }
-// n 2^-63
-__device__ __forceinline__ Two fraction63(uint64_t n) {
-  const float h = (float)n;                                      // (2^63 at most)
-  return {h * 0x1p-63f, (float)(int64_t)(n - (uint64_t)h) * 0x1p-63f};
-}
-
-// cos and sin of p * freq to 2^-42, in integers: freq / 2 pi with 96 fraction bits times p leaves the turn's 64;
-// quarter turns taken off, the rest times 2 pi is x <= pi / 4 with 63, and Taylor's series with x^2 as a
-// fraction of 64, term after term from below.
-__device__ __forceinline__ void cos_sin63(int p, double freq, Two& c, Two& s) {
-  const uint64_t bits = (uint64_t)__double_as_longlong(freq);
-  const uint64_t m = (bits & 0xFFFFFFFFFFFFFull) | 0x10000000000000ull;
-  const int down = 1075 - 30 - (int)(bits >> 52 & 0x7FF);        // freq = m 2^(-30 - down)
-  const unsigned __int128 q = (unsigned __int128)m * 0xA2F9836E4E44152Aull;               // 2^66 / 2 pi
-  const unsigned __int128 turn96 = down >= 128 ? 0 : q >> max(down, 0);
-  const uint64_t turn = (uint64_t)((turn96 * (p < 0 ? 0u - (uint32_t)p : (uint32_t)p)) >> 32);
-  const uint32_t quarter = (uint32_t)((turn + (1ull << 61)) >> 62);
-  const int64_t rest = (int64_t)(turn - ((uint64_t)quarter << 62));
-  const uint64_t x = __umul64hi((uint64_t)llabs(rest) * 4, 0xC90FDAA22168C235ull);          // pi / 4
-  const uint64_t z = __umul64hi(x, x) << 2;
-  constexpr uint64_t ONE = 1ull << 63;
-  uint64_t a = ONE / 39916800 - __umul64hi(ONE / 6227020800ull, z), b = ONE / 479001600 - __umul64hi(ONE / 87178291200ull, z);
-  a = ONE / 362880 - __umul64hi(a, z);  b = ONE / 3628800 - __umul64hi(b, z);
-  a = ONE / 5040 - __umul64hi(a, z);    b = ONE / 40320 - __umul64hi(b, z);
-  a = ONE / 120 - __umul64hi(a, z);     b = ONE / 720 - __umul64hi(b, z);
-  a = ONE / 6 - __umul64hi(a, z);       b = ONE / 24 - __umul64hi(b, z);
-  a = ONE - __umul64hi(a, z);           b = ONE / 2 - __umul64hi(b, z);
-  b = ONE - __umul64hi(b, z);
-  a = __umul64hi(a, x) << 1;
-  Two sn = fraction63(a), co = fraction63(b);
-  if (rest < 0) sn = {-sn.h, -sn.l};
-  c = quarter & 1 ? sn : co;
-  s = quarter & 1 ? co : sn;
-  if ((quarter & 3) == 1 || (quarter & 3) == 2) c = {-c.h, -c.l};
-  if (((quarter & 2) != 0) != ((p < 0) != (freq < 0.0))) s = {-s.h, -s.l};
 }
 
 // The open ones of a lane's eight again, for rows of ordinary size, in pairs of floats (about 2^-43 of a row's largest
