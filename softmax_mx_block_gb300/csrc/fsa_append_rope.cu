@@ -134,6 +134,11 @@ __device__ __forceinline__ uint4 others_of(uint4 x, int half, int row, int l) {
   }
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 __device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
 
 // What the fp32 values of a lane's eight say of their codes.
@@ -506,17 +511,18 @@ __device__ __forceinline__ void put_key(const AppendRopeArgs& p, const Lane8& f,
   float t[8], ss, s1;
 #pragma unroll
   for (int i = 0; i < 4; ++i) split(y[i], t[2 * i], t[2 * i + 1]);
-  const float own_top = fmaxf(fmaxf(fmaxf(fabsf(t[0]), fabsf(t[1])), fmaxf(fabsf(t[2]), fabsf(t[3]))),
-                    fmaxf(fmaxf(fabsf(t[4]), fabsf(t[5])), fmaxf(fabsf(t[6]), fabsf(t[7]))));
+  // (maxima that keep NaN, of an element, a weight or an angle: the row is not sure then)
+  const float own_top = max_nan(max_nan(max_nan(fabsf(t[0]), fabsf(t[1])), max_nan(fabsf(t[2]), fabsf(t[3]))),
+                                max_nan(max_nan(fabsf(t[4]), fabsf(t[5])), max_nan(fabsf(t[6]), fabsf(t[7]))));
   float top = own_top;
 #pragma unroll
-  for (int m = 1; m < PER; m *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));          // the block's
+  for (int m = 1; m < PER; m *= 2) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));          // the block's
   float most = top;
 #pragma unroll
-  for (int m = PER; m < LK; m *= 2) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, m));      // the row's
+  for (int m = PER; m < LK; m *= 2) most = max_nan(most, __shfl_xor_sync(0xFFFFFFFFu, most, m));      // the row's
   float rs = 1.f;
   bool sure = true;
-  if (a.norm) {                                               // (with an element that is not finite: not sure)
+  if (a.norm) {
     split(add(add(sq[0], sq[1]), add(sq[2], sq[3])), ss, s1);
     ss += s1;
 #pragma unroll
@@ -528,14 +534,7 @@ __device__ __forceinline__ void put_key(const AppendRopeArgs& p, const Lane8& f,
   }
   sure = sure && most * rs < 0x1p120f && (most * rs > 0x1p-90f || most == 0.f);
   float d = most * SURE;
-  if (!a.norm) {
-    // (maxima drop NaN: an element that is not finite leaves its block open)
-    constexpr uint32_t MAG = 0x7FFF7FFFu;
-    const uint32_t big = __vmaxu2(__vimax3_u16x2(w[0] & MAG, w[1] & MAG, w[2] & MAG),
-                                  __vimax3_u16x2(w[3] & MAG, __vmaxu2(v[0] & MAG, v[1] & MAG), __vmaxu2(v[2] & MAG, v[3] & MAG)));
-    sure = sure && max(big & 0xFFFFu, big >> 16) < 0x7F80u;
-    if (f.exact) d = 0.f;
-  }
+  if (!a.norm && f.exact) d = 0.f;
   // a maximum of the block lies in tlo .. thi (some lanes' values may be exact, others not)
   float tlo = fmaxf(top - d, 0.f), thi = top + d;
   if (!a.norm) {

@@ -46,3 +46,40 @@ def test_frequencies_far_over_one(fmt, norm, power):
     # a scale is that of a maximum within the error
     least, most = ref.quantise((exact.abs() - off).clamp(min=0.0), fmt)[1], ref.quantise(exact.abs() + off, fmt)[1]
     assert bool(((ks >= least) & (ks <= most)).all())
+
+
+@pytest.mark.parametrize("fmt", ["E2M1", "NVFP4"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("D,half", [(128, 64), (64, 16), (128, 0)])
+def test_weights_and_frequencies_that_are_not_finite(fmt, interleaved, D, half):
+    """Blocks with an element that a weight or an angle makes NaN or infinite are NaN as a whole, and no others."""
+    fsa = _fsa()
+    g = gen(D + half)
+    S, Hkv = 37, 3
+    k = normal(g, 2, S, Hkv, D)
+    k[:, ::5, :, 3] = 0.0                               # (0 times infinity)
+    pos = (torch.arange(S, device="cuda", dtype=torch.int32) % 7)[None].repeat(2, 1).contiguous()
+    inf, nan = float("inf"), float("nan")
+    for at, what in ((3, nan), (3, inf), (D - 2, -inf), (None, nan), (None, inf)):
+        w, freq = 1 + 0.2 * normal(g, D), None
+        if half:
+            freq = 1.0e4 ** (-torch.arange(half, device="cuda", dtype=torch.float64) / half)
+        if at is not None:
+            w[at] = what
+        elif half:
+            freq[half // 2] = what
+        else:
+            continue
+        for norm in (True, False):
+            weight = w if norm else None
+            if at is not None and not norm:
+                continue
+            cache = fsa.empty_cache(6, 16, Hkv, D, fmt)
+            fsa.fsa_cache_append_rope(cache, normal(g, 2, S, Hkv, D), k, k, i32([[0, 1, 2], [3, 4, 5]]), i32([S, S]), pos=pos,
+                                      inv_freq=freq, k_weight=weight, norm=norm, interleaved=interleaved)
+            exact, _ = ref.norm_rope(k, weight, pos[..., None], freq, [half], norm, 1e-6, interleaved)
+            codes, scales = ref.quantise(exact, fmt)
+            kc, ks, _, _ = (x.unflatten(0, (2, 3)).flatten(1, 2)[:, :S] for x in ref.unpack_pages(cache.pages, 16, Hkv, D, fmt))
+            assert bool((scales == (255 if fmt == "E2M1" else 0x7F)).any())
+            assert torch.equal(ks, scales), (at, what, norm)
+            assert torch.equal(ref.values(kc, ks, fmt).nan_to_num(1e9), ref.values(codes, scales, fmt).nan_to_num(1e9)), (at, what, norm)
