@@ -285,7 +285,7 @@ __device__ __forceinline__ void put_value(uint8_t* dst, int row, const Row<D>& s
 #pragma unroll
   for (int i = 0; i < SB; ++i) {
     const uint32_t byte = byte_of(sb, i);
-    const bool none = gone || (CF == CF_MX ? byte == 0xFFu || byte == 0u : (byte & 0x7Fu) == 0x7Fu);
+    const bool none = gone || (CF == CF_MX ? byte - 1u >= 254u : (byte & 0x7Fu) == 0x7Fu);
     f[i] = none ? 0u : CF == CF_MX ? e8m0_f16(byte) : e4m3_f16(byte);
   }
   put_row<D>(dst, row, src, [&](uint32_t w, int x, uint32_t (&o)[4]) {
@@ -812,7 +812,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache_chunk_kernel(const CacheAttn
         for (int i = 0; i < Gr::SB; ++i) {
           const uint32_t byte = byte_of(vs, i);
           nan |= CF == CF_MX ? byte == 0xFFu : (byte & 0x7Fu) == 0x7Fu;
-          far |= CF == CF_MX && byte != 0xFFu && byte != 0u && (byte < LEAST_F16 || byte > MOST_F16);
+          far |= CF == CF_MX && byte - 1u < 254u && (byte < LEAST_F16 || byte > MOST_F16);
           if constexpr (CF == CF_MX) {
             const uint32_t k = byte_of(ks, i);
             if (k != 0xFFu && k != 0u && !gone) {
