@@ -468,6 +468,9 @@ int fsa_cache_append(const fsa_cache* cache, const void* k, const void* v, const
  * the cache as fsa_cache_append puts them.  k is rounded once, to 4 bits: its codes and scales
  * are those of the exact values, for positions up to 2^24 and |inv_freq| up to 1 (angles
  * pos * inv_freq rounded to 64 bits); beyond, of values within the error of fsa_qk_norm_rope.
+ * That is what it is for: from about a thousand new tokens on the two calls are the faster ones (16384 tokens
+ * of 32+8 heads of 128: 94 us, and 76 for the two), for some hundreds this one.  A call whose rows of k
+ * are all beyond 2^60, or not finite, takes 40 times as long.
  *   args: as fsa_qk_norm_rope, without k_out (NULL).  pos may be NULL with one axis: a token
  *     then turns by its place in its sequence, lens[b] - new_lens[b] + i.  q_out may be q, and
  *     must not overlap k or v.
@@ -491,8 +494,9 @@ int fsa_cache_read(const fsa_cache* cache, void* k, void* v, const fsa_strides* 
                    const int32_t* lens, const int32_t* start, int32_t* status, void* stream);
 
 /* Attention of few query rows over the cache (decode steps, guessed tokens; the cache is read
- * again for each 16 rows a kv head, so from about 60 on fsa_attention_chunk is faster, with 64
- * dims from about 80): O = softmax(scale Q K^T) V on the values the cache stands for; q is not
+ * again for each 16 rows a kv head, so from about 60 on, with 64 dims from about 80, fsa_attention_chunk is
+ * faster over many keys, eight sequences of 2048 or one of 32768; over fewer keys later: eight sequences of 500
+ * from 90, one from some hundreds): O = softmax(scale Q K^T) V on the values the cache stands for; q is not
  * quantised, sums and softmax statistics are fp32, probabilities times V's scales are
  * rounded to f16 before the product with the codes of V (2^-11 relative, 2^-10 with
  * NVFP4; for products far below the largest block scale in V that the row sees, an absolute
@@ -555,15 +559,16 @@ int fsa_attention_cache_window(const fsa_cache_attn* args, int window, int sinks
  * maxima fp32; q goes as f16, exact down to 2^-18 of its row's largest magnitude and off by at
  * most 2^-29 of that below.  Probabilities are rounded to f16 for the product with V
  * (2^-11 of each, or an absolute 2^-32 of the largest value for small ones); with E2M1, where V's block scales in
- * a tile's 32 keys (seen by the row or not) leave 2^-23 .. 2^13, to bf16 (2^-8) for these keys (a block of zeros has no such scale).  E2M1 keys up to
- * 2^115, values up to 2^100; blocks of a key below 2^-36 of its largest lose bits, as do keys below 2^-100 and values below
- * 2^-126; a block of values that are all below 2^-124 counts as zeros.
+ * a tile's 32 keys (seen by the row or by others of its 256) leave 2^-23 .. 2^13, to bf16 (2^-8) for these keys; a block of
+ * zeros has no such scale.  E2M1 keys up to 2^115, values up to 2^100; blocks of a key below 2^-36 of its largest lose bits,
+ * as do keys below 2^-100 and values below 2^-126; a block of values that are all below 2^-124 counts as zeros.
  * |scale| times a row's largest sum of |q k| below 2^26: beyond, where a score's rounding in fp32 is more
  * than the softmax's distances, the row may be NaN or zeros.
  * A row that sees a token with a non-finite key or value is NaN as a whole, and so is a row of
  * q that is not finite; the rows beside it are as without it.
  * window and sinks as above; window 0: none (sinks 0 too), causal or not.
- * args as there, with a workspace of fsa_attention_chunk_workspace bytes.
+ * args as there, with a workspace of fsa_attention_chunk_workspace bytes: none for block tables of up to 512
+ * tokens, else 2 * SMs * 256 * (D + 2) floats and a little more, whatever the rows (40 MB with 128 dims).
  * B * Sq * H <= 2^27; B * Hkv * ceil(Sq * H/Hkv / 256) * (ceil(max_pages * page_size / 128) + 4) < 2^31. */
 int fsa_attention_chunk_workspace(const fsa_cache* cache, int B, int H, int Sq, int max_pages, size_t* bytes);
 int fsa_attention_chunk(const fsa_cache_attn* args, int window, int sinks, void* stream);

@@ -656,7 +656,9 @@ def fsa_cache_append_rope(cache: MxCache, q: torch.Tensor, k: torch.Tensor, v: t
     """What fsa_qk_norm_rope makes of q [B,S,H,D] (returned: q_out, by default a contiguous tensor of
     q's shape), and k [B,S,Hkv,D], normalised and rotated too, and v quantised into the cache as
     by fsa_cache_append, in one pass; k is rounded once.  pos as there; without it a token turns
-    by its place in its sequence, lens[b] - new_lens[b] + i.  Rows behind new_lens[b] are neither read nor written."""
+    by its place in its sequence, lens[b] - new_lens[b] + i.  Rows behind new_lens[b] are neither read nor written.
+    With some hundreds of new tokens it is faster than the two calls, with few about as fast, from about a thousand on slower
+    (16384 tokens: 94 us, 76 for the two): there it is for keys that have to be rounded once only."""
     if q_out is None:
         q_out = _new(torch.empty if new_lens is None else torch.zeros, q.shape, q.dtype, q.device, stream)
     c = cache
@@ -731,8 +733,8 @@ def fsa_attention_cache(q: torch.Tensor, cache: MxCache, block_table: torch.Tens
     (int32 [B]; the rows' own tokens are in the cache).  Row i < q_lens[b] (default all Sq)
     stands at lens[b] - q_lens[b] + i and, causal, sees the keys up to there; rows behind
     q_lens[b] are left as they were.  window (with causal only): of these keys it sees the last
-    `window`, its own among them, and the first `sinks` of the sequence.  The cache is read again
-    for each 16 rows a kv head: fsa_attention_chunk is for more.  lse: optional fp32 [B,Sq,H] for
+    `window`, its own among them, and the first `sinks` of the sequence; pages without such a key
+    are not looked up.  The cache is read again for each 16 rows a kv head: fsa_attention_chunk is for more.  lse: optional fp32 [B,Sq,H] for
     the log of the softmax sums.  workspace: uint8, at least fsa_attention_cache_workspace bytes
     (default: one of the call's own).  status: int32 [1], set where a page number lies outside
     the pool or a wait runs out."""
@@ -746,7 +748,9 @@ def fsa_attention_chunk(q: torch.Tensor, cache: MxCache, block_table: torch.Tens
                         workspace: torch.Tensor | None = None, timeout_ms=0, status: torch.Tensor | None = None,
                         stream=None) -> torch.Tensor:
     """What fsa_attention_cache computes, for chunks of a prompt: 256 rows a kv head at a time, on
-    the tensor cores in 16 bits; faster from about 60 rows a kv head on.  Arguments as there (workspace: fsa_attention_chunk_workspace bytes)."""
+    the tensor cores in 16 bits; faster from about 60 rows a kv head on where the keys are many (eight sequences of 2048, one of
+    32768), later over few.  Arguments as there (workspace: fsa_attention_chunk_workspace bytes).  Scores beyond 2^26, where fp32
+    has no fraction left, may make a row NaN or zeros here."""
     return _attend("attention_chunk", q, cache, block_table, lens, q_lens, causal, scale, window, sinks, out, lse, out_dtype,
                    workspace, timeout_ms, status, stream)
 

@@ -21,10 +21,12 @@
 // quantisation wants them; a pair's other element comes from another lane).
 //
 // Measured (one GB300, calls in a graph, 32+8 heads of 128, NVFP4, against fsa_qk_norm_rope and fsa_cache_append in
-// turn): 64 tokens 5.7 us (5.8), 512 8.0 (9.4), 2048 17.2 (15.5), 16384 96 (76), where memory takes 52.  From about a
-// thousand tokens on it is bound by instructions, 59 M a warp for 16384 tokens, 2 of 4 a cycle: half of them turn the
+// turn): 64 tokens 5.7 to 7.2 us (5.8; by whether a warp has something open), 512 8.3 (9.7), 1024 11.5 (11.9), 2048 17.7
+// (15.4), 16384 93.8 (76.2), where memory takes 52; 16384 tokens of 8+8 heads 73.6 (47.2).  From about a
+// thousand tokens on it is bound by instructions, 61.5 M a warp for 16384 tokens, 2.3 of 4 a cycle: half of them turn the
 // keys, whose two roundings and whose register need beside the rare ways cost what the saved pass over k gives; the
-// codes are those of the exact keys, which the two calls' are not.
+// codes are those of the exact keys, which the two calls' are not.  Rows that all go through fp64 (NaN, or far over
+// ordinary size) take 3.9 ms.
 #include <algorithm>
 #include "fsa_cache_codes.cuh"
 #include "fsa_rope.cuh"

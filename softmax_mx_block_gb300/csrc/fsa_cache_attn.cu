@@ -1232,7 +1232,13 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_join_kernel(const CacheAtt
 //   64 sequences of 100, 890, 1500 keys: 11.4 / 6.3, 15.0 / 13.0, 16.4 / 18.4
 //   152 sequences of 100, 890, 1 to 890: 14.5 / 6.9, 20.2 / 14.6, 14.1 / 12.0
 // The rule goes by what the host knows: one short sequence in a wide table takes the list.
-// A window bounds the tiles too: those of its keys and of the rows' own at any offset, and the first keys'.
+// A window bounds the tiles too: those of its keys and of the rows' own at any offset, and the first keys'.  List / whole
+// with 4 first keys and windows of 500, 800, 1024, 1500 (17, 27, 34 and 49 tiles and up to one more), us, 128 dims:
+//   1 sequence of 16384 keys, E2M1: 9.9 / 7.9, 9.8 / 9.3, 10.2 / 10.6, 9.9 / 14.2
+//   16, NVFP4: 13.4 / 9.9, 14.7 / 11.7, 14.7 / 13.6, 17.0 / 18.5;  64: 20.5 / 19.8, 25.0 / 22.6, 27.5 / 27.3, 35.5 / 37.5
+//   16 of 24 kv heads, 5 rows, E2M1: 19.2 / 12.3, 21.9 / 15.4, 24.8 / 18.2, 28.5 / 22.8
+//   128 of 2 kv heads of 64 dims, 7 query heads each, 2 rows, NVFP4: 17.5 / 11.8, 19.9 / 14.7, 21.7 / 17.2, 24.4 / 20.7
+// (With many segments it would pay up to about 50 tiles, with few not: the tables' limit is kept for both.)
 bool whole_segments(const Cache& c, int B, int CT, int Sq, int max_pages, int window, int sinks, int sms) {
   int64_t tiles = (((int64_t)max_pages << c.page_shift) + TILE - 1) / TILE;
   if (window) tiles = std::min(tiles, ((int64_t)window + Sq + 2 * TILE - 3) / TILE + ((int64_t)sinks + TILE - 1) / TILE);

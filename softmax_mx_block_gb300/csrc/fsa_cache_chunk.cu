@@ -28,9 +28,9 @@
 //   - A row that sees a token whose values are not finite (the scale's NaN) is NaN as a whole; the others
 //     are as without it (its V is zero in the operand, and a bit tells the rows).
 //
-// Measured (one GB300, cuBLAS at 1943 TFLOP/s in bf16): 2048 tokens over 128K keys, 32/8 heads of 128: NVFP4 1590
-// TFLOP/s (2.74 ms), E2M1 1394 (3.13); heads of 64: 942 (2.32) and 701 (3.11).  Eight sequences of 8192 keys,
-// 64 tokens each, NVFP4: 73 us, where fsa_attention_cache takes 321.
+// Measured (one GB300, cuBLAS at 1943 TFLOP/s in bf16): 2048 tokens over 128K keys, 32/8 heads of 128: NVFP4 1570
+// TFLOP/s (2.73 to 2.82 ms), E2M1 1380 (3.16); heads of 64: 921 (2.37) and 711 (3.07).  Eight sequences of 8192 keys,
+// 64 tokens each, NVFP4: 73 us, where fsa_attention_cache takes 322.  Values of which one block of 32 is zeros take no longer.
 // What bounds it: of the about 3100 cycles of a tile of 128 dims (NVFP4) its products take 2050 at the nominal rate; a row
 // tile's chain, its scores, their maximum (800 cycles), exponentials (1050), products, is as long, and the two row tiles'
 // chains cover each other but for their ends.  The operand warps work 2100 of these cycles.  E2M1 is slower by what tells
@@ -49,7 +49,11 @@ namespace {
 
 constexpr int ROWS = 256;             // of a block: two tiles of 128
 constexpr int KEYS = 128;             // of a tile
-constexpr int EXTRA = 3;              // what a segment's start costs a CTA, in tiles (eight turns: 1 174 us, 2 160, 3 150, 5 148, 8 157)
+// What a segment's start costs a CTA, in tiles.  us with 1, 2, 3, 4, 5, 6, 8 of them: eight turns over 600 to 8192 keys 142, 135,
+// 129, 127, 123, 124, 123; 300 and 500 tokens over 40000 and 9000 keys 215, 211, 211, 209, 205, 207, 209; 40 short ones over 520 to 900
+// 105, 98, 94, 96, 95, 95, 93; 64 tokens each over 24 of 1000 to 4000 (E2M1) 106, 103, 102, 98, 96, 98, 98; eight windows of 2048 130,
+// 126, 128, 125, 124, 124, 124.  (5 would do a little better than 3, but 3 is in the stated limit of the list's length.)
+constexpr int EXTRA = 3;
 constexpr int THREADS = 512;          // warps 0..7 softmax (a row a thread), 8..11 operands, 12 copies, 13 MMA
 constexpr int RAW = 3;                // stages of 64 keys of codes
 constexpr float LAZY = 8.0f;          // log2 of how far a score may beat the running maximum
